@@ -32,6 +32,7 @@ MOE_ERR_BAD_TOPK = 4
 MOE_ERR_TIMEOUT = 5
 MOE_ERR_CUDA = 6
 MOE_ERR_WORKSPACE = 7
+MOE_ERR_BAD_LOGIT = 8
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -103,6 +104,10 @@ def _configure(lib):
     lib.moe_combine_fp8_ex.restype = _I
     lib.moe_combine_ex.argtypes = [_P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P]
     lib.moe_combine_ex.restype = _I
+    lib.moe_topk_gate.argtypes = [_P, _I, _P, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P, _P]
+    lib.moe_topk_gate.restype = _I
+    lib.moe_topk_gate_backward.argtypes = [_P, _I, _P, _P, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P]
+    lib.moe_topk_gate_backward.restype = _I
     return lib
 
 
@@ -126,7 +131,7 @@ TRACE_RECORD = np.dtype([("kernel", "<u4"), ("cta", "<u4"), ("warp", "<u4"), ("s
                          ("start_ns", "<u8"), ("end_ns", "<u8")])
 TRACE_KERNELS = {1: "layout_tiles", 2: "layout_direct", 3: "layout_cluster", 4: "layout_count", 5: "layout_scan",
                  6: "layout_rows_scan", 7: "expand_layout", 8: "expand_layout_cluster", 9: "dispatch",
-                 10: "dispatch_fp8_rows", 11: "combine", 12: "layout_rows"}
+                 10: "dispatch_fp8_rows", 11: "combine", 12: "layout_rows", 13: "gate", 14: "gate_backward"}
 TRACE_PHASE = 0x10000   # warp field of a per-CTA phase record: TRACE_PHASE + phase (1, 2, ...)
 TRACE_PHASE_NAMES = {3: ("dependency wait", "top-k tile loaded", "bitmap and expert histogram",
                          "tile counts and first cluster barrier", "exchange and second barrier",
@@ -432,3 +437,71 @@ def moe_combine_ex(partial: torch.Tensor, token_dst_row: torch.Tensor, *, row_we
                               _ptr(status), _stream(stream))
     _check(code, "moe_combine_ex")
     return out, combined_topk_weights
+
+
+MOE_LOGITS_F32 = 0
+MOE_LOGITS_BF16 = 1
+MOE_GATE_SOFTMAX = 0
+MOE_GATE_SIGMOID = 1
+MOE_GATE_NORMALIZE = 0x100
+
+
+def _logits_type(logits: torch.Tensor) -> int:
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("the router's logits are float32 or bfloat16")
+    return MOE_LOGITS_BF16 if logits.dtype == torch.bfloat16 else MOE_LOGITS_F32
+
+
+def _gate_mode(score: str, normalize: bool) -> int:
+    scores = {"softmax": MOE_GATE_SOFTMAX, "sigmoid": MOE_GATE_SIGMOID}
+    if score not in scores:
+        raise ValueError(f"score is one of {sorted(scores)}, not {score!r}")
+    return scores[score] | (MOE_GATE_NORMALIZE if normalize else 0)
+
+
+def _typed(t: Optional[torch.Tensor], dtype: torch.dtype, shape: tuple, name: str):
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name} is {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    return t
+
+
+def moe_topk_gate(logits: torch.Tensor, num_topk: int, *, bias: Optional[torch.Tensor] = None, score: str = "softmax",
+                  normalize: bool = True, scale: float = 1.0, topk_idx: Optional[torch.Tensor] = None,
+                  topk_weights: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                  stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The experts (int64 [T, k], -1 where fewer than k are unmasked) and fp32
+    weights of each token from the router's ``logits`` [T, E] (fp32 or bf16):
+    the k largest logits (or score + ``bias``), weighted by their softmax or
+    sigmoid scores, normalised over the chosen ones if ``normalize``."""
+    T, E = logits.shape
+    dev = logits.device
+    topk_idx = (torch.empty(T, num_topk, dtype=torch.int64, device=dev) if topk_idx is None else
+                _typed(topk_idx, torch.int64, (T, num_topk), "topk_idx"))
+    topk_weights = (torch.empty(T, num_topk, dtype=torch.float32, device=dev) if topk_weights is None else
+                    _typed(topk_weights, torch.float32, (T, num_topk), "topk_weights"))
+    _typed(bias, torch.float32, (E,), "bias")
+    status = new_status(dev) if status is None else status
+    code = LIB.moe_topk_gate(_ptr(logits), _logits_type(logits), _ptr(bias), T, num_topk, E,
+                             _gate_mode(score, normalize), float(scale), _ptr(topk_idx), _ptr(topk_weights),
+                             _ptr(status), _stream(stream))
+    _check(code, "moe_topk_gate")
+    return topk_idx, topk_weights
+
+
+def moe_topk_gate_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_weights: torch.Tensor, *,
+                           score: str = "softmax", normalize: bool = True, scale: float = 1.0,
+                           out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                           stream=None) -> torch.Tensor:
+    """The gradient [T, E] (the logits' type) of moe_topk_gate's weights, given
+    ``grad_weights`` [T, k] fp32; pass the same score, normalize and scale."""
+    T, E = logits.shape
+    k = topk_idx.shape[1]
+    _typed(topk_idx, torch.int64, (T, k), "topk_idx")
+    _typed(grad_weights, torch.float32, (T, k), "grad_weights")
+    out = torch.empty_like(logits) if out is None else _typed(out, logits.dtype, (T, E), "out")
+    status = new_status(logits.device) if status is None else status
+    code = LIB.moe_topk_gate_backward(_ptr(logits), _logits_type(logits), _ptr(topk_idx), _ptr(grad_weights), T, k, E,
+                                      _gate_mode(score, normalize), float(scale), _ptr(out), _ptr(status),
+                                      _stream(stream))
+    _check(code, "moe_topk_gate_backward")
+    return out

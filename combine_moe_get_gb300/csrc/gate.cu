@@ -1,0 +1,389 @@
+// gate.cu -- the router's gate: scores, top-k choice and weights from logits
+// (moe_topk_gate), and the gradient of the weights with respect to the logits
+// (moe_topk_gate_backward).
+//
+// Mathematics. The chosen experts are the k largest logits (softmax and
+// sigmoid keep their order), or the k largest score + bias; ties go to the
+// lowest index. Logits are compared as 32-bit keys whose unsigned order is the
+// floats' order, so a choice is exact: no rounding takes part unless a bias is
+// given. Exponentials are taken of differences to the largest logit (0 at the
+// maximum even when that is +inf), sums are fp32.
+//
+// A warp handles a token: 32 lanes hold the row's E logits in registers (up to
+// 64 each), each choice is one max over the warp's keys and one min over the
+// indices that reach it (redux.sync), and lane j keeps entry j (k <= 32). Rows
+// longer than 2048 take one CTA per token with the keys in shared memory.
+#include <algorithm>
+#include <cuda_bf16.h>
+
+#include "moe_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kWarpsPerCta = 4;
+constexpr int kWideThreads = 256;      // CTA of a row with more experts than a warp holds
+constexpr int kMaxPerLane = 64;
+constexpr uint32_t kFull = 0xffffffffu;
+
+struct GateArgs {
+    const void *logits;
+    const float *bias;
+    int T, k, E;
+    int mode;
+    float scale;
+    int64_t *idx;
+    float *w;
+    int32_t *status;
+    TraceArgs trace;
+};
+
+struct GateBackArgs {
+    const void *logits;
+    const int64_t *idx;
+    const float *gw;
+    int T, k, E;
+    int mode;
+    float scale;
+    void *gl;
+    int32_t *status;
+    TraceArgs trace;
+};
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void store(float *p, float v) { *p = v; }
+__device__ __forceinline__ void store(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+// Unsigned order of the key = order of the float, -0 as +0; 0 (never chosen)
+// for -inf and NaN.
+__device__ __forceinline__ uint32_t order_key(float v) {
+    if (!(v > -INFINITY)) return 0;
+    const uint32_t u = __float_as_uint(v + 0.0f);   // -0 + 0 = +0
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t key) {
+    return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+
+// exp(l - m) for l <= m, 1 at l == m also when both are infinite.
+__device__ __forceinline__ float exp_below(float l, float m) { return l == m ? 1.0f : expf(l - m); }
+
+struct Sigmoid {
+    float s, not_s;   // sigmoid(l) and 1 - sigmoid(l), each without cancellation
+};
+__device__ __forceinline__ Sigmoid sigmoid(float l) {
+    const float t = expf(-fabsf(l)), a = 1.0f / (1.0f + t), b = t / (1.0f + t);
+    return l >= 0.0f ? Sigmoid{a, b} : Sigmoid{b, a};
+}
+
+// The normalised weights q_j of the chosen logits, one per lane (`on`: this
+// lane has one). The sigmoids are taken relative to exp(min(max l, 0)), so that
+// their sum does not vanish when every chosen logit is far below zero.
+__device__ __forceinline__ float normalised(float l, bool on, bool is_sigmoid) {
+    const float m = warp_max(on ? l : -INFINITY);
+    float q = 0.0f;
+    if (on) {
+        if (is_sigmoid)
+            q = exp_below(fminf(l, 0.0f), fminf(m, 0.0f)) / (1.0f + expf(-fabsf(l)));
+        else
+            q = exp_below(l, m);
+    }
+    const float sum = warp_sum(q);
+    return on ? q / sum : 0.0f;
+}
+
+// Lane j: the weight of entry j with logit l; m and z the row's maximum and
+// softmax sum (used only by the softmax that is not normalised).
+__device__ __forceinline__ float entry_weight(int mode, float l, bool on, float m, float z) {
+    const bool is_sigmoid = (mode & 0xff) == MOE_GATE_SIGMOID;
+    if (mode & MOE_GATE_NORMALIZE) return normalised(l, on, is_sigmoid);
+    if (!on) return 0.0f;
+    return is_sigmoid ? sigmoid(l).s : exp_below(l, m) / z;
+}
+
+// ------------------------------------------------------------------ forward, a warp per token
+
+template <typename L, int kPerLane>
+__global__ void __launch_bounds__(kWarpsPerCta * 32) gate_kernel(const GateArgs a) {
+    WarpTrace wt(a.trace, MOE_TRACE_GATE);
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
+    if (t >= a.T) return;
+    const L *row = static_cast<const L *>(a.logits) + (size_t)t * a.E;
+    const bool is_sigmoid = (a.mode & 0xff) == MOE_GATE_SIGMOID;
+
+    // element i of lane: expert i * 32 + lane
+    uint32_t key[kPerLane];
+    bool nan = false;
+#pragma unroll
+    for (int i = 0; i < kPerLane; ++i) {
+        const int e = i * 32 + lane;
+        const float v = e < a.E ? to_float(row[e]) : -INFINITY;
+        nan |= v != v;
+        key[i] = order_key(v);
+    }
+    if (nan) report(a.status, MOE_ERR_BAD_LOGIT);
+
+    // the row's maximum and softmax sum, where the weights or the choice need them
+    float m = 0.0f, z = 1.0f;
+    const bool whole_row = !is_sigmoid && (!(a.mode & MOE_GATE_NORMALIZE) || a.bias != nullptr);
+    if (whole_row) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) top = max(top, key[i]);
+        top = __reduce_max_sync(kFull, top);
+        m = top ? key_value(top) : 0.0f;
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i)
+            if (key[i]) s += exp_below(key_value(key[i]), m);
+        z = warp_sum(s);
+    }
+    if (a.bias != nullptr) {   // choose by score + bias; the logits are read again for the chosen
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i) {
+            if (key[i] == 0) continue;
+            const float l = key_value(key[i]);
+            const float s = is_sigmoid ? sigmoid(l).s : exp_below(l, m) / z;
+            key[i] = order_key(s + a.bias[i * 32 + lane]);
+        }
+    }
+
+    float mine = 0.0f;      // lane j: entry j's logit
+    int mine_e = -1;        // ... and expert
+    for (int j = 0; j < a.k; ++j) {
+        uint32_t best = 0;
+        int best_i = 0;
+#pragma unroll
+        for (int i = 0; i < kPerLane; ++i)
+            if (key[i] > best) best = key[i], best_i = i;
+        const uint32_t top = __reduce_max_sync(kFull, best);
+        if (top == 0) break;
+        const int e = best_i * 32 + lane;
+        const int win = (int)__reduce_min_sync(kFull, best == top ? (uint32_t)e : kFull);
+        if (e == win) {
+#pragma unroll
+            for (int i = 0; i < kPerLane; ++i)
+                if (i == best_i) key[i] = 0;
+        }
+        if (lane == j) mine = a.bias == nullptr ? key_value(top) : to_float(row[win]), mine_e = win;
+    }
+    const float w = entry_weight(a.mode, mine, mine_e >= 0, m, z);
+    if (lane < a.k) {
+        a.idx[(size_t)t * a.k + lane] = mine_e;
+        a.w[(size_t)t * a.k + lane] = mine_e >= 0 ? a.scale * w : 0.0f;
+    }
+}
+
+// ------------------------------------------------------------------ forward, a CTA per token
+
+struct Top {
+    uint32_t key;
+    int e;
+};
+__device__ __forceinline__ Top better(Top x, Top y) {
+    return y.key > x.key || (y.key == x.key && y.e < x.e) ? y : x;
+}
+
+template <typename L>
+__global__ void __launch_bounds__(kWideThreads) gate_wide_kernel(const GateArgs a) {
+    WarpTrace wt(a.trace, MOE_TRACE_GATE);
+    grid_dependency_wait();
+    extern __shared__ uint32_t keys[];
+    __shared__ Top tops[kWideThreads / 32];
+    __shared__ float sums[kWideThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = blockIdx.x;
+    const L *row = static_cast<const L *>(a.logits) + (size_t)t * a.E;
+    const bool is_sigmoid = (a.mode & 0xff) == MOE_GATE_SIGMOID;
+
+    auto block_top = [&](Top v) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            v = better(v, Top{__shfl_xor_sync(kFull, v.key, o), __shfl_xor_sync(kFull, v.e, o)});
+        __syncthreads();
+        if (lane == 0) tops[warp] = v;
+        __syncthreads();
+        v = tops[0];
+        for (int i = 1; i < kWideThreads / 32; ++i) v = better(v, tops[i]);
+        return v;
+    };
+
+    bool nan = false;
+    Top local{0, a.E};
+    for (int e = threadIdx.x; e < a.E; e += kWideThreads) {
+        const float v = to_float(row[e]);
+        nan |= v != v;
+        keys[e] = order_key(v);
+        local = better(local, Top{keys[e], e});
+    }
+    if (nan) report(a.status, MOE_ERR_BAD_LOGIT);
+    float m = 0.0f, z = 1.0f;
+    if (!is_sigmoid && (!(a.mode & MOE_GATE_NORMALIZE) || a.bias != nullptr)) {
+        const Top top = block_top(local);
+        m = top.key ? key_value(top.key) : 0.0f;
+        float s = 0.0f;
+        for (int e = threadIdx.x; e < a.E; e += kWideThreads)
+            if (keys[e]) s += exp_below(key_value(keys[e]), m);
+        s = warp_sum(s);
+        if (lane == 0) sums[warp] = s;
+        __syncthreads();
+        z = 0.0f;
+        for (int i = 0; i < kWideThreads / 32; ++i) z += sums[i];
+    }
+    if (a.bias != nullptr) {
+        local = Top{0, a.E};
+        for (int e = threadIdx.x; e < a.E; e += kWideThreads) {
+            if (keys[e] != 0) {
+                const float l = key_value(keys[e]);
+                const float s = is_sigmoid ? sigmoid(l).s : exp_below(l, m) / z;
+                keys[e] = order_key(s + a.bias[e]);
+            }
+            local = better(local, Top{keys[e], e});
+        }
+    }
+    float mine = 0.0f;
+    int mine_e = -1;
+    for (int j = 0; j < a.k; ++j) {
+        const Top top = block_top(local);
+        if (top.key == 0) break;
+        if (top.e % kWideThreads == threadIdx.x) {   // the thread that holds it looks for its next
+            keys[top.e] = 0;
+            local = Top{0, a.E};
+            for (int e = threadIdx.x; e < a.E; e += kWideThreads) local = better(local, Top{keys[e], e});
+        }
+        if (threadIdx.x == j) mine = a.bias == nullptr ? key_value(top.key) : to_float(row[top.e]), mine_e = top.e;
+    }
+    if (warp != 0) return;
+    const float w = entry_weight(a.mode, mine, mine_e >= 0, m, z);
+    if (lane < a.k) {
+        a.idx[(size_t)t * a.k + lane] = mine_e;
+        a.w[(size_t)t * a.k + lane] = mine_e >= 0 ? a.scale * w : 0.0f;
+    }
+}
+
+// ------------------------------------------------------------------ backward, a warp per token
+
+template <typename L>
+__global__ void __launch_bounds__(kWarpsPerCta * 32) gate_backward_kernel(const GateBackArgs a) {
+    WarpTrace wt(a.trace, MOE_TRACE_GATE_BACKWARD);
+    grid_dependency_wait();
+    const int lane = threadIdx.x & 31;
+    const int t = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
+    if (t >= a.T) return;
+    const L *row = static_cast<const L *>(a.logits) + (size_t)t * a.E;
+    L *out = static_cast<L *>(a.gl) + (size_t)t * a.E;
+    const bool is_sigmoid = (a.mode & 0xff) == MOE_GATE_SIGMOID;
+    const bool norm = (a.mode & MOE_GATE_NORMALIZE) != 0;
+
+    // lane j: entry j
+    int e = -1;
+    float g = 0.0f, l = 0.0f;
+    if (lane < a.k) {
+        const int64_t v = a.idx[(size_t)t * a.k + lane];
+        if (v < -1 || v >= a.E) report(a.status, MOE_ERR_BAD_TOPK);
+        else e = (int)v;
+        g = a.gw[(size_t)t * a.k + lane] * a.scale;
+        if (e >= 0) l = to_float(row[e]);
+        if (!(l > -INFINITY)) e = -1;   // a masked logit has no weight
+    }
+    const bool on = e >= 0;
+    if (!on) g = 0.0f;
+
+    // d: the entry's own part of its logit's gradient; every other logit gets -p * dot
+    float d = 0.0f, dot = 0.0f, m = 0.0f, rz = 0.0f;
+    const bool dense = !is_sigmoid && !norm;
+    if (norm) {
+        const float q = normalised(l, on, is_sigmoid);
+        d = q * (g - warp_sum(g * q));
+        if (is_sigmoid) d *= sigmoid(l).not_s;
+    } else if (is_sigmoid) {
+        const Sigmoid s = sigmoid(l);
+        d = g * s.s * s.not_s;
+    } else {
+        m = -INFINITY;
+        for (int i = lane; i < a.E; i += 32) m = fmaxf(m, to_float(row[i]));   // fmaxf passes over NaN
+        m = warp_max(m);
+        float z = 0.0f;
+        for (int i = lane; i < a.E; i += 32) {
+            const float v = to_float(row[i]);
+            if (v > -INFINITY) z += exp_below(v, m);
+        }
+        z = warp_sum(z);
+        rz = z > 0.0f ? 1.0f / z : 0.0f;
+        const float p = on ? exp_below(l, m) * rz : 0.0f;
+        dot = warp_sum(g * p);
+        d = p * (g - dot);
+    }
+    if (!on) d = 0.0f;
+    for (int i = lane; i < a.E; i += 32) {
+        float v = 0.0f;
+        if (dense) {
+            const float x = to_float(row[i]);
+            if (x > -INFINITY) v = -exp_below(x, m) * rz * dot;
+        }
+        store(out + i, v);
+    }
+    // an expert named by several entries gets the sum of their parts, in entry order
+    const uint32_t same = __match_any_sync(kFull, e);
+    float sum = 0.0f;
+    int n = 0;
+    for (int j = 0; j < a.k; ++j) {
+        const float dj = __shfl_sync(kFull, d, j);
+        if (same >> j & 1) sum += dj, ++n;
+    }
+    // ... and its -p * dot once
+    if (dense && n > 1) sum += (float)(n - 1) * exp_below(l, m) * rz * dot;
+    __syncwarp();
+    if (on && (same & ((1u << lane) - 1)) == 0) store(out + e, sum);
+}
+
+template <typename L>
+int launch_gate_typed(const GateArgs &a, cudaStream_t s) {
+    const bool overlap = tuning().overlap != 0;
+    const dim3 grid((a.T + kWarpsPerCta - 1) / kWarpsPerCta), block(kWarpsPerCta * 32);
+    cudaError_t e;
+    if (a.E <= 256) e = launch_kernel(gate_kernel<L, 8>, grid, block, 0, s, overlap, a);
+    else if (a.E <= 1024) e = launch_kernel(gate_kernel<L, 32>, grid, block, 0, s, overlap, a);
+    else if (a.E <= 32 * kMaxPerLane) e = launch_kernel(gate_kernel<L, kMaxPerLane>, grid, block, 0, s, overlap, a);
+    else e = launch_kernel(gate_wide_kernel<L>, dim3(a.T), dim3(kWideThreads), a.E * sizeof(uint32_t), s, overlap, a);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace
+
+int launch_gate(const GateLaunch &L) {
+    if (L.num_tokens == 0) return MOE_OK;
+    const GateArgs a{L.logits, L.bias, L.num_tokens, L.num_topk, L.num_experts, L.mode, L.scale,
+                     L.topk_idx, L.topk_weights, L.status, trace_args()};
+    const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
+    return L.logits_type == MOE_LOGITS_BF16 ? launch_gate_typed<__nv_bfloat16>(a, s) : launch_gate_typed<float>(a, s);
+}
+
+int launch_gate_backward(const GateBackwardLaunch &L) {
+    if (L.num_tokens == 0) return MOE_OK;
+    const GateBackArgs a{L.logits, L.topk_idx, L.grad_weights, L.num_tokens, L.num_topk, L.num_experts, L.mode,
+                         L.scale, L.grad_logits, L.status, trace_args()};
+    const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
+    const dim3 grid((a.T + kWarpsPerCta - 1) / kWarpsPerCta), block(kWarpsPerCta * 32);
+    const bool overlap = tuning().overlap != 0;
+    const cudaError_t e = L.logits_type == MOE_LOGITS_BF16
+                              ? launch_kernel(gate_backward_kernel<__nv_bfloat16>, grid, block, 0, s, overlap, a)
+                              : launch_kernel(gate_backward_kernel<float>, grid, block, 0, s, overlap, a);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace moe

@@ -255,6 +255,7 @@ MOE_API const char *moe_status_string(int status) {
         case MOE_ERR_TIMEOUT: return "MOE_ERR_TIMEOUT";
         case MOE_ERR_CUDA: return "MOE_ERR_CUDA";
         case MOE_ERR_WORKSPACE: return "MOE_ERR_WORKSPACE";
+        case MOE_ERR_BAD_LOGIT: return "MOE_ERR_BAD_LOGIT";
         default: return "MOE_ERR_UNKNOWN";
     }
 }
@@ -527,6 +528,44 @@ MOE_API int moe_combine_fp8_ex(const void *partial_codes, const float *partial_s
                                uint32_t *balance, int32_t *status, void *stream) {
     return combine_fp8_common(partial_codes, partial_scales, num_partial_rows, num_tokens, hidden, num_topk,
                               token_dst_row, out, balance, status, stream);
+}
+
+// Shape, mode and logits of a gate call, forward or backward.
+static int gate_check(const void *logits, int logits_type, int T, int k, int E, int mode, const void *idx,
+                      const void *weights, const int32_t *status) {
+    if (!shape_ok(T, k, E, 1) || k > E) return MOE_ERR_INVALID_ARG;
+    if (logits_type != MOE_LOGITS_F32 && logits_type != MOE_LOGITS_BF16) return MOE_ERR_INVALID_ARG;
+    const int score = mode & ~MOE_GATE_NORMALIZE;
+    if (score != MOE_GATE_SOFTMAX && score != MOE_GATE_SIGMOID) return MOE_ERR_INVALID_ARG;
+    if (!status || (T > 0 && (!logits || !idx || !weights))) return MOE_ERR_INVALID_ARG;
+    if (!aligned(status, 4) || !aligned(idx, 8) || !aligned(weights, 4) ||
+        !aligned(logits, logits_type == MOE_LOGITS_F32 ? 4 : 2))
+        return MOE_ERR_MISALIGNED;
+    return MOE_OK;
+}
+
+MOE_API int moe_topk_gate(const void *logits, int logits_type, const float *bias, int num_tokens, int num_topk,
+                          int num_experts, int mode, float scale, int64_t *topk_idx, float *topk_weights,
+                          int32_t *status, void *stream) {
+    const int rc = gate_check(logits, logits_type, num_tokens, num_topk, num_experts, mode, topk_idx, topk_weights,
+                              status);
+    if (rc != MOE_OK) return rc;
+    if (!aligned(bias, 4)) return MOE_ERR_MISALIGNED;
+    return moe::launch_gate(moe::GateLaunch{logits, logits_type, bias, num_tokens, num_topk, num_experts, mode, scale,
+                                            topk_idx, topk_weights, status, stream});
+}
+
+MOE_API int moe_topk_gate_backward(const void *logits, int logits_type, const int64_t *topk_idx,
+                                   const float *grad_weights, int num_tokens, int num_topk, int num_experts, int mode,
+                                   float scale, void *grad_logits, int32_t *status, void *stream) {
+    const int rc = gate_check(logits, logits_type, num_tokens, num_topk, num_experts, mode, topk_idx, grad_weights,
+                              status);
+    if (rc != MOE_OK) return rc;
+    if (num_tokens > 0 && !grad_logits) return MOE_ERR_INVALID_ARG;
+    if (!aligned(grad_logits, logits_type == MOE_LOGITS_F32 ? 4 : 2)) return MOE_ERR_MISALIGNED;
+    return moe::launch_gate_backward(moe::GateBackwardLaunch{logits, logits_type, topk_idx, grad_weights, num_tokens,
+                                                             num_topk, num_experts, mode, scale, grad_logits, status,
+                                                             stream});
 }
 
 }  // extern "C"

@@ -1,6 +1,6 @@
 // moe_internal.h -- host-side interfaces between the C ABI entry points
 // (moe_api.cu) and the kernel launchers (layout.cu, expand.cu, dispatch.cu,
-// combine.cu).
+// combine.cu, gate.cu).
 // Arguments reaching a launcher have already been validated.
 #pragma once
 
@@ -266,5 +266,35 @@ struct CombineLaunch {
 };
 
 int launch_combine(const CombineLaunch &L);
+
+struct GateLaunch {
+    const void *logits;
+    int logits_type;          // MOE_LOGITS_*
+    const float *bias;        // optional
+    int num_tokens, num_topk, num_experts;
+    int mode;                 // moe_gate_mode_t with its flag
+    float scale;
+    int64_t *topk_idx;
+    float *topk_weights;
+    int32_t *status;
+    void *stream;
+};
+
+int launch_gate(const GateLaunch &L);
+
+struct GateBackwardLaunch {
+    const void *logits;
+    int logits_type;
+    const int64_t *topk_idx;
+    const float *grad_weights;
+    int num_tokens, num_topk, num_experts;
+    int mode;
+    float scale;
+    void *grad_logits;
+    int32_t *status;
+    void *stream;
+};
+
+int launch_gate_backward(const GateBackwardLaunch &L);
 
 }  // namespace moe

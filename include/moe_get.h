@@ -27,9 +27,10 @@
  *     the first call whose errors you want to see, and read it after the stream
  *     has synchronised. Data errors are MOE_ERR_BAD_TOPK (a top-k entry outside
  *     [-1, E); that entry is treated as masked), MOE_ERR_CAPACITY (a receive row
- *     at or beyond the receive capacity; that row is not written / not read) and
+ *     at or beyond the receive capacity; that row is not written / not read),
  *     MOE_ERR_TIMEOUT (a bounded wait inside a kernel ran out; the outputs of
- *     that call are unspecified).
+ *     that call are unspecified) and MOE_ERR_BAD_LOGIT (a NaN router logit; that
+ *     expert is treated as masked).
  *   - T == 0 is a valid no-op that still writes zero counts and prefixes.
  */
 #ifndef MOE_GET_H
@@ -56,7 +57,8 @@ typedef enum {
     MOE_ERR_BAD_TOPK = 4,
     MOE_ERR_TIMEOUT = 5,
     MOE_ERR_CUDA = 6,
-    MOE_ERR_WORKSPACE = 7
+    MOE_ERR_WORKSPACE = 7,
+    MOE_ERR_BAD_LOGIT = 8
 } moe_status_t;
 
 /* Limits checked on the host (MOE_ERR_INVALID_ARG beyond them). */
@@ -421,6 +423,8 @@ enum {
     MOE_TRACE_DISPATCH_FP8_ROWS = 10,  /* quantising row pipeline */
     MOE_TRACE_COMBINE = 11,
     MOE_TRACE_LAYOUT_ROWS = 12,        /* lookback tiles launched one after another: rows */
+    MOE_TRACE_GATE = 13,
+    MOE_TRACE_GATE_BACKWARD = 14,
     MOE_TRACE_PHASE = 0x10000          /* warp field of a per-CTA phase record: MOE_TRACE_PHASE + phase */
 };
 
@@ -526,6 +530,71 @@ MOE_API int moe_combine_ex(const void *partial, int num_partial_rows, int num_to
                            const int32_t *token_dst_row, const float *row_weights,
                            const float *recv_topk_weights, float *combined_topk_weights, void *out,
                            uint32_t *balance, int32_t *status, void *stream);
+
+/*
+ * moe_topk_gate -- the router's gate: the experts of each token and their
+ * weights, from the router's logits l [T, E]. Its outputs are the topk_idx and
+ * topk_weights that every other entry point takes (a library addition; the
+ * pages start from given choices).
+ *
+ *   s[t, e] = softmax over e of l[t]         (MOE_GATE_SOFTMAX)
+ *           = 1 / (1 + exp(-l[t, e]))        (MOE_GATE_SIGMOID)
+ *   topk_idx[t]        = the k largest l[t, e], largest first; with `bias`, the k
+ *                        largest s[t, e] + bias[e] (fp32). Ties go to the lowest
+ *                        expert. (Both scores keep the logits' order, so a
+ *                        choice without bias involves no rounding.)
+ *   topk_weights[t, j] = scale * s[t, e_j], or with MOE_GATE_NORMALIZE
+ *                        scale * s[t, e_j] / sum_m s[t, e_m], fp32; the bias is
+ *                        not part of the weights.
+ * A logit of -inf masks its expert: it is never chosen. A row with fewer than
+ * k unmasked experts gets -1 and weight 0 in its last entries (all of them when
+ * the row is masked whole). The lowest finite value is an ordinary logit. A
+ * NaN logit raises MOE_ERR_BAD_LOGIT and is masked, a NaN bias masks its
+ * expert from the choice. Logits of +inf share the softmax evenly.
+ *
+ *   logits        [T, E] fp32 or bf16 (logits_type), device.
+ *   bias          [E] fp32 or NULL.
+ *   mode          MOE_GATE_SOFTMAX or MOE_GATE_SIGMOID, optionally OR-ed with
+ *                 MOE_GATE_NORMALIZE.
+ *   topk_idx      [T, k] int64, output.
+ *   topk_weights  [T, k] fp32, output.
+ * Limits: 1 <= k <= min(32, E), E <= 8192, T * k < 2^31.
+ */
+enum { MOE_LOGITS_F32 = 0, MOE_LOGITS_BF16 = 1 };
+typedef enum {
+    MOE_GATE_SOFTMAX = 0,
+    MOE_GATE_SIGMOID = 1,
+    MOE_GATE_NORMALIZE = 0x100   /* flag, OR-ed with one of the above */
+} moe_gate_mode_t;
+
+MOE_API int moe_topk_gate(const void *logits, int logits_type, const float *bias, int num_tokens, int num_topk,
+                          int num_experts, int mode, float scale, int64_t *topk_idx, float *topk_weights,
+                          int32_t *status, void *stream);
+
+/*
+ * moe_topk_gate_backward -- the gradient of moe_topk_gate's weights with
+ * respect to the logits (the choice itself has none).
+ *
+ * With g[j] = scale * grad_weights[t, j] and s, q the scores of the logits and
+ * the normalised scores of the chosen ones:
+ *   softmax              dl[i]   = s_i (sum_{j: e_j = i} g_j - sum_j g_j s_{e_j})
+ *   softmax, normalised  dl[e_j] = q_j (g_j - sum_m g_m q_m), 0 elsewhere
+ *   sigmoid              dl[e_j] = g_j s_{e_j} (1 - s_{e_j}), 0 elsewhere
+ *   sigmoid, normalised  dl[e_j] = q_j (1 - s_{e_j}) (g_j - sum_m g_m q_m), 0 elsewhere
+ * computed in fp32 from the logits (nothing of the forward call is kept) and
+ * rounded once to the logits' type. Every element is written. Entries of -1 and
+ * entries that name a masked logit have no part in it; other entries outside
+ * [0, E) raise MOE_ERR_BAD_TOPK and are treated as masked. An expert named by
+ * several entries gets the sum of their parts.
+ *
+ *   topk_idx      [T, k] int64, moe_topk_gate's output (or another choice).
+ *   grad_weights  [T, k] fp32, the loss's gradient with respect to topk_weights.
+ *   grad_logits   [T, E], the logits' type, output.
+ * Other arguments and limits as for moe_topk_gate.
+ */
+MOE_API int moe_topk_gate_backward(const void *logits, int logits_type, const int64_t *topk_idx,
+                                   const float *grad_weights, int num_tokens, int num_topk, int num_experts, int mode,
+                                   float scale, void *grad_logits, int32_t *status, void *stream);
 
 /* Human-readable name of a moe_status_t value (static string). */
 MOE_API const char *moe_status_string(int status);
