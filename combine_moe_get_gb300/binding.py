@@ -33,6 +33,7 @@ MOE_ERR_TIMEOUT = 5
 MOE_ERR_CUDA = 6
 MOE_ERR_WORKSPACE = 7
 MOE_ERR_BAD_LOGIT = 8
+MOE_ERR_BAD_ADAPTER = 9
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -108,6 +109,17 @@ def _configure(lib):
     lib.moe_topk_gate.restype = _I
     lib.moe_topk_gate_backward.argtypes = [_P, _I, _P, _P, _I, _I, _I, _I, ctypes.c_float, _P, _P, _P]
     lib.moe_topk_gate_backward.restype = _I
+    lib.moe_experts_workspace_size.argtypes = [_I, _I, _I, _I, _I]
+    lib.moe_experts_workspace_size.restype = ctypes.c_size_t
+    lib.moe_experts.argtypes = [_P, _I, _I, _P, _P, _I, _I, _P, _P, _P, _P, _I, _I, _P, _P, ctypes.c_size_t, _P, _P]
+    lib.moe_experts.restype = _I
+    lib.moe_layer.argtypes = [_P, _I, _I, _P, _I, _P, _I, _I, _I, ctypes.c_float, _P, _P, _P, _P, _P, _P, _I, _I, _P,
+                              _P, ctypes.c_size_t, _P, _P]
+    lib.moe_layer.restype = _I
+    lib.moe_adapter_linear_workspace_size.argtypes = [_I, _I, _I, _I, _I]
+    lib.moe_adapter_linear_workspace_size.restype = ctypes.c_size_t
+    lib.moe_adapter_linear.argtypes = [_P, _I, _I, _P, _I, _P, _P, _P, _P, _I, _I, _P, _P, ctypes.c_size_t, _P, _P]
+    lib.moe_adapter_linear.restype = _I
     return lib
 
 
@@ -131,7 +143,8 @@ TRACE_RECORD = np.dtype([("kernel", "<u4"), ("cta", "<u4"), ("warp", "<u4"), ("s
                          ("start_ns", "<u8"), ("end_ns", "<u8")])
 TRACE_KERNELS = {1: "layout_tiles", 2: "layout_direct", 3: "layout_cluster", 4: "layout_count", 5: "layout_scan",
                  6: "layout_rows_scan", 7: "expand_layout", 8: "expand_layout_cluster", 9: "dispatch",
-                 10: "dispatch_fp8_rows", 11: "combine", 12: "layout_rows", 13: "gate", 14: "gate_backward"}
+                 10: "dispatch_fp8_rows", 11: "combine", 12: "layout_rows", 13: "gate", 14: "gate_backward",
+                 15: "experts", 16: "adapter_shrink", 17: "adapter_project"}
 TRACE_PHASE = 0x10000   # warp field of a per-CTA phase record: TRACE_PHASE + phase (1, 2, ...)
 TRACE_PHASE_NAMES = {3: ("dependency wait", "top-k tile loaded", "bitmap and expert histogram",
                          "tile counts and first cluster barrier", "exchange and second barrier",
@@ -504,4 +517,118 @@ def moe_topk_gate_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_we
                                       _gate_mode(score, normalize), float(scale), _ptr(out), _ptr(status),
                                       _stream(stream))
     _check(code, "moe_topk_gate_backward")
+    return out
+
+
+MOE_WEIGHTS_BF16 = 0
+MOE_WEIGHTS_E4M3 = 1
+
+
+def moe_experts_workspace_size(num_tokens: int, hidden: int, intermediate: int, num_topk: int,
+                               num_experts: int) -> int:
+    return int(LIB.moe_experts_workspace_size(num_tokens, hidden, intermediate, num_topk, num_experts))
+
+
+def _expert_weights(x, w13, w2, w13_scales, w2_scales):
+    """(H, I, E, weight type) of one layer's experts, after checking types and shapes."""
+    T, H = x.shape
+    E, I = w2.shape[0], w2.shape[2]
+    e4m3 = w13.dtype == torch.uint8
+    dtype = torch.uint8 if e4m3 else torch.bfloat16
+    _typed(x, torch.bfloat16, (T, H), "x")
+    _typed(w13, dtype, (E, 2 * I, H), "w13")
+    _typed(w2, dtype, (E, H, I), "w2")
+    if e4m3 and (w13_scales is None or w2_scales is None):
+        raise ValueError("E4M3 weights need w13_scales and w2_scales")
+    if not e4m3 and (w13_scales is not None or w2_scales is not None):
+        raise ValueError("bf16 weights take no scales")
+    _typed(w13_scales, torch.float32, (E, 2 * I, H // 128), "w13_scales")
+    _typed(w2_scales, torch.float32, (E, H, I // 128), "w2_scales")
+    return H, I, E, MOE_WEIGHTS_E4M3 if e4m3 else MOE_WEIGHTS_BF16
+
+
+def moe_experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor, w13: torch.Tensor,
+                w2: torch.Tensor, *, w13_scales: Optional[torch.Tensor] = None,
+                w2_scales: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                stream=None) -> torch.Tensor:
+    """out[t] = sum_j topk_weights[t, j] * w2[e] (silu(gate) * up), [gate; up] = w13[e] x[t] and
+    e = topk_idx[t, j], for a few tokens (T <= 1024). Weights are bf16, or E4M3
+    codes (uint8) with a scale per row and 128 columns."""
+    H, I, E, wtype = _expert_weights(x, w13, w2, w13_scales, w2_scales)
+    T, k = topk_idx.shape
+    _typed(topk_idx, torch.int64, (x.shape[0], k), "topk_idx")
+    _typed(topk_weights, torch.float32, (T, k), "topk_weights")
+    out = torch.empty_like(x) if out is None else _typed(out, torch.bfloat16, (T, H), "out")
+    if workspace is None:
+        workspace = torch.empty(max(moe_experts_workspace_size(T, H, I, k, E), 16), dtype=torch.uint8, device=x.device)
+    status = new_status(x.device) if status is None else status
+    code = LIB.moe_experts(_ptr(x), T, H, _ptr(topk_idx), _ptr(topk_weights), k, E, _ptr(w13), _ptr(w13_scales),
+                           _ptr(w2), _ptr(w2_scales), I, wtype, _ptr(out), _ptr(workspace),
+                           workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+    _check(code, "moe_experts")
+    return out
+
+
+def moe_layer(x: torch.Tensor, logits: torch.Tensor, num_topk: int, w13: torch.Tensor, w2: torch.Tensor, *,
+              w13_scales: Optional[torch.Tensor] = None, w2_scales: Optional[torch.Tensor] = None,
+              bias: Optional[torch.Tensor] = None, score: str = "softmax", normalize: bool = True, scale: float = 1.0,
+              out: Optional[torch.Tensor] = None, topk_idx: Optional[torch.Tensor] = None,
+              topk_weights: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+              status: Optional[torch.Tensor] = None,
+              stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """moe_topk_gate of ``logits`` [T, E] and moe_experts of the choice in one
+    call. Returns (out, topk_idx, topk_weights)."""
+    H, I, E, wtype = _expert_weights(x, w13, w2, w13_scales, w2_scales)
+    T, dev = x.shape[0], x.device
+    _typed(logits, logits.dtype, (T, E), "logits")
+    _typed(bias, torch.float32, (E,), "bias")
+    out = torch.empty_like(x) if out is None else _typed(out, torch.bfloat16, (T, H), "out")
+    topk_idx = (torch.empty(T, num_topk, dtype=torch.int64, device=dev) if topk_idx is None else
+                _typed(topk_idx, torch.int64, (T, num_topk), "topk_idx"))
+    topk_weights = (torch.empty(T, num_topk, dtype=torch.float32, device=dev) if topk_weights is None else
+                    _typed(topk_weights, torch.float32, (T, num_topk), "topk_weights"))
+    if workspace is None:
+        workspace = torch.empty(max(moe_experts_workspace_size(T, H, I, num_topk, E), 16), dtype=torch.uint8,
+                                device=dev)
+    status = new_status(dev) if status is None else status
+    code = LIB.moe_layer(_ptr(x), T, H, _ptr(logits), _logits_type(logits), _ptr(bias), num_topk, E,
+                         _gate_mode(score, normalize), float(scale), _ptr(topk_idx), _ptr(topk_weights), _ptr(w13),
+                         _ptr(w13_scales), _ptr(w2), _ptr(w2_scales), I, wtype, _ptr(out), _ptr(workspace),
+                         workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+    _check(code, "moe_layer")
+    return out, topk_idx, topk_weights
+
+
+def moe_adapter_linear_workspace_size(num_tokens: int, in_features: int, out_features: int, num_adapters: int,
+                                      rank: int) -> int:
+    return int(LIB.moe_adapter_linear_workspace_size(num_tokens, in_features, out_features, num_adapters, rank))
+
+
+def moe_adapter_linear(x: torch.Tensor, w: torch.Tensor, adapter_idx: torch.Tensor, a: torch.Tensor, b: torch.Tensor,
+                       scales: torch.Tensor, *, out: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """out[t] = w x[t] + scales[i] * b[i] (a[i] x[t]) with i = adapter_idx[t]
+    (-1: no adapter). x [T, K], w [N, K], a [L, r, K], b [L, N, r] bf16;
+    adapter_idx int32 [T]; scales fp32 [L]."""
+    T, K = x.shape
+    N = w.shape[0]
+    L, r, _ = a.shape
+    _typed(x, torch.bfloat16, (T, K), "x")
+    _typed(w, torch.bfloat16, (N, K), "w")
+    _typed(a, torch.bfloat16, (L, r, K), "a")
+    _typed(b, torch.bfloat16, (L, N, r), "b")
+    _typed(adapter_idx, torch.int32, (T,), "adapter_idx")
+    _typed(scales, torch.float32, (L,), "scales")
+    out = (torch.empty(T, N, dtype=torch.bfloat16, device=x.device) if out is None else
+           _typed(out, torch.bfloat16, (T, N), "out"))
+    if workspace is None:
+        workspace = torch.empty(max(moe_adapter_linear_workspace_size(T, K, N, L, r), 16), dtype=torch.uint8,
+                                device=x.device)
+    status = new_status(x.device) if status is None else status
+    code = LIB.moe_adapter_linear(_ptr(x), T, K, _ptr(w), N, _ptr(adapter_idx), _ptr(a), _ptr(b), _ptr(scales), L, r,
+                                  _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                  _ptr(status), _stream(stream))
+    _check(code, "moe_adapter_linear")
     return out

@@ -256,6 +256,7 @@ MOE_API const char *moe_status_string(int status) {
         case MOE_ERR_CUDA: return "MOE_ERR_CUDA";
         case MOE_ERR_WORKSPACE: return "MOE_ERR_WORKSPACE";
         case MOE_ERR_BAD_LOGIT: return "MOE_ERR_BAD_LOGIT";
+        case MOE_ERR_BAD_ADAPTER: return "MOE_ERR_BAD_ADAPTER";
         default: return "MOE_ERR_UNKNOWN";
     }
 }
@@ -566,6 +567,102 @@ MOE_API int moe_topk_gate_backward(const void *logits, int logits_type, const in
     return moe::launch_gate_backward(moe::GateBackwardLaunch{logits, logits_type, topk_idx, grad_weights, num_tokens,
                                                              num_topk, num_experts, mode, scale, grad_logits, status,
                                                              stream});
+}
+
+constexpr int kMaxFeatures = 1 << 20;   // widest hidden, intermediate or projection size
+
+static bool experts_shape_ok(int T, int H, int I, int k, int E) {
+    if (!shape_ok(T, k, E, 1) || T > MOE_EXPERTS_MAX_TOKENS) return false;
+    if (H < 8 || H % 8 != 0 || H > kMaxFeatures || I < 8 || I % 8 != 0 || I > kMaxFeatures) return false;
+    return (int64_t)E * 2 * I < (int64_t)1 << 31 && (int64_t)E * H < (int64_t)1 << 31;
+}
+
+MOE_API size_t moe_experts_workspace_size(int num_tokens, int hidden, int intermediate, int num_topk, int num_experts) {
+    if (!experts_shape_ok(num_tokens, hidden, intermediate, num_topk, num_experts)) return 0;
+    return moe::experts_workspace_bytes(num_tokens, hidden, intermediate, num_topk, num_experts);
+}
+
+static int experts_prepare(const void *x, int T, int H, const int64_t *topk_idx, const float *topk_weights, int k,
+                           int E, const void *w13, const float *w13_scales, const void *w2, const float *w2_scales,
+                           int I, int weight_type, void *out, void *workspace, size_t workspace_bytes,
+                           int32_t *status, void *stream, moe::ExpertsLaunch &L) {
+    if (!experts_shape_ok(T, H, I, k, E)) return MOE_ERR_INVALID_ARG;
+    if (weight_type != MOE_WEIGHTS_BF16 && weight_type != MOE_WEIGHTS_E4M3) return MOE_ERR_INVALID_ARG;
+    const bool e4m3 = weight_type == MOE_WEIGHTS_E4M3;
+    if (e4m3 && (H % 128 != 0 || I % 128 != 0)) return MOE_ERR_INVALID_ARG;
+    if ((w13_scales != nullptr) != e4m3 || (w2_scales != nullptr) != e4m3) return MOE_ERR_INVALID_ARG;
+    if (!status) return MOE_ERR_INVALID_ARG;
+    if (!aligned(status, 4)) return MOE_ERR_MISALIGNED;
+    if (T > 0) {
+        if (!x || !topk_idx || !topk_weights || !w13 || !w2 || !out || !workspace) return MOE_ERR_INVALID_ARG;
+        if (!aligned(x, 16) || !aligned(topk_idx, 8) || !aligned(topk_weights, 4) || !aligned(w13, 16) ||
+            !aligned(w2, 16) || !aligned(w13_scales, 4) || !aligned(w2_scales, 4) || !aligned(out, 16) ||
+            !aligned(workspace, 16))
+            return MOE_ERR_MISALIGNED;
+        if (workspace_bytes < moe::experts_workspace_bytes(T, H, I, k, E)) return MOE_ERR_WORKSPACE;
+    }
+    L = moe::ExpertsLaunch{x, T, H, topk_idx, topk_weights, k, E, w13, w13_scales, w2, w2_scales, I,
+                           out, workspace, status, stream};
+    return MOE_OK;
+}
+
+MOE_API int moe_experts(const void *x, int num_tokens, int hidden, const int64_t *topk_idx,
+                        const float *topk_weights, int num_topk, int num_experts, const void *w13,
+                        const float *w13_scales, const void *w2, const float *w2_scales, int intermediate,
+                        int weight_type, void *out, void *workspace, size_t workspace_bytes, int32_t *status,
+                        void *stream) {
+    moe::ExpertsLaunch L;
+    const int rc = experts_prepare(x, num_tokens, hidden, topk_idx, topk_weights, num_topk, num_experts, w13,
+                                   w13_scales, w2, w2_scales, intermediate, weight_type, out, workspace,
+                                   workspace_bytes, status, stream, L);
+    return rc != MOE_OK ? rc : moe::launch_experts(L);
+}
+
+MOE_API int moe_layer(const void *x, int num_tokens, int hidden, const void *logits, int logits_type,
+                      const float *bias, int num_topk, int num_experts, int mode, float scale, int64_t *topk_idx,
+                      float *topk_weights, const void *w13, const float *w13_scales, const void *w2,
+                      const float *w2_scales, int intermediate, int weight_type, void *out, void *workspace,
+                      size_t workspace_bytes, int32_t *status, void *stream) {
+    int rc = gate_check(logits, logits_type, num_tokens, num_topk, num_experts, mode, topk_idx, topk_weights, status);
+    if (rc != MOE_OK) return rc;
+    if (!aligned(bias, 4)) return MOE_ERR_MISALIGNED;
+    moe::ExpertsLaunch L;
+    rc = experts_prepare(x, num_tokens, hidden, topk_idx, topk_weights, num_topk, num_experts, w13, w13_scales, w2,
+                         w2_scales, intermediate, weight_type, out, workspace, workspace_bytes, status, stream, L);
+    if (rc != MOE_OK) return rc;
+    rc = moe::launch_gate(moe::GateLaunch{logits, logits_type, bias, num_tokens, num_topk, num_experts, mode, scale,
+                                          topk_idx, topk_weights, status, stream});
+    return rc != MOE_OK ? rc : moe::launch_experts(L);
+}
+
+static bool adapter_shape_ok(int T, int K, int N, int L, int r) {
+    if (T < 0 || T > (1 << 20) || L < 1 || L > MOE_MAX_ADAPTERS) return false;
+    if (K < 8 || K % 8 != 0 || K > kMaxFeatures || N < 8 || N % 8 != 0 || N > kMaxFeatures) return false;
+    return r >= 8 && r % 8 == 0 && r <= MOE_MAX_ADAPTER_RANK;
+}
+
+MOE_API size_t moe_adapter_linear_workspace_size(int num_tokens, int in_features, int out_features, int num_adapters,
+                                                 int rank) {
+    if (!adapter_shape_ok(num_tokens, in_features, out_features, num_adapters, rank)) return 0;
+    return moe::adapter_workspace_bytes(num_tokens, in_features, out_features, num_adapters, rank);
+}
+
+MOE_API int moe_adapter_linear(const void *x, int num_tokens, int in_features, const void *w, int out_features,
+                               const int32_t *adapter_idx, const void *a, const void *b, const float *scales,
+                               int num_adapters, int rank, void *out, void *workspace, size_t workspace_bytes,
+                               int32_t *status, void *stream) {
+    const int T = num_tokens, K = in_features, N = out_features;
+    if (!adapter_shape_ok(T, K, N, num_adapters, rank) || !status) return MOE_ERR_INVALID_ARG;
+    if (!aligned(status, 4)) return MOE_ERR_MISALIGNED;
+    if (T > 0) {
+        if (!x || !w || !adapter_idx || !a || !b || !scales || !out || !workspace) return MOE_ERR_INVALID_ARG;
+        if (!aligned(x, 16) || !aligned(w, 16) || !aligned(adapter_idx, 4) || !aligned(a, 16) || !aligned(b, 16) ||
+            !aligned(scales, 4) || !aligned(out, 16) || !aligned(workspace, 16))
+            return MOE_ERR_MISALIGNED;
+        if (workspace_bytes < moe::adapter_workspace_bytes(T, K, N, num_adapters, rank)) return MOE_ERR_WORKSPACE;
+    }
+    return moe::launch_adapter_linear(moe::AdapterLaunch{x, T, K, w, N, adapter_idx, a, b, scales, num_adapters, rank,
+                                                         out, workspace, status, stream});
 }
 
 }  // extern "C"

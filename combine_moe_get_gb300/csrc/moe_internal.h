@@ -1,6 +1,6 @@
 // moe_internal.h -- host-side interfaces between the C ABI entry points
 // (moe_api.cu) and the kernel launchers (layout.cu, expand.cu, dispatch.cu,
-// combine.cu, gate.cu).
+// combine.cu, gate.cu, experts.cu, adapter.cu).
 // Arguments reaching a launcher have already been validated.
 #pragma once
 
@@ -296,5 +296,43 @@ struct GateBackwardLaunch {
 };
 
 int launch_gate_backward(const GateBackwardLaunch &L);
+
+struct ExpertsLaunch {
+    const void *x;
+    int num_tokens, hidden;
+    const int64_t *topk_idx;
+    const float *topk_weights;
+    int num_topk, num_experts;
+    const void *w13;
+    const float *w13_scales;   // with w2_scales: E4M3 codes; both null: bf16
+    const void *w2;
+    const float *w2_scales;
+    int intermediate;
+    void *out;
+    void *workspace;
+    int32_t *status;
+    void *stream;
+};
+
+size_t experts_workspace_bytes(int T, int H, int I, int k, int E);
+int launch_experts(const ExpertsLaunch &L);
+
+struct AdapterLaunch {
+    const void *x;
+    int num_tokens, in_features;
+    const void *w;
+    int out_features;
+    const int32_t *adapter_idx;
+    const void *a, *b;
+    const float *scales;
+    int num_adapters, rank;
+    void *out;
+    void *workspace;
+    int32_t *status;
+    void *stream;
+};
+
+size_t adapter_workspace_bytes(int T, int K, int N, int L, int r);
+int launch_adapter_linear(const AdapterLaunch &L);
 
 }  // namespace moe

@@ -29,8 +29,9 @@
  *     [-1, E); that entry is treated as masked), MOE_ERR_CAPACITY (a receive row
  *     at or beyond the receive capacity; that row is not written / not read),
  *     MOE_ERR_TIMEOUT (a bounded wait inside a kernel ran out; the outputs of
- *     that call are unspecified) and MOE_ERR_BAD_LOGIT (a NaN router logit; that
- *     expert is treated as masked).
+ *     that call are unspecified), MOE_ERR_BAD_LOGIT (a NaN router logit; that
+ *     expert is treated as masked) and MOE_ERR_BAD_ADAPTER (an adapter index
+ *     outside [-1, L); that row is treated as having no adapter).
  *   - T == 0 is a valid no-op that still writes zero counts and prefixes.
  */
 #ifndef MOE_GET_H
@@ -58,13 +59,17 @@ typedef enum {
     MOE_ERR_TIMEOUT = 5,
     MOE_ERR_CUDA = 6,
     MOE_ERR_WORKSPACE = 7,
-    MOE_ERR_BAD_LOGIT = 8
+    MOE_ERR_BAD_LOGIT = 8,
+    MOE_ERR_BAD_ADAPTER = 9
 } moe_status_t;
 
 /* Limits checked on the host (MOE_ERR_INVALID_ARG beyond them). */
 #define MOE_MAX_TOPK 32
 #define MOE_MAX_RANKS 1024
 #define MOE_MAX_EXPERTS 8192
+#define MOE_EXPERTS_MAX_TOKENS 1024   /* moe_experts, moe_layer: a few tokens */
+#define MOE_MAX_ADAPTERS 8192
+#define MOE_MAX_ADAPTER_RANK 128
 
 /* Outputs of moe_get_layout: all DEVICE pointers, caller-owned. */
 typedef struct {
@@ -425,6 +430,9 @@ enum {
     MOE_TRACE_LAYOUT_ROWS = 12,        /* lookback tiles launched one after another: rows */
     MOE_TRACE_GATE = 13,
     MOE_TRACE_GATE_BACKWARD = 14,
+    MOE_TRACE_EXPERTS = 15,
+    MOE_TRACE_ADAPTER_SHRINK = 16,
+    MOE_TRACE_ADAPTER_PROJECT = 17,
     MOE_TRACE_PHASE = 0x10000          /* warp field of a per-CTA phase record: MOE_TRACE_PHASE + phase */
 };
 
@@ -595,6 +603,91 @@ MOE_API int moe_topk_gate(const void *logits, int logits_type, const float *bias
 MOE_API int moe_topk_gate_backward(const void *logits, int logits_type, const int64_t *topk_idx,
                                    const float *grad_weights, int num_tokens, int num_topk, int num_experts, int mode,
                                    float scale, void *grad_logits, int32_t *status, void *stream);
+
+/* Weights of the experts: bf16, or E4M3 codes with fp32 scales. */
+enum { MOE_WEIGHTS_BF16 = 0, MOE_WEIGHTS_E4M3 = 1 };
+
+/* Bytes of device workspace moe_experts and moe_layer need (16-byte aligned
+ * pointer required). Host-only; never fails (0 for invalid sizes). */
+MOE_API size_t moe_experts_workspace_size(int num_tokens, int hidden, int intermediate, int num_topk, int num_experts);
+
+/*
+ * moe_experts -- the experts of a few tokens and their weighted sum: what
+ * stands between a choice of experts and the layer's output when the batch is
+ * too small to be worth a dispatch (decode). A library addition; the pages
+ * leave the experts' products to a grouped GEMM between dispatch and combine.
+ *
+ *   h[t, j] = silu(w13[e, 0:I] x[t]) * (w13[e, I:2I] x[t]),  e = topk_idx[t, j]
+ *   out[t]  = bf16_rn( sum_j topk_weights[t, j] * (w2[e] h[t, j]) )
+ * with silu(z) = z / (1 + exp(-z)). Products are summed in fp32; the terms of
+ * out[t] are added in fp32 in an order fixed by the sizes and the choice.
+ * Entries of -1 (masked, or another rank's: a dispatch's recv_topk_idx with its
+ * recv_x is such a choice) add nothing, whatever their weight; other entries
+ * outside [0, E) raise MOE_ERR_BAD_TOPK and are treated as masked. A token
+ * without entries gets +0. An expert that no entry names is not read.
+ *
+ *   x              [T, H] bf16, 16-byte aligned.
+ *   topk_idx       [T, k] int64; topk_weights [T, k] fp32 (moe_topk_gate's outputs).
+ *   w13            [E, 2I, H]: gate rows, then up rows, of each expert; w2 [E, H, I].
+ *                  bf16, or with MOE_WEIGHTS_E4M3 E4M3 codes (uint8) with
+ *   w13_scales     [E, 2I, H/128] and w2_scales [E, H, I/128] fp32: a weight is
+ *                  its code's value times its row's scale of the 128 columns (what
+ *                  MOE_DISPATCH_QUANTIZE_FP8 makes of the rows). NULL for bf16.
+ *   out            [T, H] bf16, 16-byte aligned; not one of the inputs.
+ *   workspace      at least moe_experts_workspace_size() bytes; need not be
+ *                  initialised; not shared by calls that overlap on the GPU.
+ * Limits: T <= 1024, 1 <= k <= 32, E <= 8192, H and I multiples of 8 up to 2^20
+ * (of 128 with E4M3), E * 2I and E * H < 2^31.
+ */
+MOE_API int moe_experts(const void *x, int num_tokens, int hidden, const int64_t *topk_idx,
+                        const float *topk_weights, int num_topk, int num_experts, const void *w13,
+                        const float *w13_scales, const void *w2, const float *w2_scales, int intermediate,
+                        int weight_type, void *out, void *workspace, size_t workspace_bytes, int32_t *status,
+                        void *stream);
+
+/*
+ * moe_layer -- a whole mixture-of-experts layer of a few tokens behind its
+ * router's product: moe_topk_gate of the logits, then moe_experts of the choice.
+ * topk_idx and topk_weights are outputs here; everything else as for the two.
+ */
+MOE_API int moe_layer(const void *x, int num_tokens, int hidden, const void *logits, int logits_type,
+                      const float *bias, int num_topk, int num_experts, int mode, float scale, int64_t *topk_idx,
+                      float *topk_weights, const void *w13, const float *w13_scales, const void *w2,
+                      const float *w2_scales, int intermediate, int weight_type, void *out, void *workspace,
+                      size_t workspace_bytes, int32_t *status, void *stream);
+
+/* Bytes of device workspace moe_adapter_linear needs (16-byte aligned pointer
+ * required). Host-only; never fails (0 for invalid sizes). */
+MOE_API size_t moe_adapter_linear_workspace_size(int num_tokens, int in_features, int out_features, int num_adapters,
+                                                 int rank);
+
+/*
+ * moe_adapter_linear -- a projection that all rows share, with the low-rank
+ * adapter of each row's request beside it (a library addition; rows choose one
+ * of many small weight sets, as tokens choose experts).
+ *
+ *   out[t] = bf16_rn( w x[t] + scales[i] * b[i] (a[i] x[t]) ),  i = adapter_idx[t]
+ *   out[t] = bf16_rn( w x[t] )                                 for adapter_idx[t] = -1
+ * Products are summed in fp32 and the adapter's inner vector is kept in fp32.
+ * Adapters may follow one another in any order; rows of one adapter next to each
+ * other share its reads. An adapter reaches the rows that name it and no other
+ * (its infinities and NaN too). An index outside [-1, L) raises
+ * MOE_ERR_BAD_ADAPTER and counts as -1.
+ *
+ *   x            [T, K] bf16, w [N, K] bf16, both 16-byte aligned.
+ *   adapter_idx  [T] int32.
+ *   a            [L, r, K] bf16, b [L, N, r] bf16, scales [L] fp32; an adapter of a
+ *                lower rank has zeros in its last rows of a and columns of b.
+ *   out          [T, N] bf16, 16-byte aligned; not one of the inputs.
+ *   workspace    at least moe_adapter_linear_workspace_size() bytes; need not be
+ *                initialised; not shared by calls that overlap on the GPU.
+ * Limits: K, N and r multiples of 8, K and N up to 2^20, r <= 128, L <= 8192,
+ * T <= 2^20, T * N < 2^40.
+ */
+MOE_API int moe_adapter_linear(const void *x, int num_tokens, int in_features, const void *w, int out_features,
+                               const int32_t *adapter_idx, const void *a, const void *b, const float *scales,
+                               int num_adapters, int rank, void *out, void *workspace, size_t workspace_bytes,
+                               int32_t *status, void *stream);
 
 /* Human-readable name of a moe_status_t value (static string). */
 MOE_API const char *moe_status_string(int status);
