@@ -3,109 +3,348 @@
 //   h[t, j]  = silu(G x_t) * (U x_t),  [G; U] = w13[e], e = topk_idx[t, j]
 //   out[t]   = sum_j topk_weights[t, j] * (w2[e] h[t, j])
 //
-// One warp per element of h, then one warp per element of out; every sum is
-// fp32, in a fixed order, and out is rounded once to bf16.
+// Two kernels. The plan kernel (one CTA) sorts the valid entries by expert and
+// cuts each expert's into groups of at most `cols` entries. The experts kernel
+// (one CTA per SM, launched cooperatively) runs skinny.cuh's body over two
+// lines of work: phase 0 makes h (a tile is 128 gate and the same 128 up rows,
+// so that one thread holds both sums of an element), phase 1 multiplies h by w2
+// (a tile is 256 rows) into y, one fp32 row per entry. A group's phase 1 waits
+// until all its h tiles are done; the loads of w2 do not wait, so the stream of
+// weights goes on across the border. When all of y is there, all CTAs add each
+// token's rows in entry order with their weights and round once to bf16.
+//
+// h is rounded to bf16: it is the operand of a bf16 product, and the rounding's
+// effect on an output is of the size of that output's own rounding.
 #include <algorithm>
 #include <cuda_bf16.h>
 
-#include "moe_common.cuh"
+#include "skinny.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr uint32_t kFull = 0xffffffffu;
+using skinny::kRows;
 
-struct ExpertArgs {
-    ExpertsLaunch p;
-    float *h;   // [T * k, I]
+constexpr int kPlanThreads = 1024;
+
+// Device workspace, in this order.
+struct Space {
+    size_t words, groups, order, h, y, partial, total;   // byte offsets
+    int cols, max_groups;
+};
+// words: [0] groups, [1] finished phase 1 tiles, [2..] arrivals [2][kMaxCtas], then ready [max_groups]
+constexpr int kArrivals = 2, kReady = 2 + 2 * skinny::kMaxCtas;
+
+int columns(int T, bool e4m3) { return std::min((T + 15) / 16 * 16, e4m3 ? 64 : 128); }
+
+Space space(int T, int H, int I, int k, int cols) {
+    Space s{};
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += (bytes + 255) / 256 * 256;
+        return o;
+    };
+    const size_t n = (size_t)T * k;
+    s.cols = cols;
+    s.max_groups = (int)n;
+    s.words = take((kReady + n) * 4);
+    s.groups = take(n * sizeof(int4));
+    s.order = take(n * 4);
+    s.h = take(n * I * 2);
+    s.y = take(n * H * 4);
+    s.partial = take((size_t)2 * skinny::kMaxCtas * 2 * 2 * cols * kRows * 4);
+    s.total = at;
+    return s;
+}
+
+// ------------------------------------------------------------------ plan
+
+struct PlanArgs {
+    const int64_t *topk_idx;
+    int n, E, cols;          // entries, experts, largest group
+    uint32_t *words;
+    int num_words;
+    int4 *groups;            // {expert, first sorted entry, entries, 0}
+    int *order;              // sorted entries
+    int32_t *status;
     TraceArgs trace;
 };
 
-__device__ __forceinline__ float warp_sum(float v) {
+// The order of an expert's entries is the arrival order of the counters: it says
+// only which column of a product an entry takes, and columns do not depend on
+// one another.
+__global__ void __launch_bounds__(kPlanThreads) experts_plan_kernel(const PlanArgs a) {
+    WarpTrace wt(a.trace, MOE_TRACE_EXPERTS_PLAN);
+    grid_dependency_wait();
+    extern __shared__ int32_t plan_smem[];
+    int32_t *start = plan_smem, *first_group = plan_smem + a.E + 1;
+    for (int i = threadIdx.x; i <= a.E; i += kPlanThreads) start[i] = 0;
+    for (int i = threadIdx.x; i < a.num_words; i += kPlanThreads) a.words[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
+        const int64_t e = a.topk_idx[i];
+        if (e >= 0 && e < a.E) atomicAdd(&start[e], 1);
+        else if (e != -1) report(a.status, MOE_ERR_BAD_TOPK);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kPlanThreads) first_group[e] = (start[e] + a.cols - 1) / a.cols;
+    __syncthreads();
+    if (threadIdx.x < 32) warp_exclusive_scan(start, a.E, threadIdx.x);
+    else if (threadIdx.x < 64) warp_exclusive_scan(first_group, a.E, threadIdx.x - 32);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kPlanThreads) {
+        const int end = start[e + 1];
+        for (int g = first_group[e], b = start[e]; b < end; ++g, b += a.cols)
+            a.groups[g] = make_int4(e, b, min(a.cols, end - b), 0);
+    }
+    if (threadIdx.x == 0) a.words[0] = first_group[a.E];
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
+        const int64_t e = a.topk_idx[i];
+        if (e >= 0 && e < a.E) a.order[atomicAdd(&start[e], 1)] = i;
+    }
+}
+
+// ------------------------------------------------------------------ experts
+
+struct ExpertsArgs {
+    CUtensorMap w13, w2, x, h_map;
+    const int64_t *topk_idx;
+    const float *topk_weights;
+    const float *s13, *s2;
+    uint32_t *words;
+    const int4 *groups;
+    const int *order;
+    __nv_bfloat16 *h;
+    float *y, *partials;
+    __nv_bfloat16 *out;
+    int32_t *status;
+    int T, H, I, k, E;
+    skinny::Shape shape;
+    uint32_t tmem_cols;
+    TraceArgs trace;
+};
+
+template <bool kE4m3>
+struct ExpertsProblem {
+    const ExpertsArgs &a;
+    int G;
+    int32_t *status;
+    int tiles[2], kbs[2];   // tiles per group and K blocks per tile of the two phases
+
+    __device__ explicit ExpertsProblem(const ExpertsArgs &args) : a(args), G((int)args.words[0]), status(args.status) {
+        constexpr int block = kE4m3 ? 128 : 64;
+        tiles[0] = (a.I + kRows - 1) / kRows;
+        tiles[1] = (a.H + 2 * kRows - 1) / (2 * kRows);
+        kbs[0] = (a.H + block - 1) / block;
+        kbs[1] = (a.I + block - 1) / block;
+    }
+
+    template <class F>
+    __device__ bool segments(F f) const {
+        for (int phase = 0; phase < 2; ++phase) {
+            const skinny::Line line((int64_t)G * tiles[phase], kbs[phase], gridDim.x);
+            const bool ok = line.each(blockIdx.x, [&](int64_t tile, skinny::Segment &s) {
+                s.phase = phase;
+                s.group = (int)(tile / tiles[phase]);
+                s.f = (int)(tile - (int64_t)s.group * tiles[phase]);
+                const int4 g = a.groups[s.group];
+                s.first = g.y;
+                s.n = g.z;
+                if (phase == 0) {
+                    s.a_map = &a.w13;
+                    s.row0 = g.x * 2 * a.I + s.f * kRows;
+                    s.row1 = s.row0 + a.I;
+                    s.row_end = a.E * 2 * a.I;
+                } else {
+                    s.a_map = &a.w2;
+                    s.row0 = g.x * a.H + s.f * 2 * kRows;
+                    s.row1 = s.row0 + kRows;
+                    s.row_end = a.E * a.H;
+                }
+                return f(s);
+            });
+            if (!ok) return false;
+        }
+        return true;
+    }
+
+    // ---- loads of B: x rows of the group's entries, or their rows of h
+    struct Rows {
+        int r[4];
+    };
+    __device__ bool b_ready(const skinny::Segment &s) const {
+        if (s.phase == 0) return true;
+        if (!skinny::wait_count(a.words + kReady + s.group, tiles[0])) return false;
+        fence_proxy_async();
+        return true;
+    }
+    __device__ Rows b_rows(const skinny::Segment &s, int lane) const {
+        Rows rows{};
+        if (s.phase == 0)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    return v;
-}
+            for (int i = 0; i < 4; ++i) rows.r[i] = a.order[s.first + min(4 * lane + i, s.n - 1)] / a.k;
+        return rows;
+    }
+    __device__ uint32_t b_bytes(const skinny::Segment &s) const {
+        return s.phase == 0 ? (s.n + 3) / 4 * 512 : (s.n + 7) / 8 * 1024;
+    }
+    __device__ void b_load(const skinny::Segment &s, const Rows &rows, int col, uint32_t dst, uint64_t *bar,
+                           int lane) const {
+        const uint64_t policy = policy_evict_last();
+        if (s.phase == 0) {
+            if (4 * lane < s.n)
+                tma_gather4(dst + lane * 512, &a.x, col, rows.r[0], rows.r[1], rows.r[2], rows.r[3], bar, policy);
+        } else if (8 * lane < s.n) {
+            tma_load(dst + lane * 1024, &a.h_map, col, s.first + 8 * lane, bar, policy);
+        }
+    }
 
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-    const int e = c >> 3 & 15, m = c & 7;
-    if ((c & 0x7f) == 0x7f) return __int_as_float(0x7fc00000);
-    const float v = e == 0 ? (float)m * 0x1p-9f : (float)(8 + m) * exp2f((float)(e - 10));
-    return c & 0x80 ? -v : v;
-}
+    // ---- sums
+    __device__ const float *scales(int phase) const { return phase == 0 ? a.s13 : a.s2; }
+    __device__ float *partial(int phase, int cta, int slot) const {
+        return a.partials + ((size_t)(phase * skinny::kMaxCtas + cta) * 2 + slot) * 2 * a.shape.cols * kRows;
+    }
+    __device__ uint32_t *arrivals(int phase, int cta) const {
+        return a.words + kArrivals + phase * skinny::kMaxCtas + cta;
+    }
+    struct Emit {
+        const ExpertsArgs &a;
+        const skinny::Segment &s;
+        int row;
+        __device__ Emit(const ExpertsProblem &p, const skinny::Segment &seg, int r) : a(p.a), s(seg), row(r) {}
+        __device__ void operator()(int col, const float *v0, const float *v1) const {
+            if (s.phase == 0) {
+                const int i = s.f * kRows + row;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (col + j >= s.n || i >= a.I) continue;
+                    const float g = v0[j];
+                    a.h[(size_t)(s.first + col + j) * a.I + i] = __float2bfloat16_rn(g / (1.0f + expf(-g)) * v1[j]);
+                }
+            } else {
+                const int o = s.f * 2 * kRows + row;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (col + j >= s.n) continue;
+                    float *y = a.y + (size_t)a.order[s.first + col + j] * a.H + o;
+                    if (o < a.H) y[0] = v0[j];
+                    if (o + kRows < a.H) y[kRows] = v1[j];
+                }
+            }
+        }
+    };
+    __device__ void tile_done(const skinny::Segment &s) const {
+        fence_proxy_async();   // h is read by TMA
+        __threadfence();
+        skinny::readers_sync();
+        if (threadIdx.x == skinny::kThreads - skinny::kReaders)
+            skinny::add_acq_rel(s.phase == 0 ? a.words + kReady + s.group : a.words + 1, 1);
+    }
 
-// element i of weight row `row` (of length K)
-__device__ __forceinline__ float weight(const void *w, const float *scales, size_t row, int K, int i) {
-    if (scales == nullptr) return __bfloat162float(static_cast<const __nv_bfloat16 *>(w)[row * K + i]);
-    return e4m3_value(static_cast<const uint8_t *>(w)[row * K + i]) * scales[row * (K / 128) + i / 128];
-}
+    // out[t] = sum_j w[t, j] y[t, j], eight columns to a thread
+    __device__ bool finish() const {
+        const int thread = threadIdx.x - (skinny::kThreads - skinny::kReaders);
+        bool ok = true;
+        if (thread == 0) ok = skinny::wait_count(a.words + 1, (uint32_t)G * tiles[1]);
+        if (!skinny::readers_agree(ok)) return false;
+        const int pieces = a.H / 8;
+        const int64_t all = (int64_t)a.T * pieces;
+        for (int64_t i = (int64_t)blockIdx.x * skinny::kReaders + thread; i < all;
+             i += (int64_t)gridDim.x * skinny::kReaders) {
+            const int t = (int)(i / pieces), o = (int)(i - (int64_t)t * pieces) * 8;
+            float acc[8] = {};
+#pragma unroll 4
+            for (int j = 0; j < a.k; ++j) {
+                const int64_t e = a.topk_idx[(size_t)t * a.k + j];
+                if (e < 0 || e >= a.E) continue;
+                const float w = a.topk_weights[(size_t)t * a.k + j];
+                const float4 *y = reinterpret_cast<const float4 *>(a.y + ((size_t)t * a.k + j) * a.H + o);
+                const float4 lo = __ldcg(y), hi = __ldcg(y + 1);
+                acc[0] = fmaf(w, lo.x, acc[0]), acc[1] = fmaf(w, lo.y, acc[1]);
+                acc[2] = fmaf(w, lo.z, acc[2]), acc[3] = fmaf(w, lo.w, acc[3]);
+                acc[4] = fmaf(w, hi.x, acc[4]), acc[5] = fmaf(w, hi.y, acc[5]);
+                acc[6] = fmaf(w, hi.z, acc[6]), acc[7] = fmaf(w, hi.w, acc[7]);
+            }
+            __nv_bfloat162 b[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) b[j] = __floats2bfloat162_rn(acc[2 * j], acc[2 * j + 1]);
+            *reinterpret_cast<uint4 *>(a.out + (size_t)t * a.H + o) = *reinterpret_cast<const uint4 *>(b);
+        }
+        return true;
+    }
+};
 
-__global__ void __launch_bounds__(kThreads) experts_up_kernel(const ExpertArgs a) {
+template <bool kE4m3>
+__global__ void __launch_bounds__(skinny::kThreads, 1) experts_kernel(const __grid_constant__ ExpertsArgs a) {
     WarpTrace wt(a.trace, MOE_TRACE_EXPERTS);
     grid_dependency_wait();
-    const ExpertsLaunch &p = a.p;
-    const int lane = threadIdx.x & 31, entry = blockIdx.y;
-    const int64_t e = p.topk_idx[entry];
-    if (e < 0 || e >= p.num_experts) {
-        if (e != -1 && threadIdx.x == 0) report(p.status, MOE_ERR_BAD_TOPK);
-        return;
-    }
-    const __nv_bfloat16 *x = static_cast<const __nv_bfloat16 *>(p.x) + (size_t)(entry / p.num_topk) * p.hidden;
-    const int H = p.hidden, I = p.intermediate;
-    for (int i = blockIdx.x * (kThreads / 32) + threadIdx.x / 32; i < I; i += gridDim.x * (kThreads / 32)) {
-        const size_t g = (size_t)e * 2 * I + i, u = g + I;
-        float sg = 0.0f, su = 0.0f;
-        for (int c = lane; c < H; c += 32) {
-            const float v = __bfloat162float(x[c]);
-            sg += v * weight(p.w13, p.w13_scales, g, H, c);
-            su += v * weight(p.w13, p.w13_scales, u, H, c);
-        }
-        sg = warp_sum(sg);
-        su = warp_sum(su);
-        if (lane == 0) a.h[(size_t)entry * I + i] = sg / (1.0f + expf(-sg)) * su;
-    }
-}
-
-__global__ void __launch_bounds__(kThreads) experts_down_kernel(const ExpertArgs a) {
-    WarpTrace wt(a.trace, MOE_TRACE_EXPERTS);
-    grid_dependency_wait();
-    const ExpertsLaunch &p = a.p;
-    const int lane = threadIdx.x & 31, t = blockIdx.y;
-    const int H = p.hidden, I = p.intermediate;
-    for (int o = blockIdx.x * (kThreads / 32) + threadIdx.x / 32; o < H; o += gridDim.x * (kThreads / 32)) {
-        float acc = 0.0f;
-        for (int j = 0; j < p.num_topk; ++j) {
-            const int entry = t * p.num_topk + j;
-            const int64_t e = p.topk_idx[entry];
-            if (e < 0 || e >= p.num_experts) continue;
-            float s = 0.0f;
-            for (int c = lane; c < I; c += 32)
-                s += a.h[(size_t)entry * I + c] * weight(p.w2, p.w2_scales, (size_t)e * H + o, I, c);
-            acc += p.topk_weights[entry] * warp_sum(s);
-        }
-        if (lane == 0) static_cast<__nv_bfloat16 *>(p.out)[(size_t)t * H + o] = __float2bfloat16_rn(acc);
-    }
+    const ExpertsProblem<kE4m3> p(a);
+    skinny::run<kE4m3>(p, a.shape, a.tmem_cols);
 }
 
 }  // namespace
 
 size_t experts_workspace_bytes(int T, int H, int I, int k, int E) {
-    return (size_t)T * k * I * sizeof(float);
+    return space(T, H, I, k, columns(T, false)).total;   // bf16 weights: the larger of the two
 }
 
 int launch_experts(const ExpertsLaunch &L) {
-    if (L.num_tokens == 0) return MOE_OK;
-    const ExpertArgs a{L, static_cast<float *>(L.workspace), trace_args()};
+    const int T = L.num_tokens, H = L.hidden, I = L.intermediate, k = L.num_topk, E = L.num_experts;
+    if (T == 0) return MOE_OK;
+    const bool e4m3 = L.w13_scales != nullptr;
+    const int cols = columns(T, e4m3);
+    const Space sp = space(T, H, I, k, cols);
+    char *ws = static_cast<char *>(L.workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
-    const bool overlap = tuning().overlap != 0;
-    const int warps = kThreads / 32;
-    cudaError_t e = launch_kernel(experts_up_kernel, dim3((L.intermediate + warps - 1) / warps,
-                                  L.num_tokens * L.num_topk), dim3(kThreads), 0, s, overlap, a);
-    if (e == cudaSuccess)
-        e = launch_kernel(experts_down_kernel, dim3((L.hidden + warps - 1) / warps, L.num_tokens), dim3(kThreads), 0,
-                          s, overlap, a);
-    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+
+    PlanArgs pa{L.topk_idx, T * k, E, cols, reinterpret_cast<uint32_t *>(ws + sp.words), kReady + T * k,
+                reinterpret_cast<int4 *>(ws + sp.groups), reinterpret_cast<int *>(ws + sp.order), L.status, trace_args()};
+
+    ExpertsArgs a{};
+    if (!make_tensor_map(&a.w13, L.w13, e4m3, (uint64_t)E * 2 * I, H, kRows) ||
+        !make_tensor_map(&a.w2, L.w2, e4m3, (uint64_t)E * H, I, kRows) ||
+        !make_tensor_map(&a.x, L.x, false, T, H, 1) ||
+        !make_tensor_map(&a.h_map, ws + sp.h, false, (uint64_t)T * k, I, 8))
+        return MOE_ERR_CUDA;
+    a.topk_idx = L.topk_idx;
+    a.topk_weights = L.topk_weights;
+    a.s13 = L.w13_scales;
+    a.s2 = L.w2_scales;
+    a.words = pa.words;
+    a.groups = pa.groups;
+    a.order = pa.order;
+    a.h = reinterpret_cast<__nv_bfloat16 *>(ws + sp.h);
+    a.y = reinterpret_cast<float *>(ws + sp.y);
+    a.partials = reinterpret_cast<float *>(ws + sp.partial);
+    a.out = static_cast<__nv_bfloat16 *>(L.out);
+    a.status = L.status;
+    a.T = T, a.H = H, a.I = I, a.k = k, a.E = E;
+    a.shape = skinny::Shape{cols, skinny::Shape::stages_for(cols, e4m3)};
+    a.tmem_cols = skinny::Shape::tmem_cols(cols, e4m3);
+    a.trace = trace_args();
+
+    const size_t plan_smem = (size_t)2 * (E + 1) * 4, smem = skinny::Shape::smem(cols, e4m3);
+    const void *kernel = e4m3 ? (const void *)experts_kernel<true> : (const void *)experts_kernel<false>;
+    int rc = ensure_dynamic_smem((const void *)experts_plan_kernel, plan_smem);
+    if (rc == MOE_OK) rc = ensure_dynamic_smem(kernel, smem);
+    if (rc != MOE_OK) return rc;
+    if (launch_kernel(experts_plan_kernel, dim3(1), dim3(kPlanThreads), plan_smem, s, tuning().overlap != 0, pa) !=
+        cudaSuccess)
+        return MOE_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(std::min(device_sm_count(), skinny::kMaxCtas));
+    cfg.blockDim = dim3(skinny::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void *args[] = {&a};
+    return cudaLaunchKernelExC(&cfg, kernel, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace moe

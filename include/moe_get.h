@@ -433,6 +433,7 @@ enum {
     MOE_TRACE_EXPERTS = 15,
     MOE_TRACE_ADAPTER_SHRINK = 16,
     MOE_TRACE_ADAPTER_PROJECT = 17,
+    MOE_TRACE_EXPERTS_PLAN = 18,
     MOE_TRACE_PHASE = 0x10000          /* warp field of a per-CTA phase record: MOE_TRACE_PHASE + phase */
 };
 
