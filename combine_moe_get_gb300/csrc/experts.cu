@@ -25,85 +25,26 @@ namespace {
 
 using skinny::kRows;
 
-constexpr int kPlanThreads = 1024;
-
-// Device workspace, in this order.
+// Device workspace: byte offsets.
 struct Space {
-    size_t words, groups, order, h, y, partial, total;   // byte offsets
-    int cols, max_groups;
+    size_t words, groups, order, h, y, partial, total;
 };
-// words: [0] groups, [1] finished phase 1 tiles, [2..] arrivals [2][kMaxCtas], then ready [max_groups]
-constexpr int kArrivals = 2, kReady = 2 + 2 * skinny::kMaxCtas;
+constexpr int kReady = skinny::kWords;   // then a word per group: its finished h tiles
 
 int columns(int T, bool e4m3) { return std::min((T + 15) / 16 * 16, e4m3 ? 64 : 128); }
 
 Space space(int T, int H, int I, int k, int cols) {
     Space s{};
-    size_t at = 0;
-    auto take = [&](size_t bytes) {
-        const size_t o = at;
-        at += (bytes + 255) / 256 * 256;
-        return o;
-    };
-    const size_t n = (size_t)T * k;
-    s.cols = cols;
-    s.max_groups = (int)n;
-    s.words = take((kReady + n) * 4);
-    s.groups = take(n * sizeof(int4));
-    s.order = take(n * 4);
-    s.h = take(n * I * 2);
-    s.y = take(n * H * 4);
-    s.partial = take((size_t)2 * skinny::kMaxCtas * 2 * 2 * cols * kRows * 4);
-    s.total = at;
+    skinny::Cut cut;
+    const size_t n = (size_t)T * k;   // groups are at most as many as entries
+    s.words = cut.take((kReady + n) * 4);
+    s.groups = cut.take(n * sizeof(int4));
+    s.order = cut.take(n * 4);
+    s.h = cut.take(n * I * 2);
+    s.y = cut.take(n * H * 4);
+    s.partial = cut.take(skinny::partial_floats(cols) * 4);
+    s.total = cut.at;
     return s;
-}
-
-// ------------------------------------------------------------------ plan
-
-struct PlanArgs {
-    const int64_t *topk_idx;
-    int n, E, cols;          // entries, experts, largest group
-    uint32_t *words;
-    int num_words;
-    int4 *groups;            // {expert, first sorted entry, entries, 0}
-    int *order;              // sorted entries
-    int32_t *status;
-    TraceArgs trace;
-};
-
-// The order of an expert's entries is the arrival order of the counters: it says
-// only which column of a product an entry takes, and columns do not depend on
-// one another.
-__global__ void __launch_bounds__(kPlanThreads) experts_plan_kernel(const PlanArgs a) {
-    WarpTrace wt(a.trace, MOE_TRACE_EXPERTS_PLAN);
-    grid_dependency_wait();
-    extern __shared__ int32_t plan_smem[];
-    int32_t *start = plan_smem, *first_group = plan_smem + a.E + 1;
-    for (int i = threadIdx.x; i <= a.E; i += kPlanThreads) start[i] = 0;
-    for (int i = threadIdx.x; i < a.num_words; i += kPlanThreads) a.words[i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
-        const int64_t e = a.topk_idx[i];
-        if (e >= 0 && e < a.E) atomicAdd(&start[e], 1);
-        else if (e != -1) report(a.status, MOE_ERR_BAD_TOPK);
-    }
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kPlanThreads) first_group[e] = (start[e] + a.cols - 1) / a.cols;
-    __syncthreads();
-    if (threadIdx.x < 32) warp_exclusive_scan(start, a.E, threadIdx.x);
-    else if (threadIdx.x < 64) warp_exclusive_scan(first_group, a.E, threadIdx.x - 32);
-    __syncthreads();
-    for (int e = threadIdx.x; e < a.E; e += kPlanThreads) {
-        const int end = start[e + 1];
-        for (int g = first_group[e], b = start[e]; b < end; ++g, b += a.cols)
-            a.groups[g] = make_int4(e, b, min(a.cols, end - b), 0);
-    }
-    if (threadIdx.x == 0) a.words[0] = first_group[a.E];
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
-        const int64_t e = a.topk_idx[i];
-        if (e >= 0 && e < a.E) a.order[atomicAdd(&start[e], 1)] = i;
-    }
 }
 
 // ------------------------------------------------------------------ experts
@@ -133,7 +74,7 @@ struct ExpertsProblem {
     int32_t *status;
     int tiles[2], kbs[2];   // tiles per group and K blocks per tile of the two phases
 
-    __device__ explicit ExpertsProblem(const ExpertsArgs &args) : a(args), G((int)args.words[0]), status(args.status) {
+    __device__ explicit ExpertsProblem(const ExpertsArgs &args) : a(args), G((int)args.words[skinny::kGroupsWord]), status(args.status) {
         constexpr int block = kE4m3 ? 128 : 64;
         tiles[0] = (a.I + kRows - 1) / kRows;
         tiles[1] = (a.H + 2 * kRows - 1) / (2 * kRows);
@@ -152,6 +93,8 @@ struct ExpertsProblem {
                 const int4 g = a.groups[s.group];
                 s.first = g.y;
                 s.n = g.z;
+                s.a_bytes = skinny::kHalf;
+                s.two = true;
                 if (phase == 0) {
                     s.a_map = &a.w13;
                     s.row0 = g.x * 2 * a.I + s.f * kRows;
@@ -207,8 +150,9 @@ struct ExpertsProblem {
         return a.partials + ((size_t)(phase * skinny::kMaxCtas + cta) * 2 + slot) * 2 * a.shape.cols * kRows;
     }
     __device__ uint32_t *arrivals(int phase, int cta) const {
-        return a.words + kArrivals + phase * skinny::kMaxCtas + cta;
+        return a.words + skinny::kArrivals + phase * skinny::kMaxCtas + cta;
     }
+    __device__ bool emit_ready(const skinny::Segment &) const { return true; }
     struct Emit {
         const ExpertsArgs &a;
         const skinny::Segment &s;
@@ -240,14 +184,14 @@ struct ExpertsProblem {
         __threadfence();
         skinny::readers_sync();
         if (threadIdx.x == skinny::kThreads - skinny::kReaders)
-            skinny::add_acq_rel(s.phase == 0 ? a.words + kReady + s.group : a.words + 1, 1);
+            skinny::add_acq_rel(s.phase == 0 ? a.words + kReady + s.group : a.words + skinny::kDoneWord, 1);
     }
 
     // out[t] = sum_j w[t, j] y[t, j], eight columns to a thread
     __device__ bool finish() const {
         const int thread = threadIdx.x - (skinny::kThreads - skinny::kReaders);
         bool ok = true;
-        if (thread == 0) ok = skinny::wait_count(a.words + 1, (uint32_t)G * tiles[1]);
+        if (thread == 0) ok = skinny::wait_count(a.words + skinny::kDoneWord, (uint32_t)G * tiles[1]);
         if (!skinny::readers_agree(ok)) return false;
         const int pieces = a.H / 8;
         const int64_t all = (int64_t)a.T * pieces;
@@ -299,9 +243,10 @@ int launch_experts(const ExpertsLaunch &L) {
     char *ws = static_cast<char *>(L.workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
 
-    PlanArgs pa{L.topk_idx, T * k, E, cols, reinterpret_cast<uint32_t *>(ws + sp.words), kReady + T * k,
-                reinterpret_cast<int4 *>(ws + sp.groups), reinterpret_cast<int *>(ws + sp.order), L.status, trace_args()};
-
+    const skinny::PlanArgs<int64_t> plan{L.topk_idx, T * k, E, cols, reinterpret_cast<uint32_t *>(ws + sp.words),
+                                         kReady + T * k, reinterpret_cast<int4 *>(ws + sp.groups),
+                                         reinterpret_cast<int *>(ws + sp.order), MOE_ERR_BAD_TOPK, L.status,
+                                         trace_args()};
     ExpertsArgs a{};
     if (!make_tensor_map(&a.w13, L.w13, e4m3, (uint64_t)E * 2 * I, H, kRows) ||
         !make_tensor_map(&a.w2, L.w2, e4m3, (uint64_t)E * H, I, kRows) ||
@@ -312,9 +257,9 @@ int launch_experts(const ExpertsLaunch &L) {
     a.topk_weights = L.topk_weights;
     a.s13 = L.w13_scales;
     a.s2 = L.w2_scales;
-    a.words = pa.words;
-    a.groups = pa.groups;
-    a.order = pa.order;
+    a.words = plan.words;
+    a.groups = plan.groups;
+    a.order = plan.order;
     a.h = reinterpret_cast<__nv_bfloat16 *>(ws + sp.h);
     a.y = reinterpret_cast<float *>(ws + sp.y);
     a.partials = reinterpret_cast<float *>(ws + sp.partial);
@@ -325,26 +270,10 @@ int launch_experts(const ExpertsLaunch &L) {
     a.tmem_cols = skinny::Shape::tmem_cols(cols, e4m3);
     a.trace = trace_args();
 
-    const size_t plan_smem = (size_t)2 * (E + 1) * 4, smem = skinny::Shape::smem(cols, e4m3);
-    const void *kernel = e4m3 ? (const void *)experts_kernel<true> : (const void *)experts_kernel<false>;
-    int rc = ensure_dynamic_smem((const void *)experts_plan_kernel, plan_smem);
-    if (rc == MOE_OK) rc = ensure_dynamic_smem(kernel, smem);
+    const int rc = skinny::launch_plan(plan, s);
     if (rc != MOE_OK) return rc;
-    if (launch_kernel(experts_plan_kernel, dim3(1), dim3(kPlanThreads), plan_smem, s, tuning().overlap != 0, pa) !=
-        cudaSuccess)
-        return MOE_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(std::min(device_sm_count(), skinny::kMaxCtas));
-    cfg.blockDim = dim3(skinny::kThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeCooperative;
-    attr[0].val.cooperative = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    void *args[] = {&a};
-    return cudaLaunchKernelExC(&cfg, kernel, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return skinny::launch_resident(e4m3 ? experts_kernel<true> : experts_kernel<false>, a,
+                                   skinny::Shape::smem(cols, e4m3), s);
 }
 
 }  // namespace moe

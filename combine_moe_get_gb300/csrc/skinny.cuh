@@ -43,6 +43,8 @@ struct Segment {
     const CUtensorMap *a_map;
     int row0, row1;       // weight rows of the two products
     int row_end;          // rows of the whole weight matrix
+    int a_bytes;          // bytes of A that a K block loads for one product
+    bool two;             // both products (else the first alone)
     int kb0, kb1, kbs;    // K blocks [kb0, kb1) of the tile's kbs
     int n;                // columns in use
     int phase, f, group, first;   // which tile: phase, feature tile, group and its first row
@@ -88,7 +90,6 @@ struct Control {
     uint64_t a_ready[2];     // E4M3: converted block in tensor memory
     uint64_t last;
     uint32_t tmem;
-    int failed;
     int vote;
 };
 
@@ -169,9 +170,9 @@ __device__ bool load_a(const P &p, Control &c, uint32_t ring_base, const Shape s
                 if (!wait(&c.empty[r.slot], r.round ^ 1)) return false;
                 const uint32_t dst = ring_base + r.slot * Shape::stage_bytes(sh.cols, kE4m3);
                 const int col = kb * (kE4m3 ? 128 : 64);
-                mbar_arrive_expect_tx(&c.full_a[r.slot], 2 * kHalf);
+                mbar_arrive_expect_tx(&c.full_a[r.slot], s.two ? 2 * s.a_bytes : s.a_bytes);
                 tma_load(dst, s.a_map, col, s.row0, &c.full_a[r.slot], policy);
-                tma_load(dst + kHalf, s.a_map, col, s.row1, &c.full_a[r.slot], policy);
+                if (s.two) tma_load(dst + kHalf, s.a_map, col, s.row1, &c.full_a[r.slot], policy);
             }
             return true;
         });
@@ -233,8 +234,9 @@ __device__ bool multiply(const P &p, Control &c, uint32_t ring_base, const Shape
             const uint64_t a0 = operand_desc(at), a1 = operand_desc(at + kHalf), b = operand_desc(at + 2 * kHalf);
 #pragma unroll
             for (int k = 0; k < 4; ++k) mma_ss(d0, a0 + 2 * k, b + 2 * k, desc, kb > s.kb0 || k > 0);
+            if (s.two)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_ss(d1, a1 + 2 * k, b + 2 * k, desc, kb > s.kb0 || k > 0);
+                for (int k = 0; k < 4; ++k) mma_ss(d1, a1 + 2 * k, b + 2 * k, desc, kb > s.kb0 || k > 0);
             mma_commit(&c.empty[r.slot]);
         }
         mma_commit(&c.sums_full[buf]);
@@ -296,8 +298,9 @@ __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t two) {
 // halves, columns 16 i + 8 side + 0..7. `each(f)` calls f(column, sums of half
 // 0, sums of half 1) for all of them.
 template <class P, class Each, class Release>
-__device__ void hand_over(const P &p, Control &c, const Shape sh, const Segment &s, int row, Each each, Release release) {
+__device__ bool hand_over(const P &p, Control &c, const Shape sh, const Segment &s, int row, Each each, Release release) {
     if (s.whole()) {
+        if (!p.emit_ready(s)) return false;
         typename P::Emit emit(p, s, row);
         each([&](int col, const float *v0, const float *v1) { emit(col, v0, v1); });
         release();
@@ -322,8 +325,9 @@ __device__ void hand_over(const P &p, Control &c, const Shape sh, const Segment 
         readers_sync();
         const bool last = c.vote != 0;
         readers_sync();
-        if (!last) return;
+        if (!last) return true;
         __threadfence();
+        if (!p.emit_ready(s)) return false;
         typename P::Emit emit(p, s, row);
         const int side = (threadIdx.x - (kThreads - kReaders)) / 128;
         for (int col = side * 8; col < s.n; col += 16) {
@@ -341,6 +345,7 @@ __device__ void hand_over(const P &p, Control &c, const Shape sh, const Segment 
         }
     }
     p.tile_done(s);
+    return true;
 }
 
 // Readers of bf16 weights' sums.
@@ -368,9 +373,8 @@ __device__ bool read_sums(const P &p, Control &c, const Shape sh, uint32_t tmem)
             __syncwarp();
             if (lane == 0) mbar_arrive(&c.sums_empty[buf]);
         };
-        hand_over(p, c, sh, s, row, each, release);
         ++seq;
-        return true;
+        return hand_over(p, c, sh, s, row, each, release);
     });
 }
 
@@ -444,8 +448,7 @@ __device__ bool read_sums_e4m3(const P &p, Control &c, const char *ring, const S
             for (int i = 0; i < kChunks; ++i)
                 if (i * 16 + side * 8 < s.n) f(i * 16 + side * 8, acc0 + i * 8, acc1 + i * 8);
         };
-        hand_over(p, c, sh, s, row, each, [] {});
-        return true;
+        return hand_over(p, c, sh, s, row, each, [] {});
     });
 }
 
@@ -469,7 +472,6 @@ __device__ void run(const P &p, const Shape sh, const uint32_t tmem_cols) {
             mbar_init(&c.a_ready[i], 8);
         }
         mbar_init(&c.last, 1);
-        c.failed = 0;
         fence_barrier_init();
     }
     if (warp == 3) tmem_alloc(&c.tmem, tmem_cols);
@@ -482,9 +484,13 @@ __device__ void run(const P &p, const Shape sh, const uint32_t tmem_cols) {
     if (warp == 0) ok = load_a<kE4m3>(p, c, ring_base, sh);
     else if (warp == 1) ok = load_b<kE4m3>(p, c, ring_base, sh);
     else if (warp == 2) {
-        if (lane == 0) ok = kE4m3 ? multiply_e4m3(p, c, ring_base, sh, tmem) : multiply(p, c, ring_base, sh, tmem);
+        if (lane == 0) {
+            if constexpr (kE4m3) ok = multiply_e4m3(p, c, ring_base, sh, tmem);
+            else ok = multiply(p, c, ring_base, sh, tmem);
+        }
     } else if (warp >= 4) {
-        ok = kE4m3 ? read_sums_e4m3(p, c, ring, sh, tmem) : read_sums(p, c, sh, tmem);
+        if constexpr (kE4m3) ok = read_sums_e4m3(p, c, ring, sh, tmem);
+        else ok = read_sums(p, c, sh, tmem);
         if (ok) ok = p.finish();
     }
     if (!ok) report(p.status, MOE_ERR_TIMEOUT);
@@ -493,6 +499,103 @@ __device__ void run(const P &p, const Shape sh, const uint32_t tmem_cols) {
     tc_fence_after();
     if (warp == 3) tmem_free(tmem, tmem_cols);
 }
+
+// ------------------------------------------------------------------ plan
+
+// Sorts entries by the weight set that they name and cuts each set's into groups
+// of at most `cols`; clears the counters of the kernel behind it.
+template <typename Index>
+struct PlanArgs {
+    const Index *idx;        // [n], -1: none
+    int n, sets, cols;
+    uint32_t *words;         // [0] becomes the number of groups, the rest 0
+    int num_words;
+    int4 *groups;            // {set, first sorted entry, entries, 0}
+    int *order;              // sorted entries
+    int bad;                 // status of an index out of range
+    int32_t *status;
+    TraceArgs trace;
+};
+
+constexpr int kPlanThreads = 1024;
+
+// The order of a set's entries is the arrival order of the counters: it says
+// only which column of a product an entry takes, and columns do not depend on
+// one another.
+template <typename Index>
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Index> a) {
+    WarpTrace wt(a.trace, MOE_TRACE_PLAN);
+    grid_dependency_wait();
+    extern __shared__ int32_t plan_smem[];
+    int32_t *start = plan_smem, *first_group = plan_smem + a.sets + 1;
+    for (int i = threadIdx.x; i <= a.sets; i += kPlanThreads) start[i] = 0;
+    for (int i = threadIdx.x; i < a.num_words; i += kPlanThreads) a.words[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
+        const Index e = a.idx[i];
+        if (e >= 0 && e < a.sets) atomicAdd(&start[e], 1);
+        else if (e != -1) report(a.status, a.bad);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.sets; e += kPlanThreads) first_group[e] = (start[e] + a.cols - 1) / a.cols;
+    __syncthreads();
+    if (threadIdx.x < 32) warp_exclusive_scan(start, a.sets, threadIdx.x);
+    else if (threadIdx.x < 64) warp_exclusive_scan(first_group, a.sets, threadIdx.x - 32);
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.sets; e += kPlanThreads) {
+        const int end = start[e + 1];
+        for (int g = first_group[e], b = start[e]; b < end; ++g, b += a.cols)
+            a.groups[g] = make_int4(e, b, min(a.cols, end - b), 0);
+    }
+    if (threadIdx.x == 0) a.words[0] = first_group[a.sets];
+    __syncthreads();
+    for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
+        const Index e = a.idx[i];
+        if (e >= 0 && e < a.sets) a.order[atomicAdd(&start[e], 1)] = i;
+    }
+}
+
+template <typename Index>
+int launch_plan(const PlanArgs<Index> &a, cudaStream_t s) {
+    const size_t smem = (size_t)2 * (a.sets + 1) * 4;
+    const int rc = ensure_dynamic_smem((const void *)plan_kernel<Index>, smem);
+    if (rc != MOE_OK) return rc;
+    return launch_kernel(plan_kernel<Index>, dim3(1), dim3(kPlanThreads), smem, s, tuning().overlap != 0, a) ==
+                   cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// One CTA per SM, all of them resident at once (they wait for one another).
+template <class Args>
+int launch_resident(void (*kernel)(Args), Args &a, size_t smem, cudaStream_t s) {
+    const int rc = ensure_dynamic_smem((const void *)kernel, smem);
+    if (rc != MOE_OK) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(device_sm_count() < kMaxCtas ? device_sm_count() : kMaxCtas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void *args[] = {&a};
+    return cudaLaunchKernelExC(&cfg, (const void *)kernel, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+// Words of the workspace that both sides share.
+constexpr int kGroupsWord = 0, kDoneWord = 1, kArrivals = 2, kWords = 2 + 2 * kMaxCtas;
+constexpr size_t partial_floats(int cols) { return (size_t)2 * kMaxCtas * 2 * 2 * cols * kRows; }
+
+// Byte offsets of the pieces of a workspace, each 256-byte aligned.
+struct Cut {
+    size_t at = 0;
+    size_t take(size_t bytes) {
+        const size_t o = at;
+        at += (bytes + 255) / 256 * 256;
+        return o;
+    }
+};
 
 }  // namespace skinny
 }  // namespace moe

@@ -431,9 +431,8 @@ enum {
     MOE_TRACE_GATE = 13,
     MOE_TRACE_GATE_BACKWARD = 14,
     MOE_TRACE_EXPERTS = 15,
-    MOE_TRACE_ADAPTER_SHRINK = 16,
-    MOE_TRACE_ADAPTER_PROJECT = 17,
-    MOE_TRACE_EXPERTS_PLAN = 18,
+    MOE_TRACE_ADAPTER = 16,
+    MOE_TRACE_PLAN = 17,               /* entries sorted by expert or adapter */
     MOE_TRACE_PHASE = 0x10000          /* warp field of a per-CTA phase record: MOE_TRACE_PHASE + phase */
 };
 
