@@ -6,16 +6,19 @@
 // Two kernels. The plan kernel (one CTA) sorts the valid entries by expert and
 // cuts each expert's into groups of at most `cols` entries. The experts kernel
 // (one CTA per SM, launched cooperatively) runs skinny.cuh's body over two
-// lines of work: phase 0 makes h (a tile is 128 gate and the same 128 up rows,
+// phases of work: phase 0 makes h (a tile is 128 gate and the same 128 up rows,
 // so that one thread holds both sums of an element), phase 1 multiplies h by w2
 // (a tile is 256 rows) into y, one fp32 row per entry. A group's phase 1 waits
-// until all its h tiles are done; the loads of w2 do not wait, so the stream of
-// weights goes on across the border. When all of y is there, all CTAs add each
-// token's rows in entry order with their weights and round once to bf16.
+// until all its h tiles are done; the loads of w2 do not wait. The groups go
+// through the two phases in up to two waves, phase 0 of a wave before phase 1 of the wave
+// before it, so that h is there when its turn comes and the stream of weights
+// does not pause. When all of y is there, all CTAs add each token's rows in
+// entry order with their weights and round once to bf16.
 //
 // h is rounded to bf16: it is the operand of a bf16 product, and the rounding's
 // effect on an output is of the size of that output's own rounding.
 #include <algorithm>
+#include <climits>
 #include <cuda_bf16.h>
 
 #include "skinny.cuh"
@@ -29,9 +32,24 @@ using skinny::kRows;
 struct Space {
     size_t words, groups, order, h, y, partial, total;
 };
+// Two waves from this many K blocks of phase 1 per CTA (32 KB each, some 0.7 us):
+// the hand-over of h takes about 6 us after the slowest CTA, and CTAs drift
+// apart by about 10. Three or more waves measured slower: over shorter lines
+// the CTAs differ by more.
+constexpr int kWaveBlocks = 28;
 constexpr int kReady = skinny::kWords;   // then a word per group: its finished h tiles
 
-int columns(int T, bool e4m3) { return std::min((T + 15) / 16 * 16, e4m3 ? 64 : 128); }
+// Columns of a tile: room for about twice an expert's share of the entries. An
+// expert with more takes several groups, that is, streams its weights again.
+int columns(int T, int k, int E, bool e4m3) {
+    const int most = std::min((T + 15) / 16 * 16, e4m3 ? 64 : 128);
+    const int64_t want = (2 * (int64_t)T * k / E + 8 + 15) / 16 * 16;
+    return (int)std::min<int64_t>(most, std::max<int64_t>(want, 16));
+}
+
+// Waves of groups at most (each is a line of either phase): wider tiles have
+// larger partial sums.
+int waves_for(int cols) { return cols <= 64 ? 2 : 1; }
 
 Space space(int T, int H, int I, int k, int cols) {
     Space s{};
@@ -42,7 +60,7 @@ Space space(int T, int H, int I, int k, int cols) {
     s.order = cut.take(n * 4);
     s.h = cut.take(n * I * 2);
     s.y = cut.take(n * H * 4);
-    s.partial = cut.take(skinny::partial_floats(cols) * 4);
+    s.partial = cut.take(skinny::partial_floats(2 * waves_for(cols), cols) * 4);
     s.total = cut.at;
     return s;
 }
@@ -64,11 +82,18 @@ struct ExpertsArgs {
     int T, H, I, k, E;
     skinny::Shape shape;
     uint32_t tmem_cols;
+    int max_waves;
     TraceArgs trace;
 };
 
-template <bool kE4m3>
+template <bool kE4m3, int kCols>   // kCols: the most columns of a tile
 struct ExpertsProblem {
+    static constexpr int kSteps = kCols / 8;
+    static constexpr bool kHalves = false, kAdders = true;
+    static constexpr bool kConvert = kE4m3;
+    static constexpr int kReaders = kE4m3 ? 256 : 512;
+    using Readers = skinny::ReadersOf<ExpertsProblem>;
+    using Ahead = skinny::NothingAhead;
     const ExpertsArgs &a;
     int G;
     int32_t *status;
@@ -82,44 +107,59 @@ struct ExpertsProblem {
         kbs[1] = (a.I + block - 1) / block;
     }
 
-    template <class F>
-    __device__ bool segments(F f) const {
-        for (int phase = 0; phase < 2; ++phase) {
-            const skinny::Line line((int64_t)G * tiles[phase], kbs[phase], gridDim.x);
+    template <class F, class End = skinny::Nothing>
+    __device__ bool segments(F f, End end_line = End()) const {
+        // Waves of groups, one behind the other: phase 0 of wave w + 1 comes before phase 1 of wave w.
+        const int64_t own = skinny::quotient((int64_t)G * tiles[1] * kbs[1], gridDim.x);
+        const int waves = min(G, own >= kWaveBlocks ? a.max_waves : 1);
+        for (int step = 0; step <= 2 * waves; ++step) {
+            // 0(0) 0(1) 1(0) 0(2) 1(1) ... 0(n-1) 1(n-2) 1(n-1): even steps 2w are phase 0 of wave w, odd ones 2w+1 phase 1 of wave w-1
+            const int phase = step & 1 || step == 2 * waves ? 1 : 0;
+            const int wave = phase == 0 ? step / 2 : step == 2 * waves ? waves - 1 : step / 2 - 1;
+            if (wave < 0) continue;
+            const int g0 = (int)((int64_t)G * wave / waves), g1 = (int)((int64_t)G * (wave + 1) / waves);
+            const skinny::Line line((int64_t)(g1 - g0) * tiles[phase], kbs[phase], gridDim.x,
+                                    kE4m3 || a.shape.cols > 32 ? skinny::kSlackWork : skinny::kSlackBytes);
             const bool ok = line.each(blockIdx.x, [&](int64_t tile, skinny::Segment &s) {
+                s.line = 2 * wave + phase;
                 s.phase = phase;
-                s.group = (int)(tile / tiles[phase]);
-                s.f = (int)(tile - (int64_t)s.group * tiles[phase]);
+                const int in_wave = (int)skinny::quotient(tile, tiles[phase]);
+                s.group = g0 + in_wave;
+                s.f = (int)(tile - (int64_t)in_wave * tiles[phase]);
                 const int4 g = a.groups[s.group];
                 s.first = g.y;
                 s.n = g.z;
-                s.a_bytes = skinny::kHalf;
                 s.two = true;
                 if (phase == 0) {
-                    s.a_map = &a.w13;
                     s.row0 = g.x * 2 * a.I + s.f * kRows;
                     s.row1 = s.row0 + a.I;
-                    s.row_end = a.E * 2 * a.I;
+                    s.b_from = INT_MAX;
                 } else {
-                    s.a_map = &a.w2;
                     s.row0 = g.x * a.H + s.f * 2 * kRows;
                     s.row1 = s.row0 + kRows;
-                    s.row_end = a.E * a.H;
+                    s.b_from = 0;
                 }
                 return f(s);
             });
-            if (!ok) return false;
+            if (!ok || !end_line()) return false;
         }
         return true;
     }
 
-    // ---- loads of B: x rows of the group's entries, or their rows of h
+    // ---- loads
+    __device__ void a_load(const skinny::Segment &s, int kb, uint32_t dst, uint64_t *bar, uint64_t policy) const {
+        const CUtensorMap *map = s.phase == 0 ? &a.w13 : &a.w2;
+        const int col = kb * (kE4m3 ? 128 : 64);
+        mbar_arrive_expect_tx(bar, 2 * skinny::kHalf);
+        tma_load(dst, map, col, s.row0, bar, policy);
+        tma_load(dst + skinny::kHalf, map, col, s.row1, bar, policy);
+    }
+    // B: x rows of the group's entries, or their rows of h
     struct Rows {
         int r[4];
     };
     __device__ bool b_ready(const skinny::Segment &s) const {
-        if (s.phase == 0) return true;
-        if (!skinny::wait_count(a.words + kReady + s.group, tiles[0])) return false;
+        if (!skinny::wait_count(a.words + kReady + s.group, tiles[0] * skinny::kTileWeight)) return false;
         fence_proxy_async();
         return true;
     }
@@ -130,73 +170,77 @@ struct ExpertsProblem {
             for (int i = 0; i < 4; ++i) rows.r[i] = a.order[s.first + min(4 * lane + i, s.n - 1)] / a.k;
         return rows;
     }
-    __device__ uint32_t b_bytes(const skinny::Segment &s) const {
+    __device__ uint32_t b_bytes(const skinny::Segment &s, int) const {
         return s.phase == 0 ? (s.n + 3) / 4 * 512 : (s.n + 7) / 8 * 1024;
     }
-    __device__ void b_load(const skinny::Segment &s, const Rows &rows, int col, uint32_t dst, uint64_t *bar,
-                           int lane) const {
-        const uint64_t policy = policy_evict_last();
+    __device__ void b_load(const skinny::Segment &s, const Rows &rows, int block, uint32_t dst, uint64_t *bar,
+                           uint64_t policy, int lane) const {
         if (s.phase == 0) {
             if (4 * lane < s.n)
-                tma_gather4(dst + lane * 512, &a.x, col, rows.r[0], rows.r[1], rows.r[2], rows.r[3], bar, policy);
+                tma_gather4(dst + lane * 512, &a.x, block * 64, rows.r[0], rows.r[1], rows.r[2], rows.r[3], bar, policy);
         } else if (8 * lane < s.n) {
-            tma_load(dst + lane * 1024, &a.h_map, col, s.first + 8 * lane, bar, policy);
+            tma_load(dst + lane * 1024, &a.h_map, block * 64, s.first + 8 * lane, bar, policy);
         }
     }
 
     // ---- sums
     __device__ const float *scales(int phase) const { return phase == 0 ? a.s13 : a.s2; }
-    __device__ float *partial(int phase, int cta, int slot) const {
-        return a.partials + ((size_t)(phase * skinny::kMaxCtas + cta) * 2 + slot) * 2 * a.shape.cols * kRows;
+    __device__ int weight_rows(int phase) const { return a.E * (phase == 0 ? 2 * a.I : a.H); }
+    __device__ float *partial(int line, int cta, int slot) const {
+        return a.partials + ((size_t)(line * skinny::kMaxCtas + cta) * 2 + slot) * 2 * a.shape.cols * kRows;
     }
-    __device__ uint32_t *arrivals(int phase, int cta) const {
-        return a.words + skinny::kArrivals + phase * skinny::kMaxCtas + cta;
+    __device__ uint32_t *arrivals(int line, int cta) const {
+        return a.words + skinny::kArrivals + line * skinny::kMaxCtas + cta;
     }
+    template <class Team>
     __device__ bool emit_ready(const skinny::Segment &) const { return true; }
     struct Emit {
         const ExpertsArgs &a;
         const skinny::Segment &s;
         int row;
-        __device__ Emit(const ExpertsProblem &p, const skinny::Segment &seg, int r) : a(p.a), s(seg), row(r) {}
-        __device__ void operator()(int col, const float *v0, const float *v1) const {
+        __device__ Emit(const ExpertsProblem &p, const skinny::Segment &seg, const skinny::Share<false> &me)
+            : a(p.a), s(seg), row(me.row) {}
+        __device__ void operator()(int col, const float *v) const {
             if (s.phase == 0) {
                 const int i = s.f * kRows + row;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 4; ++j) {
                     if (col + j >= s.n || i >= a.I) continue;
-                    const float g = v0[j];
-                    a.h[(size_t)(s.first + col + j) * a.I + i] = __float2bfloat16_rn(g / (1.0f + expf(-g)) * v1[j]);
+                    const float g = v[j];
+                    a.h[(size_t)(s.first + col + j) * a.I + i] = __float2bfloat16_rn(g / (1.0f + expf(-g)) * v[4 + j]);
                 }
             } else {
                 const int o = s.f * 2 * kRows + row;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 4; ++j) {
                     if (col + j >= s.n) continue;
                     float *y = a.y + (size_t)a.order[s.first + col + j] * a.H + o;
-                    if (o < a.H) y[0] = v0[j];
-                    if (o + kRows < a.H) y[kRows] = v1[j];
+                    if (o < a.H) y[0] = v[j];
+                    if (o + kRows < a.H) y[kRows] = v[4 + j];
                 }
             }
         }
     };
-    __device__ void tile_done(const skinny::Segment &s) const {
-        fence_proxy_async();   // h is read by TMA
-        __threadfence();
-        skinny::readers_sync();
-        if (threadIdx.x == skinny::kThreads - skinny::kReaders)
-            skinny::add_acq_rel(s.phase == 0 ? a.words + kReady + s.group : a.words + skinny::kDoneWord, 1);
+    // a tile's values are written: before the barrier and the count that say so
+    __device__ void before_signal(const skinny::Segment &s) const {
+        if (s.phase == 0) fence_proxy_async();   // h is read by TMA
+    }
+    __device__ uint64_t *done() const { return reinterpret_cast<uint64_t *>(a.words + skinny::kDoneWord); }
+    __device__ void tile_done(const skinny::Segment &s, uint32_t weight) const {
+        if (s.phase == 0) skinny::count_up(a.words + kReady + s.group, weight);
+        else skinny::count_up(done(), (uint64_t)weight);
     }
 
     // out[t] = sum_j w[t, j] y[t, j], eight columns to a thread
     __device__ bool finish() const {
-        const int thread = threadIdx.x - (skinny::kThreads - skinny::kReaders);
+        const int thread = threadIdx.x - Readers::first;
         bool ok = true;
-        if (thread == 0) ok = skinny::wait_count(a.words + skinny::kDoneWord, (uint32_t)G * tiles[1]);
-        if (!skinny::readers_agree(ok)) return false;
+        if (thread == 0) ok = skinny::wait_count(done(), (uint64_t)G * tiles[1] * skinny::kTileWeight);
+        if (!Readers::agree(ok)) return false;
         const int pieces = a.H / 8;
         const int64_t all = (int64_t)a.T * pieces;
-        for (int64_t i = (int64_t)blockIdx.x * skinny::kReaders + thread; i < all;
-             i += (int64_t)gridDim.x * skinny::kReaders) {
+        for (int64_t i = (int64_t)blockIdx.x * kReaders + thread; i < all;
+             i += (int64_t)gridDim.x * kReaders) {
             const int t = (int)(i / pieces), o = (int)(i - (int64_t)t * pieces) * 8;
             float acc[8] = {};
 #pragma unroll 4
@@ -220,30 +264,34 @@ struct ExpertsProblem {
     }
 };
 
-template <bool kE4m3>
-__global__ void __launch_bounds__(skinny::kThreads, 1) experts_kernel(const __grid_constant__ ExpertsArgs a) {
+template <bool kE4m3, int kCols>
+__global__ void __launch_bounds__(skinny::threads_of<ExpertsProblem<kE4m3, kCols>>(), 1)
+    experts_kernel(const __grid_constant__ ExpertsArgs a) {
     WarpTrace wt(a.trace, MOE_TRACE_EXPERTS);
-    grid_dependency_wait();
-    const ExpertsProblem<kE4m3> p(a);
-    skinny::run<kE4m3>(p, a.shape, a.tmem_cols);
+    if (threadIdx.x == 0)
+        for (const CUtensorMap *m : {&a.w13, &a.w2, &a.x, &a.h_map}) tma_prefetch_map(m);
+    skinny::run<kE4m3, ExpertsProblem<kE4m3, kCols>>([&] {
+        grid_dependency_wait();
+        return ExpertsProblem<kE4m3, kCols>(a);
+    }, a.shape, a.tmem_cols);
 }
 
 }  // namespace
 
 size_t experts_workspace_bytes(int T, int H, int I, int k, int E) {
-    return space(T, H, I, k, columns(T, false)).total;   // bf16 weights: the larger of the two
+    return space(T, H, I, k, columns(T, k, E, false)).total;   // bf16 weights: the larger of the two
 }
 
 int launch_experts(const ExpertsLaunch &L) {
     const int T = L.num_tokens, H = L.hidden, I = L.intermediate, k = L.num_topk, E = L.num_experts;
     if (T == 0) return MOE_OK;
     const bool e4m3 = L.w13_scales != nullptr;
-    const int cols = columns(T, e4m3);
+    const int cols = columns(T, k, E, e4m3);
     const Space sp = space(T, H, I, k, cols);
     char *ws = static_cast<char *>(L.workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
 
-    const skinny::PlanArgs<int64_t> plan{L.topk_idx, T * k, E, cols, reinterpret_cast<uint32_t *>(ws + sp.words),
+    const skinny::PlanArgs<int64_t> plan{L.topk_idx, T * k, E, false, cols, reinterpret_cast<uint32_t *>(ws + sp.words),
                                          kReady + T * k, reinterpret_cast<int4 *>(ws + sp.groups),
                                          reinterpret_cast<int *>(ws + sp.order), MOE_ERR_BAD_TOPK, L.status,
                                          trace_args()};
@@ -266,14 +314,18 @@ int launch_experts(const ExpertsLaunch &L) {
     a.out = static_cast<__nv_bfloat16 *>(L.out);
     a.status = L.status;
     a.T = T, a.H = H, a.I = I, a.k = k, a.E = E;
-    a.shape = skinny::Shape{cols, skinny::Shape::stages_for(cols, e4m3)};
-    a.tmem_cols = skinny::Shape::tmem_cols(cols, e4m3);
+    a.shape = skinny::Shape::of(cols, e4m3);
+    a.tmem_cols = a.shape.tmem_cols(e4m3);
+    a.max_waves = waves_for(cols);
     a.trace = trace_args();
 
     const int rc = skinny::launch_plan(plan, s);
     if (rc != MOE_OK) return rc;
-    return skinny::launch_resident(e4m3 ? experts_kernel<true> : experts_kernel<false>, a,
-                                   skinny::Shape::smem(cols, e4m3), s);
+    const size_t smem = a.shape.smem(e4m3);
+    if (!e4m3) return skinny::launch_resident(experts_kernel<false, 128>, a, skinny::threads_of<ExpertsProblem<false, 128>>(), smem, s);
+    const int threads = skinny::threads_of<ExpertsProblem<true, 64>>();
+    return cols <= 32 ? skinny::launch_resident(experts_kernel<true, 32>, a, threads, smem, s)
+                      : skinny::launch_resident(experts_kernel<true, 64>, a, threads, smem, s);
 }
 
 }  // namespace moe

@@ -570,11 +570,12 @@ MOE_API int moe_topk_gate_backward(const void *logits, int logits_type, const in
 }
 
 constexpr int kMaxFeatures = 1 << 20;   // widest hidden, intermediate or projection size
+constexpr int64_t kMaxRows = 1 << 30;    // rows of all sets of a weight: tile coordinates are 32-bit
 
 static bool experts_shape_ok(int T, int H, int I, int k, int E) {
     if (!shape_ok(T, k, E, 1) || T > MOE_EXPERTS_MAX_TOKENS) return false;
     if (H < 8 || H % 8 != 0 || H > kMaxFeatures || I < 8 || I % 8 != 0 || I > kMaxFeatures) return false;
-    return (int64_t)E * 2 * I < (int64_t)1 << 31 && (int64_t)E * H < (int64_t)1 << 31;
+    return (int64_t)E * 2 * I <= kMaxRows && (int64_t)E * H <= kMaxRows;
 }
 
 MOE_API size_t moe_experts_workspace_size(int num_tokens, int hidden, int intermediate, int num_topk, int num_experts) {
@@ -638,7 +639,7 @@ MOE_API int moe_layer(const void *x, int num_tokens, int hidden, const void *log
 static bool adapter_shape_ok(int T, int K, int N, int L, int r) {
     if (T < 0 || T > (1 << 20) || L < 1 || L > MOE_MAX_ADAPTERS) return false;
     if (K < 8 || K % 8 != 0 || K > kMaxFeatures || N < 8 || N % 8 != 0 || N > kMaxFeatures) return false;
-    return r >= 8 && r % 8 == 0 && r <= MOE_MAX_ADAPTER_RANK;
+    return r >= 8 && r % 8 == 0 && r <= MOE_MAX_ADAPTER_RANK && (int64_t)L * N <= kMaxRows;
 }
 
 MOE_API size_t moe_adapter_linear_workspace_size(int num_tokens, int in_features, int out_features, int num_adapters,

@@ -138,6 +138,9 @@ TraceArgs trace_args();
 #ifndef MOE_TUNE_DISPATCH_PREFETCH_KEEP
 #define MOE_TUNE_DISPATCH_PREFETCH_KEEP 1
 #endif
+#ifndef MOE_TUNE_SKINNY_MIN_BLOCKS   // K blocks a CTA takes at least (skinny.cuh)
+#define MOE_TUNE_SKINNY_MIN_BLOCKS 8
+#endif
 struct Tuning {
     int dispatch_warps, dispatch_stages, dispatch_chunk;
     int ld_dispatch_warps, ld_dispatch_stages;              // ... launched behind this library's layout

@@ -11,15 +11,19 @@
 // partial sums in the workspace: the result does not depend on the arrival
 // order.
 //
-// Roles of a CTA's 12 warps: 0 loads A (weights), 1 loads B (activations), 2
-// issues the products, 3 owns the tensor memory, 4..11 read the sums.
+// Roles of a CTA's warps: 0 loads A (weights), 1 loads B (activations), 2 issues
+// the products, 3 owns the tensor memory, the next 8 or 16 (P::kReaders) read the
+// sums, and where a problem has several lines of work (P::kAdders) 4 more add
+// up shared tiles while the others go on to the next line.
 //   bf16 weights: A and B from shared memory; sums stay in tensor memory for a
 //     whole stretch of K, double-buffered, so that the readers' work on one
 //     tile runs under the next tile's products.
-//   E4M3 weights: the reader warps also turn each block's codes into bf16 (exact)
-//     in tensor memory, from where the products take A; a block of 128 along K
-//     has its own fp32 scale per weight row, so the block's sums are scaled and
-//     added in registers (n <= 64).
+//   E4M3 weights: 8 more warps turn each block's codes into bf16 (exact) in
+//     tensor memory, from where the products take A; a block of 128 along K has
+//     its own fp32 scale per weight row, so the readers scale each block's sums
+//     and add them in registers (n <= 64). Blocks are double-buffered on both
+//     sides of the products. (Readers that did the conversions themselves, 8 or 16
+//     of them, took 1.6 times the time that a block's bytes take.)
 //
 // The problem P gives the segments, the loads of B and what becomes of the sums.
 #pragma once
@@ -29,40 +33,53 @@
 namespace moe {
 namespace skinny {
 
-constexpr int kThreads = 384;
-constexpr int kReaders = 256;          // threads of warps 4..11
+constexpr int kFirstReader = 128;      // first thread of the converting, else the reading warps
+constexpr int kAdders = 128;           // threads of the adding warps
+constexpr int kMaxLines = 8;
+constexpr uint32_t kTileWeight = 1024;   // what the finished parts of a tile count together
+constexpr int kConverters = 256;
+// Two thirds of the SMs draw all of HBM's bandwidth where a block costs little
+// besides its bytes (100 SMs: within 1% of 152, one token); a tile that no other
+// CTA shares saves some 10 us of hand-over. Blocks that keep an SM busy, E4M3
+// ones or products of many columns, want equal stretches.
+constexpr int kSlackBytes = 140, kSlackWork = 110;
 constexpr int kRows = 128;             // weight rows of one product; a tile has two
 constexpr int kHalf = kRows * 128;     // bytes of one A tile of a stage
 constexpr int kMaxCtas = 160;
 constexpr int kMaxStages = 8;
 constexpr int kSmemBudget = 224 << 10;
-constexpr int kMinBlocks = 8;          // K blocks a CTA takes at least (or a whole tile)
+constexpr int kMinBlocks = MOE_TUNE_SKINNY_MIN_BLOCKS;          // K blocks a CTA takes at least (or a whole tile)
 
 // One CTA's stretch of one tile.
 struct Segment {
-    const CUtensorMap *a_map;
     int row0, row1;       // weight rows of the two products
-    int row_end;          // rows of the whole weight matrix
-    int a_bytes;          // bytes of A that a K block loads for one product
     bool two;             // both products (else the first alone)
     int kb0, kb1, kbs;    // K blocks [kb0, kb1) of the tile's kbs
+    int b_from;           // first K block whose B the problem has to wait for
     int n;                // columns in use
-    int phase, f, group, first;   // which tile: phase, feature tile, group and its first row
+    int line, phase, f, group, set, first;   // which tile: line and phase, feature tile, group, its weight set and first row
     int cta0, parts;      // the CTAs that share the tile: cta0 .. cta0 + parts - 1
     __device__ int n16() const { return (n + 15) & ~15; }
     __device__ bool whole() const { return kb0 == 0 && kb1 == kbs; }
 };
 
-// The line of K blocks of one phase: `tiles` tiles of `kbs` blocks, `per` blocks to a CTA.
+// a / b, by a 32-bit division where both fit (a 64-bit one is a long sequence).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// A line of K blocks: `tiles` tiles of `kbs` blocks, `per` blocks to a CTA.
 struct Line {
     int64_t units, per;
     int kbs;
-    __device__ Line(int64_t tiles, int k_blocks, int ctas) {
+    // `slack`: whole tiles, not equal stretches, where that takes a CTA at most this percentage of a stretch
+    __device__ Line(int64_t tiles, int k_blocks, int ctas, int slack) {
         kbs = k_blocks;
         units = tiles * kbs;
-        per = (units + ctas - 1) / ctas;
-        const int64_t least = kbs < kMinBlocks ? kbs : kMinBlocks;
+        per = quotient(units + ctas - 1, ctas);
+        const int64_t least = kbs < kMinBlocks ? kbs : kMinBlocks, whole = quotient(tiles + ctas - 1, ctas) * kbs;
         if (per < least) per = least;
+        if (whole * 100 <= per * slack) per = whole;
     }
     // Each segment of CTA `cta`, in order: f(tile, segment with K range and sharing CTAs filled in).
     template <class F>
@@ -70,13 +87,13 @@ struct Line {
         int64_t u = cta * per;
         const int64_t end = u + per < units ? u + per : units;
         while (u < end) {
-            const int64_t tile = u / kbs, begin = tile * kbs;
+            const int64_t tile = quotient(u, kbs), begin = tile * kbs;
             Segment s;
             s.kbs = kbs;
             s.kb0 = (int)(u - begin);
             s.kb1 = end - begin < kbs ? (int)(end - begin) : kbs;
-            s.cta0 = (int)(begin / per);
-            s.parts = (int)((begin + kbs - 1) / per) - s.cta0 + 1;
+            s.cta0 = (int)quotient(begin, per);
+            s.parts = (int)quotient(begin + kbs - 1, per) - s.cta0 + 1;
             if (!f(tile, s)) return false;
             u = begin + s.kb1;
         }
@@ -85,30 +102,49 @@ struct Line {
 };
 
 struct Control {
-    uint64_t full_a[kMaxStages], full_b[kMaxStages], empty[kMaxStages];
+    uint64_t full_a[kMaxStages], empty_a[kMaxStages], full_b[kMaxStages], empty_b[kMaxStages];
     uint64_t sums_full[2], sums_empty[2];
     uint64_t a_ready[2];     // E4M3: converted block in tensor memory
+    uint64_t a_free[2];      // ... and used up
     uint64_t last;
     uint32_t tmem;
-    int vote;
 };
 
+// A and B have a ring each: the loads of A in flight are what keeps HBM busy (five
+// or six blocks of 32 KB; with four the stream was 10% slower), those of B come
+// from L2 and are smaller.
 struct Shape {
     int cols;      // columns a tile may have: a multiple of 16, at most 128 (E4M3: 64)
-    int stages;
-    static constexpr int b_bytes(int cols, bool e4m3) { return cols * (e4m3 ? 256 : 128); }
-    static constexpr int stage_bytes(int cols, bool e4m3) { return 2 * kHalf + b_bytes(cols, e4m3); }
-    static int stages_for(int cols, bool e4m3) {
-        const int s = kSmemBudget / stage_bytes(cols, e4m3);
-        return s < kMaxStages ? s : kMaxStages;
+    int a_stages, b_stages;
+    __host__ __device__ static constexpr int b_bytes(int cols, bool e4m3) { return cols * (e4m3 ? 256 : 128); }
+    static Shape of(int cols, bool e4m3) {
+        const int b = b_bytes(cols, e4m3), a_stages = 3 * b <= kSmemBudget - 6 * 2 * kHalf ? 6 : 5;
+        const int b_stages = (kSmemBudget - a_stages * 2 * kHalf) / b;
+        return Shape{cols, a_stages, b_stages < kMaxStages ? b_stages : kMaxStages};
     }
-    static size_t smem(int cols, bool e4m3) { return 1024 + (size_t)stages_for(cols, e4m3) * stage_bytes(cols, e4m3); }
-    static int tmem_cols(int cols, bool e4m3) {
+    size_t smem(bool e4m3) const {
+        return 1024 + (size_t)a_stages * 2 * kHalf + (size_t)b_stages * b_bytes(cols, e4m3);
+    }
+    __device__ uint32_t a_at(int slot) const { return slot * 2 * kHalf; }
+    __device__ uint32_t b_at(int slot, bool e4m3) const { return a_stages * 2 * kHalf + slot * b_bytes(cols, e4m3); }
+    int tmem_cols(bool e4m3) const {
         if (e4m3) return 512;
         int c = 32;
         while (c < 4 * cols) c *= 2;
         return c;
     }
+};
+
+// What most roles do at the end of a phase.
+struct Nothing {
+    __device__ bool operator()() const { return true; }
+};
+
+// Most problems have nothing to add to their sums.
+struct NothingAhead {
+    template <class... T>
+    __device__ explicit NothingAhead(const T &...) {}
+    __device__ void add(int, float *) const {}
 };
 
 // Counts fills of the ring: slot and the parity of its barriers.
@@ -130,56 +166,73 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait(bar, parity));
 }
 
-// All reader threads agree: true if every one of them says so.
-__device__ __forceinline__ bool readers_agree(bool ok) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r) : "r"((uint32_t)ok) : "memory");
-    return r != 0;
-}
-__device__ __forceinline__ void readers_sync() { asm volatile("barrier.cta.sync 1, 256;" ::: "memory"); }
+// The readers (barrier 1) or the adders (barrier 2) as a team of kCount threads from kFirst.
+template <int kBarrier, int kFirst, int kCount>
+struct Team {
+    static constexpr int count = kCount;
+    static constexpr int first = kFirst;
+    __device__ static bool leader() { return threadIdx.x == first; }
+    __device__ static int warp() { return (threadIdx.x - first) / 32; }
+    __device__ static void sync() { asm volatile("barrier.cta.sync %0, %1;" ::"n"(kBarrier), "n"(kCount) : "memory"); }
+    // true if every thread of the team says so
+    __device__ static bool agree(bool ok) {
+        uint32_t r;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+            "barrier.cta.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+            : "=r"(r) : "r"((uint32_t)ok), "n"(kBarrier), "n"(kCount) : "memory");
+        return r != 0;
+    }
+};
+template <class P>
+using ReadersOf = Team<1, kFirstReader + (P::kConvert ? kConverters : 0), P::kReaders>;
+template <class P>
+using AddersOf = Team<2, ReadersOf<P>::first + P::kReaders, kAdders>;
 
-// Wait (bounded) until the word reaches `want`; release/acquire with add_release.
-__device__ __forceinline__ bool wait_count(const uint32_t *p, uint32_t want) {
-    if (ld_acquire_gpu_u32(p) >= want) return true;
+// Wait (bounded) until a counter reaches `want`; release/acquire with count_up.
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t *p) { return ld_acquire_gpu_u32(p); }
+__device__ __forceinline__ uint64_t ld_acquire(const uint64_t *p) {
+    uint64_t v;
+    asm volatile("ld.acquire.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+template <typename U>
+__device__ __forceinline__ bool wait_count(const U *p, U want) {
+    if (ld_acquire(p) >= want) return true;
     const uint64_t deadline = globaltimer_ns() + kDefaultWaitNs;
-    while (ld_acquire_gpu_u32(p) < want)
+    while (ld_acquire(p) < want)
         if (globaltimer_ns() > deadline) return false;
     return true;
 }
-__device__ __forceinline__ uint32_t add_acq_rel(uint32_t *p, uint32_t v) {
-    uint32_t old;
-    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(v) : "memory");
-    return old;
+__device__ __forceinline__ void count_up(uint32_t *p, uint32_t v) {
+    asm volatile("red.release.gpu.global.add.u32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ void count_up(uint64_t *p, uint64_t v) {
+    asm volatile("red.release.gpu.global.add.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
 }
 
 // ------------------------------------------------------------------ roles
 
-template <bool kE4m3, class P>
+template <class P>
 __device__ bool load_a(const P &p, Control &c, uint32_t ring_base, const Shape sh) {
     const uint64_t policy = policy_evict_first();
     const int lane = threadIdx.x & 31;
-    Ring r(sh.stages);
+    Ring r(sh.a_stages);
     int issued = 0;
     bool ok = true;
     if (lane == 0) {
         ok = p.segments([&](const Segment &s) {
             for (int kb = s.kb0; kb < s.kb1; ++kb, r.next(), ++issued) {
-                if (!wait(&c.empty[r.slot], r.round ^ 1)) return false;
-                const uint32_t dst = ring_base + r.slot * Shape::stage_bytes(sh.cols, kE4m3);
-                const int col = kb * (kE4m3 ? 128 : 64);
-                mbar_arrive_expect_tx(&c.full_a[r.slot], s.two ? 2 * s.a_bytes : s.a_bytes);
-                tma_load(dst, s.a_map, col, s.row0, &c.full_a[r.slot], policy);
-                if (s.two) tma_load(dst + kHalf, s.a_map, col, s.row1, &c.full_a[r.slot], policy);
+                if (!wait(&c.empty_a[r.slot], r.round ^ 1)) return false;
+                const uint32_t dst = ring_base + sh.a_at(r.slot);
+                p.a_load(s, kb, dst, &c.full_a[r.slot], policy);
             }
             return true;
         });
         if (!ok)   // leave only when the loads in flight have landed
-            for (int i = 0; i < sh.stages && i < issued; ++i) {
+            for (int i = 0; i < sh.a_stages && i < issued; ++i) {
                 const int fill = issued - 1 - i;
-                wait(&c.full_a[fill % sh.stages], (fill / sh.stages) & 1);
+                wait(&c.full_a[fill % sh.a_stages], (fill / sh.a_stages) & 1);
             }
     }
     return ok;
@@ -188,62 +241,75 @@ __device__ bool load_a(const P &p, Control &c, uint32_t ring_base, const Shape s
 template <bool kE4m3, class P>
 __device__ bool load_b(const P &p, Control &c, uint32_t ring_base, const Shape sh) {
     const int lane = threadIdx.x & 31;
-    Ring r(sh.stages);
+    Ring r(sh.b_stages);
     int issued = 0;
+    const uint64_t policy = policy_evict_last();
     const bool ok = p.segments([&](const Segment &s) {
-        bool ready = true;
-        if (lane == 0) ready = p.b_ready(s);
-        if (!__shfl_sync(0xffffffffu, ready, 0)) return false;
         typename P::Rows rows = p.b_rows(s, lane);
+        bool waited = false;
         for (int kb = s.kb0; kb < s.kb1; ++kb, r.next(), ++issued) {
-            bool free = true;
+            bool go = true;
             if (lane == 0) {
-                free = wait(&c.empty[r.slot], r.round ^ 1);
-                if (free) mbar_arrive_expect_tx(&c.full_b[r.slot], p.b_bytes(s) * (kE4m3 ? 2 : 1));
+                if (kb >= s.b_from && !waited) go = p.b_ready(s);
+                if (go) go = wait(&c.empty_b[r.slot], r.round ^ 1);
+                if (go) mbar_arrive_expect_tx(&c.full_b[r.slot], p.b_bytes(s, kb) * (kE4m3 ? 2 : 1));
             }
-            if (!__shfl_sync(0xffffffffu, free, 0)) return false;
-            const uint32_t dst = ring_base + r.slot * Shape::stage_bytes(sh.cols, kE4m3) + 2 * kHalf;
+            waited |= kb >= s.b_from;
+            if (!__shfl_sync(0xffffffffu, go, 0)) return false;
+            const uint32_t dst = ring_base + sh.b_at(r.slot, kE4m3);
 #pragma unroll
             for (int h = 0; h < (kE4m3 ? 2 : 1); ++h)
-                p.b_load(s, rows, (kb * (kE4m3 ? 2 : 1) + h) * 64, dst + h * sh.cols * 128, &c.full_b[r.slot], lane);
+                p.b_load(s, rows, kb * (kE4m3 ? 2 : 1) + h, dst + h * sh.cols * 128, &c.full_b[r.slot], policy, lane);
         }
         return true;
     });
     if (!ok && lane == 0)
-        for (int i = 0; i < sh.stages && i < issued; ++i) {
+        for (int i = 0; i < sh.b_stages && i < issued; ++i) {
             const int fill = issued - 1 - i;
-            wait(&c.full_b[fill % sh.stages], (fill / sh.stages) & 1);
+            wait(&c.full_b[fill % sh.b_stages], (fill / sh.b_stages) & 1);
         }
     return ok;
 }
 
-// Products of bf16 weights: lane 0 of one warp.
+// A whole warp waits and works out the operands; the same lane of it issues
+// every product and commit.
+//
+// Products of bf16 weights.
 template <class P>
 __device__ bool multiply(const P &p, Control &c, uint32_t ring_base, const Shape sh, uint32_t tmem) {
-    Ring r(sh.stages);
+    const bool mine = elect_one();
+    Ring ra(sh.a_stages), rb(sh.b_stages);
     uint32_t seq = 0;
     const bool ok = p.segments([&](const Segment &s) {
-        const uint32_t buf = seq & 1, desc = product_desc(s.n16());
-        const uint32_t d0 = tmem + buf * 2 * sh.cols, d1 = d0 + sh.cols;
-        if (!wait(&c.sums_empty[buf], (seq >> 1 & 1) ^ 1)) return false;
+        const uint32_t buf = seq & 1;
+        const uint32_t desc = uniform(product_desc(s.n16())), d0 = uniform(tmem + buf * 2 * sh.cols);
+        const uint32_t d1 = uniform(d0 + sh.cols);
+        const bool two = uniform(s.two) != 0;
+        if (!warp_wait(&c.sums_empty[buf], (seq >> 1 & 1) ^ 1)) return false;
         tc_fence_after();
-        for (int kb = s.kb0; kb < s.kb1; ++kb, r.next()) {
-            if (!wait(&c.full_a[r.slot], r.round) || !wait(&c.full_b[r.slot], r.round)) return false;
+        for (int kb = s.kb0; kb < s.kb1; ++kb, ra.next(), rb.next()) {
+            if (!warp_wait(&c.full_a[ra.slot], ra.round) || !warp_wait(&c.full_b[rb.slot], rb.round)) return false;
             tc_fence_after();
-            const uint32_t at = ring_base + r.slot * Shape::stage_bytes(sh.cols, false);
-            const uint64_t a0 = operand_desc(at), a1 = operand_desc(at + kHalf), b = operand_desc(at + 2 * kHalf);
+            const uint32_t a = uniform(operand_low(ring_base + sh.a_at(ra.slot)));
+            const uint32_t b = uniform(operand_low(ring_base + sh.b_at(rb.slot, false)));
+            const bool more = uniform(kb > s.kb0) != 0;
+            if (mine) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mma_ss(d0, a0 + 2 * k, b + 2 * k, desc, kb > s.kb0 || k > 0);
-            if (s.two)
+                for (int k = 0; k < 4; ++k) mma_ss(d0, a + 2 * k, b + 2 * k, desc, more || k > 0);
+                if (two)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_ss(d1, a1 + 2 * k, b + 2 * k, desc, kb > s.kb0 || k > 0);
-            mma_commit(&c.empty[r.slot]);
+                    for (int k = 0; k < 4; ++k) mma_ss(d1, a + (kHalf >> 4) + 2 * k, b + 2 * k, desc, more || k > 0);
+                mma_commit(&c.empty_a[ra.slot]);
+                mma_commit(&c.empty_b[rb.slot]);
+            }
+            __syncwarp();
         }
-        mma_commit(&c.sums_full[buf]);
+        if (mine) mma_commit(&c.sums_full[buf]);
+        __syncwarp();
         ++seq;
         return true;
     });
-    if (!ok) {
+    if (!ok && mine) {
         mma_commit(&c.last);
         wait(&c.last, 0);
     }
@@ -252,31 +318,38 @@ __device__ bool multiply(const P &p, Control &c, uint32_t ring_base, const Shape
 
 constexpr int kTmemCodes = 256;   // E4M3: first tensor-memory column of the converted blocks
 
-// Products of converted E4M3 blocks: lane 0 of one warp. Each block's sums start from zero.
+// Products of converted E4M3 blocks. Each block's sums start from zero.
 template <class P>
 __device__ bool multiply_e4m3(const P &p, Control &c, uint32_t ring_base, const Shape sh, uint32_t tmem) {
-    Ring r(sh.stages);
+    const bool mine = elect_one();
+    Ring r(sh.b_stages);
     uint32_t seq = 0;
+    const uint32_t half_b = uniform(sh.cols * 128 >> 4), half_d = uniform(sh.cols);
     const bool ok = p.segments([&](const Segment &s) {
-        const uint32_t desc = product_desc(s.n16());
+        const uint32_t desc = uniform(product_desc(s.n16()));
         for (int kb = s.kb0; kb < s.kb1; ++kb, r.next(), ++seq) {
             const uint32_t buf = seq & 1;
-            if (!wait(&c.full_b[r.slot], r.round) || !wait(&c.a_ready[buf], seq >> 1 & 1)) return false;
+            if (!warp_wait(&c.full_b[r.slot], r.round) || !warp_wait(&c.a_ready[buf], seq >> 1 & 1) ||
+                !warp_wait(&c.sums_empty[buf], (seq >> 1 & 1) ^ 1))
+                return false;
             tc_fence_after();
-            const uint32_t at = ring_base + r.slot * Shape::stage_bytes(sh.cols, true) + 2 * kHalf;
-            const uint32_t a = tmem + kTmemCodes + buf * 128, d = tmem + buf * 2 * sh.cols;
+            const uint32_t b = uniform(operand_low(ring_base + sh.b_at(r.slot, true)));
+            const uint32_t a = uniform(tmem + kTmemCodes + buf * 128), d = uniform(tmem + buf * 2 * sh.cols);
+            if (mine) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    mma_ts(d + h * sh.cols, a + h * 64 + k * 8,
-                           operand_desc(at + (k >> 2) * sh.cols * 128) + 2 * (k & 3), desc, k > 0);
-            mma_commit(&c.empty[r.slot]);
-            mma_commit(&c.sums_full[buf]);
+                    for (int k = 0; k < 8; ++k)
+                        mma_ts(d + h * half_d, a + h * 64 + k * 8, b + (k >> 2) * half_b + 2 * (k & 3), desc, k > 0);
+                mma_commit(&c.empty_b[r.slot]);
+                mma_commit(&c.a_free[buf]);
+                mma_commit(&c.sums_full[buf]);
+            }
+            __syncwarp();
         }
         return true;
     });
-    if (!ok) {
+    if (!ok && mine) {
         mma_commit(&c.last);
         wait(&c.last, 0);
     }
@@ -294,78 +367,166 @@ __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t two) {
     return out;
 }
 
-// What a reader thread does with its sums of a segment: row `row` of both
-// halves, columns 16 i + 8 side + 0..7. `each(f)` calls f(column, sums of half
-// 0, sums of half 1) for all of them.
-template <class P, class Each, class Release>
-__device__ bool hand_over(const P &p, Control &c, const Shape sh, const Segment &s, int row, Each each, Release release) {
-    if (s.whole()) {
-        if (!p.emit_ready(s)) return false;
-        typename P::Emit emit(p, s, row);
-        each([&](int col, const float *v0, const float *v1) { emit(col, v0, v1); });
-        release();
-    } else {
-        const size_t half = (size_t)sh.cols * kRows;
-        float *mine = p.partial(s.phase, blockIdx.x, s.kb0 > 0 ? 0 : 1);
-        each([&](int col, const float *v0, const float *v1) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                mine[(col + j) * kRows + row] = v0[j];
-                mine[half + (col + j) * kRows + row] = v1[j];
-            }
-        });
-        release();
-        __threadfence();
-        readers_sync();
-        if (threadIdx.x == kThreads - kReaders) {
-            uint32_t *arrived = p.arrivals(s.phase, s.cta0);
-            const uint32_t before = add_acq_rel(arrived, 1);
-            c.vote = before + 1 == (uint32_t)s.parts;
+// A thread's share of a tile's sums: one row, and eight values at a time.
+// P::kHalves: eight columns of one half (side % 2), every second eight of them
+// (side / 2) where four sides share the tile; else four columns of both halves,
+// the first half's first, so that a thread holds both sums of a pair of weight
+// rows. A step is 8 columns with two sides and 16 with four.
+template <bool kHalves>
+struct Share {
+    int row, side;   // 0..127, 0..3
+    __device__ static constexpr int step(int sides) { return sides == 2 ? 8 : 16; }
+    __device__ static Share of(int warp) { return Share{(warp & 3) * 32 + (int)(threadIdx.x & 31), warp / 4}; }
+    __device__ int first_col() const { return kHalves ? (side >> 1) * 8 : side * 4; }
+    __device__ int half_of(int j) const { return kHalves ? side & 1 : j / 4; }
+    __device__ static int col_of(int j) { return kHalves ? j : j & 3; }
+    __device__ void load(uint32_t at, int cols, int col, float (&v)[8]) const {
+        if (kHalves) {
+            tmem_load8(at + (side & 1) * cols + col, v);
+        } else {
+            tmem_load4(at + col, v);
+            tmem_load4(at + cols + col, v + 4);
         }
-        readers_sync();
-        const bool last = c.vote != 0;
-        readers_sync();
-        if (!last) return true;
-        __threadfence();
-        if (!p.emit_ready(s)) return false;
-        typename P::Emit emit(p, s, row);
-        const int side = (threadIdx.x - (kThreads - kReaders)) / 128;
-        for (int col = side * 8; col < s.n; col += 16) {
-            float v0[8] = {}, v1[8] = {};
-            for (int i = 0; i < s.parts; ++i) {
-                // a stretch that begins inside the tile is its CTA's first, the one that begins the tile its last
-                const float *part = p.partial(s.phase, s.cta0 + i, i == 0 ? 1 : 0);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    v0[j] += __ldcg(part + (col + j) * kRows + row);
-                    v1[j] += __ldcg(part + half + (col + j) * kRows + row);
-                }
-            }
-            emit(col, v0, v1);
-        }
+        tmem_load_wait(v);
     }
-    p.tile_done(s);
+};
+
+// This CTA's part of a tile that it shares: fp32 partial sums to the workspace, [half][column][row].
+template <class P, class Each>
+__device__ void leave_part(const P &p, const Shape sh, const Segment &s, const Share<P::kHalves> me,
+                           const typename P::Ahead &ahead, Each each) {
+    const size_t half = (size_t)sh.cols * kRows;
+    float *mine = p.partial(s.line, blockIdx.x, s.kb0 > 0 ? 0 : 1) + me.row;
+    each([&](int col, float *v) {
+        ahead.add(col, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int at = col + me.col_of(j);
+            if (at < s.n) mine[me.half_of(j) * half + at * kRows] = v[j];
+        }
+    });
+    __threadfence();
+    ReadersOf<P>::sync();
+    if (ReadersOf<P>::leader()) count_up(p.arrivals(s.line, s.cta0), 1u);
+}
+
+// This CTA's share of the columns of such a tile, in steps of 16, once all parts are there.
+template <class Tm, class P>
+__device__ bool add_up(const P &p, const Shape sh, const Segment &s) {
+    constexpr int kSides = Tm::count / 128;
+    const int units = P::kHalves ? 2 * ((s.n + 7) / 8) : (s.n + 3) / 4;
+    const int shares = min(s.parts, (units + kSides - 1) / kSides), me = blockIdx.x - s.cta0;
+    if (me >= shares) return true;
+    bool ok = true;
+    if (Tm::leader()) ok = wait_count(p.arrivals(s.line, s.cta0), (uint32_t)s.parts);
+    if (!Tm::agree(ok) || !p.template emit_ready<Tm>(s)) return false;
+    const size_t half = (size_t)sh.cols * kRows;
+    // unit: side unit % 4 of the 16 columns unit / 4; each of the team's groups of 128 threads takes one at a time
+    for (int unit = me * kSides + Tm::warp() / 4; unit < units; unit += s.parts * kSides) {
+        Share<P::kHalves> share = Share<P::kHalves>::of(Tm::warp());
+        share.side = unit & 3;
+        const int col = (unit >> 2) * 16 + share.first_col();
+        // eight parts' loads at once: a trip to another SM's sums in L2 takes about a microsecond
+        float v[8] = {};
+        for (int i0 = 0; i0 < s.parts; i0 += 8) {
+#pragma unroll
+            for (int j0 = 0; j0 < 8; j0 += 4) {
+                float x[8][4];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    // the stretch that begins the tile is its CTA's last, the others their CTA's first
+                    const float *part = p.partial(s.line, s.cta0 + i0 + i, i0 + i == 0 ? 1 : 0) + share.row;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int at = col + share.col_of(j0 + j);
+                        x[i][j] = i0 + i < s.parts && at < s.n ? __ldcg(part + share.half_of(j0 + j) * half + at * kRows) : 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j0 + j] += x[i][j];
+            }
+        }
+        typename P::Emit emit(p, s, share);
+        emit(col, v);
+    }
+    p.before_signal(s);
+    __threadfence();
+    Tm::sync();
+    // the shares' weights add up to kTileWeight
+    if (Tm::leader()) p.tile_done(s, kTileWeight * (me + 1) / shares - kTileWeight * me / shares);
     return true;
+}
+
+// What the reader threads do with a segment's sums. `each(f)` calls f(column,
+// 8 values) for all of the thread's columns, `release()` gives up the sums' place.
+template <class P>
+struct Readers {
+    using Tm = ReadersOf<P>;
+    const P &p;
+    Control &c;
+    const Shape sh;
+    Share<P::kHalves> me;
+    int shared = 0;          // without adders: tiles of this line shared with other CTAs, at most two
+    Segment tile[2];
+
+    template <class Each, class Release>
+    __device__ bool take(const Segment &s, const typename P::Ahead &ahead, Each each, Release release) {
+        if (s.whole()) {
+            if (!p.template emit_ready<Tm>(s)) return false;
+            typename P::Emit emit(p, s, me);
+            each([&](int col, float *v) { emit(col, v); });
+            release();
+            p.before_signal(s);
+            __threadfence();
+            Tm::sync();
+            if (Tm::leader()) p.tile_done(s, kTileWeight);
+            return true;
+        }
+        leave_part(p, sh, s, me, ahead, each);
+        release();
+        if constexpr (!P::kAdders) {
+            if (shared == 0) tile[0] = s;
+            else tile[1] = s;
+            ++shared;
+        }
+        return true;
+    }
+    __device__ bool end_line() {
+        if constexpr (!P::kAdders) {
+            for (int i = 0; i < shared; ++i)
+                if (!add_up<Tm>(p, sh, i == 0 ? tile[0] : tile[1])) return false;
+            shared = 0;
+        }
+        return true;
+    }
+};
+
+template <class P>
+__device__ bool add_shared(const P &p, Control &c, const Shape sh) {
+    return p.segments([&](const Segment &s) { return s.whole() || add_up<AddersOf<P>>(p, sh, s); });
 }
 
 // Readers of bf16 weights' sums.
 template <class P>
 __device__ bool read_sums(const P &p, Control &c, const Shape sh, uint32_t tmem) {
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, quarter = warp & 3, side = (warp - 4) / 4;
-    const int row = quarter * 32 + lane;
+    using Tm = ReadersOf<P>;
+    const int lane = threadIdx.x & 31;
+    Readers<P> readers{p, c, sh, Share<P::kHalves>::of(Tm::warp())};
+    const Share<P::kHalves> me = readers.me;
     uint32_t seq = 0;
     return p.segments([&](const Segment &s) {
         const uint32_t buf = seq & 1;
-        if (!readers_agree(wait(&c.sums_full[buf], seq >> 1 & 1))) return false;
+        const typename P::Ahead ahead(p, s, me);
+        if (!Tm::agree(wait(&c.sums_full[buf], seq >> 1 & 1))) return false;
         tc_fence_after();
-        const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + buf * 2 * sh.cols;
+        const uint32_t at = tmem + ((uint32_t)(me.row & ~31) << 16) + buf * 2 * sh.cols;
         auto each = [&](auto f) {
-            for (int col = side * 8; col < s.n16(); col += 16) {
-                float v[16];
-                tmem_load8(at + col, v);
-                tmem_load8(at + sh.cols + col, v + 8);
-                tmem_load_wait(v);
-                if (col < s.n) f(col, v, v + 8);
+            for (int col = me.first_col(); col < s.n16(); col += me.step(Tm::count / 128)) {
+                float v[8];
+                me.load(at, sh.cols, col, v);
+                if (col < s.n) f(col, v);
             }
         };
         auto release = [&] {
@@ -374,102 +535,134 @@ __device__ bool read_sums(const P &p, Control &c, const Shape sh, uint32_t tmem)
             if (lane == 0) mbar_arrive(&c.sums_empty[buf]);
         };
         ++seq;
-        return hand_over(p, c, sh, s, row, each, release);
-    });
+        return readers.take(s, ahead, each, release);
+    }, [&] { return readers.end_line(); });
 }
 
-// Readers of E4M3 weights: convert block i, then add block i - 1's scaled sums.
+// E4M3: the codes of each block into tensor memory as bf16. A thread converts
+// one row (lane of tensor memory) of one half.
 template <class P>
-__device__ bool read_sums_e4m3(const P &p, Control &c, const char *ring, const Shape sh, uint32_t tmem) {
-    constexpr int kChunks = 4;   // of 8 columns to a thread: 64 columns over two sides
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, quarter = warp & 3, side = (warp - 4) / 4;
-    const int row = quarter * 32 + lane;
-    const uint32_t lanes = (uint32_t)(quarter * 32) << 16;
-    Ring r(sh.stages);
+__device__ bool convert(const P &p, Control &c, const char *ring, const Shape sh, uint32_t tmem) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 - kFirstReader / 32;
+    const int row = (warp & 3) * 32 + lane, half = warp / 4;
+    const uint32_t dst0 = tmem + ((uint32_t)(row & ~31) << 16) + kTmemCodes + half * 64;
+    Ring r(sh.a_stages);
     uint32_t seq = 0;
     return p.segments([&](const Segment &s) {
-        float acc0[kChunks * 8] = {}, acc1[kChunks * 8] = {};
-        const float *scales = p.scales(s.phase);
-        const float *s0 = scales + (size_t)min(s.row0 + row, s.row_end - 1) * s.kbs;
-        const float *s1 = scales + (size_t)min(s.row1 + row, s.row_end - 1) * s.kbs;
-        float was0 = 0.0f, was1 = 0.0f;
-        bool ok = true;
-        auto add = [&](uint32_t q, float w0, float w1) {   // block q's sums
-            const uint32_t buf = q & 1;
-            if (!warp_wait(&c.sums_full[buf], q >> 1 & 1)) return false;
-            tc_fence_after();
-            const uint32_t at = tmem + lanes + buf * 2 * sh.cols;
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i) {
-                const int col = i * 16 + side * 8;
-                if (col >= s.n16()) break;
-                float v[16];
-                tmem_load8(at + col, v);
-                tmem_load8(at + sh.cols + col, v + 8);
-                tmem_load_wait(v);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    acc0[i * 8 + j] = fmaf(w0, v[j], acc0[i * 8 + j]);
-                    acc1[i * 8 + j] = fmaf(w1, v[8 + j], acc1[i * 8 + j]);
-                }
-            }
-            return true;
-        };
         for (int kb = s.kb0; kb < s.kb1; ++kb, r.next(), ++seq) {
-            const float now0 = __ldg(s0 + kb), now1 = __ldg(s1 + kb);
-            if (!warp_wait(&c.full_a[r.slot], r.round)) { ok = false; break; }
-            // this thread's row of its side's half: 128 codes, 16-byte pieces swizzled by the row
-            const char *codes = ring + (size_t)r.slot * Shape::stage_bytes(sh.cols, true) + side * kHalf + row * 128;
-            const uint32_t dst = tmem + lanes + kTmemCodes + (seq & 1) * 128 + side * 64;
+            const uint32_t buf = seq & 1;
+            if (!warp_wait(&c.full_a[r.slot], r.round)) return false;
+            // 16-byte pieces of a 128-byte row, swizzled by the row
+            const char *codes = ring + sh.a_at(r.slot) + half * kHalf + row * 128;
+            uint4 w[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) w[q] = *reinterpret_cast<const uint4 *>(codes + ((q ^ (row & 7)) << 4));
+            if (!warp_wait(&c.a_free[buf], (seq >> 1 & 1) ^ 1)) return false;
+            tc_fence_after();
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(codes + ((q ^ (row & 7)) << 4));
                 uint32_t b[8];
-                b[0] = codes_to_bf16(w.x), b[1] = codes_to_bf16(w.x >> 16);
-                b[2] = codes_to_bf16(w.y), b[3] = codes_to_bf16(w.y >> 16);
-                b[4] = codes_to_bf16(w.z), b[5] = codes_to_bf16(w.z >> 16);
-                b[6] = codes_to_bf16(w.w), b[7] = codes_to_bf16(w.w >> 16);
-                tmem_store8(dst + q * 8, b);
+                b[0] = codes_to_bf16(w[q].x), b[1] = codes_to_bf16(w[q].x >> 16);
+                b[2] = codes_to_bf16(w[q].y), b[3] = codes_to_bf16(w[q].y >> 16);
+                b[4] = codes_to_bf16(w[q].z), b[5] = codes_to_bf16(w[q].z >> 16);
+                b[6] = codes_to_bf16(w[q].w), b[7] = codes_to_bf16(w[q].w >> 16);
+                tmem_store8(dst0 + buf * 128 + q * 8, b);
+                if (q == 3) {   // the codes are in registers by now
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&c.empty_a[r.slot]);
+                }
             }
             tmem_store_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(&c.empty[r.slot]);
-                mbar_arrive(&c.a_ready[seq & 1]);
-            }
-            if (kb > s.kb0 && !add(seq - 1, was0, was1)) { ok = false; break; }
-            was0 = now0, was1 = now1;
+            if (lane == 0) mbar_arrive(&c.a_ready[buf]);
         }
-        if (ok) ok = add(seq - 1, was0, was1);
-        if (!readers_agree(ok)) return false;
-        auto each = [&](auto f) {
-#pragma unroll
-            for (int i = 0; i < kChunks; ++i)
-                if (i * 16 + side * 8 < s.n) f(i * 16 + side * 8, acc0 + i * 8, acc1 + i * 8);
-        };
-        return hand_over(p, c, sh, s, row, each, [] {});
+        return true;
     });
 }
 
-// The whole kernel body; P::finish runs on the reader threads after the last segment.
-template <bool kE4m3, class P>
-__device__ void run(const P &p, const Shape sh, const uint32_t tmem_cols) {
+// Readers of E4M3 weights' sums: each block's, scaled, into registers; tiles of up to 8 kSteps columns.
+template <int kSteps, class P>
+__device__ bool read_sums_e4m3(const P &p, Control &c, const Shape sh, uint32_t tmem) {
+    using Tm = ReadersOf<P>;
+    static_assert(!P::kHalves && P::kReaders == 256, "a thread scales both halves, two sides share the columns");
+    const int lane = threadIdx.x & 31;
+    Readers<P> readers{p, c, sh, Share<false>::of(Tm::warp())};
+    const Share<false> me = readers.me;
+    const uint32_t at0 = tmem + ((uint32_t)(me.row & ~31) << 16);
+    uint32_t seq = 0;
+    return p.segments([&](const Segment &s) {
+        float acc[kSteps][8] = {};
+        const float *scales = p.scales(s.phase);
+        const int rows = p.weight_rows(s.phase);
+        const float *s0 = scales + (size_t)min(s.row0 + me.row, rows - 1) * s.kbs;
+        const float *s1 = scales + (size_t)min(s.row1 + me.row, rows - 1) * s.kbs;
+        bool ok = true;
+        // scales come four blocks ahead: every eighth block's are in a new sector
+        float w0[4], w1[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) w0[u] = __ldg(s0 + min(s.kb0 + u, s.kb1 - 1)), w1[u] = __ldg(s1 + min(s.kb0 + u, s.kb1 - 1));
+        for (int kb4 = s.kb0; kb4 < s.kb1 && ok; kb4 += 4) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (kb4 + u >= s.kb1) break;
+                const uint32_t buf = seq & 1;
+                const float now0 = w0[u], now1 = w1[u];
+                const int later = min(kb4 + u + 4, s.kb1 - 1);
+                w0[u] = __ldg(s0 + later), w1[u] = __ldg(s1 + later);
+                if (!warp_wait(&c.sums_full[buf], seq >> 1 & 1)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t at = at0 + buf * 2 * sh.cols;
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    if (i * 8 >= s.n16()) break;
+                    float v[8];
+                    me.load(at, sh.cols, i * 8 + me.first_col(), v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(j < 4 ? now0 : now1, v[j], acc[i][j]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&c.sums_empty[buf]);
+                ++seq;
+            }
+        }
+        if (!Tm::agree(ok)) return false;
+        auto each = [&](auto f) {
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+                if (i * 8 + me.first_col() < s.n) f(i * 8 + me.first_col(), acc[i]);
+        };
+        return readers.take(s, typename P::Ahead(p, s, me), each, [] {});
+    }, [&] { return readers.end_line(); });
+}
+
+template <class P>
+constexpr int threads_of() {
+    return ReadersOf<P>::first + P::kReaders + (P::kAdders ? kAdders : 0);
+}
+
+// The whole kernel body, threads_of<P>() threads; `problem()` makes
+// the problem after the set-up; P::finish runs on the reader threads after the last segment.
+template <bool kE4m3, class P, class Make>
+__device__ void run(Make problem, const Shape sh, const uint32_t tmem_cols) {
     extern __shared__ char smem_raw[];
     __shared__ Control c;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int warp = (int)uniform(threadIdx.x / 32);
     char *ring = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
     const uint32_t ring_base = smem_addr(ring);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < sh.stages; ++i) {
+        for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&c.full_a[i], 1);
             mbar_init(&c.full_b[i], 1);
-            mbar_init(&c.empty[i], kE4m3 ? 9 : 1);   // the products, and the 8 converting warps
+            mbar_init(&c.empty_a[i], kE4m3 ? kConverters / 32 : 1);   // the converting warps, or the products
+            mbar_init(&c.empty_b[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c.sums_full[i], 1);
-            mbar_init(&c.sums_empty[i], 8);
-            mbar_init(&c.a_ready[i], 8);
+            mbar_init(&c.sums_empty[i], P::kReaders / 32);
+            mbar_init(&c.a_ready[i], kConverters / 32);
+            mbar_init(&c.a_free[i], 1);
         }
         mbar_init(&c.last, 1);
         fence_barrier_init();
@@ -479,19 +672,22 @@ __device__ void run(const P &p, const Shape sh, const uint32_t tmem_cols) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = c.tmem;
+    const P p = problem();
 
     bool ok = true;
-    if (warp == 0) ok = load_a<kE4m3>(p, c, ring_base, sh);
+    if (warp == 0) ok = load_a(p, c, ring_base, sh);
     else if (warp == 1) ok = load_b<kE4m3>(p, c, ring_base, sh);
     else if (warp == 2) {
-        if (lane == 0) {
-            if constexpr (kE4m3) ok = multiply_e4m3(p, c, ring_base, sh, tmem);
-            else ok = multiply(p, c, ring_base, sh, tmem);
-        }
-    } else if (warp >= 4) {
-        if constexpr (kE4m3) ok = read_sums_e4m3(p, c, ring, sh, tmem);
+        if constexpr (kE4m3) ok = multiply_e4m3(p, c, ring_base, sh, tmem);
+        else ok = multiply(p, c, ring_base, sh, tmem);
+    } else if (threadIdx.x >= AddersOf<P>::first) {
+        if constexpr (P::kAdders) ok = add_shared(p, c, sh);
+    } else if (threadIdx.x >= ReadersOf<P>::first) {
+        if constexpr (kE4m3) ok = read_sums_e4m3<P::kSteps>(p, c, sh, tmem);
         else ok = read_sums(p, c, sh, tmem);
         if (ok) ok = p.finish();
+    } else if (warp >= 4) {
+        if constexpr (kE4m3) ok = convert(p, c, ring, sh, tmem);
     }
     if (!ok) report(p.status, MOE_ERR_TIMEOUT);
     tc_fence_before();
@@ -500,6 +696,10 @@ __device__ void run(const P &p, const Shape sh, const uint32_t tmem_cols) {
     if (warp == 3) tmem_free(tmem, tmem_cols);
 }
 
+// Words at the head of a workspace: groups (and those of a named set), finished
+// tiles (64 bits), arrivals of parts by line and CTA.
+constexpr int kGroupsWord = 0, kNamedWord = 1, kDoneWord = 2, kArrivals = 4, kWords = 4 + kMaxLines * kMaxCtas;
+
 // ------------------------------------------------------------------ plan
 
 // Sorts entries by the weight set that they name and cuts each set's into groups
@@ -507,8 +707,10 @@ __device__ void run(const P &p, const Shape sh, const uint32_t tmem_cols) {
 template <typename Index>
 struct PlanArgs {
     const Index *idx;        // [n], -1: none
-    int n, sets, cols;
-    uint32_t *words;         // [0] becomes the number of groups, the rest 0
+    int n, sets;
+    bool rest;               // entries that name none make up a last set of their own
+    int cols;
+    uint32_t *words;         // the numbers of groups and of those with a set that is named; the rest become 0
     int num_words;
     int4 *groups;            // {set, first sorted entry, entries, 0}
     int *order;              // sorted entries
@@ -526,38 +728,44 @@ template <typename Index>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Index> a) {
     WarpTrace wt(a.trace, MOE_TRACE_PLAN);
     grid_dependency_wait();
+    grid_launch_dependents();   // the next kernel's set-up
     extern __shared__ int32_t plan_smem[];
-    int32_t *start = plan_smem, *first_group = plan_smem + a.sets + 1;
-    for (int i = threadIdx.x; i <= a.sets; i += kPlanThreads) start[i] = 0;
+    const int sets = a.sets + (a.rest ? 1 : 0);
+    int32_t *start = plan_smem, *first_group = plan_smem + sets + 1;
+    auto set_of = [&](Index e) { return e >= 0 && e < a.sets ? (int)e : a.rest ? a.sets : -1; };
+    for (int i = threadIdx.x; i <= sets; i += kPlanThreads) start[i] = 0;
     for (int i = threadIdx.x; i < a.num_words; i += kPlanThreads) a.words[i] = 0;
     __syncthreads();
     for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
         const Index e = a.idx[i];
-        if (e >= 0 && e < a.sets) atomicAdd(&start[e], 1);
-        else if (e != -1) report(a.status, a.bad);
+        if (e < -1 || e >= a.sets) report(a.status, a.bad);
+        if (set_of(e) >= 0) atomicAdd(&start[set_of(e)], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < a.sets; e += kPlanThreads) first_group[e] = (start[e] + a.cols - 1) / a.cols;
+    for (int e = threadIdx.x; e < sets; e += kPlanThreads) first_group[e] = (start[e] + a.cols - 1) / a.cols;
     __syncthreads();
-    if (threadIdx.x < 32) warp_exclusive_scan(start, a.sets, threadIdx.x);
-    else if (threadIdx.x < 64) warp_exclusive_scan(first_group, a.sets, threadIdx.x - 32);
+    if (threadIdx.x < 32) warp_exclusive_scan(start, sets, threadIdx.x);
+    else if (threadIdx.x < 64) warp_exclusive_scan(first_group, sets, threadIdx.x - 32);
     __syncthreads();
-    for (int e = threadIdx.x; e < a.sets; e += kPlanThreads) {
+    for (int e = threadIdx.x; e < sets; e += kPlanThreads) {
         const int end = start[e + 1];
         for (int g = first_group[e], b = start[e]; b < end; ++g, b += a.cols)
             a.groups[g] = make_int4(e, b, min(a.cols, end - b), 0);
     }
-    if (threadIdx.x == 0) a.words[0] = first_group[a.sets];
+    if (threadIdx.x == 0) {
+        a.words[kGroupsWord] = first_group[sets];
+        a.words[kNamedWord] = first_group[a.sets];
+    }
     __syncthreads();
     for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
-        const Index e = a.idx[i];
-        if (e >= 0 && e < a.sets) a.order[atomicAdd(&start[e], 1)] = i;
+        const int e = set_of(a.idx[i]);
+        if (e >= 0) a.order[atomicAdd(&start[e], 1)] = i;
     }
 }
 
 template <typename Index>
 int launch_plan(const PlanArgs<Index> &a, cudaStream_t s) {
-    const size_t smem = (size_t)2 * (a.sets + 1) * 4;
+    const size_t smem = (size_t)2 * (a.sets + 2) * 4;
     const int rc = ensure_dynamic_smem((const void *)plan_kernel<Index>, smem);
     if (rc != MOE_OK) return rc;
     return launch_kernel(plan_kernel<Index>, dim3(1), dim3(kPlanThreads), smem, s, tuning().overlap != 0, a) ==
@@ -566,26 +774,27 @@ int launch_plan(const PlanArgs<Index> &a, cudaStream_t s) {
 
 // One CTA per SM, all of them resident at once (they wait for one another).
 template <class Args>
-int launch_resident(void (*kernel)(Args), Args &a, size_t smem, cudaStream_t s) {
+int launch_resident(void (*kernel)(Args), Args &a, int threads, size_t smem, cudaStream_t s) {
     const int rc = ensure_dynamic_smem((const void *)kernel, smem);
     if (rc != MOE_OK) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(device_sm_count() < kMaxCtas ? device_sm_count() : kMaxCtas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeCooperative;
     attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = tuning().overlap ? 2 : 1;
     void *args[] = {&a};
     return cudaLaunchKernelExC(&cfg, (const void *)kernel, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-// Words of the workspace that both sides share.
-constexpr int kGroupsWord = 0, kDoneWord = 1, kArrivals = 2, kWords = 2 + 2 * kMaxCtas;
-constexpr size_t partial_floats(int cols) { return (size_t)2 * kMaxCtas * 2 * 2 * cols * kRows; }
+// Partial sums of `lines` lines: two tiles per CTA and line.
+constexpr size_t partial_floats(int lines, int cols) { return (size_t)lines * kMaxCtas * 2 * 2 * cols * kRows; }
 
 // Byte offsets of the pieces of a workspace, each 256-byte aligned.
 struct Cut {

@@ -86,7 +86,14 @@ __device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// This warp's 32 lanes (of tensor memory's 128: lanes 32 * (warp % 4) up) x 8 columns from `addr`.
+// This warp's 32 lanes (of tensor memory's 128: lanes 32 * (warp % 4) up) x 4 or 8 columns from `addr`.
+__device__ __forceinline__ void tmem_load4(uint32_t addr, float *v) {
+    uint32_t r[4];
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(r[i]);
+}
 __device__ __forceinline__ void tmem_load8(uint32_t addr, float *v) {
     uint32_t r[8];
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -105,19 +112,31 @@ __device__ __forceinline__ void tmem_load_wait(float (&v)[N]) {
 
 __device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t *r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                 ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
+                 ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ------------------------------------------------------------------ matrix products
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// The same value in every lane, and known to be: products take their operands
+// from uniform registers, and moving each there from a lane's own costs more
+// than a small product (80 cycles each, measured).
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // Shared-memory operand: rows of 128 bytes (64 bf16 along K) under the 128-byte
 // swizzle, groups of 8 rows 1024 bytes apart; the 16-wide K steps of one row
-// are 32 bytes apart.
-__device__ __forceinline__ uint64_t operand_desc(uint32_t addr) {
-    return (uint64_t)((addr >> 4) & 0x3fff) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 |
-           (uint64_t)2 << 61;
+// are 32 bytes apart. The low word holds the address, the high one is constant.
+__device__ __forceinline__ uint32_t operand_low(uint32_t addr) { return ((addr >> 4) & 0x3fff) | 1u << 16; }
+__device__ __forceinline__ uint64_t operand_desc(uint32_t low) {
+    constexpr uint32_t kHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
+    return (uint64_t)kHigh << 32 | low;
 }
 
 // bf16 x bf16 -> fp32, 128 rows of A, n rows of B (a multiple of 16, 16..256), both K-major.
@@ -125,21 +144,21 @@ __device__ __forceinline__ uint32_t product_desc(int n) {
     return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
 }
 
-// d (+)= A B^T over 16 columns of K, A in shared memory.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+// d (+)= A B^T over 16 columns of K, A in shared memory. By one lane of the warp.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t desc, bool add) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add) : "memory");
+        ::"r"(d), "l"(operand_desc(a_low)), "l"(operand_desc(b_low)), "r"(desc), "r"((uint32_t)add) : "memory");
 }
 // ... A in tensor memory (lane = row, two bf16 to a column).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_low, uint32_t desc, bool add) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d), "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add) : "memory");
+        ::"r"(d), "r"(a), "l"(operand_desc(b_low)), "r"(desc), "r"((uint32_t)add) : "memory");
 }
-// One arrival on `bar` when this thread's products so far are complete.
+// One arrival on `bar` when this lane's products so far are complete.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                  ::"r"(smem_addr(bar)) : "memory");

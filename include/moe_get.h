@@ -433,6 +433,8 @@ enum {
     MOE_TRACE_EXPERTS = 15,
     MOE_TRACE_ADAPTER = 16,
     MOE_TRACE_PLAN = 17,               /* entries sorted by expert or adapter */
+    MOE_TRACE_ADAPTER_SHRINK = 18,
+    MOE_TRACE_ADAPTER_SORT = 19,
     MOE_TRACE_PHASE = 0x10000          /* warp field of a per-CTA phase record: MOE_TRACE_PHASE + phase */
 };
 
@@ -637,7 +639,7 @@ MOE_API size_t moe_experts_workspace_size(int num_tokens, int hidden, int interm
  *   workspace      at least moe_experts_workspace_size() bytes; need not be
  *                  initialised; not shared by calls that overlap on the GPU.
  * Limits: T <= 1024, 1 <= k <= 32, E <= 8192, H and I multiples of 8 up to 2^20
- * (of 128 with E4M3), E * 2I and E * H < 2^31.
+ * (of 128 with E4M3), E * 2I and E * H at most 2^30.
  */
 MOE_API int moe_experts(const void *x, int num_tokens, int hidden, const int64_t *topk_idx,
                         const float *topk_weights, int num_topk, int num_experts, const void *w13,
@@ -668,9 +670,9 @@ MOE_API size_t moe_adapter_linear_workspace_size(int num_tokens, int in_features
  *
  *   out[t] = bf16_rn( w x[t] + scales[i] * b[i] (a[i] x[t]) ),  i = adapter_idx[t]
  *   out[t] = bf16_rn( w x[t] )                                 for adapter_idx[t] = -1
- * Products are summed in fp32 and the adapter's inner vector is kept in fp32.
- * Adapters may follow one another in any order; rows of one adapter next to each
- * other share its reads. An adapter reaches the rows that name it and no other
+ * Products are summed in fp32; the adapter's inner vector is kept in fp32, or as
+ * the sum of two bf16 where many rows share an adapter. Adapters may follow one
+ * another in any order. An adapter reaches the rows that name it and no other
  * (its infinities and NaN too). An index outside [-1, L) raises
  * MOE_ERR_BAD_ADAPTER and counts as -1.
  *
@@ -682,7 +684,7 @@ MOE_API size_t moe_adapter_linear_workspace_size(int num_tokens, int in_features
  *   workspace    at least moe_adapter_linear_workspace_size() bytes; need not be
  *                initialised; not shared by calls that overlap on the GPU.
  * Limits: K, N and r multiples of 8, K and N up to 2^20, r <= 128, L <= 8192,
- * T <= 2^20, T * N < 2^40.
+ * T <= 2^20, L * N at most 2^30.
  */
 MOE_API int moe_adapter_linear(const void *x, int num_tokens, int in_features, const void *w, int out_features,
                                const int32_t *adapter_idx, const void *a, const void *b, const float *scales,

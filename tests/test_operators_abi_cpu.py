@@ -110,7 +110,7 @@ def _adapter(lib, x=A, T=8, K=256, w=A + 0x100000, N=128, idx=A + 0x10000, a=A +
 
 @pytest.mark.parametrize("kw,code", [
     (dict(T=-1), 1), (dict(T=(1 << 20) + 1), 1), (dict(K=0), 1), (dict(K=252), 1), (dict(N=0), 1), (dict(N=12), 1),
-    (dict(L=0), 1), (dict(L=8193), 1), (dict(r=0), 1), (dict(r=12), 1), (dict(r=136), 1), (dict(x=None), 1),
+    (dict(L=0), 1), (dict(L=8193), 1), (dict(L=2048, N=1 << 20), 1), (dict(r=0), 1), (dict(r=12), 1), (dict(r=136), 1), (dict(x=None), 1),
     (dict(w=None), 1), (dict(idx=None), 1), (dict(a=None), 1), (dict(b=None), 1), (dict(s=None), 1), (dict(out=None), 1),
     (dict(ws=None), 1), (dict(status=None), 1), (dict(x=A + 8), 2), (dict(w=A + 8), 2), (dict(idx=MIS), 2),
     (dict(a=A + 8), 2), (dict(b=A + 8), 2), (dict(s=MIS), 2), (dict(out=A + 8), 2), (dict(ws=A + 8), 2),
