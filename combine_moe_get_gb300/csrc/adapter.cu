@@ -16,12 +16,14 @@
 // of two products.
 //
 // Row by row (few rows to an adapter): the shrink kernel makes v in fp32, four
-// warps to a row of A, and the projection multiplies all rows, in their own
-// order, by W; the readers of its sums add B_i v[t] in fp32, each thread for its
-// own row of B. The projection's loads do not depend on the shrink kernel, so it
-// is launched to overlap it.
+// warps to a row of A, the expand kernel B v in fp32, a thread to a row of B, and
+// the projection multiplies all rows, in their own order, by W and adds B v to
+// its sums. The projection's loads depend on neither, so it is launched to
+// overlap them: 128 rows, 48 adapters of rank 16, 7168 x 7168 are bound by the
+// 103 MB of W.
 #include <algorithm>
 #include <climits>
+#include <mutex>
 #include <cuda_bf16.h>
 
 #include "skinny.cuh"
@@ -31,44 +33,52 @@ namespace {
 
 using skinny::kRows;
 
-// Grouped costs another pass over W for every group that is not full, about
-// (L + 1) / 2 of them; row by row costs a pass over A for every row, from caches
-// that are about half as fast for it.
-bool grouped(int T, int N, int L, int r) { return (int64_t)4 * T * r > (int64_t)std::min(L + 1, T) * N; }
+// Row by row costs two passes over the adapters for every row, of A through
+// the caches (some 4 TB/s) and of B (some 10^13 products a second);
+// grouped costs another pass over W for every group that is not full, about
+// (L + 1) / 2 of them at some 10 TB/s from L2, and some 25 us of sorting and
+// hand-over. In units of 0.1 ps:
+bool grouped(int T, int K, int N, int L, int r) {
+    if ((int64_t)T * N > (int64_t)1 << 26) return true;   // no fp32 copy of a large output
+    return (double)T * r * (5.0 * K + N) > 2.5e8 + (double)std::min(L + 1, T) * N * K;
+}
 
-int columns(int T) { return std::min((T + 15) / 16 * 16, 128); }
+int grouped_columns(int T) { return std::min((T + 15) / 16 * 16, 128); }
 
 struct Space {
     size_t words, groups, order, v, x, partial, total;   // byte offsets
 };
 constexpr int kReady = skinny::kWords;   // then a word per group: its v is done
 
-Space space(int T, int K, int N, int L, int r, int cols) {
+Space space(int T, int K, int N, int L, int r) {
     Space s{};
     skinny::Cut cut;
-    s.words = cut.take(((size_t)kReady + T) * 4);
-    s.groups = cut.take((size_t)T * sizeof(int4));   // groups are at most as many as rows
-    s.order = cut.take((size_t)T * 4);
-    s.v = cut.take((size_t)(T + 8) * r * 4);         // fp32, or two bf16
-    s.x = cut.take(grouped(T, N, L, r) ? (size_t)T * K * 2 : 0);   // rows of x, sorted
-    s.partial = cut.take(skinny::partial_floats(2, cols) * 4);
+    s.v = cut.take((size_t)T * r * 4);   // fp32, or two bf16
+    if (grouped(T, K, N, L, r)) {
+        s.words = cut.take(((size_t)kReady + T) * 4);
+        s.groups = cut.take((size_t)T * sizeof(int4));   // groups are at most as many as rows
+        s.order = cut.take((size_t)T * 4);
+        s.x = cut.take((size_t)T * K * 2);               // rows of x, sorted
+        s.partial = cut.take(skinny::partial_floats(2, grouped_columns(T)) * 4);
+    } else {
+        s.x = cut.take((size_t)T * N * 4);               // each row's B v
+    }
     s.total = cut.at;
     return s;
 }
 
 struct AdapterArgs {
     CUtensorMap w, a_map, b_map, x, v_map;   // x: `cols` rows a box, of x or of its sorted copy
-    const int32_t *idx;
-    const __nv_bfloat16 *b;
     const float *scales;
     uint32_t *words;
     const int4 *groups;
     const int *order;
-    void *v;
+    void *v;   // grouped: v as two bf16; row by row: B v in fp32
     float *partials;
     __nv_bfloat16 *out;
     int32_t *status;
     int T, K, N, L, r;
+    int split;   // row by row: CTAs that share a tile
     skinny::Shape shape;
     uint32_t tmem_cols;
     TraceArgs trace;
@@ -87,14 +97,6 @@ struct AdapterBase {
         tiles = (a.N + 2 * kRows - 1) / (2 * kRows);
         kbs = (a.K + 63) / 64;
     }
-    __device__ float *partial(int line, int cta, int slot) const {
-        return a.partials + ((size_t)(line * skinny::kMaxCtas + cta) * 2 + slot) * 2 * a.shape.cols * kRows;
-    }
-    __device__ uint32_t *arrivals(int line, int cta) const {
-        return a.words + skinny::kArrivals + line * skinny::kMaxCtas + cta;
-    }
-    template <class Team>
-    __device__ bool emit_ready(const skinny::Segment &) const { return true; }
     __device__ bool finish() const { return true; }
 };
 
@@ -123,7 +125,6 @@ __global__ void __launch_bounds__(256) adapter_sort_kernel(const SortArgs s) {
 struct GroupedAdapter : AdapterBase {
     static constexpr bool kAdders = true;
     static constexpr int kReaders = 512;
-    using Ahead = skinny::NothingAhead;
     int G, with_adapter;   // groups; those before it have an adapter
     int more;              // K blocks of v's first part
 
@@ -133,8 +134,15 @@ struct GroupedAdapter : AdapterBase {
         more = (a.r + 63) / 64;
     }
 
-    template <class F, class End = skinny::Nothing>
-    __device__ bool segments(F f, End end_line = End()) const {
+    __device__ float *partial(int line, int cta, int slot) const {
+        return a.partials + ((size_t)(line * skinny::kMaxCtas + cta) * 2 + slot) * 2 * a.shape.cols * kRows;
+    }
+    __device__ uint32_t *arrivals(int line, int cta) const {
+        return a.words + skinny::kArrivals + line * skinny::kMaxCtas + cta;
+    }
+
+    template <class F>
+    __device__ bool segments(F f) const {
         for (int phase = 0; phase < 2; ++phase) {
             const skinny::Line line(phase == 0 ? with_adapter : (int64_t)G * tiles, phase == 0 ? kbs : kbs + 2 * more,
                                     gridDim.x, skinny::kSlackWork);
@@ -152,7 +160,7 @@ struct GroupedAdapter : AdapterBase {
                 s.b_from = phase == 1 && g.x < a.L ? kbs : INT_MAX;
                 return f(s);
             });
-            if (!ok || !end_line()) return false;
+            if (!ok) return false;
         }
         return true;
     }
@@ -248,8 +256,7 @@ struct ShrinkArgs {
     const int32_t *idx;
     const float *scales;
     float *v;            // [T, r]
-    uint32_t *words;
-    int T, K, L, r;
+    int K, L, r;
     int32_t *status;
     TraceArgs trace;
 };
@@ -264,8 +271,6 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const ShrinkArgs s)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (s.r + kShrinkRows - 1) / kShrinkRows;
     const int t = blockIdx.x / per, row0 = (blockIdx.x - t * per) * kShrinkRows;
-    if (blockIdx.x == 0)
-        for (int i = threadIdx.x; i < skinny::kWords; i += 256) s.words[i] = 0;
     const int id = s.idx[t];
     if (id < 0 || id >= s.L) {
         if (id != -1 && row0 == 0 && threadIdx.x == 0) report(s.status, MOE_ERR_BAD_ADAPTER);
@@ -307,6 +312,65 @@ __global__ void __launch_bounds__(256) adapter_shrink_kernel(const ShrinkArgs s)
     }
 }
 
+struct ExpandArgs {
+    const __nv_bfloat16 *b;
+    const int32_t *idx;
+    const float *v;      // [T, r]
+    float *delta;        // [T, N]
+    int T, N, L, r;
+    TraceArgs trace;
+};
+
+constexpr int kExpandRows = 4;   // rows of x to a CTA, which has 256 rows of B
+
+// delta[t] = B v[t], 0 without an adapter: a thread has one row of B, its loads
+// for the CTA's rows of x all at once for every 8 of the rank.
+__global__ void __launch_bounds__(256) adapter_expand_kernel(const ExpandArgs e) {
+    WarpTrace wt(e.trace, MOE_TRACE_ADAPTER_EXPAND);
+    __shared__ float v[kExpandRows][MOE_MAX_ADAPTER_RANK];
+    const int tiles = (e.N + 255) / 256;
+    const int t0 = blockIdx.x / tiles * kExpandRows, o = (blockIdx.x % tiles) * 256 + threadIdx.x;
+    grid_launch_dependents();   // the projection's loads, before the shrink kernel ends
+    grid_dependency_wait();
+    int id[kExpandRows];
+#pragma unroll
+    for (int j = 0; j < kExpandRows; ++j) {
+        id[j] = t0 + j < e.T ? e.idx[t0 + j] : -1;
+        if (id[j] >= e.L) id[j] = -1;
+    }
+    for (int i = threadIdx.x; i < kExpandRows * e.r; i += 256) {
+        const int j = i / e.r, c = i - j * e.r;
+        if (t0 + j < e.T) v[j][c] = e.v[(size_t)(t0 + j) * e.r + c];
+    }
+    __syncthreads();
+    if (o >= e.N) return;
+    const __nv_bfloat16 *b = e.b + (size_t)o * e.r;
+    const size_t set = (size_t)e.N * e.r;
+    float acc[kExpandRows] = {};
+#pragma unroll 2
+    for (int c = 0; c < e.r; c += 8) {
+        uint4 w[kExpandRows];
+#pragma unroll
+        for (int j = 0; j < kExpandRows; ++j)
+            if (id[j] >= 0) w[j] = __ldg(reinterpret_cast<const uint4 *>(b + id[j] * set + c));
+#pragma unroll
+        for (int j = 0; j < kExpandRows; ++j) {
+            if (id[j] < 0) continue;
+            const uint32_t q[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                acc[j] = fmaf(bf16_low(q[k]), v[j][c + 2 * k], acc[j]);
+                acc[j] = fmaf(bf16_high(q[k]), v[j][c + 2 * k + 1], acc[j]);
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < kExpandRows; ++j)
+        if (t0 + j < e.T) e.delta[(size_t)(t0 + j) * e.N + o] = acc[j];
+}
+
+// Where tiles are fewer than CTAs, a cluster of `split` CTAs shares a tile, each
+// with a stretch of K; else CTAs take whole tiles in turn.
 struct RowAdapter : AdapterBase {
     static constexpr bool kAdders = false;
     static constexpr int kReaders = 256;
@@ -315,23 +379,34 @@ struct RowAdapter : AdapterBase {
         chunks = (a.T + a.shape.cols - 1) / a.shape.cols;
     }
 
-    template <class F, class End = skinny::Nothing>
-    __device__ bool segments(F f, End end_line = End()) const {
-        const skinny::Line line((int64_t)chunks * tiles, kbs, gridDim.x,
-                                a.shape.cols > 32 ? skinny::kSlackWork : skinny::kSlackBytes);
-        const bool ok = line.each(blockIdx.x, [&](int64_t tile, skinny::Segment &s) {
-            s.line = s.phase = 0;
-            s.group = (int)skinny::quotient(tile, tiles);
-            s.f = (int)(tile - (int64_t)s.group * tiles);
-            s.first = s.group * a.shape.cols;
-            s.n = min(a.shape.cols, a.T - s.first);
-            s.two = true;
-            s.row0 = s.f * 2 * kRows;
-            s.row1 = s.row0 + kRows;
-            s.b_from = INT_MAX;
+    // The one segment of a CTA of a cluster.
+    __device__ skinny::Segment of_tile(int64_t tile) const {
+        skinny::Segment s;
+        s.line = s.phase = s.set = 0;
+        s.group = (int)skinny::quotient(tile, tiles);
+        s.f = (int)(tile - (int64_t)s.group * tiles);
+        s.first = s.group * a.shape.cols;
+        s.n = min(a.shape.cols, a.T - s.first);
+        s.two = true;
+        s.row0 = s.f * 2 * kRows;
+        s.row1 = s.row0 + kRows;
+        s.b_from = INT_MAX;
+        s.kb0 = 0;
+        s.kb1 = s.kbs = kbs;
+        return s;
+    }
+    template <class F>
+    __device__ bool segments(F f) const {
+        if (a.split > 1) {
+            const int rank = blockIdx.x % a.split, per = (kbs + a.split - 1) / a.split;
+            skinny::Segment s = of_tile(blockIdx.x / a.split);
+            s.kb0 = rank * per;
+            s.kb1 = min(kbs, s.kb0 + per);
             return f(s);
-        });
-        return ok && end_line();
+        }
+        for (int64_t tile = blockIdx.x; tile < (int64_t)chunks * tiles; tile += gridDim.x)
+            if (!f(of_tile(tile))) return false;
+        return true;
     }
 
     __device__ void a_load(const skinny::Segment &s, int kb, uint32_t dst, uint64_t *bar, uint64_t policy) const {
@@ -348,124 +423,174 @@ struct RowAdapter : AdapterBase {
         if (lane == 0) tma_load(dst, &a.x, kb * 64, s.first, bar, policy);   // rows past T read as 0
     }
 
-    // B v of eight columns for one row of W and B
-    struct Part {
+    struct Emit {
         const AdapterArgs &a;
         const skinny::Segment &s;
-        int o;                    // the row
-        const __nv_bfloat16 *b;   // ... in the first adapter
-        __device__ Part(const RowAdapter &p, const skinny::Segment &seg, const skinny::Share<true> &me)
-            : a(p.a), s(seg), o(seg.row0 + (me.side & 1) * kRows + me.row) {
-            b = a.b + (size_t)min(o, a.N - 1) * a.r;
-        }
-        __device__ static float dot(const uint4 &w, const float *v, float x) {
-            const float4 lo = *reinterpret_cast<const float4 *>(v), hi = *reinterpret_cast<const float4 *>(v + 4);
-            x = fmaf(bf16_low(w.x), lo.x, x), x = fmaf(bf16_high(w.x), lo.y, x);
-            x = fmaf(bf16_low(w.y), lo.z, x), x = fmaf(bf16_high(w.y), lo.w, x);
-            x = fmaf(bf16_low(w.z), hi.x, x), x = fmaf(bf16_high(w.z), hi.y, x);
-            return fmaf(bf16_high(w.w), hi.w, fmaf(bf16_low(w.w), hi.z, x));
-        }
-        __device__ void add(int col, float *x) const {
-            int id[8];
-            bool same = true;
+        int o;   // this thread's row of W
+        __device__ Emit(const RowAdapter &p, const skinny::Segment &seg, const skinny::Share<true> &me)
+            : a(p.a), s(seg), o(seg.row0 + (me.side & 1) * kRows + me.row) {}
+        __device__ void operator()(int col, const float *sums) const {
+            if (o >= a.N) return;
+            const size_t at = (size_t)(s.first + col) * a.N + o;
+            const float *delta = static_cast<const float *>(a.v) + at;   // complete since the readers' dependency wait
+            float x[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                id[j] = a.idx[s.first + min(col + j, s.n - 1)];
-                if (id[j] >= a.L) id[j] = -1;
-                same &= id[j] == id[0];
-            }
-            const size_t set = (size_t)a.N * a.r;
-            const float *v = static_cast<const float *>(a.v) + (size_t)(s.first + col) * a.r;   // eight rows: as many are behind the last
-            if (!same) {
-                for (int i = 0; i < a.r; i += 8) {
-                    uint4 q[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (id[j] >= 0) q[j] = __ldg(reinterpret_cast<const uint4 *>(b + id[j] * set + i));
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        if (id[j] >= 0) x[j] = dot(q[j], v + j * a.r + i, x[j]);
-                }
-            } else if (id[0] >= 0) {   // one adapter: its row of B is read once for the eight
-                for (int i = 0; i < a.r; i += 8) {
-                    const uint4 q = __ldg(reinterpret_cast<const uint4 *>(b + id[0] * set + i));
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = dot(q, v + j * a.r + i, x[j]);
-                }
-            }
-        }
-    };
-    // The adapters' part of the columns that this CTA will add up of a tile that
-    // it shares (columns 8 i with i % parts its place among them): worked out
-    // while the products run, and left with this CTA's own part.
-    struct Ahead {
-        static constexpr int kKept = 3;
-        Part part;
-        int me;
-        bool shared;
-        float x[kKept][8] = {};
-        __device__ Ahead(const RowAdapter &p, const skinny::Segment &s, const skinny::Share<true> &share)
-            : part(p, s, share), me(blockIdx.x - s.cta0), shared(!s.whole()) {
-            if (!shared) return;
-#pragma unroll
-            for (int q = 0; q < kKept; ++q)
-                if (8 * (me + q * s.parts) < s.n) part.add(8 * (me + q * s.parts), x[q]);
-        }
-        __device__ void add(int col, float *v) const {
-            const int parts = part.s.parts, i = col / 8 - me;
-            if (i < 0 || i % parts != 0) return;
-            if (i / parts >= kKept) return part.add(col, v);
-#pragma unroll
-            for (int q = 0; q < kKept; ++q)
-                if (i / parts == q)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] += x[q][j];
-        }
-    };
-    struct Emit {
-        Part part;
-        bool add;   // a shared tile's parts hold it already
-        __device__ Emit(const RowAdapter &p, const skinny::Segment &s, const skinny::Share<true> &me)
-            : part(p, s, me), add(s.whole()) {}
-        __device__ void operator()(int col, float *x) const {
-            if (add) part.add(col, x);
-            const AdapterArgs &a = part.a;
-            if (part.o >= a.N) return;
+            for (int j = 0; j < 8; ++j) x[j] = col + j < s.n ? delta[(size_t)j * a.N] : 0.0f;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-                if (col + j < part.s.n)
-                    a.out[(size_t)(part.s.first + col + j) * a.N + part.o] = __float2bfloat16_rn(x[j]);
+                if (col + j < s.n) a.out[at + (size_t)j * a.N] = __float2bfloat16_rn(sums[j] + x[j]);
         }
     };
-    __device__ void before_signal(const skinny::Segment &) const {}
-    __device__ void tile_done(const skinny::Segment &, uint32_t) const {}
 };
 
-// Loads of x and W begin before the shrink kernel has ended: it passed its own
-// dependency wait, so all that came before it is complete, and it writes neither.
-__global__ void __launch_bounds__(skinny::threads_of<RowAdapter>(), 1)
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Sums of a tile whose K a cluster shares: each CTA sends its sums of the
+// columns that another will finish to that CTA's shared memory (the ring, which
+// no load or product uses any more), and adds up its own in the order of K.
+// Through L2 instead (partial sums, a counter, loads of all parts) this took
+// 18 us of 44 at 128 rows, 7168 x 7168.
+__device__ void finish_in_cluster(const RowAdapter &p, skinny::Control &c, char *ring, const skinny::Segment &s,
+                                  uint32_t tmem, bool &ok) {
+    using Tm = skinny::ReadersOf<RowAdapter>;
+    const AdapterArgs &a = p.a;
+    const skinny::Shape sh = a.shape;
+    const bool reader = threadIdx.x >= Tm::first;
+    const skinny::Share<true> me = skinny::Share<true>::of(Tm::warp());
+    const int split = a.split, rank = blockIdx.x % split, half = me.side & 1;
+    const int steps = s.n16() / 16, kept = (steps + split - 1) / split;   // steps of 16 columns, and of them one CTA's
+    constexpr int kStep = 16 * 2 * kRows;                                 // floats of a step: [column][half][row]
+    if (reader) {
+        ok = Tm::agree(skinny::wait(&c.sums_full[0], 0));
+        tc_fence_after();
+    }
+    cluster_sync();   // every ring of the cluster is free
+    if (reader && ok) {
+        const uint32_t at = tmem + ((uint32_t)(me.row & ~31) << 16);
+        const uint32_t base = smem_addr(ring);
+        for (int col = 0; col < s.n16(); col += 8) {
+            float v[8];
+            me.load(at, sh.cols, col, v);
+            const int step = col / 16;
+            uint32_t to;   // [part][step of the owner][column][half][row]
+            const uint32_t mine = base + (((rank * kept + step / split) * kStep) + ((col & 8) * 2 + half) * kRows + me.row) * 4;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(mine), "r"(step % split));
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to + j * 2 * kRows * 4), "f"(v[j]) : "memory");
+        }
+    }
+    cluster_sync();   // all parts have arrived
+    if (reader && ok) {
+        const float *parts = reinterpret_cast<const float *>(ring);
+        const RowAdapter::Emit emit(p, s, me);
+        for (int step = rank, k = 0; step < steps; step += split, ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int col = step * 16 + h * 8;
+                if (col >= s.n) break;
+                float v[8] = {};
+                for (int i = 0; i < split; ++i) {
+                    const float *part = parts + (i * kept + k) * kStep + (h * 16 + half) * kRows + me.row;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] += part[j * 2 * kRows];
+                }
+                emit(col, v);
+            }
+    }
+}
+
+// Loads of x and W begin while the two kernels before it run: the shrink kernel
+// passed its own dependency wait before it let the next start, so all that came
+// before it is complete, and neither writes x or W. At most half of an SM's
+// registers, so that their CTAs fit beside it.
+template <bool kCluster>
+__global__ void __launch_bounds__(skinny::threads_of<RowAdapter>(), 2)
     adapter_row_kernel(const __grid_constant__ AdapterArgs a) {
     WarpTrace wt(a.trace, MOE_TRACE_ADAPTER);
     if (threadIdx.x == 0)
         for (const CUtensorMap *m : {&a.w, &a.x}) tma_prefetch_map(m);
-    skinny::run<false, RowAdapter>([&] {
-        if (threadIdx.x >= skinny::ReadersOf<RowAdapter>::first) grid_dependency_wait();   // the counters and v
+    auto make = [&] {
+        if (threadIdx.x >= skinny::ReadersOf<RowAdapter>::first) grid_dependency_wait();   // B v
         return RowAdapter(a);
-    }, a.shape, a.tmem_cols);
+    };
+    if constexpr (kCluster)
+        skinny::run_one<RowAdapter>(make, a.shape, a.tmem_cols, [](const RowAdapter &p, skinny::Control &c, char *ring,
+                                                                   uint32_t tmem, bool &ok) {
+            p.segments([&](const skinny::Segment &s) {
+                finish_in_cluster(p, c, ring, s, tmem, ok);
+                return true;
+            });
+        });
+    else
+        skinny::run<false, RowAdapter>(make, a.shape, a.tmem_cols);
+}
+
+// Clusters of n CTAs of the row kernel that fit on the device at once, cached per device.
+int clusters_at_once(int n) {
+    static std::mutex mu;
+    static int known[64][skinny::kMaxSplit + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    int &v = known[dev][n];   // 0: not asked yet, else the answer + 1
+    if (v == 0) {
+        const size_t smem = 1024 + skinny::kSmemBudget;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(n);
+        cfg.blockDim = dim3(skinny::threads_of<RowAdapter>());
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {(unsigned)n, 1, 1};
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int fit = 0;
+        if (ensure_dynamic_smem((const void *)adapter_row_kernel<true>, smem) != MOE_OK ||
+            cudaOccupancyMaxActiveClusters(&fit, adapter_row_kernel<true>, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            fit = 0;
+        }
+        v = fit + 1;
+    }
+    return v - 1;
+}
+
+// Columns of a tile and the CTAs that share one. Wider tiles stream W less
+// often, narrower ones and larger clusters spread the work over more CTAs: about
+// 65 KB a microsecond to a CTA, a microsecond for each 16 columns that it
+// finishes and three for a cluster's exchange (measured).
+void choose_tiles(int T, int K, int N, int &cols, int &split) {
+    const int most = std::min((T + 15) / 16 * 16, 128), kbs = (K + 63) / 64;
+    const int64_t ctas = std::min(device_sm_count(), skinny::kMaxCtas);
+    double least = 0.0;
+    for (int c = most; c >= 16; c = c > 16 ? std::max(16, c / 32 * 16) : 0)
+        for (int n = 1; n <= skinny::kMaxSplit; n *= 2) {   // five to a cluster came in two waves on these GPCs
+            const int64_t tiles = ((int64_t)T + c - 1) / c * ((N + 2 * kRows - 1) / (2 * kRows));
+            if (n > 1 && (kbs < 2 * n || tiles > clusters_at_once(n) || (kbs + n - 1) / n * (n - 1) >= kbs)) continue;
+            const int64_t rounds = n > 1 ? 1 : (tiles + ctas - 1) / ctas;
+            const double us = (double)rounds * ((kbs + n - 1) / n * (2 * skinny::kHalf + c * 128) / 65e3 +
+                                                (c / 16 + n - 1) / n) + (n > 1 ? 3.0 : 0.0);
+            if (least == 0.0 || us < least) least = us, cols = c, split = n;
+        }
 }
 
 }  // namespace
 
-size_t adapter_workspace_bytes(int T, int K, int N, int L, int r) { return space(T, K, N, L, r, columns(T)).total; }
+size_t adapter_workspace_bytes(int T, int K, int N, int L, int r) { return space(T, K, N, L, r).total; }
 
 int launch_adapter_linear(const AdapterLaunch &L) {
     const int T = L.num_tokens, K = L.in_features, N = L.out_features, r = L.rank;
     if (T == 0) return MOE_OK;
-    const int cols = columns(T);
-    const Space sp = space(T, K, N, L.num_adapters, r, cols);
+    const bool by_group = grouped(T, K, N, L.num_adapters, r);
+    const Space sp = space(T, K, N, L.num_adapters, r);
     char *ws = static_cast<char *>(L.workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
-    const bool by_group = grouped(T, N, L.num_adapters, r);
+    const bool overlap = tuning().overlap != 0;
+    int cols = grouped_columns(T), split = 1;
+    if (!by_group) choose_tiles(T, K, N, cols, split);
 
     AdapterArgs a{};
     bool ok = make_tensor_map(&a.w, L.w, false, N, K, kRows) &&
@@ -475,41 +600,63 @@ int launch_adapter_linear(const AdapterLaunch &L) {
              make_tensor_map(&a.b_map, L.b, false, (uint64_t)L.num_adapters * N, r, kRows) &&
              make_tensor_map(&a.v_map, ws + sp.v, false, (uint64_t)2 * T, r, 8);
     if (!ok) return MOE_ERR_CUDA;
-    a.idx = L.adapter_idx;
-    a.b = static_cast<const __nv_bfloat16 *>(L.b);
     a.scales = L.scales;
-    a.words = reinterpret_cast<uint32_t *>(ws + sp.words);
-    a.groups = reinterpret_cast<const int4 *>(ws + sp.groups);
-    a.order = reinterpret_cast<const int *>(ws + sp.order);
-    a.v = ws + sp.v;
-    a.partials = reinterpret_cast<float *>(ws + sp.partial);
+    a.v = ws + (by_group ? sp.v : sp.x);
     a.out = static_cast<__nv_bfloat16 *>(L.out);
     a.status = L.status;
-    a.T = T, a.K = K, a.N = N, a.L = L.num_adapters, a.r = r;
+    a.T = T, a.K = K, a.N = N, a.L = L.num_adapters, a.r = r, a.split = split;
     a.shape = skinny::Shape::of(cols, false);
     a.tmem_cols = a.shape.tmem_cols(false);
     a.trace = trace_args();
     const size_t smem = a.shape.smem(false);
 
     if (by_group) {
+        a.words = reinterpret_cast<uint32_t *>(ws + sp.words);
+        a.groups = reinterpret_cast<const int4 *>(ws + sp.groups);
+        a.order = reinterpret_cast<const int *>(ws + sp.order);
+        a.partials = reinterpret_cast<float *>(ws + sp.partial);
         const skinny::PlanArgs<int32_t> plan{L.adapter_idx, T, L.num_adapters, true, cols, a.words, kReady + T,
                                              const_cast<int4 *>(a.groups), const_cast<int *>(a.order),
                                              MOE_ERR_BAD_ADAPTER, L.status, a.trace};
         const int rc = skinny::launch_plan(plan, s);
         if (rc != MOE_OK) return rc;
         const SortArgs so{static_cast<const uint4 *>(L.x), reinterpret_cast<uint4 *>(ws + sp.x), a.order, T, K / 8, a.trace};
-        if (launch_kernel(adapter_sort_kernel, dim3(T), dim3(256), 0, s, tuning().overlap != 0, so) != cudaSuccess)
-            return MOE_ERR_CUDA;
+        if (launch_kernel(adapter_sort_kernel, dim3(T), dim3(256), 0, s, overlap, so) != cudaSuccess) return MOE_ERR_CUDA;
         return skinny::launch_resident(adapter_grouped_kernel, a, skinny::threads_of<GroupedAdapter>(), smem, s);
     }
     const ShrinkArgs sh{static_cast<const __nv_bfloat16 *>(L.x), static_cast<const __nv_bfloat16 *>(L.a),
-                        L.adapter_idx, L.scales, static_cast<float *>(a.v), a.words, T, K, L.num_adapters, r,
+                        L.adapter_idx, L.scales, reinterpret_cast<float *>(ws + sp.v), K, L.num_adapters, r,
                         L.status, a.trace};
-    const int64_t ctas = (int64_t)T * ((r + kShrinkRows - 1) / kShrinkRows);
-    if (launch_kernel(adapter_shrink_kernel, dim3((unsigned)ctas), dim3(256), 0, s, tuning().overlap != 0, sh) !=
-        cudaSuccess)
+    const ExpandArgs ex{static_cast<const __nv_bfloat16 *>(L.b), L.adapter_idx, sh.v, static_cast<float *>(a.v), T, N,
+                        L.num_adapters, r, a.trace};
+    const int64_t shrinks = (int64_t)T * ((r + kShrinkRows - 1) / kShrinkRows);
+    const int64_t expands = (int64_t)((N + 255) / 256) * ((T + kExpandRows - 1) / kExpandRows);
+    const void *kernel = split > 1 ? (const void *)adapter_row_kernel<true> : (const void *)adapter_row_kernel<false>;
+    const int rc = ensure_dynamic_smem(kernel, smem);
+    if (rc != MOE_OK) return rc;
+    if (launch_kernel(adapter_shrink_kernel, dim3((unsigned)shrinks), dim3(256), 0, s, overlap, sh) != cudaSuccess ||
+        launch_kernel(adapter_expand_kernel, dim3((unsigned)expands), dim3(256), 0, s, overlap, ex) != cudaSuccess)
         return MOE_ERR_CUDA;
-    return skinny::launch_resident(adapter_row_kernel, a, skinny::threads_of<RowAdapter>(), smem, s);
+    const int64_t tiles = (int64_t)((T + cols - 1) / cols) * ((N + 2 * kRows - 1) / (2 * kRows));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(split > 1 ? tiles * split : std::min<int64_t>(tiles, device_sm_count())));
+    cfg.blockDim = dim3(skinny::threads_of<RowAdapter>());
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (split > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n++].val.clusterDim = {(unsigned)split, 1, 1};
+    }
+    if (overlap) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    void *args[] = {&a};
+    return cudaLaunchKernelExC(&cfg, kernel, args) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace moe

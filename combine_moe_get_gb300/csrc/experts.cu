@@ -39,11 +39,11 @@ struct Space {
 constexpr int kWaveBlocks = 28;
 constexpr int kReady = skinny::kWords;   // then a word per group: its finished h tiles
 
-// Columns of a tile: room for about twice an expert's share of the entries. An
+// Columns of a tile: room for more than an expert's even share of the entries. An
 // expert with more takes several groups, that is, streams its weights again.
 int columns(int T, int k, int E, bool e4m3) {
     const int most = std::min((T + 15) / 16 * 16, e4m3 ? 64 : 128);
-    const int64_t want = (2 * (int64_t)T * k / E + 8 + 15) / 16 * 16;
+    const int64_t want = (3 * (int64_t)T * k / (2 * E) + 8 + 15) / 16 * 16;
     return (int)std::min<int64_t>(most, std::max<int64_t>(want, 16));
 }
 
@@ -88,12 +88,12 @@ struct ExpertsArgs {
 
 template <bool kE4m3, int kCols>   // kCols: the most columns of a tile
 struct ExpertsProblem {
-    static constexpr int kSteps = kCols / 8;
+    static constexpr int kSteps = kCols / 8;   // E4M3
+    static_assert(kSteps > 0);
     static constexpr bool kHalves = false, kAdders = true;
     static constexpr bool kConvert = kE4m3;
     static constexpr int kReaders = kE4m3 ? 256 : 512;
     using Readers = skinny::ReadersOf<ExpertsProblem>;
-    using Ahead = skinny::NothingAhead;
     const ExpertsArgs &a;
     int G;
     int32_t *status;
@@ -107,8 +107,8 @@ struct ExpertsProblem {
         kbs[1] = (a.I + block - 1) / block;
     }
 
-    template <class F, class End = skinny::Nothing>
-    __device__ bool segments(F f, End end_line = End()) const {
+    template <class F>
+    __device__ bool segments(F f) const {
         // Waves of groups, one behind the other: phase 0 of wave w + 1 comes before phase 1 of wave w.
         const int64_t own = skinny::quotient((int64_t)G * tiles[1] * kbs[1], gridDim.x);
         const int waves = min(G, own >= kWaveBlocks ? a.max_waves : 1);
@@ -141,7 +141,7 @@ struct ExpertsProblem {
                 }
                 return f(s);
             });
-            if (!ok || !end_line()) return false;
+            if (!ok) return false;
         }
         return true;
     }
@@ -192,8 +192,6 @@ struct ExpertsProblem {
     __device__ uint32_t *arrivals(int line, int cta) const {
         return a.words + skinny::kArrivals + line * skinny::kMaxCtas + cta;
     }
-    template <class Team>
-    __device__ bool emit_ready(const skinny::Segment &) const { return true; }
     struct Emit {
         const ExpertsArgs &a;
         const skinny::Segment &s;

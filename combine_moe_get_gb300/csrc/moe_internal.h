@@ -139,7 +139,7 @@ TraceArgs trace_args();
 #define MOE_TUNE_DISPATCH_PREFETCH_KEEP 1
 #endif
 #ifndef MOE_TUNE_SKINNY_MIN_BLOCKS   // K blocks a CTA takes at least (skinny.cuh)
-#define MOE_TUNE_SKINNY_MIN_BLOCKS 8
+#define MOE_TUNE_SKINNY_MIN_BLOCKS 4
 #endif
 struct Tuning {
     int dispatch_warps, dispatch_stages, dispatch_chunk;

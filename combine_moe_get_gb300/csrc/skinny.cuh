@@ -6,15 +6,15 @@
 // What bounds it is the stream of weights, so the work is cut by bytes: all
 // tiles' K blocks stand in one line, each CTA takes an equal stretch of it
 // (tiles may begin and end inside a stretch), and a CTA's loads run ahead of
-// its products across tile and phase borders. A tile that several CTAs share
-// is summed by the last of them to arrive, in the order of K, from fp32
-// partial sums in the workspace: the result does not depend on the arrival
-// order.
+// its products across tile and phase borders. CTAs that share a tile leave
+// fp32 partial sums in the workspace, and each of them adds up its share of the
+// tile's columns, in the order of K, once all partial sums are there: the
+// result does not depend on the arrival order.
 //
 // Roles of a CTA's warps: 0 loads A (weights), 1 loads B (activations), 2 issues
 // the products, 3 owns the tensor memory, the next 8 or 16 (P::kReaders) read the
-// sums, and where a problem has several lines of work (P::kAdders) 4 more add
-// up shared tiles while the others go on to the next line.
+// sums, and where tiles are shared through the workspace (P::kAdders) 4 more add
+// those up while the others go on.
 //   bf16 weights: A and B from shared memory; sums stay in tensor memory for a
 //     whole stretch of K, double-buffered, so that the readers' work on one
 //     tile runs under the next tile's products.
@@ -36,6 +36,7 @@ namespace skinny {
 constexpr int kFirstReader = 128;      // first thread of the converting, else the reading warps
 constexpr int kAdders = 128;           // threads of the adding warps
 constexpr int kMaxLines = 8;
+constexpr int kMaxSplit = 8;           // CTAs of a cluster that share a tile
 constexpr uint32_t kTileWeight = 1024;   // what the finished parts of a tile count together
 constexpr int kConverters = 256;
 // Two thirds of the SMs draw all of HBM's bandwidth where a block costs little
@@ -68,18 +69,27 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
     return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// A line of K blocks: `tiles` tiles of `kbs` blocks, `per` blocks to a CTA.
+// A line of K blocks: `tiles` tiles of `kbs` blocks, cut for the CTAs in one of
+// three ways. With room for two CTAs or more to a tile, each tile goes to the
+// same number of neighbours (`span` blocks of the line, some of them past the
+// tile's end). Else whole tiles, where that makes the longest stretch at most
+// `slack` percent of an equal one; else equal stretches.
 struct Line {
-    int64_t units, per;
-    int kbs;
-    // `slack`: whole tiles, not equal stretches, where that takes a CTA at most this percentage of a stretch
-    __device__ Line(int64_t tiles, int k_blocks, int ctas, int slack) {
-        kbs = k_blocks;
-        units = tiles * kbs;
-        per = quotient(units + ctas - 1, ctas);
-        const int64_t least = kbs < kMinBlocks ? kbs : kMinBlocks, whole = quotient(tiles + ctas - 1, ctas) * kbs;
-        if (per < least) per = least;
-        if (whole * 100 <= per * slack) per = whole;
+    int64_t tiles, units, per;
+    int kbs, span;
+    __device__ Line(int64_t n, int k_blocks, int ctas, int slack) : tiles(n), kbs(k_blocks), span(k_blocks) {
+        const int least = min(kbs, kMinBlocks);
+        if (tiles > 0 && 2 * tiles <= ctas) {
+            const int share = min(ctas / (int)tiles, kbs / least);
+            per = (kbs + share - 1) / share;
+            span = (int)per * share;
+        } else {
+            const int64_t whole = quotient(tiles + ctas - 1, ctas) * kbs;
+            per = quotient(tiles * kbs + ctas - 1, ctas);
+            if (per < least) per = least;
+            if (whole * 100 <= per * slack) per = whole;
+        }
+        units = tiles * span;
     }
     // Each segment of CTA `cta`, in order: f(tile, segment with K range and sharing CTAs filled in).
     template <class F>
@@ -87,15 +97,15 @@ struct Line {
         int64_t u = cta * per;
         const int64_t end = u + per < units ? u + per : units;
         while (u < end) {
-            const int64_t tile = quotient(u, kbs), begin = tile * kbs;
+            const int64_t tile = quotient(u, span), begin = tile * span;
             Segment s;
             s.kbs = kbs;
             s.kb0 = (int)(u - begin);
-            s.kb1 = end - begin < kbs ? (int)(end - begin) : kbs;
+            s.kb1 = (int)(end - begin < kbs ? end - begin : kbs);
             s.cta0 = (int)quotient(begin, per);
             s.parts = (int)quotient(begin + kbs - 1, per) - s.cta0 + 1;
-            if (!f(tile, s)) return false;
-            u = begin + s.kb1;
+            if (s.kb0 < s.kb1 && !f(tile, s)) return false;
+            u = end - begin < span ? end : begin + span;
         }
         return true;
     }
@@ -133,18 +143,6 @@ struct Shape {
         while (c < 4 * cols) c *= 2;
         return c;
     }
-};
-
-// What most roles do at the end of a phase.
-struct Nothing {
-    __device__ bool operator()() const { return true; }
-};
-
-// Most problems have nothing to add to their sums.
-struct NothingAhead {
-    template <class... T>
-    __device__ explicit NothingAhead(const T &...) {}
-    __device__ void add(int, float *) const {}
 };
 
 // Counts fills of the ring: slot and the parity of its barriers.
@@ -393,12 +391,10 @@ struct Share {
 
 // This CTA's part of a tile that it shares: fp32 partial sums to the workspace, [half][column][row].
 template <class P, class Each>
-__device__ void leave_part(const P &p, const Shape sh, const Segment &s, const Share<P::kHalves> me,
-                           const typename P::Ahead &ahead, Each each) {
+__device__ void leave_part(const P &p, const Shape sh, const Segment &s, const Share<P::kHalves> me, Each each) {
     const size_t half = (size_t)sh.cols * kRows;
     float *mine = p.partial(s.line, blockIdx.x, s.kb0 > 0 ? 0 : 1) + me.row;
-    each([&](int col, float *v) {
-        ahead.add(col, v);
+    each([&](int col, const float *v) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int at = col + me.col_of(j);
@@ -419,7 +415,7 @@ __device__ bool add_up(const P &p, const Shape sh, const Segment &s) {
     if (me >= shares) return true;
     bool ok = true;
     if (Tm::leader()) ok = wait_count(p.arrivals(s.line, s.cta0), (uint32_t)s.parts);
-    if (!Tm::agree(ok) || !p.template emit_ready<Tm>(s)) return false;
+    if (!Tm::agree(ok)) return false;
     const size_t half = (size_t)sh.cols * kRows;
     // unit: side unit % 4 of the 16 columns unit / 4; each of the team's groups of 128 threads takes one at a time
     for (int unit = me * kSides + Tm::warp() / 4; unit < units; unit += s.parts * kSides) {
@@ -461,47 +457,28 @@ __device__ bool add_up(const P &p, const Shape sh, const Segment &s) {
 
 // What the reader threads do with a segment's sums. `each(f)` calls f(column,
 // 8 values) for all of the thread's columns, `release()` gives up the sums' place.
-template <class P>
-struct Readers {
+template <class P, class Each, class Release>
+__device__ bool take(const P &p, const Shape sh, const Segment &s, const Share<P::kHalves> me, Each each,
+                     Release release) {
     using Tm = ReadersOf<P>;
-    const P &p;
-    Control &c;
-    const Shape sh;
-    Share<P::kHalves> me;
-    int shared = 0;          // without adders: tiles of this line shared with other CTAs, at most two
-    Segment tile[2];
-
-    template <class Each, class Release>
-    __device__ bool take(const Segment &s, const typename P::Ahead &ahead, Each each, Release release) {
-        if (s.whole()) {
-            if (!p.template emit_ready<Tm>(s)) return false;
-            typename P::Emit emit(p, s, me);
-            each([&](int col, float *v) { emit(col, v); });
+    if constexpr (P::kAdders) {
+        if (!s.whole()) {
+            leave_part(p, sh, s, me, each);
             release();
-            p.before_signal(s);
-            __threadfence();
-            Tm::sync();
-            if (Tm::leader()) p.tile_done(s, kTileWeight);
             return true;
         }
-        leave_part(p, sh, s, me, ahead, each);
-        release();
-        if constexpr (!P::kAdders) {
-            if (shared == 0) tile[0] = s;
-            else tile[1] = s;
-            ++shared;
-        }
-        return true;
     }
-    __device__ bool end_line() {
-        if constexpr (!P::kAdders) {
-            for (int i = 0; i < shared; ++i)
-                if (!add_up<Tm>(p, sh, i == 0 ? tile[0] : tile[1])) return false;
-            shared = 0;
-        }
-        return true;
+    typename P::Emit emit(p, s, me);
+    each([&](int col, const float *v) { emit(col, v); });
+    release();
+    if constexpr (P::kAdders) {
+        p.before_signal(s);
+        __threadfence();
+        Tm::sync();
+        if (Tm::leader()) p.tile_done(s, kTileWeight);
     }
-};
+    return true;
+}
 
 template <class P>
 __device__ bool add_shared(const P &p, Control &c, const Shape sh) {
@@ -513,12 +490,10 @@ template <class P>
 __device__ bool read_sums(const P &p, Control &c, const Shape sh, uint32_t tmem) {
     using Tm = ReadersOf<P>;
     const int lane = threadIdx.x & 31;
-    Readers<P> readers{p, c, sh, Share<P::kHalves>::of(Tm::warp())};
-    const Share<P::kHalves> me = readers.me;
+    const Share<P::kHalves> me = Share<P::kHalves>::of(Tm::warp());
     uint32_t seq = 0;
     return p.segments([&](const Segment &s) {
         const uint32_t buf = seq & 1;
-        const typename P::Ahead ahead(p, s, me);
         if (!Tm::agree(wait(&c.sums_full[buf], seq >> 1 & 1))) return false;
         tc_fence_after();
         const uint32_t at = tmem + ((uint32_t)(me.row & ~31) << 16) + buf * 2 * sh.cols;
@@ -535,8 +510,8 @@ __device__ bool read_sums(const P &p, Control &c, const Shape sh, uint32_t tmem)
             if (lane == 0) mbar_arrive(&c.sums_empty[buf]);
         };
         ++seq;
-        return readers.take(s, ahead, each, release);
-    }, [&] { return readers.end_line(); });
+        return take(p, sh, s, me, each, release);
+    });
 }
 
 // E4M3: the codes of each block into tensor memory as bf16. A thread converts
@@ -587,8 +562,7 @@ __device__ bool read_sums_e4m3(const P &p, Control &c, const Shape sh, uint32_t 
     using Tm = ReadersOf<P>;
     static_assert(!P::kHalves && P::kReaders == 256, "a thread scales both halves, two sides share the columns");
     const int lane = threadIdx.x & 31;
-    Readers<P> readers{p, c, sh, Share<false>::of(Tm::warp())};
-    const Share<false> me = readers.me;
+    const Share<false> me = Share<false>::of(Tm::warp());
     const uint32_t at0 = tmem + ((uint32_t)(me.row & ~31) << 16);
     uint32_t seq = 0;
     return p.segments([&](const Segment &s) {
@@ -633,8 +607,8 @@ __device__ bool read_sums_e4m3(const P &p, Control &c, const Shape sh, uint32_t 
             for (int i = 0; i < kSteps; ++i)
                 if (i * 8 + me.first_col() < s.n) f(i * 8 + me.first_col(), acc[i]);
         };
-        return readers.take(s, typename P::Ahead(p, s, me), each, [] {});
-    }, [&] { return readers.end_line(); });
+        return take(p, sh, s, me, each, [] {});
+    });
 }
 
 template <class P>
@@ -642,15 +616,13 @@ constexpr int threads_of() {
     return ReadersOf<P>::first + P::kReaders + (P::kAdders ? kAdders : 0);
 }
 
-// The whole kernel body, threads_of<P>() threads; `problem()` makes
-// the problem after the set-up; P::finish runs on the reader threads after the last segment.
-template <bool kE4m3, class P, class Make>
-__device__ void run(Make problem, const Shape sh, const uint32_t tmem_cols) {
+// Barriers and tensor memory, then `roles(problem, ring, tensor memory, ok)` on
+// every thread; `problem()` makes the problem after the set-up.
+template <bool kE4m3, class P, class Make, class Roles>
+__device__ void with_set_up(Make problem, Control &c, const uint32_t tmem_cols, Roles roles) {
     extern __shared__ char smem_raw[];
-    __shared__ Control c;
     const int warp = (int)uniform(threadIdx.x / 32);
     char *ring = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
-    const uint32_t ring_base = smem_addr(ring);
     if (threadIdx.x == 0) {
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&c.full_a[i], 1);
@@ -673,27 +645,50 @@ __device__ void run(Make problem, const Shape sh, const uint32_t tmem_cols) {
     tc_fence_after();
     const uint32_t tmem = c.tmem;
     const P p = problem();
-
     bool ok = true;
-    if (warp == 0) ok = load_a(p, c, ring_base, sh);
-    else if (warp == 1) ok = load_b<kE4m3>(p, c, ring_base, sh);
-    else if (warp == 2) {
-        if constexpr (kE4m3) ok = multiply_e4m3(p, c, ring_base, sh, tmem);
-        else ok = multiply(p, c, ring_base, sh, tmem);
-    } else if (threadIdx.x >= AddersOf<P>::first) {
-        if constexpr (P::kAdders) ok = add_shared(p, c, sh);
-    } else if (threadIdx.x >= ReadersOf<P>::first) {
-        if constexpr (kE4m3) ok = read_sums_e4m3<P::kSteps>(p, c, sh, tmem);
-        else ok = read_sums(p, c, sh, tmem);
-        if (ok) ok = p.finish();
-    } else if (warp >= 4) {
-        if constexpr (kE4m3) ok = convert(p, c, ring, sh, tmem);
-    }
+    roles(p, ring, tmem, warp, ok);
     if (!ok) report(p.status, MOE_ERR_TIMEOUT);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 3) tmem_free(tmem, tmem_cols);
+}
+
+// The whole kernel body, threads_of<P>() threads; P::finish runs on the reader
+// threads after the last segment.
+template <bool kE4m3, class P, class Make>
+__device__ void run(Make problem, const Shape sh, const uint32_t tmem_cols) {
+    __shared__ Control c;
+    with_set_up<kE4m3, P>(problem, c, tmem_cols, [&](const P &p, char *ring, uint32_t tmem, int warp, bool &ok) {
+        if (warp == 0) ok = load_a(p, c, smem_addr(ring), sh);
+        else if (warp == 1) ok = load_b<kE4m3>(p, c, smem_addr(ring), sh);
+        else if (warp == 2) {
+            if constexpr (kE4m3) ok = multiply_e4m3(p, c, smem_addr(ring), sh, tmem);
+            else ok = multiply(p, c, smem_addr(ring), sh, tmem);
+        } else if (threadIdx.x >= AddersOf<P>::first) {
+            if constexpr (P::kAdders) ok = add_shared(p, c, sh);
+        } else if (threadIdx.x >= ReadersOf<P>::first) {
+            if constexpr (kE4m3) ok = read_sums_e4m3<P::kSteps>(p, c, sh, tmem);
+            else ok = read_sums(p, c, sh, tmem);
+            if (ok) ok = p.finish();
+        } else if (warp >= 4) {
+            if constexpr (kE4m3) ok = convert(p, c, ring, sh, tmem);
+        }
+    });
+}
+
+// bf16 weights, one segment: `finish(problem, control, ring, tensor memory, ok)`
+// on every thread once the other roles are through (it waits for the sums itself).
+template <class P, class Make, class Finish>
+__device__ void run_one(Make problem, const Shape sh, const uint32_t tmem_cols, Finish finish) {
+    __shared__ Control c;
+    with_set_up<false, P>(problem, c, tmem_cols, [&](const P &p, char *ring, uint32_t tmem, int warp, bool &ok) {
+        if (warp == 0) ok = load_a(p, c, smem_addr(ring), sh);
+        else if (warp == 1) ok = load_b<false>(p, c, smem_addr(ring), sh);
+        else if (warp == 2) ok = multiply(p, c, smem_addr(ring), sh, tmem);
+        __syncwarp();
+        finish(p, c, ring, tmem, ok);
+    });
 }
 
 // Words at the head of a workspace: groups (and those of a named set), finished
