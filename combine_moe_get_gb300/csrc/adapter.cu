@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(skinny::threads_of<GroupedAdapter>(), 1)
     WarpTrace wt(a.trace, MOE_TRACE_ADAPTER);
     if (threadIdx.x == 0)
         for (const CUtensorMap *m : {&a.w, &a.x, &a.a_map, &a.b_map, &a.v_map}) tma_prefetch_map(m);
-    skinny::run<false, GroupedAdapter>([&] {
+    skinny::run<false, GroupedAdapter>([&](char *) {
         grid_dependency_wait();
         return GroupedAdapter(a);
     }, a.shape, a.tmem_cols);
@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(skinny::threads_of<RowAdapter>(), 2)
     WarpTrace wt(a.trace, MOE_TRACE_ADAPTER);
     if (threadIdx.x == 0)
         for (const CUtensorMap *m : {&a.w, &a.x}) tma_prefetch_map(m);
-    auto make = [&] {
+    auto make = [&](char *) {
         if (threadIdx.x >= skinny::ReadersOf<RowAdapter>::first) grid_dependency_wait();   // B v
         return RowAdapter(a);
     };

@@ -3,9 +3,9 @@
 //   h[t, j]  = silu(G x_t) * (U x_t),  [G; U] = w13[e], e = topk_idx[t, j]
 //   out[t]   = sum_j topk_weights[t, j] * (w2[e] h[t, j])
 //
-// Two kernels. The plan kernel (one CTA) sorts the valid entries by expert and
-// cuts each expert's into groups of at most `cols` entries. The experts kernel
-// (one CTA per SM, launched cooperatively) runs skinny.cuh's body over two
+// The valid entries are sorted by expert and cut into groups of at most `cols` of
+// one expert: up to 256 entries by every CTA for itself, more by a plan kernel.
+// The experts kernel (one CTA per SM, launched cooperatively) runs skinny.cuh's body over two
 // phases of work: phase 0 makes h (a tile is 128 gate and the same 128 up rows,
 // so that one thread holds both sums of an element), phase 1 multiplies h by w2
 // (a tile is 256 rows) into y, one fp32 row per entry. A group's phase 1 waits
@@ -47,8 +47,8 @@ int columns(int T, int k, int E, bool e4m3) {
     return (int)std::min<int64_t>(most, std::max<int64_t>(want, 16));
 }
 
-// Waves of groups at most (each is a line of either phase): wider tiles have
-// larger partial sums.
+// Waves of groups at most, 1 or 2 (each is a line of either phase): wider tiles
+// have larger partial sums.
 int waves_for(int cols) { return cols <= 64 ? 2 : 1; }
 
 Space space(int T, int H, int I, int k, int cols) {
@@ -83,7 +83,15 @@ struct ExpertsArgs {
     skinny::Shape shape;
     uint32_t tmem_cols;
     int max_waves;
+    bool local;   // every CTA makes the plan for itself
     TraceArgs trace;
+};
+
+// The lines of work in their order: phase 0 of the waves, then their phase 1.
+struct Lines {
+    skinny::Line line[4];
+    int first_group[4];
+    int waves;
 };
 
 template <bool kE4m3, int kCols>   // kCols: the most columns of a tile
@@ -95,38 +103,56 @@ struct ExpertsProblem {
     static constexpr int kReaders = kE4m3 ? 256 : 512;
     using Readers = skinny::ReadersOf<ExpertsProblem>;
     const ExpertsArgs &a;
+    const skinny::LocalPlan *local;   // or null: the plan kernel's
     int G;
     int32_t *status;
     int tiles[2], kbs[2];   // tiles per group and K blocks per tile of the two phases
 
-    __device__ explicit ExpertsProblem(const ExpertsArgs &args) : a(args), G((int)args.words[skinny::kGroupsWord]), status(args.status) {
+    const Lines *lines;
+
+    // All threads of the CTA.
+    __device__ ExpertsProblem(const ExpertsArgs &args, const skinny::LocalPlan *plan, Lines &shared_lines)
+        : a(args), local(plan), status(args.status), lines(&shared_lines) {
+        G = local ? local->num_groups : (int)args.words[skinny::kGroupsWord];
         constexpr int block = kE4m3 ? 128 : 64;
         tiles[0] = (a.I + kRows - 1) / kRows;
         tiles[1] = (a.H + 2 * kRows - 1) / (2 * kRows);
         kbs[0] = (a.H + block - 1) / block;
         kbs[1] = (a.I + block - 1) / block;
+        // Waves of groups, one behind the other: phase 0 of wave 1 comes before phase 1 of wave 0. A
+        // line's divisions take the better part of a microsecond: one thread to a line.
+        const int64_t work = (int64_t)G * tiles[1] * kbs[1];
+        const int waves = a.max_waves == 2 && G > 1 && work >= (int64_t)kWaveBlocks * gridDim.x ? 2 : 1;
+        if (threadIdx.x < 2 * waves) {
+            const int phase = threadIdx.x >= waves, wave = threadIdx.x - (phase ? waves : 0);
+            const int g0 = wave == 0 ? 0 : G / 2, g1 = wave + 1 == waves ? G : G / 2;
+            shared_lines.first_group[threadIdx.x] = g0;
+            shared_lines.line[threadIdx.x] = skinny::Line((int64_t)(g1 - g0) * tiles[phase], kbs[phase], gridDim.x,
+                                                          kE4m3 || a.shape.cols > 32 ? skinny::kSlackWork : skinny::kSlackBytes);
+        }
+        if (threadIdx.x == 0) shared_lines.waves = waves;
+        __syncthreads();
     }
+
+    __device__ int4 group(int g) const {   // {expert, first sorted entry, entries}
+        if (local == nullptr) return a.groups[g];
+        const uint32_t v = local->groups[g];
+        return make_int4(v & 0x1fff, v >> 13 & 0xff, (v >> 21) + 1, 0);
+    }
+    __device__ int entry(int i) const { return local ? local->order[i] : a.order[i]; }
 
     template <class F>
     __device__ bool segments(F f) const {
-        // Waves of groups, one behind the other: phase 0 of wave w + 1 comes before phase 1 of wave w.
-        const int64_t own = skinny::quotient((int64_t)G * tiles[1] * kbs[1], gridDim.x);
-        const int waves = min(G, own >= kWaveBlocks ? a.max_waves : 1);
-        for (int step = 0; step <= 2 * waves; ++step) {
-            // 0(0) 0(1) 1(0) 0(2) 1(1) ... 0(n-1) 1(n-2) 1(n-1): even steps 2w are phase 0 of wave w, odd ones 2w+1 phase 1 of wave w-1
-            const int phase = step & 1 || step == 2 * waves ? 1 : 0;
-            const int wave = phase == 0 ? step / 2 : step == 2 * waves ? waves - 1 : step / 2 - 1;
-            if (wave < 0) continue;
-            const int g0 = (int)((int64_t)G * wave / waves), g1 = (int)((int64_t)G * (wave + 1) / waves);
-            const skinny::Line line((int64_t)(g1 - g0) * tiles[phase], kbs[phase], gridDim.x,
-                                    kE4m3 || a.shape.cols > 32 ? skinny::kSlackWork : skinny::kSlackBytes);
-            const bool ok = line.each(blockIdx.x, [&](int64_t tile, skinny::Segment &s) {
-                s.line = 2 * wave + phase;
+        const int waves = lines->waves;
+        for (int i = 0; i < 2 * waves; ++i) {
+            const int phase = i >= waves, g0 = lines->first_group[i];
+            const bool ok = lines->line[i].each(blockIdx.x, [&](int64_t tile, skinny::Segment &s) {
+                s.line = i;
                 s.phase = phase;
                 const int in_wave = (int)skinny::quotient(tile, tiles[phase]);
                 s.group = g0 + in_wave;
                 s.f = (int)(tile - (int64_t)in_wave * tiles[phase]);
-                const int4 g = a.groups[s.group];
+                const int4 g = group(s.group);
                 s.first = g.y;
                 s.n = g.z;
                 s.two = true;
@@ -167,7 +193,7 @@ struct ExpertsProblem {
         Rows rows{};
         if (s.phase == 0)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) rows.r[i] = a.order[s.first + min(4 * lane + i, s.n - 1)] / a.k;
+            for (int i = 0; i < 4; ++i) rows.r[i] = entry(s.first + min(4 * lane + i, s.n - 1)) / a.k;
         return rows;
     }
     __device__ uint32_t b_bytes(const skinny::Segment &s, int) const {
@@ -193,11 +219,12 @@ struct ExpertsProblem {
         return a.words + skinny::kArrivals + line * skinny::kMaxCtas + cta;
     }
     struct Emit {
+        const ExpertsProblem &p;
         const ExpertsArgs &a;
         const skinny::Segment &s;
         int row;
-        __device__ Emit(const ExpertsProblem &p, const skinny::Segment &seg, const skinny::Share<false> &me)
-            : a(p.a), s(seg), row(me.row) {}
+        __device__ Emit(const ExpertsProblem &problem, const skinny::Segment &seg, const skinny::Share<false> &me)
+            : p(problem), a(p.a), s(seg), row(me.row) {}
         __device__ void operator()(int col, const float *v) const {
             if (s.phase == 0) {
                 const int i = s.f * kRows + row;
@@ -212,7 +239,7 @@ struct ExpertsProblem {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (col + j >= s.n) continue;
-                    float *y = a.y + (size_t)a.order[s.first + col + j] * a.H + o;
+                    float *y = a.y + (size_t)p.entry(s.first + col + j) * a.H + o;
                     if (o < a.H) y[0] = v[j];
                     if (o + kRows < a.H) y[kRows] = v[4 + j];
                 }
@@ -268,9 +295,15 @@ __global__ void __launch_bounds__(skinny::threads_of<ExpertsProblem<kE4m3, kCols
     WarpTrace wt(a.trace, MOE_TRACE_EXPERTS);
     if (threadIdx.x == 0)
         for (const CUtensorMap *m : {&a.w13, &a.w2, &a.x, &a.h_map}) tma_prefetch_map(m);
-    skinny::run<kE4m3, ExpertsProblem<kE4m3, kCols>>([&] {
+    __shared__ Lines lines;
+    skinny::run<kE4m3, ExpertsProblem<kE4m3, kCols>>([&](char *ring) {
         grid_dependency_wait();
-        return ExpertsProblem<kE4m3, kCols>(a);
+        skinny::LocalPlan *plan = nullptr;
+        if (a.local) {
+            plan = reinterpret_cast<skinny::LocalPlan *>(ring + a.shape.ring_bytes(kE4m3));
+            skinny::local_plan(*plan, a.topk_idx, a.T * a.k, a.E, a.shape.cols, MOE_ERR_BAD_TOPK, a.status);
+        }
+        return ExpertsProblem<kE4m3, kCols>(a, plan, lines);
     }, a.shape, a.tmem_cols);
 }
 
@@ -280,7 +313,17 @@ size_t experts_workspace_bytes(int T, int H, int I, int k, int E) {
     return space(T, H, I, k, columns(T, k, E, false)).total;   // bf16 weights: the larger of the two
 }
 
-int launch_experts(const ExpertsLaunch &L) {
+namespace {
+bool is_local(int T, int k, int E) { return T * k <= skinny::kLocalEntries && E <= skinny::kLocalSets; }
+}  // namespace
+
+ExpertsWords experts_words(const ExpertsLaunch &L) {
+    const int n = L.num_tokens * L.num_topk;
+    if (L.num_tokens == 0 || !is_local(L.num_tokens, L.num_topk, L.num_experts)) return ExpertsWords{nullptr, 0};
+    return ExpertsWords{static_cast<uint32_t *>(L.workspace), kReady + n};   // the workspace's first piece
+}
+
+int launch_experts(const ExpertsLaunch &L, bool words_are_zero) {
     const int T = L.num_tokens, H = L.hidden, I = L.intermediate, k = L.num_topk, E = L.num_experts;
     if (T == 0) return MOE_OK;
     const bool e4m3 = L.w13_scales != nullptr;
@@ -289,10 +332,6 @@ int launch_experts(const ExpertsLaunch &L) {
     char *ws = static_cast<char *>(L.workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
 
-    const skinny::PlanArgs<int64_t> plan{L.topk_idx, T * k, E, false, cols, reinterpret_cast<uint32_t *>(ws + sp.words),
-                                         kReady + T * k, reinterpret_cast<int4 *>(ws + sp.groups),
-                                         reinterpret_cast<int *>(ws + sp.order), MOE_ERR_BAD_TOPK, L.status,
-                                         trace_args()};
     ExpertsArgs a{};
     if (!make_tensor_map(&a.w13, L.w13, e4m3, (uint64_t)E * 2 * I, H, kRows) ||
         !make_tensor_map(&a.w2, L.w2, e4m3, (uint64_t)E * H, I, kRows) ||
@@ -303,23 +342,33 @@ int launch_experts(const ExpertsLaunch &L) {
     a.topk_weights = L.topk_weights;
     a.s13 = L.w13_scales;
     a.s2 = L.w2_scales;
-    a.words = plan.words;
-    a.groups = plan.groups;
-    a.order = plan.order;
+    a.words = reinterpret_cast<uint32_t *>(ws + sp.words);
+    a.groups = reinterpret_cast<const int4 *>(ws + sp.groups);
+    a.order = reinterpret_cast<const int *>(ws + sp.order);
     a.h = reinterpret_cast<__nv_bfloat16 *>(ws + sp.h);
     a.y = reinterpret_cast<float *>(ws + sp.y);
     a.partials = reinterpret_cast<float *>(ws + sp.partial);
     a.out = static_cast<__nv_bfloat16 *>(L.out);
     a.status = L.status;
     a.T = T, a.H = H, a.I = I, a.k = k, a.E = E;
-    a.shape = skinny::Shape::of(cols, e4m3);
+    a.local = is_local(T, k, E);
+    a.shape = skinny::Shape::of(cols, e4m3, skinny::kSmemBudget - (a.local ? (int)sizeof(skinny::LocalPlan) : 0));
     a.tmem_cols = a.shape.tmem_cols(e4m3);
     a.max_waves = waves_for(cols);
     a.trace = trace_args();
 
-    const int rc = skinny::launch_plan(plan, s);
-    if (rc != MOE_OK) return rc;
-    const size_t smem = a.shape.smem(e4m3);
+    const bool overlap = tuning().overlap != 0;
+    if (!a.local) {
+        const skinny::PlanArgs<int64_t> plan{L.topk_idx, T * k, E, false, cols, a.words, kReady + T * k,
+                                             const_cast<int4 *>(a.groups), const_cast<int *>(a.order),
+                                             MOE_ERR_BAD_TOPK, L.status, a.trace};
+        const int rc = skinny::launch_plan(plan, s);
+        if (rc != MOE_OK) return rc;
+    } else if (!words_are_zero) {
+        if (launch_kernel(skinny::clear_kernel, dim3(1), dim3(1024), 0, s, overlap, a.words, kReady + T * k) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    }
+    const size_t smem = a.shape.smem(e4m3) + (a.local ? sizeof(skinny::LocalPlan) : 0);
     if (!e4m3) return skinny::launch_resident(experts_kernel<false, 128>, a, skinny::threads_of<ExpertsProblem<false, 128>>(), smem, s);
     const int threads = skinny::threads_of<ExpertsProblem<true, 64>>();
     return cols <= 32 ? skinny::launch_resident(experts_kernel<true, 32>, a, threads, smem, s)

@@ -4,15 +4,16 @@
 //
 // Mathematics. The chosen experts are the k largest logits (softmax and
 // sigmoid keep their order), or the k largest score + bias; ties go to the
-// lowest index. Logits are compared as 32-bit keys whose unsigned order is the
-// floats' order, so a choice is exact: no rounding takes part unless a bias is
-// given. Exponentials are taken of differences to the largest logit (0 at the
+// lowest index. Logits are compared as they are, so a choice is exact: no
+// rounding takes part unless a bias is given. Exponentials are taken of differences to the largest logit (0 at the
 // maximum even when that is +inf), sums are fp32.
 //
 // A warp handles a token: 32 lanes hold the row's E logits in registers (up to
-// 64 each), each choice is one max over the warp's keys and one min over the
-// indices that reach it (redux.sync), and lane j keeps entry j (k <= 32). Rows
-// longer than 2048 take one CTA per token with the keys in shared memory.
+// 64 each), so that a row is read once (and a gradient's written once), each
+// choice is one max over the warp's keys and one min over the indices that reach
+// it (redux.sync), and lane j keeps entry j (k <= 32). Rows longer than 2048 take
+// one CTA per token with the keys in shared memory, and in the backward pass a
+// warp that reads the row three times.
 #include <algorithm>
 #include <cuda_bf16.h>
 
@@ -35,6 +36,8 @@ struct GateArgs {
     int64_t *idx;
     float *w;
     int32_t *status;
+    uint32_t *clear;   // words zeroed for the kernel behind this one, or null
+    int num_clear;
     TraceArgs trace;
 };
 
@@ -50,12 +53,18 @@ struct GateBackArgs {
     TraceArgs trace;
 };
 
+// By the first CTA.
+__device__ __forceinline__ void clear_words(const GateArgs &a) {
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < a.num_clear; i += blockDim.x) a.clear[i] = 0;
+}
+
 __device__ __forceinline__ float to_float(float v) { return v; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
 __device__ __forceinline__ void store(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-// Unsigned order of the key = order of the float, -0 as +0; 0 (never chosen)
+// The wide kernel's keys: unsigned order of the key = order of the float, -0 as +0; 0 (never chosen)
 // for -inf and NaN.
 __device__ __forceinline__ uint32_t order_key(float v) {
     if (!(v > -INFINITY)) return 0;
@@ -113,27 +122,133 @@ __device__ __forceinline__ float entry_weight(int mode, float l, bool on, float 
     return is_sigmoid ? sigmoid(l).s : exp_below(l, m) / z;
 }
 
+// ------------------------------------------------------------------ a row in a warp's registers
+
+// Element i of a lane is expert_of(i, lane): four neighbours to a lane and load
+// where the rows allow it (kVec), else one.
+template <bool kVec>
+__device__ __forceinline__ int expert_of(int i, int lane) {
+    return kVec ? ((i >> 2) * 32 + lane) * 4 + (i & 3) : i * 32 + lane;
+}
+template <bool kVec, int kPerLane>
+__device__ __forceinline__ void load_row(const float *row, int E, int lane, float (&v)[kPerLane]) {
+#pragma unroll
+    for (int i = 0; i < kPerLane; i += kVec ? 4 : 1) {
+        const int e = expert_of<kVec>(i, lane);
+        if (kVec) {
+            const float4 f = e < E ? __ldg(reinterpret_cast<const float4 *>(row + e))
+                                   : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            v[i] = f.x, v[i + 1] = f.y, v[i + 2] = f.z, v[i + 3] = f.w;
+        } else {
+            v[i] = e < E ? row[e] : -INFINITY;
+        }
+    }
+}
+template <bool kVec, int kPerLane>
+__device__ __forceinline__ void load_row(const __nv_bfloat16 *row, int E, int lane, float (&v)[kPerLane]) {
+#pragma unroll
+    for (int i = 0; i < kPerLane; i += kVec ? 4 : 1) {
+        const int e = expert_of<kVec>(i, lane);
+        if (kVec) {
+            const uint2 f = e < E ? __ldg(reinterpret_cast<const uint2 *>(row + e)) : make_uint2(0xff80ff80u, 0xff80ff80u);
+            v[i] = __uint_as_float(f.x << 16), v[i + 1] = __uint_as_float(f.x & 0xffff0000u);
+            v[i + 2] = __uint_as_float(f.y << 16), v[i + 3] = __uint_as_float(f.y & 0xffff0000u);
+        } else {
+            v[i] = e < E ? to_float(row[e]) : -INFINITY;
+        }
+    }
+}
+template <bool kVec, int kPerLane>
+__device__ __forceinline__ void store_row(float *row, int E, int lane, const float (&v)[kPerLane]) {
+#pragma unroll
+    for (int i = 0; i < kPerLane; i += kVec ? 4 : 1) {
+        const int e = expert_of<kVec>(i, lane);
+        if (e >= E) continue;
+        if (kVec) *reinterpret_cast<float4 *>(row + e) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        else row[e] = v[i];
+    }
+}
+template <bool kVec, int kPerLane>
+__device__ __forceinline__ void store_row(__nv_bfloat16 *row, int E, int lane, const float (&v)[kPerLane]) {
+#pragma unroll
+    for (int i = 0; i < kPerLane; i += kVec ? 4 : 1) {
+        const int e = expert_of<kVec>(i, lane);
+        if (e >= E) continue;
+        if (kVec) {
+            __nv_bfloat162 b[2] = {__floats2bfloat162_rn(v[i], v[i + 1]), __floats2bfloat162_rn(v[i + 2], v[i + 3])};
+            *reinterpret_cast<uint2 *>(row + e) = *reinterpret_cast<const uint2 *>(b);
+        } else {
+            row[e] = __float2bfloat16_rn(v[i]);
+        }
+    }
+}
+
 // ------------------------------------------------------------------ forward, a warp per token
 
-template <typename L, int kPerLane>
-__global__ void __launch_bounds__(kWarpsPerCta * 32) gate_kernel(const GateArgs a) {
+// The largest of the lanes' values (none of them NaN).
+__device__ __forceinline__ float lanes_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Takes the lowest expert whose value is `top` out of group kG, the warp's number
+// `group`, and renews the group's maximum; returns the expert. The groups' code is
+// kept apart by the asm: merged, it would index the values in memory.
+template <bool kVec, int kGroup, int kG, int kHeld, int kGroups>
+__device__ __forceinline__ uint32_t take_out(float (&v)[kHeld], float (&group_top)[kGroups], uint32_t group, float top,
+                                             int lane) {
+    uint32_t win = 0;
+    if (group == kG) {
+        asm volatile("" ::"n"(kG));
+        uint32_t e = kFull;
+#pragma unroll
+        for (int i = kGroup - 1; i >= 0; --i)
+            if (v[kG * kGroup + i] == top) e = expert_of<kVec>(kG * kGroup + i, lane);
+        win = __reduce_min_sync(kFull, e);
+        float rest = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+            if (expert_of<kVec>(kG * kGroup + i, lane) == (int)win) v[kG * kGroup + i] = -INFINITY;
+            rest = fmaxf(rest, v[kG * kGroup + i]);
+        }
+        group_top[kG] = rest;
+    }
+    if constexpr (kG + 1 < kGroups) {
+        const uint32_t other = take_out<kVec, kGroup, kG + 1>(v, group_top, group, top, lane);
+        if (group != kG) win = other;
+    }
+    return win;
+}
+
+// A choice looks at the maxima of groups of eight values a lane, and only the
+// winner's group is gone through again (its number is made the same in every lane).
+// Five CTAs' registers to an SM: with what the compiler takes for 64 values a
+// lane it would be three, too few warps to cover the loads.
+template <typename L, int kPerLane, bool kVec>
+__global__ void __launch_bounds__(kWarpsPerCta * 32, kPerLane > 32 ? 5 : 8) gate_kernel(const GateArgs a) {
     WarpTrace wt(a.trace, MOE_TRACE_GATE);
     grid_dependency_wait();
+    clear_words(a);
+    constexpr int kGroup = 8, kGroups = kPerLane / kGroup;
     const int lane = threadIdx.x & 31;
     const int t = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
     if (t >= a.T) return;
     const L *row = static_cast<const L *>(a.logits) + (size_t)t * a.E;
     const bool is_sigmoid = (a.mode & 0xff) == MOE_GATE_SIGMOID;
 
-    // element i of lane: expert i * 32 + lane
-    uint32_t key[kPerLane];
+    float v[kPerLane], group_top[kGroups];   // -inf: never chosen
+    load_row<kVec>(row, a.E, lane, v);
     bool nan = false;
 #pragma unroll
-    for (int i = 0; i < kPerLane; ++i) {
-        const int e = i * 32 + lane;
-        const float v = e < a.E ? to_float(row[e]) : -INFINITY;
-        nan |= v != v;
-        key[i] = order_key(v);
+    for (int g = 0; g < kGroups; ++g) {
+        group_top[g] = -INFINITY;
+#pragma unroll
+        for (int i = g * kGroup; i < (g + 1) * kGroup; ++i) {
+            nan |= v[i] != v[i];
+            v[i] = fmaxf(v[i], -INFINITY);   // NaN becomes -inf
+            group_top[g] = fmaxf(group_top[g], v[i]);
+        }
     }
     if (nan) report(a.status, MOE_ERR_BAD_LOGIT);
 
@@ -141,45 +256,47 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) gate_kernel(const GateArgs 
     float m = 0.0f, z = 1.0f;
     const bool whole_row = !is_sigmoid && (!(a.mode & MOE_GATE_NORMALIZE) || a.bias != nullptr);
     if (whole_row) {
-        uint32_t top = 0;
+        m = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i) top = max(top, key[i]);
-        top = __reduce_max_sync(kFull, top);
-        m = top ? key_value(top) : 0.0f;
+        for (int g = 0; g < kGroups; ++g) m = fmaxf(m, group_top[g]);
+        m = lanes_max(m);
+        if (!(m > -INFINITY)) m = 0.0f;
         float s = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i)
-            if (key[i]) s += exp_below(key_value(key[i]), m);
+        for (int i = 0; i < kPerLane; ++i) s += exp_below(v[i], m);
         z = warp_sum(s);
     }
     if (a.bias != nullptr) {   // choose by score + bias; the logits are read again for the chosen
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i) {
-            if (key[i] == 0) continue;
-            const float l = key_value(key[i]);
-            const float s = is_sigmoid ? sigmoid(l).s : exp_below(l, m) / z;
-            key[i] = order_key(s + a.bias[i * 32 + lane]);
+        for (int g = 0; g < kGroups; ++g) {
+            group_top[g] = -INFINITY;
+#pragma unroll
+            for (int i = g * kGroup; i < (g + 1) * kGroup; ++i) {
+                if (v[i] > -INFINITY) {
+                    const float s = is_sigmoid ? sigmoid(v[i]).s : exp_below(v[i], m) / z;
+                    v[i] = fmaxf(s + a.bias[expert_of<kVec>(i, lane)], -INFINITY);
+                }
+                group_top[g] = fmaxf(group_top[g], v[i]);
+            }
         }
     }
 
     float mine = 0.0f;      // lane j: entry j's logit
     int mine_e = -1;        // ... and expert
     for (int j = 0; j < a.k; ++j) {
-        uint32_t best = 0;
-        int best_i = 0;
+        float best = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i)
-            if (key[i] > best) best = key[i], best_i = i;
-        const uint32_t top = __reduce_max_sync(kFull, best);
-        if (top == 0) break;
-        const int e = best_i * 32 + lane;
-        const int win = (int)__reduce_min_sync(kFull, best == top ? (uint32_t)e : kFull);
-        if (e == win) {
+        for (int g = 0; g < kGroups; ++g) best = fmaxf(best, group_top[g]);
+        const float top = lanes_max(best);
+        if (!(top > -INFINITY)) break;
+        // the lowest expert with that value is in the lowest group that has it
+        uint32_t group = kFull;
 #pragma unroll
-            for (int i = 0; i < kPerLane; ++i)
-                if (i == best_i) key[i] = 0;
-        }
-        if (lane == j) mine = a.bias == nullptr ? key_value(top) : to_float(row[win]), mine_e = win;
+        for (int g = kGroups - 1; g >= 0; --g)
+            if (group_top[g] == top) group = g;
+        group = __reduce_min_sync(kFull, group);
+        const uint32_t win = take_out<kVec, kGroup, 0>(v, group_top, group, top, lane);
+        if (lane == j) mine = a.bias == nullptr ? top : to_float(row[win]), mine_e = (int)win;
     }
     const float w = entry_weight(a.mode, mine, mine_e >= 0, m, z);
     if (lane < a.k) {
@@ -202,6 +319,7 @@ template <typename L>
 __global__ void __launch_bounds__(kWideThreads) gate_wide_kernel(const GateArgs a) {
     WarpTrace wt(a.trace, MOE_TRACE_GATE);
     grid_dependency_wait();
+    clear_words(a);
     extern __shared__ uint32_t keys[];
     __shared__ Top tops[kWideThreads / 32];
     __shared__ float sums[kWideThreads / 32];
@@ -277,8 +395,10 @@ __global__ void __launch_bounds__(kWideThreads) gate_wide_kernel(const GateArgs 
 
 // ------------------------------------------------------------------ backward, a warp per token
 
-template <typename L>
-__global__ void __launch_bounds__(kWarpsPerCta * 32) gate_backward_kernel(const GateBackArgs a) {
+// kPerLane: the row fits into the warp's registers (E <= 32 kPerLane) and is read
+// and written once; 0: longer rows, read again for each use.
+template <typename L, int kPerLane, bool kVec>
+__global__ void __launch_bounds__(kWarpsPerCta * 32, kPerLane > 32 ? 4 : 8) gate_backward_kernel(const GateBackArgs a) {
     WarpTrace wt(a.trace, MOE_TRACE_GATE_BACKWARD);
     grid_dependency_wait();
     const int lane = threadIdx.x & 31;
@@ -288,6 +408,11 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) gate_backward_kernel(const 
     L *out = static_cast<L *>(a.gl) + (size_t)t * a.E;
     const bool is_sigmoid = (a.mode & 0xff) == MOE_GATE_SIGMOID;
     const bool norm = (a.mode & MOE_GATE_NORMALIZE) != 0;
+    const bool dense = !is_sigmoid && !norm;
+
+    constexpr int kHeld = kPerLane > 0 ? kPerLane : 1;
+    float x[kHeld];
+    if (kPerLane > 0 && dense) load_row<kVec>(row, a.E, lane, x);
 
     // lane j: entry j
     int e = -1;
@@ -305,7 +430,6 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) gate_backward_kernel(const 
 
     // d: the entry's own part of its logit's gradient; every other logit gets -p * dot
     float d = 0.0f, dot = 0.0f, m = 0.0f, rz = 0.0f;
-    const bool dense = !is_sigmoid && !norm;
     if (norm) {
         const float q = normalised(l, on, is_sigmoid);
         d = q * (g - warp_sum(g * q));
@@ -315,12 +439,23 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) gate_backward_kernel(const 
         d = g * s.s * s.not_s;
     } else {
         m = -INFINITY;
-        for (int i = lane; i < a.E; i += 32) m = fmaxf(m, to_float(row[i]));   // fmaxf passes over NaN
-        m = warp_max(m);
         float z = 0.0f;
-        for (int i = lane; i < a.E; i += 32) {
-            const float v = to_float(row[i]);
-            if (v > -INFINITY) z += exp_below(v, m);
+        if (kPerLane > 0) {
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) m = fmaxf(m, x[i]);   // fmaxf passes over NaN
+            m = warp_max(m);
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+                x[i] = x[i] > -INFINITY ? exp_below(x[i], m) : 0.0f;
+                z += x[i];
+            }
+        } else {
+            for (int i = lane; i < a.E; i += 32) m = fmaxf(m, to_float(row[i]));
+            m = warp_max(m);
+            for (int i = lane; i < a.E; i += 32) {
+                const float v = to_float(row[i]);
+                if (v > -INFINITY) z += exp_below(v, m);
+            }
         }
         z = warp_sum(z);
         rz = z > 0.0f ? 1.0f / z : 0.0f;
@@ -329,13 +464,20 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) gate_backward_kernel(const 
         d = p * (g - dot);
     }
     if (!on) d = 0.0f;
-    for (int i = lane; i < a.E; i += 32) {
-        float v = 0.0f;
-        if (dense) {
-            const float x = to_float(row[i]);
-            if (x > -INFINITY) v = -exp_below(x, m) * rz * dot;
+    if (kPerLane > 0) {
+        const float c = -rz * dot;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) x[i] = dense ? x[i] * c : 0.0f;
+        store_row<kVec>(out, a.E, lane, x);
+    } else {
+        for (int i = lane; i < a.E; i += 32) {
+            float v = 0.0f;
+            if (dense) {
+                const float y = to_float(row[i]);
+                if (y > -INFINITY) v = -exp_below(y, m) * rz * dot;
+            }
+            store(out + i, v);
         }
-        store(out + i, v);
     }
     // an expert named by several entries gets the sum of their parts, in entry order
     const uint32_t same = __match_any_sync(kFull, e);
@@ -351,15 +493,48 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32) gate_backward_kernel(const 
     if (on && (same & ((1u << lane) - 1)) == 0) store(out + e, sum);
 }
 
+// Rows whose every fourth element is aligned for a load of four.
+template <typename L>
+bool rows_of_four(const void *p, int E) { return E % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (4 * sizeof(L)) == 0; }
+
+template <typename L, int kPerLane>
+cudaError_t launch_rows(const GateArgs &a, cudaStream_t s) {
+    const dim3 grid((a.T + kWarpsPerCta - 1) / kWarpsPerCta), block(kWarpsPerCta * 32);
+    const bool overlap = tuning().overlap != 0;
+    return rows_of_four<L>(a.logits, a.E) ? launch_kernel(gate_kernel<L, kPerLane, true>, grid, block, 0, s, overlap, a)
+                                          : launch_kernel(gate_kernel<L, kPerLane, false>, grid, block, 0, s, overlap, a);
+}
+
 template <typename L>
 int launch_gate_typed(const GateArgs &a, cudaStream_t s) {
-    const bool overlap = tuning().overlap != 0;
-    const dim3 grid((a.T + kWarpsPerCta - 1) / kWarpsPerCta), block(kWarpsPerCta * 32);
     cudaError_t e;
-    if (a.E <= 256) e = launch_kernel(gate_kernel<L, 8>, grid, block, 0, s, overlap, a);
-    else if (a.E <= 1024) e = launch_kernel(gate_kernel<L, 32>, grid, block, 0, s, overlap, a);
-    else if (a.E <= 32 * kMaxPerLane) e = launch_kernel(gate_kernel<L, kMaxPerLane>, grid, block, 0, s, overlap, a);
-    else e = launch_kernel(gate_wide_kernel<L>, dim3(a.T), dim3(kWideThreads), a.E * sizeof(uint32_t), s, overlap, a);
+    if (a.E <= 256) e = launch_rows<L, 8>(a, s);
+    else if (a.E <= 1024) e = launch_rows<L, 32>(a, s);
+    else if (a.E <= 32 * kMaxPerLane) e = launch_rows<L, kMaxPerLane>(a, s);
+    else
+        e = launch_kernel(gate_wide_kernel<L>, dim3(a.T), dim3(kWideThreads), a.E * sizeof(uint32_t), s,
+                          tuning().overlap != 0, a);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+template <typename L, int kPerLane>
+cudaError_t launch_back_rows(const GateBackArgs &a, cudaStream_t s) {
+    const dim3 grid((a.T + kWarpsPerCta - 1) / kWarpsPerCta), block(kWarpsPerCta * 32);
+    const bool overlap = tuning().overlap != 0;
+    return rows_of_four<L>(a.logits, a.E) && rows_of_four<L>(a.gl, a.E)
+               ? launch_kernel(gate_backward_kernel<L, kPerLane, true>, grid, block, 0, s, overlap, a)
+               : launch_kernel(gate_backward_kernel<L, kPerLane, false>, grid, block, 0, s, overlap, a);
+}
+
+template <typename L>
+int launch_back_typed(const GateBackArgs &a, cudaStream_t s) {
+    cudaError_t e;
+    if (a.E <= 256) e = launch_back_rows<L, 8>(a, s);
+    else if (a.E <= 1024) e = launch_back_rows<L, 32>(a, s);
+    else if (a.E <= 32 * kMaxPerLane) e = launch_back_rows<L, kMaxPerLane>(a, s);
+    else
+        e = launch_kernel(gate_backward_kernel<L, 0, false>, dim3((a.T + kWarpsPerCta - 1) / kWarpsPerCta),
+                          dim3(kWarpsPerCta * 32), 0, s, tuning().overlap != 0, a);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -368,7 +543,7 @@ int launch_gate_typed(const GateArgs &a, cudaStream_t s) {
 int launch_gate(const GateLaunch &L) {
     if (L.num_tokens == 0) return MOE_OK;
     const GateArgs a{L.logits, L.bias, L.num_tokens, L.num_topk, L.num_experts, L.mode, L.scale,
-                     L.topk_idx, L.topk_weights, L.status, trace_args()};
+                     L.topk_idx, L.topk_weights, L.status, L.clear, L.num_clear, trace_args()};
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
     return L.logits_type == MOE_LOGITS_BF16 ? launch_gate_typed<__nv_bfloat16>(a, s) : launch_gate_typed<float>(a, s);
 }
@@ -378,12 +553,7 @@ int launch_gate_backward(const GateBackwardLaunch &L) {
     const GateBackArgs a{L.logits, L.topk_idx, L.grad_weights, L.num_tokens, L.num_topk, L.num_experts, L.mode,
                          L.scale, L.grad_logits, L.status, trace_args()};
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
-    const dim3 grid((a.T + kWarpsPerCta - 1) / kWarpsPerCta), block(kWarpsPerCta * 32);
-    const bool overlap = tuning().overlap != 0;
-    const cudaError_t e = L.logits_type == MOE_LOGITS_BF16
-                              ? launch_kernel(gate_backward_kernel<__nv_bfloat16>, grid, block, 0, s, overlap, a)
-                              : launch_kernel(gate_backward_kernel<float>, grid, block, 0, s, overlap, a);
-    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return L.logits_type == MOE_LOGITS_BF16 ? launch_back_typed<__nv_bfloat16>(a, s) : launch_back_typed<float>(a, s);
 }
 
 }  // namespace moe

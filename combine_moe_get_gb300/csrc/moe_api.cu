@@ -631,9 +631,10 @@ MOE_API int moe_layer(const void *x, int num_tokens, int hidden, const void *log
     rc = experts_prepare(x, num_tokens, hidden, topk_idx, topk_weights, num_topk, num_experts, w13, w13_scales, w2,
                          w2_scales, intermediate, weight_type, out, workspace, workspace_bytes, status, stream, L);
     if (rc != MOE_OK) return rc;
+    const moe::ExpertsWords w = moe::experts_words(L);
     rc = moe::launch_gate(moe::GateLaunch{logits, logits_type, bias, num_tokens, num_topk, num_experts, mode, scale,
-                                          topk_idx, topk_weights, status, stream});
-    return rc != MOE_OK ? rc : moe::launch_experts(L);
+                                          topk_idx, topk_weights, status, stream, w.words, w.n});
+    return rc != MOE_OK ? rc : moe::launch_experts(L, w.words != nullptr);
 }
 
 static bool adapter_shape_ok(int T, int K, int N, int L, int r) {

@@ -281,6 +281,9 @@ struct GateLaunch {
     float *topk_weights;
     int32_t *status;
     void *stream;
+    // optional: words that the launch zeroes for the next one
+    uint32_t *clear = nullptr;
+    int num_clear = 0;
 };
 
 int launch_gate(const GateLaunch &L);
@@ -318,7 +321,14 @@ struct ExpertsLaunch {
 };
 
 size_t experts_workspace_bytes(int T, int H, int I, int k, int E);
-int launch_experts(const ExpertsLaunch &L);
+// Counters of the workspace that launch_experts wants zero and clears with a
+// kernel of its own unless it is told that they are; none for larger batches.
+struct ExpertsWords {
+    uint32_t *words;
+    int n;
+};
+ExpertsWords experts_words(const ExpertsLaunch &L);
+int launch_experts(const ExpertsLaunch &L, bool words_are_zero = false);
 
 struct AdapterLaunch {
     const void *x;

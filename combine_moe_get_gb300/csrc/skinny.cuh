@@ -77,6 +77,7 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 struct Line {
     int64_t tiles, units, per;
     int kbs, span;
+    Line() = default;
     __device__ Line(int64_t n, int k_blocks, int ctas, int slack) : tiles(n), kbs(k_blocks), span(k_blocks) {
         const int least = min(kbs, kMinBlocks);
         if (tiles > 0 && 2 * tiles <= ctas) {
@@ -127,14 +128,13 @@ struct Shape {
     int cols;      // columns a tile may have: a multiple of 16, at most 128 (E4M3: 64)
     int a_stages, b_stages;
     __host__ __device__ static constexpr int b_bytes(int cols, bool e4m3) { return cols * (e4m3 ? 256 : 128); }
-    static Shape of(int cols, bool e4m3) {
-        const int b = b_bytes(cols, e4m3), a_stages = 3 * b <= kSmemBudget - 6 * 2 * kHalf ? 6 : 5;
-        const int b_stages = (kSmemBudget - a_stages * 2 * kHalf) / b;
+    static Shape of(int cols, bool e4m3, int budget = kSmemBudget) {
+        const int b = b_bytes(cols, e4m3), a_stages = 3 * b <= budget - 6 * 2 * kHalf ? 6 : 5;
+        const int b_stages = (budget - a_stages * 2 * kHalf) / b;
         return Shape{cols, a_stages, b_stages < kMaxStages ? b_stages : kMaxStages};
     }
-    size_t smem(bool e4m3) const {
-        return 1024 + (size_t)a_stages * 2 * kHalf + (size_t)b_stages * b_bytes(cols, e4m3);
-    }
+    __host__ __device__ int ring_bytes(bool e4m3) const { return a_stages * 2 * kHalf + b_stages * b_bytes(cols, e4m3); }
+    size_t smem(bool e4m3) const { return 1024 + (size_t)ring_bytes(e4m3); }
     __device__ uint32_t a_at(int slot) const { return slot * 2 * kHalf; }
     __device__ uint32_t b_at(int slot, bool e4m3) const { return a_stages * 2 * kHalf + slot * b_bytes(cols, e4m3); }
     int tmem_cols(bool e4m3) const {
@@ -617,7 +617,8 @@ constexpr int threads_of() {
 }
 
 // Barriers and tensor memory, then `roles(problem, ring, tensor memory, ok)` on
-// every thread; `problem()` makes the problem after the set-up.
+// every thread; `problem(ring)` makes the
+// problem after the set-up, when the ring is still unused.
 template <bool kE4m3, class P, class Make, class Roles>
 __device__ void with_set_up(Make problem, Control &c, const uint32_t tmem_cols, Roles roles) {
     extern __shared__ char smem_raw[];
@@ -644,7 +645,7 @@ __device__ void with_set_up(Make problem, Control &c, const uint32_t tmem_cols, 
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = c.tmem;
-    const P p = problem();
+    const P p = problem(ring);
     bool ok = true;
     roles(p, ring, tmem, warp, ok);
     if (!ok) report(p.status, MOE_ERR_TIMEOUT);
@@ -756,6 +757,82 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Index
         const int e = set_of(a.idx[i]);
         if (e >= 0) a.order[atomicAdd(&start[e], 1)] = i;
     }
+}
+
+// The same for few entries, by every CTA for itself in its shared memory: no
+// launch before, and no chain of loads from its results. CTAs have to agree, so an
+// entry's place is fixed: by set, then in the order of the entries. A thread has
+// a set and looks through all entries for its own, 32 to a word of a mask. (By
+// counters in shared memory this took 2.8 us, by matching a warp's entries 4, and
+// the plan kernel with its launch takes 5.)
+constexpr int kLocalEntries = 256, kLocalSets = 512;
+struct LocalPlan {
+    uint32_t groups[kLocalEntries];    // set | first sorted entry << 13 | (entries - 1) << 21
+    uint16_t order[kLocalEntries];
+    uint16_t set_of[kLocalEntries];    // 0xffff: none
+    uint32_t totals[kLocalSets / 32];  // entries | groups << 16 of 32 sets
+    int num_groups;
+};
+
+// All threads of the CTA, at least kLocalSets.
+template <typename Index>
+__device__ void local_plan(LocalPlan &plan, const Index *idx, int n, int sets, int cols, int bad, int32_t *status) {
+    const int set = threadIdx.x, lane = threadIdx.x & 31;
+    if (set < kLocalEntries) {
+        const Index e = set < n ? idx[set] : (Index)-1;
+        const bool named = e >= 0 && e < sets;
+        if (!named && e != -1 && blockIdx.x == 0) report(status, bad);
+        plan.set_of[set] = named ? (uint16_t)e : (uint16_t)0xffff;
+    }
+    __syncthreads();
+    uint32_t mine[kLocalEntries / 32] = {};
+    uint32_t count = 0, before = 0;   // entries | groups << 16
+    if (set < kLocalSets) {
+        if (set < sets)
+#pragma unroll
+            for (int w = 0; w < kLocalEntries / 32; ++w) {
+                if (w * 32 >= n) break;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(&plan.set_of[w * 32 + q * 8]);
+                    const uint32_t two[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        if ((two[h] & 0xffff) == (uint32_t)set) mine[w] |= 1u << (q * 8 + 2 * h);
+                        if (two[h] >> 16 == (uint32_t)set) mine[w] |= 2u << (q * 8 + 2 * h);
+                    }
+                }
+                count += __popc(mine[w]);
+            }
+        count |= (count + cols - 1) / cols << 16;
+        before = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t v = __shfl_up_sync(0xffffffffu, before, o);
+            if (lane >= o) before += v;
+        }
+        if (lane == 31) plan.totals[set / 32] = before;
+        before -= count;
+    }
+    __syncthreads();
+    if (set < sets) {
+        for (int w = 0; w < set / 32; ++w) before += plan.totals[w];
+        int at = before & 0xffff, g = before >> 16;
+        const int entries = count & 0xffff;
+        for (int b = 0; b < entries; b += cols, ++g)
+            plan.groups[g] = (uint32_t)set | (uint32_t)(at + b) << 13 | (uint32_t)(min(cols, entries - b) - 1) << 21;
+#pragma unroll
+        for (int w = 0; w < kLocalEntries / 32; ++w)
+            for (uint32_t m = mine[w]; m != 0; m &= m - 1) plan.order[at++] = (uint16_t)(w * 32 + __ffs(m) - 1);
+        if (set == sets - 1) plan.num_groups = g;
+    }
+    __syncthreads();
+}
+
+// Zeroes the counters where no plan kernel does.
+static __global__ void __launch_bounds__(1024) clear_kernel(uint32_t *words, int n) {
+    grid_dependency_wait();
+    for (int i = threadIdx.x; i < n; i += 1024) words[i] = 0;
 }
 
 template <typename Index>
