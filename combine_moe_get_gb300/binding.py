@@ -469,9 +469,12 @@ MOE_GATE_NORMALIZE = 0x100
 
 
 def _logits_type(logits: torch.Tensor) -> int:
-    if logits.dtype not in (torch.float32, torch.bfloat16):
+    dtype = logits.dtype
+    if dtype == torch.float32:
+        return MOE_LOGITS_F32
+    if dtype != torch.bfloat16:
         raise ValueError("the router's logits are float32 or bfloat16")
-    return MOE_LOGITS_BF16 if logits.dtype == torch.bfloat16 else MOE_LOGITS_F32
+    return MOE_LOGITS_BF16
 
 
 _SCORES = {"softmax": MOE_GATE_SOFTMAX, "sigmoid": MOE_GATE_SIGMOID}
@@ -483,8 +486,8 @@ def _gate_mode(score: str, normalize: bool) -> int:
     return _SCORES[score] | (MOE_GATE_NORMALIZE if normalize else 0)
 
 
-def _typed(t: Optional[torch.Tensor], dtype: torch.dtype, shape: tuple, name: str):
-    if t is not None and (t.dtype != dtype or t.shape != shape):
+def _typed(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str) -> torch.Tensor:
+    if t.dtype != dtype or t.shape != shape:
         raise ValueError(f"{name} is {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
     return t
 
@@ -503,7 +506,8 @@ def moe_topk_gate(logits: torch.Tensor, num_topk: int, *, bias: Optional[torch.T
                 _typed(topk_idx, torch.int64, (T, num_topk), "topk_idx"))
     topk_weights = (torch.empty(T, num_topk, dtype=torch.float32, device=dev) if topk_weights is None else
                     _typed(topk_weights, torch.float32, (T, num_topk), "topk_weights"))
-    _typed(bias, torch.float32, (E,), "bias")
+    if bias is not None:
+        _typed(bias, torch.float32, (E,), "bias")
     status = new_status(dev) if status is None else status
     code = LIB.moe_topk_gate(_ptr(logits), _logits_type(logits), _ptr(bias), T, num_topk, E,
                              _gate_mode(score, normalize), float(scale), _ptr(topk_idx), _ptr(topk_weights),
@@ -541,21 +545,22 @@ def moe_experts_workspace_size(num_tokens: int, hidden: int, intermediate: int, 
 
 
 def _expert_weights(x, w13, w2, w13_scales, w2_scales):
-    """(H, I, E, weight type) of one layer's experts, after checking types and shapes."""
+    """(T, H, I, E, weight type) of one layer's experts, after checking types and shapes."""
     T, H = x.shape
-    E, I = w2.shape[0], w2.shape[2]
+    E, _, I = w2.shape
     e4m3 = w13.dtype == torch.uint8
     dtype = torch.uint8 if e4m3 else torch.bfloat16
     _typed(x, torch.bfloat16, (T, H), "x")
     _typed(w13, dtype, (E, 2 * I, H), "w13")
     _typed(w2, dtype, (E, H, I), "w2")
-    if e4m3 and (w13_scales is None or w2_scales is None):
-        raise ValueError("E4M3 weights need w13_scales and w2_scales")
-    if not e4m3 and (w13_scales is not None or w2_scales is not None):
+    if e4m3:
+        if w13_scales is None or w2_scales is None:
+            raise ValueError("E4M3 weights need w13_scales and w2_scales")
+        _typed(w13_scales, torch.float32, (E, 2 * I, H // 128), "w13_scales")
+        _typed(w2_scales, torch.float32, (E, H, I // 128), "w2_scales")
+    elif w13_scales is not None or w2_scales is not None:
         raise ValueError("bf16 weights take no scales")
-    _typed(w13_scales, torch.float32, (E, 2 * I, H // 128), "w13_scales")
-    _typed(w2_scales, torch.float32, (E, H, I // 128), "w2_scales")
-    return H, I, E, MOE_WEIGHTS_E4M3 if e4m3 else MOE_WEIGHTS_BF16
+    return T, H, I, E, MOE_WEIGHTS_E4M3 if e4m3 else MOE_WEIGHTS_BF16
 
 
 def moe_experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor, w13: torch.Tensor,
@@ -566,9 +571,9 @@ def moe_experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Ten
     """out[t] = sum_j topk_weights[t, j] * w2[e] (silu(gate) * up), [gate; up] = w13[e] x[t] and
     e = topk_idx[t, j], for a few tokens (T <= 1024). Weights are bf16, or E4M3
     codes (uint8) with a scale per row and 128 columns."""
-    H, I, E, wtype = _expert_weights(x, w13, w2, w13_scales, w2_scales)
-    T, k = topk_idx.shape
-    _typed(topk_idx, torch.int64, (x.shape[0], k), "topk_idx")
+    T, H, I, E, wtype = _expert_weights(x, w13, w2, w13_scales, w2_scales)
+    k = topk_idx.shape[1]
+    _typed(topk_idx, torch.int64, (T, k), "topk_idx")
     _typed(topk_weights, torch.float32, (T, k), "topk_weights")
     out = torch.empty_like(x) if out is None else _typed(out, torch.bfloat16, (T, H), "out")
     if workspace is None:
@@ -576,7 +581,7 @@ def moe_experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Ten
     status = new_status(x.device) if status is None else status
     code = LIB.moe_experts(_ptr(x), T, H, _ptr(topk_idx), _ptr(topk_weights), k, E, _ptr(w13), _ptr(w13_scales),
                            _ptr(w2), _ptr(w2_scales), I, wtype, _ptr(out), _ptr(workspace),
-                           workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+                           workspace.nbytes, _ptr(status), _stream(stream))
     _check(code, "moe_experts")
     return out
 
@@ -590,10 +595,11 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, num_topk: int, w13: torch.T
               stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """moe_topk_gate of ``logits`` [T, E] and moe_experts of the choice in one
     call. Returns (out, topk_idx, topk_weights)."""
-    H, I, E, wtype = _expert_weights(x, w13, w2, w13_scales, w2_scales)
-    T, dev = x.shape[0], x.device
+    T, H, I, E, wtype = _expert_weights(x, w13, w2, w13_scales, w2_scales)
+    dev = x.device
     _typed(logits, logits.dtype, (T, E), "logits")
-    _typed(bias, torch.float32, (E,), "bias")
+    if bias is not None:
+        _typed(bias, torch.float32, (E,), "bias")
     out = torch.empty_like(x) if out is None else _typed(out, torch.bfloat16, (T, H), "out")
     topk_idx = (torch.empty(T, num_topk, dtype=torch.int64, device=dev) if topk_idx is None else
                 _typed(topk_idx, torch.int64, (T, num_topk), "topk_idx"))
@@ -606,7 +612,7 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, num_topk: int, w13: torch.T
     code = LIB.moe_layer(_ptr(x), T, H, _ptr(logits), _logits_type(logits), _ptr(bias), num_topk, E,
                          _gate_mode(score, normalize), float(scale), _ptr(topk_idx), _ptr(topk_weights), _ptr(w13),
                          _ptr(w13_scales), _ptr(w2), _ptr(w2_scales), I, wtype, _ptr(out), _ptr(workspace),
-                         workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream))
+                         workspace.nbytes, _ptr(status), _stream(stream))
     _check(code, "moe_layer")
     return out, topk_idx, topk_weights
 
@@ -639,7 +645,6 @@ def moe_adapter_linear(x: torch.Tensor, w: torch.Tensor, adapter_idx: torch.Tens
                                 device=x.device)
     status = new_status(x.device) if status is None else status
     code = LIB.moe_adapter_linear(_ptr(x), T, K, _ptr(w), N, _ptr(adapter_idx), _ptr(a), _ptr(b), _ptr(scales), L, r,
-                                  _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                  _ptr(status), _stream(stream))
+                                  _ptr(out), _ptr(workspace), workspace.nbytes, _ptr(status), _stream(stream))
     _check(code, "moe_adapter_linear")
     return out

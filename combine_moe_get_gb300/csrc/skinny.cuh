@@ -21,12 +21,14 @@
 //   E4M3 weights: 8 more warps turn each block's codes into bf16 (exact) in
 //     tensor memory, from where the products take A; a block of 128 along K has
 //     its own fp32 scale per weight row, so the readers scale each block's sums
-//     and add them in registers (n <= 64). Blocks are double-buffered on both
-//     sides of the products. (Readers that did the conversions themselves, 8 or 16
+//     and add them in registers (n <= 64). Blocks are buffered on both sides of
+//     the products. (Readers that did the conversions themselves, 8 or 16
 //     of them, took 1.6 times the time that a block's bytes take.)
 //
 // The problem P gives the segments, the loads of B and what becomes of the sums.
 #pragma once
+
+#include <algorithm>
 
 #include "umma.cuh"
 
@@ -115,8 +117,8 @@ struct Line {
 struct Control {
     uint64_t full_a[kMaxStages], empty_a[kMaxStages], full_b[kMaxStages], empty_b[kMaxStages];
     uint64_t sums_full[2], sums_empty[2];
-    uint64_t a_ready[2];     // E4M3: converted block in tensor memory
-    uint64_t a_free[2];      // ... and used up
+    uint64_t a_ready[3];     // E4M3: converted block in tensor memory
+    uint64_t a_free[3];      // ... and used up
     uint64_t last;
     uint32_t tmem;
 };
@@ -314,25 +316,30 @@ __device__ bool multiply(const P &p, Control &c, uint32_t ring_base, const Shape
     return ok;
 }
 
-constexpr int kTmemCodes = 256;   // E4M3: first tensor-memory column of the converted blocks
+// E4M3: blocks that tensor memory holds converted, 128 columns each, behind the
+// sums' 4 `cols`. Three where they fit: with two, a block's conversion had to wait
+// for the products of the one before last.
+constexpr int code_buffers(int most_cols) { return most_cols <= 32 ? 3 : 2; }
+constexpr int first_code_column(int most_cols) { return 512 - 128 * code_buffers(most_cols); }
 
 // Products of converted E4M3 blocks. Each block's sums start from zero.
 template <class P>
 __device__ bool multiply_e4m3(const P &p, Control &c, uint32_t ring_base, const Shape sh, uint32_t tmem) {
     const bool mine = elect_one();
-    Ring r(sh.b_stages);
+    constexpr int kCols = 8 * P::kSteps;
+    Ring r(sh.b_stages), codes(code_buffers(kCols));
     uint32_t seq = 0;
     const uint32_t half_b = uniform(sh.cols * 128 >> 4), half_d = uniform(sh.cols);
     const bool ok = p.segments([&](const Segment &s) {
         const uint32_t desc = uniform(product_desc(s.n16()));
-        for (int kb = s.kb0; kb < s.kb1; ++kb, r.next(), ++seq) {
+        for (int kb = s.kb0; kb < s.kb1; ++kb, r.next(), codes.next(), ++seq) {
             const uint32_t buf = seq & 1;
-            if (!warp_wait(&c.full_b[r.slot], r.round) || !warp_wait(&c.a_ready[buf], seq >> 1 & 1) ||
+            if (!warp_wait(&c.full_b[r.slot], r.round) || !warp_wait(&c.a_ready[codes.slot], codes.round) ||
                 !warp_wait(&c.sums_empty[buf], (seq >> 1 & 1) ^ 1))
                 return false;
             tc_fence_after();
             const uint32_t b = uniform(operand_low(ring_base + sh.b_at(r.slot, true)));
-            const uint32_t a = uniform(tmem + kTmemCodes + buf * 128), d = uniform(tmem + buf * 2 * sh.cols);
+            const uint32_t a = uniform(tmem + first_code_column(kCols) + codes.slot * 128), d = uniform(tmem + buf * 2 * sh.cols);
             if (mine) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -340,7 +347,7 @@ __device__ bool multiply_e4m3(const P &p, Control &c, uint32_t ring_base, const 
                     for (int k = 0; k < 8; ++k)
                         mma_ts(d + h * half_d, a + h * 64 + k * 8, b + (k >> 2) * half_b + 2 * (k & 3), desc, k > 0);
                 mma_commit(&c.empty_b[r.slot]);
-                mma_commit(&c.a_free[buf]);
+                mma_commit(&c.a_free[codes.slot]);
                 mma_commit(&c.sums_full[buf]);
             }
             __syncwarp();
@@ -518,21 +525,20 @@ __device__ bool read_sums(const P &p, Control &c, const Shape sh, uint32_t tmem)
 // one row (lane of tensor memory) of one half.
 template <class P>
 __device__ bool convert(const P &p, Control &c, const char *ring, const Shape sh, uint32_t tmem) {
+    constexpr int kCols = 8 * P::kSteps;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 - kFirstReader / 32;
     const int row = (warp & 3) * 32 + lane, half = warp / 4;
-    const uint32_t dst0 = tmem + ((uint32_t)(row & ~31) << 16) + kTmemCodes + half * 64;
-    Ring r(sh.a_stages);
-    uint32_t seq = 0;
+    const uint32_t dst0 = tmem + ((uint32_t)(row & ~31) << 16) + first_code_column(kCols) + half * 64;
+    Ring r(sh.a_stages), out(code_buffers(kCols));
     return p.segments([&](const Segment &s) {
-        for (int kb = s.kb0; kb < s.kb1; ++kb, r.next(), ++seq) {
-            const uint32_t buf = seq & 1;
+        for (int kb = s.kb0; kb < s.kb1; ++kb, r.next(), out.next()) {
             if (!warp_wait(&c.full_a[r.slot], r.round)) return false;
             // 16-byte pieces of a 128-byte row, swizzled by the row
             const char *codes = ring + sh.a_at(r.slot) + half * kHalf + row * 128;
             uint4 w[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) w[q] = *reinterpret_cast<const uint4 *>(codes + ((q ^ (row & 7)) << 4));
-            if (!warp_wait(&c.a_free[buf], (seq >> 1 & 1) ^ 1)) return false;
+            if (!warp_wait(&c.a_free[out.slot], out.round ^ 1)) return false;
             tc_fence_after();
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
@@ -541,7 +547,7 @@ __device__ bool convert(const P &p, Control &c, const char *ring, const Shape sh
                 b[2] = codes_to_bf16(w[q].y), b[3] = codes_to_bf16(w[q].y >> 16);
                 b[4] = codes_to_bf16(w[q].z), b[5] = codes_to_bf16(w[q].z >> 16);
                 b[6] = codes_to_bf16(w[q].w), b[7] = codes_to_bf16(w[q].w >> 16);
-                tmem_store8(dst0 + buf * 128 + q * 8, b);
+                tmem_store8(dst0 + out.slot * 128 + q * 8, b);
                 if (q == 3) {   // the codes are in registers by now
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&c.empty_a[r.slot]);
@@ -550,7 +556,7 @@ __device__ bool convert(const P &p, Control &c, const char *ring, const Shape sh
             tmem_store_wait();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&c.a_ready[buf]);
+            if (lane == 0) mbar_arrive(&c.a_ready[out.slot]);
         }
         return true;
     });
@@ -634,6 +640,8 @@ __device__ void with_set_up(Make problem, Control &c, const uint32_t tmem_cols, 
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c.sums_full[i], 1);
             mbar_init(&c.sums_empty[i], P::kReaders / 32);
+        }
+        for (int i = 0; i < 3; ++i) {
             mbar_init(&c.a_ready[i], kConverters / 32);
             mbar_init(&c.a_free[i], 1);
         }
@@ -717,45 +725,67 @@ struct PlanArgs {
 
 constexpr int kPlanThreads = 1024;
 
-// The order of a set's entries is the arrival order of the counters: it says
-// only which column of a product an entry takes, and columns do not depend on
-// one another.
+// Warps that sort, each a stretch of the entries with counters of its own, and
+// the shared memory that they take.
+inline int plan_warps(int sets) { return std::max(1, std::min(kPlanThreads / 32, (160 << 10) / (4 * sets))); }
+inline size_t plan_smem(int sets) { return ((size_t)plan_warps(sets) + 2) * (sets + 1) * 4; }
+
+// Sets in order, entries of a set in their own order: where entries change
+// places between groups, their sums are cut elsewhere and may round otherwise, so
+// the same choice has to give the same groups.
 template <typename Index>
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Index> a) {
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Index> a, const int warps) {
     WarpTrace wt(a.trace, MOE_TRACE_PLAN);
     grid_dependency_wait();
     grid_launch_dependents();   // the next kernel's set-up
-    extern __shared__ int32_t plan_smem[];
+    extern __shared__ int32_t plan_memory[];
     const int sets = a.sets + (a.rest ? 1 : 0);
-    int32_t *start = plan_smem, *first_group = plan_smem + sets + 1;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    int32_t *start = plan_memory, *first_group = start + sets + 1;
+    int32_t *counts = first_group + sets + 1, *mine = counts + (size_t)warp * sets;   // [warps][sets]
     auto set_of = [&](Index e) { return e >= 0 && e < a.sets ? (int)e : a.rest ? a.sets : -1; };
-    for (int i = threadIdx.x; i <= sets; i += kPlanThreads) start[i] = 0;
+    for (int i = threadIdx.x; i < warps * sets; i += kPlanThreads) counts[i] = 0;
     for (int i = threadIdx.x; i < a.num_words; i += kPlanThreads) a.words[i] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
+    const int per = ((a.n + warps - 1) / warps + 31) / 32 * 32;   // entries of a warp
+    const int64_t first = (int64_t)warp * per;
+    const int begin = warp < warps && first < a.n ? (int)first : a.n, end = min(a.n, begin + per);
+    for (int i = begin + lane; i < end; i += 32) {
         const Index e = a.idx[i];
         if (e < -1 || e >= a.sets) report(a.status, a.bad);
-        if (set_of(e) >= 0) atomicAdd(&start[set_of(e)], 1);
+        if (set_of(e) >= 0) atomicAdd(&mine[set_of(e)], 1);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < sets; e += kPlanThreads) first_group[e] = (start[e] + a.cols - 1) / a.cols;
+    for (int e = threadIdx.x; e < sets; e += kPlanThreads) {   // each warp's first place in a set
+        int total = 0;
+        for (int w = 0; w < warps; ++w) {
+            const int c = counts[(size_t)w * sets + e];
+            counts[(size_t)w * sets + e] = total;
+            total += c;
+        }
+        start[e] = total;
+        first_group[e] = (total + a.cols - 1) / a.cols;
+    }
     __syncthreads();
-    if (threadIdx.x < 32) warp_exclusive_scan(start, sets, threadIdx.x);
-    else if (threadIdx.x < 64) warp_exclusive_scan(first_group, sets, threadIdx.x - 32);
+    if (warp == 0) warp_exclusive_scan(start, sets, lane);
+    else if (warp == 1) warp_exclusive_scan(first_group, sets, lane);
     __syncthreads();
     for (int e = threadIdx.x; e < sets; e += kPlanThreads) {
-        const int end = start[e + 1];
-        for (int g = first_group[e], b = start[e]; b < end; ++g, b += a.cols)
-            a.groups[g] = make_int4(e, b, min(a.cols, end - b), 0);
+        const int last = start[e + 1];
+        for (int g = first_group[e], b = start[e]; b < last; ++g, b += a.cols)
+            a.groups[g] = make_int4(e, b, min(a.cols, last - b), 0);
     }
     if (threadIdx.x == 0) {
         a.words[kGroupsWord] = first_group[sets];
         a.words[kNamedWord] = first_group[a.sets];
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < a.n; i += kPlanThreads) {
-        const int e = set_of(a.idx[i]);
-        if (e >= 0) a.order[atomicAdd(&start[e], 1)] = i;
+    for (int i0 = begin; i0 < end; i0 += 32) {
+        const int i = i0 + lane, e = i < end ? set_of(a.idx[i]) : -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, e);
+        if (e >= 0) a.order[start[e] + mine[e] + __popc(same & ((1u << lane) - 1))] = i;
+        __syncwarp();
+        if (e >= 0 && same >> lane == 1) mine[e] += __popc(same);   // the last of them
+        __syncwarp();
     }
 }
 
@@ -837,11 +867,12 @@ static __global__ void __launch_bounds__(1024) clear_kernel(uint32_t *words, int
 
 template <typename Index>
 int launch_plan(const PlanArgs<Index> &a, cudaStream_t s) {
-    const size_t smem = (size_t)2 * (a.sets + 2) * 4;
+    const int sets = a.sets + (a.rest ? 1 : 0);
+    const size_t smem = plan_smem(sets);
     const int rc = ensure_dynamic_smem((const void *)plan_kernel<Index>, smem);
     if (rc != MOE_OK) return rc;
-    return launch_kernel(plan_kernel<Index>, dim3(1), dim3(kPlanThreads), smem, s, tuning().overlap != 0, a) ==
-                   cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return launch_kernel(plan_kernel<Index>, dim3(1), dim3(kPlanThreads), smem, s, tuning().overlap != 0, a,
+                         plan_warps(sets)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 // One CTA per SM, all of them resident at once (they wait for one another).

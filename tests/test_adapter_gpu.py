@@ -146,3 +146,10 @@ def test_adapter_empty_batch(moe):
     p = Problem(4, 64, 64, 2, 8)
     p.x, p.idx = p.x[:0], p.idx[:0]
     assert p.call(moe).shape == (0, 64)
+
+
+def test_adapter_gives_the_same_bits_every_time(moe):
+    p = Problem(1500, 512, 384, 6, 64, seed=3)
+    first = p.call(moe)
+    for _ in range(5):
+        assert torch.equal(p.call(moe), first)

@@ -218,3 +218,12 @@ def test_experts_run_on_dispatched_rows(moe):
     # the two ranks' partial rows are rounded to bf16 once more before they are added
     parts_abs = moe.moe_combine(parts.abs(), lay.token_dst_row).double()
     assert bool(((got - ref).abs() <= tol + 2 * U * parts_abs).all())
+
+
+@pytest.mark.parametrize("T,E,k", [(300, 3, 2), (700, 40, 3), (1024, 1, 1)])
+def test_experts_give_the_same_bits_every_time(moe, T, E, k):
+    """Groups of many entries, whose sums several CTAs share."""
+    p = Problem(T, 512, 384, E, k, seed=T)
+    first = p.call(moe)
+    for _ in range(5):
+        assert torch.equal(p.call(moe), first)
