@@ -119,8 +119,14 @@ __global__ void __launch_bounds__(256) adapter_sort_kernel(const SortArgs s) {
     grid_launch_dependents();
     const uint4 *from = s.x + (size_t)s.order[blockIdx.x] * s.pieces;
     uint4 *to = s.sorted + (size_t)blockIdx.x * s.pieces;
+#pragma unroll 4
     for (int i = threadIdx.x; i < s.pieces; i += 256) to[i] = __ldg(from + i);
 }
+
+// Whole tiles up to this share of equal stretches: a shared tile of 128 columns is
+// 128 KB of partial sums from each CTA (4096 rows, 16 adapters: 243 us with equal
+// stretches).
+constexpr int kSlackGrouped = 130;
 
 struct GroupedAdapter : AdapterBase {
     static constexpr bool kAdders = true;
@@ -142,10 +148,10 @@ struct GroupedAdapter : AdapterBase {
     }
 
     template <class F>
-    __device__ bool segments(F f) const {
-        for (int phase = 0; phase < 2; ++phase) {
+    __device__ bool segments(F f, int first_phase = 0) const {
+        for (int phase = first_phase; phase < 2; ++phase) {
             const skinny::Line line(phase == 0 ? with_adapter : (int64_t)G * tiles, phase == 0 ? kbs : kbs + 2 * more,
-                                    gridDim.x, skinny::kSlackWork);
+                                    gridDim.x, kSlackGrouped);
             const bool ok = line.each(blockIdx.x, [&](int64_t tile, skinny::Segment &s) {
                 s.line = s.phase = phase;
                 s.group = phase == 0 ? (int)tile : (int)skinny::quotient(tile, tiles);
@@ -230,6 +236,13 @@ struct GroupedAdapter : AdapterBase {
                 if (col + j < s.n) a.out[(size_t)a.order[s.first + col + j] * a.N + o] = __float2bfloat16_rn(sums[j]);
         }
     };
+    // shared tiles of the last line are the readers': four times the threads, and nothing else left to do
+    __device__ bool adders_take(const skinny::Segment &s) const { return s.phase == 0; }
+    __device__ bool finish() const {
+        return segments([&](const skinny::Segment &s) {
+            return s.whole() || skinny::add_up<skinny::ReadersOf<GroupedAdapter>>(*this, a.shape, s);
+        }, 1);
+    }
     __device__ void before_signal(const skinny::Segment &s) const {
         if (s.phase == 0) fence_proxy_async();   // v is read by TMA
     }

@@ -246,6 +246,7 @@ struct ExpertsProblem {
             }
         }
     };
+    __device__ bool adders_take(const skinny::Segment &) const { return true; }
     // a tile's values are written: before the barrier and the count that say so
     __device__ void before_signal(const skinny::Segment &s) const {
         if (s.phase == 0) fence_proxy_async();   // h is read by TMA

@@ -29,6 +29,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "umma.cuh"
 
@@ -66,9 +67,16 @@ struct Segment {
     __device__ bool whole() const { return kb0 == 0 && kb1 == kbs; }
 };
 
-// a / b, by a 32-bit division where both fit (a 64-bit one is a long sequence).
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+// a / b for a >= 0 and b > 0. An integer division takes 250 cycles or more, and
+// a small call waits for a dozen of them before its first load; below 2^20 a
+// float one is exact: (a + 1/2) / b is at least 1 / (2 b) from the next integer,
+// its error at most 3 units of 2^-24 of a / b.
+static __device__ __noinline__ int64_t long_quotient(int64_t a, int64_t b) {
     return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if ((a | b) >> 20) return long_quotient(a, b);
+    return (int)__fdividef((float)(int)a + 0.5f, (float)(int)b);
 }
 
 // A line of K blocks: `tiles` tiles of `kbs` blocks, cut for the CTAs in one of
@@ -83,8 +91,8 @@ struct Line {
     __device__ Line(int64_t n, int k_blocks, int ctas, int slack) : tiles(n), kbs(k_blocks), span(k_blocks) {
         const int least = min(kbs, kMinBlocks);
         if (tiles > 0 && 2 * tiles <= ctas) {
-            const int share = min(ctas / (int)tiles, kbs / least);
-            per = (kbs + share - 1) / share;
+            const int share = (int)min(quotient(ctas, tiles), quotient(kbs, least));
+            per = quotient(kbs + share - 1, share);
             span = (int)per * share;
         } else {
             const int64_t whole = quotient(tiles + ctas - 1, ctas) * kbs;
@@ -131,7 +139,8 @@ struct Shape {
     int a_stages, b_stages;
     __host__ __device__ static constexpr int b_bytes(int cols, bool e4m3) { return cols * (e4m3 ? 256 : 128); }
     static Shape of(int cols, bool e4m3, int budget = kSmemBudget) {
-        const int b = b_bytes(cols, e4m3), a_stages = 3 * b <= budget - 6 * 2 * kHalf ? 6 : 5;
+        const int b = b_bytes(cols, e4m3);
+        const int a_stages = 3 * b <= budget - 6 * 2 * kHalf ? 6 : 5;
         const int b_stages = (budget - a_stages * 2 * kHalf) / b;
         return Shape{cols, a_stages, b_stages < kMaxStages ? b_stages : kMaxStages};
     }
@@ -278,14 +287,13 @@ __device__ bool load_b(const P &p, Control &c, uint32_t ring_base, const Shape s
 template <class P>
 __device__ bool multiply(const P &p, Control &c, uint32_t ring_base, const Shape sh, uint32_t tmem) {
     const bool mine = elect_one();
-    Ring ra(sh.a_stages), rb(sh.b_stages);
-    uint32_t seq = 0;
+    Ring ra(sh.a_stages), rb(sh.b_stages), sums(2);
     const bool ok = p.segments([&](const Segment &s) {
-        const uint32_t buf = seq & 1;
+        const uint32_t buf = sums.slot;
         const uint32_t desc = uniform(product_desc(s.n16())), d0 = uniform(tmem + buf * 2 * sh.cols);
         const uint32_t d1 = uniform(d0 + sh.cols);
         const bool two = uniform(s.two) != 0;
-        if (!warp_wait(&c.sums_empty[buf], (seq >> 1 & 1) ^ 1)) return false;
+        if (!warp_wait(&c.sums_empty[buf], sums.round ^ 1)) return false;
         tc_fence_after();
         for (int kb = s.kb0; kb < s.kb1; ++kb, ra.next(), rb.next()) {
             if (!warp_wait(&c.full_a[ra.slot], ra.round) || !warp_wait(&c.full_b[rb.slot], rb.round)) return false;
@@ -306,7 +314,7 @@ __device__ bool multiply(const P &p, Control &c, uint32_t ring_base, const Shape
         }
         if (mine) mma_commit(&c.sums_full[buf]);
         __syncwarp();
-        ++seq;
+        sums.next();
         return true;
     });
     if (!ok && mine) {
@@ -429,26 +437,32 @@ __device__ bool add_up(const P &p, const Shape sh, const Segment &s) {
         Share<P::kHalves> share = Share<P::kHalves>::of(Tm::warp());
         share.side = unit & 3;
         const int col = (unit >> 2) * 16 + share.first_col();
-        // eight parts' loads at once: a trip to another SM's sums in L2 takes about a microsecond
+        // 32 loads at once, of four parts or eight: a trip to another SM's sums in L2 takes about a microsecond
         float v[8] = {};
-        for (int i0 = 0; i0 < s.parts; i0 += 8) {
+        auto batch = [&](auto parts_at_once, int i0, int j0) {
+            constexpr int kParts = decltype(parts_at_once)::value, kValues = 32 / kParts;
+            float x[kParts][kValues];
 #pragma unroll
-            for (int j0 = 0; j0 < 8; j0 += 4) {
-                float x[8][4];
+            for (int i = 0; i < kParts; ++i) {
+                // the stretch that begins the tile is its CTA's last, the others their CTA's first
+                const float *part = p.partial(s.line, s.cta0 + i0 + i, i0 + i == 0 ? 1 : 0) + share.row;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    // the stretch that begins the tile is its CTA's last, the others their CTA's first
-                    const float *part = p.partial(s.line, s.cta0 + i0 + i, i0 + i == 0 ? 1 : 0) + share.row;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int at = col + share.col_of(j0 + j);
-                        x[i][j] = i0 + i < s.parts && at < s.n ? __ldcg(part + share.half_of(j0 + j) * half + at * kRows) : 0.0f;
-                    }
+                for (int j = 0; j < kValues; ++j) {
+                    const int at = col + share.col_of(j0 + j);
+                    x[i][j] = i0 + i < s.parts && at < s.n ? __ldcg(part + share.half_of(j0 + j) * half + at * kRows) : 0.0f;
                 }
+            }
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < kParts; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[j0 + j] += x[i][j];
+                for (int j = 0; j < kValues; ++j) v[j0 + j] += x[i][j];
+        };
+        if (s.parts <= 4) {
+            batch(std::integral_constant<int, 4>(), 0, 0);
+        } else {
+            for (int i0 = 0; i0 < s.parts; i0 += 8) {
+                batch(std::integral_constant<int, 8>(), i0, 0);
+                batch(std::integral_constant<int, 8>(), i0, 4);
             }
         }
         typename P::Emit emit(p, s, share);
@@ -489,7 +503,7 @@ __device__ bool take(const P &p, const Shape sh, const Segment &s, const Share<P
 
 template <class P>
 __device__ bool add_shared(const P &p, Control &c, const Shape sh) {
-    return p.segments([&](const Segment &s) { return s.whole() || add_up<AddersOf<P>>(p, sh, s); });
+    return p.segments([&](const Segment &s) { return s.whole() || !p.adders_take(s) || add_up<AddersOf<P>>(p, sh, s); });
 }
 
 // Readers of bf16 weights' sums.
@@ -498,10 +512,10 @@ __device__ bool read_sums(const P &p, Control &c, const Shape sh, uint32_t tmem)
     using Tm = ReadersOf<P>;
     const int lane = threadIdx.x & 31;
     const Share<P::kHalves> me = Share<P::kHalves>::of(Tm::warp());
-    uint32_t seq = 0;
+    Ring sums(2);
     return p.segments([&](const Segment &s) {
-        const uint32_t buf = seq & 1;
-        if (!Tm::agree(wait(&c.sums_full[buf], seq >> 1 & 1))) return false;
+        const uint32_t buf = sums.slot;
+        if (!Tm::agree(wait(&c.sums_full[buf], sums.round))) return false;
         tc_fence_after();
         const uint32_t at = tmem + ((uint32_t)(me.row & ~31) << 16) + buf * 2 * sh.cols;
         auto each = [&](auto f) {
@@ -516,7 +530,7 @@ __device__ bool read_sums(const P &p, Control &c, const Shape sh, uint32_t tmem)
             __syncwarp();
             if (lane == 0) mbar_arrive(&c.sums_empty[buf]);
         };
-        ++seq;
+        sums.next();
         return take(p, sh, s, me, each, release);
     });
 }
@@ -791,8 +805,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Index
 
 // The same for few entries, by every CTA for itself in its shared memory: no
 // launch before, and no chain of loads from its results. CTAs have to agree, so an
-// entry's place is fixed: by set, then in the order of the entries. A thread has
-// a set and looks through all entries for its own, 32 to a word of a mask. (By
+// entry's place is fixed: by set, then in the order of the entries. A few threads
+// to a set look through the entries for its own, 32 to a word of a mask. (By
 // counters in shared memory this took 2.8 us, by matching a warp's entries 4, and
 // the plan kernel with its launch takes 5.)
 constexpr int kLocalEntries = 256, kLocalSets = 512;
@@ -800,61 +814,74 @@ struct LocalPlan {
     uint32_t groups[kLocalEntries];    // set | first sorted entry << 13 | (entries - 1) << 21
     uint16_t order[kLocalEntries];
     uint16_t set_of[kLocalEntries];    // 0xffff: none
-    uint32_t totals[kLocalSets / 32];  // entries | groups << 16 of 32 sets
+    uint32_t totals[kLocalSets / 32];  // entries | groups << 16 of a warp's sets
     int num_groups;
 };
 
 // All threads of the CTA, at least kLocalSets.
 template <typename Index>
 __device__ void local_plan(LocalPlan &plan, const Index *idx, int n, int sets, int cols, int bad, int32_t *status) {
-    const int set = threadIdx.x, lane = threadIdx.x & 31;
-    if (set < kLocalEntries) {
-        const Index e = set < n ? idx[set] : (Index)-1;
+    const int tid = threadIdx.x, lane = threadIdx.x & 31;
+    if (tid < kLocalEntries) {
+        const Index e = tid < n ? idx[tid] : (Index)-1;
         const bool named = e >= 0 && e < sets;
         if (!named && e != -1 && blockIdx.x == 0) report(status, bad);
-        plan.set_of[set] = named ? (uint16_t)e : (uint16_t)0xffff;
+        plan.set_of[tid] = named ? (uint16_t)e : (uint16_t)0xffff;
     }
     __syncthreads();
-    uint32_t mine[kLocalEntries / 32] = {};
-    uint32_t count = 0, before = 0;   // entries | groups << 16
-    if (set < kLocalSets) {
-        if (set < sets)
+    // 2^split threads to a set, each with `words` words of 32 entries
+    constexpr int kWords = kLocalEntries / 32;
+    const int split = min(3, 31 - __clz(kLocalSets / sets)), part = tid & ((1 << split) - 1), set = tid >> split;
+    const int words = (((n + 31) / 32) + (1 << split) - 1) >> split;
+    uint32_t mine[kWords] = {};
+    uint32_t count = 0;
+    if (set < sets)
 #pragma unroll
-            for (int w = 0; w < kLocalEntries / 32; ++w) {
-                if (w * 32 >= n) break;
+        for (int j = 0; j < kWords; ++j) {
+            const int w = part * words + j;
+            if (j >= words || w * 32 >= n) break;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(&plan.set_of[w * 32 + q * 8]);
-                    const uint32_t two[4] = {v.x, v.y, v.z, v.w};
+            for (int q = 0; q < 4; ++q) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(&plan.set_of[w * 32 + q * 8]);
+                const uint32_t two[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        if ((two[h] & 0xffff) == (uint32_t)set) mine[w] |= 1u << (q * 8 + 2 * h);
-                        if (two[h] >> 16 == (uint32_t)set) mine[w] |= 2u << (q * 8 + 2 * h);
-                    }
+                for (int h = 0; h < 4; ++h) {
+                    if ((two[h] & 0xffff) == (uint32_t)set) mine[j] |= 1u << (q * 8 + 2 * h);
+                    if (two[h] >> 16 == (uint32_t)set) mine[j] |= 2u << (q * 8 + 2 * h);
                 }
-                count += __popc(mine[w]);
             }
-        count |= (count + cols - 1) / cols << 16;
-        before = count;
+            count += __popc(mine[j]);
+        }
+    uint32_t all = count, groups = 0, before = 0, here = 0;   // entries of the set; before the set and in it before this thread
+    if (tid < kLocalSets) {
+        for (int o = 1; o < 1 << split; o <<= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+        groups = (uint32_t)quotient(all + cols - 1, cols);
+        // entries | groups << 16 of the warp's sets, the groups by a set's first thread
+        const uint32_t both = count | (part == 0 ? groups << 16 : 0);
+        uint32_t sum = both;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t v = __shfl_up_sync(0xffffffffu, before, o);
-            if (lane >= o) before += v;
+            const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
         }
-        if (lane == 31) plan.totals[set / 32] = before;
-        before -= count;
+        if (lane == 31) plan.totals[tid / 32] = sum;
+        here = sum - both;
     }
     __syncthreads();
-    if (set < sets) {
-        for (int w = 0; w < set / 32; ++w) before += plan.totals[w];
-        int at = before & 0xffff, g = before >> 16;
-        const int entries = count & 0xffff;
-        for (int b = 0; b < entries; b += cols, ++g)
-            plan.groups[g] = (uint32_t)set | (uint32_t)(at + b) << 13 | (uint32_t)(min(cols, entries - b) - 1) << 21;
+    if (set < sets && tid < kLocalSets) {
+        for (int w = 0; w < tid / 32; ++w) before += plan.totals[w];
+        before += here;
+        int at = before & 0xffff;
+        if (part == 0) {
+            int g = before >> 16;
+            for (int b = 0; b < (int)all; b += cols, ++g)
+                plan.groups[g] = (uint32_t)set | (uint32_t)(at + b) << 13 | (uint32_t)(min(cols, (int)all - b) - 1) << 21;
+            if (set == sets - 1) plan.num_groups = g;
+        }
 #pragma unroll
-        for (int w = 0; w < kLocalEntries / 32; ++w)
-            for (uint32_t m = mine[w]; m != 0; m &= m - 1) plan.order[at++] = (uint16_t)(w * 32 + __ffs(m) - 1);
-        if (set == sets - 1) plan.num_groups = g;
+        for (int j = 0; j < kWords; ++j)
+            for (uint32_t m = mine[j]; m != 0; m &= m - 1)
+                plan.order[at++] = (uint16_t)((part * words + j) * 32 + __ffs(m) - 1);
     }
     __syncthreads();
 }
