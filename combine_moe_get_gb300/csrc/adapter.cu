@@ -188,9 +188,7 @@ struct GroupedAdapter : AdapterBase {
     struct Rows {};
     __device__ Rows b_rows(const skinny::Segment &, int) const { return Rows{}; }
     __device__ bool b_ready(const skinny::Segment &s) const {
-        if (!skinny::wait_count(a.words + kReady + s.group, skinny::kTileWeight)) return false;
-        fence_proxy_async();
-        return true;
+        return skinny::wait_count(a.words + kReady + s.group, skinny::kTileWeight);
     }
     __device__ uint32_t b_bytes(const skinny::Segment &s, int kb) const {
         return kb < kbs ? a.shape.cols * 128 : (s.n + 7) / 8 * 1024;
@@ -242,9 +240,6 @@ struct GroupedAdapter : AdapterBase {
         return segments([&](const skinny::Segment &s) {
             return s.whole() || skinny::add_up<skinny::ReadersOf<GroupedAdapter>>(*this, a.shape, s);
         }, 1);
-    }
-    __device__ void before_signal(const skinny::Segment &s) const {
-        if (s.phase == 0) fence_proxy_async();   // v is read by TMA
     }
     __device__ void tile_done(const skinny::Segment &s, uint32_t weight) const {
         if (s.phase == 0) skinny::count_up(a.words + kReady + s.group, weight);

@@ -185,9 +185,7 @@ struct ExpertsProblem {
         int r[4];
     };
     __device__ bool b_ready(const skinny::Segment &s) const {
-        if (!skinny::wait_count(a.words + kReady + s.group, tiles[0] * skinny::kTileWeight)) return false;
-        fence_proxy_async();
-        return true;
+        return skinny::wait_count(a.words + kReady + s.group, tiles[0] * skinny::kTileWeight);
     }
     __device__ Rows b_rows(const skinny::Segment &s, int lane) const {
         Rows rows{};
@@ -247,10 +245,6 @@ struct ExpertsProblem {
         }
     };
     __device__ bool adders_take(const skinny::Segment &) const { return true; }
-    // a tile's values are written: before the barrier and the count that say so
-    __device__ void before_signal(const skinny::Segment &s) const {
-        if (s.phase == 0) fence_proxy_async();   // h is read by TMA
-    }
     __device__ uint64_t *done() const { return reinterpret_cast<uint64_t *>(a.words + skinny::kDoneWord); }
     __device__ void tile_done(const skinny::Segment &s, uint32_t weight) const {
         if (s.phase == 0) skinny::count_up(a.words + kReady + s.group, weight);

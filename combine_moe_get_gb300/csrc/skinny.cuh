@@ -12,7 +12,7 @@
 // result does not depend on the arrival order.
 //
 // Roles of a CTA's warps: 0 loads A (weights), 1 loads B (activations), 2 issues
-// the products, 3 owns the tensor memory, the next 8 or 16 (P::kReaders) read the
+// the products, 3 owns the tensor memory and announces results to other CTAs, the next 8 or 16 (P::kReaders) read the
 // sums, and where tiles are shared through the workspace (P::kAdders) 4 more add
 // those up while the others go on.
 //   bf16 weights: A and B from shared memory; sums stay in tensor memory for a
@@ -51,6 +51,7 @@ constexpr int kRows = 128;             // weight rows of one product; a tile has
 constexpr int kHalf = kRows * 128;     // bytes of one A tile of a stage
 constexpr int kMaxCtas = 160;
 constexpr int kMaxStages = 8;
+constexpr int kMaxSums = 4;            // tiles' or blocks' sums in tensor memory
 constexpr int kSmemBudget = 224 << 10;
 constexpr int kMinBlocks = MOE_TUNE_SKINNY_MIN_BLOCKS;          // K blocks a CTA takes at least (or a whole tile)
 
@@ -124,11 +125,12 @@ struct Line {
 
 struct Control {
     uint64_t full_a[kMaxStages], empty_a[kMaxStages], full_b[kMaxStages], empty_b[kMaxStages];
-    uint64_t sums_full[2], sums_empty[2];
-    uint64_t a_ready[3];     // E4M3: converted block in tensor memory
-    uint64_t a_free[3];      // ... and used up
+    uint64_t sums_full[kMaxSums], sums_empty[kMaxSums];
+    uint64_t a_ready[2];     // E4M3: converted block in tensor memory
+    uint64_t a_free[2];      // ... and used up
     uint64_t last;
     uint32_t tmem;
+    uint32_t written;        // reader warps that have written a segment's results, over all segments
 };
 
 // A and B have a ring each: the loads of A in flight are what keeps HBM busy (five
@@ -263,8 +265,12 @@ __device__ bool load_b(const P &p, Control &c, uint32_t ring_base, const Shape s
                 if (go) go = wait(&c.empty_b[r.slot], r.round ^ 1);
                 if (go) mbar_arrive_expect_tx(&c.full_b[r.slot], p.b_bytes(s, kb) * (kE4m3 ? 2 : 1));
             }
-            waited |= kb >= s.b_from;
             if (!__shfl_sync(0xffffffffu, go, 0)) return false;
+            if (kb >= s.b_from && !waited) {   // other CTAs' ordinary stores, about to be read by TMA
+                waited = true;
+                __syncwarp();
+                fence_proxy_async();
+            }
             const uint32_t dst = ring_base + sh.b_at(r.slot, kE4m3);
 #pragma unroll
             for (int h = 0; h < (kE4m3 ? 2 : 1); ++h)
@@ -324,30 +330,27 @@ __device__ bool multiply(const P &p, Control &c, uint32_t ring_base, const Shape
     return ok;
 }
 
-// E4M3: blocks that tensor memory holds converted, 128 columns each, behind the
-// sums' 4 `cols`. Three where they fit: with two, a block's conversion had to wait
-// for the products of the one before last.
-constexpr int code_buffers(int most_cols) { return most_cols <= 32 ? 3 : 2; }
-constexpr int first_code_column(int most_cols) { return 512 - 128 * code_buffers(most_cols); }
+// E4M3: tensor memory holds two converted blocks, 128 columns each, behind the
+// sums of as many blocks as fit, up to four: products run ahead of their readers.
+constexpr int kTmemCodes = 256;
+constexpr int sum_buffers(int most_cols) { return most_cols <= 32 ? 4 : 2; }
 
 // Products of converted E4M3 blocks. Each block's sums start from zero.
 template <class P>
 __device__ bool multiply_e4m3(const P &p, Control &c, uint32_t ring_base, const Shape sh, uint32_t tmem) {
     const bool mine = elect_one();
-    constexpr int kCols = 8 * P::kSteps;
-    Ring r(sh.b_stages), codes(code_buffers(kCols));
-    uint32_t seq = 0;
+    Ring r(sh.b_stages), codes(2), sums(sum_buffers(8 * P::kSteps));
     const uint32_t half_b = uniform(sh.cols * 128 >> 4), half_d = uniform(sh.cols);
     const bool ok = p.segments([&](const Segment &s) {
         const uint32_t desc = uniform(product_desc(s.n16()));
-        for (int kb = s.kb0; kb < s.kb1; ++kb, r.next(), codes.next(), ++seq) {
-            const uint32_t buf = seq & 1;
+        for (int kb = s.kb0; kb < s.kb1; ++kb, r.next(), codes.next(), sums.next()) {
             if (!warp_wait(&c.full_b[r.slot], r.round) || !warp_wait(&c.a_ready[codes.slot], codes.round) ||
-                !warp_wait(&c.sums_empty[buf], (seq >> 1 & 1) ^ 1))
+                !warp_wait(&c.sums_empty[sums.slot], sums.round ^ 1))
                 return false;
             tc_fence_after();
             const uint32_t b = uniform(operand_low(ring_base + sh.b_at(r.slot, true)));
-            const uint32_t a = uniform(tmem + first_code_column(kCols) + codes.slot * 128), d = uniform(tmem + buf * 2 * sh.cols);
+            const uint32_t a = uniform(tmem + kTmemCodes + codes.slot * 128);
+            const uint32_t d = uniform(tmem + sums.slot * 2 * sh.cols);
             if (mine) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -356,7 +359,7 @@ __device__ bool multiply_e4m3(const P &p, Control &c, uint32_t ring_base, const 
                         mma_ts(d + h * half_d, a + h * 64 + k * 8, b + (k >> 2) * half_b + 2 * (k & 3), desc, k > 0);
                 mma_commit(&c.empty_b[r.slot]);
                 mma_commit(&c.a_free[codes.slot]);
-                mma_commit(&c.sums_full[buf]);
+                mma_commit(&c.sums_full[sums.slot]);
             }
             __syncwarp();
         }
@@ -416,9 +419,6 @@ __device__ void leave_part(const P &p, const Shape sh, const Segment &s, const S
             if (at < s.n) mine[me.half_of(j) * half + at * kRows] = v[j];
         }
     });
-    __threadfence();
-    ReadersOf<P>::sync();
-    if (ReadersOf<P>::leader()) count_up(p.arrivals(s.line, s.cta0), 1u);
 }
 
 // This CTA's share of the columns of such a tile, in steps of 16, once all parts are there.
@@ -468,7 +468,6 @@ __device__ bool add_up(const P &p, const Shape sh, const Segment &s) {
         typename P::Emit emit(p, s, share);
         emit(col, v);
     }
-    p.before_signal(s);
     __threadfence();
     Tm::sync();
     // the shares' weights add up to kTileWeight
@@ -478,27 +477,45 @@ __device__ bool add_up(const P &p, const Shape sh, const Segment &s) {
 
 // What the reader threads do with a segment's sums. `each(f)` calls f(column,
 // 8 values) for all of the thread's columns, `release()` gives up the sums' place.
+// Where others wait for the results the announcing warp tells them: its fences
+// take microseconds that the readers have not.
 template <class P, class Each, class Release>
-__device__ bool take(const P &p, const Shape sh, const Segment &s, const Share<P::kHalves> me, Each each,
+__device__ bool take(const P &p, Control &c, const Shape sh, const Segment &s, const Share<P::kHalves> me, Each each,
                      Release release) {
-    using Tm = ReadersOf<P>;
-    if constexpr (P::kAdders) {
-        if (!s.whole()) {
-            leave_part(p, sh, s, me, each);
-            release();
-            return true;
-        }
+    if (P::kAdders && !s.whole()) {
+        if constexpr (P::kAdders) leave_part(p, sh, s, me, each);
+    } else {
+        typename P::Emit emit(p, s, me);
+        each([&](int col, const float *v) { emit(col, v); });
     }
-    typename P::Emit emit(p, s, me);
-    each([&](int col, const float *v) { emit(col, v); });
     release();
     if constexpr (P::kAdders) {
-        p.before_signal(s);
-        __threadfence();
-        Tm::sync();
-        if (Tm::leader()) p.tile_done(s, kTileWeight);
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0)
+            asm volatile("red.release.cta.shared::cta.add.u32 [%0], 1;" ::"r"(smem_addr(&c.written)) : "memory");
     }
     return true;
+}
+
+// One lane: announces each segment once all reader warps have written its results.
+template <class P>
+__device__ bool announce(const P &p, Control &c) {
+    uint32_t want = 0;
+    return p.segments([&](const Segment &s) {
+        want += P::kReaders / 32;
+        const uint64_t deadline = globaltimer_ns() + kDefaultWaitNs;
+        while (true) {
+            uint32_t now;
+            asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(now) : "r"(smem_addr(&c.written)) : "memory");
+            if (now >= want) break;
+            if (globaltimer_ns() > deadline) return false;
+            __nanosleep(100);
+        }
+        __threadfence();
+        if (s.whole()) p.tile_done(s, kTileWeight);
+        else count_up(p.arrivals(s.line, s.cta0), 1u);
+        return true;
+    });
 }
 
 template <class P>
@@ -531,7 +548,7 @@ __device__ bool read_sums(const P &p, Control &c, const Shape sh, uint32_t tmem)
             if (lane == 0) mbar_arrive(&c.sums_empty[buf]);
         };
         sums.next();
-        return take(p, sh, s, me, each, release);
+        return take(p, c, sh, s, me, each, release);
     });
 }
 
@@ -539,11 +556,10 @@ __device__ bool read_sums(const P &p, Control &c, const Shape sh, uint32_t tmem)
 // one row (lane of tensor memory) of one half.
 template <class P>
 __device__ bool convert(const P &p, Control &c, const char *ring, const Shape sh, uint32_t tmem) {
-    constexpr int kCols = 8 * P::kSteps;
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 - kFirstReader / 32;
     const int row = (warp & 3) * 32 + lane, half = warp / 4;
-    const uint32_t dst0 = tmem + ((uint32_t)(row & ~31) << 16) + first_code_column(kCols) + half * 64;
-    Ring r(sh.a_stages), out(code_buffers(kCols));
+    const uint32_t dst0 = tmem + ((uint32_t)(row & ~31) << 16) + kTmemCodes + half * 64;
+    Ring r(sh.a_stages), out(2);
     return p.segments([&](const Segment &s) {
         for (int kb = s.kb0; kb < s.kb1; ++kb, r.next(), out.next()) {
             if (!warp_wait(&c.full_a[r.slot], r.round)) return false;
@@ -584,7 +600,7 @@ __device__ bool read_sums_e4m3(const P &p, Control &c, const Shape sh, uint32_t 
     const int lane = threadIdx.x & 31;
     const Share<false> me = Share<false>::of(Tm::warp());
     const uint32_t at0 = tmem + ((uint32_t)(me.row & ~31) << 16);
-    uint32_t seq = 0;
+    Ring sums(sum_buffers(8 * kSteps));
     return p.segments([&](const Segment &s) {
         float acc[kSteps][8] = {};
         const float *scales = p.scales(s.phase);
@@ -600,25 +616,31 @@ __device__ bool read_sums_e4m3(const P &p, Control &c, const Shape sh, uint32_t 
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 if (kb4 + u >= s.kb1) break;
-                const uint32_t buf = seq & 1;
                 const float now0 = w0[u], now1 = w1[u];
                 const int later = min(kb4 + u + 4, s.kb1 - 1);
                 w0[u] = __ldg(s0 + later), w1[u] = __ldg(s1 + later);
-                if (!warp_wait(&c.sums_full[buf], seq >> 1 & 1)) { ok = false; break; }
+                if (!warp_wait(&c.sums_full[sums.slot], sums.round)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t at = at0 + buf * 2 * sh.cols;
+                const uint32_t at = at0 + sums.slot * 2 * sh.cols;
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
+                for (int i = 0; i < kSteps; i += 2) {   // 16 columns at a time
                     if (i * 8 >= s.n16()) break;
-                    float v[8];
-                    me.load(at, sh.cols, i * 8 + me.first_col(), v);
+                    float v[16];
+                    tmem_load4(at + i * 8 + me.first_col(), v);
+                    tmem_load4(at + sh.cols + i * 8 + me.first_col(), v + 4);
+                    tmem_load4(at + i * 8 + 8 + me.first_col(), v + 8);
+                    tmem_load4(at + sh.cols + i * 8 + 8 + me.first_col(), v + 12);
+                    tmem_load_wait(v);
+                    if ((i + 2) * 8 >= s.n16()) {   // all of the block's sums are in registers
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&c.sums_empty[sums.slot]);
+                    }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) acc[i][j] = fmaf(j < 4 ? now0 : now1, v[j], acc[i][j]);
+                    for (int j = 0; j < 16; ++j)
+                        acc[i + j / 8][j & 7] = fmaf((j & 7) < 4 ? now0 : now1, v[j], acc[i + j / 8][j & 7]);
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&c.sums_empty[buf]);
-                ++seq;
+                sums.next();
             }
         }
         if (!Tm::agree(ok)) return false;
@@ -627,7 +649,7 @@ __device__ bool read_sums_e4m3(const P &p, Control &c, const Shape sh, uint32_t 
             for (int i = 0; i < kSteps; ++i)
                 if (i * 8 + me.first_col() < s.n) f(i * 8 + me.first_col(), acc[i]);
         };
-        return take(p, sh, s, me, each, [] {});
+        return take(p, c, sh, s, me, each, [] {});
     });
 }
 
@@ -651,15 +673,16 @@ __device__ void with_set_up(Make problem, Control &c, const uint32_t tmem_cols, 
             mbar_init(&c.empty_a[i], kE4m3 ? kConverters / 32 : 1);   // the converting warps, or the products
             mbar_init(&c.empty_b[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kMaxSums; ++i) {
             mbar_init(&c.sums_full[i], 1);
             mbar_init(&c.sums_empty[i], P::kReaders / 32);
         }
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&c.a_ready[i], kConverters / 32);
             mbar_init(&c.a_free[i], 1);
         }
         mbar_init(&c.last, 1);
+        c.written = 0;
         fence_barrier_init();
     }
     if (warp == 3) tmem_alloc(&c.tmem, tmem_cols);
@@ -671,6 +694,7 @@ __device__ void with_set_up(Make problem, Control &c, const uint32_t tmem_cols, 
     bool ok = true;
     roles(p, ring, tmem, warp, ok);
     if (!ok) report(p.status, MOE_ERR_TIMEOUT);
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -688,6 +712,9 @@ __device__ void run(Make problem, const Shape sh, const uint32_t tmem_cols) {
         else if (warp == 2) {
             if constexpr (kE4m3) ok = multiply_e4m3(p, c, smem_addr(ring), sh, tmem);
             else ok = multiply(p, c, smem_addr(ring), sh, tmem);
+        } else if (warp == 3) {
+            if constexpr (P::kAdders)
+                if ((threadIdx.x & 31) == 0) ok = announce(p, c);
         } else if (threadIdx.x >= AddersOf<P>::first) {
             if constexpr (P::kAdders) ok = add_shared(p, c, sh);
         } else if (threadIdx.x >= ReadersOf<P>::first) {
