@@ -145,7 +145,7 @@ TRACE_KERNELS = {1: "layout_tiles", 2: "layout_direct", 3: "layout_cluster", 4: 
                  6: "layout_rows_scan", 7: "expand_layout", 8: "expand_layout_cluster", 9: "dispatch",
                  10: "dispatch_fp8_rows", 11: "combine", 12: "layout_rows", 13: "gate", 14: "gate_backward",
                  15: "experts", 16: "adapter", 17: "plan", 18: "adapter_shrink",
-                 19: "adapter_sort", 20: "adapter_expand"}
+                 19: "adapter_sort", 20: "adapter_expand", 21: "experts_split"}
 TRACE_PHASE = 0x10000   # warp field of a per-CTA phase record: TRACE_PHASE + phase (1, 2, ...)
 TRACE_PHASE_NAMES = {3: ("dependency wait", "top-k tile loaded", "bitmap and expert histogram",
                          "tile counts and first cluster barrier", "exchange and second barrier",

@@ -89,7 +89,7 @@ __device__ __forceinline__ float bf16_high(uint32_t v) { return __uint_as_float(
 
 // What both ways share.
 struct AdapterBase {
-    static constexpr bool kHalves = true, kConvert = false;
+    static constexpr bool kHalves = true, kCodes = false;
     const AdapterArgs &a;
     int32_t *status;
     int tiles, kbs;   // feature tiles of W, K blocks of x

@@ -15,8 +15,11 @@
 // does not pause. When all of y is there, all CTAs add each token's rows in
 // entry order with their weights and round once to bf16.
 //
-// h is rounded to bf16: it is the operand of a bf16 product, and the rounding's
-// effect on an output is of the size of that output's own rounding.
+// h is rounded to bf16, or with E4M3 weights to a sum of two codes of the same
+// eight bits: it is the operand of a product, and the rounding's effect on an
+// output is of the size of that output's own rounding. With E4M3 weights a split
+// kernel makes two codes of x before, which is exact for all elements within
+// 2^-10 of their block's largest, and off by 2^-17 of that for smaller ones.
 #include <algorithm>
 #include <climits>
 #include <cuda_bf16.h>
@@ -30,7 +33,7 @@ using skinny::kRows;
 
 // Device workspace: byte offsets.
 struct Space {
-    size_t words, groups, order, h, y, partial, total;
+    size_t words, groups, order, h, h_scales, x_codes, x_scales, y, partial, total;
 };
 // Two waves from this many K blocks of phase 1 per CTA (32 KB each, some 0.7 us):
 // the hand-over of h takes about 6 us after the slowest CTA, and CTAs drift
@@ -51,14 +54,17 @@ int columns(int T, int k, int E, bool e4m3) {
 // have larger partial sums.
 int waves_for(int cols) { return cols <= 64 ? 2 : 1; }
 
-Space space(int T, int H, int I, int k, int cols) {
+Space space(int T, int H, int I, int k, int cols, bool e4m3) {
     Space s{};
     skinny::Cut cut;
     const size_t n = (size_t)T * k;   // groups are at most as many as entries
     s.words = cut.take((kReady + n) * 4);
     s.groups = cut.take(n * sizeof(int4));
     s.order = cut.take(n * 4);
-    s.h = cut.take(n * I * 2);
+    s.h = cut.take(n * I * 2);   // bf16, or first codes of all entries, then second ones
+    s.h_scales = cut.take(e4m3 ? n * (I / 128) * 4 : 0);
+    s.x_codes = cut.take(e4m3 ? (size_t)T * H * 2 : 0);
+    s.x_scales = cut.take(e4m3 ? (size_t)T * (H / 128) * 4 : 0);
     s.y = cut.take(n * H * 4);
     s.partial = cut.take(skinny::partial_floats(2 * waves_for(cols), cols) * 4);
     s.total = cut.at;
@@ -68,14 +74,16 @@ Space space(int T, int H, int I, int k, int cols) {
 // ------------------------------------------------------------------ experts
 
 struct ExpertsArgs {
-    CUtensorMap w13, w2, x, h_map;
+    CUtensorMap w13, w2, x, h_map;   // x and h: bf16, or codes [2 rows]
     const int64_t *topk_idx;
     const float *topk_weights;
     const float *s13, *s2;
+    const float *x_scales;   // E4M3: of x and of h, [row][block]
+    float *h_scales;
     uint32_t *words;
     const int4 *groups;
     const int *order;
-    __nv_bfloat16 *h;
+    void *h;
     float *y, *partials;
     __nv_bfloat16 *out;
     int32_t *status;
@@ -94,12 +102,16 @@ struct Lines {
     int waves;
 };
 
+// E4M3: largest magnitudes of 32 rows, [readers' two sides and adders][quarter][column].
+struct Most {
+    float of[3][4][4];
+};
+
 template <bool kE4m3, int kCols>   // kCols: the most columns of a tile
 struct ExpertsProblem {
     static constexpr int kSteps = kCols / 8;   // E4M3
     static_assert(kSteps > 0);
-    static constexpr bool kHalves = false, kAdders = true;
-    static constexpr bool kConvert = kE4m3;
+    static constexpr bool kHalves = false, kAdders = true, kCodes = kE4m3;
     static constexpr int kReaders = kE4m3 ? 256 : 512;
     using Readers = skinny::ReadersOf<ExpertsProblem>;
     const ExpertsArgs &a;
@@ -109,10 +121,11 @@ struct ExpertsProblem {
     int tiles[2], kbs[2];   // tiles per group and K blocks per tile of the two phases
 
     const Lines *lines;
+    Most *most;
 
     // All threads of the CTA.
-    __device__ ExpertsProblem(const ExpertsArgs &args, const skinny::LocalPlan *plan, Lines &shared_lines)
-        : a(args), local(plan), status(args.status), lines(&shared_lines) {
+    __device__ ExpertsProblem(const ExpertsArgs &args, const skinny::LocalPlan *plan, Lines &shared_lines, Most &shared_most)
+        : a(args), local(plan), status(args.status), lines(&shared_lines), most(&shared_most) {
         G = local ? local->num_groups : (int)args.words[skinny::kGroupsWord];
         constexpr int block = kE4m3 ? 128 : 64;
         tiles[0] = (a.I + kRows - 1) / kRows;
@@ -194,17 +207,29 @@ struct ExpertsProblem {
             for (int i = 0; i < 4; ++i) rows.r[i] = entry(s.first + min(4 * lane + i, s.n - 1)) / a.k;
         return rows;
     }
+    static constexpr int kParts = kE4m3 ? 2 : 1, kBlock = kE4m3 ? 128 : 64;
     __device__ uint32_t b_bytes(const skinny::Segment &s, int) const {
-        return s.phase == 0 ? (s.n + 3) / 4 * 512 : (s.n + 7) / 8 * 1024;
+        return kParts * (s.phase == 0 ? (s.n + 3) / 4 * 512 : (s.n + 7) / 8 * 1024);
     }
-    __device__ void b_load(const skinny::Segment &s, const Rows &rows, int block, uint32_t dst, uint64_t *bar,
+    __device__ void b_load(const skinny::Segment &s, const Rows &rows, int kb, uint32_t dst, uint64_t *bar,
                            uint64_t policy, int lane) const {
-        if (s.phase == 0) {
-            if (4 * lane < s.n)
-                tma_gather4(dst + lane * 512, &a.x, block * 64, rows.r[0], rows.r[1], rows.r[2], rows.r[3], bar, policy);
-        } else if (8 * lane < s.n) {
-            tma_load(dst + lane * 1024, &a.h_map, block * 64, s.first + 8 * lane, bar, policy);
+#pragma unroll
+        for (int part = 0; part < kParts; ++part) {   // second codes behind the first ones' rows
+            const uint32_t to = dst + part * s.n16() * 128;
+            if (s.phase == 0) {
+                const int o = part * a.T;
+                if (4 * lane < s.n)
+                    tma_gather4(to + lane * 512, &a.x, kb * kBlock, o + rows.r[0], o + rows.r[1], o + rows.r[2],
+                                o + rows.r[3], bar, policy);
+            } else if (8 * lane < s.n) {
+                tma_load(to + lane * 1024, &a.h_map, kb * kBlock, part * a.T * a.k + s.first + 8 * lane, bar, policy);
+            }
         }
+    }
+    // the scales of column c's activations, block by block
+    __device__ const float *b_scales(const skinny::Segment &s, int c) const {
+        return s.phase == 0 ? a.x_scales + (size_t)(entry(s.first + c) / a.k) * kbs[0]
+                            : a.h_scales + (size_t)(s.first + c) * kbs[1];
     }
 
     // ---- sums
@@ -223,14 +248,47 @@ struct ExpertsProblem {
         int row;
         __device__ Emit(const ExpertsProblem &problem, const skinny::Segment &seg, const skinny::Share<false> &me)
             : p(problem), a(p.a), s(seg), row(me.row) {}
-        __device__ void operator()(int col, const float *v) const {
-            if (s.phase == 0) {
-                const int i = s.f * kRows + row;
+        // Four columns of a block of 128 rows, which the four warps of a side hold:
+        // their largest magnitudes go through shared memory.
+        __device__ void emit_codes(int col, const float (&h)[4], int i) {
+            const int group = (threadIdx.x - Readers::first) / 128, quarter = threadIdx.x / 32 & 3;
+            float (&most)[4][4] = p.most->of[group];
+            auto side_sync = [&] { asm volatile("barrier.cta.sync %0, 128;" ::"r"(3 + group) : "memory"); };
+            side_sync();   // the columns before these are done with it
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (col + j >= s.n || i >= a.I) continue;
-                    const float g = v[j];
-                    a.h[(size_t)(s.first + col + j) * a.I + i] = __float2bfloat16_rn(g / (1.0f + expf(-g)) * v[4 + j]);
+            for (int j = 0; j < 4; ++j) {
+                const float m = skinny::lanes_max_nan(fabsf(h[j]));
+                if ((threadIdx.x & 31) == 0) most[quarter][j] = m;
+            }
+            side_sync();
+            uint8_t *codes = static_cast<uint8_t *>(a.h);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (col + j >= s.n) continue;
+                float m = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) m = most[q][j] <= m ? m : most[q][j];   // NaN stays
+                const skinny::BlockScale scale(m);
+                const skinny::Split two(h[j] * scale.inverse);
+                const size_t pos = s.first + col + j;
+                codes[pos * a.I + i] = (uint8_t)two.first;
+                codes[((size_t)a.T * a.k + pos) * a.I + i] = (uint8_t)two.second;
+                if (row == 0) a.h_scales[pos * p.kbs[1] + s.f] = scale.scale;
+            }
+        }
+        __device__ void operator()(int col, const float *v) {
+            if (s.phase == 0) {
+                float h[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) h[j] = v[j] / (1.0f + expf(-v[j])) * v[4 + j];
+                const int i = s.f * kRows + row;
+                if constexpr (kE4m3) {
+                    emit_codes(col, h, i);
+                } else if (i < a.I) {
+                    __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.h) + (size_t)(s.first + col) * a.I + i;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (col + j < s.n) to[(size_t)j * a.I] = __float2bfloat16_rn(h[j]);
                 }
             } else {
                 const int o = s.f * 2 * kRows + row;
@@ -291,21 +349,64 @@ __global__ void __launch_bounds__(skinny::threads_of<ExpertsProblem<kE4m3, kCols
     if (threadIdx.x == 0)
         for (const CUtensorMap *m : {&a.w13, &a.w2, &a.x, &a.h_map}) tma_prefetch_map(m);
     __shared__ Lines lines;
+    __shared__ Most most;
     skinny::run<kE4m3, ExpertsProblem<kE4m3, kCols>>([&](char *ring) {
         grid_dependency_wait();
         skinny::LocalPlan *plan = nullptr;
         if (a.local) {
-            plan = reinterpret_cast<skinny::LocalPlan *>(ring + a.shape.ring_bytes(kE4m3));
+            plan = reinterpret_cast<skinny::LocalPlan *>(ring + a.shape.used_bytes(kE4m3));
             skinny::local_plan(*plan, a.topk_idx, a.T * a.k, a.E, a.shape.cols, MOE_ERR_BAD_TOPK, a.status);
         }
-        return ExpertsProblem<kE4m3, kCols>(a, plan, lines);
+        return ExpertsProblem<kE4m3, kCols>(a, plan, lines, most);
     }, a.shape, a.tmem_cols);
+}
+
+// ------------------------------------------------------------------ x as codes
+
+struct SplitArgs {
+    const __nv_bfloat16 *x;
+    uint8_t *codes;      // [2T, H]: first codes, then second ones
+    float *scales;       // [T, H / 128]
+    uint32_t *clear;     // words zeroed for the experts kernel, or null
+    int T, H, num_clear;
+    TraceArgs trace;
+};
+
+// A warp to a block of 128 elements.
+__global__ void __launch_bounds__(256) experts_split_kernel(const SplitArgs s) {
+    WarpTrace wt(s.trace, MOE_TRACE_EXPERTS_SPLIT);
+    grid_dependency_wait();
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < s.num_clear; i += 256) s.clear[i] = 0;
+    const int lane = threadIdx.x & 31;
+    const int64_t block = (int64_t)blockIdx.x * 8 + threadIdx.x / 32;
+    if (block >= (int64_t)s.T * (s.H / 128)) return;
+    const size_t at = (size_t)block * 128 + lane * 4;
+    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(s.x + at));
+    const float x[4] = {__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                        __uint_as_float(v.y & 0xffff0000u)};
+    float most = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) most = fabsf(x[i]) <= most ? most : fabsf(x[i]);   // NaN stays
+    const skinny::BlockScale scale(skinny::lanes_max_nan(most));
+    uint32_t first = 0, second = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const skinny::Split two(x[i] * scale.inverse);
+        first |= (two.first & 0xff) << (8 * i);
+        second |= (two.second & 0xff) << (8 * i);
+    }
+    *reinterpret_cast<uint32_t *>(s.codes + at) = first;
+    *reinterpret_cast<uint32_t *>(s.codes + (size_t)s.T * s.H + at) = second;
+    if (lane == 0) s.scales[block] = scale.scale;
 }
 
 }  // namespace
 
 size_t experts_workspace_bytes(int T, int H, int I, int k, int E) {
-    return space(T, H, I, k, columns(T, k, E, false)).total;   // bf16 weights: the larger of the two
+    // one size for both types of weights
+    return std::max(space(T, H, I, k, columns(T, k, E, false), false).total,
+                    space(T, H, I, k, columns(T, k, E, true), true).total);
 }
 
 namespace {
@@ -323,15 +424,15 @@ int launch_experts(const ExpertsLaunch &L, bool words_are_zero) {
     if (T == 0) return MOE_OK;
     const bool e4m3 = L.w13_scales != nullptr;
     const int cols = columns(T, k, E, e4m3);
-    const Space sp = space(T, H, I, k, cols);
+    const Space sp = space(T, H, I, k, cols, e4m3);
     char *ws = static_cast<char *>(L.workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
 
     ExpertsArgs a{};
     if (!make_tensor_map(&a.w13, L.w13, e4m3, (uint64_t)E * 2 * I, H, kRows) ||
         !make_tensor_map(&a.w2, L.w2, e4m3, (uint64_t)E * H, I, kRows) ||
-        !make_tensor_map(&a.x, L.x, false, T, H, 1) ||
-        !make_tensor_map(&a.h_map, ws + sp.h, false, (uint64_t)T * k, I, 8))
+        !make_tensor_map(&a.x, e4m3 ? ws + sp.x_codes : L.x, e4m3, e4m3 ? 2 * T : T, H, 1) ||
+        !make_tensor_map(&a.h_map, ws + sp.h, e4m3, (uint64_t)T * k * (e4m3 ? 2 : 1), I, 8))
         return MOE_ERR_CUDA;
     a.topk_idx = L.topk_idx;
     a.topk_weights = L.topk_weights;
@@ -340,7 +441,9 @@ int launch_experts(const ExpertsLaunch &L, bool words_are_zero) {
     a.words = reinterpret_cast<uint32_t *>(ws + sp.words);
     a.groups = reinterpret_cast<const int4 *>(ws + sp.groups);
     a.order = reinterpret_cast<const int *>(ws + sp.order);
-    a.h = reinterpret_cast<__nv_bfloat16 *>(ws + sp.h);
+    a.h = ws + sp.h;
+    a.x_scales = reinterpret_cast<const float *>(ws + sp.x_scales);
+    a.h_scales = reinterpret_cast<float *>(ws + sp.h_scales);
     a.y = reinterpret_cast<float *>(ws + sp.y);
     a.partials = reinterpret_cast<float *>(ws + sp.partial);
     a.out = static_cast<__nv_bfloat16 *>(L.out);
@@ -359,8 +462,18 @@ int launch_experts(const ExpertsLaunch &L, bool words_are_zero) {
                                              MOE_ERR_BAD_TOPK, L.status, a.trace};
         const int rc = skinny::launch_plan(plan, s);
         if (rc != MOE_OK) return rc;
-    } else if (!words_are_zero) {
+    } else if (!words_are_zero && !e4m3) {
         if (launch_kernel(skinny::clear_kernel, dim3(1), dim3(1024), 0, s, overlap, a.words, kReady + T * k) != cudaSuccess)
+            return MOE_ERR_CUDA;
+    }
+    if (e4m3) {
+        const bool clear = a.local && !words_are_zero;
+        const SplitArgs split{static_cast<const __nv_bfloat16 *>(L.x), reinterpret_cast<uint8_t *>(ws + sp.x_codes),
+                              reinterpret_cast<float *>(ws + sp.x_scales), clear ? a.words : nullptr, T, H,
+                              clear ? kReady + T * k : 0, a.trace};
+        const int64_t blocks = (int64_t)T * (H / 128);
+        if (launch_kernel(experts_split_kernel, dim3((unsigned)((blocks + 7) / 8)), dim3(256), 0, s, overlap, split) !=
+            cudaSuccess)
             return MOE_ERR_CUDA;
     }
     const size_t smem = a.shape.smem(e4m3) + (a.local ? sizeof(skinny::LocalPlan) : 0);

@@ -18,12 +18,14 @@
 //   bf16 weights: A and B from shared memory; sums stay in tensor memory for a
 //     whole stretch of K, double-buffered, so that the readers' work on one
 //     tile runs under the next tile's products.
-//   E4M3 weights: 8 more warps turn each block's codes into bf16 (exact) in
-//     tensor memory, from where the products take A; a block of 128 along K has
-//     its own fp32 scale per weight row, so the readers scale each block's sums
-//     and add them in registers (n <= 64). Blocks are buffered on both sides of
-//     the products. (Readers that did the conversions themselves, 8 or 16
-//     of them, took 1.6 times the time that a block's bytes take.)
+//   E4M3 weights: the activations come as the sum of two E4M3 codes under a power
+//     of two per row and block (Split, below), the second codes as further
+//     columns, so that the codes go to the tensor core as they are. A block of 128
+//     along K has its own fp32 scale per weight row, so the readers scale each
+//     block's sums and add them in registers (n <= 64); four blocks' sums in
+//     tensor memory let the products run ahead. (Turning the codes into bf16 in
+//     tensor memory, by 8 more warps, was bound by that memory's ports: 2.01 ms
+//     where this takes 1.83.)
 //
 // The problem P gives the segments, the loads of B and what becomes of the sums.
 #pragma once
@@ -36,12 +38,11 @@
 namespace moe {
 namespace skinny {
 
-constexpr int kFirstReader = 128;      // first thread of the converting, else the reading warps
+constexpr int kFirstReader = 128;      // first thread of the reading warps
 constexpr int kAdders = 128;           // threads of the adding warps
 constexpr int kMaxLines = 8;
 constexpr int kMaxSplit = 8;           // CTAs of a cluster that share a tile
 constexpr uint32_t kTileWeight = 1024;   // what the finished parts of a tile count together
-constexpr int kConverters = 256;
 // Two thirds of the SMs draw all of HBM's bandwidth where a block costs little
 // besides its bytes (100 SMs: within 1% of 152, one token); a tile that no other
 // CTA shares saves some 10 us of hand-over. Blocks that keep an SM busy, E4M3
@@ -126,12 +127,16 @@ struct Line {
 struct Control {
     uint64_t full_a[kMaxStages], empty_a[kMaxStages], full_b[kMaxStages], empty_b[kMaxStages];
     uint64_t sums_full[kMaxSums], sums_empty[kMaxSums];
-    uint64_t a_ready[2];     // E4M3: converted block in tensor memory
-    uint64_t a_free[2];      // ... and used up
     uint64_t last;
     uint32_t tmem;
     uint32_t written;        // reader warps that have written a segment's results, over all segments
 };
+
+// E4M3: the scales of a block's activations, a place for each column and block.
+// Loads run at most kMaxStages blocks ahead of the products, those kMaxSums ahead
+// of the readers.
+constexpr int kScaleSlots = 16, kScaleBytes = kScaleSlots * 64 * 4;
+static_assert(kMaxStages + kMaxSums < kScaleSlots, "a place may be in use when its turn comes");
 
 // A and B have a ring each: the loads of A in flight are what keeps HBM busy (five
 // or six blocks of 32 KB; with four the stream was 10% slower), those of B come
@@ -141,15 +146,19 @@ struct Shape {
     int a_stages, b_stages;
     __host__ __device__ static constexpr int b_bytes(int cols, bool e4m3) { return cols * (e4m3 ? 256 : 128); }
     static Shape of(int cols, bool e4m3, int budget = kSmemBudget) {
+        if (e4m3) budget -= kScaleBytes;
         const int b = b_bytes(cols, e4m3);
         const int a_stages = 3 * b <= budget - 6 * 2 * kHalf ? 6 : 5;
         const int b_stages = (budget - a_stages * 2 * kHalf) / b;
         return Shape{cols, a_stages, b_stages < kMaxStages ? b_stages : kMaxStages};
     }
     __host__ __device__ int ring_bytes(bool e4m3) const { return a_stages * 2 * kHalf + b_stages * b_bytes(cols, e4m3); }
-    size_t smem(bool e4m3) const { return 1024 + (size_t)ring_bytes(e4m3); }
+    // the ring, and for E4M3 the activations' scales behind it
+    __host__ __device__ int used_bytes(bool e4m3) const { return ring_bytes(e4m3) + (e4m3 ? kScaleBytes : 0); }
+    size_t smem(bool e4m3) const { return 1024 + (size_t)used_bytes(e4m3); }
     __device__ uint32_t a_at(int slot) const { return slot * 2 * kHalf; }
     __device__ uint32_t b_at(int slot, bool e4m3) const { return a_stages * 2 * kHalf + slot * b_bytes(cols, e4m3); }
+    // bf16: two tiles' sums of 2 `cols` columns; E4M3: kMaxSums blocks' of twice as many, or two
     int tmem_cols(bool e4m3) const {
         if (e4m3) return 512;
         int c = 32;
@@ -196,7 +205,7 @@ struct Team {
     }
 };
 template <class P>
-using ReadersOf = Team<1, kFirstReader + (P::kConvert ? kConverters : 0), P::kReaders>;
+using ReadersOf = Team<1, kFirstReader, P::kReaders>;
 template <class P>
 using AddersOf = Team<2, ReadersOf<P>::first + P::kReaders, kAdders>;
 
@@ -250,7 +259,7 @@ __device__ bool load_a(const P &p, Control &c, uint32_t ring_base, const Shape s
 }
 
 template <bool kE4m3, class P>
-__device__ bool load_b(const P &p, Control &c, uint32_t ring_base, const Shape sh) {
+__device__ bool load_b(const P &p, Control &c, uint32_t ring_base, float *scales, const Shape sh) {
     const int lane = threadIdx.x & 31;
     Ring r(sh.b_stages);
     int issued = 0;
@@ -258,12 +267,22 @@ __device__ bool load_b(const P &p, Control &c, uint32_t ring_base, const Shape s
     const bool ok = p.segments([&](const Segment &s) {
         typename P::Rows rows = p.b_rows(s, lane);
         bool waited = false;
+        // E4M3: scales of this lane's columns, of this block and the next two
+        const float *from[2] = {};
+        float ahead[3][2] = {};
+        if constexpr (kE4m3)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) from[h] = p.b_scales(s, min(lane + 32 * h, s.n - 1));
+        auto load_scales = [&](int kb, float (&x)[2]) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (lane + 32 * h < s.n) x[h] = __ldcg(from[h] + min(kb, s.kb1 - 1));
+        };
         for (int kb = s.kb0; kb < s.kb1; ++kb, r.next(), ++issued) {
             bool go = true;
             if (lane == 0) {
                 if (kb >= s.b_from && !waited) go = p.b_ready(s);
                 if (go) go = wait(&c.empty_b[r.slot], r.round ^ 1);
-                if (go) mbar_arrive_expect_tx(&c.full_b[r.slot], p.b_bytes(s, kb) * (kE4m3 ? 2 : 1));
             }
             if (!__shfl_sync(0xffffffffu, go, 0)) return false;
             if (kb >= s.b_from && !waited) {   // other CTAs' ordinary stores, about to be read by TMA
@@ -271,10 +290,22 @@ __device__ bool load_b(const P &p, Control &c, uint32_t ring_base, const Shape s
                 __syncwarp();
                 fence_proxy_async();
             }
-            const uint32_t dst = ring_base + sh.b_at(r.slot, kE4m3);
+            if constexpr (kE4m3) {
+                if (kb == s.kb0)
 #pragma unroll
-            for (int h = 0; h < (kE4m3 ? 2 : 1); ++h)
-                p.b_load(s, rows, kb * (kE4m3 ? 2 : 1) + h, dst + h * sh.cols * 128, &c.full_b[r.slot], policy, lane);
+                    for (int i = 0; i < 3; ++i) load_scales(kb + i, ahead[i]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    scales[(issued % kScaleSlots) * 64 + lane + 32 * h] = ahead[0][h];
+                    ahead[0][h] = ahead[1][h];
+                    ahead[1][h] = ahead[2][h];
+                }
+                load_scales(kb + 3, ahead[2]);
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive_expect_tx(&c.full_b[r.slot], p.b_bytes(s, kb));
+            __syncwarp();
+            p.b_load(s, rows, kb, ring_base + sh.b_at(r.slot, kE4m3), &c.full_b[r.slot], policy, lane);
         }
         return true;
     });
@@ -330,36 +361,34 @@ __device__ bool multiply(const P &p, Control &c, uint32_t ring_base, const Shape
     return ok;
 }
 
-// E4M3: tensor memory holds two converted blocks, 128 columns each, behind the
-// sums of as many blocks as fit, up to four: products run ahead of their readers.
-constexpr int kTmemCodes = 256;
+// E4M3: blocks' sums in tensor memory, 4 columns of it for each of a tile's.
 constexpr int sum_buffers(int most_cols) { return most_cols <= 32 ? 4 : 2; }
 
-// Products of converted E4M3 blocks. Each block's sums start from zero.
+// Products of E4M3 weights with activations split in two: first codes in columns
+// [0, n16), second ones in [n16, 2 n16). Each block's sums start from zero.
 template <class P>
 __device__ bool multiply_e4m3(const P &p, Control &c, uint32_t ring_base, const Shape sh, uint32_t tmem) {
     const bool mine = elect_one();
-    Ring r(sh.b_stages), codes(2), sums(sum_buffers(8 * P::kSteps));
-    const uint32_t half_b = uniform(sh.cols * 128 >> 4), half_d = uniform(sh.cols);
+    Ring ra(sh.a_stages), rb(sh.b_stages), sums(sum_buffers(8 * P::kSteps));
     const bool ok = p.segments([&](const Segment &s) {
-        const uint32_t desc = uniform(product_desc(s.n16()));
-        for (int kb = s.kb0; kb < s.kb1; ++kb, r.next(), codes.next(), sums.next()) {
-            if (!warp_wait(&c.full_b[r.slot], r.round) || !warp_wait(&c.a_ready[codes.slot], codes.round) ||
+        const uint32_t desc = uniform(product_desc(2 * s.n16(), true));
+        for (int kb = s.kb0; kb < s.kb1; ++kb, ra.next(), rb.next(), sums.next()) {
+            if (!warp_wait(&c.full_a[ra.slot], ra.round) || !warp_wait(&c.full_b[rb.slot], rb.round) ||
                 !warp_wait(&c.sums_empty[sums.slot], sums.round ^ 1))
                 return false;
             tc_fence_after();
-            const uint32_t b = uniform(operand_low(ring_base + sh.b_at(r.slot, true)));
-            const uint32_t a = uniform(tmem + kTmemCodes + codes.slot * 128);
-            const uint32_t d = uniform(tmem + sums.slot * 2 * sh.cols);
+            const uint32_t a = uniform(operand_low(ring_base + sh.a_at(ra.slot)));
+            const uint32_t b = uniform(operand_low(ring_base + sh.b_at(rb.slot, true)));
+            const uint32_t d0 = uniform(tmem + sums.slot * 4 * sh.cols), d1 = uniform(d0 + 2 * sh.cols);
             if (mine) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int k = 0; k < 4; ++k) mma_e4m3(d0, a + 2 * k, b + 2 * k, desc, k > 0);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_ts(d + h * half_d, a + h * 64 + k * 8, b + (k >> 2) * half_b + 2 * (k & 3), desc, k > 0);
-                mma_commit(&c.empty_b[r.slot]);
-                mma_commit(&c.a_free[codes.slot]);
+                for (int k = 0; k < 4; ++k) mma_e4m3(d1, a + (kHalf >> 4) + 2 * k, b + 2 * k, desc, k > 0);
+                mma_commit(&c.empty_a[ra.slot]);
+                mma_commit(&c.empty_b[rb.slot]);
                 mma_commit(&c.sums_full[sums.slot]);
+                mbar_arrive(&c.sums_full[sums.slot]);   // hands the readers the scales that came with B
             }
             __syncwarp();
         }
@@ -372,15 +401,47 @@ __device__ bool multiply_e4m3(const P &p, Control &c, uint32_t ring_base, const 
     return ok;
 }
 
-// Two E4M3 codes (the low 16 bits) as two bf16, exactly.
-__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t two) {
-    uint32_t h, out;
-    asm("{\n\t.reg .b16 t, lo, hi;\n\t.reg .f32 x, y;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
-        : "=r"(h) : "r"(two));
-    asm("{\n\t.reg .b16 lo, hi;\n\t.reg .f32 x, y;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 x, lo;\n\t"
-        "cvt.f32.f16 y, hi;\n\tcvt.rn.bf16x2.f32 %0, y, x;\n\t}"
-        : "=r"(out) : "r"(h));
-    return out;
+// y scaled to |y| < 256 as the sum of two E4M3 codes. The first holds four bits,
+// what is left has at most four more of a bf16's eight: the sum is y exactly for
+// |y| >= 1/4, and off by 2^-10 at most below. Of an fp32 it is the nearest within
+// 2^-9 of y.
+struct Split {
+    uint32_t first, second;   // low bytes
+    __device__ __forceinline__ explicit Split(float y) {
+        first = code(y);
+        second = code(y - value(first));
+    }
+    __device__ __forceinline__ static uint32_t code(float v) {
+        uint16_t r;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.0f), "f"(v));
+        return r;
+    }
+    __device__ __forceinline__ static float value(uint32_t code) {
+        float f;
+        asm("{\n\t.reg .b16 t, lo, hi;\n\t.reg .b32 h;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 h, t;\n\t"
+            "mov.b32 {lo, hi}, h;\n\tcvt.f32.f16 %0, lo;\n\t}"
+            : "=f"(f) : "r"(code));
+        return f;
+    }
+};
+
+// The power of two under which a block with this largest magnitude stays below
+// 256, and its inverse. A block that is not finite gets NaN for its scale: so does
+// all that it is multiplied with.
+struct BlockScale {
+    float scale, inverse;
+    __device__ __forceinline__ explicit BlockScale(float most) {
+        const int e = max((int)(__float_as_uint(most) >> 23) - 7, 7);
+        scale = most < INFINITY ? __uint_as_float((uint32_t)e << 23) : __uint_as_float(0x7fc00000u);
+        inverse = __uint_as_float((uint32_t)(254 - e) << 23);
+    }
+};
+
+// The largest of the lanes' values; NaN wins.
+__device__ __forceinline__ float lanes_max_nan(float v) {
+    float r;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 // A thread's share of a tile's sums: one row, and eight values at a time.
@@ -552,55 +613,16 @@ __device__ bool read_sums(const P &p, Control &c, const Shape sh, uint32_t tmem)
     });
 }
 
-// E4M3: the codes of each block into tensor memory as bf16. A thread converts
-// one row (lane of tensor memory) of one half.
-template <class P>
-__device__ bool convert(const P &p, Control &c, const char *ring, const Shape sh, uint32_t tmem) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 - kFirstReader / 32;
-    const int row = (warp & 3) * 32 + lane, half = warp / 4;
-    const uint32_t dst0 = tmem + ((uint32_t)(row & ~31) << 16) + kTmemCodes + half * 64;
-    Ring r(sh.a_stages), out(2);
-    return p.segments([&](const Segment &s) {
-        for (int kb = s.kb0; kb < s.kb1; ++kb, r.next(), out.next()) {
-            if (!warp_wait(&c.full_a[r.slot], r.round)) return false;
-            // 16-byte pieces of a 128-byte row, swizzled by the row
-            const char *codes = ring + sh.a_at(r.slot) + half * kHalf + row * 128;
-            uint4 w[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) w[q] = *reinterpret_cast<const uint4 *>(codes + ((q ^ (row & 7)) << 4));
-            if (!warp_wait(&c.a_free[out.slot], out.round ^ 1)) return false;
-            tc_fence_after();
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                uint32_t b[8];
-                b[0] = codes_to_bf16(w[q].x), b[1] = codes_to_bf16(w[q].x >> 16);
-                b[2] = codes_to_bf16(w[q].y), b[3] = codes_to_bf16(w[q].y >> 16);
-                b[4] = codes_to_bf16(w[q].z), b[5] = codes_to_bf16(w[q].z >> 16);
-                b[6] = codes_to_bf16(w[q].w), b[7] = codes_to_bf16(w[q].w >> 16);
-                tmem_store8(dst0 + out.slot * 128 + q * 8, b);
-                if (q == 3) {   // the codes are in registers by now
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&c.empty_a[r.slot]);
-                }
-            }
-            tmem_store_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&c.a_ready[out.slot]);
-        }
-        return true;
-    });
-}
-
 // Readers of E4M3 weights' sums: each block's, scaled, into registers; tiles of up to 8 kSteps columns.
 template <int kSteps, class P>
-__device__ bool read_sums_e4m3(const P &p, Control &c, const Shape sh, uint32_t tmem) {
+__device__ bool read_sums_e4m3(const P &p, Control &c, const float *b_scales, const Shape sh, uint32_t tmem) {
     using Tm = ReadersOf<P>;
     static_assert(!P::kHalves && P::kReaders == 256, "a thread scales both halves, two sides share the columns");
     const int lane = threadIdx.x & 31;
     const Share<false> me = Share<false>::of(Tm::warp());
     const uint32_t at0 = tmem + ((uint32_t)(me.row & ~31) << 16);
     Ring sums(sum_buffers(8 * kSteps));
+    uint32_t block = 0;
     return p.segments([&](const Segment &s) {
         float acc[kSteps][8] = {};
         const float *scales = p.scales(s.phase);
@@ -608,37 +630,43 @@ __device__ bool read_sums_e4m3(const P &p, Control &c, const Shape sh, uint32_t 
         const float *s0 = scales + (size_t)min(s.row0 + me.row, rows - 1) * s.kbs;
         const float *s1 = scales + (size_t)min(s.row1 + me.row, rows - 1) * s.kbs;
         bool ok = true;
-        // scales come four blocks ahead: every eighth block's are in a new sector
+        // weights' scales come four blocks ahead: every eighth block's are in a new sector
         float w0[4], w1[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) w0[u] = __ldg(s0 + min(s.kb0 + u, s.kb1 - 1)), w1[u] = __ldg(s1 + min(s.kb0 + u, s.kb1 - 1));
         for (int kb4 = s.kb0; kb4 < s.kb1 && ok; kb4 += 4) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                if (kb4 + u >= s.kb1) break;
+                const int kb = kb4 + u;
+                if (kb >= s.kb1) break;
                 const float now0 = w0[u], now1 = w1[u];
-                const int later = min(kb4 + u + 4, s.kb1 - 1);
+                const int later = min(kb + 4, s.kb1 - 1);
                 w0[u] = __ldg(s0 + later), w1[u] = __ldg(s1 + later);
                 if (!warp_wait(&c.sums_full[sums.slot], sums.round)) { ok = false; break; }
                 tc_fence_after();
-                const uint32_t at = at0 + sums.slot * 2 * sh.cols;
+                const float *of_block = b_scales + (block++ % kScaleSlots) * 64 + me.first_col();
+                const uint32_t at = at0 + sums.slot * 4 * sh.cols + me.first_col();
 #pragma unroll
-                for (int i = 0; i < kSteps; i += 2) {   // 16 columns at a time
+                for (int i = 0; i < kSteps; ++i) {
                     if (i * 8 >= s.n16()) break;
-                    float v[16];
-                    tmem_load4(at + i * 8 + me.first_col(), v);
-                    tmem_load4(at + sh.cols + i * 8 + me.first_col(), v + 4);
-                    tmem_load4(at + i * 8 + 8 + me.first_col(), v + 8);
-                    tmem_load4(at + sh.cols + i * 8 + 8 + me.first_col(), v + 12);
+                    float v[16];   // first and second codes' sums of half 0, then of half 1
+                    tmem_load4(at + i * 8, v);
+                    tmem_load4(at + s.n16() + i * 8, v + 4);
+                    tmem_load4(at + 2 * sh.cols + i * 8, v + 8);
+                    tmem_load4(at + 2 * sh.cols + s.n16() + i * 8, v + 12);
                     tmem_load_wait(v);
-                    if ((i + 2) * 8 >= s.n16()) {   // all of the block's sums are in registers
+                    if ((i + 1) * 8 >= s.n16()) {   // all of the block's sums are in registers
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&c.sums_empty[sums.slot]);
                     }
+                    const float4 bs = *reinterpret_cast<const float4 *>(of_block + i * 8);
+                    const float scale[4] = {bs.x, bs.y, bs.z, bs.w};
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        acc[i + j / 8][j & 7] = fmaf((j & 7) < 4 ? now0 : now1, v[j], acc[i + j / 8][j & 7]);
+                    for (int j = 0; j < 4; ++j) {
+                        acc[i][j] = fmaf(now0 * scale[j], v[j] + v[4 + j], acc[i][j]);
+                        acc[i][4 + j] = fmaf(now1 * scale[j], v[8 + j] + v[12 + j], acc[i][4 + j]);
+                    }
                 }
                 sums.next();
             }
@@ -661,7 +689,7 @@ constexpr int threads_of() {
 // Barriers and tensor memory, then `roles(problem, ring, tensor memory, ok)` on
 // every thread; `problem(ring)` makes the
 // problem after the set-up, when the ring is still unused.
-template <bool kE4m3, class P, class Make, class Roles>
+template <class P, class Make, class Roles>
 __device__ void with_set_up(Make problem, Control &c, const uint32_t tmem_cols, Roles roles) {
     extern __shared__ char smem_raw[];
     const int warp = (int)uniform(threadIdx.x / 32);
@@ -670,16 +698,12 @@ __device__ void with_set_up(Make problem, Control &c, const uint32_t tmem_cols, 
         for (int i = 0; i < kMaxStages; ++i) {
             mbar_init(&c.full_a[i], 1);
             mbar_init(&c.full_b[i], 1);
-            mbar_init(&c.empty_a[i], kE4m3 ? kConverters / 32 : 1);   // the converting warps, or the products
+            mbar_init(&c.empty_a[i], 1);
             mbar_init(&c.empty_b[i], 1);
         }
         for (int i = 0; i < kMaxSums; ++i) {
-            mbar_init(&c.sums_full[i], 1);
+            mbar_init(&c.sums_full[i], P::kCodes ? 2 : 1);
             mbar_init(&c.sums_empty[i], P::kReaders / 32);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&c.a_ready[i], kConverters / 32);
-            mbar_init(&c.a_free[i], 1);
         }
         mbar_init(&c.last, 1);
         c.written = 0;
@@ -706,9 +730,10 @@ __device__ void with_set_up(Make problem, Control &c, const uint32_t tmem_cols, 
 template <bool kE4m3, class P, class Make>
 __device__ void run(Make problem, const Shape sh, const uint32_t tmem_cols) {
     __shared__ Control c;
-    with_set_up<kE4m3, P>(problem, c, tmem_cols, [&](const P &p, char *ring, uint32_t tmem, int warp, bool &ok) {
+    with_set_up<P>(problem, c, tmem_cols, [&](const P &p, char *ring, uint32_t tmem, int warp, bool &ok) {
+        float *scales = reinterpret_cast<float *>(ring + sh.ring_bytes(kE4m3));   // E4M3
         if (warp == 0) ok = load_a(p, c, smem_addr(ring), sh);
-        else if (warp == 1) ok = load_b<kE4m3>(p, c, smem_addr(ring), sh);
+        else if (warp == 1) ok = load_b<kE4m3>(p, c, smem_addr(ring), scales, sh);
         else if (warp == 2) {
             if constexpr (kE4m3) ok = multiply_e4m3(p, c, smem_addr(ring), sh, tmem);
             else ok = multiply(p, c, smem_addr(ring), sh, tmem);
@@ -718,11 +743,9 @@ __device__ void run(Make problem, const Shape sh, const uint32_t tmem_cols) {
         } else if (threadIdx.x >= AddersOf<P>::first) {
             if constexpr (P::kAdders) ok = add_shared(p, c, sh);
         } else if (threadIdx.x >= ReadersOf<P>::first) {
-            if constexpr (kE4m3) ok = read_sums_e4m3<P::kSteps>(p, c, sh, tmem);
+            if constexpr (kE4m3) ok = read_sums_e4m3<P::kSteps>(p, c, scales, sh, tmem);
             else ok = read_sums(p, c, sh, tmem);
             if (ok) ok = p.finish();
-        } else if (warp >= 4) {
-            if constexpr (kE4m3) ok = convert(p, c, ring, sh, tmem);
         }
     });
 }
@@ -732,9 +755,9 @@ __device__ void run(Make problem, const Shape sh, const uint32_t tmem_cols) {
 template <class P, class Make, class Finish>
 __device__ void run_one(Make problem, const Shape sh, const uint32_t tmem_cols, Finish finish) {
     __shared__ Control c;
-    with_set_up<false, P>(problem, c, tmem_cols, [&](const P &p, char *ring, uint32_t tmem, int warp, bool &ok) {
+    with_set_up<P>(problem, c, tmem_cols, [&](const P &p, char *ring, uint32_t tmem, int warp, bool &ok) {
         if (warp == 0) ok = load_a(p, c, smem_addr(ring), sh);
-        else if (warp == 1) ok = load_b<false>(p, c, smem_addr(ring), sh);
+        else if (warp == 1) ok = load_b<false>(p, c, smem_addr(ring), nullptr, sh);
         else if (warp == 2) ok = multiply(p, c, smem_addr(ring), sh, tmem);
         __syncwarp();
         finish(p, c, ring, tmem, ok);

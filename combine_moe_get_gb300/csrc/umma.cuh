@@ -1,6 +1,6 @@
 // umma.cuh -- tensor-core and tensor-copy building blocks for sm_103a as inline
 // PTX: tensor maps (host), TMA tile and gather loads, tensor memory, and
-// tcgen05 matrix products with operands in shared or tensor memory.
+// tcgen05 matrix products with operands in shared memory.
 #pragma once
 
 #include <cstdint>
@@ -110,12 +110,6 @@ __device__ __forceinline__ void tmem_load_wait(float (&v)[N]) {
     for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
 
-__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t *r) {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
-                 ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]));
-}
-__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
 // ------------------------------------------------------------------ matrix products
 
 // One lane of a converged warp.
@@ -130,33 +124,33 @@ __device__ __forceinline__ bool elect_one() {
 // than a small product (80 cycles each, measured).
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-// Shared-memory operand: rows of 128 bytes (64 bf16 along K) under the 128-byte
-// swizzle, groups of 8 rows 1024 bytes apart; the 16-wide K steps of one row
-// are 32 bytes apart. The low word holds the address, the high one is constant.
+// Shared-memory operand: rows of 128 bytes (64 bf16 or 128 E4M3 along K) under the
+// 128-byte swizzle, groups of 8 rows 1024 bytes apart; the steps of one product
+// along K (16 bf16, 32 E4M3) are 32 bytes apart. The low word holds the address, the high one is constant.
 __device__ __forceinline__ uint32_t operand_low(uint32_t addr) { return ((addr >> 4) & 0x3fff) | 1u << 16; }
 __device__ __forceinline__ uint64_t operand_desc(uint32_t low) {
     constexpr uint32_t kHigh = (1024 >> 4) | 1u << 14 | 2u << 29;
     return (uint64_t)kHigh << 32 | low;
 }
 
-// bf16 x bf16 -> fp32, 128 rows of A, n rows of B (a multiple of 16, 16..256), both K-major.
-__device__ __forceinline__ uint32_t product_desc(int n) {
-    return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+// bf16 x bf16 or E4M3 x E4M3 -> fp32, 128 rows of A, n rows of B (a multiple of 16, 16..256), both K-major.
+__device__ __forceinline__ uint32_t product_desc(int n, bool e4m3 = false) {
+    return 1u << 4 | (e4m3 ? 0 : 1u << 7 | 1u << 10) | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
 }
 
-// d (+)= A B^T over 16 columns of K, A in shared memory. By one lane of the warp.
+// d (+)= A B^T over 16 columns of bf16. By one lane of the warp.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t desc, bool add) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
         ::"r"(d), "l"(operand_desc(a_low)), "l"(operand_desc(b_low)), "r"(desc), "r"((uint32_t)add) : "memory");
 }
-// ... A in tensor memory (lane = row, two bf16 to a column).
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_low, uint32_t desc, bool add) {
+// ... over 32 columns of E4M3.
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t desc, bool add) {
     asm volatile(
         "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-        ::"r"(d), "r"(a), "l"(operand_desc(b_low)), "r"(desc), "r"((uint32_t)add) : "memory");
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(operand_desc(a_low)), "l"(operand_desc(b_low)), "r"(desc), "r"((uint32_t)add) : "memory");
 }
 // One arrival on `bar` when this lane's products so far are complete.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {

@@ -436,6 +436,7 @@ enum {
     MOE_TRACE_ADAPTER_SHRINK = 18,
     MOE_TRACE_ADAPTER_SORT = 19,
     MOE_TRACE_ADAPTER_EXPAND = 20,
+    MOE_TRACE_EXPERTS_SPLIT = 21,
     MOE_TRACE_PHASE = 0x10000          /* warp field of a per-CTA phase record: MOE_TRACE_PHASE + phase */
 };
 
