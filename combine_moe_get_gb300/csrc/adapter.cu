@@ -8,12 +8,14 @@
 // with zero in another row's. Two ways to do that, in two or three kernels:
 //
 // Grouped (many rows to an adapter): the plan kernel sorts the rows by adapter,
-// rows without one last, and cuts groups of one adapter; the sort kernel copies
-// x in that order. The projection runs
-// skinny.cuh's body over two lines: phase 0 multiplies a group's x rows by its A
-// into v, phase 1 multiplies them by W and then, as more K blocks of the same
-// sums, v by B. v is held as the sum of two bf16 (16 bits of it), the operands
-// of two products.
+// rows without one last, each adapter's from a multiple of 16 places on, and the
+// sort kernel copies x to those places. The projection runs skinny.cuh's body
+// over two lines: phase 0 multiplies the rows of one adapter in a tile (a piece)
+// by its A into v; phase 1 multiplies a tile's rows by W, whatever their adapters,
+// and then, as more K blocks of the same sums but of the piece's columns alone,
+// each piece's v by its B. v is held as the sum of two bf16 (16 bits of it), the
+// operands of two products. (Tiles of one adapter each ran W over 1.4 times as
+// many tiles with 4096 rows of 16 adapters in runs: 312 us in all.)
 //
 // Row by row (few rows to an adapter): the shrink kernel makes v in fp32, four
 // warps to a row of A, the expand kernel B v in fp32, a thread to a row of B, and
@@ -23,6 +25,7 @@
 // 103 MB of W.
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <mutex>
 #include <cuda_bf16.h>
 
@@ -33,34 +36,69 @@ namespace {
 
 using skinny::kRows;
 
-// Row by row costs two passes over the adapters for every row, of A through
-// the caches (some 4 TB/s) and of B (some 10^13 products a second);
-// grouped costs another pass over W for every group that is not full, about
-// (L + 1) / 2 of them at some 10 TB/s from L2, and some 25 us of sorting and
-// hand-over. In units of 0.1 ps:
+// Places of the sorted rows: each adapter's (and those without one) begin at a multiple of 16.
+int places(int T, int L) { return T + (skinny::kPlaceStep - 1) * std::min(L + 1, T); }
+
+// Which way is faster, and how wide the grouped way's tiles are, by estimates in
+// microseconds. They need not know the device: a workspace's size depends on them.
+// A block of a tile takes its bytes of A and B at a CTA's share of what L2 gives
+// them all, some 12.7 TB/s, or the tensor core's time for its columns.
+constexpr double kCtas = 152;
+double block_us(double ctas, int cols) {
+    return std::max((2 * skinny::kHalf + cols * 128) * ctas / 12.7e6, cols * 2.2e-3);
+}
+// Row by row: passes over the adapters for every row, of A through the caches
+// (some 4 TB/s) and of B (some 10^13 products a second), and W.
+double row_us(int T, int K, int N, int r) {
+    const double tiles = (double)((T + 127) / 128) * ((N + 2 * kRows - 1) / (2 * kRows)), kbs = (K + 63) / 64;
+    return 15 + 1e-7 * T * r * (5.0 * K + N) +
+           (tiles < kCtas ? tiles / kCtas : std::ceil(tiles / kCtas)) * kbs * block_us(kCtas, 128);
+}
+// Grouped: the plan and the copy of x, v by pieces, and then W (whole tiles, or
+// few ones shared) with B's blocks for each piece of each tile. Half of the steps
+// between adapters is padding.
+double grouped_us(int T, int K, int N, int L, int r, int cols) {
+    const double sets = std::min(L + 1, T), kbs = (K + 63) / 64, features = (N + 2 * kRows - 1) / (2 * kRows);
+    const double rows = std::ceil((T + skinny::kPlaceStep / 2 * sets) / cols), tiles = rows * features;
+    const double pieces = sets + rows, extra = pieces * features * 2 * ((r + 63) / 64);
+    const double share = 2 * tiles <= kCtas ? std::floor(kCtas / tiles) : 1;
+    const double block = block_us(std::min(kCtas, tiles * share), cols);
+    const double w = std::ceil(tiles / kCtas) * kbs / share + extra / std::min(kCtas, tiles * share);
+    return 40 + T * 4e-6 * K / 7 + pieces * kbs / kCtas * 0.4 + w * block + (share > 1 ? 0.05 * cols : 0);
+}
+int grouped_columns(int T, int K, int N, int L, int r) {
+    const int cols = grouped_us(T, K, N, L, r, 256) < grouped_us(T, K, N, L, r, 128) ? 256 : 128;
+    return std::min((places(T, L) + 15) / 16 * 16, cols);
+}
+// Measured with 152 CTAs, row by row against grouped (us): 1024 rows of 8 adapters,
+// 4096 x 4096, rank 16 71 : 65, rank 128 338 : 68; of 128 adapters, rank 16 78 : 115.
+// Tiles of 128 columns against 256: 4096 rows of 16 adapters, 7168 x 4096 294 : 234;
+// 1024 rows of 8 adapters, 4096 x 4096 65 : 110.
 bool grouped(int T, int K, int N, int L, int r) {
     if ((int64_t)T * N > (int64_t)1 << 26) return true;   // no fp32 copy of a large output
-    return (double)T * r * (5.0 * K + N) > 2.5e8 + (double)std::min(L + 1, T) * N * K;
+    return std::min(grouped_us(T, K, N, L, r, 128), grouped_us(T, K, N, L, r, 256)) < row_us(T, K, N, r);
 }
 
-int grouped_columns(int T) { return std::min((T + 15) / 16 * 16, 128); }
-
 struct Space {
-    size_t words, groups, order, v, x, partial, total;   // byte offsets
+    size_t words, groups, order, place, tiles, v, x, partial, total;   // byte offsets
 };
-constexpr int kReady = skinny::kWords;   // then a word per group: its v is done
+constexpr int kReady = skinny::kWords;   // then a word per tile of rows: its pieces' v are done
 
 Space space(int T, int K, int N, int L, int r) {
     Space s{};
     skinny::Cut cut;
-    s.v = cut.take((size_t)T * r * 4);   // fp32, or two bf16
     if (grouped(T, K, N, L, r)) {
-        s.words = cut.take(((size_t)kReady + T) * 4);
-        s.groups = cut.take((size_t)T * sizeof(int4));   // groups are at most as many as rows
-        s.order = cut.take((size_t)T * 4);
-        s.x = cut.take((size_t)T * K * 2);               // rows of x, sorted
-        s.partial = cut.take(skinny::partial_floats(2, grouped_columns(T)) * 4);
+        const int P = places(T, L), cols = grouped_columns(T, K, N, L, r), tiles = (P + cols - 1) / cols;
+        s.words = cut.take(((size_t)kReady + tiles) * 4);
+        s.groups = cut.take(((size_t)tiles + std::min(L + 1, T)) * sizeof(int4));
+        s.order = cut.take((size_t)P * 4);
+        s.place = cut.take((size_t)T * 4);
+        s.tiles = cut.take(((size_t)tiles + 1) * 4);
+        s.v = cut.take((size_t)P * r * 4);               // two bf16
+        s.x = cut.take((size_t)P * K * 2);               // rows of x, sorted
+        s.partial = cut.take(skinny::partial_floats(2, cols) * 4);
     } else {
+        s.v = cut.take((size_t)T * r * 4);               // fp32
         s.x = cut.take((size_t)T * N * 4);               // each row's B v
     }
     s.total = cut.at;
@@ -68,16 +106,17 @@ Space space(int T, int K, int N, int L, int r) {
 }
 
 struct AdapterArgs {
-    CUtensorMap w, a_map, b_map, x, v_map;   // x: `cols` rows a box, of x or of its sorted copy
+    CUtensorMap w, a_map, b_map, x, x16, v_map;   // x: `cols` rows a box (x16: 16), of x or of its sorted copy
     const float *scales;
     uint32_t *words;
-    const int4 *groups;
-    const int *order;
+    const int4 *groups;   // grouped: pieces
+    const int *order, *tile_pieces;
     void *v;   // grouped: v as two bf16; row by row: B v in fp32
     float *partials;
     __nv_bfloat16 *out;
     int32_t *status;
     int T, K, N, L, r;
+    int places;  // grouped: rows of the sorted copy
     int split;   // row by row: CTAs that share a tile
     skinny::Shape shape;
     uint32_t tmem_cols;
@@ -105,38 +144,40 @@ struct AdapterBase {
 struct SortArgs {
     const uint4 *x;
     uint4 *sorted;
-    const int *order;
-    int T, pieces;   // rows, 16-byte pieces of a row
+    const int *place;
+    int pieces;   // 16-byte pieces of a row
     TraceArgs trace;
 };
 
-// sorted[p] = x[order[p]], one CTA per row. (Gathering the rows by TMA in the
+// sorted[place[t]] = x[t], one CTA per row. (Gathering the rows by TMA in the
 // products' loads instead, four rows a copy, took 22 cycles a row: 2.5 times the
 // whole projection's time at 128 rows to a tile.)
 __global__ void __launch_bounds__(256) adapter_sort_kernel(const SortArgs s) {
     WarpTrace wt(s.trace, MOE_TRACE_ADAPTER_SORT);
     grid_dependency_wait();
     grid_launch_dependents();
-    const uint4 *from = s.x + (size_t)s.order[blockIdx.x] * s.pieces;
-    uint4 *to = s.sorted + (size_t)blockIdx.x * s.pieces;
+    const uint4 *from = s.x + (size_t)blockIdx.x * s.pieces;
+    uint4 *to = s.sorted + (size_t)s.place[blockIdx.x] * s.pieces;
 #pragma unroll 4
     for (int i = threadIdx.x; i < s.pieces; i += 256) to[i] = __ldg(from + i);
 }
 
-// Whole tiles up to this share of equal stretches: a shared tile of 128 columns is
-// 128 KB of partial sums from each CTA (4096 rows, 16 adapters: 243 us with equal
-// stretches).
-constexpr int kSlackGrouped = 130;
+// Shared tiles cost a CTA a hundred blocks' time or more: 256 KB of partial sums
+// and as much to read, and stretches that are not at the same columns of W, so
+// that L2 has to hold more of it (4096 rows of 16 adapters, 7168 x 4096: 299 us
+// with equal stretches, 234 with whole tiles). Whole tiles cost a tile's blocks less than one at most.
+constexpr int kWholeBlocks = 128, kSlackGrouped = 150;
 
 struct GroupedAdapter : AdapterBase {
-    static constexpr bool kAdders = true;
-    static constexpr int kReaders = 512;
-    int G, with_adapter;   // groups; those before it have an adapter
-    int more;              // K blocks of v's first part
+    static constexpr bool kShares = true, kAdders = false, kPieces = true;
+    static constexpr int kReaders = 512, kPhases = 2;
+    int pieces, row_tiles, rows;   // pieces with an adapter; tiles of rows, and their places
+    int more;                      // K blocks of v's first part
 
     __device__ explicit GroupedAdapter(const AdapterArgs &args) : AdapterBase(args) {
-        G = (int)a.words[skinny::kGroupsWord];
-        with_adapter = (int)a.words[skinny::kNamedWord];
+        pieces = (int)a.words[skinny::kNamedWord];
+        row_tiles = (int)a.words[skinny::kTilesWord];
+        rows = (int)a.words[skinny::kPlacesWord];
         more = (a.r + 63) / 64;
     }
 
@@ -147,29 +188,52 @@ struct GroupedAdapter : AdapterBase {
         return a.words + skinny::kArrivals + line * skinny::kMaxCtas + cta;
     }
 
+    // Phase 0: a segment's group is a piece, its set the adapter. Phase 1: its group is
+    // a tile of rows, its set the tile's first piece; the pieces' blocks follow W's in
+    // the last stretch of the tile.
     template <class F>
-    __device__ bool segments(F f, int first_phase = 0) const {
-        for (int phase = first_phase; phase < 2; ++phase) {
-            const skinny::Line line(phase == 0 ? with_adapter : (int64_t)G * tiles, phase == 0 ? kbs : kbs + 2 * more,
-                                    gridDim.x, kSlackGrouped);
+    __device__ bool segments(F f, int first_phase = 0, int end_phase = kPhases) const {
+        for (int phase = first_phase; phase < end_phase; ++phase) {
+            const skinny::Line line(phase == 0 ? pieces : (int64_t)row_tiles * tiles, kbs, gridDim.x,
+                                    kbs <= kWholeBlocks ? INT_MAX : kSlackGrouped);
             const bool ok = line.each(blockIdx.x, [&](int64_t tile, skinny::Segment &s) {
                 s.line = s.phase = phase;
-                s.group = phase == 0 ? (int)tile : (int)skinny::quotient(tile, tiles);
-                s.f = phase == 0 ? 0 : (int)(tile - (int64_t)s.group * tiles);
-                const int4 g = a.groups[s.group];
-                s.first = g.y;
-                s.n = g.z;
-                s.set = g.x;
+                if (phase == 0) {
+                    const int4 g = a.groups[tile];
+                    s.group = (int)tile;
+                    s.f = 0;
+                    s.set = g.x;
+                    s.first = g.y;
+                    s.n = g.z;
+                    s.row0 = g.x * a.r;
+                    s.b_from = INT_MAX;
+                } else {
+                    s.group = (int)skinny::quotient(tile, tiles);
+                    s.f = (int)(tile - (int64_t)s.group * tiles);
+                    s.set = a.tile_pieces[s.group];
+                    s.first = s.group * a.shape.cols;
+                    s.n = min(a.shape.cols, rows - s.first);
+                    s.row0 = s.f * 2 * kRows;
+                    s.b_from = kbs;
+                    const int extra = tile_pieces(s) * 2 * more;
+                    if (s.kb1 == kbs) s.kb1 += extra;
+                    s.kbs += extra;
+                }
                 s.two = phase == 1;
-                s.row0 = phase == 0 ? g.x * a.r : s.f * 2 * kRows;
                 s.row1 = s.row0 + kRows;
-                s.b_from = phase == 1 && g.x < a.L ? kbs : INT_MAX;
                 return f(s);
             });
             if (!ok) return false;
         }
         return true;
     }
+    __device__ int tile_pieces(const skinny::Segment &s) const {
+        return max(0, min(a.tile_pieces[s.group + 1], pieces) - s.set);
+    }
+    // Block kb of phase 1, behind W's: v's first parts of a piece (more blocks), then its second ones.
+    __device__ int4 piece(const skinny::Segment &s, int kb) const { return a.groups[s.set + (kb - kbs) / 2 / more]; }
+    __device__ int v_block(int kb) const { return more == 1 ? 0 : (kb - kbs) & 1; }
+    __device__ int v_part(int kb) const { return more == 1 ? (kb - kbs) & 1 : (kb - kbs) >> 1 & 1; }
 
     __device__ void a_load(const skinny::Segment &s, int kb, uint32_t dst, uint64_t *bar, uint64_t policy) const {
         if (s.phase == 0) {
@@ -177,10 +241,9 @@ struct GroupedAdapter : AdapterBase {
             tma_load(dst, &a.a_map, kb * 64, s.row0, bar, policy);
             return;
         }
-        // rows behind the last adapter's B read as 0: groups without an adapter
         const bool is_w = kb < kbs;
         const CUtensorMap *map = is_w ? &a.w : &a.b_map;
-        const int col = is_w ? kb * 64 : (kb - kbs) % more * 64, row = is_w ? s.row0 : s.set * a.N + s.row0;
+        const int col = is_w ? kb * 64 : v_block(kb) * 64, row = is_w ? s.row0 : piece(s, kb).x * a.N + s.row0;
         mbar_arrive_expect_tx(bar, 2 * skinny::kHalf);
         tma_load(dst, map, col, row, bar, policy);
         tma_load(dst + skinny::kHalf, map, col, row + kRows, bar, policy);
@@ -188,19 +251,22 @@ struct GroupedAdapter : AdapterBase {
     struct Rows {};
     __device__ Rows b_rows(const skinny::Segment &, int) const { return Rows{}; }
     __device__ bool b_ready(const skinny::Segment &s) const {
-        return skinny::wait_count(a.words + kReady + s.group, skinny::kTileWeight);
+        return skinny::wait_count(a.words + kReady + s.group, skinny::kTileWeight * tile_pieces(s));
     }
     __device__ uint32_t b_bytes(const skinny::Segment &s, int kb) const {
-        return kb < kbs ? a.shape.cols * 128 : (s.n + 7) / 8 * 1024;
+        if (s.phase == 0) return s.n16() * 128;
+        return kb < kbs ? a.shape.cols * 128 : (piece(s, kb).z + 7) / 8 * 1024;
     }
     __device__ void b_load(const skinny::Segment &s, const Rows &, int kb, uint32_t dst, uint64_t *bar, uint64_t policy,
                            int lane) const {
-        if (kb < kbs) {
-            if (lane == 0) tma_load(dst, &a.x, kb * 64, s.first, bar, policy);   // the next groups' rows fill the box
-        } else if (8 * lane < s.n) {
-            // v's first parts [T, r], then the second ones; behind both, zeros for groups without an adapter
-            const int part = (kb - kbs) / more, row = s.set < a.L ? part * a.T + s.first + 8 * lane : 2 * a.T;
-            tma_load(dst + lane * 1024, &a.v_map, (kb - kbs) % more * 64, row, bar, policy);
+        if (s.phase == 0) {
+            if (16 * lane < s.n) tma_load(dst + lane * 2048, &a.x16, kb * 64, s.first + 16 * lane, bar, policy);
+        } else if (kb < kbs) {
+            if (lane == 0) tma_load(dst, &a.x, kb * 64, s.first, bar, policy);
+        } else {
+            const int4 g = piece(s, kb);   // v's first parts [places, r], then the second ones
+            if (8 * lane < g.z)
+                tma_load(dst + lane * 1024, &a.v_map, v_block(kb) * 64, v_part(kb) * a.places + g.y + 8 * lane, bar, policy);
         }
     }
 
@@ -223,26 +289,21 @@ struct GroupedAdapter : AdapterBase {
                     const float rest = x - __bfloat162float(hi);
                     const size_t at = (size_t)(s.first + col + j) * a.r + row;
                     v[at] = hi;
-                    v[(size_t)a.T * a.r + at] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
+                    v[(size_t)a.places * a.r + at] = __float2bfloat16_rn(isfinite(rest) ? rest : 0.0f);
                 }
                 return;
             }
             const int o = s.row0 + half * kRows + row;
             if (o >= a.N) return;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (col + j < s.n) a.out[(size_t)a.order[s.first + col + j] * a.N + o] = __float2bfloat16_rn(sums[j]);
+            for (int j = 0; j < 8; ++j) {
+                const int t = col + j < s.n ? a.order[s.first + col + j] : -1;
+                if (t >= 0) a.out[(size_t)t * a.N + o] = __float2bfloat16_rn(sums[j]);
+            }
         }
     };
-    // shared tiles of the last line are the readers': four times the threads, and nothing else left to do
-    __device__ bool adders_take(const skinny::Segment &s) const { return s.phase == 0; }
-    __device__ bool finish() const {
-        return segments([&](const skinny::Segment &s) {
-            return s.whole() || skinny::add_up<skinny::ReadersOf<GroupedAdapter>>(*this, a.shape, s);
-        }, 1);
-    }
     __device__ void tile_done(const skinny::Segment &s, uint32_t weight) const {
-        if (s.phase == 0) skinny::count_up(a.words + kReady + s.group, weight);
+        if (s.phase == 0) skinny::count_up(a.words + kReady + s.first / a.shape.cols, weight);
     }
 };
 
@@ -250,7 +311,7 @@ __global__ void __launch_bounds__(skinny::threads_of<GroupedAdapter>(), 1)
     adapter_grouped_kernel(const __grid_constant__ AdapterArgs a) {
     WarpTrace wt(a.trace, MOE_TRACE_ADAPTER);
     if (threadIdx.x == 0)
-        for (const CUtensorMap *m : {&a.w, &a.x, &a.a_map, &a.b_map, &a.v_map}) tma_prefetch_map(m);
+        for (const CUtensorMap *m : {&a.w, &a.x, &a.x16, &a.a_map, &a.b_map, &a.v_map}) tma_prefetch_map(m);
     skinny::run<false, GroupedAdapter>([&](char *) {
         grid_dependency_wait();
         return GroupedAdapter(a);
@@ -380,7 +441,7 @@ __global__ void __launch_bounds__(256) adapter_expand_kernel(const ExpandArgs e)
 // Where tiles are fewer than CTAs, a cluster of `split` CTAs shares a tile, each
 // with a stretch of K; else CTAs take whole tiles in turn.
 struct RowAdapter : AdapterBase {
-    static constexpr bool kAdders = false;
+    static constexpr bool kShares = false, kAdders = false, kPieces = false;
     static constexpr int kReaders = 256;
     int chunks;
     __device__ explicit RowAdapter(const AdapterArgs &args) : AdapterBase(args) {
@@ -597,22 +658,24 @@ int launch_adapter_linear(const AdapterLaunch &L) {
     char *ws = static_cast<char *>(L.workspace);
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
     const bool overlap = tuning().overlap != 0;
-    int cols = grouped_columns(T), split = 1;
+    const int P = places(T, L.num_adapters);
+    int cols = by_group ? grouped_columns(T, K, N, L.num_adapters, r) : 0, split = 1;
     if (!by_group) choose_tiles(T, K, N, cols, split);
 
     AdapterArgs a{};
     bool ok = make_tensor_map(&a.w, L.w, false, N, K, kRows) &&
-              make_tensor_map(&a.x, by_group ? ws + sp.x : L.x, false, T, K, cols);
+              make_tensor_map(&a.x, by_group ? ws + sp.x : L.x, false, by_group ? P : T, K, cols);
     if (by_group)
         ok = ok && make_tensor_map(&a.a_map, L.a, false, (uint64_t)L.num_adapters * r, K, r) &&
              make_tensor_map(&a.b_map, L.b, false, (uint64_t)L.num_adapters * N, r, kRows) &&
-             make_tensor_map(&a.v_map, ws + sp.v, false, (uint64_t)2 * T, r, 8);
+             make_tensor_map(&a.x16, ws + sp.x, false, P, K, 16) &&
+             make_tensor_map(&a.v_map, ws + sp.v, false, (uint64_t)2 * P, r, 8);
     if (!ok) return MOE_ERR_CUDA;
     a.scales = L.scales;
     a.v = ws + (by_group ? sp.v : sp.x);
     a.out = static_cast<__nv_bfloat16 *>(L.out);
     a.status = L.status;
-    a.T = T, a.K = K, a.N = N, a.L = L.num_adapters, a.r = r, a.split = split;
+    a.T = T, a.K = K, a.N = N, a.L = L.num_adapters, a.r = r, a.places = P, a.split = split;
     a.shape = skinny::Shape::of(cols, false);
     a.tmem_cols = a.shape.tmem_cols(false);
     a.trace = trace_args();
@@ -622,13 +685,16 @@ int launch_adapter_linear(const AdapterLaunch &L) {
         a.words = reinterpret_cast<uint32_t *>(ws + sp.words);
         a.groups = reinterpret_cast<const int4 *>(ws + sp.groups);
         a.order = reinterpret_cast<const int *>(ws + sp.order);
+        a.tile_pieces = reinterpret_cast<const int *>(ws + sp.tiles);
         a.partials = reinterpret_cast<float *>(ws + sp.partial);
-        const skinny::PlanArgs<int32_t> plan{L.adapter_idx, T, L.num_adapters, true, cols, a.words, kReady + T,
-                                             const_cast<int4 *>(a.groups), const_cast<int *>(a.order),
+        int *const place = reinterpret_cast<int *>(ws + sp.place);
+        const skinny::PlanArgs<int32_t> plan{L.adapter_idx, T, L.num_adapters, true, cols, a.words,
+                                             kReady + (P + cols - 1) / cols, const_cast<int4 *>(a.groups),
+                                             const_cast<int *>(a.order), place, const_cast<int *>(a.tile_pieces),
                                              MOE_ERR_BAD_ADAPTER, L.status, a.trace};
-        const int rc = skinny::launch_plan(plan, s);
+        const int rc = skinny::launch_plan<true>(plan, s);
         if (rc != MOE_OK) return rc;
-        const SortArgs so{static_cast<const uint4 *>(L.x), reinterpret_cast<uint4 *>(ws + sp.x), a.order, T, K / 8, a.trace};
+        const SortArgs so{static_cast<const uint4 *>(L.x), reinterpret_cast<uint4 *>(ws + sp.x), place, K / 8, a.trace};
         if (launch_kernel(adapter_sort_kernel, dim3(T), dim3(256), 0, s, overlap, so) != cudaSuccess) return MOE_ERR_CUDA;
         return skinny::launch_resident(adapter_grouped_kernel, a, skinny::threads_of<GroupedAdapter>(), smem, s);
     }

@@ -111,7 +111,7 @@ template <bool kE4m3, int kCols>   // kCols: the most columns of a tile
 struct ExpertsProblem {
     static constexpr int kSteps = kCols / 8;   // E4M3
     static_assert(kSteps > 0);
-    static constexpr bool kHalves = false, kAdders = true, kCodes = kE4m3;
+    static constexpr bool kHalves = false, kShares = true, kAdders = true, kCodes = kE4m3, kPieces = false;
     static constexpr int kReaders = kE4m3 ? 256 : 512;
     using Readers = skinny::ReadersOf<ExpertsProblem>;
     const ExpertsArgs &a;
@@ -302,7 +302,6 @@ struct ExpertsProblem {
             }
         }
     };
-    __device__ bool adders_take(const skinny::Segment &) const { return true; }
     __device__ uint64_t *done() const { return reinterpret_cast<uint64_t *>(a.words + skinny::kDoneWord); }
     __device__ void tile_done(const skinny::Segment &s, uint32_t weight) const {
         if (s.phase == 0) skinny::count_up(a.words + kReady + s.group, weight);
@@ -458,9 +457,9 @@ int launch_experts(const ExpertsLaunch &L, bool words_are_zero) {
     const bool overlap = tuning().overlap != 0;
     if (!a.local) {
         const skinny::PlanArgs<int64_t> plan{L.topk_idx, T * k, E, false, cols, a.words, kReady + T * k,
-                                             const_cast<int4 *>(a.groups), const_cast<int *>(a.order),
+                                             const_cast<int4 *>(a.groups), const_cast<int *>(a.order), nullptr, nullptr,
                                              MOE_ERR_BAD_TOPK, L.status, a.trace};
-        const int rc = skinny::launch_plan(plan, s);
+        const int rc = skinny::launch_plan<false>(plan, s);
         if (rc != MOE_OK) return rc;
     } else if (!words_are_zero && !e4m3) {
         if (launch_kernel(skinny::clear_kernel, dim3(1), dim3(1024), 0, s, overlap, a.words, kReady + T * k) != cudaSuccess)

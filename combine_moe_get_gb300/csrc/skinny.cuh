@@ -12,9 +12,10 @@
 // result does not depend on the arrival order.
 //
 // Roles of a CTA's warps: 0 loads A (weights), 1 loads B (activations), 2 issues
-// the products, 3 owns the tensor memory and announces results to other CTAs, the next 8 or 16 (P::kReaders) read the
-// sums, and where tiles are shared through the workspace (P::kAdders) 4 more add
-// those up while the others go on.
+// the products, 3 owns the tensor memory and announces results to other CTAs, and
+// the next 8 or 16 (P::kReaders) read the sums. Tiles shared through the workspace
+// (P::kShares) are added up by 4 more warps while the others go on (P::kAdders), or
+// by the readers at the end of each phase.
 //   bf16 weights: A and B from shared memory; sums stay in tensor memory for a
 //     whole stretch of K, double-buffered, so that the readers' work on one
 //     tile runs under the next tile's products.
@@ -61,7 +62,7 @@ struct Segment {
     int row0, row1;       // weight rows of the two products
     bool two;             // both products (else the first alone)
     int kb0, kb1, kbs;    // K blocks [kb0, kb1) of the tile's kbs
-    int b_from;           // first K block whose B the problem has to wait for
+    int b_from;           // first K block whose B the problem has to wait for (P::kPieces: and that is a piece's)
     int n;                // columns in use
     int line, phase, f, group, set, first;   // which tile: line and phase, feature tile, group, its weight set and first row
     int cta0, parts;      // the CTAs that share the tile: cta0 .. cta0 + parts - 1
@@ -142,13 +143,13 @@ static_assert(kMaxStages + kMaxSums < kScaleSlots, "a place may be in use when i
 // or six blocks of 32 KB; with four the stream was 10% slower), those of B come
 // from L2 and are smaller.
 struct Shape {
-    int cols;      // columns a tile may have: a multiple of 16, at most 128 (E4M3: 64)
+    int cols;      // columns a tile may have: a multiple of 16, at most 256 (E4M3: 64)
     int a_stages, b_stages;
     __host__ __device__ static constexpr int b_bytes(int cols, bool e4m3) { return cols * (e4m3 ? 256 : 128); }
     static Shape of(int cols, bool e4m3, int budget = kSmemBudget) {
         if (e4m3) budget -= kScaleBytes;
         const int b = b_bytes(cols, e4m3);
-        const int a_stages = 3 * b <= budget - 6 * 2 * kHalf ? 6 : 5;
+        const int a_stages = 3 * b <= budget - 6 * 2 * kHalf ? 6 : cols <= 128 ? 5 : 4;
         const int b_stages = (budget - a_stages * 2 * kHalf) / b;
         return Shape{cols, a_stages, b_stages < kMaxStages ? b_stages : kMaxStages};
     }
@@ -158,11 +159,12 @@ struct Shape {
     size_t smem(bool e4m3) const { return 1024 + (size_t)used_bytes(e4m3); }
     __device__ uint32_t a_at(int slot) const { return slot * 2 * kHalf; }
     __device__ uint32_t b_at(int slot, bool e4m3) const { return a_stages * 2 * kHalf + slot * b_bytes(cols, e4m3); }
-    // bf16: two tiles' sums of 2 `cols` columns; E4M3: kMaxSums blocks' of twice as many, or two
+    // bf16: two tiles' sums of 2 `cols` columns, or one's where two do not fit; E4M3: kMaxSums blocks' of twice as many, or two
+    __host__ __device__ int sums() const { return cols <= 128 ? 2 : 1; }
     int tmem_cols(bool e4m3) const {
         if (e4m3) return 512;
         int c = 32;
-        while (c < 4 * cols) c *= 2;
+        while (c < 2 * sums() * cols) c *= 2;
         return c;
     }
 };
@@ -324,7 +326,7 @@ __device__ bool load_b(const P &p, Control &c, uint32_t ring_base, float *scales
 template <class P>
 __device__ bool multiply(const P &p, Control &c, uint32_t ring_base, const Shape sh, uint32_t tmem) {
     const bool mine = elect_one();
-    Ring ra(sh.a_stages), rb(sh.b_stages), sums(2);
+    Ring ra(sh.a_stages), rb(sh.b_stages), sums(sh.sums());
     const bool ok = p.segments([&](const Segment &s) {
         const uint32_t buf = sums.slot;
         const uint32_t desc = uniform(product_desc(s.n16())), d0 = uniform(tmem + buf * 2 * sh.cols);
@@ -338,12 +340,19 @@ __device__ bool multiply(const P &p, Control &c, uint32_t ring_base, const Shape
             const uint32_t a = uniform(operand_low(ring_base + sh.a_at(ra.slot)));
             const uint32_t b = uniform(operand_low(ring_base + sh.b_at(rb.slot, false)));
             const bool more = uniform(kb > s.kb0) != 0;
+            uint32_t columns = desc, at = 0;
+            if constexpr (P::kPieces)
+                if (kb >= s.b_from) {   // a block of some of the tile's columns
+                    const int4 piece = p.piece(s, kb);
+                    columns = uniform(product_desc((piece.z + 15) & ~15));
+                    at = uniform(piece.y - s.first);
+                }
             if (mine) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) mma_ss(d0, a + 2 * k, b + 2 * k, desc, more || k > 0);
+                for (int k = 0; k < 4; ++k) mma_ss(d0 + at, a + 2 * k, b + 2 * k, columns, more || k > 0);
                 if (two)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mma_ss(d1, a + (kHalf >> 4) + 2 * k, b + 2 * k, desc, more || k > 0);
+                    for (int k = 0; k < 4; ++k) mma_ss(d1 + at, a + (kHalf >> 4) + 2 * k, b + 2 * k, columns, more || k > 0);
                 mma_commit(&c.empty_a[ra.slot]);
                 mma_commit(&c.empty_b[rb.slot]);
             }
@@ -471,6 +480,7 @@ struct Share {
 // This CTA's part of a tile that it shares: fp32 partial sums to the workspace, [half][column][row].
 template <class P, class Each>
 __device__ void leave_part(const P &p, const Shape sh, const Segment &s, const Share<P::kHalves> me, Each each) {
+    if (P::kHalves && !s.two && (me.side & 1)) return;
     const size_t half = (size_t)sh.cols * kRows;
     float *mine = p.partial(s.line, blockIdx.x, s.kb0 > 0 ? 0 : 1) + me.row;
     each([&](int col, const float *v) {
@@ -486,7 +496,8 @@ __device__ void leave_part(const P &p, const Shape sh, const Segment &s, const S
 template <class Tm, class P>
 __device__ bool add_up(const P &p, const Shape sh, const Segment &s) {
     constexpr int kSides = Tm::count / 128;
-    const int units = P::kHalves ? 2 * ((s.n + 7) / 8) : (s.n + 3) / 4;
+    const int skip = P::kHalves && !s.two ? 2 : 1;   // the first half's units alone
+    const int units = P::kHalves ? (s.n + 7) / 8 * 2 / skip : (s.n + 3) / 4;
     const int shares = min(s.parts, (units + kSides - 1) / kSides), me = blockIdx.x - s.cta0;
     if (me >= shares) return true;
     bool ok = true;
@@ -496,8 +507,8 @@ __device__ bool add_up(const P &p, const Shape sh, const Segment &s) {
     // unit: side unit % 4 of the 16 columns unit / 4; each of the team's groups of 128 threads takes one at a time
     for (int unit = me * kSides + Tm::warp() / 4; unit < units; unit += s.parts * kSides) {
         Share<P::kHalves> share = Share<P::kHalves>::of(Tm::warp());
-        share.side = unit & 3;
-        const int col = (unit >> 2) * 16 + share.first_col();
+        share.side = unit * skip & 3;
+        const int col = (unit * skip >> 2) * 16 + share.first_col();
         // 32 loads at once, of four parts or eight: a trip to another SM's sums in L2 takes about a microsecond
         float v[8] = {};
         auto batch = [&](auto parts_at_once, int i0, int j0) {
@@ -543,14 +554,14 @@ __device__ bool add_up(const P &p, const Shape sh, const Segment &s) {
 template <class P, class Each, class Release>
 __device__ bool take(const P &p, Control &c, const Shape sh, const Segment &s, const Share<P::kHalves> me, Each each,
                      Release release) {
-    if (P::kAdders && !s.whole()) {
-        if constexpr (P::kAdders) leave_part(p, sh, s, me, each);
+    if (P::kShares && !s.whole()) {
+        if constexpr (P::kShares) leave_part(p, sh, s, me, each);
     } else {
         typename P::Emit emit(p, s, me);
         each([&](int col, const float *v) { emit(col, v); });
     }
     release();
-    if constexpr (P::kAdders) {
+    if constexpr (P::kShares) {
         __syncwarp();
         if ((threadIdx.x & 31) == 0)
             asm volatile("red.release.cta.shared::cta.add.u32 [%0], 1;" ::"r"(smem_addr(&c.written)) : "memory");
@@ -579,9 +590,10 @@ __device__ bool announce(const P &p, Control &c) {
     });
 }
 
-template <class P>
-__device__ bool add_shared(const P &p, Control &c, const Shape sh) {
-    return p.segments([&](const Segment &s) { return s.whole() || !p.adders_take(s) || add_up<AddersOf<P>>(p, sh, s); });
+// A CTA's shared tiles (of one phase, by the readers), all of whose parts it has left or will leave.
+template <class Tm, class P, class... Phase>
+__device__ bool add_shared(const P &p, const Shape sh, Phase... phase) {
+    return p.segments([&](const Segment &s) { return s.whole() || add_up<Tm>(p, sh, s); }, phase...);
 }
 
 // Readers of bf16 weights' sums.
@@ -590,8 +602,13 @@ __device__ bool read_sums(const P &p, Control &c, const Shape sh, uint32_t tmem)
     using Tm = ReadersOf<P>;
     const int lane = threadIdx.x & 31;
     const Share<P::kHalves> me = Share<P::kHalves>::of(Tm::warp());
-    Ring sums(2);
-    return p.segments([&](const Segment &s) {
+    Ring sums(sh.sums());
+    constexpr bool kAdd = P::kShares && !P::kAdders;
+    int phase = 0;
+    bool ok = p.segments([&](const Segment &s) {
+        if constexpr (kAdd)
+            for (; phase < s.phase; ++phase)
+                if (!add_shared<Tm>(p, sh, phase, phase + 1)) return false;
         const uint32_t buf = sums.slot;
         if (!Tm::agree(wait(&c.sums_full[buf], sums.round))) return false;
         tc_fence_after();
@@ -611,6 +628,9 @@ __device__ bool read_sums(const P &p, Control &c, const Shape sh, uint32_t tmem)
         sums.next();
         return take(p, c, sh, s, me, each, release);
     });
+    if constexpr (kAdd)
+        for (; ok && phase < P::kPhases; ++phase) ok = add_shared<Tm>(p, sh, phase, phase + 1);
+    return ok;
 }
 
 // Readers of E4M3 weights' sums: each block's, scaled, into registers; tiles of up to 8 kSteps columns.
@@ -738,10 +758,10 @@ __device__ void run(Make problem, const Shape sh, const uint32_t tmem_cols) {
             if constexpr (kE4m3) ok = multiply_e4m3(p, c, smem_addr(ring), sh, tmem);
             else ok = multiply(p, c, smem_addr(ring), sh, tmem);
         } else if (warp == 3) {
-            if constexpr (P::kAdders)
+            if constexpr (P::kShares)
                 if ((threadIdx.x & 31) == 0) ok = announce(p, c);
         } else if (threadIdx.x >= AddersOf<P>::first) {
-            if constexpr (P::kAdders) ok = add_shared(p, c, sh);
+            if constexpr (P::kAdders) ok = add_shared<AddersOf<P>>(p, sh);
         } else if (threadIdx.x >= ReadersOf<P>::first) {
             if constexpr (kE4m3) ok = read_sums_e4m3<P::kSteps>(p, c, scales, sh, tmem);
             else ok = read_sums(p, c, sh, tmem);
@@ -766,12 +786,17 @@ __device__ void run_one(Make problem, const Shape sh, const uint32_t tmem_cols, 
 
 // Words at the head of a workspace: groups (and those of a named set), finished
 // tiles (64 bits), arrivals of parts by line and CTA.
-constexpr int kGroupsWord = 0, kNamedWord = 1, kDoneWord = 2, kArrivals = 4, kWords = 4 + kMaxLines * kMaxCtas;
+// or of a plan in tiles their number and that of its places.
+constexpr int kGroupsWord = 0, kNamedWord = 1, kDoneWord = 2, kTilesWord = 2, kPlacesWord = 3, kArrivals = 4,
+              kWords = 4 + kMaxLines * kMaxCtas;
 
 // ------------------------------------------------------------------ plan
 
 // Sorts entries by the weight set that they name and cuts each set's into groups
-// of at most `cols`; clears the counters of the kernel behind it.
+// of at most `cols`; clears the counters of the kernel behind it. In tiles
+// (kTiles): each set begins at a multiple of 16 places, and groups end where
+// tiles of `cols` places do, so that a tile consists of whole groups.
+constexpr int kPlaceStep = 16;   // the tensor core's step of columns
 template <typename Index>
 struct PlanArgs {
     const Index *idx;        // [n], -1: none
@@ -781,7 +806,9 @@ struct PlanArgs {
     uint32_t *words;         // the numbers of groups and of those with a set that is named; the rest become 0
     int num_words;
     int4 *groups;            // {set, first sorted entry, entries, 0}
-    int *order;              // sorted entries
+    int *order;              // sorted entries, in tiles -1 in the places between them
+    int *place;              // in tiles: each entry's place
+    int *tiles;              // in tiles: each tile's first group, then the number of groups
     int bad;                 // status of an index out of range
     int32_t *status;
     TraceArgs trace;
@@ -790,14 +817,14 @@ struct PlanArgs {
 constexpr int kPlanThreads = 1024;
 
 // Warps that sort, each a stretch of the entries with counters of its own, and
-// the shared memory that they take.
-inline int plan_warps(int sets) { return std::max(1, std::min(kPlanThreads / 32, (160 << 10) / (4 * sets))); }
-inline size_t plan_smem(int sets) { return ((size_t)plan_warps(sets) + 2) * (sets + 1) * 4; }
+// the shared memory that they and the three sums over the sets take.
+inline int plan_warps(int sets) { return std::max(1, std::min(kPlanThreads / 32, (220 << 10) / (4 * (sets + 1)) - 3)); }
+inline size_t plan_smem(int sets) { return ((size_t)plan_warps(sets) + 3) * (sets + 1) * 4; }
 
 // Sets in order, entries of a set in their own order: where entries change
 // places between groups, their sums are cut elsewhere and may round otherwise, so
 // the same choice has to give the same groups.
-template <typename Index>
+template <typename Index, bool kTiles>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Index> a, const int warps) {
     WarpTrace wt(a.trace, MOE_TRACE_PLAN);
     grid_dependency_wait();
@@ -805,8 +832,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Index
     extern __shared__ int32_t plan_memory[];
     const int sets = a.sets + (a.rest ? 1 : 0);
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    int32_t *start = plan_memory, *first_group = start + sets + 1;
-    int32_t *counts = first_group + sets + 1, *mine = counts + (size_t)warp * sets;   // [warps][sets]
+    int32_t *start = plan_memory, *first_group = start + sets + 1, *entries = first_group + sets + 1;
+    int32_t *counts = entries + sets + 1, *mine = counts + (size_t)warp * sets;   // [warps][sets]
     auto set_of = [&](Index e) { return e >= 0 && e < a.sets ? (int)e : a.rest ? a.sets : -1; };
     for (int i = threadIdx.x; i < warps * sets; i += kPlanThreads) counts[i] = 0;
     for (int i = threadIdx.x; i < a.num_words; i += kPlanThreads) a.words[i] = 0;
@@ -827,26 +854,50 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Index
             counts[(size_t)w * sets + e] = total;
             total += c;
         }
-        start[e] = total;
-        first_group[e] = (total + a.cols - 1) / a.cols;
+        entries[e] = total;
+        start[e] = kTiles ? (total + kPlaceStep - 1) / kPlaceStep * kPlaceStep : total;
+        if (!kTiles) first_group[e] = (total + a.cols - 1) / a.cols;
     }
     __syncthreads();
     if (warp == 0) warp_exclusive_scan(start, sets, lane);
-    else if (warp == 1) warp_exclusive_scan(first_group, sets, lane);
+    if constexpr (kTiles) {
+        __syncthreads();
+        for (int e = threadIdx.x; e < sets; e += kPlanThreads)
+            first_group[e] = entries[e] > 0 ? (start[e] + entries[e] - 1) / a.cols - start[e] / a.cols + 1 : 0;
+        __syncthreads();
+    }
+    if (warp == 1) warp_exclusive_scan(first_group, sets, lane);
     __syncthreads();
     for (int e = threadIdx.x; e < sets; e += kPlanThreads) {
-        const int last = start[e + 1];
-        for (int g = first_group[e], b = start[e]; b < last; ++g, b += a.cols)
-            a.groups[g] = make_int4(e, b, min(a.cols, last - b), 0);
+        const int last = start[e] + entries[e];
+        for (int g = first_group[e], b = start[e]; b < last; ++g) {
+            const int end = min(last, kTiles ? (b / a.cols + 1) * a.cols : b + a.cols);
+            a.groups[g] = make_int4(e, b, end - b, 0);
+            // the first group of a tile begins it: a set that begins elsewhere follows another's last entries
+            if (kTiles && b % a.cols == 0) a.tiles[b / a.cols] = g;
+            b = end;
+        }
+        if constexpr (kTiles)
+            for (int b = last; b < start[e + 1]; ++b) a.order[b] = -1;
     }
     if (threadIdx.x == 0) {
         a.words[kGroupsWord] = first_group[sets];
         a.words[kNamedWord] = first_group[a.sets];
+        if constexpr (kTiles) {
+            const int tiles = (start[sets] + a.cols - 1) / a.cols;
+            a.words[kTilesWord] = tiles;
+            a.words[kPlacesWord] = start[sets];
+            a.tiles[tiles] = first_group[sets];
+        }
     }
     for (int i0 = begin; i0 < end; i0 += 32) {
         const int i = i0 + lane, e = i < end ? set_of(a.idx[i]) : -1;
         const uint32_t same = __match_any_sync(0xffffffffu, e);
-        if (e >= 0) a.order[start[e] + mine[e] + __popc(same & ((1u << lane) - 1))] = i;
+        if (e >= 0) {
+            const int place = start[e] + mine[e] + __popc(same & ((1u << lane) - 1));
+            a.order[place] = i;
+            if constexpr (kTiles) a.place[i] = place;
+        }
         __syncwarp();
         if (e >= 0 && same >> lane == 1) mine[e] += __popc(same);   // the last of them
         __syncwarp();
@@ -942,13 +993,13 @@ static __global__ void __launch_bounds__(1024) clear_kernel(uint32_t *words, int
     for (int i = threadIdx.x; i < n; i += 1024) words[i] = 0;
 }
 
-template <typename Index>
+template <bool kTiles, typename Index>
 int launch_plan(const PlanArgs<Index> &a, cudaStream_t s) {
     const int sets = a.sets + (a.rest ? 1 : 0);
     const size_t smem = plan_smem(sets);
-    const int rc = ensure_dynamic_smem((const void *)plan_kernel<Index>, smem);
+    const int rc = ensure_dynamic_smem((const void *)plan_kernel<Index, kTiles>, smem);
     if (rc != MOE_OK) return rc;
-    return launch_kernel(plan_kernel<Index>, dim3(1), dim3(kPlanThreads), smem, s, tuning().overlap != 0, a,
+    return launch_kernel(plan_kernel<Index, kTiles>, dim3(1), dim3(kPlanThreads), smem, s, tuning().overlap != 0, a,
                          plan_warps(sets)) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

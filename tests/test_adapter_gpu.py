@@ -153,3 +153,48 @@ def test_adapter_gives_the_same_bits_every_time(moe):
     first = p.call(moe)
     for _ in range(5):
         assert torch.equal(p.call(moe), first)
+
+
+# Sorted by adapter: tiles of 128 and of 256 rows that several adapters share, ranks of
+# one and two blocks, more adapters than rows to a tile, tiles that CTAs share.
+TILED = [(4100, 264, 4104, 5, 64), (4100, 264, 4104, 40, 72), (5000, 64, 2056, 9, 128), (6000, 128, 4096, 200, 128),
+         (513, 1288, 1288, 2, 128), (20000, 64, 4096, 1000, 8), (1030, 2056, 1032, 30, 104), (2000, 8, 4096, 2, 128),
+         (600, 8200, 1064, 2, 128), (1100, 8328, 5000, 3, 64)]
+
+
+@pytest.mark.parametrize("spread", ["rows", "runs", "one"])
+@pytest.mark.parametrize("shape", TILED)
+def test_adapter_tiles_match_definition(moe, shape, spread):
+    p = Problem(*shape, spread=spread, seed=sum(shape))
+    status = moe.new_status()
+    need = moe.moe_adapter_linear_workspace_size(*shape)
+    ws = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device="cuda")
+    first = p.call(moe, workspace=ws[:need], status=status)
+    check(first, *p.reference())
+    assert torch.equal(p.call(moe, workspace=ws[:need], status=status), first)
+    assert bool((ws[need:] == 0xFF).all())
+    moe.check_status(status)
+
+
+@pytest.mark.parametrize("shape", [(4100, 264, 4104, 5, 64), (1030, 2056, 1032, 30, 104)])
+def test_adapter_in_a_tile_reaches_only_its_rows(moe, shape):
+    p = Problem(*shape, seed=7)
+    clean = p.call(moe)
+    p.a[2, 3, 5] = math.nan
+    p.b[2, 7] = math.inf
+    p.x[9, 1] = math.nan
+    p.x[33] = math.inf
+    got = p.call(moe)
+    keep = p.idx != 2
+    hit = p.idx == 2
+    keep[9] = keep[33] = False
+    assert torch.equal(got[keep], clean[keep])
+    assert bool(got[hit].isnan().all()) and bool(got[9].isnan().all())
+
+
+def test_adapter_tiles_report_an_index_out_of_range(moe):
+    p = Problem(4100, 264, 4104, 5, 64, seed=1)
+    p.idx[4], p.idx[5] = 5, -2
+    status = moe.new_status()
+    check(p.call(moe, status=status), *p.reference())
+    assert int(status.item()) == moe.MOE_ERR_BAD_ADAPTER
