@@ -4,7 +4,9 @@ Argument marshalling only: every function takes CUDA tensors, allocates the
 outputs it is not given with torch (device memory is torch's job here), and
 passes raw pointers, sizes and the current CUDA stream to the C entry point
 of the same name. All computation runs in the library's CUDA kernels; there
-is no CPU path. If the library cannot be built or loaded, import fails.
+is no CPU path. If the library cannot be built or loaded, import fails. The
+functions behind a router's logits are for calls so small that marshalling
+them in Python took longer than the call: theirs is csrc/marshal.cpp.
 
 Errors the host detects come back as ``MoeError``. Errors that depend on the
 data land in the int32 ``status`` tensor (first error wins; never cleared by
@@ -15,6 +17,8 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import dataclasses
+import importlib.machinery
+import importlib.util
 import os
 from typing import Optional
 
@@ -120,10 +124,20 @@ def _configure(lib):
     lib.moe_adapter_linear_workspace_size.restype = ctypes.c_size_t
     lib.moe_adapter_linear.argtypes = [_P, _I, _I, _P, _I, _P, _P, _P, _P, _I, _I, _P, _P, ctypes.c_size_t, _P, _P]
     lib.moe_adapter_linear.restype = _I
+    lib.entries = {name: ctypes.cast(getattr(lib, name), _P).value for name in
+                   ("moe_topk_gate", "moe_topk_gate_backward", "moe_experts", "moe_layer", "moe_adapter_linear")}
     return lib
 
 
+def _load_marshal():
+    loader = importlib.machinery.ExtensionFileLoader("_marshal", _build.build_marshal())
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+    loader.exec_module(module)
+    return module
+
+
 LIB = _load()
+_marshal = _load_marshal()
 
 
 @contextlib.contextmanager
@@ -466,16 +480,8 @@ MOE_LOGITS_BF16 = 1
 MOE_GATE_SOFTMAX = 0
 MOE_GATE_SIGMOID = 1
 MOE_GATE_NORMALIZE = 0x100
-
-
-def _logits_type(logits: torch.Tensor) -> int:
-    dtype = logits.dtype
-    if dtype == torch.float32:
-        return MOE_LOGITS_F32
-    if dtype != torch.bfloat16:
-        raise ValueError("the router's logits are float32 or bfloat16")
-    return MOE_LOGITS_BF16
-
+MOE_WEIGHTS_BF16 = 0
+MOE_WEIGHTS_E4M3 = 1
 
 _SCORES = {"softmax": MOE_GATE_SOFTMAX, "sigmoid": MOE_GATE_SIGMOID}
 
@@ -486,10 +492,8 @@ def _gate_mode(score: str, normalize: bool) -> int:
     return _SCORES[score] | (MOE_GATE_NORMALIZE if normalize else 0)
 
 
-def _typed(t: torch.Tensor, dtype: torch.dtype, shape: tuple, name: str) -> torch.Tensor:
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError(f"{name} is {dtype} {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
-    return t
+def _handle(stream: Optional[torch.cuda.Stream]) -> Optional[int]:
+    return None if stream is None else stream.cuda_stream
 
 
 def moe_topk_gate(logits: torch.Tensor, num_topk: int, *, bias: Optional[torch.Tensor] = None, score: str = "softmax",
@@ -500,18 +504,10 @@ def moe_topk_gate(logits: torch.Tensor, num_topk: int, *, bias: Optional[torch.T
     weights of each token from the router's ``logits`` [T, E] (fp32 or bf16):
     the k largest logits (or score + ``bias``), weighted by their softmax or
     sigmoid scores, normalised over the chosen ones if ``normalize``."""
-    T, E = logits.shape
-    dev = logits.device
-    topk_idx = (torch.empty(T, num_topk, dtype=torch.int64, device=dev) if topk_idx is None else
-                _typed(topk_idx, torch.int64, (T, num_topk), "topk_idx"))
-    topk_weights = (torch.empty(T, num_topk, dtype=torch.float32, device=dev) if topk_weights is None else
-                    _typed(topk_weights, torch.float32, (T, num_topk), "topk_weights"))
-    if bias is not None:
-        _typed(bias, torch.float32, (E,), "bias")
-    status = new_status(dev) if status is None else status
-    code = LIB.moe_topk_gate(_ptr(logits), _logits_type(logits), _ptr(bias), T, num_topk, E,
-                             _gate_mode(score, normalize), float(scale), _ptr(topk_idx), _ptr(topk_weights),
-                             _ptr(status), _stream(stream))
+    status = new_status(logits.device) if status is None else status
+    code, topk_idx, topk_weights = _marshal.topk_gate(
+        LIB.entries["moe_topk_gate"], logits, num_topk, bias, _gate_mode(score, normalize), scale, topk_idx,
+        topk_weights, status, _handle(stream))
     _check(code, "moe_topk_gate")
     return topk_idx, topk_weights
 
@@ -522,21 +518,11 @@ def moe_topk_gate_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_we
                            stream=None) -> torch.Tensor:
     """The gradient [T, E] (the logits' type) of moe_topk_gate's weights, given
     ``grad_weights`` [T, k] fp32; pass the same score, normalize and scale."""
-    T, E = logits.shape
-    k = topk_idx.shape[1]
-    _typed(topk_idx, torch.int64, (T, k), "topk_idx")
-    _typed(grad_weights, torch.float32, (T, k), "grad_weights")
-    out = torch.empty_like(logits) if out is None else _typed(out, logits.dtype, (T, E), "out")
     status = new_status(logits.device) if status is None else status
-    code = LIB.moe_topk_gate_backward(_ptr(logits), _logits_type(logits), _ptr(topk_idx), _ptr(grad_weights), T, k, E,
-                                      _gate_mode(score, normalize), float(scale), _ptr(out), _ptr(status),
-                                      _stream(stream))
+    code, out = _marshal.topk_gate_backward(LIB.entries["moe_topk_gate_backward"], logits, topk_idx, grad_weights,
+                                            _gate_mode(score, normalize), scale, out, status, _handle(stream))
     _check(code, "moe_topk_gate_backward")
     return out
-
-
-MOE_WEIGHTS_BF16 = 0
-MOE_WEIGHTS_E4M3 = 1
 
 
 def moe_experts_workspace_size(num_tokens: int, hidden: int, intermediate: int, num_topk: int,
@@ -544,23 +530,9 @@ def moe_experts_workspace_size(num_tokens: int, hidden: int, intermediate: int, 
     return int(LIB.moe_experts_workspace_size(num_tokens, hidden, intermediate, num_topk, num_experts))
 
 
-def _expert_weights(x, w13, w2, w13_scales, w2_scales):
-    """(T, H, I, E, weight type) of one layer's experts, after checking types and shapes."""
-    T, H = x.shape
-    E, _, I = w2.shape
-    e4m3 = w13.dtype == torch.uint8
-    dtype = torch.uint8 if e4m3 else torch.bfloat16
-    _typed(x, torch.bfloat16, (T, H), "x")
-    _typed(w13, dtype, (E, 2 * I, H), "w13")
-    _typed(w2, dtype, (E, H, I), "w2")
-    if e4m3:
-        if w13_scales is None or w2_scales is None:
-            raise ValueError("E4M3 weights need w13_scales and w2_scales")
-        _typed(w13_scales, torch.float32, (E, 2 * I, H // 128), "w13_scales")
-        _typed(w2_scales, torch.float32, (E, H, I // 128), "w2_scales")
-    elif w13_scales is not None or w2_scales is not None:
-        raise ValueError("bf16 weights take no scales")
-    return T, H, I, E, MOE_WEIGHTS_E4M3 if e4m3 else MOE_WEIGHTS_BF16
+def _experts_workspace(x, w2, num_topk):
+    n = moe_experts_workspace_size(x.shape[0], x.shape[1], w2.shape[2], num_topk, w2.shape[0])
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=x.device)
 
 
 def moe_experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor, w13: torch.Tensor,
@@ -571,17 +543,10 @@ def moe_experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Ten
     """out[t] = sum_j topk_weights[t, j] * w2[e] (silu(gate) * up), [gate; up] = w13[e] x[t] and
     e = topk_idx[t, j], for a few tokens (T <= 1024). Weights are bf16, or E4M3
     codes (uint8) with a scale per row and 128 columns."""
-    T, H, I, E, wtype = _expert_weights(x, w13, w2, w13_scales, w2_scales)
-    k = topk_idx.shape[1]
-    _typed(topk_idx, torch.int64, (T, k), "topk_idx")
-    _typed(topk_weights, torch.float32, (T, k), "topk_weights")
-    out = torch.empty_like(x) if out is None else _typed(out, torch.bfloat16, (T, H), "out")
-    if workspace is None:
-        workspace = torch.empty(max(moe_experts_workspace_size(T, H, I, k, E), 16), dtype=torch.uint8, device=x.device)
+    workspace = _experts_workspace(x, w2, topk_idx.shape[1]) if workspace is None else workspace
     status = new_status(x.device) if status is None else status
-    code = LIB.moe_experts(_ptr(x), T, H, _ptr(topk_idx), _ptr(topk_weights), k, E, _ptr(w13), _ptr(w13_scales),
-                           _ptr(w2), _ptr(w2_scales), I, wtype, _ptr(out), _ptr(workspace),
-                           workspace.nbytes, _ptr(status), _stream(stream))
+    code, out = _marshal.experts(LIB.entries["moe_experts"], x, w13, w2, w13_scales, w2_scales, topk_idx, topk_weights,
+                                 out, workspace, status, _handle(stream))
     _check(code, "moe_experts")
     return out
 
@@ -595,24 +560,11 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, num_topk: int, w13: torch.T
               stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """moe_topk_gate of ``logits`` [T, E] and moe_experts of the choice in one
     call. Returns (out, topk_idx, topk_weights)."""
-    T, H, I, E, wtype = _expert_weights(x, w13, w2, w13_scales, w2_scales)
-    dev = x.device
-    _typed(logits, logits.dtype, (T, E), "logits")
-    if bias is not None:
-        _typed(bias, torch.float32, (E,), "bias")
-    out = torch.empty_like(x) if out is None else _typed(out, torch.bfloat16, (T, H), "out")
-    topk_idx = (torch.empty(T, num_topk, dtype=torch.int64, device=dev) if topk_idx is None else
-                _typed(topk_idx, torch.int64, (T, num_topk), "topk_idx"))
-    topk_weights = (torch.empty(T, num_topk, dtype=torch.float32, device=dev) if topk_weights is None else
-                    _typed(topk_weights, torch.float32, (T, num_topk), "topk_weights"))
-    if workspace is None:
-        workspace = torch.empty(max(moe_experts_workspace_size(T, H, I, num_topk, E), 16), dtype=torch.uint8,
-                                device=dev)
-    status = new_status(dev) if status is None else status
-    code = LIB.moe_layer(_ptr(x), T, H, _ptr(logits), _logits_type(logits), _ptr(bias), num_topk, E,
-                         _gate_mode(score, normalize), float(scale), _ptr(topk_idx), _ptr(topk_weights), _ptr(w13),
-                         _ptr(w13_scales), _ptr(w2), _ptr(w2_scales), I, wtype, _ptr(out), _ptr(workspace),
-                         workspace.nbytes, _ptr(status), _stream(stream))
+    workspace = _experts_workspace(x, w2, num_topk) if workspace is None else workspace
+    status = new_status(x.device) if status is None else status
+    code, out, topk_idx, topk_weights = _marshal.layer(
+        LIB.entries["moe_layer"], x, w13, w2, w13_scales, w2_scales, logits, num_topk, bias,
+        _gate_mode(score, normalize), scale, topk_idx, topk_weights, out, workspace, status, _handle(stream))
     _check(code, "moe_layer")
     return out, topk_idx, topk_weights
 
@@ -629,22 +581,11 @@ def moe_adapter_linear(x: torch.Tensor, w: torch.Tensor, adapter_idx: torch.Tens
     """out[t] = w x[t] + scales[i] * b[i] (a[i] x[t]) with i = adapter_idx[t]
     (-1: no adapter). x [T, K], w [N, K], a [L, r, K], b [L, N, r] bf16;
     adapter_idx int32 [T]; scales fp32 [L]."""
-    T, K = x.shape
-    N = w.shape[0]
-    L, r, _ = a.shape
-    _typed(x, torch.bfloat16, (T, K), "x")
-    _typed(w, torch.bfloat16, (N, K), "w")
-    _typed(a, torch.bfloat16, (L, r, K), "a")
-    _typed(b, torch.bfloat16, (L, N, r), "b")
-    _typed(adapter_idx, torch.int32, (T,), "adapter_idx")
-    _typed(scales, torch.float32, (L,), "scales")
-    out = (torch.empty(T, N, dtype=torch.bfloat16, device=x.device) if out is None else
-           _typed(out, torch.bfloat16, (T, N), "out"))
     if workspace is None:
-        workspace = torch.empty(max(moe_adapter_linear_workspace_size(T, K, N, L, r), 16), dtype=torch.uint8,
-                                device=x.device)
+        n = moe_adapter_linear_workspace_size(*x.shape, w.shape[0], a.shape[0], a.shape[1])
+        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=x.device)
     status = new_status(x.device) if status is None else status
-    code = LIB.moe_adapter_linear(_ptr(x), T, K, _ptr(w), N, _ptr(adapter_idx), _ptr(a), _ptr(b), _ptr(scales), L, r,
-                                  _ptr(out), _ptr(workspace), workspace.nbytes, _ptr(status), _stream(stream))
+    code, out = _marshal.adapter_linear(LIB.entries["moe_adapter_linear"], x, w, adapter_idx, a, b, scales, out,
+                                        workspace, status, _handle(stream))
     _check(code, "moe_adapter_linear")
     return out

@@ -1,6 +1,7 @@
 """Build ``libmoe_get.so`` in place: nvcc for sm_103a, one object per .cu
 (compiled in parallel), linked against the shared CUDA runtime so that the
-library and PyTorch share one runtime instance in a process."""
+library and PyTorch share one runtime instance in a process. Also the Python
+module ``_marshal`` (csrc/marshal.cpp), by the host compiler against torch."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -8,6 +9,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -17,6 +19,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_get.so")
 # the same library compiled with MOE_PROFILE: every kernel warp records its start and end (moe_trace_enable)
 TRACE_LIB = os.path.join(HERE, "libmoe_get_trace.so")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -87,6 +90,30 @@ def build(force: bool = False, verbose: bool = False, defines: tuple = (), lib: 
 def build_trace(force: bool = False, verbose: bool = False) -> str:
     """libmoe_get_trace.so: the library compiled with MOE_PROFILE (per-warp timer records)."""
     return build(force, verbose, defines=("MOE_PROFILE=1",), lib=TRACE_LIB, build_dir=BUILD_DIR + "_trace")
+
+
+def build_marshal(force: bool = False) -> str:
+    """_marshal.so: argument marshalling of the small calls."""
+    src = os.path.join(CSRC, "marshal.cpp")
+    inputs = [src, os.path.join(INCLUDE, "moe_get.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in inputs):
+        return MARSHAL
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    includes = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(root, "include"),
+                os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
+    tmp = MARSHAL + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *(f"-I{d}" for d in includes), src, "-o", tmp, f"-L{os.path.join(root, 'lib')}", "-ltorch_python",
+           "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", f"-Wl,-rpath,{os.path.join(root, 'lib')}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MARSHAL)
+    return MARSHAL
 
 
 if __name__ == "__main__":
