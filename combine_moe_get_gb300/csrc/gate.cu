@@ -5,8 +5,9 @@
 // Mathematics. The chosen experts are the k largest logits (softmax and
 // sigmoid keep their order), or the k largest score + bias; ties go to the
 // lowest index. Logits are compared as they are, so a choice is exact: no
-// rounding takes part unless a bias is given. Exponentials are taken of differences to the largest logit (0 at the
-// maximum even when that is +inf), sums are fp32.
+// rounding takes part unless a bias is given. Exponentials are taken of
+// differences to the largest logit (0 at the maximum even when that is +inf), sums
+// are fp32.
 //
 // A warp handles a token: 32 lanes hold the row's E logits in registers (up to
 // 64 each), so that a row is read once (and a gradient's written once), each
@@ -15,6 +16,7 @@
 // one CTA per token with the keys in shared memory, and in the backward pass a
 // warp that reads the row three times.
 #include <algorithm>
+#include <cfloat>
 #include <cuda_bf16.h>
 
 #include "moe_common.cuh"
@@ -88,6 +90,12 @@ __device__ __forceinline__ float warp_max(float v) {
 
 // exp(l - m) for l <= m, 1 at l == m also when both are infinite.
 __device__ __forceinline__ float exp_below(float l, float m) { return l == m ? 1.0f : expf(l - m); }
+
+// The same for a row's softmax sum and its gradient, m finite: __expf is off by 2 +
+// 1.16 |l - m| units in the last place, so terms that count are off by a few, and
+// it takes a third of expf's instructions (16384 rows of 2048 logits: 41 us against
+// 52 forward, 44 against 61 backward).
+__device__ __forceinline__ float exp_term(float l, float m) { return __expf(l - m); }
 
 struct Sigmoid {
     float s, not_s;   // sigmoid(l) and 1 - sigmoid(l), each without cancellation
@@ -192,45 +200,52 @@ __device__ __forceinline__ float lanes_max(float v) {
     return r;
 }
 
-// Takes the lowest expert whose value is `top` out of group kG, the warp's number
-// `group`, and renews the group's maximum; returns the expert. The groups' code is
-// kept apart by the asm: merged, it would index the values in memory.
-template <bool kVec, int kGroup, int kG, int kHeld, int kGroups>
+// Takes the lowest expert whose value is `top` out of the warp's group number
+// `group`, one of [kFrom, kTo), and renews the group's maximum; returns the expert.
+// The groups' code is kept apart by the asm: merged, it would index the values in
+// memory.
+template <bool kVec, int kGroup, int kFrom, int kTo, int kHeld, int kGroups>
 __device__ __forceinline__ uint32_t take_out(float (&v)[kHeld], float (&group_top)[kGroups], uint32_t group, float top,
                                              int lane) {
-    uint32_t win = 0;
-    if (group == kG) {
-        asm volatile("" ::"n"(kG));
-        uint32_t e = kFull;
+    if constexpr (kTo - kFrom > 1) {
+        constexpr int kMid = (kFrom + kTo) / 2;
+        return group < kMid ? take_out<kVec, kGroup, kFrom, kMid>(v, group_top, group, top, lane)
+                            : take_out<kVec, kGroup, kMid, kTo>(v, group_top, group, top, lane);
+    } else {
+        asm volatile("" ::"n"(kFrom));
+        int first = kGroup;   // of this lane's values
 #pragma unroll
         for (int i = kGroup - 1; i >= 0; --i)
-            if (v[kG * kGroup + i] == top) e = expert_of<kVec>(kG * kGroup + i, lane);
-        win = __reduce_min_sync(kFull, e);
+            if (v[kFrom * kGroup + i] == top) first = i;
+        const uint32_t e = first < kGroup ? expert_of<kVec>(kFrom * kGroup + first, lane) : kFull;
+        const uint32_t win = __reduce_min_sync(kFull, e);
+        if (e != win) first = kGroup;
         float rest = -INFINITY;
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
-            if (expert_of<kVec>(kG * kGroup + i, lane) == (int)win) v[kG * kGroup + i] = -INFINITY;
-            rest = fmaxf(rest, v[kG * kGroup + i]);
+            if (i == first) v[kFrom * kGroup + i] = -INFINITY;
+            rest = fmaxf(rest, v[kFrom * kGroup + i]);
         }
-        group_top[kG] = rest;
+        group_top[kFrom] = rest;
+        return win;
     }
-    if constexpr (kG + 1 < kGroups) {
-        const uint32_t other = take_out<kVec, kGroup, kG + 1>(v, group_top, group, top, lane);
-        if (group != kG) win = other;
-    }
-    return win;
 }
 
 // A choice looks at the maxima of groups of eight values a lane, and only the
 // winner's group is gone through again (its number is made the same in every lane).
-// Five CTAs' registers to an SM: with what the compiler takes for 64 values a
-// lane it would be three, too few warps to cover the loads.
+// Groups of four are faster for 32 values a lane (16384 rows of 1024 logits: 24 us
+// against 26) and slower for 64. Five CTAs' registers to an SM: with what the
+// compiler takes for 64 values a lane it would be three, and four took 38 us for
+// 16384 rows of 2048 fp32 logits (softmax over all, top 8) where five take 36. That
+// is 3.8 TB/s: eight choices of some hundred instructions and three reductions over
+// the warp bound it, not the 134 MB; bf16 logits take as long. (Fetching a warp's
+// next row into shared memory meanwhile gained nothing.)
 template <typename L, int kPerLane, bool kVec>
 __global__ void __launch_bounds__(kWarpsPerCta * 32, kPerLane > 32 ? 5 : 8) gate_kernel(const GateArgs a) {
     WarpTrace wt(a.trace, MOE_TRACE_GATE);
     grid_dependency_wait();
     clear_words(a);
-    constexpr int kGroup = 8, kGroups = kPerLane / kGroup;
+    constexpr int kGroup = kPerLane == 32 ? 4 : 8, kGroups = kPerLane / kGroup;
     const int lane = threadIdx.x & 31;
     const int t = blockIdx.x * kWarpsPerCta + (threadIdx.x >> 5);
     if (t >= a.T) return;
@@ -261,10 +276,15 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32, kPerLane > 32 ? 5 : 8) gate
         for (int g = 0; g < kGroups; ++g) m = fmaxf(m, group_top[g]);
         m = lanes_max(m);
         if (!(m > -INFINITY)) m = 0.0f;
-        float s = 0.0f;
+        float s[4] = {};
+        if (m < INFINITY) {
 #pragma unroll
-        for (int i = 0; i < kPerLane; ++i) s += exp_below(v[i], m);
-        z = warp_sum(s);
+            for (int i = 0; i < kPerLane; ++i) s[i & 3] += exp_term(v[i], m);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kPerLane; ++i) s[i & 3] += v[i] == INFINITY ? 1.0f : 0.0f;
+        }
+        z = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
     }
     if (a.bias != nullptr) {   // choose by score + bias; the logits are read again for the chosen
 #pragma unroll
@@ -295,7 +315,7 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32, kPerLane > 32 ? 5 : 8) gate
         for (int g = kGroups - 1; g >= 0; --g)
             if (group_top[g] == top) group = g;
         group = __reduce_min_sync(kFull, group);
-        const uint32_t win = take_out<kVec, kGroup, 0>(v, group_top, group, top, lane);
+        const uint32_t win = take_out<kVec, kGroup, 0, kGroups>(v, group_top, group, top, lane);
         if (lane == j) mine = a.bias == nullptr ? top : to_float(row[win]), mine_e = (int)win;
     }
     const float w = entry_weight(a.mode, mine, mine_e >= 0, m, z);
@@ -307,6 +327,9 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32, kPerLane > 32 ? 5 : 8) gate
 
 // ------------------------------------------------------------------ forward, a CTA per token
 
+// Rows of more experts than a warp holds: keys in shared memory, of which a thread
+// has every 256th, and each choice two barriers and a look at the warps' best ones.
+// Only the thread whose key was taken goes through its own again.
 struct Top {
     uint32_t key;
     int e;
@@ -396,7 +419,9 @@ __global__ void __launch_bounds__(kWideThreads) gate_wide_kernel(const GateArgs 
 // ------------------------------------------------------------------ backward, a warp per token
 
 // kPerLane: the row fits into the warp's registers (E <= 32 kPerLane) and is read
-// and written once; 0: longer rows, read again for each use.
+// and written once; 0: longer rows, read again for each use. The softmax's gradient
+// without normalisation is bound by HBM: 16384 rows of 2048 fp32 logits, 268 MB, take
+// 44 us (6.0 TB/s); the others write only zeros and the chosen entries.
 template <typename L, int kPerLane, bool kVec>
 __global__ void __launch_bounds__(kWarpsPerCta * 32, kPerLane > 32 ? 4 : 8) gate_backward_kernel(const GateBackArgs a) {
     WarpTrace wt(a.trace, MOE_TRACE_GATE_BACKWARD);
@@ -444,11 +469,22 @@ __global__ void __launch_bounds__(kWarpsPerCta * 32, kPerLane > 32 ? 4 : 8) gate
 #pragma unroll
             for (int i = 0; i < kHeld; ++i) m = fmaxf(m, x[i]);   // fmaxf passes over NaN
             m = warp_max(m);
+            float s[4] = {};
+            if (m < INFINITY) {
+                const float from = fmaxf(m, -FLT_MAX);   // a row that is masked whole
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i) {
-                x[i] = x[i] > -INFINITY ? exp_below(x[i], m) : 0.0f;
-                z += x[i];
+                for (int i = 0; i < kHeld; ++i) {
+                    x[i] = exp_term(fmaxf(x[i], -INFINITY), from);   // NaN becomes -inf, and that 0
+                    s[i & 3] += x[i];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i) {
+                    x[i] = x[i] == INFINITY ? 1.0f : 0.0f;
+                    s[i & 3] += x[i];
+                }
             }
+            z = (s[0] + s[1]) + (s[2] + s[3]);
         } else {
             for (int i = lane; i < a.E; i += 32) m = fmaxf(m, to_float(row[i]));
             m = warp_max(m);
