@@ -15,14 +15,19 @@
 // and then, as more K blocks of the same sums but of the piece's columns alone,
 // each piece's v by its B. v is held as the sum of two bf16 (16 bits of it), the
 // operands of two products. (Tiles of one adapter each ran W over 1.4 times as
-// many tiles with 4096 rows of 16 adapters in runs: 312 us in all.)
+// many tiles with 4096 rows of 16 adapters in runs: 312 us in all.) 4096 rows, 16
+// adapters of rank 64, 7168 x 4096: 233 us, 1.06 PFLOP/s; the plan takes 10, the copy
+// 17, v about 30 and W's two rounds of tiles 175. There a block of 64 KB arrives
+// every 1500 cycles where its products take 1024: L2's latency under that load, with
+// 160 KB in flight, not its bandwidth (38% of peak).
 //
 // Row by row (few rows to an adapter): the shrink kernel makes v in fp32, four
 // warps to a row of A, the expand kernel B v in fp32, a thread to a row of B, and
 // the projection multiplies all rows, in their own order, by W and adds B v to
 // its sums. The projection's loads depend on neither, so it is launched to
 // overlap them: 128 rows, 48 adapters of rank 16, 7168 x 7168 are bound by the
-// 103 MB of W.
+// 103 MB of W and the 22 MB of adapters, 33 us (3.9 TB/s) of which the exchange of
+// sums in clusters and the last stores take 8; one row, 7168 x 2048, takes 11.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -330,7 +335,11 @@ struct ShrinkArgs {
     TraceArgs trace;
 };
 
-constexpr int kShrinkRows = 8;   // rows of A to a CTA: two groups of four warps, a quarter of K to a warp, four rows to a warp
+// v = scale * (A x), for every row of x. Rows of A to a CTA: two groups of four
+// warps, a quarter of K to a warp, four rows to a warp. The loads of A and x bound
+// it, from HBM the first time an adapter's rows are used and from L2 then: 128 rows,
+// 48 adapters of rank 16, K = 7168: 10 us with all of it in HBM.
+constexpr int kShrinkRows = 8;
 
 __global__ void __launch_bounds__(256) adapter_shrink_kernel(const ShrinkArgs s) {
     WarpTrace wt(s.trace, MOE_TRACE_ADAPTER_SHRINK);
@@ -393,7 +402,8 @@ struct ExpandArgs {
 constexpr int kExpandRows = 4;   // rows of x to a CTA, which has 256 rows of B
 
 // delta[t] = B v[t], 0 without an adapter: a thread has one row of B, its loads
-// for the CTA's rows of x all at once for every 8 of the rank.
+// for the CTA's rows of x all at once for every 8 of the rank. Bound by those loads:
+// 128 rows, 48 adapters of rank 16, N = 7168: 11 us with all of it in HBM.
 __global__ void __launch_bounds__(256) adapter_expand_kernel(const ExpandArgs e) {
     WarpTrace wt(e.trace, MOE_TRACE_ADAPTER_EXPAND);
     __shared__ float v[kExpandRows][MOE_MAX_ADAPTER_RANK];

@@ -5,14 +5,14 @@
 //
 // The valid entries are sorted by expert and cut into groups of at most `cols` of
 // one expert: up to 256 entries by every CTA for itself, more by a plan kernel.
-// The experts kernel (one CTA per SM, launched cooperatively) runs skinny.cuh's body over two
-// phases of work: phase 0 makes h (a tile is 128 gate and the same 128 up rows,
+// The experts kernel (one CTA per SM, launched cooperatively) runs skinny.cuh's body
+// over two phases of work: phase 0 makes h (a tile is 128 gate and the same 128 up rows,
 // so that one thread holds both sums of an element), phase 1 multiplies h by w2
 // (a tile is 256 rows) into y, one fp32 row per entry. A group's phase 1 waits
 // until all its h tiles are done; the loads of w2 do not wait. The groups go
-// through the two phases in up to two waves, phase 0 of a wave before phase 1 of the wave
-// before it, so that h is there when its turn comes and the stream of weights
-// does not pause. When all of y is there, all CTAs add each token's rows in
+// through the two phases in up to two waves, phase 0 of a wave before phase 1 of
+// the wave before it, so that h is there when its turn comes and the stream of
+// weights does not pause. When all of y is there, all CTAs add each token's rows in
 // entry order with their weights and round once to bf16.
 //
 // h is rounded to bf16, or with E4M3 weights to a sum of two codes of the same
@@ -20,6 +20,13 @@
 // output is of the size of that output's own rounding. With E4M3 weights a split
 // kernel makes two codes of x before, which is exact for all elements within
 // 2^-10 of their block's largest, and off by 2^-17 of that for smaller ones.
+//
+// The stream of the chosen experts' weights bounds it. Experts of 7168 x 2048: one
+// token, 8 in bf16 (705 MB), 118 us, 6.0 TB/s; 64 tokens' local entries, 32 in E4M3
+// (1.46 GB), 272 us, 5.4 TB/s; 128 tokens, 256 in E4M3 (11.4 GB), 1850 us, 6.2 TB/s.
+// The rest of a call is set-up (5 us), the wait for the first and the last wave's h
+// (6 us each) and the sums over y (3 us): 24 experts of 1160 x 520 and 37 tokens, 86 MB,
+// take 31 us where the bytes take 13.
 #include <algorithm>
 #include <climits>
 #include <cuda_bf16.h>

@@ -823,7 +823,8 @@ inline size_t plan_smem(int sets) { return ((size_t)plan_warps(sets) + 3) * (set
 
 // Sets in order, entries of a set in their own order: where entries change
 // places between groups, their sums are cut elsewhere and may round otherwise, so
-// the same choice has to give the same groups.
+// the same choice has to give the same groups. One CTA, bound by the latency of its
+// passes: 512 entries of 32 sets 7 us, 4096 entries of 17 sets in tiles 10 us.
 template <typename Index, bool kTiles>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Index> a, const int warps) {
     WarpTrace wt(a.trace, MOE_TRACE_PLAN);

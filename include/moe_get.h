@@ -637,6 +637,11 @@ MOE_API size_t moe_experts_workspace_size(int num_tokens, int hidden, int interm
  *   w13_scales     [E, 2I, H/128] and w2_scales [E, H, I/128] fp32: a weight is
  *                  its code's value times its row's scale of the 128 columns (what
  *                  MOE_DISPATCH_QUANTIZE_FP8 makes of the rows). NULL for bf16.
+ *                  With E4M3 weights x is taken as the sum of two E4M3 codes under a
+ *                  power of two per 128 channels (exact down to 2^-10 of the block's
+ *                  largest, off by 2^-17 of it below), h alike with eight bits, and a
+ *                  block of either that is not finite makes its token's outputs NaN.
+ *                  With bf16 weights h is rounded to bf16.
  *   out            [T, H] bf16, 16-byte aligned; not one of the inputs.
  *   workspace      at least moe_experts_workspace_size() bytes; need not be
  *                  initialised; not shared by calls that overlap on the GPU.
@@ -675,7 +680,8 @@ MOE_API size_t moe_adapter_linear_workspace_size(int num_tokens, int in_features
  * Products are summed in fp32; the adapter's inner vector is kept in fp32, or as
  * the sum of two bf16 where many rows share an adapter. Adapters may follow one
  * another in any order. An adapter reaches the rows that name it and no other
- * (its infinities and NaN too). An index outside [-1, L) raises
+ * (its infinities and NaN too; where its rows share a tile, an infinity in b may
+ * come out as NaN). An index outside [-1, L) raises
  * MOE_ERR_BAD_ADAPTER and counts as -1.
  *
  *   x            [T, K] bf16, w [N, K] bf16, both 16-byte aligned.
