@@ -654,48 +654,53 @@ __device__ bool read_sums_e4m3(const P &p, Control &c, const float *b_scales, co
         float w0[4], w1[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) w0[u] = __ldg(s0 + min(s.kb0 + u, s.kb1 - 1)), w1[u] = __ldg(s1 + min(s.kb0 + u, s.kb1 - 1));
-        for (int kb4 = s.kb0; kb4 < s.kb1 && ok; kb4 += 4) {
+#pragma unroll 1
+        for (int kb = s.kb0; kb < s.kb1; ++kb) {
+            const float now0 = w0[0], now1 = w1[0];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int kb = kb4 + u;
-                if (kb >= s.kb1) break;
-                const float now0 = w0[u], now1 = w1[u];
-                const int later = min(kb + 4, s.kb1 - 1);
-                w0[u] = __ldg(s0 + later), w1[u] = __ldg(s1 + later);
-                if (!warp_wait(&c.sums_full[sums.slot], sums.round)) { ok = false; break; }
-                tc_fence_after();
-                const float *of_block = b_scales + (block++ % kScaleSlots) * 64 + me.first_col();
-                const uint32_t at = at0 + sums.slot * 4 * sh.cols + me.first_col();
+            for (int u = 0; u < 3; ++u) w0[u] = w0[u + 1], w1[u] = w1[u + 1];
+            const int later = min(kb + 4, s.kb1 - 1);
+            w0[3] = __ldg(s0 + later), w1[3] = __ldg(s1 + later);
+            if (!warp_wait(&c.sums_full[sums.slot], sums.round)) { ok = false; break; }
+            tc_fence_after();
+            const float *of_block = b_scales + (block++ % kScaleSlots) * 64 + me.first_col();
+            const uint32_t at = at0 + sums.slot * 4 * sh.cols + me.first_col();
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
-                    if (i * 8 >= s.n16()) break;
-                    float v[16];   // first and second codes' sums of half 0, then of half 1
-                    tmem_load4(at + i * 8, v);
-                    tmem_load4(at + s.n16() + i * 8, v + 4);
-                    tmem_load4(at + 2 * sh.cols + i * 8, v + 8);
-                    tmem_load4(at + 2 * sh.cols + s.n16() + i * 8, v + 12);
-                    tmem_load_wait(v);
-                    if ((i + 1) * 8 >= s.n16()) {   // all of the block's sums are in registers
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&c.sums_empty[sums.slot]);
-                    }
-                    const float4 bs = *reinterpret_cast<const float4 *>(of_block + i * 8);
-                    const float scale[4] = {bs.x, bs.y, bs.z, bs.w};
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        acc[i][j] = fmaf(now0 * scale[j], v[j] + v[4 + j], acc[i][j]);
-                        acc[i][4 + j] = fmaf(now1 * scale[j], v[8 + j] + v[12 + j], acc[i][4 + j]);
-                    }
+            for (int i = 0; i < kSteps; ++i) {
+                if (i * 8 >= s.n16()) break;
+                float v[16];   // first and second codes' sums of half 0, then of half 1
+                tmem_load4(at + i * 8, v);
+                tmem_load4(at + s.n16() + i * 8, v + 4);
+                tmem_load4(at + 2 * sh.cols + i * 8, v + 8);
+                tmem_load4(at + 2 * sh.cols + s.n16() + i * 8, v + 12);
+                tmem_load_wait(v);
+                if ((i + 1) * 8 >= s.n16()) {   // all of the block's sums are in registers
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&c.sums_empty[sums.slot]);
                 }
-                sums.next();
+                const float4 bs = *reinterpret_cast<const float4 *>(of_block + i * 8);
+                const float scale[4] = {bs.x, bs.y, bs.z, bs.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    acc[i][j] = fmaf(now0 * scale[j], v[j] + v[4 + j], acc[i][j]);
+                    acc[i][4 + j] = fmaf(now1 * scale[j], v[8 + j] + v[12 + j], acc[i][4 + j]);
+                }
             }
+            sums.next();
         }
         if (!Tm::agree(ok)) return false;
+        // One copy of f's code: a tile runs it once, and with a copy for every step the
+        // instructions came from L2 at some 2 us a step.
         auto each = [&](auto f) {
+#pragma unroll 1
+            for (int col = me.first_col(); col < s.n; col += 8) {
+                f(col, acc[0]);
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i)
-                if (i * 8 + me.first_col() < s.n) f(i * 8 + me.first_col(), acc[i]);
+                for (int i = 0; i + 1 < kSteps; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) acc[i][j] = acc[i + 1][j];
+            }
         };
         return take(p, c, sh, s, me, each, [] {});
     });
