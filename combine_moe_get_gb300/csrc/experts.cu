@@ -109,9 +109,9 @@ struct Lines {
     int waves;
 };
 
-// E4M3: largest magnitudes of 32 rows, [readers' two sides and adders][quarter][column].
+// E4M3: largest magnitudes of 32 rows, [readers' two sides and adders][column][quarter].
 struct Most {
-    float of[3][4][4];
+    float4 of[3][4];
 };
 
 template <bool kE4m3, int kCols>   // kCols: the most columns of a tile
@@ -259,35 +259,37 @@ struct ExpertsProblem {
         // their largest magnitudes go through shared memory.
         __device__ void emit_codes(int col, const float (&h)[4], int i) {
             const int group = (threadIdx.x - Readers::first) / 128, quarter = threadIdx.x / 32 & 3;
-            float (&most)[4][4] = p.most->of[group];
+            float4 (&most)[4] = p.most->of[group];
             auto side_sync = [&] { asm volatile("barrier.cta.sync %0, 128;" ::"r"(3 + group) : "memory"); };
             side_sync();   // the columns before these are done with it
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float m = skinny::lanes_max_nan(fabsf(h[j]));
-                if ((threadIdx.x & 31) == 0) most[quarter][j] = m;
+                const float m = skinny::lanes_max(fabsf(h[j]));
+                if ((threadIdx.x & 31) == 0) reinterpret_cast<float *>(&most[j])[quarter] = m;
             }
             side_sync();
-            uint8_t *codes = static_cast<uint8_t *>(a.h);
+            const size_t pos = s.first + col, second = (size_t)a.T * a.k * a.I;
+            uint8_t *to = static_cast<uint8_t *>(a.h) + pos * a.I + i;
+            float *scales = a.h_scales + pos * p.kbs[1] + s.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                if (col + j >= s.n) continue;
-                float m = 0.0f;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) m = most[q][j] <= m ? m : most[q][j];   // NaN stays
-                const skinny::BlockScale scale(m);
+                const float4 q = most[j];
+                const skinny::BlockScale scale(fmaxf(fmaxf(q.x, q.y), fmaxf(q.z, q.w)));   // a NaN's code is one too
                 const skinny::Split two(h[j] * scale.inverse);
-                const size_t pos = s.first + col + j;
-                codes[pos * a.I + i] = (uint8_t)two.first;
-                codes[((size_t)a.T * a.k + pos) * a.I + i] = (uint8_t)two.second;
-                if (row == 0) a.h_scales[pos * p.kbs[1] + s.f] = scale.scale;
+                if (col + j < s.n) {
+                    to[0] = (uint8_t)two.first;
+                    to[second] = (uint8_t)two.second;
+                    if (row == 0) *scales = scale.scale;
+                }
+                to += a.I, scales += p.kbs[1];
             }
         }
         __device__ void operator()(int col, const float *v) {
             if (s.phase == 0) {
                 float h[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) h[j] = v[j] / (1.0f + expf(-v[j])) * v[4 + j];
+                for (int j = 0; j < 4; ++j)   // off by some 2^-21, far below the eight bits that h keeps
+                    h[j] = __fdividef(v[j], 1.0f + __expf(-v[j])) * v[4 + j];
                 const int i = s.f * kRows + row;
                 if constexpr (kE4m3) {
                     emit_codes(col, h, i);
@@ -299,10 +301,13 @@ struct ExpertsProblem {
                 }
             } else {
                 const int o = s.f * 2 * kRows + row;
+                int e[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) e[j] = p.entry(s.first + min(col + j, s.n - 1));
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (col + j >= s.n) continue;
-                    float *y = a.y + (size_t)p.entry(s.first + col + j) * a.H + o;
+                    float *y = a.y + (size_t)e[j] * a.H + o;
                     if (o < a.H) y[0] = v[j];
                     if (o + kRows < a.H) y[kRows] = v[4 + j];
                 }
@@ -393,8 +398,8 @@ __global__ void __launch_bounds__(256) experts_split_kernel(const SplitArgs s) {
                         __uint_as_float(v.y & 0xffff0000u)};
     float most = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) most = fabsf(x[i]) <= most ? most : fabsf(x[i]);   // NaN stays
-    const skinny::BlockScale scale(skinny::lanes_max_nan(most));
+    for (int i = 0; i < 4; ++i) most = fmaxf(most, fabsf(x[i]));   // a NaN's code is one too
+    const skinny::BlockScale scale(skinny::lanes_max(most));
     uint32_t first = 0, second = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

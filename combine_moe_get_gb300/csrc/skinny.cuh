@@ -32,7 +32,6 @@
 #pragma once
 
 #include <algorithm>
-#include <type_traits>
 
 #include "umma.cuh"
 
@@ -435,7 +434,7 @@ struct Split {
 };
 
 // The power of two under which a block with this largest magnitude stays below
-// 256, and its inverse. A block that is not finite gets NaN for its scale: so does
+// 256, and its inverse. A block with an infinity gets NaN for its scale: so does
 // all that it is multiplied with.
 struct BlockScale {
     float scale, inverse;
@@ -446,10 +445,10 @@ struct BlockScale {
     }
 };
 
-// The largest of the lanes' values; NaN wins.
-__device__ __forceinline__ float lanes_max_nan(float v) {
+// The largest of the lanes' values; NaN loses.
+__device__ __forceinline__ float lanes_max(float v) {
     float r;
-    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
 }
 
@@ -509,33 +508,26 @@ __device__ bool add_up(const P &p, const Shape sh, const Segment &s) {
         Share<P::kHalves> share = Share<P::kHalves>::of(Tm::warp());
         share.side = unit * skip & 3;
         const int col = (unit * skip >> 2) * 16 + share.first_col();
-        // 32 loads at once, of four parts or eight: a trip to another SM's sums in L2 takes about a microsecond
+        // 32 loads at once, of four parts: a trip to another SM's sums in L2 takes about a microsecond.
+        // (Twice as many for two units were no faster: code that runs once waits for its instructions.)
         float v[8] = {};
-        auto batch = [&](auto parts_at_once, int i0, int j0) {
-            constexpr int kParts = decltype(parts_at_once)::value, kValues = 32 / kParts;
-            float x[kParts][kValues];
+#pragma unroll 1
+        for (int i0 = 0; i0 < s.parts; i0 += 4) {
+            float x[4][8];
 #pragma unroll
-            for (int i = 0; i < kParts; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 // the stretch that begins the tile is its CTA's last, the others their CTA's first
                 const float *part = p.partial(s.line, s.cta0 + i0 + i, i0 + i == 0 ? 1 : 0) + share.row;
 #pragma unroll
-                for (int j = 0; j < kValues; ++j) {
-                    const int at = col + share.col_of(j0 + j);
-                    x[i][j] = i0 + i < s.parts && at < s.n ? __ldcg(part + share.half_of(j0 + j) * half + at * kRows) : 0.0f;
+                for (int j = 0; j < 8; ++j) {
+                    const int at = col + share.col_of(j);
+                    x[i][j] = i0 + i < s.parts && at < s.n ? __ldcg(part + share.half_of(j) * half + at * kRows) : 0.0f;
                 }
             }
 #pragma unroll
-            for (int i = 0; i < kParts; ++i)
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int j = 0; j < kValues; ++j) v[j0 + j] += x[i][j];
-        };
-        if (s.parts <= 4) {
-            batch(std::integral_constant<int, 4>(), 0, 0);
-        } else {
-            for (int i0 = 0; i0 < s.parts; i0 += 8) {
-                batch(std::integral_constant<int, 8>(), i0, 0);
-                batch(std::integral_constant<int, 8>(), i0, 4);
-            }
+                for (int j = 0; j < 8; ++j) v[j] += x[i][j];
         }
         typename P::Emit emit(p, s, share);
         emit(col, v);
