@@ -701,7 +701,7 @@ int launch_adapter_linear(const AdapterLaunch &L) {
         const skinny::PlanArgs<int32_t> plan{L.adapter_idx, T, L.num_adapters, true, cols, a.words,
                                              kReady + (P + cols - 1) / cols, const_cast<int4 *>(a.groups),
                                              const_cast<int *>(a.order), place, const_cast<int *>(a.tile_pieces),
-                                             MOE_ERR_BAD_ADAPTER, L.status, a.trace};
+                                             MOE_ERR_BAD_ADAPTER, false, L.status, a.trace};
         const int rc = skinny::launch_plan<true>(plan, s);
         if (rc != MOE_OK) return rc;
         const SortArgs so{static_cast<const uint4 *>(L.x), reinterpret_cast<uint4 *>(ws + sp.x), place, K / 8, a.trace};

@@ -387,6 +387,7 @@ struct SplitArgs {
 __global__ void __launch_bounds__(256) experts_split_kernel(const SplitArgs s) {
     WarpTrace wt(s.trace, MOE_TRACE_EXPERTS_SPLIT);
     grid_dependency_wait();
+    grid_launch_dependents();   // the plan, which does not depend on this
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < s.num_clear; i += 256) s.clear[i] = 0;
     const int lane = threadIdx.x & 31;
@@ -467,16 +468,6 @@ int launch_experts(const ExpertsLaunch &L, bool words_are_zero) {
     a.trace = trace_args();
 
     const bool overlap = tuning().overlap != 0;
-    if (!a.local) {
-        const skinny::PlanArgs<int64_t> plan{L.topk_idx, T * k, E, false, cols, a.words, kReady + T * k,
-                                             const_cast<int4 *>(a.groups), const_cast<int *>(a.order), nullptr, nullptr,
-                                             MOE_ERR_BAD_TOPK, L.status, a.trace};
-        const int rc = skinny::launch_plan<false>(plan, s);
-        if (rc != MOE_OK) return rc;
-    } else if (!words_are_zero && !e4m3) {
-        if (launch_kernel(skinny::clear_kernel, dim3(1), dim3(1024), 0, s, overlap, a.words, kReady + T * k) != cudaSuccess)
-            return MOE_ERR_CUDA;
-    }
     if (e4m3) {
         const bool clear = a.local && !words_are_zero;
         const SplitArgs split{static_cast<const __nv_bfloat16 *>(L.x), reinterpret_cast<uint8_t *>(ws + sp.x_codes),
@@ -485,6 +476,16 @@ int launch_experts(const ExpertsLaunch &L, bool words_are_zero) {
         const int64_t blocks = (int64_t)T * (H / 128);
         if (launch_kernel(experts_split_kernel, dim3((unsigned)((blocks + 7) / 8)), dim3(256), 0, s, overlap, split) !=
             cudaSuccess)
+            return MOE_ERR_CUDA;
+    }
+    if (!a.local) {
+        const skinny::PlanArgs<int64_t> plan{L.topk_idx, T * k, E, false, cols, a.words, kReady + T * k,
+                                             const_cast<int4 *>(a.groups), const_cast<int *>(a.order), nullptr, nullptr,
+                                             MOE_ERR_BAD_TOPK, e4m3 && overlap, L.status, a.trace};
+        const int rc = skinny::launch_plan<false>(plan, s);
+        if (rc != MOE_OK) return rc;
+    } else if (!words_are_zero && !e4m3) {
+        if (launch_kernel(skinny::clear_kernel, dim3(1), dim3(1024), 0, s, overlap, a.words, kReady + T * k) != cudaSuccess)
             return MOE_ERR_CUDA;
     }
     const size_t smem = a.shape.smem(e4m3) + (a.local ? sizeof(skinny::LocalPlan) : 0);

@@ -246,6 +246,7 @@ template <typename L, int kPerLane, bool kVec>
 __global__ void __launch_bounds__(kWarpsPerCta * 32, kPerLane > 32 ? 5 : 8) gate_kernel(const GateArgs a) {
     WarpTrace wt(a.trace, MOE_TRACE_GATE);
     grid_dependency_wait();
+    grid_launch_dependents();   // the next kernel's set-up
     clear_words(a);
     constexpr int kGroup = kPerLane == 32 ? 4 : 8, kGroups = kPerLane / kGroup;
     const int lane = threadIdx.x & 31;

@@ -807,6 +807,7 @@ struct PlanArgs {
     int *place;              // in tiles: each entry's place
     int *tiles;              // in tiles: each tile's first group, then the number of groups
     int bad;                 // status of an index out of range
+    bool beside;             // runs beside the kernel before it, which began after all that idx depends on was complete
     int32_t *status;
     TraceArgs trace;
 };
@@ -825,7 +826,7 @@ inline size_t plan_smem(int sets) { return ((size_t)plan_warps(sets) + 3) * (set
 template <typename Index, bool kTiles>
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Index> a, const int warps) {
     WarpTrace wt(a.trace, MOE_TRACE_PLAN);
-    grid_dependency_wait();
+    if (!a.beside) grid_dependency_wait();
     grid_launch_dependents();   // the next kernel's set-up
     extern __shared__ int32_t plan_memory[];
     const int sets = a.sets + (a.rest ? 1 : 0);
@@ -900,6 +901,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanArgs<Index
         if (e >= 0 && same >> lane == 1) mine[e] += __popc(same);   // the last of them
         __syncwarp();
     }
+    if (a.beside) grid_dependency_wait();   // the next kernel waits for this one alone
 }
 
 // The same for few entries, by every CTA for itself in its shared memory: no
