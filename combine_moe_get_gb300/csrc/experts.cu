@@ -23,10 +23,11 @@
 //
 // The stream of the chosen experts' weights bounds it. Experts of 7168 x 2048: one
 // token, 8 in bf16 (705 MB), 118 us, 6.0 TB/s; 64 tokens' local entries, 32 in E4M3
-// (1.46 GB), 272 us, 5.4 TB/s; 128 tokens, 256 in E4M3 (11.4 GB), 1850 us, 6.2 TB/s.
+// (1.46 GB), 265 us, 5.5 TB/s; 128 tokens, 256 in E4M3 (11.4 GB), 1800 us, 6.3 TB/s.
 // The rest of a call is set-up (5 us), the wait for the first and the last wave's h
 // (6 us each) and the sums over y (3 us): 24 experts of 1160 x 520 and 37 tokens, 86 MB,
-// take 31 us where the bytes take 13.
+// take 30 us where the bytes take 13. In calls this short the kernel's instructions
+// come from L2 as well: what runs once for a tile is kept in one short copy.
 #include <algorithm>
 #include <climits>
 #include <cuda_bf16.h>

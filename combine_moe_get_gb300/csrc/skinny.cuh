@@ -25,8 +25,8 @@
 //     along K has its own fp32 scale per weight row, so the readers scale each
 //     block's sums and add them in registers (n <= 64); four blocks' sums in
 //     tensor memory let the products run ahead. (Turning the codes into bf16 in
-//     tensor memory, by 8 more warps, was bound by that memory's ports: 2.01 ms
-//     where this takes 1.83.)
+//     tensor memory, by 8 more warps, was bound by that memory's ports: 2.01 ms for
+//     256 experts of 7168 x 2048 where this took 1.83, and now takes 1.80.)
 //
 // The problem P gives the segments, the loads of B and what becomes of the sums.
 #pragma once
