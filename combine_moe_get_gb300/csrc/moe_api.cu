@@ -633,7 +633,7 @@ MOE_API int moe_layer(const void *x, int num_tokens, int hidden, const void *log
     if (rc != MOE_OK) return rc;
     const moe::ExpertsWords w = moe::experts_words(L);
     rc = moe::launch_gate(moe::GateLaunch{logits, logits_type, bias, num_tokens, num_topk, num_experts, mode, scale,
-                                          topk_idx, topk_weights, status, stream, w.words, w.n});
+                                          topk_idx, topk_weights, status, stream, w.words, w.n, true});
     return rc != MOE_OK ? rc : moe::launch_experts(L, w.words != nullptr);
 }
 

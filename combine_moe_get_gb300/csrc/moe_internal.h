@@ -284,6 +284,7 @@ struct GateLaunch {
     // optional: words that the launch zeroes for the next one
     uint32_t *clear = nullptr;
     int num_clear = 0;
+    bool early = false;       // the next launch's CTAs may be placed beside this one's
 };
 
 int launch_gate(const GateLaunch &L);

@@ -162,7 +162,7 @@ TILED = [(4100, 264, 4104, 5, 64), (4100, 264, 4104, 40, 72), (5000, 64, 2056, 9
          (600, 8200, 1064, 2, 128), (1100, 8328, 5000, 3, 64)]
 
 
-@pytest.mark.parametrize("spread", ["rows", "runs", "one"])
+@pytest.mark.parametrize("spread", ["rows", "runs", "none", "one"])
 @pytest.mark.parametrize("shape", TILED)
 def test_adapter_tiles_match_definition(moe, shape, spread):
     p = Problem(*shape, spread=spread, seed=sum(shape))
