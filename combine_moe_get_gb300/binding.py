@@ -2,8 +2,10 @@
 
 Argument marshalling only: every function takes CUDA tensors, allocates the
 outputs it is not given with torch (device memory is torch's job here), and
-passes raw pointers, sizes and the current CUDA stream to the C entry point
-of the same name. All computation runs in the library's CUDA kernels; there
+passes raw pointers, sizes and the current CUDA stream, or the one given as
+``stream``, to the C entry point of the same name. What it allocates belongs
+to that stream: memory given up is reused in that stream's order, and an output
+that another stream reads is the caller's to keep. All computation runs in the library's CUDA kernels; there
 is no CPU path. If the library cannot be built or loaded, import fails. The
 functions behind a router's logits are for calls so small that marshalling
 them in Python took longer than the call: theirs is csrc/marshal.cpp.
@@ -225,6 +227,15 @@ def _stream(stream: Optional[torch.cuda.Stream]):
     return torch.cuda.current_stream().cuda_stream
 
 
+def _on(stream: Optional[torch.cuda.Stream], make, *args, **kw):
+    """``make(...)`` with ``stream`` as the current one: torch's allocator reuses memory in the order of the stream that
+    it was taken under, and a call's outputs and scratch are used by the stream that the call runs on."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
 def _check(code: int, where: str) -> None:
     if code != MOE_OK:
         raise MoeError(code, where)
@@ -278,11 +289,11 @@ def moe_get_layout(topk_idx: torch.Tensor, num_experts: int, num_ranks: int, *,
     ``layout_mode`` 1 keeps the call off the cluster mode, 2 on the lookback modes (same outputs)."""
     T, k = topk_idx.shape
     dev = topk_idx.device
-    out = out or Layout.empty(T, k, num_experts, num_ranks, dev)
+    out = out or _on(stream, Layout.empty, T, k, num_experts, num_ranks, dev)
     ws_bytes = moe_get_layout_workspace_size(T, num_experts, num_ranks)
     if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
-    status = new_status(dev) if status is None else status
+        workspace = _on(stream, torch.empty, max(ws_bytes, 16), dtype=torch.uint8, device=dev)
+    status = _on(stream, new_status, dev) if status is None else status
     opts = MoeLayoutOptionsC(int(wait_timeout_ns), int(test_unpublished_tile), int(layout_mode))
     code = LIB.moe_get_layout_ex(_ptr(topk_idx), T, k, num_experts, num_ranks, out.c(), _ptr(workspace),
                                  workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream),
@@ -303,11 +314,11 @@ def moe_get_expand_layout(topk_idx: torch.Tensor, expert_prefix: torch.Tensor, n
     expert); ``expert_prefix`` is the layout's [E+1] prefix for ``topk_idx``."""
     T, k = topk_idx.shape
     dev = topk_idx.device
-    out = torch.empty(T, k, dtype=torch.int32, device=dev) if out is None else out
+    out = _on(stream, torch.empty, T, k, dtype=torch.int32, device=dev) if out is None else out
     ws_bytes = moe_get_expand_layout_workspace_size(T, num_experts)
     if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
-    status = new_status(dev) if status is None else status
+        workspace = _on(stream, torch.empty, max(ws_bytes, 16), dtype=torch.uint8, device=dev)
+    status = _on(stream, new_status, dev) if status is None else status
     opts = MoeLayoutOptionsC(int(wait_timeout_ns), int(test_unpublished_tile), int(layout_mode))
     code = LIB.moe_get_expand_layout(_ptr(topk_idx), T, k, num_experts, _ptr(expert_prefix), _ptr(out),
                                      _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(status),
@@ -324,6 +335,21 @@ class Dispatched:
     recv_topk_weights: Optional[torch.Tensor] # [capacity, k] fp32
     recv_src_idx: Optional[torch.Tensor]      # [capacity] int32
     x_scales: Optional[torch.Tensor]          # [T, H/128] fp32 (FP8)
+
+    @staticmethod
+    def empty(num_tokens: int, hidden: int, num_topk: int, capacity: int, device, *, fp8: bool, with_metadata: bool,
+              x_scales: Optional[torch.Tensor], quantize_fp8: bool) -> "Dispatched":
+        def f32(*shape):
+            return torch.empty(*shape, dtype=torch.float32, device=device)
+
+        nb = hidden // 128
+        return Dispatched(
+            recv_x=torch.empty(capacity, hidden, dtype=torch.uint8 if fp8 else torch.bfloat16, device=device),
+            recv_x_scales=f32(capacity, nb) if fp8 else None,
+            recv_topk_idx=torch.empty(capacity, num_topk, dtype=torch.int64, device=device) if with_metadata else None,
+            recv_topk_weights=f32(capacity, num_topk) if with_metadata else None,
+            recv_src_idx=torch.empty(capacity, dtype=torch.int32, device=device) if with_metadata else None,
+            x_scales=x_scales if x_scales is not None else f32(num_tokens, nb) if quantize_fp8 else None)
 
 
 MOE_DISPATCH_BF16 = 0
@@ -353,17 +379,9 @@ def moe_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: Optional
     if fp8_in and x_scales is None:
         raise ValueError("E4M3 input needs its x_scales")
     if out is None:
-        nb = H // 128
-        out = Dispatched(
-            recv_x=torch.empty(recv_capacity, H, dtype=torch.uint8 if fp8_out else torch.bfloat16, device=dev),
-            recv_x_scales=torch.empty(recv_capacity, nb, dtype=torch.float32, device=dev) if fp8_out else None,
-            recv_topk_idx=torch.empty(recv_capacity, k, dtype=torch.int64, device=dev) if with_metadata else None,
-            recv_topk_weights=(torch.empty(recv_capacity, k, dtype=torch.float32, device=dev)
-                               if with_metadata else None),
-            recv_src_idx=torch.empty(recv_capacity, dtype=torch.int32, device=dev) if with_metadata else None,
-            x_scales=(x_scales if fp8_in else
-                      (torch.empty(T, nb, dtype=torch.float32, device=dev) if quantize_fp8 else None)))
-    status = new_status(dev) if status is None else status
+        out = _on(stream, Dispatched.empty, T, H, k, recv_capacity, dev, fp8=fp8_out, with_metadata=with_metadata,
+                  x_scales=x_scales if fp8_in else None, quantize_fp8=quantize_fp8)
+    status = _on(stream, new_status, dev) if status is None else status
     scales_arg = x_scales if fp8_in else out.x_scales
     args = (_ptr(x), T, H, _ptr(topk_idx), _ptr(topk_weights), k, num_experts, num_ranks, _ptr(token_dst_row),
             recv_capacity, mode | (MOE_DISPATCH_EXPAND if expand else 0), _ptr(out.recv_x), _ptr(out.recv_x_scales),
@@ -391,22 +409,14 @@ def moe_layout_dispatch(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: O
     fp8_out = mode != MOE_DISPATCH_BF16
     if fp8_in and x_scales is None:
         raise ValueError("E4M3 input needs its x_scales")
-    layout = layout or Layout.empty(T, k, num_experts, num_ranks, dev)
+    layout = layout or _on(stream, Layout.empty, T, k, num_experts, num_ranks, dev)
     ws_bytes = moe_get_layout_workspace_size(T, num_experts, num_ranks)
     if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
+        workspace = _on(stream, torch.empty, max(ws_bytes, 16), dtype=torch.uint8, device=dev)
     if out is None:
-        nb = H // 128
-        out = Dispatched(
-            recv_x=torch.empty(recv_capacity, H, dtype=torch.uint8 if fp8_out else torch.bfloat16, device=dev),
-            recv_x_scales=torch.empty(recv_capacity, nb, dtype=torch.float32, device=dev) if fp8_out else None,
-            recv_topk_idx=torch.empty(recv_capacity, k, dtype=torch.int64, device=dev) if with_metadata else None,
-            recv_topk_weights=(torch.empty(recv_capacity, k, dtype=torch.float32, device=dev)
-                               if with_metadata else None),
-            recv_src_idx=torch.empty(recv_capacity, dtype=torch.int32, device=dev) if with_metadata else None,
-            x_scales=(x_scales if fp8_in else
-                      (torch.empty(T, nb, dtype=torch.float32, device=dev) if quantize_fp8 else None)))
-    status = new_status(dev) if status is None else status
+        out = _on(stream, Dispatched.empty, T, H, k, recv_capacity, dev, fp8=fp8_out, with_metadata=with_metadata,
+                  x_scales=x_scales if fp8_in else None, quantize_fp8=quantize_fp8)
+    status = _on(stream, new_status, dev) if status is None else status
     scales_arg = x_scales if fp8_in else out.x_scales
     code = LIB.moe_layout_dispatch(_ptr(x), T, H, _ptr(topk_idx), _ptr(topk_weights), k, num_experts, num_ranks,
                                    layout.c(), _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -423,8 +433,8 @@ def moe_combine(partial: torch.Tensor, token_dst_row: torch.Tensor, *, out: Opti
     rows, H = partial.shape
     T, k = token_dst_row.shape
     dev = partial.device
-    out = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if out is None else out
-    status = new_status(dev) if status is None else status
+    out = _on(stream, torch.empty, T, H, dtype=torch.bfloat16, device=dev) if out is None else out
+    status = _on(stream, new_status, dev) if status is None else status
     code = LIB.moe_combine(_ptr(partial), rows, T, H, k, _ptr(token_dst_row), _ptr(out), _ptr(status),
                            _stream(stream))
     _check(code, "moe_combine")
@@ -439,8 +449,8 @@ def moe_combine_fp8(partial_codes: torch.Tensor, partial_scales: torch.Tensor, t
     rows, H = partial_codes.shape
     T, k = token_dst_row.shape
     dev = partial_codes.device
-    out = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if out is None else out
-    status = new_status(dev) if status is None else status
+    out = _on(stream, torch.empty, T, H, dtype=torch.bfloat16, device=dev) if out is None else out
+    status = _on(stream, new_status, dev) if status is None else status
     if balance is None:
         code = LIB.moe_combine_fp8(_ptr(partial_codes), _ptr(partial_scales), rows, T, H, k, _ptr(token_dst_row),
                                    _ptr(out), _ptr(status), _stream(stream))
@@ -464,10 +474,10 @@ def moe_combine_ex(partial: torch.Tensor, token_dst_row: torch.Tensor, *, row_we
     rows, H = partial.shape
     T, k = token_dst_row.shape
     dev = partial.device
-    out = torch.empty(T, H, dtype=torch.bfloat16, device=dev) if out is None else out
+    out = _on(stream, torch.empty, T, H, dtype=torch.bfloat16, device=dev) if out is None else out
     if recv_topk_weights is not None and combined_topk_weights is None:
-        combined_topk_weights = torch.empty(T, k, dtype=torch.float32, device=dev)
-    status = new_status(dev) if status is None else status
+        combined_topk_weights = _on(stream, torch.empty, T, k, dtype=torch.float32, device=dev)
+    status = _on(stream, new_status, dev) if status is None else status
     code = LIB.moe_combine_ex(_ptr(partial), rows, T, H, k, _ptr(token_dst_row), _ptr(row_weights),
                               _ptr(recv_topk_weights), _ptr(combined_topk_weights), _ptr(out), _ptr(balance),
                               _ptr(status), _stream(stream))
@@ -504,7 +514,7 @@ def moe_topk_gate(logits: torch.Tensor, num_topk: int, *, bias: Optional[torch.T
     weights of each token from the router's ``logits`` [T, E] (fp32 or bf16):
     the k largest logits (or score + ``bias``), weighted by their softmax or
     sigmoid scores, normalised over the chosen ones if ``normalize``."""
-    status = new_status(logits.device) if status is None else status
+    status = _on(stream, new_status, logits.device) if status is None else status
     code, topk_idx, topk_weights = _marshal.topk_gate(
         LIB.entries["moe_topk_gate"], logits, num_topk, bias, _gate_mode(score, normalize), scale, topk_idx,
         topk_weights, status, _handle(stream))
@@ -518,7 +528,7 @@ def moe_topk_gate_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_we
                            stream=None) -> torch.Tensor:
     """The gradient [T, E] (the logits' type) of moe_topk_gate's weights, given
     ``grad_weights`` [T, k] fp32; pass the same score, normalize and scale."""
-    status = new_status(logits.device) if status is None else status
+    status = _on(stream, new_status, logits.device) if status is None else status
     code, out = _marshal.topk_gate_backward(LIB.entries["moe_topk_gate_backward"], logits, topk_idx, grad_weights,
                                             _gate_mode(score, normalize), scale, out, status, _handle(stream))
     _check(code, "moe_topk_gate_backward")
@@ -530,9 +540,9 @@ def moe_experts_workspace_size(num_tokens: int, hidden: int, intermediate: int, 
     return int(LIB.moe_experts_workspace_size(num_tokens, hidden, intermediate, num_topk, num_experts))
 
 
-def _experts_workspace(x, w2, num_topk):
+def _experts_workspace(x, w2, num_topk, stream):
     n = moe_experts_workspace_size(x.shape[0], x.shape[1], w2.shape[2], num_topk, w2.shape[0])
-    return torch.empty(max(n, 16), dtype=torch.uint8, device=x.device)
+    return _on(stream, torch.empty, max(n, 16), dtype=torch.uint8, device=x.device)
 
 
 def moe_experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor, w13: torch.Tensor,
@@ -543,8 +553,8 @@ def moe_experts(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Ten
     """out[t] = sum_j topk_weights[t, j] * w2[e] (silu(gate) * up), [gate; up] = w13[e] x[t] and
     e = topk_idx[t, j], for a few tokens (T <= 1024). Weights are bf16, or E4M3
     codes (uint8) with a scale per row and 128 columns."""
-    workspace = _experts_workspace(x, w2, topk_idx.shape[1]) if workspace is None else workspace
-    status = new_status(x.device) if status is None else status
+    workspace = _experts_workspace(x, w2, topk_idx.shape[1], stream) if workspace is None else workspace
+    status = _on(stream, new_status, x.device) if status is None else status
     code, out = _marshal.experts(LIB.entries["moe_experts"], x, w13, w2, w13_scales, w2_scales, topk_idx, topk_weights,
                                  out, workspace, status, _handle(stream))
     _check(code, "moe_experts")
@@ -560,8 +570,8 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, num_topk: int, w13: torch.T
               stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """moe_topk_gate of ``logits`` [T, E] and moe_experts of the choice in one
     call. Returns (out, topk_idx, topk_weights)."""
-    workspace = _experts_workspace(x, w2, num_topk) if workspace is None else workspace
-    status = new_status(x.device) if status is None else status
+    workspace = _experts_workspace(x, w2, num_topk, stream) if workspace is None else workspace
+    status = _on(stream, new_status, x.device) if status is None else status
     code, out, topk_idx, topk_weights = _marshal.layer(
         LIB.entries["moe_layer"], x, w13, w2, w13_scales, w2_scales, logits, num_topk, bias,
         _gate_mode(score, normalize), scale, topk_idx, topk_weights, out, workspace, status, _handle(stream))
@@ -583,8 +593,8 @@ def moe_adapter_linear(x: torch.Tensor, w: torch.Tensor, adapter_idx: torch.Tens
     adapter_idx int32 [T]; scales fp32 [L]."""
     if workspace is None:
         n = moe_adapter_linear_workspace_size(*x.shape, w.shape[0], a.shape[0], a.shape[1])
-        workspace = torch.empty(max(n, 16), dtype=torch.uint8, device=x.device)
-    status = new_status(x.device) if status is None else status
+        workspace = _on(stream, torch.empty, max(n, 16), dtype=torch.uint8, device=x.device)
+    status = _on(stream, new_status, x.device) if status is None else status
     code, out = _marshal.adapter_linear(LIB.entries["moe_adapter_linear"], x, w, adapter_idx, a, b, scales, out,
                                         workspace, status, _handle(stream))
     _check(code, "moe_adapter_linear")

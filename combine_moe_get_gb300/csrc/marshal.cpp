@@ -11,6 +11,7 @@
 #include <string>
 
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -43,11 +44,15 @@ std::string text(at::ScalarType t) {
     }
 }
 
-// A call's positional arguments, taken in order.
+// A call's positional arguments, taken in order; the stream is the last.
 class Args {
   public:
     Args(PyObject *const *args, Py_ssize_t n, Py_ssize_t want) : at_(args) {
         if (n != want) refuse(PyExc_TypeError, "wrong number of arguments");
+        if (args[n - 1] == Py_None) return;
+        given_ = PyLong_AsVoidPtr(args[n - 1]);
+        if (given_ == nullptr && PyErr_Occurred()) throw python_error();
+        stream_given_ = true;
     }
     template <class F>
     F *entry() {
@@ -66,13 +71,7 @@ class Args {
         return (float)v;
     }
     // the handle, or None for the current stream
-    void *stream() {
-        PyObject *o = *at_++;
-        if (o == Py_None) return (void *)c10::cuda::getCurrentCUDAStream().stream();
-        void *p = PyLong_AsVoidPtr(o);
-        if (p == nullptr && PyErr_Occurred()) throw python_error();
-        return p;
-    }
+    void *stream() const { return stream_given_ ? given_ : (void *)c10::cuda::getCurrentCUDAStream().stream(); }
     const Tensor &tensor(const char *name, int64_t dims = -1) {
         PyObject *o = *at_++;
         if (!THPVariable_Check(o)) refuse(PyExc_TypeError, std::string(name) + " is not a tensor");
@@ -99,16 +98,21 @@ class Args {
         if (*at_ == Py_None) return ++at_, nullptr;
         return tensor(name, type, shape).data_ptr();
     }
-    // an output: allocated for None
+    // an output: allocated for None, under the stream that writes it
     Tensor output(const char *name, at::ScalarType type, Shape shape, const Tensor &like) {
-        if (*at_ == Py_None)
-            return ++at_, at::empty(at::IntArrayRef(shape), at::TensorOptions().dtype(type).device(like.device()));
-        return tensor(name, type, shape);
+        if (*at_ != Py_None) return tensor(name, type, shape);
+        ++at_;
+        c10::cuda::OptionalCUDAStreamGuard under;
+        if (stream_given_)
+            under.reset_stream(c10::cuda::getStreamFromExternal((cudaStream_t)given_, like.device().index()));
+        return at::empty(at::IntArrayRef(shape), at::TensorOptions().dtype(type).device(like.device()));
     }
     bool none() const { return *at_ == Py_None; }
 
   private:
     PyObject *const *at_;
+    void *given_ = nullptr;
+    bool stream_given_ = false;
 };
 
 // {status, outputs...}
