@@ -126,6 +126,8 @@ def _configure(lib):
     lib.moe_adapter_linear_workspace_size.restype = ctypes.c_size_t
     lib.moe_adapter_linear.argtypes = [_P, _I, _I, _P, _I, _P, _P, _P, _P, _I, _I, _P, _P, ctypes.c_size_t, _P, _P]
     lib.moe_adapter_linear.restype = _I
+    lib.moe_test_wait_limits.argtypes = [ctypes.c_int64, _I]
+    lib.moe_test_wait_limits.restype = _I
     lib.entries = {name: ctypes.cast(getattr(lib, name), _P).value for name in
                    ("moe_topk_gate", "moe_topk_gate_backward", "moe_experts", "moe_layer", "moe_adapter_linear")}
     return lib
@@ -202,6 +204,18 @@ def trace_split(rec: np.ndarray) -> tuple[np.ndarray, np.ndarray]:
 
 def status_string(code: int) -> str:
     return LIB.moe_status_string(int(code)).decode()
+
+
+@contextlib.contextmanager
+def test_wait_limits(wait_timeout_ns: int, withheld_cta: int = -1):
+    """For tests: within the context, kernels of moe_experts, moe_layer and
+    moe_adapter_linear give up a wait after ``wait_timeout_ns``, and their CTA
+    ``withheld_cta`` does not announce its first results to the others."""
+    _check(LIB.moe_test_wait_limits(wait_timeout_ns, withheld_cta), "moe_test_wait_limits")
+    try:
+        yield
+    finally:
+        LIB.moe_test_wait_limits(0, -1)
 
 
 def _ptr(t: Optional[torch.Tensor]):

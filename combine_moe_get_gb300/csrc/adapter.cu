@@ -125,6 +125,7 @@ struct AdapterArgs {
     int split;   // row by row: CTAs that share a tile
     skinny::Shape shape;
     uint32_t tmem_cols;
+    WaitLimits limits;
     TraceArgs trace;
 };
 
@@ -256,7 +257,7 @@ struct GroupedAdapter : AdapterBase {
     struct Rows {};
     __device__ Rows b_rows(const skinny::Segment &, int) const { return Rows{}; }
     __device__ bool b_ready(const skinny::Segment &s) const {
-        return skinny::wait_count(a.words + kReady + s.group, skinny::kTileWeight * tile_pieces(s));
+        return skinny::wait_count(a.words + kReady + s.group, skinny::kTileWeight * tile_pieces(s), a.limits.wait_ns);
     }
     __device__ uint32_t b_bytes(const skinny::Segment &s, int kb) const {
         if (s.phase == 0) return s.n16() * 128;
@@ -542,7 +543,7 @@ __device__ void finish_in_cluster(const RowAdapter &p, skinny::Control &c, char 
     const int steps = s.n16() / 16, kept = (steps + split - 1) / split;   // steps of 16 columns, and of them one CTA's
     constexpr int kStep = 16 * 2 * kRows;                                 // floats of a step: [column][half][row]
     if (reader) {
-        ok = Tm::agree(skinny::wait(&c.sums_full[0], 0));
+        ok = Tm::agree(skinny::wait(&c.sums_full[0], 0, a.limits.wait_ns));
         tc_fence_after();
     }
     cluster_sync();   // every ring of the cluster is free
@@ -688,6 +689,7 @@ int launch_adapter_linear(const AdapterLaunch &L) {
     a.T = T, a.K = K, a.N = N, a.L = L.num_adapters, a.r = r, a.places = P, a.split = split;
     a.shape = skinny::Shape::of(cols, false);
     a.tmem_cols = a.shape.tmem_cols(false);
+    a.limits = wait_limits();
     a.trace = trace_args();
     const size_t smem = a.shape.smem(false);
 

@@ -100,6 +100,7 @@ struct ExpertsArgs {
     uint32_t tmem_cols;
     int max_waves;
     bool local;   // every CTA makes the plan for itself
+    WaitLimits limits;
     TraceArgs trace;
 };
 
@@ -206,7 +207,7 @@ struct ExpertsProblem {
         int r[4];
     };
     __device__ bool b_ready(const skinny::Segment &s) const {
-        return skinny::wait_count(a.words + kReady + s.group, tiles[0] * skinny::kTileWeight);
+        return skinny::wait_count(a.words + kReady + s.group, tiles[0] * skinny::kTileWeight, a.limits.wait_ns);
     }
     __device__ Rows b_rows(const skinny::Segment &s, int lane) const {
         Rows rows{};
@@ -325,7 +326,7 @@ struct ExpertsProblem {
     __device__ bool finish() const {
         const int thread = threadIdx.x - Readers::first;
         bool ok = true;
-        if (thread == 0) ok = skinny::wait_count(done(), (uint64_t)G * tiles[1] * skinny::kTileWeight);
+        if (thread == 0) ok = skinny::wait_count(done(), (uint64_t)G * tiles[1] * skinny::kTileWeight, a.limits.wait_ns);
         if (!Readers::agree(ok)) return false;
         const int pieces = a.H / 8;
         const int64_t all = (int64_t)a.T * pieces;
@@ -466,6 +467,7 @@ int launch_experts(const ExpertsLaunch &L, bool words_are_zero) {
     a.shape = skinny::Shape::of(cols, e4m3, skinny::kSmemBudget - (a.local ? (int)sizeof(skinny::LocalPlan) : 0));
     a.tmem_cols = a.shape.tmem_cols(e4m3);
     a.max_waves = waves_for(cols);
+    a.limits = wait_limits();
     a.trace = trace_args();
 
     const bool overlap = tuning().overlap != 0;

@@ -113,6 +113,16 @@ TraceArgs trace_args() {
     return t;
 }
 
+namespace {
+std::atomic<int64_t> g_wait_ns{0};
+std::atomic<int> g_withheld_cta{-1};
+}  // namespace
+
+WaitLimits wait_limits() {
+    const int64_t ns = g_wait_ns.load(std::memory_order_relaxed);
+    return WaitLimits{ns > 0 ? (uint64_t)ns : kDefaultWaitNs, g_withheld_cta.load(std::memory_order_relaxed)};
+}
+
 const Tuning &tuning() {
     // Compile-time settings (moe_internal.h): nothing read from the environment,
     // so every call takes the configuration the parity tests ran.
@@ -529,6 +539,13 @@ MOE_API int moe_combine_fp8_ex(const void *partial_codes, const float *partial_s
                                uint32_t *balance, int32_t *status, void *stream) {
     return combine_fp8_common(partial_codes, partial_scales, num_partial_rows, num_tokens, hidden, num_topk,
                               token_dst_row, out, balance, status, stream);
+}
+
+MOE_API int moe_test_wait_limits(int64_t wait_timeout_ns, int withheld_cta) {
+    if (withheld_cta < -1) return MOE_ERR_INVALID_ARG;
+    moe::g_wait_ns.store(wait_timeout_ns, std::memory_order_relaxed);
+    moe::g_withheld_cta.store(withheld_cta, std::memory_order_relaxed);
+    return MOE_OK;
 }
 
 // Shape, mode and logits of a gate call, forward or backward.

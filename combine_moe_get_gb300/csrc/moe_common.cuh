@@ -13,9 +13,6 @@
 
 namespace moe {
 
-// Default bound on any spin or barrier wait inside a kernel.
-constexpr uint64_t kDefaultWaitNs = 1000000000ull;  // 1 s
-
 // ------------------------------------------------------------------ launch overlap
 //
 // Programmatic dependent launch (PTX griddepcontrol, sm_90+). A grid launched

@@ -11,6 +11,9 @@
 
 namespace moe {
 
+// Default bound on any spin or barrier wait inside a kernel.
+constexpr uint64_t kDefaultWaitNs = 1000000000ull;  // 1 s
+
 // Per-device facts, queried once per device (thread-safe).
 int device_sm_count();             // SMs of the current device
 size_t device_smem_per_sm();       // shared memory per SM (bytes)
@@ -269,6 +272,14 @@ struct CombineLaunch {
 };
 
 int launch_combine(const CombineLaunch &L);
+
+// Waits of the experts' and the adapter projection's kernels: their limit, and
+// the CTA whose first results a test withholds from the others (-1: none).
+struct WaitLimits {
+    uint64_t wait_ns;
+    int withheld_cta;
+};
+WaitLimits wait_limits();
 
 struct GateLaunch {
     const void *logits;

@@ -178,13 +178,22 @@ struct Ring {
     }
 };
 
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity) {
-    return mbar_wait_bounded(bar, parity, kDefaultWaitNs);
+// Every wait has a limit of `ns`. A role whose wait runs out gives up; the others run
+// out of theirs in turn. Gave up or not, the roles that start copies and products
+// wait for their own last ones, so that none is in flight when the CTA gives up
+// its tensor memory and its shared memory.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, uint64_t ns) {
+    return mbar_wait_bounded(bar, parity, ns);
 }
 
 // ... by a whole warp, which goes on or gives up as one.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait(bar, parity));
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64_t ns) {
+    return __all_sync(0xffffffffu, wait(bar, parity, ns));
+}
+
+// The last fills of a ring have landed.
+__device__ __forceinline__ void wait_fills(uint64_t *full, int stages, int issued, uint64_t ns) {
+    for (int fill = max(issued - stages, 0); fill < issued; ++fill) wait(&full[fill % stages], (fill / stages) & 1, ns);
 }
 
 // The readers (barrier 1) or the adders (barrier 2) as a team of kCount threads from kFirst.
@@ -218,9 +227,9 @@ __device__ __forceinline__ uint64_t ld_acquire(const uint64_t *p) {
     return v;
 }
 template <typename U>
-__device__ __forceinline__ bool wait_count(const U *p, U want) {
+__device__ __forceinline__ bool wait_count(const U *p, U want, uint64_t ns) {
     if (ld_acquire(p) >= want) return true;
-    const uint64_t deadline = globaltimer_ns() + kDefaultWaitNs;
+    const uint64_t deadline = globaltimer_ns() + ns;
     while (ld_acquire(p) < want)
         if (globaltimer_ns() > deadline) return false;
     return true;
@@ -244,17 +253,13 @@ __device__ bool load_a(const P &p, Control &c, uint32_t ring_base, const Shape s
     if (lane == 0) {
         ok = p.segments([&](const Segment &s) {
             for (int kb = s.kb0; kb < s.kb1; ++kb, r.next(), ++issued) {
-                if (!wait(&c.empty_a[r.slot], r.round ^ 1)) return false;
+                if (!wait(&c.empty_a[r.slot], r.round ^ 1, p.a.limits.wait_ns)) return false;
                 const uint32_t dst = ring_base + sh.a_at(r.slot);
                 p.a_load(s, kb, dst, &c.full_a[r.slot], policy);
             }
             return true;
         });
-        if (!ok)   // leave only when the loads in flight have landed
-            for (int i = 0; i < sh.a_stages && i < issued; ++i) {
-                const int fill = issued - 1 - i;
-                wait(&c.full_a[fill % sh.a_stages], (fill / sh.a_stages) & 1);
-            }
+        wait_fills(c.full_a, sh.a_stages, issued, p.a.limits.wait_ns);
     }
     return ok;
 }
@@ -283,7 +288,7 @@ __device__ bool load_b(const P &p, Control &c, uint32_t ring_base, float *scales
             bool go = true;
             if (lane == 0) {
                 if (kb >= s.b_from && !waited) go = p.b_ready(s);
-                if (go) go = wait(&c.empty_b[r.slot], r.round ^ 1);
+                if (go) go = wait(&c.empty_b[r.slot], r.round ^ 1, p.a.limits.wait_ns);
             }
             if (!__shfl_sync(0xffffffffu, go, 0)) return false;
             if (kb >= s.b_from && !waited) {   // other CTAs' ordinary stores, about to be read by TMA
@@ -310,11 +315,7 @@ __device__ bool load_b(const P &p, Control &c, uint32_t ring_base, float *scales
         }
         return true;
     });
-    if (!ok && lane == 0)
-        for (int i = 0; i < sh.b_stages && i < issued; ++i) {
-            const int fill = issued - 1 - i;
-            wait(&c.full_b[fill % sh.b_stages], (fill / sh.b_stages) & 1);
-        }
+    if (lane == 0) wait_fills(c.full_b, sh.b_stages, issued, p.a.limits.wait_ns);
     return ok;
 }
 
@@ -331,10 +332,12 @@ __device__ bool multiply(const P &p, Control &c, uint32_t ring_base, const Shape
         const uint32_t desc = uniform(product_desc(s.n16())), d0 = uniform(tmem + buf * 2 * sh.cols);
         const uint32_t d1 = uniform(d0 + sh.cols);
         const bool two = uniform(s.two) != 0;
-        if (!warp_wait(&c.sums_empty[buf], sums.round ^ 1)) return false;
+        if (!warp_wait(&c.sums_empty[buf], sums.round ^ 1, p.a.limits.wait_ns)) return false;
         tc_fence_after();
         for (int kb = s.kb0; kb < s.kb1; ++kb, ra.next(), rb.next()) {
-            if (!warp_wait(&c.full_a[ra.slot], ra.round) || !warp_wait(&c.full_b[rb.slot], rb.round)) return false;
+            if (!warp_wait(&c.full_a[ra.slot], ra.round, p.a.limits.wait_ns) ||
+                !warp_wait(&c.full_b[rb.slot], rb.round, p.a.limits.wait_ns))
+                return false;
             tc_fence_after();
             const uint32_t a = uniform(operand_low(ring_base + sh.a_at(ra.slot)));
             const uint32_t b = uniform(operand_low(ring_base + sh.b_at(rb.slot, false)));
@@ -362,9 +365,9 @@ __device__ bool multiply(const P &p, Control &c, uint32_t ring_base, const Shape
         sums.next();
         return true;
     });
-    if (!ok && mine) {
+    if (mine) {
         mma_commit(&c.last);
-        wait(&c.last, 0);
+        wait(&c.last, 0, p.a.limits.wait_ns);
     }
     return ok;
 }
@@ -381,8 +384,9 @@ __device__ bool multiply_e4m3(const P &p, Control &c, uint32_t ring_base, const 
     const bool ok = p.segments([&](const Segment &s) {
         const uint32_t desc = uniform(product_desc(2 * s.n16(), true));
         for (int kb = s.kb0; kb < s.kb1; ++kb, ra.next(), rb.next(), sums.next()) {
-            if (!warp_wait(&c.full_a[ra.slot], ra.round) || !warp_wait(&c.full_b[rb.slot], rb.round) ||
-                !warp_wait(&c.sums_empty[sums.slot], sums.round ^ 1))
+            if (!warp_wait(&c.full_a[ra.slot], ra.round, p.a.limits.wait_ns) ||
+                !warp_wait(&c.full_b[rb.slot], rb.round, p.a.limits.wait_ns) ||
+                !warp_wait(&c.sums_empty[sums.slot], sums.round ^ 1, p.a.limits.wait_ns))
                 return false;
             tc_fence_after();
             const uint32_t a = uniform(operand_low(ring_base + sh.a_at(ra.slot)));
@@ -402,9 +406,9 @@ __device__ bool multiply_e4m3(const P &p, Control &c, uint32_t ring_base, const 
         }
         return true;
     });
-    if (!ok && mine) {
+    if (mine) {
         mma_commit(&c.last);
-        wait(&c.last, 0);
+        wait(&c.last, 0, p.a.limits.wait_ns);
     }
     return ok;
 }
@@ -500,7 +504,7 @@ __device__ bool add_up(const P &p, const Shape sh, const Segment &s) {
     const int shares = min(s.parts, (units + kSides - 1) / kSides), me = blockIdx.x - s.cta0;
     if (me >= shares) return true;
     bool ok = true;
-    if (Tm::leader()) ok = wait_count(p.arrivals(s.line, s.cta0), (uint32_t)s.parts);
+    if (Tm::leader()) ok = wait_count(p.arrivals(s.line, s.cta0), (uint32_t)s.parts, p.a.limits.wait_ns);
     if (!Tm::agree(ok)) return false;
     const size_t half = (size_t)sh.cols * kRows;
     // unit: side unit % 4 of the 16 columns unit / 4; each of the team's groups of 128 threads takes one at a time
@@ -561,19 +565,25 @@ __device__ bool take(const P &p, Control &c, const Shape sh, const Segment &s, c
     return true;
 }
 
-// One lane: announces each segment once all reader warps have written its results.
+// One lane: announces each segment once all reader warps have written its results
+// (but for a test's withheld one).
 template <class P>
 __device__ bool announce(const P &p, Control &c) {
     uint32_t want = 0;
+    bool withheld = blockIdx.x == p.a.limits.withheld_cta;
     return p.segments([&](const Segment &s) {
         want += P::kReaders / 32;
-        const uint64_t deadline = globaltimer_ns() + kDefaultWaitNs;
+        const uint64_t deadline = globaltimer_ns() + p.a.limits.wait_ns;
         while (true) {
             uint32_t now;
             asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(now) : "r"(smem_addr(&c.written)) : "memory");
             if (now >= want) break;
             if (globaltimer_ns() > deadline) return false;
             __nanosleep(100);
+        }
+        if (withheld) {
+            withheld = false;
+            return true;
         }
         __threadfence();
         if (s.whole()) p.tile_done(s, kTileWeight);
@@ -602,7 +612,7 @@ __device__ bool read_sums(const P &p, Control &c, const Shape sh, uint32_t tmem)
             for (; phase < s.phase; ++phase)
                 if (!add_shared<Tm>(p, sh, phase, phase + 1)) return false;
         const uint32_t buf = sums.slot;
-        if (!Tm::agree(wait(&c.sums_full[buf], sums.round))) return false;
+        if (!Tm::agree(wait(&c.sums_full[buf], sums.round, p.a.limits.wait_ns))) return false;
         tc_fence_after();
         const uint32_t at = tmem + ((uint32_t)(me.row & ~31) << 16) + buf * 2 * sh.cols;
         auto each = [&](auto f) {
@@ -653,7 +663,7 @@ __device__ bool read_sums_e4m3(const P &p, Control &c, const float *b_scales, co
             for (int u = 0; u < 3; ++u) w0[u] = w0[u + 1], w1[u] = w1[u + 1];
             const int later = min(kb + 4, s.kb1 - 1);
             w0[3] = __ldg(s0 + later), w1[3] = __ldg(s1 + later);
-            if (!warp_wait(&c.sums_full[sums.slot], sums.round)) { ok = false; break; }
+            if (!warp_wait(&c.sums_full[sums.slot], sums.round, p.a.limits.wait_ns)) { ok = false; break; }
             tc_fence_after();
             const float *of_block = b_scales + (block++ % kScaleSlots) * 64 + me.first_col();
             const uint32_t at = at0 + sums.slot * 4 * sh.cols + me.first_col();

@@ -699,6 +699,17 @@ MOE_API int moe_adapter_linear(const void *x, int num_tokens, int in_features, c
                                int num_adapters, int rank, void *out, void *workspace, size_t workspace_bytes,
                                int32_t *status, void *stream);
 
+/*
+ * Failure injection for tests of moe_experts, moe_layer and moe_adapter_linear:
+ * the process's later calls bound each wait inside their kernels by
+ * `wait_timeout_ns` of the GPU's global timer (<= 0: the default, 1 s), and their
+ * CTA `withheld_cta` keeps the first results that others wait for to itself, so
+ * that those waits run out, the kernel ends and MOE_ERR_TIMEOUT is reported
+ * (-1: none, the only value for production use). The rows of an adapter
+ * projection that are not sorted by adapter wait for no other CTA's results.
+ */
+MOE_API int moe_test_wait_limits(int64_t wait_timeout_ns, int withheld_cta);
+
 /* Human-readable name of a moe_status_t value (static string). */
 MOE_API const char *moe_status_string(int status);
 
