@@ -19,7 +19,8 @@
 // eight bits: it is the operand of a product, and the rounding's effect on an
 // output is of the size of that output's own rounding. With E4M3 weights a split
 // kernel makes two codes of x before, which is exact for all elements within
-// 2^-10 of their block's largest, and off by 2^-17 of that for smaller ones.
+// 2^-14 of their block's largest, and off by 2^-22 of that at most for smaller ones:
+// channels that are thousands of times the others cost these no bits.
 //
 // The stream of the chosen experts' weights bounds it. Experts of 7168 x 2048: one
 // token, 8 in bf16 (705 MB), 118 us, 6.0 TB/s; 64 tokens' local entries, 32 in E4M3

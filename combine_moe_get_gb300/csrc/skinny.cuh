@@ -19,9 +19,9 @@
 //   bf16 weights: A and B from shared memory; sums stay in tensor memory for a
 //     whole stretch of K, double-buffered, so that the readers' work on one
 //     tile runs under the next tile's products.
-//   E4M3 weights: the activations come as the sum of two E4M3 codes under a power
-//     of two per row and block (Split, below), the second codes as further
-//     columns, so that the codes go to the tensor core as they are. A block of 128
+//   E4M3 weights: the activations come as the sum of two E4M3 codes, the second
+//     one's 32nd, under a power of two per row and block (Split, below), the second
+//     codes as further columns, so that the codes go to the tensor core as they are. A block of 128
 //     along K has its own fp32 scale per weight row, so the readers scale each
 //     block's sums and add them in registers (n <= 64); four blocks' sums in
 //     tensor memory let the products run ahead. (Turning the codes into bf16 in
@@ -413,15 +413,19 @@ __device__ bool multiply_e4m3(const P &p, Control &c, uint32_t ring_base, const 
     return ok;
 }
 
-// y scaled to |y| < 256 as the sum of two E4M3 codes. The first holds four bits,
-// what is left has at most four more of a bf16's eight: the sum is y exactly for
-// |y| >= 1/4, and off by 2^-10 at most below. Of an fp32 it is the nearest within
-// 2^-9 of y.
+// y scaled to |y| < 256 as a + b / 32, a and b E4M3 codes: what a leaves of y is 8 at
+// most, half a step of the largest codes, so 32 times that stays below 448 and has
+// five bits more to go before b's smallest step. a holds four bits, what is left
+// has at most four more of a bf16's eight: the sum is y exactly for |y| >= 2^-7,
+// and off by 2^-15 at most below, which is 2^-22 of a block's largest. Of an fp32
+// it is within 2^-9 of y, or those 2^-15. (With b taken as it is, a block with one
+// element 4096 times the others held these to six bits.)
+constexpr float kSecond = 1.0f / 32;
 struct Split {
     uint32_t first, second;   // low bytes
     __device__ __forceinline__ explicit Split(float y) {
         first = code(y);
-        second = code(y - value(first));
+        second = code((y - value(first)) * (1.0f / kSecond));
     }
     __device__ __forceinline__ static uint32_t code(float v) {
         uint16_t r;
@@ -685,8 +689,8 @@ __device__ bool read_sums_e4m3(const P &p, Control &c, const float *b_scales, co
                 const float scale[4] = {bs.x, bs.y, bs.z, bs.w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    acc[i][j] = fmaf(now0 * scale[j], v[j] + v[4 + j], acc[i][j]);
-                    acc[i][4 + j] = fmaf(now1 * scale[j], v[8 + j] + v[12 + j], acc[i][4 + j]);
+                    acc[i][j] = fmaf(now0 * scale[j], fmaf(v[4 + j], kSecond, v[j]), acc[i][j]);
+                    acc[i][4 + j] = fmaf(now1 * scale[j], fmaf(v[12 + j], kSecond, v[8 + j]), acc[i][4 + j]);
                 }
             }
             sums.next();

@@ -637,9 +637,9 @@ MOE_API size_t moe_experts_workspace_size(int num_tokens, int hidden, int interm
  *   w13_scales     [E, 2I, H/128] and w2_scales [E, H, I/128] fp32: a weight is
  *                  its code's value times its row's scale of the 128 columns (what
  *                  MOE_DISPATCH_QUANTIZE_FP8 makes of the rows). NULL for bf16.
- *                  With E4M3 weights x is taken as the sum of two E4M3 codes under a
- *                  power of two per 128 channels (exact down to 2^-10 of the block's
- *                  largest, off by 2^-17 of it below), h alike with eight bits, and a
+ *                  With E4M3 weights x is taken as the sum of an E4M3 code and a 32nd of
+ *                  another under a power of two per 128 channels (exact down to 2^-14 of
+ *                  the block's largest, off by 2^-22 of it below), h alike with eight bits, and a
  *                  block of either that is not finite makes its token's outputs NaN.
  *                  With bf16 weights h is rounded to bf16.
  *   out            [T, H] bf16, 16-byte aligned; not one of the inputs.
