@@ -549,9 +549,14 @@ def moe_topk_gate_backward(logits: torch.Tensor, topk_idx: torch.Tensor, grad_we
     return out
 
 
+def _size(entry, *sizes: int) -> int:
+    """A workspace size; 0 (invalid) where one of the sizes is no C int, which ctypes would cut to 32 bits."""
+    return int(entry(*sizes)) if max(sizes) < 2 ** 31 and min(sizes) >= -(2 ** 31) else 0
+
+
 def moe_experts_workspace_size(num_tokens: int, hidden: int, intermediate: int, num_topk: int,
                                num_experts: int) -> int:
-    return int(LIB.moe_experts_workspace_size(num_tokens, hidden, intermediate, num_topk, num_experts))
+    return _size(LIB.moe_experts_workspace_size, num_tokens, hidden, intermediate, num_topk, num_experts)
 
 
 def _experts_workspace(x, w2, num_topk, stream):
@@ -595,7 +600,7 @@ def moe_layer(x: torch.Tensor, logits: torch.Tensor, num_topk: int, w13: torch.T
 
 def moe_adapter_linear_workspace_size(num_tokens: int, in_features: int, out_features: int, num_adapters: int,
                                       rank: int) -> int:
-    return int(LIB.moe_adapter_linear_workspace_size(num_tokens, in_features, out_features, num_adapters, rank))
+    return _size(LIB.moe_adapter_linear_workspace_size, num_tokens, in_features, out_features, num_adapters, rank)
 
 
 def moe_adapter_linear(x: torch.Tensor, w: torch.Tensor, adapter_idx: torch.Tensor, a: torch.Tensor, b: torch.Tensor,

@@ -7,6 +7,7 @@
 // included. Each function takes an entry point's address
 // first, so that another build of the library can be called, and returns its
 // status and the outputs.
+#include <climits>
 #include <initializer_list>
 #include <string>
 
@@ -44,6 +45,12 @@ std::string text(at::ScalarType t) {
     }
 }
 
+// The entry points take sizes as int.
+void check_sizes(std::initializer_list<int64_t> sizes) {
+    for (int64_t n : sizes)
+        if (n > INT_MAX) refuse(PyExc_ValueError, "a size of " + std::to_string(n) + " does not fit in 32 bits");
+}
+
 // A call's positional arguments, taken in order; the stream is the last.
 class Args {
   public:
@@ -60,9 +67,11 @@ class Args {
         if (p == nullptr) throw python_error();
         return reinterpret_cast<F *>(p);
     }
-    int integer() {
-        const long v = PyLong_AsLong(*at_++);
+    int integer(const char *name) {
+        const long long v = PyLong_AsLongLong(*at_++);
         if (v == -1 && PyErr_Occurred()) throw python_error();
+        if (v < INT_MIN || v > INT_MAX)
+            refuse(PyExc_OverflowError, std::string(name) + " is " + std::to_string(v) + ", which does not fit in 32 bits");
         return (int)v;
     }
     float real() {
@@ -148,9 +157,10 @@ PyObject *topk_gate(PyObject *, PyObject *const *args, Py_ssize_t n) {
     auto *entry = a.entry<decltype(moe_topk_gate)>();
     const Tensor &logits = a.tensor("logits", 2);
     const int64_t T = logits.size(0), E = logits.size(1);
-    const int type = logits_type(logits), k = a.integer();
+    check_sizes({T, E});
+    const int type = logits_type(logits), k = a.integer("num_topk");
     const void *bias = a.pointer_or_null("bias", at::kFloat, {E});
-    const int mode = a.integer();
+    const int mode = a.integer("mode");
     const float scale = a.real();
     const Tensor idx = a.output("topk_idx", at::kLong, {T, k}, logits);
     const Tensor weights = a.output("topk_weights", at::kFloat, {T, k}, logits);
@@ -174,11 +184,12 @@ PyObject *topk_gate_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const int type = logits_type(logits);
     const Tensor &idx = a.tensor("topk_idx", 2);
     const int64_t k = idx.size(1);
+    check_sizes({T, E, k});
     if (idx.scalar_type() != at::kLong || idx.size(0) != T)
         refuse(PyExc_ValueError, "topk_idx is torch.int64 " + text(at::IntArrayRef{T, k}) + ", not " +
                                      text(idx.scalar_type()) + " " + text(idx.sizes()));
     const Tensor &grad = a.tensor("grad_weights", at::kFloat, {T, k});
-    const int mode = a.integer();
+    const int mode = a.integer("mode");
     const float scale = a.real();
     const Tensor out = a.output("out", logits.scalar_type(), {T, E}, logits);
     const Tensor &status = a.tensor("status");
@@ -202,6 +213,7 @@ struct Experts {
         const bool e4m3 = up.scalar_type() == at::kByte;
         const at::ScalarType dtype = e4m3 ? at::kByte : at::kBFloat16;
         E = down.size(0), I = down.size(2);
+        check_sizes({E, I});
         auto check = [&](const Tensor &t, const char *name, Shape shape) {
             if (t.scalar_type() != dtype || t.sizes() != at::IntArrayRef(shape))
                 refuse(PyExc_ValueError, std::string(name) + " is " + text(dtype) + " " + text(at::IntArrayRef(shape)) +
@@ -233,6 +245,7 @@ PyObject *experts(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const Experts w(a, H);
     const Tensor &idx = a.tensor("topk_idx", 2);
     const int64_t k = idx.size(1);
+    check_sizes({T, H, k});
     if (idx.scalar_type() != at::kLong || idx.size(0) != T)
         refuse(PyExc_ValueError, "topk_idx is torch.int64 " + text(at::IntArrayRef{T, k}) + ", not " +
                                      text(idx.scalar_type()) + " " + text(idx.sizes()));
@@ -257,15 +270,16 @@ PyObject *layer(PyObject *, PyObject *const *args, Py_ssize_t n) {
     auto *entry = a.entry<decltype(moe_layer)>();
     const Tensor &x = a.tensor("x", 2);
     const int64_t T = x.size(0), H = x.size(1);
+    check_sizes({T, H});
     if (x.scalar_type() != at::kBFloat16)
         refuse(PyExc_ValueError, "x is torch.bfloat16, not " + text(x.scalar_type()));
     const Experts w(a, H);
     const Tensor &logits = a.tensor("logits", 2);
     if (logits.size(0) != T || logits.size(1) != w.E)
         refuse(PyExc_ValueError, "logits are " + text(at::IntArrayRef{T, w.E}) + ", not " + text(logits.sizes()));
-    const int type = logits_type(logits), k = a.integer();
+    const int type = logits_type(logits), k = a.integer("num_topk");
     const void *bias = a.pointer_or_null("bias", at::kFloat, {w.E});
-    const int mode = a.integer();
+    const int mode = a.integer("mode");
     const float scale = a.real();
     const Tensor idx = a.output("topk_idx", at::kLong, {T, k}, x);
     const Tensor weights = a.output("topk_weights", at::kFloat, {T, k}, x);
@@ -295,6 +309,7 @@ PyObject *adapter_linear(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const Tensor &idx = a.tensor("adapter_idx", at::kInt, {T});
     const Tensor &down = a.tensor("a", 3);
     const int64_t L = down.size(0), r = down.size(1);
+    check_sizes({T, K, N, L, r});
     if (down.scalar_type() != at::kBFloat16 || down.size(2) != K)
         refuse(PyExc_ValueError, "a is torch.bfloat16 " + text(at::IntArrayRef{L, r, K}) + ", not " +
                                      text(down.scalar_type()) + " " + text(down.sizes()));
