@@ -79,8 +79,14 @@ class Args {
         if (v == -1.0 && PyErr_Occurred()) throw python_error();
         return (float)v;
     }
-    // the handle, or None for the current stream
-    void *stream() const { return stream_given_ ? given_ : (void *)c10::cuda::getCurrentCUDAStream().stream(); }
+    // the handle, or None for the current stream; the call goes to the current device
+    void *stream() const {
+        const int current = c10::cuda::current_device();
+        if (device_ != current)
+            refuse(PyExc_ValueError, "tensors on cuda:" + std::to_string(device_) + ", the current device is cuda:" +
+                                         std::to_string(current));
+        return stream_given_ ? given_ : (void *)c10::cuda::getCurrentCUDAStream(current).stream();
+    }
     const Tensor &tensor(const char *name, int64_t dims = -1) {
         PyObject *o = *at_++;
         if (!THPVariable_Check(o)) refuse(PyExc_TypeError, std::string(name) + " is not a tensor");
@@ -90,6 +96,10 @@ class Args {
                                          std::to_string(t.dim()));
         if (!t.is_cuda()) refuse(PyExc_ValueError, "libmoe_get takes CUDA tensors only");
         if (!t.is_contiguous()) refuse(PyExc_ValueError, "libmoe_get takes contiguous tensors only");
+        if (device_ < 0) device_ = t.device().index();
+        if (t.device().index() != device_)
+            refuse(PyExc_ValueError, std::string(name) + " is on " + t.device().str() + ", other tensors on cuda:" +
+                                         std::to_string(device_));
         return t;
     }
     const Tensor &tensor(const char *name, at::ScalarType type, Shape shape) {
@@ -122,6 +132,7 @@ class Args {
     PyObject *const *at_;
     void *given_ = nullptr;
     bool stream_given_ = false;
+    int device_ = -1;   // of the tensors so far
 };
 
 // {status, outputs...}
