@@ -112,6 +112,14 @@ class Args {
         }
         return tensor(name);
     }
+    // the word that kernels report to
+    int32_t *status() {
+        const Tensor &t = tensor("status");
+        if (t.scalar_type() != at::kInt || t.numel() < 1)
+            refuse(PyExc_ValueError, "status is torch.int32 of one element, not " + text(t.scalar_type()) + " " +
+                                         text(t.sizes()));
+        return static_cast<int32_t *>(t.data_ptr());
+    }
     // null for None
     void *pointer_or_null(const char *name, at::ScalarType type, Shape shape) {
         if (*at_ == Py_None) return ++at_, nullptr;
@@ -175,11 +183,11 @@ PyObject *topk_gate(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const float scale = a.real();
     const Tensor idx = a.output("topk_idx", at::kLong, {T, k}, logits);
     const Tensor weights = a.output("topk_weights", at::kFloat, {T, k}, logits);
-    const Tensor &status = a.tensor("status");
+    int32_t *const status = a.status();
     void *const stream = a.stream();
     const int code = unlocked([&] {
         return entry(logits.data_ptr(), type, (const float *)bias, (int)T, k, (int)E, mode, scale,
-                     (int64_t *)idx.data_ptr(), (float *)weights.data_ptr(), (int32_t *)status.data_ptr(), stream);
+                     (int64_t *)idx.data_ptr(), (float *)weights.data_ptr(), status, stream);
     });
     return result(code, {&idx, &weights});
     END_HANDLE_TH_ERRORS
@@ -203,11 +211,11 @@ PyObject *topk_gate_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const int mode = a.integer("mode");
     const float scale = a.real();
     const Tensor out = a.output("out", logits.scalar_type(), {T, E}, logits);
-    const Tensor &status = a.tensor("status");
+    int32_t *const status = a.status();
     void *const stream = a.stream();
     const int code = unlocked([&] {
         return entry(logits.data_ptr(), type, (const int64_t *)idx.data_ptr(), (const float *)grad.data_ptr(), (int)T,
-                     (int)k, (int)E, mode, scale, out.data_ptr(), (int32_t *)status.data_ptr(), stream);
+                     (int)k, (int)E, mode, scale, out.data_ptr(), status, stream);
     });
     return result(code, {&out});
     END_HANDLE_TH_ERRORS
@@ -262,12 +270,13 @@ PyObject *experts(PyObject *, PyObject *const *args, Py_ssize_t n) {
                                      text(idx.scalar_type()) + " " + text(idx.sizes()));
     const Tensor &weights = a.tensor("topk_weights", at::kFloat, {T, k});
     const Tensor out = a.output("out", at::kBFloat16, {T, H}, x);
-    const Tensor &workspace = a.tensor("workspace"), &status = a.tensor("status");
+    const Tensor &workspace = a.tensor("workspace");
+    int32_t *const status = a.status();
     void *const stream = a.stream();
     const int code = unlocked([&] {
         return entry(x.data_ptr(), (int)T, (int)H, (const int64_t *)idx.data_ptr(), (const float *)weights.data_ptr(),
                      (int)k, (int)w.E, w.w13, w.w13_scales, w.w2, w.w2_scales, (int)w.I, w.type, out.data_ptr(),
-                     workspace.data_ptr(), workspace.nbytes(), (int32_t *)status.data_ptr(), stream);
+                     workspace.data_ptr(), workspace.nbytes(), status, stream);
     });
     return result(code, {&out});
     END_HANDLE_TH_ERRORS
@@ -295,13 +304,14 @@ PyObject *layer(PyObject *, PyObject *const *args, Py_ssize_t n) {
     const Tensor idx = a.output("topk_idx", at::kLong, {T, k}, x);
     const Tensor weights = a.output("topk_weights", at::kFloat, {T, k}, x);
     const Tensor out = a.output("out", at::kBFloat16, {T, H}, x);
-    const Tensor &workspace = a.tensor("workspace"), &status = a.tensor("status");
+    const Tensor &workspace = a.tensor("workspace");
+    int32_t *const status = a.status();
     void *const stream = a.stream();
     const int code = unlocked([&] {
         return entry(x.data_ptr(), (int)T, (int)H, logits.data_ptr(), type, (const float *)bias, k, (int)w.E, mode, scale,
                      (int64_t *)idx.data_ptr(), (float *)weights.data_ptr(), w.w13, w.w13_scales, w.w2, w.w2_scales,
                      (int)w.I, w.type, out.data_ptr(), workspace.data_ptr(), workspace.nbytes(),
-                     (int32_t *)status.data_ptr(), stream);
+                     status, stream);
     });
     return result(code, {&out, &idx, &weights});
     END_HANDLE_TH_ERRORS
@@ -326,12 +336,13 @@ PyObject *adapter_linear(PyObject *, PyObject *const *args, Py_ssize_t n) {
                                      text(down.scalar_type()) + " " + text(down.sizes()));
     const Tensor &up = a.tensor("b", at::kBFloat16, {L, N, r}), &scales = a.tensor("scales", at::kFloat, {L});
     const Tensor out = a.output("out", at::kBFloat16, {T, N}, x);
-    const Tensor &workspace = a.tensor("workspace"), &status = a.tensor("status");
+    const Tensor &workspace = a.tensor("workspace");
+    int32_t *const status = a.status();
     void *const stream = a.stream();
     const int code = unlocked([&] {
         return entry(x.data_ptr(), (int)T, (int)K, w.data_ptr(), (int)N, (const int32_t *)idx.data_ptr(), down.data_ptr(),
                      up.data_ptr(), (const float *)scales.data_ptr(), (int)L, (int)r, out.data_ptr(),
-                     workspace.data_ptr(), workspace.nbytes(), (int32_t *)status.data_ptr(), stream);
+                     workspace.data_ptr(), workspace.nbytes(), status, stream);
     });
     return result(code, {&out});
     END_HANDLE_TH_ERRORS

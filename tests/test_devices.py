@@ -1,5 +1,5 @@
-"""Tensors on several devices, or on another one than the current, are refused. (Tensors without memory stand for those
-of a second device.)"""
+"""Tensors on several devices, or on another one than the current, are refused, and a status that is no int32 word.
+(Tensors without memory stand for those of a second device.)"""
 from __future__ import annotations
 
 import inspect
@@ -51,3 +51,11 @@ def test_one_tensor_on_another_device(f, tensors, name):
 def test_all_tensors_on_another_device_than_the_current(f, tensors):
     with pytest.raises(ValueError, match="tensors on cuda:1, the current device is cuda:0"):
         call(f, tensors, lambda n: "cuda:1")
+
+
+@pytest.mark.parametrize("f,tensors", CALLS)
+@pytest.mark.parametrize("status", [(1, U8), (1, I64), (1, F32), (0, I32)])
+def test_status_of_another_type_or_without_an_element(f, tensors, status):
+    """Kernels write four bytes to it."""
+    with pytest.raises(ValueError, match="status is torch.int32"):
+        call(f, dict(tensors, status=status), lambda n: "cuda:0")
