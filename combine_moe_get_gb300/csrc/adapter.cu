@@ -49,6 +49,7 @@ int places(int T, int L) { return T + (skinny::kPlaceStep - 1) * std::min(L + 1,
 // A block of a tile takes its bytes of A and B at a CTA's share of what L2 gives
 // them all, some 12.7 TB/s, or the tensor core's time for its columns.
 constexpr double kCtas = 152;
+constexpr double kGroupedLeast = 40;   // what the plan and the other launches of the grouped way take
 double block_us(double ctas, int cols) {
     return std::max((2 * skinny::kHalf + cols * 128) * ctas / 12.7e6, cols * 2.2e-3);
 }
@@ -69,7 +70,7 @@ double grouped_us(int T, int K, int N, int L, int r, int cols) {
     const double share = 2 * tiles <= kCtas ? std::floor(kCtas / tiles) : 1;
     const double block = block_us(std::min(kCtas, tiles * share), cols);
     const double w = std::ceil(tiles / kCtas) * kbs / share + extra / std::min(kCtas, tiles * share);
-    return 40 + T * 4e-6 * K / 7 + pieces * kbs / kCtas * 0.4 + w * block + (share > 1 ? 0.05 * cols : 0);
+    return kGroupedLeast + T * 4e-6 * K / 7 + pieces * kbs / kCtas * 0.4 + w * block + (share > 1 ? 0.05 * cols : 0);
 }
 int grouped_columns(int T, int K, int N, int L, int r) {
     const int cols = grouped_us(T, K, N, L, r, 256) < grouped_us(T, K, N, L, r, 128) ? 256 : 128;
@@ -79,8 +80,9 @@ int grouped_columns(int T, int K, int N, int L, int r) {
 // 4096 x 4096, rank 16 71 : 65, rank 128 338 : 68; of 128 adapters, rank 16 78 : 115.
 // Tiles of 128 columns against 256: 4096 rows of 16 adapters, 7168 x 4096 294 : 234;
 // 1024 rows of 8 adapters, 4096 x 4096 65 : 110.
+constexpr int64_t kMostByRow = (int64_t)1 << 26;   // elements of out: no fp32 copy of a large one
 bool grouped(int T, int K, int N, int L, int r) {
-    if ((int64_t)T * N > (int64_t)1 << 26) return true;   // no fp32 copy of a large output
+    if ((int64_t)T * N > kMostByRow) return true;
     return std::min(grouped_us(T, K, N, L, r, 128), grouped_us(T, K, N, L, r, 256)) < row_us(T, K, N, r);
 }
 
@@ -89,25 +91,31 @@ struct Space {
 };
 constexpr int kReady = skinny::kWords;   // then a word per tile of rows: its pieces' v are done
 
-Space space(int T, int K, int N, int L, int r) {
+Space grouped_space(int T, int K, int L, int r, int cols) {
     Space s{};
     skinny::Cut cut;
-    if (grouped(T, K, N, L, r)) {
-        const int P = places(T, L), cols = grouped_columns(T, K, N, L, r), tiles = (P + cols - 1) / cols;
-        s.words = cut.take(((size_t)kReady + tiles) * 4);
-        s.groups = cut.take(((size_t)tiles + std::min(L + 1, T)) * sizeof(int4));
-        s.order = cut.take((size_t)P * 4);
-        s.place = cut.take((size_t)T * 4);
-        s.tiles = cut.take(((size_t)tiles + 1) * 4);
-        s.v = cut.take((size_t)P * r * 4);               // two bf16
-        s.x = cut.take((size_t)P * K * 2);               // rows of x, sorted
-        s.partial = cut.take(skinny::partial_floats(2, cols) * 4);
-    } else {
-        s.v = cut.take((size_t)T * r * 4);               // fp32
-        s.x = cut.take((size_t)T * N * 4);               // each row's B v
-    }
+    const int P = places(T, L), tiles = (P + cols - 1) / cols;
+    s.words = cut.take(((size_t)kReady + tiles) * 4);
+    s.groups = cut.take(((size_t)tiles + std::min(L + 1, T)) * sizeof(int4));
+    s.order = cut.take((size_t)P * 4);
+    s.place = cut.take((size_t)T * 4);
+    s.tiles = cut.take(((size_t)tiles + 1) * 4);
+    s.v = cut.take((size_t)P * r * 4);               // two bf16
+    s.x = cut.take((size_t)P * K * 2);               // rows of x, sorted
+    s.partial = cut.take(skinny::partial_floats(2, cols) * 4);
     s.total = cut.at;
     return s;
+}
+Space row_space(int T, int N, int r) {
+    Space s{};
+    skinny::Cut cut;
+    s.v = cut.take((size_t)T * r * 4);               // fp32
+    s.x = cut.take((size_t)T * N * 4);               // each row's B v
+    s.total = cut.at;
+    return s;
+}
+Space space(int T, int K, int N, int L, int r) {
+    return grouped(T, K, N, L, r) ? grouped_space(T, K, L, r, grouped_columns(T, K, N, L, r)) : row_space(T, N, r);
 }
 
 struct AdapterArgs {
@@ -659,7 +667,19 @@ void choose_tiles(int T, int K, int N, int &cols, int &split) {
 
 }  // namespace
 
-size_t adapter_workspace_bytes(int T, int K, int N, int L, int r) { return space(T, K, N, L, r).total; }
+size_t adapter_workspace_need(int T, int K, int N, int L, int r) { return space(T, K, N, L, r).total; }
+
+// Room for any number of rows up to T, though the ways and widths change back and
+// forth between them: the row by row way's for as many as it may have, and the
+// grouped way's in its widest tiles, if it comes into question for any, which it
+// does not while row_us, which grows with the rows, is below the least that it takes.
+size_t adapter_workspace_bytes(int T, int K, int N, int L, int r) {
+    if (T == 0) return 0;
+    size_t most = row_space((int)std::min<int64_t>(T, kMostByRow / N), N, r).total;
+    if (T * (int64_t)N > kMostByRow || row_us(T, K, N, r) > kGroupedLeast)
+        most = std::max(most, grouped_space(T, K, L, r, std::min((places(T, L) + 15) / 16 * 16, 256)).total);
+    return most;
+}
 
 int launch_adapter_linear(const AdapterLaunch &L) {
     const int T = L.num_tokens, K = L.in_features, N = L.out_features, r = L.rank;

@@ -678,7 +678,7 @@ MOE_API int moe_adapter_linear(const void *x, int num_tokens, int in_features, c
         if (!aligned(x, 16) || !aligned(w, 16) || !aligned(adapter_idx, 4) || !aligned(a, 16) || !aligned(b, 16) ||
             !aligned(scales, 4) || !aligned(out, 16) || !aligned(workspace, 16))
             return MOE_ERR_MISALIGNED;
-        if (workspace_bytes < moe::adapter_workspace_bytes(T, K, N, num_adapters, rank)) return MOE_ERR_WORKSPACE;
+        if (workspace_bytes < moe::adapter_workspace_need(T, K, N, num_adapters, rank)) return MOE_ERR_WORKSPACE;
     }
     return moe::launch_adapter_linear(moe::AdapterLaunch{x, T, K, w, N, adapter_idx, a, b, scales, num_adapters, rank,
                                                          out, workspace, status, stream});

@@ -357,7 +357,8 @@ struct AdapterLaunch {
     void *stream;
 };
 
-size_t adapter_workspace_bytes(int T, int K, int N, int L, int r);
+size_t adapter_workspace_bytes(int T, int K, int N, int L, int r);   // for up to T rows
+size_t adapter_workspace_need(int T, int K, int N, int L, int r);    // for T rows
 int launch_adapter_linear(const AdapterLaunch &L);
 
 }  // namespace moe

@@ -71,9 +71,9 @@ class Block:
         if e4m3:
             self.w13, self.w13_scales = e4m3_rows(self.w13)
             self.w2, self.w2_scales = e4m3_rows(self.w2)
-        sizes = range(1, max_tokens + 1)
-        need = max(max(moe.moe_adapter_linear_workspace_size(t, hidden, hidden, num_adapters, rank),
-                       moe.moe_experts_workspace_size(t, hidden, intermediate, num_topk, num_experts)) for t in sizes)
+        # enough for smaller steps too
+        need = max(moe.moe_adapter_linear_workspace_size(max_tokens, hidden, hidden, num_adapters, rank),
+                   moe.moe_experts_workspace_size(max_tokens, hidden, intermediate, num_topk, num_experts))
         self.workspace = torch.empty(need, dtype=torch.uint8, device=device)
         self.status = moe.new_status(torch.device(device))
 

@@ -612,7 +612,8 @@ MOE_API int moe_topk_gate_backward(const void *logits, int logits_type, const in
 enum { MOE_WEIGHTS_BF16 = 0, MOE_WEIGHTS_E4M3 = 1 };
 
 /* Bytes of device workspace moe_experts and moe_layer need (16-byte aligned
- * pointer required). Host-only; never fails (0 for invalid sizes). */
+ * pointer required), enough for fewer tokens too. Host-only; never fails (0 for
+ * invalid sizes). */
 MOE_API size_t moe_experts_workspace_size(int num_tokens, int hidden, int intermediate, int num_topk, int num_experts);
 
 /*
@@ -666,7 +667,8 @@ MOE_API int moe_layer(const void *x, int num_tokens, int hidden, const void *log
                       size_t workspace_bytes, int32_t *status, void *stream);
 
 /* Bytes of device workspace moe_adapter_linear needs (16-byte aligned pointer
- * required). Host-only; never fails (0 for invalid sizes). */
+ * required), enough for fewer rows too. Host-only; never fails (0 for invalid
+ * sizes). */
 MOE_API size_t moe_adapter_linear_workspace_size(int num_tokens, int in_features, int out_features, int num_adapters,
                                                  int rank);
 
