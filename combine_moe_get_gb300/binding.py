@@ -8,7 +8,8 @@ to that stream: memory given up is reused in that stream's order, and an output
 that another stream reads is the caller's to keep. All computation runs in the library's CUDA kernels; there
 is no CPU path. If the library cannot be built or loaded, import fails. The
 functions behind a router's logits are for calls so small that marshalling
-them in Python took longer than the call: theirs is csrc/marshal.cpp.
+them in Python took longer than the call: theirs is csrc/marshal.cpp, which is
+built and loaded when the first of them is called.
 
 Errors the host detects come back as ``MoeError``. Errors that depend on the
 data land in the int32 ``status`` tensor (first error wins; never cleared by
@@ -22,6 +23,7 @@ import dataclasses
 import importlib.machinery
 import importlib.util
 import os
+import threading
 from typing import Optional
 
 import numpy as np
@@ -133,15 +135,26 @@ def _configure(lib):
     return lib
 
 
-def _load_marshal():
-    loader = importlib.machinery.ExtensionFileLoader("_marshal", _build.build_marshal())
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
-    loader.exec_module(module)
-    return module
+class _Marshal:
+    """The functions of csrc/marshal.cpp, built (if need be) and loaded when the first of them is used: dispatch and
+    combine do without a host compiler and torch's headers."""
+
+    _lock = threading.Lock()
+
+    def __getattr__(self, name):
+        if name.startswith("_"):
+            raise AttributeError(name)
+        with self._lock:
+            if name not in self.__dict__:
+                loader = importlib.machinery.ExtensionFileLoader("_marshal", _build.build_marshal())
+                module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
+                loader.exec_module(module)
+                self.__dict__.update((n, f) for n, f in vars(module).items() if not n.startswith("_"))
+        return self.__dict__[name]
 
 
 LIB = _load()
-_marshal = _load_marshal()
+_marshal = _Marshal()
 
 
 @contextlib.contextmanager
