@@ -145,11 +145,13 @@ class _Marshal:
         if name.startswith("_"):
             raise AttributeError(name)
         with self._lock:
-            if name not in self.__dict__:
+            if not self.__dict__:
                 loader = importlib.machinery.ExtensionFileLoader("_marshal", _build.build_marshal())
                 module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_marshal", loader))
                 loader.exec_module(module)
                 self.__dict__.update((n, f) for n, f in vars(module).items() if not n.startswith("_"))
+        if name not in self.__dict__:
+            raise AttributeError(name)
         return self.__dict__[name]
 
 

@@ -19,7 +19,6 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_get.so")
 # the same library compiled with MOE_PROFILE: every kernel warp records its start and end (moe_trace_enable)
 TRACE_LIB = os.path.join(HERE, "libmoe_get_trace.so")
-MARSHAL = os.path.join(HERE, "_marshal.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -93,18 +92,20 @@ def build_trace(force: bool = False, verbose: bool = False) -> str:
 
 
 def build_marshal(force: bool = False) -> str:
-    """_marshal.so: argument marshalling of the small calls."""
-    src = os.path.join(CSRC, "marshal.cpp")
-    inputs = [src, os.path.join(INCLUDE, "moe_get.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(MARSHAL) and all(os.path.getmtime(p) <= os.path.getmtime(MARSHAL) for p in inputs):
-        return MARSHAL
+    """Argument marshalling of the small calls. The file's name has the versions of torch and Python in it, whose
+    binary interfaces it is compiled against: another version's is never taken for it."""
     import torch
 
+    path = os.path.join(HERE, f"_marshal-{torch.__version__}-{sysconfig.get_config_var('SOABI')}.so")
+    src = os.path.join(CSRC, "marshal.cpp")
+    inputs = [src, os.path.join(INCLUDE, "moe_get.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in inputs):
+        return path
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
     includes = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(root, "include"),
                 os.path.join(root, "include", "torch", "csrc", "api", "include"), os.path.join(cuda, "include")]
-    tmp = MARSHAL + f".tmp{os.getpid()}"
+    tmp = path + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
            *(f"-I{d}" for d in includes), src, "-o", tmp, f"-L{os.path.join(root, 'lib')}", "-ltorch_python",
@@ -112,8 +113,8 @@ def build_marshal(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, MARSHAL)
-    return MARSHAL
+    os.replace(tmp, path)
+    return path
 
 
 if __name__ == "__main__":

@@ -6,6 +6,8 @@ import subprocess
 import sys
 import textwrap
 
+import pytest
+
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
@@ -28,3 +30,18 @@ def test_import_does_without_it():
             raise AssertionError("no error")
         """)], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_another_torch_gets_a_build_of_its_own(monkeypatch):
+    import torch
+
+    from combine_moe_get_gb300 import build
+    here = build.build_marshal()
+    assert build.build_marshal() == here                    # not built again
+
+    def run(cmd, **kw):
+        raise RuntimeError("built again")
+    monkeypatch.setattr(torch, "__version__", "0.0")
+    monkeypatch.setattr(build.subprocess, "run", run)
+    with pytest.raises(RuntimeError, match="built again"):
+        build.build_marshal()
