@@ -18,6 +18,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
@@ -36,6 +37,7 @@ class TopkGate(torch.autograd.Function):
         return idx, weights
 
     @staticmethod
+    @once_differentiable   # the gradient kernel has no gradient of its own
     def backward(ctx, _, grad_weights):
         logits, idx = ctx.saved_tensors
         grad = moe.moe_topk_gate_backward(logits, idx, grad_weights.contiguous(), status=ctx.status, **ctx.options)
