@@ -267,7 +267,7 @@ struct ExpertsProblem {
             side_sync();   // the columns before these are done with it
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float m = skinny::lanes_max(fabsf(h[j]));
+                const float m = lanes_max(fabsf(h[j]));
                 if ((threadIdx.x & 31) == 0) reinterpret_cast<float *>(&most[j])[quarter] = m;
             }
             side_sync();
@@ -291,7 +291,7 @@ struct ExpertsProblem {
             if (s.phase == 0) {
                 float h[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)   // off by some 2^-21, far below the eight bits that h keeps
+                for (int j = 0; j < 4; ++j)   // off by some 2^-21 near 0 and 2^-17 at -40: below the eight bits that h keeps
                     h[j] = __fdividef(v[j], 1.0f + __expf(-v[j])) * v[4 + j];
                 const int i = s.f * kRows + row;
                 if constexpr (kE4m3) {
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(256) experts_split_kernel(const SplitArgs s) {
     float most = 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) most = fmaxf(most, fabsf(x[i]));   // a NaN's code is one too
-    const skinny::BlockScale scale(skinny::lanes_max(most));
+    const skinny::BlockScale scale(lanes_max(most));
     uint32_t first = 0, second = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -196,13 +196,6 @@ __device__ __forceinline__ void store_row(__nv_bfloat16 *row, int E, int lane, c
 
 // ------------------------------------------------------------------ forward, a warp per token
 
-// The largest of the lanes' values (none of them NaN).
-__device__ __forceinline__ float lanes_max(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
-}
-
 // Takes the lowest expert whose value is `top` out of the warp's group number
 // `group`, one of [kFrom, kTo), and renews the group's maximum; returns the expert.
 // The groups' code is kept apart by the asm: merged, it would index the values in

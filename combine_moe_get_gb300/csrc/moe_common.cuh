@@ -251,6 +251,13 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
     }
 }
 
+// The largest of the warp's values; NaN loses.
+__device__ __forceinline__ float lanes_max(float v) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // ------------------------------------------------------------------ L2 cache policies
 
 __device__ __forceinline__ uint64_t policy_evict_first() {

@@ -453,13 +453,6 @@ struct BlockScale {
     }
 };
 
-// The largest of the lanes' values; NaN loses.
-__device__ __forceinline__ float lanes_max(float v) {
-    float r;
-    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-    return r;
-}
-
 // A thread's share of a tile's sums: one row, and eight values at a time.
 // P::kHalves: eight columns of one half (side % 2), every second eight of them
 // (side / 2) where four sides share the tile; else four columns of both halves,
@@ -717,9 +710,9 @@ constexpr int threads_of() {
     return ReadersOf<P>::first + P::kReaders + (P::kAdders ? kAdders : 0);
 }
 
-// Barriers and tensor memory, then `roles(problem, ring, tensor memory, ok)` on
-// every thread; `problem(ring)` makes the
-// problem after the set-up, when the ring is still unused.
+// Barriers and tensor memory, then `roles(problem, ring, tensor memory, warp, ok)`
+// on every thread; `problem(ring)` makes the problem after the set-up, when the
+// ring is still unused.
 template <class P, class Make, class Roles>
 __device__ void with_set_up(Make problem, Control &c, const uint32_t tmem_cols, Roles roles) {
     extern __shared__ char smem_raw[];
@@ -795,9 +788,9 @@ __device__ void run_one(Make problem, const Shape sh, const uint32_t tmem_cols, 
     });
 }
 
-// Words at the head of a workspace: groups (and those of a named set), finished
-// tiles (64 bits), arrivals of parts by line and CTA.
-// or of a plan in tiles their number and that of its places.
+// Words at the head of a workspace: the numbers of groups and of those with a set
+// that is named; the count of finished tiles (64 bits), or of a plan in tiles their
+// number and that of its places; arrivals of parts by line and CTA.
 constexpr int kGroupsWord = 0, kNamedWord = 1, kDoneWord = 2, kTilesWord = 2, kPlacesWord = 3, kArrivals = 4,
               kWords = 4 + kMaxLines * kMaxCtas;
 
