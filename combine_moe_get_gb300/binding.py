@@ -542,7 +542,8 @@ def moe_topk_gate(logits: torch.Tensor, num_topk: int, *, bias: Optional[torch.T
     """The experts (int64 [T, k], -1 where fewer than k are unmasked) and fp32
     weights of each token from the router's ``logits`` [T, E] (fp32 or bf16):
     the k largest logits (or score + ``bias``), weighted by their softmax or
-    sigmoid scores, normalised over the chosen ones if ``normalize``."""
+    sigmoid scores, normalised over the chosen ones if ``normalize``. No autograd
+    graph is recorded: moe_topk_gate_backward is the weights' gradient, once."""
     status = _on(stream, new_status, logits.device) if status is None else status
     code, topk_idx, topk_weights = _marshal.topk_gate(
         LIB.entries["moe_topk_gate"], logits, num_topk, bias, _gate_mode(score, normalize), scale, topk_idx,

@@ -14,9 +14,10 @@
 // by its A into v; phase 1 multiplies a tile's rows by W, whatever their adapters,
 // and then, as more K blocks of the same sums but of the piece's columns alone,
 // each piece's v by its B. v is held as the sum of two bf16 (16 bits of it), the
-// operands of two products. (Tiles of one adapter each ran W over 1.4 times as
-// many tiles with 4096 rows of 16 adapters in runs: 312 us in all.) 4096 rows, 16
-// adapters of rank 64, 7168 x 4096: 233 us, 1.06 PFLOP/s; the plan takes 10, the copy
+// operands of two products; row by row it stays in fp32, so that a row may round
+// otherwise in a batch that goes the other way. (Tiles of one adapter each ran W
+// over 1.4 times as many tiles with 4096 rows of 16 adapters in runs: 312 us in all.)
+// 4096 rows, 16 adapters of rank 64, 7168 x 4096: 230 us, 1.07 PFLOP/s; the plan takes 10, the copy
 // 17, v about 30 and W's two rounds of tiles 175. There a block of 64 KB arrives
 // every 1500 cycles where its products take 1024: L2's latency under that load, with
 // 160 KB in flight, not its bandwidth (38% of peak).
@@ -77,9 +78,11 @@ int grouped_columns(int T, int K, int N, int L, int r) {
     return std::min((places(T, L) + 15) / 16 * 16, cols);
 }
 // Measured with 152 CTAs, row by row against grouped (us): 1024 rows of 8 adapters,
-// 4096 x 4096, rank 16 71 : 65, rank 128 338 : 68; of 128 adapters, rank 16 78 : 115.
-// Tiles of 128 columns against 256: 4096 rows of 16 adapters, 7168 x 4096 294 : 234;
-// 1024 rows of 8 adapters, 4096 x 4096 65 : 110.
+// 4096 x 4096, rank 16 73 : 65, rank 128 353 : 69; of 128 adapters, rank 16 79 : 112.
+// Tiles of 128 columns against 256: 4096 rows of 16 adapters, 7168 x 4096 286 : 232;
+// 1024 rows of 8 adapters, 4096 x 4096, rank 16 65 : 83. Close to a border either way
+// may be taken: 48 adapters of rank 16, 7168 x 7168, 888 rows grouped 136, 889 row by
+// row 151 (grouped 134).
 constexpr int64_t kMostByRow = (int64_t)1 << 26;   // elements of out: no fp32 copy of a large one
 bool grouped(int T, int K, int N, int L, int r) {
     if ((int64_t)T * N > kMostByRow) return true;

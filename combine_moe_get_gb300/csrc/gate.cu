@@ -16,7 +16,9 @@
 // one CTA per token with the keys in shared memory, and in the backward pass a
 // warp that reads the row three times. 128 tokens, 256 experts, top 8 take 2.0 us,
 // which is a launch and a row's latency; rows are bound by the instructions of a
-// choice (forward) and by HBM (backward), see there.
+// choice (forward) and by HBM (backward), see there. A choice by score + bias takes a
+// score for every expert: 16384 rows of 2048 fp32 logits 76 us (sigmoid, top 8), of 256
+// 19 us where the choice by logits takes 16.
 #include <algorithm>
 #include <cfloat>
 #include <cuda_bf16.h>
@@ -94,10 +96,12 @@ __device__ __forceinline__ float warp_max(float v) {
 // exp(l - m) for l <= m, 1 at l == m also when both are infinite.
 __device__ __forceinline__ float exp_below(float l, float m) { return l == m ? 1.0f : expf(l - m); }
 
-// The same for a row's softmax sum and its gradient, m finite: __expf is off by 2 +
-// 1.16 |l - m| units in the last place, so terms that count are off by a few, and
-// it takes a third of expf's instructions (16384 rows of 2048 logits: 41 us against
-// 52 forward, 44 against 61 backward).
+// The same for a row's softmax sum and its gradient's elements, m finite: __expf is
+// off by 2 + 1.16 |l - m| units in the last place, about what the rounding of l - m
+// itself does. Terms that count are off by a few units; an element of the
+// gradient e^-20 times the largest by 3e-6 of itself. It takes a third of
+// expf's instructions (16384 rows of 2048 fp32 logits: 35.9 us against 36.7
+// forward, 44.5 against 46.2 backward; bf16 36.9 against 39.8 backward).
 __device__ __forceinline__ float exp_term(float l, float m) { return __expf(l - m); }
 
 struct Sigmoid {
