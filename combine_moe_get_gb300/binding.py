@@ -7,8 +7,9 @@ passes raw pointers, sizes and the current CUDA stream, or the one given as
 to that stream: memory given up is reused in that stream's order, and an output
 that another stream reads is the caller's to keep. All computation runs in the library's CUDA kernels; there
 is no CPU path. If the library cannot be built or loaded, import fails. The
-functions behind a router's logits are for calls so small that marshalling
-them in Python took longer than the call: theirs is csrc/marshal.cpp, which is
+functions behind a router's logits, the grouped products, the activation and
+the norm are for calls so small that marshalling them in Python took longer
+than the call: theirs is csrc/marshal.cpp, which is
 built and loaded when the first of them is called.
 
 Errors the host detects come back as ``MoeError``. Errors that depend on the
@@ -42,6 +43,7 @@ MOE_ERR_CUDA = 6
 MOE_ERR_WORKSPACE = 7
 MOE_ERR_BAD_LOGIT = 8
 MOE_ERR_BAD_ADAPTER = 9
+MOE_ERR_BAD_PREFIX = 10
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -128,10 +130,29 @@ def _configure(lib):
     lib.moe_adapter_linear_workspace_size.restype = ctypes.c_size_t
     lib.moe_adapter_linear.argtypes = [_P, _I, _I, _P, _I, _P, _P, _P, _P, _I, _I, _P, _P, ctypes.c_size_t, _P, _P]
     lib.moe_adapter_linear.restype = _I
+    lib.moe_grouped_linear.argtypes = [_P, _P, _I, _I, _P, _P, _I, _I, _P, _I, _P, _P, _P]
+    lib.moe_grouped_linear.restype = _I
+    lib.moe_grouped_linear_grad_x.argtypes = [_P, _I, _I, _P, _I, _I, _P, _P, _P, _P]
+    lib.moe_grouped_linear_grad_x.restype = _I
+    lib.moe_grouped_linear_grad_w.argtypes = [_P, _P, _I, _I, _I, _I, _P, _I, _I, _P, _P, _P]
+    lib.moe_grouped_linear_grad_w.restype = _I
+    lib.moe_swiglu.argtypes = [_P, _I, _I, _P, _P, _P, _P, _P, _P]
+    lib.moe_swiglu.restype = _I
+    lib.moe_swiglu_backward.argtypes = [_P, _P, _I, _I, _P, _P, _P, _P, _P, _P]
+    lib.moe_swiglu_backward.restype = _I
+    lib.moe_add_rms_norm.argtypes = [_P, _P, _I, _I, _P, _I, ctypes.c_float, _P, _P, _P, _P, _P, _P]
+    lib.moe_add_rms_norm.restype = _I
+    lib.moe_add_rms_norm_backward_workspace_size.argtypes = [_I, _I]
+    lib.moe_add_rms_norm_backward_workspace_size.restype = ctypes.c_size_t
+    lib.moe_add_rms_norm_backward.argtypes = [_P, _P, _I, _P, _P, _I, _I, ctypes.c_float, _P, _P, _P, ctypes.c_size_t,
+                                              _P, _P]
+    lib.moe_add_rms_norm_backward.restype = _I
     lib.moe_test_wait_limits.argtypes = [ctypes.c_int64, _I]
     lib.moe_test_wait_limits.restype = _I
     lib.entries = {name: ctypes.cast(getattr(lib, name), _P).value for name in
-                   ("moe_topk_gate", "moe_topk_gate_backward", "moe_experts", "moe_layer", "moe_adapter_linear")}
+                   ("moe_topk_gate", "moe_topk_gate_backward", "moe_experts", "moe_layer", "moe_adapter_linear",
+                    "moe_grouped_linear", "moe_grouped_linear_grad_x", "moe_grouped_linear_grad_w", "moe_swiglu",
+                    "moe_swiglu_backward", "moe_add_rms_norm", "moe_add_rms_norm_backward")}
     return lib
 
 
@@ -178,7 +199,8 @@ TRACE_KERNELS = {1: "layout_tiles", 2: "layout_direct", 3: "layout_cluster", 4: 
                  6: "layout_rows_scan", 7: "expand_layout", 8: "expand_layout_cluster", 9: "dispatch",
                  10: "dispatch_fp8_rows", 11: "combine", 12: "layout_rows", 13: "gate", 14: "gate_backward",
                  15: "experts", 16: "adapter", 17: "plan", 18: "adapter_shrink",
-                 19: "adapter_sort", 20: "adapter_expand", 21: "experts_split"}
+                 19: "adapter_sort", 20: "adapter_expand", 21: "experts_split", 22: "grouped", 23: "swiglu",
+                 24: "swiglu_backward", 25: "norm", 26: "norm_backward", 27: "norm_weight"}
 TRACE_PHASE = 0x10000   # warp field of a per-CTA phase record: TRACE_PHASE + phase (1, 2, ...)
 TRACE_PHASE_NAMES = {3: ("dependency wait", "top-k tile loaded", "bitmap and expert histogram",
                          "tile counts and first cluster barrier", "exchange and second barrier",
@@ -223,8 +245,8 @@ def status_string(code: int) -> str:
 
 @contextlib.contextmanager
 def test_wait_limits(wait_timeout_ns: int, withheld_cta: int = -1):
-    """For tests: within the context, kernels of moe_experts, moe_layer and
-    moe_adapter_linear give up a wait after ``wait_timeout_ns``, and their CTA
+    """For tests: within the context, kernels of moe_experts, moe_layer,
+    moe_adapter_linear and the grouped products give up a wait after ``wait_timeout_ns``, and their CTA
     ``withheld_cta`` does not announce its first results to the others."""
     _check(LIB.moe_test_wait_limits(wait_timeout_ns, withheld_cta), "moe_test_wait_limits")
     try:
@@ -634,3 +656,122 @@ def moe_adapter_linear(x: torch.Tensor, w: torch.Tensor, adapter_idx: torch.Tens
                                         workspace, status, _handle(stream))
     _check(code, "moe_adapter_linear")
     return out
+
+
+def moe_grouped_linear(x: torch.Tensor, w: torch.Tensor, expert_prefix: torch.Tensor, *,
+                       x_scales: Optional[torch.Tensor] = None, w_scales: Optional[torch.Tensor] = None,
+                       out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                       stream=None) -> torch.Tensor:
+    """out[r] = w[e] x[r] for the rows r of expert e, [expert_prefix[e], expert_prefix[e + 1]): an expanded
+    dispatch's rows through their experts' weights. x [M, K], w [E, N, K], bf16, or E4M3 codes (uint8) with
+    ``x_scales`` [M, K/128] and ``w_scales`` [E, N, K/128]; expert_prefix int32 [E + 1] (the layout's). Rows of no
+    expert are not written. No autograd graph is recorded: moe_grouped_linear_grad_x and _grad_w are the gradients
+    (bf16)."""
+    status = _on(stream, new_status, x.device) if status is None else status
+    code, out = _marshal.grouped_linear(LIB.entries["moe_grouped_linear"], x, w, expert_prefix, x_scales, w_scales, out,
+                                        status, _handle(stream))
+    _check(code, "moe_grouped_linear")
+    return out
+
+
+def moe_grouped_linear_grad_x(grad: torch.Tensor, w: torch.Tensor, expert_prefix: torch.Tensor, *,
+                              out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+    """The gradient [M, K] bf16 of moe_grouped_linear's rows, given ``grad`` [M, N] bf16: w[e]^T grad[r]."""
+    status = _on(stream, new_status, grad.device) if status is None else status
+    code, out = _marshal.grouped_linear_grad_x(LIB.entries["moe_grouped_linear_grad_x"], grad, w, expert_prefix, out,
+                                               status, _handle(stream))
+    _check(code, "moe_grouped_linear_grad_x")
+    return out
+
+
+def moe_grouped_linear_grad_w(grad: torch.Tensor, x: torch.Tensor, expert_prefix: torch.Tensor, *,
+                              dtype: torch.dtype = torch.float32, accumulate: bool = False,
+                              out: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                              stream=None) -> torch.Tensor:
+    """The gradient [E, N, K] of moe_grouped_linear's weights: each expert's sum of grad[r] x[r]^T, fp32 or bf16
+    (``dtype``, or that of ``out``). With ``accumulate`` it is added to what ``out`` holds."""
+    dtype = dtype if out is None else out.dtype
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"a weight's gradient is torch.float32 or torch.bfloat16, not {dtype}")
+    if accumulate and out is None:
+        raise ValueError("accumulate adds to out, which is not given")
+    status = _on(stream, new_status, grad.device) if status is None else status
+    code, out = _marshal.grouped_linear_grad_w(LIB.entries["moe_grouped_linear_grad_w"], grad, x, expert_prefix,
+                                               dtype == torch.bfloat16, bool(accumulate), out, status, _handle(stream))
+    _check(code, "moe_grouped_linear_grad_w")
+    return out
+
+
+def moe_swiglu(gate_up: torch.Tensor, *, row_weights: Optional[torch.Tensor] = None,
+               num_rows: Optional[torch.Tensor] = None, quantize_fp8: bool = False, out: Optional[torch.Tensor] = None,
+               out_scales: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+               stream=None) -> tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """(out, scales): row_weights[r] * silu(gate) * up of ``gate_up`` [M, 2I] bf16, as bf16 (scales None) or, with
+    ``quantize_fp8``, as E4M3 codes (uint8) with their scales [M, I/128]. ``num_rows`` (an int32 of one element on the
+    GPU, such as expert_prefix[-1:]): rows at or beyond it are left alone."""
+    status = _on(stream, new_status, gate_up.device) if status is None else status
+    code, out, scales = _marshal.swiglu(LIB.entries["moe_swiglu"], gate_up, row_weights, num_rows, bool(quantize_fp8),
+                                        out, out_scales, status, _handle(stream))
+    _check(code, "moe_swiglu")
+    return out, scales
+
+
+def moe_swiglu_backward(gate_up: torch.Tensor, grad: torch.Tensor, *, row_weights: Optional[torch.Tensor] = None,
+                        num_rows: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                        grad_row_weights: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                        stream=None) -> tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """(grad_gate_up [M, 2I] bf16, grad_row_weights [M] fp32 or None) of moe_swiglu's bf16 output, given ``grad``
+    [M, I] bf16; the latter where row_weights are given. ``out`` may be gate_up."""
+    status = _on(stream, new_status, gate_up.device) if status is None else status
+    code, out, weights = _marshal.swiglu_backward(LIB.entries["moe_swiglu_backward"], gate_up, grad, row_weights,
+                                                  num_rows, row_weights is not None, out, grad_row_weights, status,
+                                                  _handle(stream))
+    _check(code, "moe_swiglu_backward")
+    return out, weights
+
+
+@dataclasses.dataclass
+class Normed:
+    out: Optional[torch.Tensor]        # [T, H] bf16
+    residual: Optional[torch.Tensor]   # [T, H] bf16: x + residual
+    codes: Optional[torch.Tensor]      # [T, H] uint8, E4M3
+    scales: Optional[torch.Tensor]     # [T, H/128] fp32
+
+
+def moe_add_rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: Optional[torch.Tensor] = None,
+                     eps: float = 1e-6, bf16_out: bool = True, quantize_fp8: bool = False,
+                     out: Optional[torch.Tensor] = None, residual_out: Optional[torch.Tensor] = None,
+                     codes: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None, stream=None) -> Normed:
+    """The root-mean-square norm of h = x + residual [T, H] bf16 times ``weight`` [H] (bf16 or fp32): as bf16 (for the
+    router) unless ``bf16_out`` is false, as E4M3 codes with scales (for moe_dispatch) with ``quantize_fp8``, and h
+    itself in bf16 where there is a residual (``residual_out`` may be residual)."""
+    status = _on(stream, new_status, x.device) if status is None else status
+    code, *parts = _marshal.add_rms_norm(LIB.entries["moe_add_rms_norm"], x, residual, weight, eps, bool(bf16_out),
+                                         bool(quantize_fp8), out, residual_out, codes, scales, status, _handle(stream))
+    _check(code, "moe_add_rms_norm")
+    return Normed(*parts)
+
+
+def moe_add_rms_norm_backward_workspace_size(num_tokens: int, hidden: int) -> int:
+    return _size(LIB.moe_add_rms_norm_backward_workspace_size, num_tokens, hidden)
+
+
+def moe_add_rms_norm_backward(h: torch.Tensor, weight: torch.Tensor, grad: torch.Tensor, *,
+                              grad_residual: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                              out: Optional[torch.Tensor] = None, grad_weight: Optional[torch.Tensor] = None,
+                              workspace: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                              stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(grad_x [T, H] bf16, grad_weight [H] fp32) of moe_add_rms_norm's output, given ``grad`` [T, H] bf16 and h (its
+    residual output, or x where it had none). grad_x is the gradient of x and of the residual; ``grad_residual`` is
+    what reaches the residual output elsewhere."""
+    if workspace is None:
+        n = moe_add_rms_norm_backward_workspace_size(*h.shape)
+        workspace = _on(stream, torch.empty, max(n, 16), dtype=torch.uint8, device=h.device)
+    status = _on(stream, new_status, h.device) if status is None else status
+    code, out, grad_weight = _marshal.add_rms_norm_backward(
+        LIB.entries["moe_add_rms_norm_backward"], h, weight, grad, grad_residual, eps, out, grad_weight, workspace, status,
+        _handle(stream))
+    _check(code, "moe_add_rms_norm_backward")
+    return out, grad_weight

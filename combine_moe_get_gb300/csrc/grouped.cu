@@ -1,0 +1,834 @@
+// grouped.cu -- matrix products grouped by expert, with ragged numbers of rows:
+// the rows of expert e are [prefix[e], prefix[e+1]) (the expand layout's order).
+//
+//   forward     y[r]  = w[e] x[r]                 D = 128 features of w[e] x n rows, over K
+//   gradient    dx[r] = w[e]^T dy[r]              D = 128 columns of w[e] x n rows, over N
+//   of weights  dw[e] = sum over r of dy[r] x[r]^T   D = 128 rows of dw[e] x 256 columns, over the expert's rows
+//
+// The ragged side is the tensor core's n, which goes in steps of 16, so that an
+// expert with 140 rows costs 144 and not 256; features fill its fixed 128 rows.
+// One persistent CTA per SM; each finds its tiles by a scan over the experts'
+// numbers of rows, which stay on the device.
+//
+// Roles of a CTA's warps: 0 loads both operands by TMA, 1 issues the products,
+// 2 owns the tensor memory and finds the tiles, 3 prepares what the products
+// need besides (weights' gradients: zeros in place of the next expert's rows;
+// E4M3: the rows' scales), 4 to 11 read the sums.
+#include <algorithm>
+#include <atomic>
+
+#include <cuda_bf16.h>
+
+#include "umma.cuh"
+
+namespace moe {
+namespace grouped {
+
+constexpr int kThreads = 384;
+constexpr int kReaders = 8;                // warps that read sums
+constexpr int kFirstReader = 4;
+constexpr int kRows = 128;                 // features of a CTA's tile
+constexpr int kTileA = kRows * 128;        // bytes of A in a stage
+constexpr int kTileSlots = 4;              // tiles found ahead
+constexpr int kSmemBudget = 226 << 10;
+constexpr int kBoxRows = 32;               // rows of one copy of the ragged operand
+constexpr int kDepth = 64;                 // bf16 elements of a block along the reduction (E4M3: 128)
+constexpr int kRowGroup = 8;               // row tiles that share a pass over the features
+
+enum Op { kForward, kForwardE4m3, kGradX, kGradW };
+
+struct Tile {
+    int e;          // -1: no more
+    int a0;         // first feature of the pair's (or CTA's) tile
+    int row0;       // first row
+    int n;          // rows (weights' gradients: columns) of the tile
+    int c0;         // weights' gradients: first column
+    int blocks;     // blocks along the reduction
+    int last;       // weights' gradients: rows in the last block
+    int pad;
+};
+
+struct Args {
+    CUtensorMap a, b;
+    const int32_t *prefix;
+    const float *a_scales, *b_scales;   // E4M3: [E, N, K/128] and [M, K/128]
+    void *out;
+    int32_t *status;
+    int E, M;
+    int features, depth;     // rows of D over all tiles, length of the reduction (weights' gradients: columns of D)
+    int feature_tiles, column_tiles;
+    bool accumulate;
+    WaitLimits limits;
+    TraceArgs trace;
+};
+
+// kCols: the most columns of a tile. kCtas: CTAs of a cluster that work on one tile of kCtas * 128 features,
+// each with its part of the columns' operand.
+template <Op kOp, int kCtas, int kCols>
+struct Config {
+    static constexpr bool kE4m3 = kOp == kForwardE4m3;
+    static constexpr int kTileB = kCols / kCtas * 128;
+    static constexpr int kSums = kE4m3 ? (512 / kCols < 4 ? 512 / kCols : 4) : 2;
+    static constexpr int kScaleBytes = kE4m3 ? kSums * kCols * 4 : 0;
+    static constexpr int kStages = (kSmemBudget - 1024 - 2048 - kScaleBytes) / (kTileA + kTileB) < 12
+                                       ? (kSmemBudget - 1024 - 2048 - kScaleBytes) / (kTileA + kTileB) : 12;
+    static constexpr int kTmemCols = kSums * kCols <= 64 ? 64 : kSums * kCols <= 128 ? 128 : kSums * kCols <= 256 ? 256 : 512;
+    static constexpr int kBlock = kE4m3 ? 128 : kDepth;
+    static constexpr size_t smem() { return 1024 + (size_t)kStages * (kTileA + kTileB) + kScaleBytes; }
+    static_assert(kStages >= 3 && kSums >= 2);
+    // who takes a tile from the scan: loads, products (one CTA of a pair), warp 3 (if it has work), readers
+    static constexpr bool kHelper = kOp == kGradW || kE4m3;
+};
+
+constexpr int kMaxStages = 12, kMaxSums = 4;
+struct Control {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t masked_full[kMaxStages];   // a block whose rows past the expert's end are to be zeroed
+    uint64_t sums_full[kMaxSums], sums_empty[kMaxSums];
+    uint64_t scales_full[kMaxSums], scales_empty[kMaxSums];
+    uint64_t tile_full[kTileSlots], tile_empty[kTileSlots];
+    uint64_t last;
+    Tile tiles[kTileSlots];
+    uint32_t tmem;
+};
+
+// ------------------------------------------------------------------ PTX of pairs
+
+__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {   // of the cluster's CTA `rank`
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_expect_at(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, uint64_t ns) {
+    if (try_wait_cluster(bar, parity)) return true;
+    const uint64_t deadline = globaltimer_ns() + ns;
+    while (true) {
+        if (try_wait_cluster(bar, parity)) return true;
+        if (globaltimer_ns() > deadline) return false;
+    }
+}
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64_t ns) {
+    return __all_sync(0xffffffffu, wait(bar, parity, ns));
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Tiles by TMA; `bar` is a shared::cluster address, of this CTA or its pair's first.
+template <int kCtas>
+__device__ __forceinline__ void load2(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar, uint64_t policy) {
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3}], [%4], %5;"
+            ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar), "l"(policy) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3}], [%4], %5;"
+            ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar), "l"(policy) : "memory");
+}
+template <int kCtas>
+__device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint32_t bar,
+                                      uint64_t policy) {
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3, %4}], [%5], %6;"
+            ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
+            "[%0], [%1, {%2, %3, %4}], [%5], %6;"
+            ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "l"(policy) : "memory");
+}
+
+template <int kCtas>
+__device__ __forceinline__ void tmem_take(uint32_t *slot, uint32_t cols) {
+    if constexpr (kCtas == 2) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_addr(slot)), "r"(cols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        tmem_alloc(slot, cols);
+    }
+}
+template <int kCtas>
+__device__ __forceinline__ void tmem_give(uint32_t base, uint32_t cols) {
+    if constexpr (kCtas == 2)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(base), "r"(cols));
+    else
+        tmem_free(base, cols);
+}
+
+// Operand whose rows of 128 bytes are steps of the reduction, 64 bf16 of M or N each (128-byte swizzle): 8 steps are
+// 1024 bytes apart (the high word's stride), the next 64 of M or N `chunk` bytes (the low word's).
+__device__ __forceinline__ uint32_t operand_low_mn(uint32_t addr, uint32_t chunk) {
+    return ((addr >> 4) & 0x3fff) | (chunk >> 4) << 16;
+}
+
+template <int kCtas, bool kE4m3>
+__device__ __forceinline__ void product(uint32_t d, uint32_t a_low, uint32_t b_low, uint32_t desc, bool add) {
+    if constexpr (kCtas == 1) {
+        if constexpr (kE4m3) mma_e4m3(d, a_low, b_low, desc, add);
+        else mma_ss(d, a_low, b_low, desc, add);
+    } else if constexpr (kE4m3) {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d), "l"(operand_desc(a_low)), "l"(operand_desc(b_low)), "r"(desc), "r"((uint32_t)add) : "memory");
+    } else {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+            ::"r"(d), "l"(operand_desc(a_low)), "l"(operand_desc(b_low)), "r"(desc), "r"((uint32_t)add) : "memory");
+    }
+}
+// One arrival on `bar` of each CTA of the tile when the products so far are complete.
+template <int kCtas>
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    if constexpr (kCtas == 2)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+            ::"r"(smem_addr(bar)), "h"((uint16_t)3) : "memory");
+    else
+        mma_commit(bar);
+}
+
+// ... of this CTA's alone.
+template <int kCtas>
+__device__ __forceinline__ void commit_here(uint64_t *bar) {
+    if constexpr (kCtas == 2)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                     ::"r"(smem_addr(bar)) : "memory");
+    else
+        mma_commit(bar);
+}
+
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float *v) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// ------------------------------------------------------------------ tiles
+
+__device__ __forceinline__ int round16(int n) { return (n + 15) & ~15; }
+
+// Rows of expert e, whatever the prefix holds: inside [0, M], in order.
+struct Range {
+    int lo, hi;
+    bool bad;
+};
+__device__ __forceinline__ Range rows_of(const Args &a, int e) {
+    const int p0 = __ldg(a.prefix + e), p1 = __ldg(a.prefix + e + 1);
+    Range r;
+    r.lo = min(max(p0, 0), a.M);
+    r.hi = min(max(p1, r.lo), a.M);
+    r.bad = r.lo != p0 || r.hi != p1;
+    return r;
+}
+
+struct TileRing {
+    int slot = 0;
+    uint32_t round = 0;
+    __device__ void next() {
+        if (++slot == kTileSlots) slot = 0, round ^= 1;
+    }
+};
+
+// By warp 2: hands every tile of this CTA (or pair) to the others, in order.
+template <Op kOp, int kCtas, int kCols>
+__device__ bool find_tiles(const Args &a, Control &c) {
+    using C = Config<kOp, kCtas, kCols>;
+    const int lane = threadIdx.x & 31;
+    TileRing ring;
+    bool ok = true;
+    auto hand = [&](const Tile &t) {   // by lane 0
+        if (lane == 0) {
+            ok = wait(&c.tile_empty[ring.slot], ring.round ^ 1, a.limits.wait_ns);
+            if (ok) {
+                c.tiles[ring.slot] = t;
+                mbar_arrive(&c.tile_full[ring.slot]);
+            }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        ring.next();
+        return ok;
+    };
+    int64_t t = blockIdx.x / kCtas;
+    const int64_t step = gridDim.x / kCtas;
+    if constexpr (kOp == kGradW) {
+        const int per = a.feature_tiles * a.column_tiles;
+        const int64_t total = (int64_t)a.E * per;
+        int at = -1;
+        Range r{};
+        for (; t < total; t += step) {
+            const int e = (int)(t / per), i = (int)(t - (int64_t)e * per);
+            if (e != at) {
+                r = rows_of(a, at = e);
+                if (r.bad && lane == 0) report(a.status, MOE_ERR_BAD_PREFIX);
+            }
+            const int rows = r.hi - r.lo, f = i / a.column_tiles, col = i - f * a.column_tiles;
+            const int blocks = (rows + kDepth - 1) / kDepth;
+            if (!hand(Tile{e, f * kCtas * kRows, r.lo, min(kCols, a.depth - col * kCols), col * kCols, blocks,
+                           rows - (blocks - 1) * kDepth, 0}))
+                return false;
+        }
+    } else {
+        const int F = a.feature_tiles, blocks = (a.depth + C::kBlock - 1) / C::kBlock;
+        int64_t before = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            Range r{};
+            if (e0 + lane < a.E) r = rows_of(a, e0 + lane);
+            if (r.bad && blockIdx.x == 0) report(a.status, MOE_ERR_BAD_PREFIX);
+            const int rows = r.hi - r.lo, R = (rows + kCols - 1) / kCols;
+            const int64_t mine = (int64_t)R * F;
+            int64_t upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
+            while (t < before + all) {
+                const int l = __ffs(__ballot_sync(0xffffffffu, before + upto > t)) - 1;
+                const int64_t i = t - before - __shfl_sync(0xffffffffu, upto - mine, l);
+                const int er = __shfl_sync(0xffffffffu, rows, l), eR = __shfl_sync(0xffffffffu, R, l);
+                const int lo = __shfl_sync(0xffffffffu, r.lo, l);
+                // row tiles of equal size, eight of them to a pass over the features
+                const int per = round16((er + eR - 1) / eR);
+                const int64_t pass = (int64_t)kRowGroup * F;
+                const int g = (int)(i / pass), in = (int)(i - g * pass), width = min(kRowGroup, eR - g * kRowGroup);
+                const int f = in / width, rt = g * kRowGroup + in - f * width;
+                if (!hand(Tile{e0 + l, f * kCtas * kRows, lo + rt * per, min(per, er - rt * per), 0, blocks, 0, 0}))
+                    return false;
+                t += step;
+            }
+            before += all;
+        }
+    }
+    return hand(Tile{-1, 0, 0, 0, 0, 0, 0, 0});
+}
+
+// f(tile, its number) for each tile, by a whole warp.
+template <class F>
+__device__ bool each_tile(const Args &a, Control &c, F f) {
+    TileRing ring;
+    for (;; ring.next()) {
+        if (!warp_wait(&c.tile_full[ring.slot], ring.round, a.limits.wait_ns)) return false;
+        const Tile t = c.tiles[ring.slot];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&c.tile_empty[ring.slot]);
+        if (t.e < 0) return true;
+        if (!f(t)) return false;
+    }
+}
+
+struct Ring {
+    int slot = 0, stages;
+    uint32_t round = 0;
+    __device__ explicit Ring(int n) : stages(n) {}
+    __device__ void next() {
+        if (++slot == stages) slot = 0, round ^= 1;
+    }
+};
+
+// ------------------------------------------------------------------ roles
+
+template <Op kOp, int kCtas, int kCols>
+__device__ bool load(const Args &a, Control &c, uint32_t ring_base, uint32_t rank) {
+    using C = Config<kOp, kCtas, kCols>;
+    Ring r(C::kStages);
+    int issued = 0;
+    const bool mine = elect_one();
+    // weights of one pass are read once or by a few CTAs at about the same time; rows by every feature's tile
+    const uint64_t once = policy_evict_first(), often = policy_evict_last();
+    bool ok = (int)blockIdx.x != a.limits.withheld_cta;
+    ok = ok && each_tile(a, c, [&](const Tile &t) {
+        const int a0 = t.a0 + (int)rank * kRows;
+        const int part = kOp == kGradW ? kCols / kCtas : round16(t.n) / kCtas;   // columns that this CTA loads
+        const int boxes = kOp == kGradW ? part / 64 : (part + kBoxRows - 1) / kBoxRows;
+        const uint32_t bytes = kTileA + boxes * (kOp == kGradW ? 64 : kBoxRows) * 128;
+        for (int kb = 0; kb < t.blocks; ++kb, r.next(), ++issued) {
+            if (!warp_wait(&c.empty[r.slot], r.round ^ 1, a.limits.wait_ns)) return false;
+            const uint32_t to_a = ring_base + r.slot * (kTileA + C::kTileB), to_b = to_a + kTileA;
+            const bool mask = kOp == kGradW && kb == t.blocks - 1 && t.last < kDepth;
+            if (mine) {
+                // what the products wait for lies in the pair's first CTA; a block to be masked is this CTA's affair first
+                const uint32_t bar = mask ? peer_addr(&c.masked_full[r.slot], rank) : peer_addr(&c.full[r.slot], 0);
+                arrive_expect_at(bar, bytes);
+                if constexpr (kOp == kForward || kOp == kForwardE4m3) {
+                    load3<kCtas>(to_a, &a.a, kb * C::kBlock, a0, t.e, bar, once);
+                } else if constexpr (kOp == kGradX) {
+                    for (int i = 0; i < 2; ++i) load3<kCtas>(to_a + i * 8192, &a.a, a0 + i * 64, kb * kDepth, t.e, bar, once);
+                } else {
+                    for (int i = 0; i < 2; ++i) load2<kCtas>(to_a + i * 8192, &a.a, a0 + i * 64, t.row0 + kb * kDepth, bar, often);
+                }
+                for (int i = 0; i < boxes; ++i) {
+                    if constexpr (kOp == kGradW)
+                        load2<kCtas>(to_b + i * 8192, &a.b, t.c0 + (int)rank * part + i * 64, t.row0 + kb * kDepth, bar, often);
+                    else
+                        load2<kCtas>(to_b + i * kBoxRows * 128, &a.b, kb * C::kBlock, t.row0 + (int)rank * part + i * kBoxRows,
+                                     bar, often);
+                }
+            }
+            __syncwarp();
+        }
+        return true;
+    });
+    // the last fills have been used, so none is in flight
+    for (int fill = max(issued - C::kStages, 0); fill < issued; ++fill)
+        warp_wait(&c.empty[fill % C::kStages], (fill / C::kStages) & 1, a.limits.wait_ns);
+    return ok;
+}
+
+template <Op kOp, int kCtas, int kCols>
+__device__ bool multiply(const Args &a, Control &c, uint32_t ring_base, uint32_t tmem) {
+    using C = Config<kOp, kCtas, kCols>;
+    const bool mine = elect_one();
+    Ring r(C::kStages), sums(C::kSums);
+    constexpr bool kAmn = kOp == kGradX || kOp == kGradW, kBmn = kOp == kGradW;
+    // steps of one product along the reduction, in the descriptors' units of 16 bytes
+    constexpr uint32_t kStepA = kAmn ? 2048 >> 4 : 2, kStepB = kBmn ? 2048 >> 4 : 2;
+    const bool ok = each_tile(a, c, [&](const Tile &t) {
+        const int n = round16(t.n);
+        const uint32_t desc = 1u << 4 | (C::kE4m3 ? 0 : 1u << 7 | 1u << 10) | (uint32_t)kAmn << 15 | (uint32_t)kBmn << 16 |
+                              (uint32_t)(n >> 3) << 17 | (uint32_t)(kCtas * kRows >> 4) << 24;
+        if (t.blocks == 0) return true;   // weights' gradients of an expert without rows: nothing to wait for
+        if (!C::kE4m3 && !warp_wait(&c.sums_empty[sums.slot], sums.round ^ 1, a.limits.wait_ns)) return false;
+        for (int kb = 0; kb < t.blocks; ++kb, r.next()) {
+            if (C::kE4m3 && !warp_wait(&c.sums_empty[sums.slot], sums.round ^ 1, a.limits.wait_ns)) return false;
+            if (!warp_wait(&c.full[r.slot], r.round, a.limits.wait_ns)) return false;
+            tc_fence_after();
+            const uint32_t d = uniform(tmem + sums.slot * kCols);
+            const uint32_t at = ring_base + r.slot * (kTileA + C::kTileB);
+            const uint32_t al = uniform(kAmn ? operand_low_mn(at, 8192) : operand_low(at));
+            const uint32_t bl = uniform(kBmn ? operand_low_mn(at + kTileA, 8192) : operand_low(at + kTileA));
+            if (mine) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    product<kCtas, C::kE4m3>(d, al + j * kStepA, bl + j * kStepB, desc, j > 0 || (!C::kE4m3 && kb > 0));
+                commit<kCtas>(&c.empty[r.slot]);
+                if (C::kE4m3 || kb == t.blocks - 1) commit<kCtas>(&c.sums_full[sums.slot]);
+            }
+            __syncwarp();
+            if (C::kE4m3) sums.next();
+        }
+        if (!C::kE4m3) sums.next();
+        return true;
+    });
+    if (mine) commit_here<kCtas>(&c.last);   // kept waiting or not, no product is in flight behind this
+    __syncwarp();
+    warp_wait(&c.last, 0, a.limits.wait_ns);
+    return ok;
+}
+
+// Weights' gradients: the last block of an expert's rows goes on into the next
+// expert's. Zeros in both operands take those rows out (in one alone, an infinity
+// in the other would still make NaN).
+template <int kCtas, int kCols>
+__device__ bool mask_blocks(const Args &a, Control &c, char *ring) {
+    using C = Config<kGradW, kCtas, kCols>;
+    Ring r(C::kStages);
+    uint32_t seen = 0;   // phases of each slot's masked_full, a bit a slot
+    const int lane = threadIdx.x & 31;
+    return each_tile(a, c, [&](const Tile &t) {
+        if (t.blocks == 0) return true;
+        for (int kb = 0; kb < t.blocks - 1; ++kb) r.next();
+        if (t.last < kDepth) {
+            if (!warp_wait(&c.masked_full[r.slot], seen >> r.slot & 1, a.limits.wait_ns)) return false;
+            seen ^= 1u << r.slot;
+            char *at = ring + (size_t)r.slot * (kTileA + C::kTileB);
+            constexpr int kChunks = 2 + kCols / kCtas / 64;
+            for (int i = lane; i < kChunks * (kDepth - t.last) * 8; i += 32) {   // 16 bytes each
+                const int chunk = i / ((kDepth - t.last) * 8), in = i - chunk * (kDepth - t.last) * 8;
+                *reinterpret_cast<int4 *>(at + chunk * 8192 + t.last * 128 + in * 16) = make_int4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) arrive_at(peer_addr(&c.full[r.slot], 0));
+        }
+        r.next();
+        return true;
+    });
+}
+
+// E4M3: the scales of a block's rows, beside the block's sums.
+template <int kCtas, int kCols>
+__device__ bool load_scales(const Args &a, Control &c, float *scales) {
+    using C = Config<kForwardE4m3, kCtas, kCols>;
+    const int lane = threadIdx.x & 31;
+    Ring r(C::kSums);
+    return each_tile(a, c, [&](const Tile &t) {
+        constexpr int kPer = (kCols + 31) / 32;
+        const float *from[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) from[i] = a.b_scales + (size_t)(t.row0 + min(lane + 32 * i, t.n - 1)) * t.blocks;
+        float next[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) next[i] = __ldg(from[i]);
+        for (int kb = 0; kb < t.blocks; ++kb, r.next()) {
+            if (!warp_wait(&c.scales_empty[r.slot], r.round ^ 1, a.limits.wait_ns)) return false;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i)
+                if (lane + 32 * i < kCols) scales[r.slot * kCols + lane + 32 * i] = next[i];
+            if (kb + 1 < t.blocks)
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) next[i] = __ldg(from[i] + kb + 1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&c.scales_full[r.slot]);
+        }
+        return true;
+    });
+}
+
+// Lanes hold features, registers rows: neighbouring lanes exchange halves of two
+// rows, so that a lane writes two features of one row (64 bytes of a row a warp).
+__device__ __forceinline__ void store_rows(const Args &a, const Tile &t, int f, int col, const float (&v)[16]) {
+    const int odd = threadIdx.x & 1;
+    uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                                 (size_t)(t.row0 + col + odd) * a.features + (f & ~1));
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+        const __nv_bfloat162 pair = odd ? __floats2bfloat162_rn(got, v[j + 1]) : __floats2bfloat162_rn(v[j], got);
+        if (f < a.features && col + j + odd < t.n)
+            *reinterpret_cast<__nv_bfloat162 *>(out + (size_t)j * (a.features / 2)) = pair;
+    }
+}
+
+// A lane's row of a weight's gradient: 16 columns from `col`.
+template <typename Out>
+__device__ __forceinline__ void store_weights(const Args &a, const Tile &t, int f, int col, float (&v)[16]) {
+    if (f >= a.features) return;
+    Out *out = static_cast<Out *>(a.out) + ((size_t)t.e * a.features + f) * a.depth + t.c0 + col;
+#pragma unroll
+    for (int j = 0; j < 16; j += 8) {   // sizes are multiples of 8
+        if (col + j >= t.n) break;
+        if constexpr (sizeof(Out) == 4) {
+            float4 *p = reinterpret_cast<float4 *>(out + j);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float4 x = make_float4(v[j + 4 * i], v[j + 4 * i + 1], v[j + 4 * i + 2], v[j + 4 * i + 3]);
+                if (a.accumulate) {
+                    const float4 y = p[i];
+                    x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                }
+                p[i] = x;
+            }
+        } else {
+            uint4 *p = reinterpret_cast<uint4 *>(out + j);
+            uint4 x = {};
+            __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&x);
+            if (a.accumulate) {
+                x = *p;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 y = __bfloat1622float2(h[i]);
+                    v[j + 2 * i] += y.x, v[j + 2 * i + 1] += y.y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[j + 2 * i], v[j + 2 * i + 1]);
+            *p = x;
+        }
+    }
+}
+
+// Warps 4 to 11: a quarter of tensor memory's lanes each, every other 16 columns.
+template <Op kOp, int kCtas, int kCols, typename Out>
+__device__ bool read_sums(const Args &a, Control &c, const float *scales, uint32_t tmem, uint32_t rank) {
+    using C = Config<kOp, kCtas, kCols>;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, q = warp % 4, half = (warp - kFirstReader) / 4;
+    const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
+    Ring sums(C::kSums);
+    constexpr int kChunks = (kCols + 31) / 32;
+    return each_tile(a, c, [&](const Tile &t) {
+        const int f = t.a0 + (int)rank * kRows + q * 32 + lane;
+        if constexpr (C::kE4m3) {
+            float sum[kChunks][16] = {};
+            // this lane's weight row's scales, one a block
+            const float *sw = a.a_scales + ((size_t)t.e * a.features + min(f, a.features - 1)) * t.blocks;
+            float next = __ldg(sw);
+            for (int kb = 0; kb < t.blocks; ++kb, sums.next()) {
+                const float scale = next;
+                if (kb + 1 < t.blocks) next = __ldg(sw + kb + 1);
+                if (!warp_wait(&c.scales_full[sums.slot], sums.round, a.limits.wait_ns)) return false;
+                if (!warp_wait(&c.sums_full[sums.slot], sums.round, a.limits.wait_ns)) return false;
+                tc_fence_after();
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) {
+                    const int col = (2 * i + half) * 16;
+                    if (col < t.n) {
+                        float v[16];
+                        tmem_load16(lanes + sums.slot * kCols + col, v);
+                        tmem_load_wait(v);
+                        const float4 *sx = reinterpret_cast<const float4 *>(scales + sums.slot * kCols + col);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float4 s = sx[j];
+                            sum[i][4 * j] = fmaf(v[4 * j], scale * s.x, sum[i][4 * j]);
+                            sum[i][4 * j + 1] = fmaf(v[4 * j + 1], scale * s.y, sum[i][4 * j + 1]);
+                            sum[i][4 * j + 2] = fmaf(v[4 * j + 2], scale * s.z, sum[i][4 * j + 2]);
+                            sum[i][4 * j + 3] = fmaf(v[4 * j + 3], scale * s.w, sum[i][4 * j + 3]);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    arrive_at(peer_addr(&c.sums_empty[sums.slot], 0));
+                    mbar_arrive(&c.scales_empty[sums.slot]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) {
+                const int col = (2 * i + half) * 16;
+                if (col < t.n) store_rows(a, t, f, col, sum[i]);
+            }
+        } else {
+            const bool some = t.blocks > 0;
+            if (some && !warp_wait(&c.sums_full[sums.slot], sums.round, a.limits.wait_ns)) return false;
+            tc_fence_after();
+            for (int col = half * 16; col < t.n; col += 32) {
+                float v[16] = {};
+                if (some) {
+                    tmem_load16(lanes + sums.slot * kCols + col, v);
+                    tmem_load_wait(v);
+                }
+                if constexpr (kOp == kGradW) {
+                    if (some || !a.accumulate) store_weights<Out>(a, t, f, col, v);
+                } else {
+                    store_rows(a, t, f, col, v);
+                }
+            }
+            if (some) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) arrive_at(peer_addr(&c.sums_empty[sums.slot], 0));
+                sums.next();
+            }
+        }
+        return true;
+    });
+}
+
+template <Op kOp, int kCtas, int kCols, typename Out>
+__global__ __launch_bounds__(kThreads, 1) void grouped_kernel(const __grid_constant__ Args a) {
+    using C = Config<kOp, kCtas, kCols>;
+    const WarpTrace trace(a.trace, MOE_TRACE_GROUPED);
+    extern __shared__ char smem_raw[];
+    __shared__ Control c;
+    char *ring = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    float *scales = reinterpret_cast<float *>(ring + C::kStages * (kTileA + C::kTileB));
+    const uint32_t ring_base = smem_addr(ring);
+    const int warp = threadIdx.x / 32;
+    const uint32_t rank = kCtas == 1 ? 0 : blockIdx.x % kCtas;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::kStages; ++i) {
+            mbar_init(&c.full[i], kCtas);
+            mbar_init(&c.empty[i], 1);
+            mbar_init(&c.masked_full[i], 1);
+        }
+        for (int i = 0; i < C::kSums; ++i) {
+            mbar_init(&c.sums_full[i], 1);
+            mbar_init(&c.sums_empty[i], kCtas * kReaders);
+            mbar_init(&c.scales_full[i], 1);
+            mbar_init(&c.scales_empty[i], kReaders);
+        }
+        for (int i = 0; i < kTileSlots; ++i) {
+            mbar_init(&c.tile_full[i], 1);
+            mbar_init(&c.tile_empty[i], 1 + (rank == 0) + C::kHelper + kReaders);
+        }
+        mbar_init(&c.last, 1);
+        fence_barrier_init();
+        tma_prefetch_map(&a.a);
+        tma_prefetch_map(&a.b);
+    }
+    if (warp == 2) tmem_take<kCtas>(&c.tmem, C::kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (kCtas == 2) cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = c.tmem;
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    bool ok = true;
+    if (warp == 0) {
+        ok = load<kOp, kCtas, kCols>(a, c, ring_base, rank);
+    } else if (warp == 1) {
+        if (rank == 0) ok = multiply<kOp, kCtas, kCols>(a, c, ring_base, tmem);
+    } else if (warp == 2) {
+        ok = find_tiles<kOp, kCtas, kCols>(a, c);
+    } else if (warp == 3) {
+        if constexpr (kOp == kGradW) ok = mask_blocks<kCtas, kCols>(a, c, ring);
+        if constexpr (C::kE4m3) ok = load_scales<kCtas, kCols>(a, c, scales);
+    } else {
+        ok = read_sums<kOp, kCtas, kCols, Out>(a, c, scales, tmem, rank);
+    }
+    if (!ok && (threadIdx.x & 31) == 0) report(a.status, MOE_ERR_TIMEOUT);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (kCtas == 2) cluster_sync();   // no arrival or product of the other CTA is under way
+    tc_fence_after();
+    if (warp == 2) tmem_give<kCtas>(tmem, C::kTmemCols);
+}
+
+// ------------------------------------------------------------------ host
+
+// CTA pairs that are resident at once (0: none): GPCs with an odd number of SMs leave one over.
+template <Op kOp, int kCtas, int kCols, typename Out>
+int resident() {
+    auto kernel = grouped_kernel<kOp, kCtas, kCols, Out>;
+    if (kCtas == 1) return device_sm_count();
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(device_sm_count() / kCtas * kCtas);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = Config<kOp, kCtas, kCols>::smem();
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim = {kCtas, 1, 1};
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) n = 1;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n * kCtas;
+}
+
+template <Op kOp, int kCtas, int kCols, typename Out = __nv_bfloat16>
+int launch(Args &a, int64_t most_tiles, cudaStream_t s) {
+    using C = Config<kOp, kCtas, kCols>;
+    auto kernel = grouped_kernel<kOp, kCtas, kCols, Out>;
+    const int rc = ensure_dynamic_smem((const void *)kernel, C::smem());
+    if (rc != MOE_OK) return rc;
+    const int64_t ctas = std::min<int64_t>(resident<kOp, kCtas, kCols, Out>(), most_tiles * kCtas);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = C::smem();
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    int n = 0;
+    if (kCtas > 1) {
+        attr[n].id = cudaLaunchAttributeClusterDimension;
+        attr[n++].val.clusterDim = {kCtas, 1, 1};
+    }
+    if (tuning().overlap) {
+        attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[n++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    cfg.attrs = attr;
+    cfg.numAttrs = n;
+    return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace grouped
+
+namespace {
+using namespace grouped;
+
+constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// Row tiles that M rows in E groups make at most.
+int64_t most_row_tiles(int M, int E, int cols) { return (int64_t)M / cols + std::min(M, E); }
+
+template <Op kOp, int kCtas, int kCols>
+int launch_rows(Args &a, cudaStream_t s) {
+    a.feature_tiles = ceil_div(a.features, kCtas * kRows);
+    return launch<kOp, kCtas, kCols>(a, most_row_tiles(a.M, a.E, kCols) * a.feature_tiles, s);
+}
+}  // namespace
+
+int launch_grouped_linear(const GroupedLaunch &L) {
+    const bool e4m3 = L.x_scales != nullptr;
+    Args a{};
+    if (!make_tensor_map3(&a.a, L.w, e4m3, L.num_experts, L.out_features, L.in_features, kRows) ||
+        !make_tensor_map(&a.b, L.x, e4m3, L.num_rows, L.in_features, kBoxRows))
+        return MOE_ERR_CUDA;
+    a.prefix = L.expert_prefix;
+    a.a_scales = L.w_scales, a.b_scales = L.x_scales;
+    a.out = L.out;
+    a.status = L.status;
+    a.E = L.num_experts, a.M = L.num_rows;
+    a.features = L.out_features, a.depth = L.in_features;
+    a.limits = wait_limits();
+    a.trace = trace_args();
+    const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
+    if (e4m3) return launch_rows<kForwardE4m3, 1, 128>(a, s);
+    return launch_rows<kForward, 1, 128>(a, s);
+}
+
+int launch_grouped_grad_x(const GroupedLaunch &L) {
+    Args a{};
+    if (!make_tensor_map3(&a.a, L.w, false, L.num_experts, L.out_features, L.in_features, kDepth) ||
+        !make_tensor_map(&a.b, L.x, false, L.num_rows, L.out_features, kBoxRows))
+        return MOE_ERR_CUDA;
+    a.prefix = L.expert_prefix;
+    a.out = L.out;
+    a.status = L.status;
+    a.E = L.num_experts, a.M = L.num_rows;
+    a.features = L.in_features, a.depth = L.out_features;
+    a.limits = wait_limits();
+    a.trace = trace_args();
+    return launch_rows<kGradX, 1, 128>(a, static_cast<cudaStream_t>(L.stream));
+}
+
+int launch_grouped_grad_w(const GroupedGradWLaunch &L) {
+    const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
+    const size_t cell = L.out_type == MOE_GRAD_F32 ? 4 : 2;
+    if (L.num_rows == 0) {
+        if (L.accumulate) return MOE_OK;
+        const size_t bytes = (size_t)L.num_experts * L.out_features * L.in_features * cell;
+        return cudaMemsetAsync(L.out, 0, bytes, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
+    Args a{};
+    if (!make_tensor_map(&a.a, L.grad, false, L.num_rows, L.out_features, kDepth) ||
+        !make_tensor_map(&a.b, L.x, false, L.num_rows, L.in_features, kDepth))
+        return MOE_ERR_CUDA;
+    a.prefix = L.expert_prefix;
+    a.out = L.out;
+    a.status = L.status;
+    a.E = L.num_experts, a.M = L.num_rows;
+    a.features = L.out_features, a.depth = L.in_features;
+    a.accumulate = L.accumulate;
+    a.limits = wait_limits();
+    a.trace = trace_args();
+    constexpr int kCols = 256;
+    a.feature_tiles = ceil_div(a.features, kRows);
+    a.column_tiles = ceil_div(a.depth, kCols);
+    const int64_t tiles = (int64_t)a.E * a.feature_tiles * a.column_tiles;
+    return L.out_type == MOE_GRAD_F32 ? launch<kGradW, 1, kCols, float>(a, tiles, s)
+                                      : launch<kGradW, 1, kCols, __nv_bfloat16>(a, tiles, s);
+}
+
+}  // namespace moe

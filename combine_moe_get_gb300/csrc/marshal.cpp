@@ -1,5 +1,6 @@
 // marshal.cpp -- Python module _marshal: the arguments of the gate, the few-token
-// experts and the adapter projection, from tensors to the C entry points.
+// experts, the adapter projection, the grouped products, the activation and the norm, from
+// tensors to the C entry points.
 //
 // Small ones take 2 to 20 us of the GPU's time. In Python, checks of a dozen
 // tensors, two or three outputs to allocate and up to 25 arguments to convert made
@@ -134,6 +135,14 @@ class Args {
             under.reset_stream(c10::cuda::getStreamFromExternal((cudaStream_t)given_, like.device().index()));
         return at::empty(at::IntArrayRef(shape), at::TensorOptions().dtype(type).device(like.device()));
     }
+    // an output that is left out: an undefined tensor, None in Python
+    Tensor optional_output(bool wanted, const char *name, at::ScalarType type, Shape shape, const Tensor &like) {
+        if (wanted) return output(name, type, shape, like);
+        if (*at_ != Py_None) refuse(PyExc_ValueError, std::string(name) + " is not written by this call");
+        ++at_;
+        return Tensor();
+    }
+    bool flag() { return integer("flag") != 0; }
     bool none() const { return *at_ == Py_None; }
 
   private:
@@ -142,6 +151,8 @@ class Args {
     bool stream_given_ = false;
     int device_ = -1;   // of the tensors so far
 };
+
+void *data_or_null(const Tensor &t) { return t.defined() ? t.data_ptr() : nullptr; }
 
 // {status, outputs...}
 PyObject *result(int code, std::initializer_list<const Tensor *> outputs) {
@@ -348,9 +359,225 @@ PyObject *adapter_linear(PyObject *, PyObject *const *args, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
+// Rows [M, columns] of a grouped product or its gradient, bf16 unless `codes`.
+const Tensor &rows_of(Args &a, const char *name, bool codes_too) {
+    const Tensor &t = a.tensor(name, 2);
+    if (t.scalar_type() != at::kBFloat16 && !(codes_too && t.scalar_type() == at::kByte))
+        refuse(PyExc_ValueError, std::string(name) + (codes_too ? " is torch.bfloat16 or torch.uint8, not " : " is torch.bfloat16, not ") +
+                                     text(t.scalar_type()));
+    return t;
+}
+
+// (entry, x, w, expert_prefix, x_scales, w_scales, out, status, stream)
+PyObject *grouped_linear(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Args a(args, n, 9);
+    auto *entry = a.entry<decltype(moe_grouped_linear)>();
+    const Tensor &x = rows_of(a, "x", true), &w = a.tensor("w", 3);
+    const int64_t M = x.size(0), K = x.size(1), E = w.size(0), N = w.size(1);
+    check_sizes({M, K, E, N});
+    const bool e4m3 = x.scalar_type() == at::kByte;
+    if (w.scalar_type() != x.scalar_type() || w.size(2) != K)
+        refuse(PyExc_ValueError, "w is " + text(x.scalar_type()) + " " + text(at::IntArrayRef{E, N, K}) + ", not " +
+                                     text(w.scalar_type()) + " " + text(w.sizes()));
+    const Tensor &prefix = a.tensor("expert_prefix", at::kInt, {E + 1});
+    auto scales = [&](const char *name, Shape shape) {
+        if (a.none() == e4m3)
+            refuse(PyExc_ValueError, e4m3 ? "E4M3 codes need x_scales and w_scales" : "bf16 rows and weights take no scales");
+        return (const float *)a.pointer_or_null(name, at::kFloat, shape);
+    };
+    const float *x_scales = scales("x_scales", {M, K / 128});
+    const float *w_scales = scales("w_scales", {E, N, K / 128});
+    const Tensor out = a.output("out", at::kBFloat16, {M, N}, x);
+    int32_t *const status = a.status();
+    void *const stream = a.stream();
+    const int code = unlocked([&] {
+        return entry(x.data_ptr(), x_scales, (int)M, (int)K, w.data_ptr(), w_scales, (int)E, (int)N,
+                     (const int32_t *)prefix.data_ptr(), e4m3 ? MOE_WEIGHTS_E4M3 : MOE_WEIGHTS_BF16, out.data_ptr(), status,
+                     stream);
+    });
+    return result(code, {&out});
+    END_HANDLE_TH_ERRORS
+}
+
+// (entry, grad, w, expert_prefix, out, status, stream)
+PyObject *grouped_linear_grad_x(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Args a(args, n, 7);
+    auto *entry = a.entry<decltype(moe_grouped_linear_grad_x)>();
+    const Tensor &grad = rows_of(a, "grad", false), &w = a.tensor("w", 3);
+    const int64_t M = grad.size(0), N = grad.size(1), E = w.size(0), K = w.size(2);
+    check_sizes({M, K, E, N});
+    if (w.scalar_type() != at::kBFloat16 || w.size(1) != N)
+        refuse(PyExc_ValueError, "w is torch.bfloat16 " + text(at::IntArrayRef{E, N, K}) + ", not " + text(w.scalar_type()) +
+                                     " " + text(w.sizes()));
+    const Tensor &prefix = a.tensor("expert_prefix", at::kInt, {E + 1});
+    const Tensor out = a.output("out", at::kBFloat16, {M, K}, grad);
+    int32_t *const status = a.status();
+    void *const stream = a.stream();
+    const int code = unlocked([&] {
+        return entry(grad.data_ptr(), (int)M, (int)N, w.data_ptr(), (int)E, (int)K, (const int32_t *)prefix.data_ptr(),
+                     out.data_ptr(), status, stream);
+    });
+    return result(code, {&out});
+    END_HANDLE_TH_ERRORS
+}
+
+// (entry, grad, x, expert_prefix, bf16, accumulate, out, status, stream)
+PyObject *grouped_linear_grad_w(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Args a(args, n, 9);
+    auto *entry = a.entry<decltype(moe_grouped_linear_grad_w)>();
+    const Tensor &grad = rows_of(a, "grad", false), &x = rows_of(a, "x", false);
+    const int64_t M = grad.size(0), N = grad.size(1), K = x.size(1);
+    if (x.size(0) != M)
+        refuse(PyExc_ValueError, "x is torch.bfloat16 " + text(at::IntArrayRef{M, K}) + ", not " + text(x.sizes()));
+    const Tensor &prefix = a.tensor("expert_prefix", 1);
+    const int64_t E = prefix.size(0) - 1;
+    check_sizes({M, K, E, N});
+    if (prefix.scalar_type() != at::kInt || E < 1)
+        refuse(PyExc_ValueError, "expert_prefix is torch.int32 of at least two elements, not " + text(prefix.scalar_type()) +
+                                     " " + text(prefix.sizes()));
+    const bool bf16 = a.flag(), accumulate = a.flag();
+    const Tensor out = a.output("out", bf16 ? at::kBFloat16 : at::kFloat, {E, N, K}, x);
+    int32_t *const status = a.status();
+    void *const stream = a.stream();
+    const int code = unlocked([&] {
+        return entry(grad.data_ptr(), x.data_ptr(), (int)M, (int)N, (int)K, (int)E, (const int32_t *)prefix.data_ptr(),
+                     bf16 ? MOE_GRAD_BF16 : MOE_GRAD_F32, accumulate, out.data_ptr(), status, stream);
+    });
+    return result(code, {&out});
+    END_HANDLE_TH_ERRORS
+}
+
+// gate_up [M, 2 I]
+const Tensor &gate_up_of(Args &a) {
+    const Tensor &t = rows_of(a, "gate_up", false);
+    if (t.size(1) % 2 != 0) refuse(PyExc_ValueError, "gate_up has an odd number of columns");
+    return t;
+}
+
+// (entry, gate_up, row_weights, num_rows, quantize, out, out_scales, status, stream)
+PyObject *swiglu(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Args a(args, n, 9);
+    auto *entry = a.entry<decltype(moe_swiglu)>();
+    const Tensor &gate_up = gate_up_of(a);
+    const int64_t M = gate_up.size(0), I = gate_up.size(1) / 2;
+    check_sizes({M, I});
+    const void *weights = a.pointer_or_null("row_weights", at::kFloat, {M});
+    const void *rows = a.pointer_or_null("num_rows", at::kInt, {1});
+    const bool codes = a.flag();
+    if (codes && I % 128 != 0) refuse(PyExc_ValueError, "E4M3 codes need a multiple of 128 channels, not " + std::to_string(I));
+    const Tensor out = a.output("out", codes ? at::kByte : at::kBFloat16, {M, I}, gate_up);
+    const Tensor scales = a.optional_output(codes, "out_scales", at::kFloat, {M, I / 128}, gate_up);
+    int32_t *const status = a.status();
+    void *const stream = a.stream();
+    const int code = unlocked([&] {
+        return codes && M == 0 ? (int)MOE_OK   // scales without an element have no address
+                               : entry(gate_up.data_ptr(), (int)M, (int)I, (const float *)weights, (const int32_t *)rows,
+                                       out.data_ptr(), (float *)data_or_null(scales), status, stream);
+    });
+    return result(code, {&out, &scales});
+    END_HANDLE_TH_ERRORS
+}
+
+// (entry, gate_up, grad, row_weights, num_rows, weights_too, out, grad_row_weights, status, stream)
+PyObject *swiglu_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Args a(args, n, 10);
+    auto *entry = a.entry<decltype(moe_swiglu_backward)>();
+    const Tensor &gate_up = gate_up_of(a);
+    const int64_t M = gate_up.size(0), I = gate_up.size(1) / 2;
+    check_sizes({M, I});
+    const Tensor &grad = a.tensor("grad", at::kBFloat16, {M, I});
+    const void *weights = a.pointer_or_null("row_weights", at::kFloat, {M});
+    const void *rows = a.pointer_or_null("num_rows", at::kInt, {1});
+    const bool too = a.flag();
+    const Tensor out = a.output("out", at::kBFloat16, {M, 2 * I}, gate_up);
+    const Tensor grad_weights = a.optional_output(too, "grad_row_weights", at::kFloat, {M}, gate_up);
+    int32_t *const status = a.status();
+    void *const stream = a.stream();
+    const int code = unlocked([&] {
+        return entry(gate_up.data_ptr(), grad.data_ptr(), (int)M, (int)I, (const float *)weights, (const int32_t *)rows,
+                     out.data_ptr(), (float *)data_or_null(grad_weights), status, stream);
+    });
+    return result(code, {&out, &grad_weights});
+    END_HANDLE_TH_ERRORS
+}
+
+// weight [H], bf16 or fp32
+const Tensor &norm_weight(Args &a, int64_t H, int &type) {
+    const Tensor &w = a.tensor("weight", 1);
+    if ((w.scalar_type() != at::kBFloat16 && w.scalar_type() != at::kFloat) || w.size(0) != H)
+        refuse(PyExc_ValueError, "weight is torch.bfloat16 or torch.float32 " + text(at::IntArrayRef{H}) + ", not " +
+                                     text(w.scalar_type()) + " " + text(w.sizes()));
+    type = w.scalar_type() == at::kFloat ? MOE_NORM_WEIGHT_F32 : MOE_NORM_WEIGHT_BF16;
+    return w;
+}
+
+// (entry, x, residual, weight, eps, bf16_out, quantize, out, residual_out, codes, scales, status, stream)
+PyObject *add_rms_norm(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Args a(args, n, 13);
+    auto *entry = a.entry<decltype(moe_add_rms_norm)>();
+    const Tensor &x = rows_of(a, "x", false);
+    const int64_t T = x.size(0), H = x.size(1);
+    check_sizes({T, H});
+    const bool add = !a.none();
+    const void *residual = a.pointer_or_null("residual", at::kBFloat16, {T, H});
+    int type;
+    const Tensor &weight = norm_weight(a, H, type);
+    const float eps = a.real();
+    const bool wide = a.flag(), quantize = a.flag();
+    if (quantize && H % 128 != 0) refuse(PyExc_ValueError, "E4M3 codes need a multiple of 128 channels, not " + std::to_string(H));
+    const Tensor out = a.optional_output(wide, "out", at::kBFloat16, {T, H}, x);
+    const Tensor residual_out = a.optional_output(add, "residual_out", at::kBFloat16, {T, H}, x);
+    const Tensor codes = a.optional_output(quantize, "codes", at::kByte, {T, H}, x);
+    const Tensor scales = a.optional_output(quantize, "scales", at::kFloat, {T, H / 128}, x);
+    int32_t *const status = a.status();
+    void *const stream = a.stream();
+    const int code = unlocked([&] {
+        return entry(x.data_ptr(), residual, (int)T, (int)H, weight.data_ptr(), type, eps, data_or_null(out),
+                     data_or_null(residual_out), data_or_null(codes), (float *)data_or_null(scales), status, stream);
+    });
+    return result(code, {&out, &residual_out, &codes, &scales});
+    END_HANDLE_TH_ERRORS
+}
+
+// (entry, h, weight, grad, grad_residual, eps, out, grad_weight, workspace, status, stream)
+PyObject *add_rms_norm_backward(PyObject *, PyObject *const *args, Py_ssize_t n) {
+    HANDLE_TH_ERRORS
+    Args a(args, n, 11);
+    auto *entry = a.entry<decltype(moe_add_rms_norm_backward)>();
+    const Tensor &h = rows_of(a, "h", false);
+    const int64_t T = h.size(0), H = h.size(1);
+    check_sizes({T, H});
+    int type;
+    const Tensor &weight = norm_weight(a, H, type);
+    const Tensor &grad = a.tensor("grad", at::kBFloat16, {T, H});
+    const void *grad_residual = a.pointer_or_null("grad_residual", at::kBFloat16, {T, H});
+    const float eps = a.real();
+    const Tensor out = a.output("out", at::kBFloat16, {T, H}, h);
+    const Tensor grad_weight = a.output("grad_weight", at::kFloat, {H}, h);
+    const Tensor &workspace = a.tensor("workspace");
+    int32_t *const status = a.status();
+    void *const stream = a.stream();
+    const int code = unlocked([&] {
+        return entry(h.data_ptr(), weight.data_ptr(), type, grad.data_ptr(), grad_residual, (int)T, (int)H, eps,
+                     out.data_ptr(), (float *)grad_weight.data_ptr(), workspace.data_ptr(), workspace.nbytes(), status,
+                     stream);
+    });
+    return result(code, {&out, &grad_weight});
+    END_HANDLE_TH_ERRORS
+}
+
 #define MARSHAL_METHOD(f) {#f, (PyCFunction)(void (*)())f, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {MARSHAL_METHOD(topk_gate), MARSHAL_METHOD(topk_gate_backward), MARSHAL_METHOD(experts),
-                         MARSHAL_METHOD(layer), MARSHAL_METHOD(adapter_linear), {nullptr, nullptr, 0, nullptr}};
+                         MARSHAL_METHOD(layer), MARSHAL_METHOD(adapter_linear),
+                         MARSHAL_METHOD(grouped_linear), MARSHAL_METHOD(grouped_linear_grad_x),
+                         MARSHAL_METHOD(grouped_linear_grad_w), MARSHAL_METHOD(swiglu), MARSHAL_METHOD(swiglu_backward),
+                         MARSHAL_METHOD(add_rms_norm), MARSHAL_METHOD(add_rms_norm_backward), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -267,6 +267,7 @@ MOE_API const char *moe_status_string(int status) {
         case MOE_ERR_WORKSPACE: return "MOE_ERR_WORKSPACE";
         case MOE_ERR_BAD_LOGIT: return "MOE_ERR_BAD_LOGIT";
         case MOE_ERR_BAD_ADAPTER: return "MOE_ERR_BAD_ADAPTER";
+        case MOE_ERR_BAD_PREFIX: return "MOE_ERR_BAD_PREFIX";
         default: return "MOE_ERR_UNKNOWN";
     }
 }
@@ -682,6 +683,131 @@ MOE_API int moe_adapter_linear(const void *x, int num_tokens, int in_features, c
     }
     return moe::launch_adapter_linear(moe::AdapterLaunch{x, T, K, w, N, adapter_idx, a, b, scales, num_adapters, rank,
                                                          out, workspace, status, stream});
+}
+
+// Sizes and pointers of a grouped product: rows [M, a] and [M, b], weights [E, N, K].
+static int grouped_check(int M, int E, int N, int K, const void *r0, const void *r1, const void *w, const int32_t *prefix,
+                         const int32_t *status) {
+    if (M < 0 || M > MOE_MAX_ROWS || E < 1 || E > MOE_MAX_EXPERTS) return MOE_ERR_INVALID_ARG;
+    if (K < 8 || K % 8 != 0 || K > kMaxFeatures || N < 8 || N % 8 != 0 || N > kMaxFeatures) return MOE_ERR_INVALID_ARG;
+    if (!prefix || !w || !status || (M > 0 && (!r0 || !r1))) return MOE_ERR_INVALID_ARG;
+    if (!aligned(status, 4) || !aligned(prefix, 4) || !aligned(w, 16) || !aligned(r0, 16) || !aligned(r1, 16))
+        return MOE_ERR_MISALIGNED;
+    return MOE_OK;
+}
+
+MOE_API int moe_grouped_linear(const void *x, const float *x_scales, int num_rows, int in_features, const void *w,
+                               const float *w_scales, int num_experts, int out_features, const int32_t *expert_prefix,
+                               int weight_type, void *out, int32_t *status, void *stream) {
+    if (weight_type != MOE_WEIGHTS_BF16 && weight_type != MOE_WEIGHTS_E4M3) return MOE_ERR_INVALID_ARG;
+    const int rc = grouped_check(num_rows, num_experts, out_features, in_features, x, out, w, expert_prefix, status);
+    if (rc != MOE_OK) return rc;
+    const bool e4m3 = weight_type == MOE_WEIGHTS_E4M3;
+    if (e4m3 && in_features % 128 != 0) return MOE_ERR_INVALID_ARG;
+    if ((w_scales != nullptr) != e4m3 || (x_scales != nullptr && !e4m3) || (x_scales == nullptr && e4m3 && num_rows > 0))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned(w_scales, 4) || !aligned(x_scales, 4)) return MOE_ERR_MISALIGNED;
+    if (num_rows == 0) return MOE_OK;
+    return moe::launch_grouped_linear(moe::GroupedLaunch{x, x_scales, num_rows, w, w_scales, num_experts, out_features,
+                                                         in_features, expert_prefix, out, status, stream});
+}
+
+MOE_API int moe_grouped_linear_grad_x(const void *grad, int num_rows, int out_features, const void *w, int num_experts,
+                                      int in_features, const int32_t *expert_prefix, void *grad_x, int32_t *status,
+                                      void *stream) {
+    const int rc = grouped_check(num_rows, num_experts, out_features, in_features, grad, grad_x, w, expert_prefix, status);
+    if (rc != MOE_OK || num_rows == 0) return rc;
+    return moe::launch_grouped_grad_x(moe::GroupedLaunch{grad, nullptr, num_rows, w, nullptr, num_experts, out_features,
+                                                         in_features, expert_prefix, grad_x, status, stream});
+}
+
+MOE_API int moe_grouped_linear_grad_w(const void *grad, const void *x, int num_rows, int out_features, int in_features,
+                                      int num_experts, const int32_t *expert_prefix, int grad_type, int accumulate,
+                                      void *grad_w, int32_t *status, void *stream) {
+    if (grad_type != MOE_GRAD_F32 && grad_type != MOE_GRAD_BF16) return MOE_ERR_INVALID_ARG;
+    if (accumulate != 0 && accumulate != 1) return MOE_ERR_INVALID_ARG;
+    const int rc = grouped_check(num_rows, num_experts, out_features, in_features, grad, x, grad_w, expert_prefix, status);
+    if (rc != MOE_OK) return rc;
+    return moe::launch_grouped_grad_w(moe::GroupedGradWLaunch{grad, x, num_rows, num_experts, out_features, in_features,
+                                                              expert_prefix, grad_w, grad_type, accumulate != 0, status,
+                                                              stream});
+}
+
+static int swiglu_check(const void *gate_up, int M, int I, const float *row_weights, const int32_t *num_rows,
+                        const void *out, bool codes, const int32_t *status) {
+    if (M < 0 || M > MOE_MAX_ROWS || I < 8 || I % (codes ? 128 : 8) != 0 || I > kMaxFeatures) return MOE_ERR_INVALID_ARG;
+    if (!status || (M > 0 && (!gate_up || !out))) return MOE_ERR_INVALID_ARG;
+    if (!aligned(gate_up, 16) || !aligned(out, codes ? 8 : 16) || !aligned(row_weights, 4) || !aligned(num_rows, 4) ||
+        !aligned(status, 4))
+        return MOE_ERR_MISALIGNED;
+    return MOE_OK;
+}
+
+MOE_API int moe_swiglu(const void *gate_up, int num_rows_most, int intermediate, const float *row_weights,
+                       const int32_t *num_rows, void *out, float *out_scales, int32_t *status, void *stream) {
+    const int rc = swiglu_check(gate_up, num_rows_most, intermediate, row_weights, num_rows, out, out_scales != nullptr,
+                                status);
+    if (rc != MOE_OK) return rc;
+    if (!aligned(out_scales, 4)) return MOE_ERR_MISALIGNED;
+    return moe::launch_swiglu(moe::SwigluLaunch{gate_up, nullptr, num_rows_most, intermediate, row_weights, num_rows, out,
+                                                out_scales, nullptr, status, stream});
+}
+
+MOE_API int moe_swiglu_backward(const void *gate_up, const void *grad, int num_rows_most, int intermediate,
+                                const float *row_weights, const int32_t *num_rows, void *grad_gate_up,
+                                float *grad_row_weights, int32_t *status, void *stream) {
+    const int rc = swiglu_check(gate_up, num_rows_most, intermediate, row_weights, num_rows, grad_gate_up, false, status);
+    if (rc != MOE_OK) return rc;
+    if (num_rows_most > 0 && !grad) return MOE_ERR_INVALID_ARG;
+    if (!aligned(grad, 16) || !aligned(grad_row_weights, 4)) return MOE_ERR_MISALIGNED;
+    return moe::launch_swiglu_backward(moe::SwigluLaunch{gate_up, grad, num_rows_most, intermediate, row_weights, num_rows,
+                                                         grad_gate_up, nullptr, grad_row_weights, status, stream});
+}
+
+static bool norm_shape_ok(int T, int H) {
+    return T >= 0 && T <= MOE_MAX_ROWS && H >= 8 && H % 8 == 0 && H <= MOE_MAX_NORM_HIDDEN;
+}
+
+static int norm_check(const void *x, int T, int H, const void *weight, int weight_type, const int32_t *status) {
+    if (!norm_shape_ok(T, H)) return MOE_ERR_INVALID_ARG;
+    if (weight_type != MOE_NORM_WEIGHT_BF16 && weight_type != MOE_NORM_WEIGHT_F32) return MOE_ERR_INVALID_ARG;
+    if (!status || (T > 0 && (!x || !weight))) return MOE_ERR_INVALID_ARG;
+    if (!aligned(status, 4) || !aligned(x, 16) || !aligned(weight, 16)) return MOE_ERR_MISALIGNED;
+    return MOE_OK;
+}
+
+MOE_API int moe_add_rms_norm(const void *x, const void *residual, int num_tokens, int hidden, const void *weight,
+                             int weight_type, float eps, void *out, void *residual_out, void *codes, float *scales,
+                             int32_t *status, void *stream) {
+    const int rc = norm_check(x, num_tokens, hidden, weight, weight_type, status);
+    if (rc != MOE_OK) return rc;
+    if ((codes != nullptr) != (scales != nullptr) || (codes && hidden % 128 != 0)) return MOE_ERR_INVALID_ARG;
+    if (residual_out && !residual && num_tokens > 0) return MOE_ERR_INVALID_ARG;
+    if (num_tokens > 0 && !out && !residual_out && !codes) return MOE_ERR_INVALID_ARG;
+    if (!aligned(residual, 16) || !aligned(out, 16) || !aligned(residual_out, 16) || !aligned(codes, 8) ||
+        !aligned(scales, 4))
+        return MOE_ERR_MISALIGNED;
+    return moe::launch_norm(moe::NormLaunch{x, residual, nullptr, num_tokens, hidden, weight, weight_type, eps, out,
+                                            residual_out, codes, scales, nullptr, nullptr, stream});
+}
+
+MOE_API size_t moe_add_rms_norm_backward_workspace_size(int num_tokens, int hidden) {
+    return norm_shape_ok(num_tokens, hidden) ? moe::norm_backward_workspace_bytes(num_tokens, hidden) : 0;
+}
+
+MOE_API int moe_add_rms_norm_backward(const void *h, const void *weight, int weight_type, const void *grad,
+                                      const void *grad_residual, int num_tokens, int hidden, float eps, void *grad_x,
+                                      float *grad_weight, void *workspace, size_t workspace_bytes, int32_t *status,
+                                      void *stream) {
+    const int rc = norm_check(h, num_tokens, hidden, weight, weight_type, status);
+    if (rc != MOE_OK) return rc;
+    if (!grad_weight || (num_tokens > 0 && (!grad || !grad_x || !workspace))) return MOE_ERR_INVALID_ARG;
+    if (!aligned(grad, 16) || !aligned(grad_residual, 16) || !aligned(grad_x, 16) || !aligned(grad_weight, 4) ||
+        !aligned(workspace, 16))
+        return MOE_ERR_MISALIGNED;
+    if (num_tokens > 0 && workspace_bytes < moe::norm_backward_workspace_bytes(num_tokens, hidden)) return MOE_ERR_WORKSPACE;
+    return moe::launch_norm_backward(moe::NormLaunch{h, grad_residual, grad, num_tokens, hidden, weight, weight_type, eps,
+                                                     grad_x, nullptr, nullptr, nullptr, grad_weight, workspace, stream});
 }
 
 }  // extern "C"

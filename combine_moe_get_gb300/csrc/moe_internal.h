@@ -1,6 +1,6 @@
 // moe_internal.h -- host-side interfaces between the C ABI entry points
 // (moe_api.cu) and the kernel launchers (layout.cu, expand.cu, dispatch.cu,
-// combine.cu, gate.cu, experts.cu, adapter.cu).
+// combine.cu, gate.cu, experts.cu, adapter.cu, grouped.cu, swiglu.cu, norm.cu).
 // Arguments reaching a launcher have already been validated.
 #pragma once
 
@@ -360,5 +360,71 @@ struct AdapterLaunch {
 size_t adapter_workspace_bytes(int T, int K, int N, int L, int r);   // for up to T rows
 size_t adapter_workspace_need(int T, int K, int N, int L, int r);    // for T rows
 int launch_adapter_linear(const AdapterLaunch &L);
+
+struct GroupedLaunch {
+    const void *x;             // rows; launch_grouped_grad_x: the gradient's rows [M, N]
+    const float *x_scales;     // with w_scales: E4M3 codes; both null: bf16
+    int num_rows;
+    const void *w;
+    const float *w_scales;
+    int num_experts, out_features, in_features;
+    const int32_t *expert_prefix;
+    void *out;
+    int32_t *status;
+    void *stream;
+};
+
+int launch_grouped_linear(const GroupedLaunch &L);
+int launch_grouped_grad_x(const GroupedLaunch &L);
+
+struct GroupedGradWLaunch {
+    const void *grad, *x;
+    int num_rows, num_experts, out_features, in_features;
+    const int32_t *expert_prefix;
+    void *out;
+    int out_type;              // MOE_GRAD_*
+    bool accumulate;
+    int32_t *status;
+    void *stream;
+};
+
+int launch_grouped_grad_w(const GroupedGradWLaunch &L);
+
+struct SwigluLaunch {
+    const void *gate_up;
+    const void *grad;          // backward
+    int num_rows_most, intermediate;
+    const float *row_weights;  // optional
+    const int32_t *num_rows;   // optional
+    void *out;
+    float *out_scales;         // E4M3; null: bf16
+    float *grad_row_weights;   // backward, optional
+    int32_t *status;
+    void *stream;
+};
+
+int launch_swiglu(const SwigluLaunch &L);
+int launch_swiglu_backward(const SwigluLaunch &L);
+
+struct NormLaunch {
+    const void *x;             // backward: h
+    const void *residual;      // optional; backward: the gradient of the residual
+    const void *grad;          // backward
+    int num_tokens, hidden;
+    const void *weight;
+    int weight_type;           // MOE_NORM_WEIGHT_*
+    float eps;
+    void *out;                 // optional; backward: grad_x
+    void *residual_out;        // optional
+    void *codes;               // optional, with scales
+    float *scales;
+    float *grad_weight;        // backward
+    void *workspace;           // backward
+    void *stream;
+};
+
+size_t norm_backward_workspace_bytes(int T, int H);
+int launch_norm(const NormLaunch &L);
+int launch_norm_backward(const NormLaunch &L);
 
 }  // namespace moe

@@ -30,8 +30,10 @@
  *     at or beyond the receive capacity; that row is not written / not read),
  *     MOE_ERR_TIMEOUT (a bounded wait inside a kernel ran out; the outputs of
  *     that call are unspecified), MOE_ERR_BAD_LOGIT (a NaN router logit; that
- *     expert is treated as masked) and MOE_ERR_BAD_ADAPTER (an adapter index
- *     outside [-1, L); that row is treated as having no adapter).
+ *     expert is treated as masked), MOE_ERR_BAD_ADAPTER (an adapter index
+ *     outside [-1, L); that row is treated as having no adapter) and
+ *     MOE_ERR_BAD_PREFIX (an expert prefix that leaves the rows or descends; it
+ *     is cut to the rows).
  *   - T == 0 is a valid no-op that still writes zero counts and prefixes.
  */
 #ifndef MOE_GET_H
@@ -60,7 +62,8 @@ typedef enum {
     MOE_ERR_CUDA = 6,
     MOE_ERR_WORKSPACE = 7,
     MOE_ERR_BAD_LOGIT = 8,
-    MOE_ERR_BAD_ADAPTER = 9
+    MOE_ERR_BAD_ADAPTER = 9,
+    MOE_ERR_BAD_PREFIX = 10
 } moe_status_t;
 
 /* Limits checked on the host (MOE_ERR_INVALID_ARG beyond them). */
@@ -70,6 +73,8 @@ typedef enum {
 #define MOE_EXPERTS_MAX_TOKENS 1024   /* moe_experts, moe_layer: a few tokens */
 #define MOE_MAX_ADAPTERS 8192
 #define MOE_MAX_ADAPTER_RANK 128
+#define MOE_MAX_ROWS (1 << 30)        /* rows of the grouped products, the activation and the norm */
+#define MOE_MAX_NORM_HIDDEN 65536
 
 /* Outputs of moe_get_layout: all DEVICE pointers, caller-owned. */
 typedef struct {
@@ -437,6 +442,12 @@ enum {
     MOE_TRACE_ADAPTER_SORT = 19,
     MOE_TRACE_ADAPTER_EXPAND = 20,
     MOE_TRACE_EXPERTS_SPLIT = 21,
+    MOE_TRACE_GROUPED = 22,
+    MOE_TRACE_SWIGLU = 23,
+    MOE_TRACE_SWIGLU_BACKWARD = 24,
+    MOE_TRACE_NORM = 25,
+    MOE_TRACE_NORM_BACKWARD = 26,
+    MOE_TRACE_NORM_WEIGHT = 27,        /* sums of the weight's gradient */
     MOE_TRACE_PHASE = 0x10000          /* warp field of a per-CTA phase record: MOE_TRACE_PHASE + phase */
 };
 
@@ -702,7 +713,154 @@ MOE_API int moe_adapter_linear(const void *x, int num_tokens, int in_features, c
                                int32_t *status, void *stream);
 
 /*
- * Failure injection for tests of moe_experts, moe_layer and moe_adapter_linear:
+ * moe_grouped_linear -- matrix products grouped by expert, the grouped GEMM that
+ * the pages put between dispatch and combine: each expert's weights times its
+ * rows, for any numbers of rows (prompts and training; for a few tokens without a
+ * dispatch there is moe_experts).
+ *
+ *   out[r] = bf16_rn( w[e] x[r] )   for r in [expert_prefix[e], expert_prefix[e+1])
+ *
+ * Rows are in the order of moe_get_expand_layout with MOE_DISPATCH_EXPAND, and
+ * expert_prefix is moe_get_layout's (a rank's own experts take the part of it
+ * that begins at their first). It need not begin at 0 nor end at num_rows: rows of
+ * no expert, those of a receive buffer behind the last one among them, are not
+ * written, whatever they hold; an expert without rows is not read. Sums are fp32.
+ * A prefix outside [0, num_rows] or one that descends raises MOE_ERR_BAD_PREFIX and
+ * is cut to what is inside and in order.
+ *
+ *   x              [M, K] bf16, or E4M3 codes (uint8, MOE_WEIGHTS_E4M3) with
+ *   x_scales       [M, K/128] fp32, as MOE_DISPATCH_QUANTIZE_FP8 and moe_swiglu make them.
+ *   w              [E, N, K] bf16, or E4M3 codes with
+ *   w_scales       [E, N, K/128] fp32 (the format of moe_experts). Scales NULL for bf16.
+ *                  Each block of 128 is summed from the codes as they are and then
+ *                  scaled by the product of its two scales in fp32.
+ *   expert_prefix  [E+1] int32, device.
+ *   out            [M, N] bf16; not one of the inputs.
+ * x, w and out are 16-byte aligned. Limits: M <= 2^30, E <= 8192, K and N multiples of 8
+ * (K of 128 with E4M3) up to 2^20.
+ */
+MOE_API int moe_grouped_linear(const void *x, const float *x_scales, int num_rows, int in_features, const void *w,
+                               const float *w_scales, int num_experts, int out_features,
+                               const int32_t *expert_prefix, int weight_type, void *out, int32_t *status,
+                               void *stream);
+
+/*
+ * moe_grouped_linear_grad_x -- the gradient of moe_grouped_linear's rows (bf16):
+ *
+ *   grad_x[r] = bf16_rn( w[e]^T grad[r] )   for r in [expert_prefix[e], expert_prefix[e+1])
+ *
+ *   grad [M, N], w [E, N, K], grad_x [M, K] bf16. Otherwise as moe_grouped_linear.
+ */
+MOE_API int moe_grouped_linear_grad_x(const void *grad, int num_rows, int out_features, const void *w,
+                                      int num_experts, int in_features, const int32_t *expert_prefix,
+                                      void *grad_x, int32_t *status, void *stream);
+
+/*
+ * moe_grouped_linear_grad_w -- the gradient of moe_grouped_linear's weights (bf16):
+ *
+ *   grad_w[e] = sum over r in [expert_prefix[e], expert_prefix[e+1]) of grad[r] x[r]^T
+ *
+ * summed in fp32 in the order of the rows. An expert without rows gets zeros.
+ *
+ *   grad [M, N], x [M, K] bf16.
+ *   grad_type   MOE_GRAD_F32 or MOE_GRAD_BF16: the type of grad_w [E, N, K].
+ *   accumulate  0: grad_w is written; 1: it is added to what is there (in fp32, then
+ *               rounded once for bf16).
+ * Otherwise as moe_grouped_linear.
+ */
+enum { MOE_GRAD_F32 = 0, MOE_GRAD_BF16 = 1 };
+MOE_API int moe_grouped_linear_grad_w(const void *grad, const void *x, int num_rows, int out_features,
+                                      int in_features, int num_experts, const int32_t *expert_prefix, int grad_type,
+                                      int accumulate, void *grad_w, int32_t *status, void *stream);
+
+/*
+ * moe_swiglu -- the gated activation between an expert's two products, for rows
+ * of any expert:
+ *
+ *   out[r] = row_weights[r] * silu(gate_up[r, 0:I]) * gate_up[r, I:2I],  silu(z) = z / (1 + exp(-z))
+ *
+ * rounded once from fp32, to bf16 or to E4M3 codes with one scale per 128 channels
+ * (scale = amax / 448, code = E4M3(value / scale), as MOE_DISPATCH_QUANTIZE_FP8; a
+ * quotient within 2^-22 of the middle between two codes may round to either).
+ * Row weights here (a top-k entry's router weight) save moe_combine_ex's: the second
+ * product is linear.
+ *
+ *   gate_up      [M, 2I] bf16: gate, then up.
+ *   row_weights  [M] fp32 or NULL (1).
+ *   num_rows     device int32 or NULL: rows at or beyond *num_rows are neither
+ *                read nor written (expert_prefix + E for a receive buffer with room to
+ *                spare). Outside [0, M] it raises MOE_ERR_CAPACITY and is cut to it.
+ *   out          [M, I] bf16, or E4M3 codes (uint8) with out_scales [M, I/128] fp32
+ *                (NULL for bf16).
+ * gate_up and out are 16-byte aligned (E4M3 codes: 8). Limits: M <= 2^30, I a multiple of 8 (128
+ * with E4M3) up to 2^20.
+ */
+MOE_API int moe_swiglu(const void *gate_up, int num_rows_most, int intermediate, const float *row_weights,
+                       const int32_t *num_rows, void *out, float *out_scales, int32_t *status, void *stream);
+
+/*
+ * moe_swiglu_backward -- the gradients of moe_swiglu (bf16), from its inputs:
+ * with s = 1 / (1 + exp(-g)), [g, u] = gate_up[r] and d = grad[r]
+ *
+ *   grad_gate_up[r]     = [ d w u s (1 + g (1 - s)), d w g s ],  w = row_weights[r]
+ *   grad_row_weights[r] = sum over i of d u g s        (fp32)
+ *
+ *   grad [M, I], grad_gate_up [M, 2I] bf16 (may be gate_up itself).
+ *   grad_row_weights  [M] fp32, or NULL where it is not wanted.
+ * Otherwise as moe_swiglu.
+ */
+MOE_API int moe_swiglu_backward(const void *gate_up, const void *grad, int num_rows_most, int intermediate,
+                                const float *row_weights, const int32_t *num_rows, void *grad_gate_up,
+                                float *grad_row_weights, int32_t *status, void *stream);
+
+/*
+ * moe_add_rms_norm -- what makes a layer's rows: the residual's addition and the
+ * root-mean-square norm, with the rows for the router in bf16, those for
+ * MOE_DISPATCH_FP8 in E4M3, or both.
+ *
+ *   h = x + residual,  y = h / sqrt(mean over H of h^2 + eps) * weight
+ *   residual_out = bf16_rn(h),  out = bf16_rn(y),  codes, scales = E4M3 of y as in moe_swiglu
+ *
+ * all from the unrounded fp32 h.
+ *
+ *   x, residual   [T, H] bf16; residual may be NULL (h = x).
+ *   weight        [H] bf16 or fp32 (weight_type).
+ *   out, residual_out  [T, H] bf16 or NULL; residual_out may be residual or x itself, and wants a residual.
+ *   codes, scales      [T, H] uint8 and [T, H/128] fp32, or both NULL.
+ * Rows are 16-byte aligned (codes: 8, an fp32 weight: 16). Limits: T <= 2^30, H a multiple of 8 (128 with
+ * codes) up to 65536. No data raises an error here; `status` is part of every call.
+ */
+enum { MOE_NORM_WEIGHT_BF16 = 0, MOE_NORM_WEIGHT_F32 = 1 };
+MOE_API int moe_add_rms_norm(const void *x, const void *residual, int num_tokens, int hidden, const void *weight,
+                             int weight_type, float eps, void *out, void *residual_out, void *codes, float *scales,
+                             int32_t *status, void *stream);
+
+/* Bytes of device workspace moe_add_rms_norm_backward needs (16-byte aligned
+ * pointer required), enough for fewer rows too. Host-only; never fails (0 for
+ * invalid sizes). */
+MOE_API size_t moe_add_rms_norm_backward_workspace_size(int num_tokens, int hidden);
+
+/*
+ * moe_add_rms_norm_backward -- the gradients of moe_add_rms_norm's y, at h as the
+ * forward pass kept it (residual_out, or x where there was no residual):
+ * with r = 1 / sqrt(mean(h^2) + eps), n = h r and d = grad * weight
+ *
+ *   grad_x = bf16_rn( r (d - n mean(d n)) + grad_residual )    (x's and the residual's: they share it)
+ *   grad_weight = sum over rows of grad n                     (fp32, in an order fixed by the sizes)
+ *
+ *   h, grad        [T, H] bf16.
+ *   grad_residual  [T, H] bf16, the gradient that reaches residual_out elsewhere, or NULL.
+ *   grad_x         [T, H] bf16 (may be grad, grad_residual or h itself); grad_weight [H] fp32.
+ *   workspace      at least moe_add_rms_norm_backward_workspace_size() bytes; need not be
+ *                  initialised; not shared by calls that overlap on the GPU.
+ */
+MOE_API int moe_add_rms_norm_backward(const void *h, const void *weight, int weight_type, const void *grad,
+                                      const void *grad_residual, int num_tokens, int hidden, float eps, void *grad_x,
+                                      float *grad_weight, void *workspace, size_t workspace_bytes, int32_t *status,
+                                      void *stream);
+
+/*
+ * Failure injection for tests of moe_experts, moe_layer, moe_adapter_linear and the grouped products:
  * the process's later calls bound each wait inside their kernels by
  * `wait_timeout_ns` of the GPU's global timer (<= 0: the default, 1 s), and their
  * CTA `withheld_cta` keeps the first results that others wait for to itself, so
