@@ -226,6 +226,11 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float *v) {
 // ------------------------------------------------------------------ tiles
 
 __device__ __forceinline__ int round16(int n) { return (n + 15) & ~15; }
+// Columns of a tile's products: weights' gradients load theirs 64 at a time into each CTA.
+template <Op kOp, int kCtas>
+__device__ __forceinline__ int columns_of(const Tile &t) {
+    return kOp == kGradW ? (t.n + kCtas * 64 - 1) / (kCtas * 64) * (kCtas * 64) : round16(t.n);
+}
 
 // Rows of expert e, whatever the prefix holds: inside [0, M], in order.
 struct Range {
@@ -359,7 +364,7 @@ __device__ bool load(const Args &a, Control &c, uint32_t ring_base, uint32_t ran
     bool ok = (int)blockIdx.x != a.limits.withheld_cta;
     ok = ok && each_tile(a, c, [&](const Tile &t) {
         const int a0 = t.a0 + (int)rank * kRows;
-        const int part = kOp == kGradW ? kCols / kCtas : round16(t.n) / kCtas;   // columns that this CTA loads
+        const int part = columns_of<kOp, kCtas>(t) / kCtas;   // columns that this CTA loads
         const int boxes = kOp == kGradW ? part / 64 : (part + kBoxRows - 1) / kBoxRows;
         const uint32_t bytes = kTileA + boxes * (kOp == kGradW ? 64 : kBoxRows) * 128;
         for (int kb = 0; kb < t.blocks; ++kb, r.next(), ++issued) {
@@ -404,7 +409,7 @@ __device__ bool multiply(const Args &a, Control &c, uint32_t ring_base, uint32_t
     // steps of one product along the reduction, in the descriptors' units of 16 bytes
     constexpr uint32_t kStepA = kAmn ? 2048 >> 4 : 2, kStepB = kBmn ? 2048 >> 4 : 2;
     const bool ok = each_tile(a, c, [&](const Tile &t) {
-        const int n = round16(t.n);
+        const int n = columns_of<kOp, kCtas>(t);
         const uint32_t desc = 1u << 4 | (C::kE4m3 ? 0 : 1u << 7 | 1u << 10) | (uint32_t)kAmn << 15 | (uint32_t)kBmn << 16 |
                               (uint32_t)(n >> 3) << 17 | (uint32_t)(kCtas * kRows >> 4) << 24;
         if (t.blocks == 0) return true;   // weights' gradients of an expert without rows: nothing to wait for
@@ -452,8 +457,8 @@ __device__ bool mask_blocks(const Args &a, Control &c, char *ring) {
             if (!warp_wait(&c.masked_full[r.slot], seen >> r.slot & 1, a.limits.wait_ns)) return false;
             seen ^= 1u << r.slot;
             char *at = ring + (size_t)r.slot * (kTileA + C::kTileB);
-            constexpr int kChunks = 2 + kCols / kCtas / 64;
-            for (int i = lane; i < kChunks * (kDepth - t.last) * 8; i += 32) {   // 16 bytes each
+            const int chunks = 2 + columns_of<kGradW, kCtas>(t) / kCtas / 64;
+            for (int i = lane; i < chunks * (kDepth - t.last) * 8; i += 32) {   // 16 bytes each
                 const int chunk = i / ((kDepth - t.last) * 8), in = i - chunk * (kDepth - t.last) * 8;
                 *reinterpret_cast<int4 *>(at + chunk * 8192 + t.last * 128 + in * 16) = make_int4(0, 0, 0, 0);
             }
@@ -775,8 +780,8 @@ int launch_grouped_linear(const GroupedLaunch &L) {
     a.limits = wait_limits();
     a.trace = trace_args();
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
-    if (e4m3) return launch_rows<kForwardE4m3, 1, 128>(a, s);
-    return launch_rows<kForward, 1, 128>(a, s);
+    if (e4m3) return launch_rows<kForwardE4m3, 2, 128>(a, s);
+    return launch_rows<kForward, 2, 256>(a, s);
 }
 
 int launch_grouped_grad_x(const GroupedLaunch &L) {
@@ -791,7 +796,7 @@ int launch_grouped_grad_x(const GroupedLaunch &L) {
     a.features = L.in_features, a.depth = L.out_features;
     a.limits = wait_limits();
     a.trace = trace_args();
-    return launch_rows<kGradX, 1, 128>(a, static_cast<cudaStream_t>(L.stream));
+    return launch_rows<kGradX, 2, 256>(a, static_cast<cudaStream_t>(L.stream));
 }
 
 int launch_grouped_grad_w(const GroupedGradWLaunch &L) {
@@ -815,11 +820,11 @@ int launch_grouped_grad_w(const GroupedGradWLaunch &L) {
     a.limits = wait_limits();
     a.trace = trace_args();
     constexpr int kCols = 256;
-    a.feature_tiles = ceil_div(a.features, kRows);
+    a.feature_tiles = ceil_div(a.features, 2 * kRows);
     a.column_tiles = ceil_div(a.depth, kCols);
     const int64_t tiles = (int64_t)a.E * a.feature_tiles * a.column_tiles;
-    return L.out_type == MOE_GRAD_F32 ? launch<kGradW, 1, kCols, float>(a, tiles, s)
-                                      : launch<kGradW, 1, kCols, __nv_bfloat16>(a, tiles, s);
+    return L.out_type == MOE_GRAD_F32 ? launch<kGradW, 2, kCols, float>(a, tiles, s)
+                                      : launch<kGradW, 2, kCols, __nv_bfloat16>(a, tiles, s);
 }
 
 }  // namespace moe
