@@ -30,7 +30,8 @@ constexpr int kFirstReader = 4;
 constexpr int kRows = 128;                 // features of a CTA's tile
 constexpr int kTileA = kRows * 128;        // bytes of A in a stage
 constexpr int kTileSlots = 4;              // tiles found ahead
-constexpr int kSmemBudget = 226 << 10;
+constexpr int kSmemBudget = 226 << 10;     // ring, what stands beside it, and 1 KB to align them
+constexpr int kStoreBytes = 32 * 128;      // weights' gradients: 32 rows of a warp on their way out
 constexpr int kBoxRows = 32;               // rows of one copy of the ragged operand
 constexpr int kDepth = 64;                 // bf16 elements of a block along the reduction (E4M3: 128)
 constexpr int kRowGroup = 8;               // row tiles that share a pass over the features
@@ -49,7 +50,7 @@ struct Tile {
 };
 
 struct Args {
-    CUtensorMap a, b;
+    CUtensorMap a, b, out_map;          // out_map: weights' gradients
     const int32_t *prefix;
     const float *a_scales, *b_scales;   // E4M3: [E, N, K/128] and [M, K/128]
     void *out;
@@ -69,12 +70,12 @@ struct Config {
     static constexpr bool kE4m3 = kOp == kForwardE4m3;
     static constexpr int kTileB = kCols / kCtas * 128;
     static constexpr int kSums = kE4m3 ? (512 / kCols < 4 ? 512 / kCols : 4) : 2;
-    static constexpr int kScaleBytes = kE4m3 ? kSums * kCols * 4 : 0;
-    static constexpr int kStages = (kSmemBudget - 1024 - 2048 - kScaleBytes) / (kTileA + kTileB) < 12
-                                       ? (kSmemBudget - 1024 - 2048 - kScaleBytes) / (kTileA + kTileB) : 12;
+    static constexpr int kBeside = kE4m3 ? kSums * kCols * 4 : kOp == kGradW ? kReaders * 2 * kStoreBytes : 0;
+    static constexpr int kFit = (kSmemBudget - 1024 - kBeside) / (kTileA + kTileB);
+    static constexpr int kStages = kFit < 12 ? kFit : 12;
     static constexpr int kTmemCols = kSums * kCols <= 64 ? 64 : kSums * kCols <= 128 ? 128 : kSums * kCols <= 256 ? 256 : 512;
     static constexpr int kBlock = kE4m3 ? 128 : kDepth;
-    static constexpr size_t smem() { return 1024 + (size_t)kStages * (kTileA + kTileB) + kScaleBytes; }
+    static constexpr size_t smem() { return 1024 + (size_t)kStages * (kTileA + kTileB) + kBeside; }
     static_assert(kStages >= 3 && kSums >= 2);
     // who takes a tile from the scan: loads, products (one CTA of a pair), warp 3 (if it has work), readers
     static constexpr bool kHelper = kOp == kGradW || kE4m3;
@@ -515,53 +516,71 @@ __device__ __forceinline__ void store_rows(const Args &a, const Tile &t, int f, 
     }
 }
 
-// A lane's row of a weight's gradient: 16 columns from `col`.
+// A warp's 32 rows x 128 bytes of a weight's gradient: into shared memory, swizzled as the map wants it, and out as one
+// tile, whose part outside the matrix is not written. (Lanes that store 16 bytes each to rows of their own took 1660 us
+// where this takes @W@, 16384 rows, 32 experts, 7168 x 4096.) Two buffers a warp.
 template <typename Out>
-__device__ __forceinline__ void store_weights(const Args &a, const Tile &t, int f, int col, float (&v)[16]) {
-    if (f >= a.features) return;
-    Out *out = static_cast<Out *>(a.out) + ((size_t)t.e * a.features + f) * a.depth + t.c0 + col;
+__device__ __forceinline__ void store_weights(const Args &a, const Tile &t, int f0, int col, const float (&v)[128 / sizeof(Out)],
+                                              char *buffer) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) bulk_wait_read<1>();   // the tile before last has left this buffer
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 16; j += 8) {   // sizes are multiples of 8
-        if (col + j >= t.n) break;
+    for (int i = 0; i < 8; ++i) {
+        uint4 x;
         if constexpr (sizeof(Out) == 4) {
-            float4 *p = reinterpret_cast<float4 *>(out + j);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float4 x = make_float4(v[j + 4 * i], v[j + 4 * i + 1], v[j + 4 * i + 2], v[j + 4 * i + 3]);
-                if (a.accumulate) {
-                    const float4 y = p[i];
-                    x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-                }
-                p[i] = x;
-            }
+            x = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
+                           __float_as_uint(v[4 * i + 3]));
         } else {
-            uint4 *p = reinterpret_cast<uint4 *>(out + j);
-            uint4 x = {};
             __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&x);
-            if (a.accumulate) {
-                x = *p;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 y = __bfloat1622float2(h[i]);
-                    v[j + 2 * i] += y.x, v[j + 2 * i + 1] += y.y;
-                }
-            }
+            for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+        }
+        *reinterpret_cast<uint4 *>(buffer + lane * 128 + ((i ^ (lane & 7)) * 16)) = x;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        if (sizeof(Out) == 4 && a.accumulate)
+            asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                         ::"l"(&a.out_map), "r"(t.c0 + col), "r"(f0), "r"(t.e), "r"(smem_addr(buffer)) : "memory");
+        else
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                         ::"l"(&a.out_map), "r"(t.c0 + col), "r"(f0), "r"(t.e), "r"(smem_addr(buffer)) : "memory");
+        bulk_commit();
+    }
+}
+
+// bf16 that is added to is read into registers, so that the sum is rounded once.
+__device__ __forceinline__ void add_weights(const Args &a, const Tile &t, int f, int col, float (&v)[64]) {
+    if (f >= a.features) return;
+    const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.out) +
+                                                        ((size_t)t.e * a.features + f) * a.depth + t.c0 + col);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[j + 2 * i], v[j + 2 * i + 1]);
-            *p = x;
+    for (int i = 0; i < 8; ++i) {
+        if (col + 8 * i >= t.n) break;   // sizes are multiples of 8
+        const uint4 x = from[i];
+        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&x);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 y = __bfloat1622float2(h[j]);
+            v[8 * i + 2 * j] += y.x, v[8 * i + 2 * j + 1] += y.y;
         }
     }
 }
 
 // Warps 4 to 11: a quarter of tensor memory's lanes each, every other 16 columns.
 template <Op kOp, int kCtas, int kCols, typename Out>
-__device__ bool read_sums(const Args &a, Control &c, const float *scales, uint32_t tmem, uint32_t rank) {
+__device__ bool read_sums(const Args &a, Control &c, char *beside, uint32_t tmem, uint32_t rank) {
     using C = Config<kOp, kCtas, kCols>;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, q = warp % 4, half = (warp - kFirstReader) / 4;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     Ring sums(C::kSums);
     constexpr int kChunks = (kCols + 31) / 32;
-    return each_tile(a, c, [&](const Tile &t) {
+    const float *scales = reinterpret_cast<const float *>(beside);
+    char *const buffers = beside + (warp - kFirstReader) * 2 * kStoreBytes;
+    int stored = 0;
+    const bool ok = each_tile(a, c, [&](const Tile &t) {
         const int f = t.a0 + (int)rank * kRows + q * 32 + lane;
         if constexpr (C::kE4m3) {
             float sum[kChunks][16] = {};
@@ -608,15 +627,27 @@ __device__ bool read_sums(const Args &a, Control &c, const float *scales, uint32
             const bool some = t.blocks > 0;
             if (some && !warp_wait(&c.sums_full[sums.slot], sums.round, a.limits.wait_ns)) return false;
             tc_fence_after();
-            for (int col = half * 16; col < t.n; col += 32) {
-                float v[16] = {};
-                if (some) {
+            if constexpr (kOp == kGradW) {
+                constexpr int kWide = 128 / sizeof(Out);
+                const int f0 = t.a0 + (int)rank * kRows + q * 32;
+                for (int col = half * kWide; col < t.n; col += 2 * kWide) {
+                    float v[kWide] = {};
+                    if (some) {
+#pragma unroll
+                        for (int i = 0; i < kWide; i += 16)
+                            tmem_load16(lanes + sums.slot * kCols + col + i, v + i);
+                        tmem_load_wait(v);
+                    }
+                    if (f0 >= a.features || (!some && a.accumulate)) continue;
+                    if constexpr (sizeof(Out) == 2)
+                        if (a.accumulate) add_weights(a, t, f, col, v);
+                    store_weights<Out>(a, t, f0, col, v, buffers + (stored++ & 1) * kStoreBytes);
+                }
+            } else {
+                for (int col = half * 16; col < t.n; col += 32) {
+                    float v[16];
                     tmem_load16(lanes + sums.slot * kCols + col, v);
                     tmem_load_wait(v);
-                }
-                if constexpr (kOp == kGradW) {
-                    if (some || !a.accumulate) store_weights<Out>(a, t, f, col, v);
-                } else {
                     store_rows(a, t, f, col, v);
                 }
             }
@@ -629,6 +660,9 @@ __device__ bool read_sums(const Args &a, Control &c, const float *scales, uint32
         }
         return true;
     });
+    if (kOp == kGradW && lane == 0) bulk_wait_all();
+    __syncwarp();
+    return ok;
 }
 
 template <Op kOp, int kCtas, int kCols, typename Out>
@@ -638,7 +672,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(const __grid_const
     extern __shared__ char smem_raw[];
     __shared__ Control c;
     char *ring = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-    float *scales = reinterpret_cast<float *>(ring + C::kStages * (kTileA + C::kTileB));
+    char *beside = ring + C::kStages * (kTileA + C::kTileB);
     const uint32_t ring_base = smem_addr(ring);
     const int warp = threadIdx.x / 32;
     const uint32_t rank = kCtas == 1 ? 0 : blockIdx.x % kCtas;
@@ -681,9 +715,9 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(const __grid_const
         ok = find_tiles<kOp, kCtas, kCols>(a, c);
     } else if (warp == 3) {
         if constexpr (kOp == kGradW) ok = mask_blocks<kCtas, kCols>(a, c, ring);
-        if constexpr (C::kE4m3) ok = load_scales<kCtas, kCols>(a, c, scales);
+        if constexpr (C::kE4m3) ok = load_scales<kCtas, kCols>(a, c, reinterpret_cast<float *>(beside));
     } else {
-        ok = read_sums<kOp, kCtas, kCols, Out>(a, c, scales, tmem, rank);
+        ok = read_sums<kOp, kCtas, kCols, Out>(a, c, beside, tmem, rank);
     }
     if (!ok && (threadIdx.x & 31) == 0) report(a.status, MOE_ERR_TIMEOUT);
     __syncwarp();
@@ -768,7 +802,7 @@ int launch_rows(Args &a, cudaStream_t s) {
 int launch_grouped_linear(const GroupedLaunch &L) {
     const bool e4m3 = L.x_scales != nullptr;
     Args a{};
-    if (!make_tensor_map3(&a.a, L.w, e4m3, L.num_experts, L.out_features, L.in_features, kRows) ||
+    if (!make_tensor_map3(&a.a, L.w, e4m3 ? 1 : 2, L.num_experts, L.out_features, L.in_features, kRows) ||
         !make_tensor_map(&a.b, L.x, e4m3, L.num_rows, L.in_features, kBoxRows))
         return MOE_ERR_CUDA;
     a.prefix = L.expert_prefix;
@@ -786,7 +820,7 @@ int launch_grouped_linear(const GroupedLaunch &L) {
 
 int launch_grouped_grad_x(const GroupedLaunch &L) {
     Args a{};
-    if (!make_tensor_map3(&a.a, L.w, false, L.num_experts, L.out_features, L.in_features, kDepth) ||
+    if (!make_tensor_map3(&a.a, L.w, 2, L.num_experts, L.out_features, L.in_features, kDepth) ||
         !make_tensor_map(&a.b, L.x, false, L.num_rows, L.out_features, kBoxRows))
         return MOE_ERR_CUDA;
     a.prefix = L.expert_prefix;
@@ -809,7 +843,8 @@ int launch_grouped_grad_w(const GroupedGradWLaunch &L) {
     }
     Args a{};
     if (!make_tensor_map(&a.a, L.grad, false, L.num_rows, L.out_features, kDepth) ||
-        !make_tensor_map(&a.b, L.x, false, L.num_rows, L.in_features, kDepth))
+        !make_tensor_map(&a.b, L.x, false, L.num_rows, L.in_features, kDepth) ||
+        !make_tensor_map3(&a.out_map, L.out, (int)cell, L.num_experts, L.out_features, L.in_features, 32))
         return MOE_ERR_CUDA;
     a.prefix = L.expert_prefix;
     a.out = L.out;

@@ -13,11 +13,11 @@ namespace moe {
 
 // ------------------------------------------------------------------ tensor maps (host)
 
-// Map of `sets` row-major matrices [rows, cols], one behind another, whose tiles are
-// [box_rows, box_cols], box_cols covering 128 bytes, laid out in shared memory with the
-// 128-byte swizzle. Coordinates are (col, row, set), or (col, row) where sets is 0.
-// Elements outside a matrix read as 0. False if the driver refuses.
-inline bool make_tensor_map3(CUtensorMap *map, const void *base, bool bytes, uint64_t sets, uint64_t rows, uint64_t cols,
+// Map of `sets` row-major matrices [rows, cols] of `cell` bytes an element (1, 2: bf16, 4: fp32),
+// one behind another, whose tiles are [box_rows, box_cols], box_cols covering 128 bytes, laid out
+// in shared memory with the 128-byte swizzle. Coordinates are (col, row, set), or (col, row) where
+// sets is 0. Elements outside a matrix read as 0 and are not written. False if the driver refuses.
+inline bool make_tensor_map3(CUtensorMap *map, const void *base, int cell, uint64_t sets, uint64_t rows, uint64_t cols,
                              uint32_t box_rows) {
     using Encode = decltype(&cuTensorMapEncodeTiled);
     static const Encode encode = [] {
@@ -29,17 +29,19 @@ inline bool make_tensor_map3(CUtensorMap *map, const void *base, bool bytes, uin
         return reinterpret_cast<Encode>(fn);
     }();
     if (encode == nullptr) return false;
-    const cuuint64_t size = bytes ? 1 : 2;
+    const cuuint64_t size = (cuuint64_t)cell;
     const cuuint64_t dims[3] = {cols, rows, sets}, strides[2] = {cols * size, rows * cols * size};
     const cuuint32_t box[3] = {(cuuint32_t)(128 / size), box_rows, 1}, step[3] = {1, 1, 1};
-    return encode(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, sets ? 3 : 2,
-                  const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const CUtensorMapDataType type = cell == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : cell == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    return encode(map, type, sets ? 3 : 2, const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 inline bool make_tensor_map(CUtensorMap *map, const void *base, bool bytes, uint64_t rows, uint64_t cols,
                             uint32_t box_rows) {
-    return make_tensor_map3(map, base, bytes, 0, rows, cols, box_rows);
+    return make_tensor_map3(map, base, bytes ? 1 : 2, 0, rows, cols, box_rows);
 }
 
 // ------------------------------------------------------------------ TMA loads
