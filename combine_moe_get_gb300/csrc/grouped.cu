@@ -16,6 +16,7 @@
 // E4M3: the rows' scales), 4 to 11 read the sums.
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -24,13 +25,12 @@
 namespace moe {
 namespace grouped {
 
-constexpr int kThreads = 384;
-constexpr int kReaders = 8;                // warps that read sums
-constexpr int kFirstReader = 4;
+constexpr int kFirstReader = 4;            // first of the warps that read sums
 constexpr int kRows = 128;                 // features of a CTA's tile
 constexpr int kTileA = kRows * 128;        // bytes of A in a stage
 constexpr int kTileSlots = 4;              // tiles found ahead
 constexpr int kSmemBudget = 226 << 10;     // ring, what stands beside it, and 1 KB to align them
+constexpr int kScaleSlots = 2;             // E4M3: scales of four blocks each
 constexpr int kStoreBytes = 32 * 128;      // weights' gradients: 32 rows of a warp on their way out
 constexpr int kBoxRows = 32;               // rows of one copy of the ragged operand
 constexpr int kDepth = 64;                 // bf16 elements of a block along the reduction (E4M3: 128)
@@ -68,9 +68,12 @@ struct Args {
 template <Op kOp, int kCtas, int kCols>
 struct Config {
     static constexpr bool kE4m3 = kOp == kForwardE4m3;
+    static constexpr int kReaders = kE4m3 ? 12 : 8, kThreads = (kFirstReader + kReaders) * 32;
+    static constexpr int kSides = kReaders / 4;   // a quarter of the lanes is read by as many warps, 16 columns in turn
     static constexpr int kTileB = kCols / kCtas * 128;
     static constexpr int kSums = kE4m3 ? (512 / kCols < 4 ? 512 / kCols : 4) : 2;
-    static constexpr int kBeside = kE4m3 ? kSums * kCols * 4 : kOp == kGradW ? kReaders * 2 * kStoreBytes : 0;
+    static constexpr int kScales = kCols + kRows;   // E4M3: scales of a block's rows and features
+    static constexpr int kBeside = kE4m3 ? kScaleSlots * 4 * kScales * 4 : kOp == kGradW ? kReaders * 2 * kStoreBytes : 0;
     static constexpr int kFit = (kSmemBudget - 1024 - kBeside) / (kTileA + kTileB);
     static constexpr int kStages = kFit < 12 ? kFit : 12;
     static constexpr int kTmemCols = kSums * kCols <= 64 ? 64 : kSums * kCols <= 128 ? 128 : kSums * kCols <= 256 ? 256 : 512;
@@ -86,7 +89,7 @@ struct Control {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t masked_full[kMaxStages];   // a block whose rows past the expert's end are to be zeroed
     uint64_t sums_full[kMaxSums], sums_empty[kMaxSums];
-    uint64_t scales_full[kMaxSums], scales_empty[kMaxSums];
+    uint64_t scales_full[kScaleSlots], scales_empty[kScaleSlots];
     uint64_t tile_full[kTileSlots], tile_empty[kTileSlots];
     uint64_t last;
     Tile tiles[kTileSlots];
@@ -472,33 +475,113 @@ __device__ bool mask_blocks(const Args &a, Control &c, char *ring) {
     });
 }
 
-// E4M3: the scales of a block's rows, beside the block's sums.
+// Four blocks' scales of one row, from block kb: one load where rows are whole groups of four.
+__device__ __forceinline__ float4 four_scales(const float *row, int kb, int blocks, bool whole) {
+    if (whole) return __ldg(reinterpret_cast<const float4 *>(row + kb));
+    float4 v;
+    v.x = __ldg(row + min(kb, blocks - 1)), v.y = __ldg(row + min(kb + 1, blocks - 1));
+    v.z = __ldg(row + min(kb + 2, blocks - 1)), v.w = __ldg(row + min(kb + 3, blocks - 1));
+    return v;
+}
+__device__ __forceinline__ float part_of(const float4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ bool whole_fours(const float *scales, int blocks) {
+    return blocks % 4 == 0 && (reinterpret_cast<uintptr_t>(scales) & 15) == 0;
+}
+
+// E4M3: the scales of the blocks' rows and features, four blocks at a time; the loads of the next four are under way
+// while the readers use these (a load behind each block would be waited for each time).
 template <int kCtas, int kCols>
-__device__ bool load_scales(const Args &a, Control &c, float *scales) {
+__device__ bool load_scales(const Args &a, Control &c, float *scales, uint32_t rank) {
     using C = Config<kForwardE4m3, kCtas, kCols>;
     const int lane = threadIdx.x & 31;
-    Ring r(C::kSums);
+    Ring r(kScaleSlots);
     return each_tile(a, c, [&](const Tile &t) {
-        constexpr int kPer = (kCols + 31) / 32;
-        const float *from[kPer];
+        constexpr int kPerRow = kCols / 32, kPer = kPerRow + kRows / 32;
+        static_assert(kCols % 32 == 0);
+        const bool whole = whole_fours(a.b_scales, t.blocks) && whole_fours(a.a_scales, t.blocks);
+        const int f0 = t.a0 + (int)rank * kRows;
+        float4 next[kPer];
+        const auto fetch = [&](int kb) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) from[i] = a.b_scales + (size_t)(t.row0 + min(lane + 32 * i, t.n - 1)) * t.blocks;
-        float next[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) next[i] = __ldg(from[i]);
-        for (int kb = 0; kb < t.blocks; ++kb, r.next()) {
+            for (int i = 0; i < kPer; ++i) {
+                const float *from = i < kPerRow
+                                        ? a.b_scales + (size_t)(t.row0 + min(lane + 32 * i, t.n - 1)) * t.blocks
+                                        : a.a_scales + ((size_t)t.e * a.features + min(f0 + lane + 32 * (i - kPerRow), a.features - 1)) * t.blocks;
+                if (i >= kPerRow || 32 * i < t.n) next[i] = four_scales(from, kb, t.blocks, whole);
+            }
+        };
+        fetch(0);
+        for (int kb = 0; kb < t.blocks; kb += 4, r.next()) {
             if (!warp_wait(&c.scales_empty[r.slot], r.round ^ 1, a.limits.wait_ns)) return false;
+            float *to = scales + r.slot * 4 * C::kScales + lane;
 #pragma unroll
             for (int i = 0; i < kPer; ++i)
-                if (lane + 32 * i < kCols) scales[r.slot * kCols + lane + 32 * i] = next[i];
-            if (kb + 1 < t.blocks)
+                if (i >= kPerRow || 32 * i < t.n)
 #pragma unroll
-                for (int i = 0; i < kPer; ++i) next[i] = __ldg(from[i] + kb + 1);
+                    for (int j = 0; j < 4; ++j) to[j * C::kScales + 32 * i] = part_of(next[i], j);
             __syncwarp();
             if (lane == 0) mbar_arrive(&c.scales_full[r.slot]);
+            if (kb + 4 < t.blocks) fetch(kb + 4);
         }
         return true;
     });
+}
+
+// Sums of E4M3 blocks are read in the tensor core's own fragments, 32 lanes of tensor memory x 16 columns: register
+// 8 h + 4 g + 2 p + i of a lane holds feature 16 h + 8 p + lane / 4 and column 8 g + 2 (lane % 4) + i. A lane then
+// needs four features' scales and a quarter of the columns', where lanes that hold whole rows need all of them: their
+// loads from shared memory were 60% of the time.
+__device__ __forceinline__ void tmem_load_fragments(uint32_t addr, float (&v)[16]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t r[8];
+        asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(addr + ((uint32_t)(16 * h) << 16)));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * h + i] = __uint_as_float(r[i]);
+    }
+}
+// Two columns to an instruction: a multiplication and an addition for each pair of sums, as fast as two of each but half
+// the instructions, which are what the readers run out of.
+__device__ __forceinline__ void scaled_add(float (&sum)[16], const float (&v)[16], const float2 (&columns)[2],
+                                           const float (&features)[4]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {   // 4 h + 2 g + p
+        const float2 c = columns[j / 2 % 2];
+        asm("{\n\t.reg .b64 s, f, v;\n\t"
+            "mov.b64 s, {%4, %5};\n\tmov.b64 f, {%6, %6};\n\tmul.rn.f32x2 s, s, f;\n\t"
+            "mov.b64 f, {%2, %3};\n\tmov.b64 v, {%0, %1};\n\tfma.rn.f32x2 v, f, s, v;\n\tmov.b64 {%0, %1}, v;\n\t}"
+            : "+f"(sum[2 * j]), "+f"(sum[2 * j + 1])
+            : "f"(v[2 * j]), "f"(v[2 * j + 1]), "f"(c.x), "f"(c.y), "f"(features[j / 4 * 2 + j % 2]));
+    }
+}
+// One block's sums, kN times 16 columns kStep apart.
+template <int kN, int kStep>
+__device__ __forceinline__ void add_block(float (*sum)[16], uint32_t from, const float *sx, const float (&features)[4]) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+        float v[16];
+        tmem_load_fragments(from + i * kStep, v);
+        const float2 columns[2] = {*reinterpret_cast<const float2 *>(sx + i * kStep),
+                                   *reinterpret_cast<const float2 *>(sx + i * kStep + 8)};
+        tmem_load_wait(v);
+        scaled_add(sum[i], v, columns, features);
+    }
+}
+
+// Neighbouring features, held four lanes apart, come together for one store.
+__device__ __forceinline__ void store_fragments(const Args &a, const Tile &t, int f0, int col, const float (&sum)[16]) {
+    const int lane = threadIdx.x & 31, odd = lane >> 2 & 1;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float x = sum[2 * j], y = sum[2 * j + 1];
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? x : y, 4);
+        const __nv_bfloat162 pair = odd ? __floats2bfloat162_rn(got, y) : __floats2bfloat162_rn(x, got);
+        const int f = f0 + j / 4 * 16 + j % 2 * 8 + (lane >> 3) * 2, c = col + j / 2 % 2 * 8 + (lane & 3) * 2 + odd;
+        if (f < a.features && c < t.n)
+            *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + (size_t)(t.row0 + c) * a.features + f) = pair;
+    }
 }
 
 // Lanes hold features, registers rows: neighbouring lanes exchange halves of two
@@ -573,10 +656,10 @@ __device__ __forceinline__ void add_weights(const Args &a, const Tile &t, int f,
 template <Op kOp, int kCtas, int kCols, typename Out>
 __device__ bool read_sums(const Args &a, Control &c, char *beside, uint32_t tmem, uint32_t rank) {
     using C = Config<kOp, kCtas, kCols>;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, q = warp % 4, half = (warp - kFirstReader) / 4;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, q = warp % 4, side = (warp - kFirstReader) / 4;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
-    Ring sums(C::kSums);
-    constexpr int kChunks = (kCols + 31) / 32;
+    Ring sums(C::kSums), fours(kScaleSlots);
+    constexpr int kStep = 16 * C::kSides, kChunks = (kCols + kStep - 1) / kStep;
     const float *scales = reinterpret_cast<const float *>(beside);
     char *const buffers = beside + (warp - kFirstReader) * 2 * kStoreBytes;
     int stored = 0;
@@ -584,44 +667,42 @@ __device__ bool read_sums(const Args &a, Control &c, char *beside, uint32_t tmem
         const int f = t.a0 + (int)rank * kRows + q * 32 + lane;
         if constexpr (C::kE4m3) {
             float sum[kChunks][16] = {};
-            // this lane's weight row's scales, one a block
-            const float *sw = a.a_scales + ((size_t)t.e * a.features + min(f, a.features - 1)) * t.blocks;
-            float next = __ldg(sw);
-            for (int kb = 0; kb < t.blocks; ++kb, sums.next()) {
-                const float scale = next;
-                if (kb + 1 < t.blocks) next = __ldg(sw + kb + 1);
-                if (!warp_wait(&c.scales_full[sums.slot], sums.round, a.limits.wait_ns)) return false;
-                if (!warp_wait(&c.sums_full[sums.slot], sums.round, a.limits.wait_ns)) return false;
-                tc_fence_after();
+            const uint32_t empty = peer_addr(&c.sums_empty[0], 0);
+            const auto blocks = [&](auto chunks) {   // straight code for each number of chunks: branches cost as much as sums
+                constexpr int kN = decltype(chunks)::value;
+                for (int kb = 0; kb < t.blocks; ++kb, sums.next()) {
+                    if (kb % 4 == 0 && !warp_wait(&c.scales_full[fours.slot], fours.round, a.limits.wait_ns)) return false;
+                    const float *sx = scales + (fours.slot * 4 + kb % 4) * C::kScales;
+                    float features[4];
 #pragma unroll
-                for (int i = 0; i < kChunks; ++i) {
-                    const int col = (2 * i + half) * 16;
-                    if (col < t.n) {
-                        float v[16];
-                        tmem_load16(lanes + sums.slot * kCols + col, v);
-                        tmem_load_wait(v);
-                        const float4 *sx = reinterpret_cast<const float4 *>(scales + sums.slot * kCols + col);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float4 s = sx[j];
-                            sum[i][4 * j] = fmaf(v[4 * j], scale * s.x, sum[i][4 * j]);
-                            sum[i][4 * j + 1] = fmaf(v[4 * j + 1], scale * s.y, sum[i][4 * j + 1]);
-                            sum[i][4 * j + 2] = fmaf(v[4 * j + 2], scale * s.z, sum[i][4 * j + 2]);
-                            sum[i][4 * j + 3] = fmaf(v[4 * j + 3], scale * s.w, sum[i][4 * j + 3]);
-                        }
+                    for (int j = 0; j < 4; ++j) features[j] = sx[kCols + q * 32 + j * 8 + lane / 4];
+                    if (!warp_wait(&c.sums_full[sums.slot], sums.round, a.limits.wait_ns)) return false;
+                    tc_fence_after();
+                    add_block<kN, kStep>(sum, lanes + sums.slot * kCols + side * 16, sx + side * 16 + (lane & 3) * 2, features);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_at(empty + sums.slot * 8);
+                    if (kb % 4 == 3 || kb + 1 == t.blocks) {
+                        if (lane == 0) mbar_arrive(&c.scales_empty[fours.slot]);
+                        fours.next();
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    arrive_at(peer_addr(&c.sums_empty[sums.slot], 0));
-                    mbar_arrive(&c.scales_empty[sums.slot]);
-                }
+                return true;
+            };
+            const int chunks = t.n <= side * 16 ? 0 : (t.n - side * 16 + kStep - 1) / kStep;
+            bool done;
+            switch (chunks) {
+                case 0: done = blocks(std::integral_constant<int, 0>()); break;
+                case 1: done = blocks(std::integral_constant<int, 1>()); break;
+                case 2: done = blocks(std::integral_constant<int, 2>()); break;
+                case 3: done = blocks(std::integral_constant<int, 3>()); break;
+                default: done = blocks(std::integral_constant<int, kChunks>()); break;
             }
+            if (!done) return false;
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
-                const int col = (2 * i + half) * 16;
-                if (col < t.n) store_rows(a, t, f, col, sum[i]);
+                const int col = i * kStep + side * 16;
+                if (col < t.n) store_fragments(a, t, t.a0 + (int)rank * kRows + q * 32, col, sum[i]);
             }
         } else {
             const bool some = t.blocks > 0;
@@ -630,7 +711,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *beside, uint32_t tmem
             if constexpr (kOp == kGradW) {
                 constexpr int kWide = 128 / sizeof(Out);
                 const int f0 = t.a0 + (int)rank * kRows + q * 32;
-                for (int col = half * kWide; col < t.n; col += 2 * kWide) {
+                for (int col = side * kWide; col < t.n; col += C::kSides * kWide) {
                     float v[kWide] = {};
                     if (some) {
 #pragma unroll
@@ -644,7 +725,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *beside, uint32_t tmem
                     store_weights<Out>(a, t, f0, col, v, buffers + (stored++ & 1) * kStoreBytes);
                 }
             } else {
-                for (int col = half * 16; col < t.n; col += 32) {
+                for (int col = side * 16; col < t.n; col += kStep) {
                     float v[16];
                     tmem_load16(lanes + sums.slot * kCols + col, v);
                     tmem_load_wait(v);
@@ -666,7 +747,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *beside, uint32_t tmem
 }
 
 template <Op kOp, int kCtas, int kCols, typename Out>
-__global__ __launch_bounds__(kThreads, 1) void grouped_kernel(const __grid_constant__ Args a) {
+__global__ __launch_bounds__((Config<kOp, kCtas, kCols>::kThreads), 1) void grouped_kernel(const __grid_constant__ Args a) {
     using C = Config<kOp, kCtas, kCols>;
     const WarpTrace trace(a.trace, MOE_TRACE_GROUPED);
     extern __shared__ char smem_raw[];
@@ -684,13 +765,15 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(const __grid_const
         }
         for (int i = 0; i < C::kSums; ++i) {
             mbar_init(&c.sums_full[i], 1);
-            mbar_init(&c.sums_empty[i], kCtas * kReaders);
+            mbar_init(&c.sums_empty[i], kCtas * C::kReaders);
+        }
+        for (int i = 0; i < kScaleSlots; ++i) {
             mbar_init(&c.scales_full[i], 1);
-            mbar_init(&c.scales_empty[i], kReaders);
+            mbar_init(&c.scales_empty[i], C::kReaders);
         }
         for (int i = 0; i < kTileSlots; ++i) {
             mbar_init(&c.tile_full[i], 1);
-            mbar_init(&c.tile_empty[i], 1 + (rank == 0) + C::kHelper + kReaders);
+            mbar_init(&c.tile_empty[i], 1 + (rank == 0) + C::kHelper + C::kReaders);
         }
         mbar_init(&c.last, 1);
         fence_barrier_init();
@@ -715,7 +798,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_kernel(const __grid_const
         ok = find_tiles<kOp, kCtas, kCols>(a, c);
     } else if (warp == 3) {
         if constexpr (kOp == kGradW) ok = mask_blocks<kCtas, kCols>(a, c, ring);
-        if constexpr (C::kE4m3) ok = load_scales<kCtas, kCols>(a, c, reinterpret_cast<float *>(beside));
+        if constexpr (C::kE4m3) ok = load_scales<kCtas, kCols>(a, c, reinterpret_cast<float *>(beside), rank);
     } else {
         ok = read_sums<kOp, kCtas, kCols, Out>(a, c, beside, tmem, rank);
     }
@@ -742,7 +825,7 @@ int resident() {
     if (n == 0) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(device_sm_count() / kCtas * kCtas);
-        cfg.blockDim = dim3(kThreads);
+        cfg.blockDim = dim3(Config<kOp, kCtas, kCols>::kThreads);
         cfg.dynamicSmemBytes = Config<kOp, kCtas, kCols>::smem();
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -764,7 +847,7 @@ int launch(Args &a, int64_t most_tiles, cudaStream_t s) {
     const int64_t ctas = std::min<int64_t>(resident<kOp, kCtas, kCols, Out>(), most_tiles * kCtas);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(C::kThreads);
     cfg.dynamicSmemBytes = C::smem();
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
@@ -814,7 +897,7 @@ int launch_grouped_linear(const GroupedLaunch &L) {
     a.limits = wait_limits();
     a.trace = trace_args();
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
-    if (e4m3) return launch_rows<kForwardE4m3, 2, 128>(a, s);
+    if (e4m3) return launch_rows<kForwardE4m3, 2, 192>(a, s);
     return launch_rows<kForward, 2, 256>(a, s);
 }
 
