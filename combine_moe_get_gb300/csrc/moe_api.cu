@@ -788,7 +788,7 @@ MOE_API int moe_add_rms_norm(const void *x, const void *residual, int num_tokens
         !aligned(scales, 4))
         return MOE_ERR_MISALIGNED;
     return moe::launch_norm(moe::NormLaunch{x, residual, nullptr, num_tokens, hidden, weight, weight_type, eps, out,
-                                            residual_out, codes, scales, nullptr, nullptr, stream});
+                                            residual_out, codes, scales, nullptr, nullptr, status, stream});
 }
 
 MOE_API size_t moe_add_rms_norm_backward_workspace_size(int num_tokens, int hidden) {
@@ -807,7 +807,8 @@ MOE_API int moe_add_rms_norm_backward(const void *h, const void *weight, int wei
         return MOE_ERR_MISALIGNED;
     if (num_tokens > 0 && workspace_bytes < moe::norm_backward_workspace_bytes(num_tokens, hidden)) return MOE_ERR_WORKSPACE;
     return moe::launch_norm_backward(moe::NormLaunch{h, grad_residual, grad, num_tokens, hidden, weight, weight_type, eps,
-                                                     grad_x, nullptr, nullptr, nullptr, grad_weight, workspace, stream});
+                                                     grad_x, nullptr, nullptr, nullptr, grad_weight, workspace, status,
+                                                     stream});
 }
 
 }  // extern "C"

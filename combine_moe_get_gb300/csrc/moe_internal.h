@@ -420,6 +420,7 @@ struct NormLaunch {
     float *scales;
     float *grad_weight;        // backward
     void *workspace;           // backward
+    int32_t *status;
     void *stream;
 };
 

@@ -24,6 +24,9 @@ struct NormArgs {
     uint8_t *codes;
     float *scales;
     float *parts, *grad_weight;          // backward: [parts][H] sums of a CTA's rows each
+    int32_t *status;
+    uint64_t wait_ns;
+    int stages;
     int T, H, num_parts;
     int row_warps;                       // warps of a row
     TraceArgs trace;
@@ -62,7 +65,7 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*space)[kMaxWarps
 }
 
 template <int kVec, bool kCodes>
-__global__ __launch_bounds__(kVec < 8 ? 512 : 1024) void norm_kernel(const __grid_constant__ NormArgs a) {
+__global__ __launch_bounds__(512) void norm_kernel(const __grid_constant__ NormArgs a) {
     const WarpTrace trace(a.trace, MOE_TRACE_NORM);
     __shared__ float space[1][kMaxWarps];
     grid_dependency_wait();
@@ -118,104 +121,175 @@ __global__ __launch_bounds__(kVec < 8 ? 512 : 1024) void norm_kernel(const __gri
     }
 }
 
-// A CTA takes every num_parts-th row and keeps the weight's gradient of its columns in registers.
+// Barrier `id` for `threads` of the CTA.
+__device__ __forceinline__ void barrier(int id, int threads) {
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Two vectors a thread and 28 warps, in groups where rows are short: fewer shuffles a row than with one vector, and two
+// rows at once where 28 warps in step would all wait for each row's sums. Rows beyond 14336 take four and 16 warps.
+__host__ __device__ constexpr int backward_warps(int vec) { return vec == 2 ? 28 : 16; }
+
+// Rows on their way to a group of warps: h, the gradient and the residual's gradient of a row to a stage.
+constexpr int kMostStages = 8;
+struct RowRing {
+    char *at;
+    uint64_t *full;
+    int stages, arrays, row_bytes;
+    __device__ int stage_bytes() const { return arrays * row_bytes; }
+    // By one thread; nothing for rows past the last.
+    __device__ void fetch(const NormArgs &a, int64_t row, int slot, uint64_t policy) const {
+        if (row >= a.T) return;
+        mbar_arrive_expect_tx(full + slot, stage_bytes());
+        const size_t from = (size_t)row * a.H;
+        char *to = at + (size_t)slot * stage_bytes();
+        bulk_load(to, a.x + from, row_bytes, full + slot, policy);
+        bulk_load(to + row_bytes, a.grad + from, row_bytes, full + slot, policy);
+        if (arrays == 3) bulk_load(to + 2 * row_bytes, a.residual + from, row_bytes, full + slot, policy);
+    }
+    __device__ uint4 read(int slot, int array, int col) const {
+        return *reinterpret_cast<const uint4 *>(at + (size_t)slot * stage_bytes() + array * row_bytes + col * 2);
+    }
+};
+
+// The CTA's groups of `row_warps` warps take rows in turn, and keep the weight's gradient of their columns in registers;
+// at the end the groups' sums are added up in shared memory, in order. Rows come through rings in shared memory, as
+// many ahead as it holds. 4096 x 7168: 47 us, the weight's sums included (5.0 TB/s); with loads into registers, one row
+// ahead, 81; one vector a thread 54.
 template <int kVec>
-__global__ __launch_bounds__(kVec < 8 ? 512 : 1024) void norm_backward_kernel(const __grid_constant__ NormArgs a) {
+__global__ __launch_bounds__(backward_warps(kVec) * 32) void norm_backward_kernel(const __grid_constant__ NormArgs a) {
     const WarpTrace trace(a.trace, MOE_TRACE_NORM_BACKWARD);
     __shared__ float space[2][2][kMaxWarps];
+    __shared__ uint64_t full[kMaxWarps][kMostStages];
+    extern __shared__ __align__(128) char rings[];
+    const int threads = a.row_warps * 32, groups = blockDim.x / threads, group = threadIdx.x / threads;
+    const int tid = threadIdx.x - group * threads, lane = threadIdx.x & 31, warp = threadIdx.x / 32, first = group * a.row_warps;
+    RowRing ring{nullptr, full[group], a.stages, a.residual ? 3 : 2, a.H * 2};
+    ring.at = rings + (size_t)group * a.stages * ring.stage_bytes();
+    if (tid == 0) {
+        for (int i = 0; i < a.stages; ++i) mbar_init(ring.full + i, 1);
+        fence_barrier_init();
+    }
+    __syncthreads();
     grid_dependency_wait();
     grid_launch_dependents();
-    const int threads = blockDim.x, tid = threadIdx.x;
     float dw[kVec][8] = {};
-    int turn = 0;
-    for (int64_t row = blockIdx.x; row < a.T; row += gridDim.x, turn ^= 1) {
-        const size_t base = (size_t)row * a.H;
-        uint4 h4[kVec], g4[kVec], res[kVec];
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            const int col = (j * threads + tid) * 8;
-            h4[j] = g4[j] = res[j] = make_uint4(0, 0, 0, 0);
-            if (col < a.H) {
-                h4[j] = load_once(a.x + base + col);
-                g4[j] = load_once(a.grad + base + col);
-                if (a.residual) res[j] = load_once(a.residual + base + col);
-            }
-        }
+    const int64_t step = (int64_t)gridDim.x * groups;
+    int64_t row = (int64_t)blockIdx.x * groups + group;
+    const uint64_t policy = policy_evict_first();
+    if (tid == 0)
+        for (int i = 0; i < a.stages; ++i) ring.fetch(a, row + i * step, i, policy);
+    int slot = 0, turn = 0;
+    uint32_t round = 0;
+    bool ok = true;
+    for (; row < a.T; row += step, turn ^= 1) {
+        ok = mbar_wait_bounded(ring.full + slot, round, a.wait_ns) && ok;
+        uint4 now[kVec][3];
         float sum[2] = {};   // of h^2 and of d h
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
             const int col = (j * threads + tid) * 8;
-            float h[8], g[8], w[8] = {};
-            widen(h4[j], h);
-            widen(g4[j], g);
-            if (col < a.H) load_weight(a, col, w);
+            now[j][0] = now[j][1] = now[j][2] = make_uint4(0, 0, 0, 0);
+            if (col >= a.H) continue;
+            now[j][0] = ring.read(slot, 0, col);
+            now[j][1] = ring.read(slot, 1, col);
+            if (a.residual) now[j][2] = ring.read(slot, 2, col);
+            float h[8], g[8], w[8];
+            widen(now[j][0], h);
+            widen(now[j][1], g);
+            load_weight(a, col, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 sum[0] = fmaf(h[i], h[i], sum[0]);
                 sum[1] = fmaf(g[i] * w[i], h[i], sum[1]);
             }
         }
-        row_sums(sum, space[turn], a.row_warps);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+        if (a.row_warps > 1) {   // the two halves of `space` in turn, so that one barrier a row is enough
+            if (lane == 0) space[turn][0][warp] = sum[0], space[turn][1][warp] = sum[1];
+            barrier(1 + group, threads);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                sum[i] = lane < a.row_warps ? space[turn][i][first + lane] : 0.0f;
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+            }
+        } else {
+            __syncwarp();
+        }
+        if (tid == 0) ring.fetch(a, row + a.stages * step, slot, policy);   // every thread has read the stage
+        if (++slot == a.stages) slot = 0, round ^= 1;
         const float r = rsqrtf(sum[0] / a.H + a.eps), m = r * r * (sum[1] / a.H);   // m h = n mean(d n)
 #pragma unroll
         for (int j = 0; j < kVec; ++j) {
             const int col = (j * threads + tid) * 8;
             if (col >= a.H) continue;
             float h[8], g[8], w[8], add[8];
-            widen(h4[j], h);
-            widen(g4[j], g);
-            widen(res[j], add);
+            widen(now[j][0], h);
+            widen(now[j][1], g);
+            widen(now[j][2], add);
             load_weight(a, col, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 dw[j][i] = fmaf(g[i], h[i] * r, dw[j][i]);
                 add[i] += r * (g[i] * w[i] - h[i] * m);
             }
-            *reinterpret_cast<uint4 *>(a.out + base + col) = narrow(add);
+            *reinterpret_cast<uint4 *>(a.out + (size_t)row * a.H + col) = narrow(add);
         }
     }
+    if (!ok && lane == 0) report(a.status, MOE_ERR_TIMEOUT);
+    __syncthreads();   // no copy is under way: every stage that was fetched has been waited for
+    float *sums = reinterpret_cast<float *>(rings);   // [H], with more than one group
+    for (int k = groups - 1; k >= 0; --k) {   // the last group's first, the first group's out
+        if (group == k)
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-        const int col = (j * threads + tid) * 8;
-        if (col >= a.H) continue;
-        float4 *p = reinterpret_cast<float4 *>(a.parts + (size_t)blockIdx.x * a.H + col);
-        p[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
-        p[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+            for (int j = 0; j < kVec; ++j) {
+                const int col = (j * threads + tid) * 8;
+                if (col >= a.H) continue;
+                if (k + 1 < groups)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dw[j][i] += sums[col + i];
+                float4 *to = reinterpret_cast<float4 *>(k > 0 ? sums + col : a.parts + (size_t)blockIdx.x * a.H + col);
+                to[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
+                to[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+            }
+        __syncthreads();
     }
 }
 
-// The weight's gradient: the CTAs' sums, in order. 32 columns a CTA, its 8 warps every eighth part each.
-__global__ __launch_bounds__(256) void norm_weight_kernel(const __grid_constant__ NormArgs a) {
+// The weight's gradient: the CTAs' sums, in order. 32 columns a CTA, its 16 warps every 16th part each.
+constexpr int kWeightWarps = 16;
+__global__ __launch_bounds__(kWeightWarps * 32) void norm_weight_kernel(const __grid_constant__ NormArgs a) {
     const WarpTrace trace(a.trace, MOE_TRACE_NORM_WEIGHT);
-    __shared__ float space[8][32];
+    __shared__ float space[kWeightWarps][32];
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x / 32, col = blockIdx.x * 32 + lane;
     float sum = 0.0f;
     if (col < a.H)
 #pragma unroll 8
-        for (int p = warp; p < a.num_parts; p += 8) sum += __ldcg(a.parts + (size_t)p * a.H + col);
+        for (int p = warp; p < a.num_parts; p += kWeightWarps) sum += __ldcg(a.parts + (size_t)p * a.H + col);
     space[warp][lane] = sum;
     __syncthreads();
     if (warp == 0 && col < a.H) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) sum += space[i][lane];
+        for (int i = 1; i < kWeightWarps; ++i) sum += space[i][lane];
         a.grad_weight[col] = sum;
     }
 }
 
-// Vectors of 8 channels that a thread holds, for rows of H: `most` warps a row at best, else as many as fit.
+// Vectors of 8 channels that a thread holds so that a row of H takes at most `most_warps` warps.
 int vectors(int H, int most_warps) {
     int v = 1;
-    while (v < 8 && (H + v * 256 - 1) / (v * 256) > most_warps) v *= 2;
+    while ((H + v * 256 - 1) / (v * 256) > most_warps) v *= 2;
     return v;
 }
 
-// CTAs of the backward kernel, each with a part of the weight's gradient.
-int backward_parts(int T) {
-    const int most = 2 * device_sm_count();
-    return T < most ? T : most;
-}
+constexpr int kRingBytes = 200 << 10;   // of a CTA's rings
+constexpr int kMaxParts = 160;   // CTAs of the backward kernel, each with a part of the weight's gradient
 
 template <int kVec>
 cudaError_t launch_forward(NormArgs &a, cudaStream_t s) {
@@ -229,12 +303,25 @@ cudaError_t launch_forward(NormArgs &a, cudaStream_t s) {
 template <int kVec>
 cudaError_t launch_backward(NormArgs &a, cudaStream_t s) {
     a.row_warps = (a.H + kVec * 256 - 1) / (kVec * 256);
-    return launch_kernel(norm_backward_kernel<kVec>, dim3(a.num_parts), dim3(a.row_warps * 32), 0, s, tuning().overlap != 0, a);
+    // as many rows at once as a CTA has warps for (15: a barrier each), one CTA an SM
+    int groups = backward_warps(kVec) / a.row_warps;
+    if (groups > 15) groups = 15;
+    const int ctas = device_sm_count() < kMaxParts ? device_sm_count() : kMaxParts;
+    if (groups > (a.T + ctas - 1) / ctas) groups = (a.T + ctas - 1) / ctas;
+    const int64_t need = ((int64_t)a.T + groups - 1) / groups;
+    a.num_parts = need < ctas ? (int)need : ctas;
+    const int stage = groups * (a.residual ? 3 : 2) * a.H * 2;   // at most 96 KB
+    a.stages = kRingBytes / stage < kMostStages ? kRingBytes / stage : kMostStages;
+    size_t smem = (size_t)a.stages * stage;   // at least two stages of 4 H bytes, room for the groups' sums too
+    const int rc = ensure_dynamic_smem((const void *)norm_backward_kernel<kVec>, kRingBytes);
+    if (rc != MOE_OK) return cudaErrorUnknown;
+    return launch_kernel(norm_backward_kernel<kVec>, dim3(a.num_parts), dim3(groups * a.row_warps * 32), smem, s,
+                         tuning().overlap != 0, a);
 }
 
 }  // namespace
 
-size_t norm_backward_workspace_bytes(int T, int H) { return (size_t)(T < 512 ? T : 512) * H * sizeof(float); }
+size_t norm_backward_workspace_bytes(int T, int H) { return (size_t)(T < kMaxParts ? T : kMaxParts) * H * sizeof(float); }
 
 int launch_norm(const NormLaunch &L) {
     if (L.num_tokens == 0) return MOE_OK;
@@ -251,8 +338,7 @@ int launch_norm(const NormLaunch &L) {
     switch (vectors(a.H, 16)) {
         case 1: e = launch_forward<1>(a, s); break;
         case 2: e = launch_forward<2>(a, s); break;
-        case 4: e = launch_forward<4>(a, s); break;
-        default: e = launch_forward<8>(a, s); break;
+        default: e = launch_forward<4>(a, s); break;
     }
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -269,17 +355,13 @@ int launch_norm_backward(const NormLaunch &L) {
     a.out = static_cast<__nv_bfloat16 *>(L.out);
     a.parts = static_cast<float *>(L.workspace), a.grad_weight = L.grad_weight;
     a.T = L.num_tokens, a.H = L.hidden;
-    a.num_parts = backward_parts(a.T) < 512 ? backward_parts(a.T) : 512;
+    a.status = L.status;
+    a.wait_ns = wait_limits().wait_ns;
     a.trace = trace_args();
     cudaError_t e;
-    switch (vectors(a.H, 16)) {
-        case 1: e = launch_backward<1>(a, s); break;
-        case 2: e = launch_backward<2>(a, s); break;
-        case 4: e = launch_backward<4>(a, s); break;
-        default: e = launch_backward<8>(a, s); break;
-    }
+    e = a.H <= 14336 ? launch_backward<2>(a, s) : launch_backward<4>(a, s);
     if (e == cudaSuccess)
-        e = launch_kernel(norm_weight_kernel, dim3((a.H + 31) / 32), dim3(256), 0, s, tuning().overlap != 0, a);
+        e = launch_kernel(norm_weight_kernel, dim3((a.H + 31) / 32), dim3(kWeightWarps * 32), 0, s, tuning().overlap != 0, a);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

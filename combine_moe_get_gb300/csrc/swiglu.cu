@@ -12,7 +12,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;         // pieces that a warp loads before it works on the first
+constexpr int kUnroll = 4;         // backward: vectors that a thread loads before it works on the first
 constexpr int kPiece = 256;        // channels of a warp's piece
 
 struct SwigluArgs {
@@ -24,6 +24,7 @@ struct SwigluArgs {
     float *grad_weights;   // backward
     int32_t *status;
     int M, I;
+    int row_warps;         // backward
     TraceArgs trace;
 };
 
@@ -37,95 +38,131 @@ __device__ __forceinline__ int rows_in_use(const SwigluArgs &a) {
 // exp and the quotient are the fast ones, off by some 2^-21 of the sigmoid: an eighth of an E4M3 or bf16 rounding's 2^-9 at most
 __device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
 
+// Pieces of 256 channels in order, a warp's own `step` apart, without a division for each.
+struct Pieces {
+    int64_t row;
+    int piece, pieces, step_piece;
+    int64_t step_row;
+    __device__ Pieces(int64_t first, int64_t step, int n) : pieces(n) {
+        row = div_count(first, n), piece = (int)(first - row * n);
+        step_row = div_count(step, n), step_piece = (int)(step - step_row * n);
+    }
+    __device__ void next() {
+        row += step_row, piece += step_piece;
+        if (piece >= pieces) piece -= pieces, ++row;
+    }
+};
+
 template <bool kE4m3>
 __global__ __launch_bounds__(kThreads) void swiglu_kernel(const __grid_constant__ SwigluArgs a) {
     const WarpTrace trace(a.trace, MOE_TRACE_SWIGLU);
     grid_dependency_wait();
     grid_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int pieces = (a.I + kPiece - 1) / kPiece;
-    const int64_t total = (int64_t)rows_in_use(a) * pieces;
-    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-    for (int64_t u0 = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; u0 < total; u0 += warps * kUnroll) {
-        uint4 g[kUnroll], u[kUnroll];
-        int64_t row[kUnroll];
-        int col[kUnroll];
-#pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-            const int64_t piece = u0 + j * warps;
-            row[j] = div_count(piece, pieces);
-            col[j] = (int)(piece - row[j] * pieces) * kPiece + lane * 8;
-            g[j] = u[j] = make_uint4(0, 0, 0, 0);
-            if (piece < total && col[j] < a.I) {
-                const __nv_bfloat16 *p = a.gate_up + (size_t)row[j] * 2 * a.I + col[j];
-                g[j] = load_once(p);
-                u[j] = load_once(p + a.I);
-            }
+    const int64_t rows = rows_in_use(a);
+    Pieces p((int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32, (int64_t)gridDim.x * (kThreads / 32),
+             (a.I + kPiece - 1) / kPiece);
+    for (; p.row < rows; p.next()) {
+        const int col = p.piece * kPiece + lane * 8;
+        const bool in = col < a.I;
+        const size_t at = (size_t)p.row * a.I + col;
+        uint4 g = make_uint4(0, 0, 0, 0), u = g;
+        if (in) {
+            const __nv_bfloat16 *from = a.gate_up + at + (size_t)p.row * a.I;
+            g = load_once(from);
+            u = load_once(from + a.I);
         }
+        const float w = a.row_weights == nullptr ? 1.0f : __ldg(a.row_weights + p.row);
+        float z[8], v[8];
+        widen(g, z);
+        widen(u, v);
 #pragma unroll
-        for (int j = 0; j < kUnroll; ++j) {
-            if (u0 + j * warps >= total) break;
-            const float w = a.row_weights == nullptr ? 1.0f : __ldg(a.row_weights + row[j]);
-            float z[8], v[8];
-            widen(g[j], z);
-            widen(u[j], v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = z[i] * sigmoid(z[i]) * v[i] * w;
-            const size_t at = (size_t)row[j] * a.I + col[j];
-            if constexpr (kE4m3) {   // I is a multiple of 128: 16 lanes are in it or not
-                uint2 codes;
-                const float scale = quantise(v, codes);
-                if (col[j] < a.I) {
-                    *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + at) = codes;
-                    if ((lane & 15) == 0) a.scales[at / 128] = scale;
-                }
-            } else if (col[j] < a.I) {
-                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at) = narrow(v);
+        for (int i = 0; i < 8; ++i) v[i] *= z[i] * sigmoid(z[i]) * w;
+        if constexpr (kE4m3) {   // I is a multiple of 128: 16 lanes are in it or not
+            uint2 codes;
+            const float scale = quantise(v, codes);
+            if (in) {
+                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(a.out) + at) = codes;
+                if ((lane & 15) == 0) a.scales[at / 128] = scale;
             }
+        } else if (in) {
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + at) = narrow(v);
         }
     }
 }
 
-// A warp takes whole rows where their weights want a gradient (a row's sum stays in
-// the warp, in a fixed order), else pieces.
-template <bool kWeights>
+struct Gradients {
+    uint4 gate, up;
+};
+// Of eight channels; returns their part of the row weight's gradient.
+__device__ __forceinline__ float gradients(const uint4 &g4, const uint4 &u4, const uint4 &d4, float w, Gradients &out) {
+    float z[8], v[8], d[8], sum = 0.0f;
+    widen(g4, z);
+    widen(u4, v);
+    widen(d4, d);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float s = sigmoid(z[i]), silu = z[i] * s, up = v[i], dh = d[i] * w;
+        sum = fmaf(d[i], silu * up, sum);
+        v[i] = dh * silu;
+        z[i] = dh * up * s * fmaf(z[i], 1.0f - s, 1.0f);
+    }
+    out.gate = narrow(z);
+    out.up = narrow(v);
+    return sum;
+}
+
+// `row_warps` warps to a row, up to kUnroll times 8 channels a thread at once; a row's sum of the weight's gradient is
+// added up in a fixed order.
 __global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(const __grid_constant__ SwigluArgs a) {
     const WarpTrace trace(a.trace, MOE_TRACE_SWIGLU_BACKWARD);
+    __shared__ float space[2][kThreads / 32];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int pieces = (a.I + kPiece - 1) / kPiece;
-    const int rows = rows_in_use(a);
-    const int64_t total = kWeights ? rows : (int64_t)rows * pieces;
-    const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-    for (int64_t u = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32; u < total; u += warps) {
-        const int64_t row = kWeights ? u : div_count(u, pieces);
-        const int first = kWeights ? 0 : (int)(u - row * pieces) * kPiece, last = kWeights ? a.I : min(a.I, first + kPiece);
-        const float w = a.row_weights == nullptr ? 1.0f : __ldg(a.row_weights + row);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const int sub = warp / a.row_warps, threads = a.row_warps * 32, tid = threadIdx.x - sub * threads;
+    const int per = kThreads / threads, rows = rows_in_use(a);
+    int turn = 0;
+    for (int64_t first = (int64_t)blockIdx.x * per; first < rows; first += (int64_t)gridDim.x * per, turn ^= 1) {
+        const int64_t row = first + sub;
+        const bool live = row < rows;
+        const float w = live && a.row_weights != nullptr ? __ldg(a.row_weights + row) : 1.0f;
+        const __nv_bfloat16 *from = a.gate_up + (size_t)row * 2 * a.I, *grad = a.grad + (size_t)row * a.I;
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (size_t)row * 2 * a.I;
         float sum = 0.0f;
-        for (int col = first + lane * 8; col < last; col += kPiece) {
-            const __nv_bfloat16 *p = a.gate_up + (size_t)row * 2 * a.I + col;
-            float z[8], v[8], d[8];
-            const uint4 g4 = load_once(p), u4 = load_once(p + a.I), d4 = load_once(a.grad + (size_t)row * a.I + col);
-            widen(g4, z);
-            widen(u4, v);
-            widen(d4, d);
+        if (live)
+            for (int col0 = tid * 8; col0 < a.I; col0 += kUnroll * threads * 8) {
+                uint4 g4[kUnroll], u4[kUnroll], d4[kUnroll];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float s = sigmoid(z[i]), silu = z[i] * s, up = v[i], dh = d[i] * w;
-                if constexpr (kWeights) sum = fmaf(d[i], silu * up, sum);
-                v[i] = dh * silu;
-                z[i] = dh * up * s * fmaf(z[i], 1.0f - s, 1.0f);
+                for (int j = 0; j < kUnroll; ++j) {
+                    const int col = col0 + j * threads * 8;
+                    if (col < a.I) {
+                        g4[j] = load_once(from + col);
+                        u4[j] = load_once(from + a.I + col);
+                        d4[j] = load_once(grad + col);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < kUnroll; ++j) {
+                    const int col = col0 + j * threads * 8;
+                    if (col < a.I) {
+                        Gradients r;
+                        sum += gradients(g4[j], u4[j], d4[j], w, r);
+                        *reinterpret_cast<uint4 *>(out + col) = r.gate;
+                        *reinterpret_cast<uint4 *>(out + a.I + col) = r.up;
+                    }
+                }
             }
-            __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.out) + (size_t)row * 2 * a.I + col;
-            *reinterpret_cast<uint4 *>(out) = narrow(z);
-            *reinterpret_cast<uint4 *>(out + a.I) = narrow(v);
-        }
-        if constexpr (kWeights) {
+        if (a.grad_weights == nullptr) continue;
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == 0) a.grad_weights[row] = sum;
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (a.row_warps > 1) {
+            if (lane == 0) space[turn][warp] = sum;
+            __syncthreads();   // one is enough: the next row's sums go to the other half
+            sum = 0.0f;
+            for (int i = 0; i < a.row_warps; ++i) sum += space[turn][sub * a.row_warps + i];
         }
+        if (live && tid == 0) a.grad_weights[row] = sum;
     }
 }
 
@@ -139,9 +176,9 @@ int blocks_for(int64_t warps, int per_sm) {
 int launch_swiglu(const SwigluLaunch &L) {
     if (L.num_rows_most == 0) return MOE_OK;
     const SwigluArgs a{static_cast<const __nv_bfloat16 *>(L.gate_up), nullptr, L.row_weights, L.num_rows, L.out, L.out_scales,
-                       nullptr, L.status, L.num_rows_most, L.intermediate, trace_args()};
+                       nullptr, L.status, L.num_rows_most, L.intermediate, 0, trace_args()};
     const int64_t pieces = (int64_t)a.M * ((a.I + kPiece - 1) / kPiece);
-    const dim3 grid(blocks_for(pieces, 8));
+    const dim3 grid(blocks_for(pieces, 16));
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
     const cudaError_t e = L.out_scales ? launch_kernel(swiglu_kernel<true>, grid, dim3(kThreads), 0, s, tuning().overlap != 0, a)
                                        : launch_kernel(swiglu_kernel<false>, grid, dim3(kThreads), 0, s, tuning().overlap != 0, a);
@@ -150,17 +187,13 @@ int launch_swiglu(const SwigluLaunch &L) {
 
 int launch_swiglu_backward(const SwigluLaunch &L) {
     if (L.num_rows_most == 0) return MOE_OK;
-    const SwigluArgs a{static_cast<const __nv_bfloat16 *>(L.gate_up), static_cast<const __nv_bfloat16 *>(L.grad), L.row_weights,
-                       L.num_rows, L.out, nullptr, L.grad_row_weights, L.status, L.num_rows_most, L.intermediate,
-                       trace_args()};
-    const int64_t pieces = L.grad_row_weights ? a.M : (int64_t)a.M * ((a.I + kPiece - 1) / kPiece);
-    const dim3 grid(blocks_for(pieces, 8));
+    SwigluArgs a{static_cast<const __nv_bfloat16 *>(L.gate_up), static_cast<const __nv_bfloat16 *>(L.grad), L.row_weights,
+                 L.num_rows, L.out, nullptr, L.grad_row_weights, L.status, L.num_rows_most, L.intermediate, 1, trace_args()};
+    while (a.row_warps < kThreads / 32 && a.I > a.row_warps * 256 * kUnroll) a.row_warps *= 2;
+    const dim3 grid(blocks_for((int64_t)a.M * a.row_warps, 4));
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
-    const cudaError_t e =
-        L.grad_row_weights
-            ? launch_kernel(swiglu_backward_kernel<true>, grid, dim3(kThreads), 0, s, tuning().overlap != 0, a)
-            : launch_kernel(swiglu_backward_kernel<false>, grid, dim3(kThreads), 0, s, tuning().overlap != 0, a);
-    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return launch_kernel(swiglu_backward_kernel, grid, dim3(kThreads), 0, s, tuning().overlap != 0, a) == cudaSuccess
+               ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // namespace moe

@@ -74,7 +74,7 @@ typedef enum {
 #define MOE_MAX_ADAPTERS 8192
 #define MOE_MAX_ADAPTER_RANK 128
 #define MOE_MAX_ROWS (1 << 30)        /* rows of the grouped products, the activation and the norm */
-#define MOE_MAX_NORM_HIDDEN 65536
+#define MOE_MAX_NORM_HIDDEN 16384
 
 /* Outputs of moe_get_layout: all DEVICE pointers, caller-owned. */
 typedef struct {
@@ -828,7 +828,7 @@ MOE_API int moe_swiglu_backward(const void *gate_up, const void *grad, int num_r
  *   out, residual_out  [T, H] bf16 or NULL; residual_out may be residual or x itself, and wants a residual.
  *   codes, scales      [T, H] uint8 and [T, H/128] fp32, or both NULL.
  * Rows are 16-byte aligned (codes: 8, an fp32 weight: 16). Limits: T <= 2^30, H a multiple of 8 (128 with
- * codes) up to 65536. No data raises an error here; `status` is part of every call.
+ * codes) up to 16384. No data raises an error here; `status` is part of every call.
  */
 enum { MOE_NORM_WEIGHT_BF16 = 0, MOE_NORM_WEIGHT_F32 = 1 };
 MOE_API int moe_add_rms_norm(const void *x, const void *residual, int num_tokens, int hidden, const void *weight,
