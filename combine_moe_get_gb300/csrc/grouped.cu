@@ -44,9 +44,8 @@ struct Tile {
     int row0;       // first row
     int n;          // rows (weights' gradients: columns) of the tile
     int c0;         // weights' gradients: first column
-    int blocks;     // blocks along the reduction
-    int last;       // weights' gradients: rows in the last block
-    int pad;
+    int kb0, blocks;   // first block along the reduction, and how many
+    int last;          // weights' gradients: rows in the last block
 };
 
 struct Args {
@@ -58,6 +57,9 @@ struct Args {
     int E, M;
     int features, depth;     // rows of D over all tiles, length of the reduction (weights' gradients: columns of D)
     int feature_tiles, column_tiles;
+    int blocks;              // along the whole reduction (rows of scales are this long)
+    int split, per_split;    // CTAs of a cluster that share a tile's reduction, and the blocks of each
+    bool read_once;          // hardly any expert has rows for two tiles: its weights pass once
     bool accumulate;
     WaitLimits limits;
     TraceArgs trace;
@@ -102,6 +104,11 @@ __device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {   
     uint32_t r;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
     return r;
+}
+// ... of the CTA whose products these are: a pair's first, or this one (whatever cluster it is in).
+template <int kCtas>
+__device__ __forceinline__ uint32_t home_addr(const void *p) {
+    return kCtas == 2 ? peer_addr(p, 0) : smem_addr(p);
 }
 // Arrivals and waits have the CTA's scope: what they order, tensor memory and shared memory that TMA and the products
 // touch, is ordered by those units' own barriers and fences. (With the cluster's scope each wait took L1 with it: 2.5
@@ -277,8 +284,9 @@ __device__ bool find_tiles(const Args &a, Control &c) {
         ring.next();
         return ok;
     };
-    int64_t t = blockIdx.x / kCtas;
-    const int64_t step = gridDim.x / kCtas;
+    const int share = kCtas * a.split;   // CTAs of a tile
+    int64_t t = blockIdx.x / share;
+    const int64_t step = gridDim.x / share;
     if constexpr (kOp == kGradW) {
         const int per = a.feature_tiles * a.column_tiles;
         const int64_t total = (int64_t)a.E * per;
@@ -292,12 +300,13 @@ __device__ bool find_tiles(const Args &a, Control &c) {
             }
             const int rows = r.hi - r.lo, f = i / a.column_tiles, col = i - f * a.column_tiles;
             const int blocks = (rows + kDepth - 1) / kDepth;
-            if (!hand(Tile{e, f * kCtas * kRows, r.lo, min(kCols, a.depth - col * kCols), col * kCols, blocks,
-                           rows - (blocks - 1) * kDepth, 0}))
+            if (!hand(Tile{e, f * kCtas * kRows, r.lo, min(kCols, a.depth - col * kCols), col * kCols, 0, blocks,
+                           rows - (blocks - 1) * kDepth}))
                 return false;
         }
     } else {
-        const int F = a.feature_tiles, blocks = (a.depth + C::kBlock - 1) / C::kBlock;
+        const int F = a.feature_tiles, kb0 = blockIdx.x / kCtas % a.split * a.per_split;
+        const int blocks = min(a.per_split, a.blocks - kb0);
         int64_t before = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             Range r{};
@@ -322,9 +331,10 @@ __device__ bool find_tiles(const Args &a, Control &c) {
                 const int64_t pass = (int64_t)kRowGroup * F;
                 const int g = (int)(i / pass), in = (int)(i - g * pass), width = min(kRowGroup, eR - g * kRowGroup);
                 const int f = in / width, rt = g * kRowGroup + in - f * width;
-                if (!hand(Tile{e0 + l, f * kCtas * kRows, lo + rt * per, min(per, er - rt * per), 0, blocks, 0, 0}))
+                if (!hand(Tile{e0 + l, f * kCtas * kRows, lo + rt * per, min(per, er - rt * per), 0, kb0, blocks, 0}))
                     return false;
                 t += step;
+                if (a.split > 1) return hand(Tile{-1, 0, 0, 0, 0, 0, 0, 0});   // a tile to a cluster
             }
             before += all;
         }
@@ -363,8 +373,8 @@ __device__ bool load(const Args &a, Control &c, uint32_t ring_base, uint32_t ran
     Ring r(C::kStages);
     int issued = 0;
     const bool mine = elect_one();
-    // weights of one pass are read once or by a few CTAs at about the same time; rows by every feature's tile
-    const uint64_t once = policy_evict_first(), often = policy_evict_last();
+    // rows are read for every tile of features (weights kept out of L2 where other tiles read them too cost 4%)
+    const uint64_t weights = a.read_once ? policy_evict_first() : policy_evict_normal(), often = policy_evict_last();
     bool ok = (int)blockIdx.x != a.limits.withheld_cta;
     ok = ok && each_tile(a, c, [&](const Tile &t) {
         const int a0 = t.a0 + (int)rank * kRows;
@@ -377,12 +387,12 @@ __device__ bool load(const Args &a, Control &c, uint32_t ring_base, uint32_t ran
             const bool mask = kOp == kGradW && kb == t.blocks - 1 && t.last < kDepth;
             if (mine) {
                 // what the products wait for lies in the pair's first CTA; a block to be masked is this CTA's affair first
-                const uint32_t bar = mask ? peer_addr(&c.masked_full[r.slot], rank) : peer_addr(&c.full[r.slot], 0);
+                const uint32_t bar = mask ? smem_addr(&c.masked_full[r.slot]) : home_addr<kCtas>(&c.full[r.slot]);
                 arrive_expect_at(bar, bytes);
                 if constexpr (kOp == kForward || kOp == kForwardE4m3) {
-                    load3<kCtas>(to_a, &a.a, kb * C::kBlock, a0, t.e, bar, once);
+                    load3<kCtas>(to_a, &a.a, (t.kb0 + kb) * C::kBlock, a0, t.e, bar, weights);
                 } else if constexpr (kOp == kGradX) {
-                    for (int i = 0; i < 2; ++i) load3<kCtas>(to_a + i * 8192, &a.a, a0 + i * 64, kb * kDepth, t.e, bar, once);
+                    for (int i = 0; i < 2; ++i) load3<kCtas>(to_a + i * 8192, &a.a, a0 + i * 64, (t.kb0 + kb) * kDepth, t.e, bar, weights);
                 } else {
                     for (int i = 0; i < 2; ++i) load2<kCtas>(to_a + i * 8192, &a.a, a0 + i * 64, t.row0 + kb * kDepth, bar, often);
                 }
@@ -390,7 +400,7 @@ __device__ bool load(const Args &a, Control &c, uint32_t ring_base, uint32_t ran
                     if constexpr (kOp == kGradW)
                         load2<kCtas>(to_b + i * 8192, &a.b, t.c0 + (int)rank * part + i * 64, t.row0 + kb * kDepth, bar, often);
                     else
-                        load2<kCtas>(to_b + i * kBoxRows * 128, &a.b, kb * C::kBlock, t.row0 + (int)rank * part + i * kBoxRows,
+                        load2<kCtas>(to_b + i * kBoxRows * 128, &a.b, (t.kb0 + kb) * C::kBlock, t.row0 + (int)rank * part + i * kBoxRows,
                                      bar, often);
                 }
             }
@@ -468,7 +478,7 @@ __device__ bool mask_blocks(const Args &a, Control &c, char *ring) {
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) arrive_released(peer_addr(&c.full[r.slot], 0));
+            if (lane == 0) arrive_released(home_addr<kCtas>(&c.full[r.slot]));
         }
         r.next();
         return true;
@@ -495,19 +505,20 @@ __device__ bool load_scales(const Args &a, Control &c, float *scales, uint32_t r
     using C = Config<kForwardE4m3, kCtas, kCols>;
     const int lane = threadIdx.x & 31;
     Ring r(kScaleSlots);
+    const int all = a.blocks;
     return each_tile(a, c, [&](const Tile &t) {
         constexpr int kPerRow = kCols / 32, kPer = kPerRow + kRows / 32;
         static_assert(kCols % 32 == 0);
-        const bool whole = whole_fours(a.b_scales, t.blocks) && whole_fours(a.a_scales, t.blocks);
+        const bool whole = whole_fours(a.b_scales, all) && whole_fours(a.a_scales, all);   // kb0 is a multiple of four
         const int f0 = t.a0 + (int)rank * kRows;
         float4 next[kPer];
         const auto fetch = [&](int kb) {
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
                 const float *from = i < kPerRow
-                                        ? a.b_scales + (size_t)(t.row0 + min(lane + 32 * i, t.n - 1)) * t.blocks
-                                        : a.a_scales + ((size_t)t.e * a.features + min(f0 + lane + 32 * (i - kPerRow), a.features - 1)) * t.blocks;
-                if (i >= kPerRow || 32 * i < t.n) next[i] = four_scales(from, kb, t.blocks, whole);
+                                        ? a.b_scales + (size_t)(t.row0 + min(lane + 32 * i, t.n - 1)) * all
+                                        : a.a_scales + ((size_t)t.e * a.features + min(f0 + lane + 32 * (i - kPerRow), a.features - 1)) * all;
+                if (i >= kPerRow || 32 * i < t.n) next[i] = four_scales(from, t.kb0 + kb, all, whole);
             }
         };
         fetch(0);
@@ -652,9 +663,42 @@ __device__ __forceinline__ void add_weights(const Args &a, const Tile &t, int f,
     }
 }
 
+// A tile whose reduction a cluster shares: each of its CTAs adds up the sums of as many columns. They come through
+// distributed shared memory into the ring, which no copy or product uses any more once every CTA's roles have ended, and
+// are added in the order of the reduction. `put` hands this thread's sums to f(column, feature, value); all warps of all
+// CTAs of the cluster come here or through two cluster_sync() of their own.
+template <class Put>
+__device__ void share_tile(const Args &a, const Tile &t, char *ring, int readers, int tid, Put put) {
+    const int split = a.split, rank = blockIdx.x % split, width = (t.n + split - 1) / split;
+    cluster_sync();
+    const uint32_t here = smem_addr(ring);
+    put([&](int col, int feature, float v) {
+        const int owner = col / width;
+        uint32_t to;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(here), "r"(owner));
+        to += ((rank * width + col - owner * width) * kRows + feature) * 4;
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
+    });
+    __syncwarp();
+    cluster_sync();
+    const float *parts = reinterpret_cast<const float *>(ring);
+    const int mine = min(width, t.n - rank * width), f = tid % 64 * 2;
+    if (t.a0 + f >= a.features) return;
+    for (int i = tid / 64; i < mine; i += readers * 32 / 64) {
+        float2 sum = make_float2(0.0f, 0.0f);
+        for (int p = 0; p < split; ++p) {
+            const float2 v = *reinterpret_cast<const float2 *>(parts + (p * width + i) * kRows + f);
+            sum.x += v.x, sum.y += v.y;
+        }
+        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                            (size_t)(t.row0 + rank * width + i) * a.features + t.a0 + f) =
+            __floats2bfloat162_rn(sum.x, sum.y);
+    }
+}
+
 // Warps 4 to 11: a quarter of tensor memory's lanes each, every other 16 columns.
 template <Op kOp, int kCtas, int kCols, typename Out>
-__device__ bool read_sums(const Args &a, Control &c, char *beside, uint32_t tmem, uint32_t rank) {
+__device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, uint32_t tmem, uint32_t rank, bool &shared) {
     using C = Config<kOp, kCtas, kCols>;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, q = warp % 4, side = (warp - kFirstReader) / 4;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
@@ -667,7 +711,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *beside, uint32_t tmem
         const int f = t.a0 + (int)rank * kRows + q * 32 + lane;
         if constexpr (C::kE4m3) {
             float sum[kChunks][16] = {};
-            const uint32_t empty = peer_addr(&c.sums_empty[0], 0);
+            const uint32_t empty = home_addr<kCtas>(&c.sums_empty[0]);
             const auto blocks = [&](auto chunks) {   // straight code for each number of chunks: branches cost as much as sums
                 constexpr int kN = decltype(chunks)::value;
                 for (int kb = 0; kb < t.blocks; ++kb, sums.next()) {
@@ -699,6 +743,19 @@ __device__ bool read_sums(const Args &a, Control &c, char *beside, uint32_t tmem
                 default: done = blocks(std::integral_constant<int, kChunks>()); break;
             }
             if (!done) return false;
+            if (kCtas == 1 && a.split > 1) {
+                shared = true;
+                share_tile(a, t, ring, C::kReaders, threadIdx.x - kFirstReader * 32, [&](auto f) {
+#pragma unroll
+                    for (int i = 0; i < kChunks; ++i)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {   // 8 h + 4 g + 2 p + i
+                            const int col = i * kStep + side * 16 + j / 4 % 2 * 8 + (lane & 3) * 2 + j % 2;
+                            if (col < t.n) f(col, q * 32 + j / 8 * 16 + j / 2 % 2 * 8 + lane / 4, sum[i][j]);
+                        }
+                });
+                return true;
+            }
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
                 const int col = i * kStep + side * 16;
@@ -724,6 +781,18 @@ __device__ bool read_sums(const Args &a, Control &c, char *beside, uint32_t tmem
                         if (a.accumulate) add_weights(a, t, f, col, v);
                     store_weights<Out>(a, t, f0, col, v, buffers + (stored++ & 1) * kStoreBytes);
                 }
+            } else if (kCtas == 1 && a.split > 1) {
+                shared = true;
+                share_tile(a, t, ring, C::kReaders, threadIdx.x - kFirstReader * 32, [&](auto put) {
+                    for (int col = side * 16; col < t.n; col += kStep) {
+                        float v[16];
+                        tmem_load16(lanes + sums.slot * kCols + col, v);
+                        tmem_load_wait(v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (col + j < t.n) put(col + j, q * 32 + lane, v[j]);
+                    }
+                });
             } else {
                 for (int col = side * 16; col < t.n; col += kStep) {
                     float v[16];
@@ -735,7 +804,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *beside, uint32_t tmem
             if (some) {
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) arrive_at(peer_addr(&c.sums_empty[sums.slot], 0));
+                if (lane == 0) arrive_at(home_addr<kCtas>(&c.sums_empty[sums.slot]));
                 sums.next();
             }
         }
@@ -789,7 +858,7 @@ __global__ __launch_bounds__((Config<kOp, kCtas, kCols>::kThreads), 1) void grou
     grid_dependency_wait();
     grid_launch_dependents();
 
-    bool ok = true;
+    bool ok = true, shared = false;
     if (warp == 0) {
         ok = load<kOp, kCtas, kCols>(a, c, ring_base, rank);
     } else if (warp == 1) {
@@ -800,10 +869,14 @@ __global__ __launch_bounds__((Config<kOp, kCtas, kCols>::kThreads), 1) void grou
         if constexpr (kOp == kGradW) ok = mask_blocks<kCtas, kCols>(a, c, ring);
         if constexpr (C::kE4m3) ok = load_scales<kCtas, kCols>(a, c, reinterpret_cast<float *>(beside), rank);
     } else {
-        ok = read_sums<kOp, kCtas, kCols, Out>(a, c, beside, tmem, rank);
+        ok = read_sums<kOp, kCtas, kCols, Out>(a, c, ring, beside, tmem, rank, shared);
     }
     if (!ok && (threadIdx.x & 31) == 0) report(a.status, MOE_ERR_TIMEOUT);
     __syncwarp();
+    if (kCtas == 1 && a.split > 1 && !shared) {   // beside share_tile
+        cluster_sync();
+        cluster_sync();
+    }
     tc_fence_before();
     __syncthreads();
     if constexpr (kCtas == 2) cluster_sync();   // no arrival or product of the other CTA is under way
@@ -844,7 +917,8 @@ int launch(Args &a, int64_t most_tiles, cudaStream_t s) {
     auto kernel = grouped_kernel<kOp, kCtas, kCols, Out>;
     const int rc = ensure_dynamic_smem((const void *)kernel, C::smem());
     if (rc != MOE_OK) return rc;
-    const int64_t ctas = std::min<int64_t>(resident<kOp, kCtas, kCols, Out>(), most_tiles * kCtas);
+    const int64_t ctas = a.split > 1 ? most_tiles * a.split   // a cluster each, that wait for no other
+                                     : std::min<int64_t>(resident<kOp, kCtas, kCols, Out>(), most_tiles * kCtas);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(C::kThreads);
@@ -852,9 +926,9 @@ int launch(Args &a, int64_t most_tiles, cudaStream_t s) {
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     int n = 0;
-    if (kCtas > 1) {
+    if (kCtas * a.split > 1) {
         attr[n].id = cudaLaunchAttributeClusterDimension;
-        attr[n++].val.clusterDim = {kCtas, 1, 1};
+        attr[n++].val.clusterDim = {(unsigned)(kCtas * a.split), 1, 1};
     }
     if (tuning().overlap) {
         attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -876,9 +950,51 @@ constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
 int64_t most_row_tiles(int M, int E, int cols) { return (int64_t)M / cols + std::min(M, E); }
 
 template <Op kOp, int kCtas, int kCols>
-int launch_rows(Args &a, cudaStream_t s) {
+int launch_rows(Args &a, int split, cudaStream_t s) {
     a.feature_tiles = ceil_div(a.features, kCtas * kRows);
+    a.split = split;
+    a.per_split = Config<kOp, kCtas, kCols>::kE4m3 ? ceil_div(a.blocks, 4 * split) * 4 : ceil_div(a.blocks, split);
+    a.read_once = a.M <= (int64_t)a.E * kCols;
     return launch<kOp, kCtas, kCols>(a, most_row_tiles(a.M, a.E, kCols) * a.feature_tiles, s);
+}
+
+// Pairs of CTAs with 256 features to a tile, or single CTAs with 128 features and at most 128 rows, up to eight of them
+// (a cluster) to a tile's reduction: whichever an estimate finds faster, from rows that are spread evenly. A block takes
+// the tensor core 2 n cycles and its loads a cycle for 64 bytes; a tile's ends cost some 2000 cycles and a shared
+// tile's exchange 4000 more (@SPLIT@).
+struct Way {
+    bool pair;
+    int split;
+};
+Way way_for(const Args &a, int block_cells, int pair_cols) {
+    const int groups = std::min(a.M, a.E), sms = device_sm_count();
+    const double rows = (double)a.M / groups;
+    Way best{true, 1};
+    double least = 0;
+    for (int pair = 1; pair >= 0; --pair) {
+        const int cols = pair ? pair_cols : 128, per = (int)((rows + cols - 1) / cols);
+        const double n = rows / per, features = pair ? 256 : 128;
+        const int64_t tiles = (int64_t)groups * per * ceil_div(a.features, (int)features);
+        const int64_t most = most_row_tiles(a.M, a.E, cols) * ceil_div(a.features, (int)features);
+        const double block = std::max(2.0 * n, (128 * 128 + (pair ? n / 2 : n) * 128) / 64.0);
+        for (int split = 1; split <= (pair ? 1 : 8); split *= 2) {
+            const int step = block_cells == 128 ? 4 : 1, of = ceil_div(a.blocks, split * step) * step;
+            // the grid has a cluster for every tile there may be; four fifths of the SMs take clusters of eight at once
+            if (split > 1 && (most * split > (split == 8 ? sms * 4 / 5 : sms) || (split - 1) * of >= a.blocks)) break;
+            const int64_t at_once = pair ? sms / 2 : sms / split;
+            const double cycles = (double)((tiles + at_once - 1) / at_once) * (of * block + 2000) + (split > 1 ? 4000 : 0);
+            if (least == 0 || cycles < least) least = cycles, best = Way{pair != 0, split};
+        }
+    }
+    return best;
+}
+
+template <Op kOp, int kPairCols>
+int launch_best(Args &a, cudaStream_t s) {
+    constexpr int cells = kOp == kForwardE4m3 ? 128 : kDepth;
+    a.blocks = ceil_div(a.depth, cells);
+    const Way w = way_for(a, cells, kPairCols);
+    return w.pair ? launch_rows<kOp, 2, kPairCols>(a, 1, s) : launch_rows<kOp, 1, 128>(a, w.split, s);
 }
 }  // namespace
 
@@ -897,8 +1013,7 @@ int launch_grouped_linear(const GroupedLaunch &L) {
     a.limits = wait_limits();
     a.trace = trace_args();
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
-    if (e4m3) return launch_rows<kForwardE4m3, 2, 192>(a, s);
-    return launch_rows<kForward, 2, 256>(a, s);
+    return e4m3 ? launch_best<kForwardE4m3, 192>(a, s) : launch_best<kForward, 256>(a, s);
 }
 
 int launch_grouped_grad_x(const GroupedLaunch &L) {
@@ -913,7 +1028,7 @@ int launch_grouped_grad_x(const GroupedLaunch &L) {
     a.features = L.in_features, a.depth = L.out_features;
     a.limits = wait_limits();
     a.trace = trace_args();
-    return launch_rows<kGradX, 2, 256>(a, static_cast<cudaStream_t>(L.stream));
+    return launch_best<kGradX, 256>(a, static_cast<cudaStream_t>(L.stream));
 }
 
 int launch_grouped_grad_w(const GroupedGradWLaunch &L) {
@@ -938,6 +1053,7 @@ int launch_grouped_grad_w(const GroupedGradWLaunch &L) {
     a.limits = wait_limits();
     a.trace = trace_args();
     constexpr int kCols = 256;
+    a.split = 1;
     a.feature_tiles = ceil_div(a.features, 2 * kRows);
     a.column_tiles = ceil_div(a.depth, kCols);
     const int64_t tiles = (int64_t)a.E * a.feature_tiles * a.column_tiles;
