@@ -72,7 +72,7 @@ struct Config {
     static constexpr bool kE4m3 = kOp == kForwardE4m3;
     static constexpr int kReaders = kE4m3 ? 12 : 8, kThreads = (kFirstReader + kReaders) * 32;
     static constexpr int kSides = kReaders / 4;   // a quarter of the lanes is read by as many warps, 16 columns in turn
-    static constexpr int kTileB = kCols / kCtas * 128;
+    static constexpr int kTileB = (kCols / kCtas + kBoxRows - 1) / kBoxRows * kBoxRows * 128;
     static constexpr int kSums = kE4m3 ? (512 / kCols < 4 ? 512 / kCols : 4) : 2;
     static constexpr int kScales = kCols + kRows;   // E4M3: scales of a block's rows and features
     static constexpr int kBeside = kE4m3 ? kScaleSlots * 4 * kScales * 4 : kOp == kGradW ? kReaders * 2 * kStoreBytes : 0;
@@ -125,8 +125,13 @@ __device__ __forceinline__ void arrive_expect_at(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, uint64_t ns) {
     return mbar_wait_bounded(bar, parity, ns);
 }
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64_t ns) {
+// By a whole warp, which goes on or gives up as one. What is waited for has often happened: the rest stays out of the
+// way of the code around (E4M3's readers were 4% slower with it in each place).
+__device__ __noinline__ bool warp_wait_longer(uint64_t *bar, uint32_t parity, uint64_t ns) {
     return __all_sync(0xffffffffu, wait(bar, parity, ns));
+}
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, uint64_t ns) {
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || warp_wait_longer(bar, parity, ns);
 }
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -714,22 +719,25 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
             const uint32_t empty = home_addr<kCtas>(&c.sums_empty[0]);
             const auto blocks = [&](auto chunks) {   // straight code for each number of chunks: branches cost as much as sums
                 constexpr int kN = decltype(chunks)::value;
-                for (int kb = 0; kb < t.blocks; ++kb, sums.next()) {
-                    if (kb % 4 == 0 && !warp_wait(&c.scales_full[fours.slot], fours.round, a.limits.wait_ns)) return false;
-                    const float *sx = scales + (fours.slot * 4 + kb % 4) * C::kScales;
-                    float features[4];
+                for (int kb = 0; kb < t.blocks; kb += 4, fours.next()) {
+                    if (!warp_wait(&c.scales_full[fours.slot], fours.round, a.limits.wait_ns)) return false;
+                    const float *four = scales + fours.slot * 4 * C::kScales;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) features[j] = sx[kCols + q * 32 + j * 8 + lane / 4];
-                    if (!warp_wait(&c.sums_full[sums.slot], sums.round, a.limits.wait_ns)) return false;
-                    tc_fence_after();
-                    add_block<kN, kStep>(sum, lanes + sums.slot * kCols + side * 16, sx + side * 16 + (lane & 3) * 2, features);
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_at(empty + sums.slot * 8);
-                    if (kb % 4 == 3 || kb + 1 == t.blocks) {
-                        if (lane == 0) mbar_arrive(&c.scales_empty[fours.slot]);
-                        fours.next();
+                    for (int i = 0; i < 4; ++i) {
+                        if (kb + i >= t.blocks) break;
+                        const float *sx = four + i * C::kScales;
+                        float features[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) features[j] = sx[kCols + q * 32 + j * 8 + lane / 4];
+                        if (!warp_wait(&c.sums_full[sums.slot], sums.round, a.limits.wait_ns)) return false;
+                        tc_fence_after();
+                        add_block<kN, kStep>(sum, lanes + sums.slot * kCols + side * 16, sx + side * 16 + (lane & 3) * 2, features);
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_at(empty + sums.slot * 8);
+                        sums.next();
                     }
+                    if (lane == 0) mbar_arrive(&c.scales_empty[fours.slot]);   // behind the last block's __syncwarp
                 }
                 return true;
             };
@@ -1013,7 +1021,7 @@ int launch_grouped_linear(const GroupedLaunch &L) {
     a.limits = wait_limits();
     a.trace = trace_args();
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
-    return e4m3 ? launch_best<kForwardE4m3, 192>(a, s) : launch_best<kForward, 256>(a, s);
+    return e4m3 ? launch_best<kForwardE4m3, 160>(a, s) : launch_best<kForward, 256>(a, s);
 }
 
 int launch_grouped_grad_x(const GroupedLaunch &L) {
