@@ -1,0 +1,236 @@
+"""The grouped products where their kernels differ (pairs of CTAs, single ones, clusters that share a tile's reduction),
+over long offsets, in CUDA graphs, on two streams at once, and where their waits run out."""
+from __future__ import annotations
+
+import time
+
+import pytest
+import torch
+
+from test_grouped_gpu import BF, DEV, close, codes, normal, prefix_of, values
+
+pytestmark = pytest.mark.gpu
+LIMIT_NS = 20_000_000
+
+
+@pytest.fixture(scope="module")
+def moe():
+    from combine_moe_get_gb300 import binding
+    return binding
+
+
+# counts, K, N: many tiles for pairs; few, with a long reduction, for clusters of 8, 4 and 2; single CTAs; reductions that
+# do not divide by the cluster; rows for several tiles, and one
+WAYS = {
+    "pairs": ([130, 0, 257, 64, 300, 31, 511, 7], 264, 4104),
+    "cluster of 8": ([100], 7168, 512),
+    "cluster of 4": ([32, 0, 32, 31, 33], 7168, 264),
+    "cluster of 2": ([2048], 4104, 512),
+    "one row": ([0, 1, 0], 7168, 1048),
+    "uneven parts": ([3, 90], 2120, 392),
+    "single": ([10, 3, 0, 25, 1], 1000, 2056),
+    "several tiles": ([300, 129], 1288, 256),
+}
+
+
+def operands(name, e4m3=False):
+    counts, K, N = WAYS[name]
+    K = -(-K // 128) * 128 if e4m3 else K
+    gen = torch.Generator(DEV).manual_seed(len(name))
+    p = prefix_of(counts, 2)
+    M, E = p[-1] + 3, len(counts)
+    prefix = torch.tensor(p, dtype=torch.int32, device=DEV)
+    if e4m3:
+        return p, prefix, codes(gen, M, K), codes(gen, E, N, K)
+    return p, prefix, normal(gen, M, K), normal(gen, E, N, K, std=K ** -0.5), normal(gen, M, N)
+
+
+@pytest.mark.parametrize("name", WAYS)
+def test_bf16(moe, name):
+    p, prefix, x, w, g = operands(name)
+    K, N, status = x.shape[1], w.shape[1], moe.new_status()
+    out, gx = torch.full_like(g, 7.0), torch.full_like(x, 7.0)
+    moe.moe_grouped_linear(x, w, prefix, out=out, status=status)
+    moe.moe_grouped_linear_grad_x(g, w, prefix, out=gx, status=status)
+    assert torch.equal(moe.moe_grouped_linear(x, w, prefix, out=torch.full_like(g, 7.0)), out)
+    moe.check_status(status)
+    for t in (out, gx):
+        assert (t[: p[0]] == 7).all() and (t[p[-1]:] == 7).all()
+    for e in range(len(p) - 1):
+        r = slice(p[e], p[e + 1])
+        xe, ge, we = x[r].double(), g[r].double(), w[e].double()
+        close(out[r], xe @ we.T, xe.abs() @ we.abs().T, K, 2.0 ** -8)
+        close(gx[r], ge @ we, ge.abs() @ we.abs(), N, 2.0 ** -8)
+
+
+@pytest.mark.parametrize("name", WAYS)
+def test_gradient_of_rows_over_the_long_side(moe, name):
+    """The reduction of grad_x is over N: the same sizes with K and N in each other's place."""
+    counts, N, K = WAYS[name]
+    gen = torch.Generator(DEV).manual_seed(len(name))
+    p = prefix_of(counts)
+    prefix = torch.tensor(p, dtype=torch.int32, device=DEV)
+    g, w = normal(gen, p[-1], N), normal(gen, len(counts), N, K, std=N ** -0.5)
+    gx = moe.moe_grouped_linear_grad_x(g, w, prefix)
+    for e in range(len(counts)):
+        r = slice(p[e], p[e + 1])
+        ge, we = g[r].double(), w[e].double()
+        close(gx[r], ge @ we, ge.abs() @ we.abs(), N, 2.0 ** -8)
+
+
+@pytest.mark.parametrize("name", WAYS)
+def test_e4m3(moe, name):
+    p, prefix, (x, xs), (w, ws) = operands(name, True)
+    status = moe.new_status()
+    out = torch.full((x.shape[0], w.shape[1]), 7.0, dtype=BF, device=DEV)
+    moe.moe_grouped_linear(x, w, prefix, x_scales=xs, w_scales=ws, out=out, status=status)
+    moe.check_status(status)
+    assert (out[: p[0]] == 7).all() and (out[p[-1]:] == 7).all()
+    for e in range(len(p) - 1):
+        r = slice(p[e], p[e + 1])
+        xe, we = values(x[r], xs[r]), values(w[e], ws[e])
+        close(out[r], xe @ we.T, xe.abs() @ we.abs().T, x.shape[1], 2.0 ** -8)
+
+
+def test_e4m3_scales_far_apart(moe):
+    """Blocks whose scales differ by 2^40, and scales at no 16-byte boundary."""
+    gen = torch.Generator(DEV).manual_seed(9)
+    p = [0, 40, 200]
+    prefix = torch.tensor(p, dtype=torch.int32, device=DEV)
+    (x, xs), (w, ws) = codes(gen, 200, 1024), codes(gen, 2, 72, 1024)
+    xs, ws = xs * 2.0 ** torch.randint(-20, 20, xs.shape, device=DEV, generator=gen), ws * 2.0 ** -30
+    odd = [torch.empty(t.numel() + 1, device=DEV)[1:].view(t.shape).copy_(t) for t in (xs, ws)]
+    for a, b in ((xs, ws), odd):
+        out = moe.moe_grouped_linear(x, w, prefix, x_scales=a, w_scales=b)
+        for e in range(2):
+            r = slice(p[e], p[e + 1])
+            xe, we = values(x[r], xs[r]), values(w[e], ws[e])
+            close(out[r], xe @ we.T, xe.abs() @ we.abs().T, 1024, 2.0 ** -8)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_weights_offsets_beyond_32_bits(moe, dtype):
+    """Weights of 2^32 elements and more, rows at both ends."""
+    E, N, K = 66, 8192, 8192
+    gen = torch.Generator(DEV).manual_seed(10)
+    p = [0, 5] + [5] * (E - 2) + [12]
+    prefix = torch.tensor(p, dtype=torch.int32, device=DEV)
+    x, g = normal(gen, 12, K), normal(gen, 12, N)
+    w = torch.empty(E, N, K, dtype=BF, device=DEV)
+    w[0], w[-1] = normal(gen, N, K, std=K ** -0.5), normal(gen, N, K, std=K ** -0.5)
+    out, gx = moe.moe_grouped_linear(x, w, prefix), moe.moe_grouped_linear_grad_x(g, w, prefix)
+    for e, r in ((0, slice(0, 5)), (E - 1, slice(5, 12))):
+        xe, ge, we = x[r].double(), g[r].double(), w[e].double()
+        close(out[r], xe @ we.T, xe.abs() @ we.abs().T, K, 2.0 ** -8)
+        close(gx[r], ge @ we, ge.abs() @ we.abs(), N, 2.0 ** -8)
+    del w
+    gw = moe.moe_grouped_linear_grad_w(g, x, prefix, dtype=dtype)
+    half = 2.0 ** -24 if dtype == torch.float32 else 2.0 ** -8
+    for e, r in ((0, slice(0, 5)), (E - 1, slice(5, 12))):
+        xe, ge = x[r].double(), g[r].double()
+        close(gw[e], ge.T @ xe, ge.abs().T @ xe.abs(), 7, half)
+    assert not gw[1: E - 1].any()
+
+
+def test_rows_offsets_beyond_32_bits(moe):
+    M, K, N = 280_000, 64, 8192   # 2.3 * 10^9 outputs
+    gen = torch.Generator(DEV).manual_seed(11)
+    p = [0, 3, M - 300, M]
+    prefix = torch.tensor(p, dtype=torch.int32, device=DEV)
+    x, w = normal(gen, M, K), normal(gen, 3, N, K, std=K ** -0.5)
+    out = moe.moe_grouped_linear(x, w, prefix)
+    for e in range(3):
+        r = slice(max(p[e], p[e + 1] - 300), p[e + 1])
+        xe, we = x[r].double(), w[e].double()
+        close(out[r], xe @ we.T, xe.abs() @ we.abs().T, K, 2.0 ** -8)
+    gx = moe.moe_grouped_linear_grad_x(out, w, prefix)
+    r = slice(M - 300, M)
+    close(gx[r], out[r].double() @ w[2].double(), out[r].double().abs() @ w[2].double().abs(), N, 2.0 ** -8)
+
+
+def test_a_graph_follows_the_prefix(moe):
+    """Numbers of rows stay on the device: a captured call serves whatever the prefix says when it runs."""
+    gen = torch.Generator(DEV).manual_seed(12)
+    E, M, K, N = 6, 700, 520, 264
+    x, g, w = normal(gen, M, K), normal(gen, M, N), normal(gen, E, N, K, std=K ** -0.5)
+    prefix = torch.zeros(E + 1, dtype=torch.int32, device=DEV)
+    out, gx, gw = torch.empty(M, N, dtype=BF, device=DEV), torch.empty(M, K, dtype=BF, device=DEV), torch.empty(E, N, K, device=DEV)
+    status = moe.new_status()
+
+    def step():
+        moe.moe_grouped_linear(x, w, prefix, out=out, status=status)
+        moe.moe_grouped_linear_grad_x(g, w, prefix, out=gx, status=status)
+        moe.moe_grouped_linear_grad_w(g, x, prefix, out=gw, status=status)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for counts in ([700, 0, 0, 0, 0, 0], [1, 2, 3, 4, 5, 6], [0, 0, 300, 250, 0, 0], [116] * 6):
+        prefix.copy_(torch.tensor(prefix_of(counts), dtype=torch.int32))
+        for t in (out, gx, gw):
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (out, gx, gw)]
+        n = sum(counts)
+        assert (got[0][n:] == 7).all() and (got[1][n:] == 7).all()
+        for t in (out, gx, gw):
+            t.fill_(7)
+        step()
+        assert all(torch.equal(a, b) for a, b in zip(got, (out, gx, gw)))
+        for e in range(E):
+            r = slice(sum(counts[:e]), sum(counts[: e + 1]))
+            xe, ge, we = x[r].double(), g[r].double(), w[e].double()
+            close(got[0][r], xe @ we.T, xe.abs() @ we.abs().T, K, 2.0 ** -8)
+            close(got[2][e], ge.T @ xe, ge.abs().T @ xe.abs(), max(1, counts[e]), 2.0 ** -24)
+    moe.check_status(status)
+
+
+def test_two_calls_at_once(moe):
+    calls = []
+    for name in ("pairs", "cluster of 8", "single"):
+        _, prefix, x, w, g = operands(name)
+        calls.append((lambda x=x, w=w, prefix=prefix, **kw: moe.moe_grouped_linear(x, w, prefix, **kw)))
+        calls.append((lambda g=g, w=w, prefix=prefix, **kw: moe.moe_grouped_linear_grad_x(g, w, prefix, **kw)))
+    want = [c() for c in calls]
+    rows = [slice(2, -3)] * len(calls)   # those of no expert are not written
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [c(stream=s) for c, s in zip(calls, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a[r], b[r]) for a, b, r in zip(got, want, rows))
+
+
+# ------------------------------------------------------------------ waits
+
+def withheld_cases(moe):
+    for name in ("pairs", "cluster of 8", "single"):
+        _, prefix, x, w, g = operands(name)
+        yield name, lambda s, x=x, w=w, p=prefix: moe.moe_grouped_linear(x, w, p, out=torch.zeros(x.shape[0], w.shape[1], dtype=BF, device=DEV), status=s)
+        yield name + ", rows", lambda s, g=g, w=w, p=prefix: moe.moe_grouped_linear_grad_x(g, w, p, out=torch.zeros(g.shape[0], w.shape[2], dtype=BF, device=DEV), status=s)
+        yield name + ", weights", lambda s, g=g, x=x, p=prefix: moe.moe_grouped_linear_grad_w(g, x, p, status=s)
+        _, prefix, (x, xs), (w, ws) = operands(name, True)
+        yield name + ", E4M3", lambda s, x=x, xs=xs, w=w, ws=ws, p=prefix: moe.moe_grouped_linear(
+            x, w, p, x_scales=xs, w_scales=ws, out=torch.zeros(x.shape[0], w.shape[1], dtype=BF, device=DEV), status=s)
+
+
+@pytest.mark.parametrize("cta", [0, 1])
+def test_withheld_operands_end_in_a_timeout(moe, cta):
+    for name, call in withheld_cases(moe):
+        status = moe.new_status()
+        want = call(status)
+        moe.check_status(status, name)
+        torch.cuda.synchronize()
+        with moe.test_wait_limits(LIMIT_NS, cta):
+            start = time.monotonic()
+            call(status)
+            torch.cuda.synchronize()
+            took = time.monotonic() - start
+        assert int(status.item()) == moe.MOE_ERR_TIMEOUT, name
+        assert took < 1.0, name   # some waits one after another, of 20 ms each
+        status.zero_()
+        assert torch.equal(call(status), want), name
+        moe.check_status(status, name)

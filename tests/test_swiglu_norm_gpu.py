@@ -225,3 +225,84 @@ def test_norm_backward_without_rows_and_twice(moe, T, H):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     gx, gw = moe.moe_add_rms_norm_backward(x[:0], w, g[:0])
     assert gx.shape == (0, H) and not gw.any()
+
+
+def test_offsets_beyond_32_bits(moe):
+    """2.3 * 10^9 elements; the last rows."""
+    gen = torch.Generator(DEV).manual_seed(13)
+    M, I = 280_000, 4096
+    gu = torch.zeros(M, 2 * I, dtype=BF, device=DEV)
+    gu[-3:] = normal(gen, 3, 2 * I)
+    want = torch.nn.functional.silu(gu[-3:, :I].double()) * gu[-3:, I:].double()
+    out, _ = moe.moe_swiglu(gu)
+    close(out[-3:], want, 2.0 ** -8 + FAST)
+    c, s = moe.moe_swiglu(gu, quantize_fp8=True)
+    check_codes(c[-3:], s[-3:], want, FAST)
+    grad = torch.zeros(M, I, dtype=BF, device=DEV)
+    grad[-3:] = normal(gen, 3, I)
+    d, _ = moe.moe_swiglu_backward(gu, grad)
+    few, _ = moe.moe_swiglu_backward(gu[-3:].contiguous(), grad[-3:].contiguous())
+    assert torch.equal(d[-3:], few) and not d[0].any()
+    del out, c, s, grad, d
+    w = normal(gen, 2 * I)
+    r = moe.moe_add_rms_norm(gu, w, residual=gu)
+    few = moe.moe_add_rms_norm(gu[-3:].contiguous(), w, residual=gu[-3:].contiguous())
+    assert torch.equal(r.out[-3:], few.out) and torch.equal(r.residual[-3:], few.residual)
+    gx, gw = moe.moe_add_rms_norm_backward(gu, w, r.out, eps=1.0)
+    few = moe.moe_add_rms_norm_backward(gu[-3:].contiguous(), w, r.out[-3:].contiguous(), eps=1.0)
+    assert torch.equal(gx[-3:], few[0])
+    close(gw, few[1].double(), 2.0 ** -20, 2.0 ** -20 * float(few[1].abs().max()))   # three rows in another order
+
+
+def test_a_limit_alone_changes_nothing_for_the_norms_gradient(moe):
+    gen = torch.Generator(DEV).manual_seed(14)
+    x, w, g = normal(gen, 500, 1024), normal(gen, 1024), normal(gen, 500, 1024)
+    want, status = moe.moe_add_rms_norm_backward(x, w, g), moe.new_status()
+    with moe.test_wait_limits(20_000_000):
+        got = moe.moe_add_rms_norm_backward(x, w, g, status=status)
+    moe.check_status(status)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_in_a_graph_and_on_another_stream(moe):
+    gen = torch.Generator(DEV).manual_seed(15)
+    M, H = 60, 512
+    x, res, w, g, gu = normal(gen, M, H), normal(gen, M, H), normal(gen, H), normal(gen, M, H), normal(gen, M, 2 * H)
+    rw, num = torch.rand(M, device=DEV, generator=gen), torch.tensor([M], dtype=torch.int32, device=DEV)
+    ws = torch.empty(moe.moe_add_rms_norm_backward_workspace_size(M, H), dtype=torch.uint8, device=DEV)
+    status = moe.new_status()
+
+    def step(**kw):
+        kw["status"] = status
+        n = moe.moe_add_rms_norm(x, w, residual=res, quantize_fp8=True, **kw)
+        b = moe.moe_add_rms_norm_backward(n.residual, w, g, grad_residual=g, workspace=ws, **kw)
+        h, _ = moe.moe_swiglu(gu, row_weights=rw, num_rows=num, **kw)
+        q = moe.moe_swiglu(gu, row_weights=rw, num_rows=num, quantize_fp8=True, **kw)
+        d = moe.moe_swiglu_backward(gu, g, row_weights=rw, num_rows=num, **kw)
+        return [n.out, n.residual, n.codes, n.scales, *b, h, *q, *d]
+
+    want = [t.clone() for t in step()]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = step(stream=side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    segments = [s for s in torch.cuda.memory_snapshot() if s["stream"] == side.cuda_stream]
+    for t in got:   # outputs are memory of the stream that wrote them
+        assert any(s["address"] <= t.data_ptr() < s["address"] + s["total_size"] for s in segments)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for _ in range(3):
+        for t in outs:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    num.fill_(7)   # the number of rows stays on the device
+    for t in outs:
+        t.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[6][:7], want[6][:7]) and not outs[6][7:].any()
+    moe.check_status(status)
