@@ -298,12 +298,12 @@ __device__ bool find_tiles(const Args &a, Control &c) {
         int at = -1;
         Range r{};
         for (; t < total; t += step) {
-            const int e = (int)(t / per), i = (int)(t - (int64_t)e * per);
+            const int e = (int)quotient(t, per), i = (int)(t - (int64_t)e * per);
             if (e != at) {
                 r = rows_of(a, at = e);
                 if (r.bad && lane == 0) report(a.status, MOE_ERR_BAD_PREFIX);
             }
-            const int rows = r.hi - r.lo, f = i / a.column_tiles, col = i - f * a.column_tiles;
+            const int rows = r.hi - r.lo, f = (int)quotient(i, a.column_tiles), col = i - f * a.column_tiles;
             const int blocks = (rows + kDepth - 1) / kDepth;
             if (!hand(Tile{e, f * kCtas * kRows, r.lo, min(kCols, a.depth - col * kCols), col * kCols, 0, blocks,
                            rows - (blocks - 1) * kDepth}))
@@ -318,6 +318,7 @@ __device__ bool find_tiles(const Args &a, Control &c) {
             if (e0 + lane < a.E) r = rows_of(a, e0 + lane);
             if (r.bad && blockIdx.x == 0) report(a.status, MOE_ERR_BAD_PREFIX);
             const int rows = r.hi - r.lo, R = (rows + kCols - 1) / kCols;
+            const int per = R > 1 ? round16((int)quotient(rows + R - 1, R)) : rows;   // row tiles of equal size
             const int64_t mine = (int64_t)R * F;
             int64_t upto = mine;
 #pragma unroll
@@ -330,13 +331,13 @@ __device__ bool find_tiles(const Args &a, Control &c) {
                 const int l = __ffs(__ballot_sync(0xffffffffu, before + upto > t)) - 1;
                 const int64_t i = t - before - __shfl_sync(0xffffffffu, upto - mine, l);
                 const int er = __shfl_sync(0xffffffffu, rows, l), eR = __shfl_sync(0xffffffffu, R, l);
-                const int lo = __shfl_sync(0xffffffffu, r.lo, l);
-                // row tiles of equal size, eight of them to a pass over the features
-                const int per = round16((er + eR - 1) / eR);
+                const int lo = __shfl_sync(0xffffffffu, r.lo, l), size = __shfl_sync(0xffffffffu, per, l);
+                // eight row tiles to a pass over the features
                 const int64_t pass = (int64_t)kRowGroup * F;
-                const int g = (int)(i / pass), in = (int)(i - g * pass), width = min(kRowGroup, eR - g * kRowGroup);
-                const int f = in / width, rt = g * kRowGroup + in - f * width;
-                if (!hand(Tile{e0 + l, f * kCtas * kRows, lo + rt * per, min(per, er - rt * per), 0, kb0, blocks, 0}))
+                const int g = eR > kRowGroup ? (int)quotient(i, pass) : 0, width = min(kRowGroup, eR - g * kRowGroup);
+                const int in = (int)(i - g * pass), f = width > 1 ? (int)quotient(in, width) : in;
+                const int rt = g * kRowGroup + in - f * width;
+                if (!hand(Tile{e0 + l, f * kCtas * kRows, lo + rt * size, min(size, er - rt * size), 0, kb0, blocks, 0}))
                     return false;
                 t += step;
                 if (a.split > 1) return hand(Tile{-1, 0, 0, 0, 0, 0, 0, 0});   // a tile to a cluster
@@ -477,10 +478,9 @@ __device__ bool mask_blocks(const Args &a, Control &c, char *ring) {
             seen ^= 1u << r.slot;
             char *at = ring + (size_t)r.slot * (kTileA + C::kTileB);
             const int chunks = 2 + columns_of<kGradW, kCtas>(t) / kCtas / 64;
-            for (int i = lane; i < chunks * (kDepth - t.last) * 8; i += 32) {   // 16 bytes each
-                const int chunk = i / ((kDepth - t.last) * 8), in = i - chunk * (kDepth - t.last) * 8;
-                *reinterpret_cast<int4 *>(at + chunk * 8192 + t.last * 128 + in * 16) = make_int4(0, 0, 0, 0);
-            }
+            for (int chunk = 0; chunk < chunks; ++chunk)
+                for (int at16 = t.last * 8 + lane; at16 < kDepth * 8; at16 += 32)   // 16 bytes each
+                    *reinterpret_cast<int4 *>(at + chunk * 8192 + at16 * 16) = make_int4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) arrive_released(home_addr<kCtas>(&c.full[r.slot]));
@@ -818,7 +818,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
         }
         return true;
     });
-    if (kOp == kGradW && lane == 0) bulk_wait_all();
+    if (kOp == kGradW && lane == 0) bulk_wait_read<0>();
     __syncwarp();
     return ok;
 }

@@ -38,6 +38,8 @@
 namespace moe {
 namespace skinny {
 
+using moe::quotient;
+
 constexpr int kFirstReader = 128;      // first thread of the reading warps
 constexpr int kAdders = 128;           // threads of the adding warps
 constexpr int kMaxLines = 8;
@@ -68,18 +70,6 @@ struct Segment {
     __device__ int n16() const { return (n + 15) & ~15; }
     __device__ bool whole() const { return kb0 == 0 && kb1 == kbs; }
 };
-
-// a / b for a >= 0 and b > 0. An integer division takes 250 cycles or more, and
-// a small call waits for a dozen of them before its first load; below 2^20 a
-// float one is exact: (a + 1/2) / b is at least 1 / (2 b) from the next integer,
-// its error at most 3 units of 2^-24 of a / b.
-static __device__ __noinline__ int64_t long_quotient(int64_t a, int64_t b) {
-    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-    if ((a | b) >> 20) return long_quotient(a, b);
-    return (int)__fdividef((float)(int)a + 0.5f, (float)(int)b);
-}
 
 // A line of K blocks: `tiles` tiles of `kbs` blocks, cut for the CTAs in one of
 // three ways. With room for two CTAs or more to a tile, each tile goes to the
