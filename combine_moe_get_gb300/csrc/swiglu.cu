@@ -12,7 +12,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;         // backward: vectors that a thread loads before it works on the first
+constexpr int kUnroll = 3;         // backward: vectors that a thread loads before it works on the first
 constexpr int kPiece = 256;        // channels of a warp's piece
 
 struct SwigluArgs {
@@ -114,7 +114,7 @@ __device__ __forceinline__ float gradients(const uint4 &g4, const uint4 &u4, con
 
 // `row_warps` warps to a row, up to kUnroll times 8 channels a thread at once; a row's sum of the weight's gradient is
 // added up in a fixed order.
-__global__ __launch_bounds__(kThreads) void swiglu_backward_kernel(const __grid_constant__ SwigluArgs a) {
+__global__ __launch_bounds__(kThreads, 3) void swiglu_backward_kernel(const __grid_constant__ SwigluArgs a) {
     const WarpTrace trace(a.trace, MOE_TRACE_SWIGLU_BACKWARD);
     __shared__ float space[2][kThreads / 32];
     grid_dependency_wait();
@@ -190,7 +190,7 @@ int launch_swiglu_backward(const SwigluLaunch &L) {
     SwigluArgs a{static_cast<const __nv_bfloat16 *>(L.gate_up), static_cast<const __nv_bfloat16 *>(L.grad), L.row_weights,
                  L.num_rows, L.out, nullptr, L.grad_row_weights, L.status, L.num_rows_most, L.intermediate, 1, trace_args()};
     while (a.row_warps < kThreads / 32 && a.I > a.row_warps * 256 * kUnroll) a.row_warps *= 2;
-    const dim3 grid(blocks_for((int64_t)a.M * a.row_warps, 4));
+    const dim3 grid(blocks_for((int64_t)a.M * a.row_warps, 3));
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
     return launch_kernel(swiglu_backward_kernel, grid, dim3(kThreads), 0, s, tuning().overlap != 0, a) == cudaSuccess
                ? MOE_OK : MOE_ERR_CUDA;
