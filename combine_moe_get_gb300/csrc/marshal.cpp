@@ -12,7 +12,7 @@
 #include <initializer_list>
 #include <string>
 
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -126,14 +126,15 @@ class Args {
         if (*at_ == Py_None) return ++at_, nullptr;
         return tensor(name, type, shape).data_ptr();
     }
-    // an output: allocated for None, under the stream that writes it
+    // an output: allocated for None, under the stream that writes it (by the allocator's own entry: past torch's
+    // dispatcher each takes 0.6 us less)
     Tensor output(const char *name, at::ScalarType type, Shape shape, const Tensor &like) {
         if (*at_ != Py_None) return tensor(name, type, shape);
         ++at_;
         c10::cuda::OptionalCUDAStreamGuard under;
         if (stream_given_)
             under.reset_stream(c10::cuda::getStreamFromExternal((cudaStream_t)given_, like.device().index()));
-        return at::empty(at::IntArrayRef(shape), at::TensorOptions().dtype(type).device(like.device()));
+        return at::Tensor(at::detail::empty_cuda(at::IntArrayRef(shape), type, like.device(), std::nullopt));
     }
     // an output that is left out: an undefined tensor, None in Python
     Tensor optional_output(bool wanted, const char *name, at::ScalarType type, Shape shape, const Tensor &like) {
