@@ -6,14 +6,27 @@
 //   of weights  dw[e] = sum over r of dy[r] x[r]^T   D = 128 rows of dw[e] x 256 columns, over the expert's rows
 //
 // The ragged side is the tensor core's n, which goes in steps of 16, so that an
-// expert with 140 rows costs 144 and not 256; features fill its fixed 128 rows.
-// One persistent CTA per SM; each finds its tiles by a scan over the experts'
-// numbers of rows, which stay on the device.
+// expert with 140 rows costs 144 and not 256; features fill its fixed 128 rows,
+// or 256 of a pair of CTAs that work as one (each holds half of both operands, which
+// halves what a block takes from L2: 128 x 128 tiles of single CTAs ran at 1.13
+// PFLOP/s where pairs' 256 x 256 run at 1.5 to 1.67, 16384 rows, 32 experts, 7168 x 4096;
+// one expert 1.8, where a dense library product has 1.9). One persistent CTA per SM;
+// each finds its tiles by a scan over the experts' numbers of rows, which stay on
+// the device. Few rows to an expert are bound by reading the weights: 128 a piece 6.5
+// to 7.0 TB/s, four a piece in E4M3 6.6.
 //
 // Roles of a CTA's warps: 0 loads both operands by TMA, 1 issues the products,
 // 2 owns the tensor memory and finds the tiles, 3 prepares what the products
 // need besides (weights' gradients: zeros in place of the next expert's rows;
-// E4M3: the rows' scales), 4 to 11 read the sums.
+// E4M3: scales), 4 to 11 (E4M3: to 15) read the sums.
+//
+// E4M3 has an fp32 scale for each row and feature and 128 of the reduction, so a
+// block's sums leave the tensor core unscaled, into registers, where they are
+// multiplied by the product of their two scales and added: two operations for each of
+// D's elements and block, 128 x n of them while the pair's products take 2 n cycles.
+// That is all that the ordinary cores have to give, so these readers bound E4M3 where
+// rows are many: 1.7 PFLOP/s (the rate without them 3.2, without their
+// arithmetic 2.7), and what helped was fewer instructions and waits around it.
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -348,7 +361,7 @@ __device__ bool find_tiles(const Args &a, Control &c) {
     return hand(Tile{-1, 0, 0, 0, 0, 0, 0, 0});
 }
 
-// f(tile, its number) for each tile, by a whole warp.
+// f(tile) for each tile, by a whole warp.
 template <class F>
 __device__ bool each_tile(const Args &a, Control &c, F f) {
     TileRing ring;
@@ -617,7 +630,7 @@ __device__ __forceinline__ void store_rows(const Args &a, const Tile &t, int f, 
 
 // A warp's 32 rows x 128 bytes of a weight's gradient: into shared memory, swizzled as the map wants it, and out as one
 // tile, whose part outside the matrix is not written. (Lanes that store 16 bytes each to rows of their own took 1660 us
-// where this takes @W@, 16384 rows, 32 experts, 7168 x 4096.) Two buffers a warp.
+// where this takes 1140, 16384 rows, 32 experts, 7168 x 4096; writing 3.8 GB alone takes 930.) Two buffers a warp.
 template <typename Out>
 __device__ __forceinline__ void store_weights(const Args &a, const Tile &t, int f0, int col, const float (&v)[128 / sizeof(Out)],
                                               char *buffer) {
@@ -969,7 +982,10 @@ int launch_rows(Args &a, int split, cudaStream_t s) {
 // Pairs of CTAs with 256 features to a tile, or single CTAs with 128 features and at most 128 rows, up to eight of them
 // (a cluster) to a tile's reduction: whichever an estimate finds faster, from rows that are spread evenly. A block takes
 // the tensor core 2 n cycles and its loads a cycle for 64 bytes; a tile's ends cost some 2000 cycles and a shared
-// tile's exchange 4000 more (@SPLIT@).
+// tile's exchange 4000 more. Captured calls, us, as pairs / single / clusters of 2, 4, 8, launch and flush (7) included:
+// 100 rows, 7168 x 512: 34 / 38 / 32 / 26 / 22; 4 x 32 rows, 7168 x 512: 32 / 34 / 27 / 22 / 27; 2048 rows, 7168 x 512:
+// 40 / 38 / 35 / 46 / 85; 2 x 700 rows, 4096 x 1024: 30 / 27 / 48 / 56 / 99; 8 x 128 rows, 2048 x 2048: 24 / 28 / 54 /
+// 75 / 149.
 struct Way {
     bool pair;
     int split;

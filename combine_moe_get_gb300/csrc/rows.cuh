@@ -37,8 +37,7 @@ __device__ __forceinline__ uint4 narrow(const float (&x)[8]) {
 // scale amax / 448 (its rounded product with 1 / 448, corrected by what that leaves:
 // off by 2^-24 of it). Codes are those of x * r with r the fast reciprocal, off x / scale by
 // at most 2^-22 of it: where a quotient is that near the middle between two codes,
-// either may come out. (Two IEEE divisions for each lane's eight channels took a fifth of the
-// activation's time.) Scales whose reciprocal could overflow, or that are not normal, take the division. NaN has no part
+// either may come out. Scales whose reciprocal could overflow, or that are not normal, take the division. NaN has no part
 // in amax and keeps its code; with an infinity the scale is infinite, its code NaN and all others 0.
 __device__ __forceinline__ float quantise(const float (&x)[8], uint2 &codes) {
     float amax = 0.0f;

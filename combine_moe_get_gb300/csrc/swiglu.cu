@@ -5,7 +5,10 @@
 //
 // One pass over the rows, bound by HBM. A warp takes 256 channels of a row: 16 bytes
 // of gate and of up a lane, so that 16 lanes hold a block of 128 and its largest
-// magnitude takes four shuffles.
+// magnitude takes four shuffles. 32768 x 2048: 62 us to bf16 (6.5 TB/s), 62 to E4M3
+// (5.5 TB/s: the exponentials, reciprocals and codes take as long as the bytes);
+// the gradient 107 (6.3 TB/s). Four pieces to a warp, loaded at once, were no faster
+// than one, and slower in small calls.
 #include "rows.cuh"
 
 namespace moe {

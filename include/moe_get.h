@@ -725,8 +725,9 @@ MOE_API int moe_adapter_linear(const void *x, int num_tokens, int in_features, c
  * that begins at their first). It need not begin at 0 nor end at num_rows: rows of
  * no expert, those of a receive buffer behind the last one among them, are not
  * written, whatever they hold; an expert without rows is not read. Sums are fp32.
- * A prefix outside [0, num_rows] or one that descends raises MOE_ERR_BAD_PREFIX and
- * is cut to what is inside and in order.
+ * A prefix outside [0, num_rows] or one that descends raises MOE_ERR_BAD_PREFIX; each
+ * expert's rows are cut to those inside, and a row that several experts then claim
+ * gets one's product.
  *
  *   x              [M, K] bf16, or E4M3 codes (uint8, MOE_WEIGHTS_E4M3) with
  *   x_scales       [M, K/128] fp32, as MOE_DISPATCH_QUANTIZE_FP8 and moe_swiglu make them.
@@ -760,7 +761,7 @@ MOE_API int moe_grouped_linear_grad_x(const void *grad, int num_rows, int out_fe
  *
  *   grad_w[e] = sum over r in [expert_prefix[e], expert_prefix[e+1]) of grad[r] x[r]^T
  *
- * summed in fp32 in the order of the rows. An expert without rows gets zeros.
+ * summed in fp32 in an order fixed by the number of rows. An expert without rows gets zeros.
  *
  *   grad [M, N], x [M, K] bf16.
  *   grad_type   MOE_GRAD_F32 or MOE_GRAD_BF16: the type of grad_w [E, N, K].
@@ -791,7 +792,7 @@ MOE_API int moe_grouped_linear_grad_w(const void *grad, const void *x, int num_r
  *                read nor written (expert_prefix + E for a receive buffer with room to
  *                spare). Outside [0, M] it raises MOE_ERR_CAPACITY and is cut to it.
  *   out          [M, I] bf16, or E4M3 codes (uint8) with out_scales [M, I/128] fp32
- *                (NULL for bf16).
+ *                (NULL for bf16); not one of the inputs.
  * gate_up and out are 16-byte aligned (E4M3 codes: 8). Limits: M <= 2^30, I a multiple of 8 (128
  * with E4M3) up to 2^20.
  */
