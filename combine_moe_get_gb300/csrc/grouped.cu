@@ -125,12 +125,10 @@ __device__ __forceinline__ uint32_t home_addr(const void *p) {
 }
 // Arrivals and waits have the CTA's scope: what they order, tensor memory and shared memory that TMA and the products
 // touch, is ordered by those units' own barriers and fences. (With the cluster's scope each wait took L1 with it: 2.5
-// times slower.) Ordinary stores that the pair's other CTA is to see go through arrive_released.
+// times slower.) The zeros of mask_blocks are no exception: fence.proxy.async has them in this CTA's shared memory, where
+// its own tensor core reads them, before the arrival leaves (one with the cluster's scope cost a sixth of the kernel's time).
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void arrive_released(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void arrive_expect_at(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -403,7 +401,7 @@ __device__ bool load(const Args &a, Control &c, uint32_t ring_base, uint32_t ran
         for (int kb = 0; kb < t.blocks; ++kb, r.next(), ++issued) {
             if (!warp_wait(&c.empty[r.slot], r.round ^ 1, a.limits.wait_ns)) return false;
             const uint32_t to_a = ring_base + r.slot * (kTileA + C::kTileB), to_b = to_a + kTileA;
-            const bool mask = kOp == kGradW && kb == t.blocks - 1 && t.last < kDepth;
+            const bool mask = kOp == kGradW && kb == t.blocks - 1 && t.last % 16 != 0;
             if (mine) {
                 // what the products wait for lies in the pair's first CTA; a block to be masked is this CTA's affair first
                 const uint32_t bar = mask ? smem_addr(&c.masked_full[r.slot]) : home_addr<kCtas>(&c.full[r.slot]);
@@ -458,7 +456,8 @@ __device__ bool multiply(const Args &a, Control &c, uint32_t ring_base, uint32_t
             if (mine) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    product<kCtas, C::kE4m3>(d, al + j * kStepA, bl + j * kStepB, desc, j > 0 || (!C::kE4m3 && kb > 0));
+                    if (kOp != kGradW || kb + 1 < t.blocks || j * 16 < t.last)   // steps that have a row
+                        product<kCtas, C::kE4m3>(d, al + j * kStepA, bl + j * kStepB, desc, j > 0 || (!C::kE4m3 && kb > 0));
                 commit<kCtas>(&c.empty[r.slot]);
                 if (C::kE4m3 || kb == t.blocks - 1) commit<kCtas>(&c.sums_full[sums.slot]);
             }
@@ -475,8 +474,9 @@ __device__ bool multiply(const Args &a, Control &c, uint32_t ring_base, uint32_t
 }
 
 // Weights' gradients: the last block of an expert's rows goes on into the next
-// expert's. Zeros in both operands take those rows out (in one alone, an infinity
-// in the other would still make NaN).
+// expert's. Its steps of 16 without a row of this one are left out, and in one that has
+// some, zeros in both operands take the others out (in one alone, an infinity in the
+// other would still make NaN).
 template <int kCtas, int kCols>
 __device__ bool mask_blocks(const Args &a, Control &c, char *ring) {
     using C = Config<kGradW, kCtas, kCols>;
@@ -486,17 +486,17 @@ __device__ bool mask_blocks(const Args &a, Control &c, char *ring) {
     return each_tile(a, c, [&](const Tile &t) {
         if (t.blocks == 0) return true;
         for (int kb = 0; kb < t.blocks - 1; ++kb) r.next();
-        if (t.last < kDepth) {
+        if (t.last % 16 != 0) {
             if (!warp_wait(&c.masked_full[r.slot], seen >> r.slot & 1, a.limits.wait_ns)) return false;
             seen ^= 1u << r.slot;
             char *at = ring + (size_t)r.slot * (kTileA + C::kTileB);
             const int chunks = 2 + columns_of<kGradW, kCtas>(t) / kCtas / 64;
             for (int chunk = 0; chunk < chunks; ++chunk)
-                for (int at16 = t.last * 8 + lane; at16 < kDepth * 8; at16 += 32)   // 16 bytes each
+                for (int at16 = t.last * 8 + lane; at16 < round16(t.last) * 8; at16 += 32)   // 16 bytes each
                     *reinterpret_cast<int4 *>(at + chunk * 8192 + at16 * 16) = make_int4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) arrive_released(home_addr<kCtas>(&c.full[r.slot]));
+            if (lane == 0) arrive_at(home_addr<kCtas>(&c.full[r.slot]));
         }
         r.next();
         return true;
