@@ -62,7 +62,8 @@ struct Tile {
 };
 
 struct Args {
-    CUtensorMap a, b, out_map;          // out_map: weights' gradients
+    CUtensorMap a, b;
+    CUtensorMap a16, b16, out_map;      // weights' gradients: operands 16 rows at a time, the result
     const int32_t *prefix;
     const float *a_scales, *b_scales;   // E4M3: [E, N, K/128] and [M, K/128]
     void *out;
@@ -88,7 +89,7 @@ struct Config {
     static constexpr int kTileB = (kCols / kCtas + kBoxRows - 1) / kBoxRows * kBoxRows * 128;
     static constexpr int kSums = kE4m3 ? (512 / kCols < 4 ? 512 / kCols : 4) : 2;
     static constexpr int kScales = kCols + kRows;   // E4M3: scales of a block's rows and features
-    static constexpr int kBeside = kE4m3 ? kScaleSlots * 4 * kScales * 4 : kOp == kGradW ? kReaders * 2 * kStoreBytes : 0;
+    static constexpr int kBeside = kE4m3 ? kScaleSlots * 4 * kScales * 4 : kOp == kGradW ? kReaders * kStoreBytes : 0;
     static constexpr int kFit = (kSmemBudget - 1024 - kBeside) / (kTileA + kTileB);
     static constexpr int kStages = kFit < 12 ? kFit : 12;
     static constexpr int kTmemCols = kSums * kCols <= 64 ? 64 : kSums * kCols <= 128 ? 128 : kSums * kCols <= 256 ? 256 : 512;
@@ -398,28 +399,34 @@ __device__ bool load(const Args &a, Control &c, uint32_t ring_base, uint32_t ran
         const int part = columns_of<kOp, kCtas>(t) / kCtas;   // columns that this CTA loads
         const int boxes = kOp == kGradW ? part / 64 : (part + kBoxRows - 1) / kBoxRows;
         const uint32_t bytes = kTileA + boxes * (kOp == kGradW ? 64 : kBoxRows) * 128;
+        const int steps = round16(t.last) / 16;   // weights' gradients: of the last block, 16 rows each
         for (int kb = 0; kb < t.blocks; ++kb, r.next(), ++issued) {
             if (!warp_wait(&c.empty[r.slot], r.round ^ 1, a.limits.wait_ns)) return false;
             const uint32_t to_a = ring_base + r.slot * (kTileA + C::kTileB), to_b = to_a + kTileA;
             const bool mask = kOp == kGradW && kb == t.blocks - 1 && t.last % 16 != 0;
+            const bool part_block = kOp == kGradW && kb == t.blocks - 1 && steps < kDepth / 16;
             if (mine) {
                 // what the products wait for lies in the pair's first CTA; a block to be masked is this CTA's affair first
                 const uint32_t bar = mask ? smem_addr(&c.masked_full[r.slot]) : home_addr<kCtas>(&c.full[r.slot]);
-                arrive_expect_at(bar, bytes);
+                arrive_expect_at(bar, part_block ? bytes / (kDepth / 16) * steps : bytes);
                 if constexpr (kOp == kForward || kOp == kForwardE4m3) {
                     load3<kCtas>(to_a, &a.a, (t.kb0 + kb) * C::kBlock, a0, t.e, bar, weights);
                 } else if constexpr (kOp == kGradX) {
                     for (int i = 0; i < 2; ++i) load3<kCtas>(to_a + i * 8192, &a.a, a0 + i * 64, (t.kb0 + kb) * kDepth, t.e, bar, weights);
                 } else {
-                    for (int i = 0; i < 2; ++i) load2<kCtas>(to_a + i * 8192, &a.a, a0 + i * 64, t.row0 + kb * kDepth, bar, often);
+                    // of the last block, no more rows than the products take
+                    const CUtensorMap *map_a = part_block ? &a.a16 : &a.a, *map_b = part_block ? &a.b16 : &a.b;
+                    for (int j = 0; j < (part_block ? steps : 1); ++j) {
+                        const int row = t.row0 + kb * kDepth + j * 16;
+                        for (int i = 0; i < 2; ++i) load2<kCtas>(to_a + i * 8192 + j * 2048, map_a, a0 + i * 64, row, bar, often);
+                        for (int i = 0; i < boxes; ++i)
+                            load2<kCtas>(to_b + i * 8192 + j * 2048, map_b, t.c0 + (int)rank * part + i * 64, row, bar, often);
+                    }
                 }
-                for (int i = 0; i < boxes; ++i) {
-                    if constexpr (kOp == kGradW)
-                        load2<kCtas>(to_b + i * 8192, &a.b, t.c0 + (int)rank * part + i * 64, t.row0 + kb * kDepth, bar, often);
-                    else
+                if constexpr (kOp != kGradW)
+                    for (int i = 0; i < boxes; ++i)
                         load2<kCtas>(to_b + i * kBoxRows * 128, &a.b, (t.kb0 + kb) * C::kBlock, t.row0 + (int)rank * part + i * kBoxRows,
                                      bar, often);
-                }
             }
             __syncwarp();
         }
@@ -629,13 +636,14 @@ __device__ __forceinline__ void store_rows(const Args &a, const Tile &t, int f, 
 }
 
 // A warp's 32 rows x 128 bytes of a weight's gradient: into shared memory, swizzled as the map wants it, and out as one
-// tile, whose part outside the matrix is not written. (Lanes that store 16 bytes each to rows of their own took 1660 us
-// where this takes 1140, 16384 rows, 32 experts, 7168 x 4096; writing 3.8 GB alone takes 930.) Two buffers a warp.
+// tile, whose part outside the matrix is not written. Lanes that stored 16 bytes each to rows of their own took 1660 us
+// where this took 1150 (16384 rows, 32 experts, 7168 x 4096, fp32; with the other steps it is 840, for 3.8 GB written). One
+// buffer a warp: the room of a second holds a sixth stage of the ring, without which masked blocks come late (955 us).
 template <typename Out>
 __device__ __forceinline__ void store_weights(const Args &a, const Tile &t, int f0, int col, const float (&v)[128 / sizeof(Out)],
                                               char *buffer) {
     const int lane = threadIdx.x & 31;
-    if (lane == 0) bulk_wait_read<1>();   // the tile before last has left this buffer
+    if (lane == 0) bulk_wait_read<0>();   // the last one has left the buffer
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -723,8 +731,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
     Ring sums(C::kSums), fours(kScaleSlots);
     constexpr int kStep = 16 * C::kSides, kChunks = (kCols + kStep - 1) / kStep;
     const float *scales = reinterpret_cast<const float *>(beside);
-    char *const buffers = beside + (warp - kFirstReader) * 2 * kStoreBytes;
-    int stored = 0;
+    char *const buffer = beside + (warp - kFirstReader) * kStoreBytes;
     const bool ok = each_tile(a, c, [&](const Tile &t) {
         const int f = t.a0 + (int)rank * kRows + q * 32 + lane;
         if constexpr (C::kE4m3) {
@@ -800,7 +807,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
                     if (f0 >= a.features || (!some && a.accumulate)) continue;
                     if constexpr (sizeof(Out) == 2)
                         if (a.accumulate) add_weights(a, t, f, col, v);
-                    store_weights<Out>(a, t, f0, col, v, buffers + (stored++ & 1) * kStoreBytes);
+                    store_weights<Out>(a, t, f0, col, v, buffer);
                 }
             } else if (kCtas == 1 && a.split > 1) {
                 shared = true;
@@ -1066,6 +1073,8 @@ int launch_grouped_grad_w(const GroupedGradWLaunch &L) {
     Args a{};
     if (!make_tensor_map(&a.a, L.grad, false, L.num_rows, L.out_features, kDepth) ||
         !make_tensor_map(&a.b, L.x, false, L.num_rows, L.in_features, kDepth) ||
+        !make_tensor_map(&a.a16, L.grad, false, L.num_rows, L.out_features, 16) ||
+        !make_tensor_map(&a.b16, L.x, false, L.num_rows, L.in_features, 16) ||
         !make_tensor_map3(&a.out_map, L.out, (int)cell, L.num_experts, L.out_features, L.in_features, 32))
         return MOE_ERR_CUDA;
     a.prefix = L.expert_prefix;
