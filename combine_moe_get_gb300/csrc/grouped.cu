@@ -29,6 +29,7 @@
 // arithmetic 2.7), and what helped was fewer instructions and waits around it.
 #include <algorithm>
 #include <atomic>
+#include <cstdint>
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -352,7 +353,10 @@ __device__ bool find_tiles(const Args &a, Control &c) {
                 if (!hand(Tile{e0 + l, f * kCtas * kRows, lo + rt * size, min(size, er - rt * size), 0, kb0, blocks, 0}))
                     return false;
                 t += step;
-                if (a.split > 1) return hand(Tile{-1, 0, 0, 0, 0, 0, 0, 0});   // a tile to a cluster
+                if (a.split > 1) {   // a tile to a cluster; the first CTA goes on to see the rest of the prefix
+                    if (blockIdx.x != 0) return hand(Tile{-1, 0, 0, 0, 0, 0, 0, 0});
+                    t = INT64_MAX;
+                }
             }
             before += all;
         }

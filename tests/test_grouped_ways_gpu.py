@@ -2,6 +2,9 @@
 over long offsets, in CUDA graphs, on two streams at once, and where their waits run out."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
 import time
 
 import pytest
@@ -202,6 +205,112 @@ def test_two_calls_at_once(moe):
         got = [c(stream=s) for c, s in zip(calls, streams)]
         torch.cuda.synchronize()
         assert all(torch.equal(a[r], b[r]) for a, b, r in zip(got, want, rows))
+
+
+@pytest.mark.parametrize("E,counts", [(8192, {0: 3, 31: 1, 32: 40, 5000: 17, 8191: 200}), (40, {e: 1 for e in range(40)}),
+                                      (2, {0: 5000, 1: 2300})])
+def test_many_experts_and_many_rows(moe, E, counts):
+    K, N = 72, 264
+    gen = torch.Generator(DEV).manual_seed(E)
+    p = prefix_of([counts.get(e, 0) for e in range(E)])
+    prefix = torch.tensor(p, dtype=torch.int32, device=DEV)
+    x, g, w = normal(gen, p[-1], K), normal(gen, p[-1], N), normal(gen, E, N, K, std=K ** -0.5)
+    status = moe.new_status()
+    out = moe.moe_grouped_linear(x, w, prefix, status=status)
+    gx = moe.moe_grouped_linear_grad_x(g, w, prefix, status=status)
+    gw = moe.moe_grouped_linear_grad_w(g, x, prefix, status=status)
+    moe.check_status(status)
+    for e in counts:
+        r = slice(p[e], p[e + 1])
+        xe, ge, we = x[r].double(), g[r].double(), w[e].double()
+        close(out[r], xe @ we.T, xe.abs() @ we.abs().T, K, 2.0 ** -8)
+        close(gx[r], ge @ we, ge.abs() @ we.abs(), N, 2.0 ** -8)
+        close(gw[e], ge.T @ xe, ge.abs().T @ xe.abs(), counts[e], 2.0 ** -24)
+    empty = [e for e in range(E) if e not in counts]
+    assert not gw[empty].any()
+
+
+@pytest.mark.parametrize("name", ["pairs", "cluster of 8", "cluster of 4", "single"])
+@pytest.mark.parametrize("last", [-1, 10 ** 9])
+def test_a_bad_end_of_the_prefix_is_seen(moe, name, last):
+    p, prefix, x, w, g = operands(name)
+    prefix[-1] = last
+    for call in (lambda s: moe.moe_grouped_linear(x, w, prefix, status=s),
+                 lambda s: moe.moe_grouped_linear_grad_x(g, w, prefix, status=s),
+                 lambda s: moe.moe_grouped_linear_grad_w(g, x, prefix, status=s)):
+        status = moe.new_status()
+        call(status)
+        assert int(status.item()) == moe.MOE_ERR_BAD_PREFIX
+
+
+def test_a_rank_takes_its_part_of_the_prefix(moe):
+    """The received rows of all ranks in one buffer, each rank's weights by themselves."""
+    gen = torch.Generator(DEV).manual_seed(16)
+    counts, K, N = [5, 0, 130, 9, 64, 31], 136, 72
+    p = prefix_of(counts)
+    prefix = torch.tensor(p, dtype=torch.int32, device=DEV)
+    x, w = normal(gen, p[-1], K), normal(gen, 6, N, K, std=K ** -0.5)
+    want = moe.moe_grouped_linear(x, w, prefix)
+    got = torch.zeros_like(want)
+    for rank in range(3):
+        moe.moe_grouped_linear(x, w[2 * rank: 2 * rank + 2], prefix[2 * rank: 2 * rank + 3], out=got)
+    assert torch.equal(got, want)
+
+
+FIRST_IN_CAPTURE = """
+import torch
+from combine_moe_get_gb300 import binding as moe
+gen = torch.Generator("cuda").manual_seed(1)
+x, w, g = (torch.randn(*s, device="cuda", generator=gen).bfloat16() for s in ((300, 256), (3, 2048, 256), (300, 2048)))
+prefix = torch.tensor([0, 100, 100, 300], dtype=torch.int32, device="cuda")
+gu, n = torch.randn(300, 512, device="cuda").bfloat16(), torch.ones(256, device="cuda")
+status = moe.new_status()
+moe.moe_topk_gate(torch.zeros(1, 8, device="cuda"), 1, status=status)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+def step():
+    r = moe.moe_add_rms_norm(x, n, quantize_fp8=True, status=status)
+    return (moe.moe_grouped_linear(x, w, prefix, status=status), moe.moe_grouped_linear_grad_x(g, w, prefix, status=status),
+            moe.moe_grouped_linear_grad_w(g, x, prefix, status=status), moe.moe_swiglu(gu, status=status)[0],
+            moe.moe_swiglu_backward(gu, x, status=status)[0], r.out, r.codes,
+            *moe.moe_add_rms_norm_backward(x, n, x, status=status))
+with torch.cuda.graph(graph):
+    outs = step()
+graph.replay()
+torch.cuda.synchronize()
+moe.check_status(status)
+assert all(torch.equal(a, b) for a, b in zip(outs, step()))
+print("captured")
+"""
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stdout + r.stderr
+
+
+def test_traced(moe):
+    """Every new kernel leaves records in the tracing build."""
+    from combine_moe_get_gb300 import build
+    lib = moe.load_library(build.build_trace())
+    records, count = torch.zeros(1 << 20, dtype=torch.uint8, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    p, prefix, x, w, g = operands("uneven parts")
+    gu, ones = normal(torch.Generator(DEV).manual_seed(17), 40, 512), torch.ones(256, device=DEV)
+    h = gu[:, :256].contiguous()
+    with moe.using(lib):
+        moe.trace_enable(records, count)
+        try:
+            moe.moe_grouped_linear(x, w, prefix)
+            moe.moe_swiglu(gu)
+            moe.moe_swiglu_backward(gu, h)
+            moe.moe_add_rms_norm(h, ones)
+            moe.moe_add_rms_norm_backward(h, ones, h)
+            torch.cuda.synchronize()
+        finally:
+            moe.trace_enable(None, None)
+    seen = {moe.TRACE_KERNELS[k] for k in moe.trace_read(records, count)["kernel"]}
+    assert seen == {"grouped", "swiglu", "swiglu_backward", "norm", "norm_backward", "norm_weight"}
 
 
 # ------------------------------------------------------------------ waits
