@@ -109,6 +109,7 @@ struct Control {
     uint64_t scales_full[kScaleSlots], scales_empty[kScaleSlots];
     uint64_t tile_full[kTileSlots], tile_empty[kTileSlots];
     uint64_t last;
+    uint64_t parts;   // a shared tile's sums from the other CTAs
     Tile tiles[kTileSlots];
     uint32_t tmem;
 };
@@ -120,10 +121,15 @@ __device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {   
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_addr(p)), "r"(rank));
     return r;
 }
-// ... of the CTA whose products these are: a pair's first, or this one (whatever cluster it is in).
+// ... of the CTA whose products these are: its pair's first (a cluster's neighbours are pairs), or this one.
+__device__ __forceinline__ uint32_t first_of_pair() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r & ~1u;
+}
 template <int kCtas>
 __device__ __forceinline__ uint32_t home_addr(const void *p) {
-    return kCtas == 2 ? peer_addr(p, 0) : smem_addr(p);
+    return kCtas == 2 ? peer_addr(p, first_of_pair()) : smem_addr(p);
 }
 // Arrivals and waits have the CTA's scope: what they order, tensor memory and shared memory that TMA and the products
 // touch, is ordered by those units' own barriers and fences. (With the cluster's scope each wait took L1 with it: 2.5
@@ -226,7 +232,7 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
     if constexpr (kCtas == 2)
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-            ::"r"(smem_addr(bar)), "h"((uint16_t)3) : "memory");
+            ::"r"(smem_addr(bar)), "h"((uint16_t)(3u << first_of_pair())) : "memory");
     else
         mma_commit(bar);
 }
@@ -693,37 +699,49 @@ __device__ __forceinline__ void add_weights(const Args &a, const Tile &t, int f,
     }
 }
 
-// A tile whose reduction a cluster shares: each of its CTAs adds up the sums of as many columns. They come through
-// distributed shared memory into the ring, which no copy or product uses any more once every CTA's roles have ended, and
-// are added in the order of the reduction. `put` hands this thread's sums to f(column, feature, value); all warps of all
-// CTAs of the cluster come here or through two cluster_sync() of their own.
-template <class Put>
-__device__ void share_tile(const Args &a, const Tile &t, char *ring, int readers, int tid, Put put) {
-    const int split = a.split, rank = blockIdx.x % split, width = (t.n + split - 1) / split;
+// A tile whose reduction a cluster shares: each of its CTAs (of a pair's two, each for its own features) adds up the sums
+// of as many columns. Every CTA lays its sums out in its ring, which no copy or product uses any more once every CTA's
+// roles have ended, and bulk copies take each column's to the CTA that adds them, in the order of the reduction. (Sums
+// stored into the other CTAs' memory four bytes a lane took some 10 us longer for 256 x 256.) `put` hands this
+// thread's sums to f(column, feature, value). All warps of all CTAs of the cluster come here, or through two
+// cluster_sync() of their own: one before the rings are written, one behind the last copy.
+template <int kCtas, class Put>
+__device__ bool share_tile(const Args &a, Control &c, const Tile &t, char *ring, int readers, int tid, Put put) {
+    const int split = a.split, side = blockIdx.x % kCtas, part = blockIdx.x / kCtas % split;
+    const int width = (t.n + split - 1) / split, mine = max(min(width, t.n - part * width), 0);
+    float *sums = reinterpret_cast<float *>(ring), *others = sums + t.n * kRows;   // [column][feature]; the others' of mine
     cluster_sync();
-    const uint32_t here = smem_addr(ring);
-    put([&](int col, int feature, float v) {
-        const int owner = col / width;
-        uint32_t to;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(here), "r"(owner));
-        to += ((rank * width + col - owner * width) * kRows + feature) * 4;
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(to), "f"(v) : "memory");
-    });
+    put([&](int col, int feature, float v) { sums[col * kRows + feature] = v; });
+    fence_proxy_async_smem();
+    asm volatile("barrier.cta.sync 1, %0;" ::"r"(readers * 32) : "memory");
+    if (tid == 0) {
+        if (mine > 0) mbar_arrive_expect_tx(&c.parts, (split - 1) * mine * kRows * 4);
+        for (int p = 0; p < split; ++p) {
+            const int cols = min(width, t.n - p * width);
+            if (p == part || cols <= 0) continue;
+            const uint32_t to = peer_addr(others + (part < p ? part : part - 1) * cols * kRows, p * kCtas + side);
+            asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                         ::"r"(to), "r"(smem_addr(sums + p * width * kRows)), "r"(cols * kRows * 4),
+                           "r"(peer_addr(&c.parts, p * kCtas + side)) : "memory");
+        }
+    }
     __syncwarp();
-    cluster_sync();
-    const float *parts = reinterpret_cast<const float *>(ring);
-    const int mine = min(width, t.n - rank * width), f = tid % 64 * 2;
-    if (t.a0 + f >= a.features) return;
-    for (int i = tid / 64; i < mine; i += readers * 32 / 64) {
+    const bool ok = mine == 0 || warp_wait(&c.parts, 0, a.limits.wait_ns);
+    const int f = tid % 64 * 2, feature = t.a0 + side * kRows + f;
+    for (int i = tid / 64; ok && feature < a.features && i < mine; i += readers * 32 / 64) {
         float2 sum = make_float2(0.0f, 0.0f);
         for (int p = 0; p < split; ++p) {
-            const float2 v = *reinterpret_cast<const float2 *>(parts + (p * width + i) * kRows + f);
+            const float *from = p == part ? sums + (part * width + i) * kRows : others + ((p < part ? p : p - 1) * mine + i) * kRows;
+            const float2 v = *reinterpret_cast<const float2 *>(from + f);
             sum.x += v.x, sum.y += v.y;
         }
         *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                            (size_t)(t.row0 + rank * width + i) * a.features + t.a0 + f) =
+                                            (size_t)(t.row0 + part * width + i) * a.features + feature) =
             __floats2bfloat162_rn(sum.x, sum.y);
     }
+    __syncwarp();
+    cluster_sync();
+    return ok;
 }
 
 // Warps 4 to 11: a quarter of tensor memory's lanes each, every other 16 columns.
@@ -775,9 +793,9 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
                 default: done = blocks(std::integral_constant<int, kChunks>()); break;
             }
             if (!done) return false;
-            if (kCtas == 1 && a.split > 1) {
+            if (a.split > 1) {
                 shared = true;
-                share_tile(a, t, ring, C::kReaders, threadIdx.x - kFirstReader * 32, [&](auto f) {
+                const bool all = share_tile<kCtas>(a, c, t, ring, C::kReaders, threadIdx.x - kFirstReader * 32, [&](auto f) {
 #pragma unroll
                     for (int i = 0; i < kChunks; ++i)
 #pragma unroll
@@ -786,7 +804,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
                             if (col < t.n) f(col, q * 32 + j / 8 * 16 + j / 2 % 2 * 8 + lane / 4, sum[i][j]);
                         }
                 });
-                return true;
+                return all;
             }
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
@@ -813,9 +831,9 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
                         if (a.accumulate) add_weights(a, t, f, col, v);
                     store_weights<Out>(a, t, f0, col, v, buffer);
                 }
-            } else if (kCtas == 1 && a.split > 1) {
+            } else if (a.split > 1) {
                 shared = true;
-                share_tile(a, t, ring, C::kReaders, threadIdx.x - kFirstReader * 32, [&](auto put) {
+                const bool all = share_tile<kCtas>(a, c, t, ring, C::kReaders, threadIdx.x - kFirstReader * 32, [&](auto put) {
                     for (int col = side * 16; col < t.n; col += kStep) {
                         float v[16];
                         tmem_load16(lanes + sums.slot * kCols + col, v);
@@ -825,6 +843,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
                             if (col + j < t.n) put(col + j, q * 32 + lane, v[j]);
                     }
                 });
+                if (!all) return false;
             } else {
                 for (int col = side * 16; col < t.n; col += kStep) {
                     float v[16];
@@ -877,6 +896,7 @@ __global__ __launch_bounds__((Config<kOp, kCtas, kCols>::kThreads), 1) void grou
             mbar_init(&c.tile_empty[i], 1 + (rank == 0) + C::kHelper + C::kReaders);
         }
         mbar_init(&c.last, 1);
+        mbar_init(&c.parts, 1);
         fence_barrier_init();
         tma_prefetch_map(&a.a);
         tma_prefetch_map(&a.b);
@@ -905,7 +925,7 @@ __global__ __launch_bounds__((Config<kOp, kCtas, kCols>::kThreads), 1) void grou
     }
     if (!ok && (threadIdx.x & 31) == 0) report(a.status, MOE_ERR_TIMEOUT);
     __syncwarp();
-    if (kCtas == 1 && a.split > 1 && !shared) {   // beside share_tile
+    if (kOp != kGradW && a.split > 1 && !shared) {   // beside share_tile
         cluster_sync();
         cluster_sync();
     }
@@ -949,7 +969,7 @@ int launch(Args &a, int64_t most_tiles, cudaStream_t s) {
     auto kernel = grouped_kernel<kOp, kCtas, kCols, Out>;
     const int rc = ensure_dynamic_smem((const void *)kernel, C::smem());
     if (rc != MOE_OK) return rc;
-    const int64_t ctas = a.split > 1 ? most_tiles * a.split   // a cluster each, that wait for no other
+    const int64_t ctas = a.split > 1 ? most_tiles * a.split * kCtas   // a cluster each, that wait for no other
                                      : std::min<int64_t>(resident<kOp, kCtas, kCols, Out>(), most_tiles * kCtas);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
@@ -990,13 +1010,13 @@ int launch_rows(Args &a, int split, cudaStream_t s) {
     return launch<kOp, kCtas, kCols>(a, most_row_tiles(a.M, a.E, kCols) * a.feature_tiles, s);
 }
 
-// Pairs of CTAs with 256 features to a tile, or single CTAs with 128 features and at most 128 rows, up to eight of them
-// (a cluster) to a tile's reduction: whichever an estimate finds faster, from rows that are spread evenly. A block takes
-// the tensor core 2 n cycles and its loads a cycle for 64 bytes; a tile's ends cost some 2000 cycles and a shared
-// tile's exchange 4000 more. Captured calls, us, as pairs / single / clusters of 2, 4, 8, launch and flush (7) included:
-// 100 rows, 7168 x 512: 34 / 38 / 32 / 26 / 22; 4 x 32 rows, 7168 x 512: 32 / 34 / 27 / 22 / 27; 2048 rows, 7168 x 512:
-// 40 / 38 / 35 / 46 / 85; 2 x 700 rows, 4096 x 1024: 30 / 27 / 48 / 56 / 99; 8 x 128 rows, 2048 x 2048: 24 / 28 / 54 /
-// 75 / 149.
+// Pairs of CTAs with 256 features to a tile, or single CTAs with 128 features and at most 128 rows, either alone or up to
+// four (eight) to a tile's reduction, in a cluster: whichever an estimate finds faster, from rows that are spread evenly.
+// A block takes the tensor core 2 n cycles and its loads a cycle for 64 bytes (70 for single CTAs); a tile's ends cost
+// some 2000 cycles and a shared tile's exchange 1000 and 55 a column. Captured calls, us, launch and flush (7) included, as
+// pairs / 2 / 4 of them / single / 2 / 4 / 8: 100 rows, 7168 x 512: 34 / 27 / 22 / 36 / 28 / 22 / 20; 4 x 32 rows, 7168 x 512:
+// 32 / 24 / 20 / 34 / 26 / 20 / 26; 2048 rows, 7168 x 512: 40 / 34 / 48 / 38 / 30 / 40 / 71; 2 x 700 rows, 4096 x 1024:
+// 30 / 30 / 42 / 26 / 38 / 44 / 81; 8 x 128 rows, 2048 x 2048: 24 / 38 / 67 / 29 / 44 / 61 / 122.
 struct Way {
     bool pair;
     int split;
@@ -1011,13 +1031,14 @@ Way way_for(const Args &a, int block_cells, int pair_cols) {
         const double n = rows / per, features = pair ? 256 : 128;
         const int64_t tiles = (int64_t)groups * per * ceil_div(a.features, (int)features);
         const int64_t most = most_row_tiles(a.M, a.E, cols) * ceil_div(a.features, (int)features);
-        const double block = std::max(2.0 * n, (128 * 128 + (pair ? n / 2 : n) * 128) / 64.0);
-        for (int split = 1; split <= (pair ? 1 : 8); split *= 2) {
+        const double block = std::max(2.0 * n, (128 * 128 + (pair ? n / 2 : n) * 128) / (pair ? 64.0 : 70.0));
+        for (int split = 1; split <= (pair ? 4 : 8); split *= 2) {
             const int step = block_cells == 128 ? 4 : 1, of = ceil_div(a.blocks, split * step) * step;
+            const int size = split * (pair ? 2 : 1);
             // the grid has a cluster for every tile there may be; four fifths of the SMs take clusters of eight at once
-            if (split > 1 && (most * split > (split == 8 ? sms * 4 / 5 : sms) || (split - 1) * of >= a.blocks)) break;
-            const int64_t at_once = pair ? sms / 2 : sms / split;
-            const double cycles = (double)((tiles + at_once - 1) / at_once) * (of * block + 2000) + (split > 1 ? 4000 : 0);
+            if (split > 1 && (most * size > (size == 8 ? sms * 4 / 5 : sms) || (split - 1) * of >= a.blocks)) break;
+            const int64_t at_once = sms / size;
+            const double cycles = (double)((tiles + at_once - 1) / at_once) * (of * block + 2000) + (split > 1 ? 1000 + 55 * n : 0);
             if (least == 0 || cycles < least) least = cycles, best = Way{pair != 0, split};
         }
     }
@@ -1029,7 +1050,7 @@ int launch_best(Args &a, cudaStream_t s) {
     constexpr int cells = kOp == kForwardE4m3 ? 128 : kDepth;
     a.blocks = ceil_div(a.depth, cells);
     const Way w = way_for(a, cells, kPairCols);
-    return w.pair ? launch_rows<kOp, 2, kPairCols>(a, 1, s) : launch_rows<kOp, 1, 128>(a, w.split, s);
+    return w.pair ? launch_rows<kOp, 2, kPairCols>(a, w.split, s) : launch_rows<kOp, 1, 128>(a, w.split, s);
 }
 }  // namespace
 
