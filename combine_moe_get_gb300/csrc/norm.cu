@@ -244,21 +244,24 @@ __global__ __launch_bounds__(backward_warps(kVec) * 32) void norm_backward_kerne
     }
     if (!ok && lane == 0) report(a.status, MOE_ERR_TIMEOUT);
     __syncthreads();   // no copy is under way: every stage that was fetched has been waited for
-    float *sums = reinterpret_cast<float *>(rings);   // [H], with more than one group
-    for (int k = groups - 1; k >= 0; --k) {   // the last group's first, the first group's out
-        if (group == k)
+    float *sums = reinterpret_cast<float *>(rings);   // [groups][H]: half of the smallest ring
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                const int col = (j * threads + tid) * 8;
-                if (col >= a.H) continue;
-                if (k + 1 < groups)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) dw[j][i] += sums[col + i];
-                float4 *to = reinterpret_cast<float4 *>(k > 0 ? sums + col : a.parts + (size_t)blockIdx.x * a.H + col);
-                to[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
-                to[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
-            }
-        __syncthreads();
+    for (int j = 0; j < kVec; ++j) {
+        const int col = (j * threads + tid) * 8;
+        if (col >= a.H) continue;
+        float4 *to = reinterpret_cast<float4 *>(groups > 1 ? sums + group * a.H + col : a.parts + (size_t)blockIdx.x * a.H + col);
+        to[0] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
+        to[1] = make_float4(dw[j][4], dw[j][5], dw[j][6], dw[j][7]);
+    }
+    if (groups == 1) return;
+    __syncthreads();
+    for (int col = threadIdx.x * 4; col < a.H; col += blockDim.x * 4) {
+        float4 sum = *reinterpret_cast<const float4 *>(sums + col);
+        for (int g = 1; g < groups; ++g) {
+            const float4 v = *reinterpret_cast<const float4 *>(sums + g * a.H + col);
+            sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        }
+        *reinterpret_cast<float4 *>(a.parts + (size_t)blockIdx.x * a.H + col) = sum;
     }
 }
 
@@ -314,7 +317,7 @@ cudaError_t launch_backward(NormArgs &a, cudaStream_t s) {
     a.num_parts = need < ctas ? (int)need : ctas;
     const int stage = groups * (a.residual ? 3 : 2) * a.H * 2;   // at most 96 KB
     a.stages = kRingBytes / stage < kMostStages ? kRingBytes / stage : kMostStages;
-    size_t smem = (size_t)a.stages * stage;   // at least two stages of 4 H bytes, room for the groups' sums too
+    const size_t smem = (size_t)a.stages * stage;   // two stages at least, of 4 H bytes a group: room for the groups' sums
     const int rc = ensure_dynamic_smem((const void *)norm_backward_kernel<kVec>, kRingBytes);
     if (rc != MOE_OK) return cudaErrorUnknown;
     return launch_kernel(norm_backward_kernel<kVec>, dim3(a.num_parts), dim3(groups * a.row_warps * 32), smem, s,
