@@ -58,7 +58,7 @@ struct Tile {
     int row0;       // first row
     int n;          // rows (weights' gradients: columns) of the tile
     int c0;         // weights' gradients: first column
-    int kb0, blocks;   // first block along the reduction, and how many
+    int kb0, blocks;   // first block along the reduction, and how many (weights' gradients: the expert's, and this CTA's of them)
     int last;          // weights' gradients: rows in the last block
 };
 
@@ -323,10 +323,12 @@ __device__ bool find_tiles(const Args &a, Control &c) {
                 if (r.bad && lane == 0) report(a.status, MOE_ERR_BAD_PREFIX);
             }
             const int rows = r.hi - r.lo, f = (int)quotient(i, a.column_tiles), col = i - f * a.column_tiles;
-            const int blocks = (rows + kDepth - 1) / kDepth;
-            if (!hand(Tile{e, f * kCtas * kRows, r.lo, min(kCols, a.depth - col * kCols), col * kCols, 0, blocks,
-                           rows - (blocks - 1) * kDepth}))
+            const int all = (rows + kDepth - 1) / kDepth, each = (all + a.split - 1) / a.split;
+            const int kb0 = blockIdx.x / kCtas % a.split * each, blocks = max(min(all - kb0, each), 0);
+            if (!hand(Tile{e, f * kCtas * kRows, r.lo + kb0 * kDepth, min(kCols, a.depth - col * kCols), col * kCols, all, blocks,
+                           kb0 + blocks == all ? rows - (all - 1) * kDepth : kDepth}))
                 return false;
+            if (a.split > 1) break;   // a tile to a cluster
         }
     } else {
         const int F = a.feature_tiles, kb0 = blockIdx.x / kCtas % a.split * a.per_split;
@@ -699,21 +701,22 @@ __device__ __forceinline__ void add_weights(const Args &a, const Tile &t, int f,
     }
 }
 
-// A tile whose reduction a cluster shares: each of its CTAs (of a pair's two, each for its own features) adds up the sums
-// of as many columns. Every CTA lays its sums out in its ring, which no copy or product uses any more once every CTA's
-// roles have ended, and bulk copies take each column's to the CTA that adds them, in the order of the reduction. (Sums
-// stored into the other CTAs' memory four bytes a lane took some 10 us longer for 256 x 256.) `put` hands this
-// thread's sums to f(column, feature, value). All warps of all CTAs of the cluster come here, or through two
-// cluster_sync() of their own: one before the rings are written, one behind the last copy.
-template <int kCtas, class Put>
-__device__ bool share_tile(const Args &a, Control &c, const Tile &t, char *ring, int readers, int tid, Put put) {
+// A tile whose reduction a cluster shares: each of its CTAs (of a pair's two, each for its own features) adds up the
+// sums of as many columns. Every CTA lays its sums out in its ring, which no copy or product uses any more once every
+// CTA's roles have ended, and bulk copies take each column's to the CTA that adds them, in the order of the reduction.
+// (Sums stored into the other CTAs' memory four bytes a lane took some 10 us longer for 256 x 256.) `put` hands this
+// thread's sums to f(column, feature, value); take(first column, columns, sum) stores this CTA's, where sum(i, f) is
+// what the i-th of them has for features f and f + 1. All warps of all CTAs of the cluster come here, or through
+// cluster_sync() of their own: before the rings are written, before they are copied, and behind the last copy.
+template <int kCtas, class Put, class Take>
+__device__ bool share_tile(const Args &a, Control &c, const Tile &t, char *ring, int tid, Put put, Take take) {
     const int split = a.split, side = blockIdx.x % kCtas, part = blockIdx.x / kCtas % split;
-    const int width = (t.n + split - 1) / split, mine = max(min(width, t.n - part * width), 0);
+    const int width = ((t.n + split - 1) / split + 7) & ~7, mine = max(min(width, t.n - part * width), 0);
     float *sums = reinterpret_cast<float *>(ring), *others = sums + t.n * kRows;   // [column][feature]; the others' of mine
     cluster_sync();
     put([&](int col, int feature, float v) { sums[col * kRows + feature] = v; });
     fence_proxy_async_smem();
-    asm volatile("barrier.cta.sync 1, %0;" ::"r"(readers * 32) : "memory");
+    cluster_sync();
     if (tid == 0) {
         if (mine > 0) mbar_arrive_expect_tx(&c.parts, (split - 1) * mine * kRows * 4);
         for (int p = 0; p < split; ++p) {
@@ -727,21 +730,76 @@ __device__ bool share_tile(const Args &a, Control &c, const Tile &t, char *ring,
     }
     __syncwarp();
     const bool ok = mine == 0 || warp_wait(&c.parts, 0, a.limits.wait_ns);
-    const int f = tid % 64 * 2, feature = t.a0 + side * kRows + f;
-    for (int i = tid / 64; ok && feature < a.features && i < mine; i += readers * 32 / 64) {
-        float2 sum = make_float2(0.0f, 0.0f);
-        for (int p = 0; p < split; ++p) {
-            const float *from = p == part ? sums + (part * width + i) * kRows : others + ((p < part ? p : p - 1) * mine + i) * kRows;
-            const float2 v = *reinterpret_cast<const float2 *>(from + f);
-            sum.x += v.x, sum.y += v.y;
-        }
-        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                            (size_t)(t.row0 + part * width + i) * a.features + feature) =
-            __floats2bfloat162_rn(sum.x, sum.y);
-    }
+    if (ok)
+        take(part * width, mine, [&](int i, int f) {
+            float2 sum = make_float2(0.0f, 0.0f);
+            for (int p = 0; p < split; ++p) {
+                const float *from = p == part ? sums + (part * width + i) * kRows : others + ((p < part ? p : p - 1) * mine + i) * kRows;
+                const float2 v = *reinterpret_cast<const float2 *>(from + f);
+                sum.x += v.x, sum.y += v.y;
+            }
+            return sum;
+        });
     __syncwarp();
     cluster_sync();
     return ok;
+}
+
+// A shared tile's part of the result's rows: two features a thread, 64 threads to a row.
+template <int kCtas, class Sum>
+__device__ void store_shared_rows(const Args &a, const Tile &t, int readers, int tid, int col0, int cols, Sum sum) {
+    const int f = tid % 64 * 2, feature = t.a0 + (int)(blockIdx.x % kCtas) * kRows + f;
+    if (feature >= a.features) return;
+    for (int i = tid / 64; i < cols; i += readers * 32 / 64) {
+        const float2 v = sum(i, f);
+        *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + (size_t)(t.row0 + col0 + i) * a.features + feature) =
+            __floats2bfloat162_rn(v.x, v.y);
+    }
+}
+// ... of a weight's gradient: eight columns of two of its rows a thread.
+template <int kCtas, typename Out, class Sum>
+__device__ void store_shared_weights(const Args &a, const Tile &t, int readers, int tid, int col0, int cols, Sum sum) {
+    const int f = tid % 64 * 2, feature = t.a0 + (int)(blockIdx.x % kCtas) * kRows + f;
+    if (feature >= a.features || (t.kb0 == 0 && a.accumulate)) return;
+    for (int i = tid / 64 * 8; i < cols; i += readers * 32 / 64 * 8) {   // columns come in eights
+        float v[2][8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 x = sum(i + j, f);
+            v[0][j] = x.x, v[1][j] = x.y;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            Out *out = static_cast<Out *>(a.out) + ((size_t)t.e * a.features + feature + h) * a.depth + t.c0 + col0 + i;
+            if constexpr (sizeof(Out) == 4) {
+                float4 *to = reinterpret_cast<float4 *>(out);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    float4 x = make_float4(v[h][4 * j], v[h][4 * j + 1], v[h][4 * j + 2], v[h][4 * j + 3]);
+                    if (a.accumulate) {
+                        const float4 y = to[j];
+                        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+                    }
+                    to[j] = x;
+                }
+            } else {
+                uint4 *to = reinterpret_cast<uint4 *>(out);
+                uint4 x = {};
+                __nv_bfloat162 *b = reinterpret_cast<__nv_bfloat162 *>(&x);
+                if (a.accumulate) {
+                    x = *to;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 y = __bfloat1622float2(b[j]);
+                        v[h][2 * j] += y.x, v[h][2 * j + 1] += y.y;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) b[j] = __floats2bfloat162_rn(v[h][2 * j], v[h][2 * j + 1]);
+                *to = x;
+            }
+        }
+    }
 }
 
 // Warps 4 to 11: a quarter of tensor memory's lanes each, every other 16 columns.
@@ -749,6 +807,7 @@ template <Op kOp, int kCtas, int kCols, typename Out>
 __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, uint32_t tmem, uint32_t rank, bool &shared) {
     using C = Config<kOp, kCtas, kCols>;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, q = warp % 4, side = (warp - kFirstReader) / 4;
+    const int tid = threadIdx.x - kFirstReader * 32;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     Ring sums(C::kSums), fours(kScaleSlots);
     constexpr int kStep = 16 * C::kSides, kChunks = (kCols + kStep - 1) / kStep;
@@ -795,7 +854,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
             if (!done) return false;
             if (a.split > 1) {
                 shared = true;
-                const bool all = share_tile<kCtas>(a, c, t, ring, C::kReaders, threadIdx.x - kFirstReader * 32, [&](auto f) {
+                const bool all = share_tile<kCtas>(a, c, t, ring, tid, [&](auto f) {
 #pragma unroll
                     for (int i = 0; i < kChunks; ++i)
 #pragma unroll
@@ -803,7 +862,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
                             const int col = i * kStep + side * 16 + j / 4 % 2 * 8 + (lane & 3) * 2 + j % 2;
                             if (col < t.n) f(col, q * 32 + j / 8 * 16 + j / 2 % 2 * 8 + lane / 4, sum[i][j]);
                         }
-                });
+                }, [&](int col0, int cols, auto total) { store_shared_rows<kCtas>(a, t, C::kReaders, tid, col0, cols, total); });
                 return all;
             }
 #pragma unroll
@@ -815,7 +874,26 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
             const bool some = t.blocks > 0;
             if (some && !warp_wait(&c.sums_full[sums.slot], sums.round, a.limits.wait_ns)) return false;
             tc_fence_after();
-            if constexpr (kOp == kGradW) {
+            if (a.split > 1) {
+                shared = true;
+                const auto put_all = [&](auto put) {
+                    for (int col = side * 16; col < t.n; col += kStep) {
+                        float v[16] = {};
+                        if (some) {
+                            tmem_load16(lanes + sums.slot * kCols + col, v);
+                            tmem_load_wait(v);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (col + j < t.n) put(col + j, q * 32 + lane, v[j]);
+                    }
+                };
+                const bool all = share_tile<kCtas>(a, c, t, ring, tid, put_all, [&](int col0, int cols, auto total) {
+                    if constexpr (kOp == kGradW) store_shared_weights<kCtas, Out>(a, t, C::kReaders, tid, col0, cols, total);
+                    else store_shared_rows<kCtas>(a, t, C::kReaders, tid, col0, cols, total);
+                });
+                if (!all) return false;
+            } else if constexpr (kOp == kGradW) {
                 constexpr int kWide = 128 / sizeof(Out);
                 const int f0 = t.a0 + (int)rank * kRows + q * 32;
                 for (int col = side * kWide; col < t.n; col += C::kSides * kWide) {
@@ -831,19 +909,6 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
                         if (a.accumulate) add_weights(a, t, f, col, v);
                     store_weights<Out>(a, t, f0, col, v, buffer);
                 }
-            } else if (a.split > 1) {
-                shared = true;
-                const bool all = share_tile<kCtas>(a, c, t, ring, C::kReaders, threadIdx.x - kFirstReader * 32, [&](auto put) {
-                    for (int col = side * 16; col < t.n; col += kStep) {
-                        float v[16];
-                        tmem_load16(lanes + sums.slot * kCols + col, v);
-                        tmem_load_wait(v);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            if (col + j < t.n) put(col + j, q * 32 + lane, v[j]);
-                    }
-                });
-                if (!all) return false;
             } else {
                 for (int col = side * 16; col < t.n; col += kStep) {
                     float v[16];
@@ -925,8 +990,10 @@ __global__ __launch_bounds__((Config<kOp, kCtas, kCols>::kThreads), 1) void grou
     }
     if (!ok && (threadIdx.x & 31) == 0) report(a.status, MOE_ERR_TIMEOUT);
     __syncwarp();
-    if (kOp != kGradW && a.split > 1 && !shared) {   // beside share_tile
+    if (a.split > 1 && !shared) {   // beside share_tile
         cluster_sync();
+        cluster_sync();
+        if (!ok) warp_wait(&c.parts, 0, a.limits.wait_ns);   // the others' copies may be on their way here all the same
         cluster_sync();
     }
     tc_fence_before();
@@ -1045,6 +1112,41 @@ Way way_for(const Args &a, int block_cells, int pair_cols) {
     return best;
 }
 
+// Weights' gradients, likewise: pairs with 256 x 256 of a weight to a tile or single CTAs with 128 x 128, alone or in
+// clusters that share an expert's rows. us as above: 16384 rows, 1024 x 512: 81 / 57 / 41 / 79 / 52 / 36 / 67; 4096 rows,
+// 2048 x 512: 30 / 32 / 46 / 28 / 26 / 36 / 72; 8 x 16384 rows, 512 x 512: 89 / 74 / 121 / 83 / 103 / 123 / 188; 100 rows,
+// 7168 x 512: 14 / 39 / 71 / 13 / 40 / 77 / 174; 4096 rows, 7168 x 2048: 79 / 190 / 323 / 124 / 247 / 375 / 788.
+Way way_for_weights(const Args &a) {
+    const int sms = device_sm_count(), rows = ceil_div(a.M, a.E), blocks = ceil_div(rows, kDepth);
+    Way best{true, 1};
+    double least = 0;
+    for (int pair = 1; pair >= 0; --pair) {
+        const int edge = pair ? 256 : 128;
+        const int64_t tiles = (int64_t)a.E * ceil_div(a.features, edge) * ceil_div(a.depth, edge);
+        const double block = pair ? 512 : 468;
+        for (int split = 1; split <= (pair ? 4 : 8); split *= 2) {
+            const int size = split * (pair ? 2 : 1), of = ceil_div(blocks, split);
+            if (split > 1 && (tiles * size > (size == 8 ? sms * 4 / 5 : sms) || (split - 1) * of >= blocks)) break;
+            const int64_t at_once = sms / size;
+            const double cycles = (double)((tiles + at_once - 1) / at_once) * (of * block + 2000) + (split > 1 ? 1000 + 55 * edge : 0);
+            if (least == 0 || cycles < least) least = cycles, best = Way{pair != 0, split};
+        }
+    }
+    return best;
+}
+template <int kCtas, int kCols, typename Out>
+int launch_weights(Args &a, int split, cudaStream_t s) {
+    a.split = split;
+    a.feature_tiles = ceil_div(a.features, kCtas * kRows);
+    a.column_tiles = ceil_div(a.depth, kCols);
+    return launch<kGradW, kCtas, kCols, Out>(a, (int64_t)a.E * a.feature_tiles * a.column_tiles, s);
+}
+template <typename Out>
+int launch_weights(Args &a, cudaStream_t s) {
+    const Way w = way_for_weights(a);
+    return w.pair ? launch_weights<2, 256, Out>(a, w.split, s) : launch_weights<1, 128, Out>(a, w.split, s);
+}
+
 template <Op kOp, int kPairCols>
 int launch_best(Args &a, cudaStream_t s) {
     constexpr int cells = kOp == kForwardE4m3 ? 128 : kDepth;
@@ -1110,13 +1212,7 @@ int launch_grouped_grad_w(const GroupedGradWLaunch &L) {
     a.accumulate = L.accumulate;
     a.limits = wait_limits();
     a.trace = trace_args();
-    constexpr int kCols = 256;
-    a.split = 1;
-    a.feature_tiles = ceil_div(a.features, 2 * kRows);
-    a.column_tiles = ceil_div(a.depth, kCols);
-    const int64_t tiles = (int64_t)a.E * a.feature_tiles * a.column_tiles;
-    return L.out_type == MOE_GRAD_F32 ? launch<kGradW, 2, kCols, float>(a, tiles, s)
-                                      : launch<kGradW, 2, kCols, __nv_bfloat16>(a, tiles, s);
+    return L.out_type == MOE_GRAD_F32 ? launch_weights<float>(a, s) : launch_weights<__nv_bfloat16>(a, s);
 }
 
 }  // namespace moe

@@ -95,6 +95,53 @@ def test_e4m3(moe, name):
         close(out[r], xe @ we.T, xe.abs() @ we.abs().T, x.shape[1], 2.0 ** -8)
 
 
+# counts, K, N: weights' gradients whose tiles are few and rows many; an expert without rows and one with fewer blocks
+# than the cluster has CTAs
+WEIGHTS = {
+    "pairs, 2 of them": ([6001], 1272, 1528),
+    "pairs, 4 of them": ([11998, 3], 1016, 504),
+    "single": ([130, 128, 0, 1, 127] * 3, 520, 392),
+    "2 of them": ([3500], 2040, 512),
+    "4 of them": ([5001], 1000, 504),
+    "8 of them": ([5000], 512, 264),
+    "uneven experts": ([9000, 0, 40, 65], 136, 72),
+}
+
+
+def weights_operands(name):
+    counts, K, N = WEIGHTS[name]
+    gen = torch.Generator(DEV).manual_seed(len(name))
+    p = prefix_of(counts, 5)
+    return p, torch.tensor(p, dtype=torch.int32, device=DEV), normal(gen, p[-1] + 9, K), normal(gen, p[-1] + 9, N)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("name", WEIGHTS)
+def test_weights_shared(moe, name, dtype):
+    p, prefix, x, g = weights_operands(name)
+    E, N, K, status = len(p) - 1, g.shape[1], x.shape[1], moe.new_status()
+    # rows of no expert, which the first and last block of an expert's rows go on into
+    x[: p[0]], x[p[-1]:], g[: p[0]], g[p[-1]:] = float("nan"), float("inf"), float("inf"), float("nan")
+    out = torch.full((E, N, K), 7.0, dtype=dtype, device=DEV)
+    moe.moe_grouped_linear_grad_w(g, x, prefix, out=out, status=status)
+    again = torch.randn(E, N, K, device=DEV, generator=torch.Generator(DEV).manual_seed(1)).to(dtype)
+    start = again.clone()
+    moe.moe_grouped_linear_grad_w(g, x, prefix, out=again, accumulate=True, status=status)
+    assert torch.equal(moe.moe_grouped_linear_grad_w(g, x, prefix, dtype=dtype), out)
+    moe.check_status(status)
+    half = 2.0 ** -24 if dtype == torch.float32 else 2.0 ** -8
+    for e in range(E):
+        r = slice(p[e], p[e + 1])
+        rows = p[e + 1] - p[e]
+        if rows == 0:
+            assert not out[e].any() and torch.equal(again[e], start[e])
+            continue
+        xe, ge, s = x[r].double(), g[r].double(), start[e].double()
+        want, size = ge.T @ xe, ge.abs().T @ xe.abs()
+        close(out[e], want, size, rows, half)
+        close(again[e], want + s, size + s.abs(), rows + 1, half)
+
+
 def test_e4m3_scales_far_apart(moe):
     """Blocks whose scales differ by 2^40, and scales at no 16-byte boundary."""
     gen = torch.Generator(DEV).manual_seed(9)
@@ -324,6 +371,25 @@ def withheld_cases(moe):
         _, prefix, (x, xs), (w, ws) = operands(name, True)
         yield name + ", E4M3", lambda s, x=x, xs=xs, w=w, ws=ws, p=prefix: moe.moe_grouped_linear(
             x, w, p, x_scales=xs, w_scales=ws, out=torch.zeros(x.shape[0], w.shape[1], dtype=BF, device=DEV), status=s)
+
+
+@pytest.mark.parametrize("cta", [0, 1, 5])
+def test_withheld_rows_of_a_shared_gradient(moe, cta):
+    for name in ("pairs, 4 of them", "2 of them", "8 of them", "uneven experts"):
+        _, prefix, x, g = weights_operands(name)
+        status = moe.new_status()
+        want = moe.moe_grouped_linear_grad_w(g, x, prefix, status=status)
+        moe.check_status(status, name)
+        torch.cuda.synchronize()
+        with moe.test_wait_limits(LIMIT_NS, cta):
+            start = time.monotonic()
+            moe.moe_grouped_linear_grad_w(g, x, prefix, status=status)
+            torch.cuda.synchronize()
+            assert time.monotonic() - start < 1.0, name
+        assert int(status.item()) == moe.MOE_ERR_TIMEOUT, name
+        status.zero_()
+        assert torch.equal(moe.moe_grouped_linear_grad_w(g, x, prefix, status=status), want), name
+        moe.check_status(status, name)
 
 
 @pytest.mark.parametrize("cta", [0, 1])
