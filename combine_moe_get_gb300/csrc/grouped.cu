@@ -64,7 +64,7 @@ struct Tile {
 
 struct Args {
     CUtensorMap a, b;
-    CUtensorMap a16, b16, out_map;      // weights' gradients: operands 16 rows at a time, the result
+    CUtensorMap a16, b16;               // weights' gradients: operands 16 rows at a time
     const int32_t *prefix;
     const float *a_scales, *b_scales;   // E4M3: [E, N, K/128] and [M, K/128]
     void *out;
@@ -647,16 +647,15 @@ __device__ __forceinline__ void store_rows(const Args &a, const Tile &t, int f, 
     }
 }
 
-// A warp's 32 rows x 128 bytes of a weight's gradient: into shared memory, swizzled as the map wants it, and out as one
-// tile, whose part outside the matrix is not written. Lanes that stored 16 bytes each to rows of their own took 1660 us
-// where this took 1150 (16384 rows, 32 experts, 7168 x 4096, fp32; with the other steps it is 840, for 3.8 GB written). One
-// buffer a warp: the room of a second holds a sixth stage of the ring, without which masked blocks come late (955 us).
+// A warp's 32 rows x 128 bytes of a weight's gradient, through shared memory so that eight lanes write 128 bytes of a row.
+// Lanes that stored 16 bytes each to rows of their own took 1660 us where TMA tiles took 1150 (16384 rows, 32 experts, 7168 x
+// 4096, fp32; with the other steps those took 850, for 3.8 GB written). But the tiles' rows kept TMA from the loads: 190
+// cycles to issue one, 6000 a tile whose products take 4100.
 template <typename Out>
 __device__ __forceinline__ void store_weights(const Args &a, const Tile &t, int f0, int col, const float (&v)[128 / sizeof(Out)],
                                               char *buffer) {
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) bulk_wait_read<0>();   // the last one has left the buffer
-    __syncwarp();
+    const int lane = threadIdx.x & 31, piece = lane & 7, row = lane / 8;
+    __syncwarp();   // the last ones have been read
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         uint4 x;
@@ -670,16 +669,22 @@ __device__ __forceinline__ void store_weights(const Args &a, const Tile &t, int 
         }
         *reinterpret_cast<uint4 *>(buffer + lane * 128 + ((i ^ (lane & 7)) * 16)) = x;
     }
-    fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) {
-        if (sizeof(Out) == 4 && a.accumulate)
-            asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
-                         ::"l"(&a.out_map), "r"(t.c0 + col), "r"(f0), "r"(t.e), "r"(smem_addr(buffer)) : "memory");
-        else
-            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
-                         ::"l"(&a.out_map), "r"(t.c0 + col), "r"(f0), "r"(t.e), "r"(smem_addr(buffer)) : "memory");
-        bulk_commit();
+    const int c = col + piece * (int)(16 / sizeof(Out));
+    if (c >= t.n) return;
+    Out *out = static_cast<Out *>(a.out) + ((size_t)t.e * a.features + f0 + row) * a.depth + t.c0 + c;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(buffer + (i + row) * 128 + ((piece ^ ((i + row) & 7)) * 16));
+        if (f0 + i + row < a.features) {
+            uint4 *to = reinterpret_cast<uint4 *>(out + (size_t)i * a.depth);
+            if (sizeof(Out) == 4 && a.accumulate)
+                asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};"
+                             ::"l"(to), "f"(__uint_as_float(x.x)), "f"(__uint_as_float(x.y)), "f"(__uint_as_float(x.z)),
+                               "f"(__uint_as_float(x.w)) : "memory");
+            else
+                *to = x;
+        }
     }
 }
 
@@ -926,7 +931,6 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
         }
         return true;
     });
-    if (kOp == kGradW && lane == 0) bulk_wait_read<0>();
     __syncwarp();
     return ok;
 }
@@ -1201,8 +1205,7 @@ int launch_grouped_grad_w(const GroupedGradWLaunch &L) {
     if (!make_tensor_map(&a.a, L.grad, false, L.num_rows, L.out_features, kDepth) ||
         !make_tensor_map(&a.b, L.x, false, L.num_rows, L.in_features, kDepth) ||
         !make_tensor_map(&a.a16, L.grad, false, L.num_rows, L.out_features, 16) ||
-        !make_tensor_map(&a.b16, L.x, false, L.num_rows, L.in_features, 16) ||
-        !make_tensor_map3(&a.out_map, L.out, (int)cell, L.num_experts, L.out_features, L.in_features, 32))
+        !make_tensor_map(&a.b16, L.x, false, L.num_rows, L.in_features, 16))
         return MOE_ERR_CUDA;
     a.prefix = L.expert_prefix;
     a.out = L.out;
