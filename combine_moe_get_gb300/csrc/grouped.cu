@@ -64,7 +64,7 @@ struct Tile {
 
 struct Args {
     CUtensorMap a, b;
-    CUtensorMap a16, b16;               // weights' gradients: operands 16 rows at a time
+    CUtensorMap a16, b16, out_map;      // weights' gradients: operands 16 rows at a time, the result in bf16
     const int32_t *prefix;
     const float *a_scales, *b_scales;   // E4M3: [E, N, K/128] and [M, K/128]
     void *out;
@@ -647,15 +647,43 @@ __device__ __forceinline__ void store_rows(const Args &a, const Tile &t, int f, 
     }
 }
 
-// A warp's 32 rows x 128 bytes of a weight's gradient, through shared memory so that eight lanes write 128 bytes of a row.
-// Lanes that stored 16 bytes each to rows of their own took 1660 us where TMA tiles took 1150 (16384 rows, 32 experts, 7168 x
-// 4096, fp32; with the other steps those took 850, for 3.8 GB written). But the tiles' rows kept TMA from the loads: 190
-// cycles to issue one, 6000 a tile whose products take 4100.
+// A warp's 32 rows x 128 bytes of a weight's gradient, through shared memory. (Lanes that stored 16 bytes each to rows of
+// their own took 1660 us where this took 1150: 16384 rows, 32 experts, 7168 x 4096, fp32.) fp32 goes out by stores of eight
+// lanes to 128 bytes of a row: as TMA tiles, twice bf16's, it keeps TMA from the loads, where issuing one takes 190 cycles,
+// 6000 a tile whose products take 4100. bf16 goes out as TMA tiles, which the warps need not wait for. us, stores / TMA: fp32,
+// 32 experts of some 512 rows 787 / 853, of some 128 615 / 673, adding to 512 1467 / 1490; bf16 629 / 644, 383 / 312, 930 / 863.
+// What a bf16 gradient holds is added in registers, to be rounded once: `before`, asked for as early as the tile is known,
+// goes through the same place. (fp32 is added in L2.)
+struct Rows {   // 16 bytes of every fourth of 32 rows, from lane / 8
+    uint4 v[8];
+};
 template <typename Out>
+__device__ __forceinline__ Out *rows_at(const Args &a, const Tile &t, int f0, int col) {
+    const int lane = threadIdx.x & 31;
+    return static_cast<Out *>(a.out) + ((size_t)t.e * a.features + f0 + lane / 8) * a.depth + t.c0 + col + (lane & 7) * (int)(16 / sizeof(Out));
+}
+__device__ __forceinline__ void load_rows(const Args &a, const Tile &t, int f0, int col, Rows &rows) {
+    const int lane = threadIdx.x & 31;
+    const __nv_bfloat16 *from = rows_at<__nv_bfloat16>(a, t, f0, col);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        rows.v[i] = col + (lane & 7) * 8 < t.n && f0 + i * 4 + lane / 8 < a.features
+                        ? *reinterpret_cast<const uint4 *>(from + (size_t)i * 4 * a.depth)
+                        : uint4{};
+}
+template <typename Out, bool kAdd>
 __device__ __forceinline__ void store_weights(const Args &a, const Tile &t, int f0, int col, const float (&v)[128 / sizeof(Out)],
-                                              char *buffer) {
+                                              const Rows &before, char *buffer) {
     const int lane = threadIdx.x & 31, piece = lane & 7, row = lane / 8;
+    const auto place = [&](int r, int p) { return reinterpret_cast<uint4 *>(buffer + r * 128 + ((p ^ (r & 7)) * 16)); };
+    constexpr bool kTma = sizeof(Out) == 2, add = kAdd && kTma;
+    if (kTma && lane == 0) bulk_wait_read<0>();
     __syncwarp();   // the last ones have been read
+    if constexpr (add) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *place(i * 4 + row, piece) = before.v[i];
+        __syncwarp();
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         uint4 x;
@@ -663,45 +691,40 @@ __device__ __forceinline__ void store_weights(const Args &a, const Tile &t, int 
             x = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
                            __float_as_uint(v[4 * i + 3]));
         } else {
+            if constexpr (add) x = *place(lane, i);
             __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&x);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = __floats2bfloat162_rn(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+            for (int j = 0; j < 4; ++j) {
+                const float2 y = add ? __bfloat1622float2(h[j]) : make_float2(0.0f, 0.0f);
+                h[j] = __floats2bfloat162_rn(v[8 * i + 2 * j] + y.x, v[8 * i + 2 * j + 1] + y.y);
+            }
         }
-        *reinterpret_cast<uint4 *>(buffer + lane * 128 + ((i ^ (lane & 7)) * 16)) = x;
+        *place(lane, i) = x;
     }
-    __syncwarp();
-    const int c = col + piece * (int)(16 / sizeof(Out));
-    if (c >= t.n) return;
-    Out *out = static_cast<Out *>(a.out) + ((size_t)t.e * a.features + f0 + row) * a.depth + t.c0 + c;
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(buffer + (i + row) * 128 + ((piece ^ ((i + row) & 7)) * 16));
-        if (f0 + i + row < a.features) {
-            uint4 *to = reinterpret_cast<uint4 *>(out + (size_t)i * a.depth);
-            if (sizeof(Out) == 4 && a.accumulate)
-                asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};"
-                             ::"l"(to), "f"(__uint_as_float(x.x)), "f"(__uint_as_float(x.y)), "f"(__uint_as_float(x.z)),
-                               "f"(__uint_as_float(x.w)) : "memory");
-            else
-                *to = x;
+    if constexpr (kTma) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                         ::"l"(&a.out_map), "r"(t.c0 + col), "r"(f0), "r"(t.e), "r"(smem_addr(buffer)) : "memory");
+            bulk_commit();
         }
-    }
-}
-
-// bf16 that is added to is read into registers, so that the sum is rounded once.
-__device__ __forceinline__ void add_weights(const Args &a, const Tile &t, int f, int col, float (&v)[64]) {
-    if (f >= a.features) return;
-    const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.out) +
-                                                        ((size_t)t.e * a.features + f) * a.depth + t.c0 + col);
+    } else {
+        __syncwarp();
+        if (col + piece * 4 >= t.n) return;
+        float *out = rows_at<float>(a, t, f0, col);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (col + 8 * i >= t.n) break;   // sizes are multiples of 8
-        const uint4 x = from[i];
-        const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&x);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 y = __bfloat1622float2(h[j]);
-            v[8 * i + 2 * j] += y.x, v[8 * i + 2 * j + 1] += y.y;
+        for (int i = 0; i < 32; i += 4) {
+            const uint4 x = *place(i + row, piece);
+            if (f0 + i + row < a.features) {
+                uint4 *to = reinterpret_cast<uint4 *>(out + (size_t)i * a.depth);
+                if constexpr (kAdd)
+                    asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};"
+                                 ::"l"(to), "f"(__uint_as_float(x.x)), "f"(__uint_as_float(x.y)), "f"(__uint_as_float(x.z)),
+                                   "f"(__uint_as_float(x.w)) : "memory");
+                else
+                    *to = x;
+            }
         }
     }
 }
@@ -877,6 +900,10 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
             }
         } else {
             const bool some = t.blocks > 0;
+            Rows before;
+            if constexpr (kOp == kGradW && sizeof(Out) == 2)
+                if (some && a.accumulate && a.split == 1)
+                    load_rows(a, t, t.a0 + (int)rank * kRows + q * 32, side * 64, before);
             if (some && !warp_wait(&c.sums_full[sums.slot], sums.round, a.limits.wait_ns)) return false;
             tc_fence_after();
             if (a.split > 1) {
@@ -910,9 +937,12 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
                         tmem_load_wait(v);
                     }
                     if (f0 >= a.features || (!some && a.accumulate)) continue;
-                    if constexpr (sizeof(Out) == 2)
-                        if (a.accumulate) add_weights(a, t, f, col, v);
-                    store_weights<Out>(a, t, f0, col, v, buffer);
+                    if (a.accumulate) {
+                        store_weights<Out, true>(a, t, f0, col, v, before, buffer);
+                        if (sizeof(Out) == 2 && col + C::kSides * kWide < t.n) load_rows(a, t, f0, col + C::kSides * kWide, before);
+                    } else {
+                        store_weights<Out, false>(a, t, f0, col, v, before, buffer);
+                    }
                 }
             } else {
                 for (int col = side * 16; col < t.n; col += kStep) {
@@ -931,6 +961,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
         }
         return true;
     });
+    if (kOp == kGradW && sizeof(Out) == 2 && lane == 0) bulk_wait_read<0>();
     __syncwarp();
     return ok;
 }
@@ -1205,7 +1236,8 @@ int launch_grouped_grad_w(const GroupedGradWLaunch &L) {
     if (!make_tensor_map(&a.a, L.grad, false, L.num_rows, L.out_features, kDepth) ||
         !make_tensor_map(&a.b, L.x, false, L.num_rows, L.in_features, kDepth) ||
         !make_tensor_map(&a.a16, L.grad, false, L.num_rows, L.out_features, 16) ||
-        !make_tensor_map(&a.b16, L.x, false, L.num_rows, L.in_features, 16))
+        !make_tensor_map(&a.b16, L.x, false, L.num_rows, L.in_features, 16) ||
+        (cell == 2 && !make_tensor_map3(&a.out_map, L.out, 2, L.num_experts, L.out_features, L.in_features, 32)))
         return MOE_ERR_CUDA;
     a.prefix = L.expert_prefix;
     a.out = L.out;

@@ -13,7 +13,7 @@ namespace moe {
 
 // ------------------------------------------------------------------ tensor maps (host)
 
-// Map of `sets` row-major matrices [rows, cols] of `cell` bytes an element (1, 2: bf16, 4: fp32),
+// Map of `sets` row-major matrices [rows, cols] of `cell` bytes an element (1, or 2: bf16),
 // one behind another, whose tiles are [box_rows, box_cols], box_cols covering 128 bytes, laid out
 // in shared memory with the 128-byte swizzle. Coordinates are (col, row, set), or (col, row) where
 // sets is 0. Elements outside a matrix read as 0 and are not written. False if the driver refuses.
@@ -32,9 +32,7 @@ inline bool make_tensor_map3(CUtensorMap *map, const void *base, int cell, uint6
     const cuuint64_t size = (cuuint64_t)cell;
     const cuuint64_t dims[3] = {cols, rows, sets}, strides[2] = {cols * size, rows * cols * size};
     const cuuint32_t box[3] = {(cuuint32_t)(128 / size), box_rows, 1}, step[3] = {1, 1, 1};
-    const CUtensorMapDataType type = cell == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                     : cell == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                                 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    const CUtensorMapDataType type = cell == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     return encode(map, type, sets ? 3 : 2, const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
