@@ -3,7 +3,7 @@
 //
 //   forward     y[r]  = w[e] x[r]                 D = 128 features of w[e] x n rows, over K
 //   gradient    dx[r] = w[e]^T dy[r]              D = 128 columns of w[e] x n rows, over N
-//   of weights  dw[e] = sum over r of dy[r] x[r]^T   D = 128 rows of dw[e] x 256 columns, over the expert's rows
+//   of weights  dw[e] = sum over r of dy[r] x[r]^T   D = 128 rows of dw[e] x up to 256 columns, over the expert's rows
 //
 // The ragged side is the tensor core's n, which goes in steps of 16, so that an
 // expert with 140 rows costs 144 and not 256; features fill its fixed 128 rows,
@@ -1116,9 +1116,9 @@ int launch_rows(Args &a, int split, cudaStream_t s) {
 // four (eight) to a tile's reduction, in a cluster: whichever an estimate finds faster, from rows that are spread evenly.
 // A block takes the tensor core 2 n cycles and its loads a cycle for 64 bytes (70 for single CTAs); a tile's ends cost
 // some 2000 cycles and a shared tile's exchange 1000 and 55 a column. Captured calls, us, launch and flush (7) included, as
-// pairs / 2 / 4 of them / single / 2 / 4 / 8: 100 rows, 7168 x 512: 34 / 27 / 22 / 36 / 28 / 22 / 20; 4 x 32 rows, 7168 x 512:
-// 32 / 24 / 20 / 34 / 26 / 20 / 26; 2048 rows, 7168 x 512: 40 / 34 / 48 / 38 / 30 / 40 / 71; 2 x 700 rows, 4096 x 1024:
-// 30 / 30 / 42 / 26 / 38 / 44 / 81; 8 x 128 rows, 2048 x 2048: 24 / 38 / 67 / 29 / 44 / 61 / 122.
+// pairs / 2 / 4 of them / single / 2 / 4 / 8: 100 rows, 7168 x 512: 34 / 26 / 22 / 36 / 28 / 22 / 20; 4 x 32 rows, 7168 x 512:
+// 32 / 26 / 20 / 34 / 26 / 20 / 28; 2048 rows, 7168 x 512: 40 / 36 / 48 / 36 / 30 / 40 / 73; 2 x 700 rows, 4096 x 1024:
+// 30 / 30 / 44 / 26 / 40 / 46 / 84; 8 x 128 rows, 2048 x 2048: 24 / 38 / 67 / 28 / 44 / 63 / 128.
 struct Way {
     bool pair;
     int split;

@@ -8,7 +8,7 @@
 // (kVec times 8 channels each) between the sum of squares and the output. The sums
 // are fp32; h enters them unrounded, and is rounded to bf16 only where it is stored.
 // 4096 x 7168 with a residual, to bf16: 36 us (6.5 TB/s); 16384 x 7168 to E4M3: 136
-// (6.1 TB/s); the gradient of 4096 x 7168 47 (5.0 TB/s).
+// (6.1 TB/s); the gradient of 4096 x 7168 45 (5.2 TB/s).
 #include "rows.cuh"
 
 namespace moe {
@@ -156,7 +156,7 @@ struct RowRing {
 
 // The CTA's groups of `row_warps` warps take rows in turn, and keep the weight's gradient of their columns in registers;
 // at the end the groups' sums are added up in shared memory, in order. Rows come through rings in shared memory, as
-// many ahead as it holds. 4096 x 7168: 47 us, the weight's sums included (5.0 TB/s); with loads into registers, one row
+// many ahead as it holds. 4096 x 7168: 45 us, the weight's sums included (5.2 TB/s); with loads into registers, one row
 // ahead, 81; one vector a thread 54.
 template <int kVec>
 __global__ __launch_bounds__(backward_warps(kVec) * 32) void norm_backward_kernel(const __grid_constant__ NormArgs a) {
