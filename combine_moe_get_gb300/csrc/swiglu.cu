@@ -5,10 +5,11 @@
 //
 // One pass over the rows, bound by HBM. A warp takes 256 channels of a row: 16 bytes
 // of gate and of up a lane, so that 16 lanes hold a block of 128 and its largest
-// magnitude takes four shuffles. 32768 x 2048: 62 us to bf16 (6.5 TB/s), 62 to E4M3
-// (5.5 TB/s: the exponentials, reciprocals and codes take as long as the bytes);
-// the gradient 107 (6.3 TB/s). Four pieces to a warp, loaded at once, were no faster
-// than one, and slower in small calls.
+// magnitude takes four shuffles. 32768 x 2048: 62 us to bf16 (6.5 TB/s), 54 to E4M3
+// (6.3 TB/s; 60 with one element to an instruction and as many registers as the
+// compiler takes, 40, which leaves out a quarter of the warps); the gradient 107
+// (6.3 TB/s). Four pieces to a warp, loaded at once, were no faster than one, and
+// slower in small calls; the next piece's loads ahead of this one's sums were slower.
 #include "rows.cuh"
 
 namespace moe {
@@ -38,8 +39,36 @@ __device__ __forceinline__ int rows_in_use(const SwigluArgs &a) {
     return cut;
 }
 
-// exp and the quotient are the fast ones, off by some 2^-21 of the sigmoid: an eighth of an E4M3 or bf16 rounding's 2^-9 at most
-__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+// Two fp32 to an instruction.
+struct Two {
+    uint64_t v;
+    __device__ Two(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ explicit Two(float a) : Two(a, a) {}
+    __device__ void parts(float &a, float &b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+    asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+    return a;
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    asm("add.rn.f32x2 %0, %0, %1;" : "+l"(a.v) : "l"(b.v));
+    return a;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a.v) : "l"(b.v), "l"(c.v));
+    return a;
+}
+// exp and the reciprocal are the fast ones, off by some 2^-21 of the sigmoid: an eighth of an E4M3 or bf16 rounding's 2^-9 at most
+__device__ __forceinline__ Two sigmoid(Two z) {
+    float a, b;
+    (z * Two(-1.4426950408889634f)).parts(a, b);   // log2(e)
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+    (Two(a, b) + Two(1.0f)).parts(a, b);
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+    return Two(a, b);
+}
 
 // Pieces of 256 channels in order, a warp's own `step` apart, without a division for each.
 struct Pieces {
@@ -57,7 +86,7 @@ struct Pieces {
 };
 
 template <bool kE4m3>
-__global__ __launch_bounds__(kThreads) void swiglu_kernel(const __grid_constant__ SwigluArgs a) {
+__global__ __launch_bounds__(kThreads, 8) void swiglu_kernel(const __grid_constant__ SwigluArgs a) {
     const WarpTrace trace(a.trace, MOE_TRACE_SWIGLU);
     grid_dependency_wait();
     grid_launch_dependents();
@@ -80,7 +109,10 @@ __global__ __launch_bounds__(kThreads) void swiglu_kernel(const __grid_constant_
         widen(g, z);
         widen(u, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= z[i] * sigmoid(z[i]) * w;
+        for (int i = 0; i < 8; i += 2) {
+            const Two gate(z[i], z[i + 1]);
+            (gate * sigmoid(gate) * Two(w) * Two(v[i], v[i + 1])).parts(v[i], v[i + 1]);
+        }
         if constexpr (kE4m3) {   // I is a multiple of 128: 16 lanes are in it or not
             uint2 codes;
             const float scale = quantise(v, codes);
@@ -99,20 +131,23 @@ struct Gradients {
 };
 // Of eight channels; returns their part of the row weight's gradient.
 __device__ __forceinline__ float gradients(const uint4 &g4, const uint4 &u4, const uint4 &d4, float w, Gradients &out) {
-    float z[8], v[8], d[8], sum = 0.0f;
+    float z[8], v[8], d[8];
     widen(g4, z);
     widen(u4, v);
     widen(d4, d);
+    Two sum(0.0f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float s = sigmoid(z[i]), silu = z[i] * s, up = v[i], dh = d[i] * w;
-        sum = fmaf(d[i], silu * up, sum);
-        v[i] = dh * silu;
-        z[i] = dh * up * s * fmaf(z[i], 1.0f - s, 1.0f);
+    for (int i = 0; i < 8; i += 2) {
+        const Two gate(z[i], z[i + 1]), up(v[i], v[i + 1]), dh(d[i], d[i + 1]), s = sigmoid(gate), silu = gate * s, wdh = dh * Two(w);
+        sum = fma2(dh, silu * up, sum);
+        (wdh * silu).parts(v[i], v[i + 1]);
+        (wdh * up * s * fma2(gate, fma2(s, Two(-1.0f), Two(1.0f)), Two(1.0f))).parts(z[i], z[i + 1]);
     }
     out.gate = narrow(z);
     out.up = narrow(v);
-    return sum;
+    float even, odd;
+    sum.parts(even, odd);
+    return even + odd;
 }
 
 // `row_warps` warps to a row, up to kUnroll times 8 channels a thread at once; a row's sum of the weight's gradient is
