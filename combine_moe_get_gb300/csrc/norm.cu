@@ -7,8 +7,8 @@
 // One pass over the rows, bound by HBM: a row stays in the registers of its threads
 // (kVec times 8 channels each) between the sum of squares and the output. The sums
 // are fp32; h enters them unrounded, and is rounded to bf16 only where it is stored.
-// 4096 x 7168 with a residual, to bf16: 36 us (6.5 TB/s); 16384 x 7168 to E4M3: 136
-// (6.1 TB/s); the gradient of 4096 x 7168 45 (5.2 TB/s).
+// 4096 x 7168 with a residual, to bf16: 36 us (6.5 TB/s); 16384 x 7168 to E4M3: 127
+// (6.5 TB/s); the gradient of 4096 x 7168 45 (5.2 TB/s).
 #include "rows.cuh"
 
 namespace moe {
@@ -44,32 +44,47 @@ __device__ __forceinline__ void load_weight(const NormArgs &a, int col, float (&
     }
 }
 
-// Sums of N values over the warps of this thread's row, in a fixed order. `place` alternates from call to call, so
-// that one barrier is enough. Every thread of the CTA calls it.
-template <int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float (*space)[kMaxWarps], int row_warps) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-    if (row_warps == 1) return;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, first = warp / row_warps * row_warps;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (lane == 0) space[i][warp] = v[i];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        v[i] = lane < row_warps ? space[i][first + lane] : 0.0f;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+// Sum over a row of what its threads have, v[j] for its vectors j * row_warps * 32 + thread: over the lanes of each 32
+// vectors, then over those, so that equal rows have equal bits whichever way they are laid out over warps. `first` is the
+// row's place in `space`. Every thread of the CTA calls it.
+template <int kVec>
+__device__ __forceinline__ float row_sum(const float (&v)[kVec], float *space, int first, int row_warps) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x / 32 % row_warps;
+    float sum;
+    int o = 16;
+    if constexpr (kVec == 4) {   // halves of a warp take two of the four on, quarters one
+        const bool upper = lane & 16, odd = lane & 8;
+        const float a = (upper ? v[2] : v[0]) + __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[2], 16);
+        const float b = (upper ? v[3] : v[1]) + __shfl_xor_sync(0xffffffffu, upper ? v[1] : v[3], 16);
+        sum = (odd ? b : a) + __shfl_xor_sync(0xffffffffu, odd ? a : b, 8);
+        o = 4;
+    } else if constexpr (kVec == 2) {
+        const bool upper = lane & 16;
+        sum = (upper ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, upper ? v[0] : v[1], 16);
+        o = 8;
+    } else {
+        sum = v[0];
     }
+#pragma unroll
+    for (; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const int n = row_warps * kVec;
+    if (n == 1) return sum;
+    constexpr int kShare = 32 / kVec;
+    if (lane % kShare == 0) space[first + lane / kShare * row_warps + warp] = sum;
+    __syncthreads();
+    sum = lane < n ? space[first + lane] : 0.0f;
+    if (kVec == 4 && lane + 32 < n) sum += space[first + lane + 32];
+#pragma unroll
+    for (o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
 }
 
+// Registers, for as many rows at once: 40 for two vectors (with 42 a third row of 14 warps does not fit beside two: 4096 x 7168 to
+// both types takes 55 us, not 47), 64 for four (86: 16384 x 7168 to E4M3 194 us, not 134).
 template <int kVec, bool kCodes>
-__global__ __launch_bounds__(512) void norm_kernel(const __grid_constant__ NormArgs a) {
+__global__ __launch_bounds__(512, kVec == 4 ? 2 : 3) void norm_kernel(const __grid_constant__ NormArgs a) {
     const WarpTrace trace(a.trace, MOE_TRACE_NORM);
-    __shared__ float space[1][kMaxWarps];
+    __shared__ float space[64];   // a value for 256 channels of each row
     grid_dependency_wait();
     grid_launch_dependents();
     const int threads = a.row_warps * 32, sub = threadIdx.x / threads, tid = threadIdx.x - sub * threads;
@@ -86,7 +101,7 @@ __global__ __launch_bounds__(512) void norm_kernel(const __grid_constant__ NormA
             if (a.residual) res[j] = load_once(a.residual + base + col);
         }
     }
-    float h[kVec][8], sum[1] = {};
+    float h[kVec][8], sums[kVec] = {};
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
         widen(x[j], h[j]);
@@ -99,10 +114,9 @@ __global__ __launch_bounds__(512) void norm_kernel(const __grid_constant__ NormA
             if (a.residual_out && live && col < a.H) *reinterpret_cast<uint4 *>(a.residual_out + base + col) = narrow(h[j]);
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum[0] = fmaf(h[j][i], h[j][i], sum[0]);
+        for (int i = 0; i < 8; ++i) sums[j] = fmaf(h[j][i], h[j][i], sums[j]);
     }
-    row_sums(sum, space, a.row_warps);
-    const float r = rsqrtf(sum[0] / a.H + a.eps);
+    const float r = rsqrtf(row_sum(sums, space, sub * a.row_warps * kVec, a.row_warps) / a.H + a.eps);
 #pragma unroll
     for (int j = 0; j < kVec; ++j) {
         const int col = (j * threads + tid) * 8;
@@ -340,7 +354,10 @@ int launch_norm(const NormLaunch &L) {
     a.trace = trace_args();
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
     cudaError_t e;
-    switch (vectors(a.H, 16)) {
+    // Fewer warps with more of a row each, where that keeps enough of them at work. us (7 of them the launch's), at most 8
+    // warps / 16: 4096 channels, 16384 rows to E4M3 85 / 95, to bf16 85 / 91, 128 rows 9.4 / 9.4; 7168 channels to E4M3 alone
+    // 134 / 143, 4096 rows 42 / 44; but with bf16 rows 4096 rows 50 / 48, 128 rows 11.4 / 9.4.
+    switch (vectors(a.H, a.H <= 4096 || (a.H <= 8192 && !a.out) ? 8 : 16)) {
         case 1: e = launch_forward<1>(a, s); break;
         case 2: e = launch_forward<2>(a, s); break;
         default: e = launch_forward<4>(a, s); break;
