@@ -45,7 +45,6 @@ constexpr int kTileA = kRows * 128;        // bytes of A in a stage
 constexpr int kTileSlots = 4;              // tiles found ahead
 constexpr int kSmemBudget = 226 << 10;     // ring, what stands beside it, and 1 KB to align them
 constexpr int kScaleSlots = 2;             // E4M3: scales of four blocks each
-constexpr int kStoreBytes = 32 * 128;      // weights' gradients: 32 rows of a warp on their way out
 constexpr int kBoxRows = 32;               // rows of one copy of the ragged operand
 constexpr int kDepth = 64;                 // bf16 elements of a block along the reduction (E4M3: 128)
 constexpr int kRowGroup = 8;               // row tiles that share a pass over the features
@@ -90,7 +89,9 @@ struct Config {
     static constexpr int kTileB = (kCols / kCtas + kBoxRows - 1) / kBoxRows * kBoxRows * 128;
     static constexpr int kSums = kE4m3 ? (512 / kCols < 4 ? 512 / kCols : 4) : 2;
     static constexpr int kScales = kCols + kRows;   // E4M3: scales of a block's rows and features
-    static constexpr int kBeside = kE4m3 ? kScaleSlots * 4 * kScales * 4 : kOp == kGradW ? kReaders * kStoreBytes : 0;
+    static constexpr int kScaleBytes = kE4m3 ? kScaleSlots * 4 * kScales * 4 : 0;
+    static constexpr int kStore = kE4m3 ? 16 * 64 : kOp == kGradW ? 32 * 128 : 0;   // what a warp of readers has on its way out
+    static constexpr int kBeside = kScaleBytes + kReaders * kStore;
     static constexpr int kFit = (kSmemBudget - 1024 - kBeside) / (kTileA + kTileB);
     static constexpr int kStages = kFit < 12 ? kFit : 12;
     static constexpr int kTmemCols = kSums * kCols <= 64 ? 64 : kSums * kCols <= 128 ? 128 : kSums * kCols <= 256 ? 256 : 512;
@@ -618,17 +619,32 @@ __device__ __forceinline__ void add_block(float (*sum)[16], uint32_t from, const
     }
 }
 
-// Neighbouring features, held four lanes apart, come together for one store.
-__device__ __forceinline__ void store_fragments(const Args &a, const Tile &t, int f0, int col, const float (&sum)[16]) {
-    const int lane = threadIdx.x & 31, odd = lane >> 2 & 1;
+// 32 features of 16 columns leave through shared memory, transposed on the way in, so that a lane writes eight features of a
+// row and four lanes its 64 bytes. Pieces of 16 bytes lie where neither side meets itself in a bank.
+__device__ __forceinline__ void store_fragments(const Args &a, const Tile &t, int f0, int col, const float (&sum)[16], char *buffer) {
+    const int lane = threadIdx.x & 31;
+    const auto place = [](int column, int piece) { return column * 64 + ((piece ^ (column >> 1 & 3)) * 16); };
+    __syncwarp();   // the last columns have been read
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float x = sum[2 * j], y = sum[2 * j + 1];
-        const float got = __shfl_xor_sync(0xffffffffu, odd ? x : y, 4);
-        const __nv_bfloat162 pair = odd ? __floats2bfloat162_rn(got, y) : __floats2bfloat162_rn(x, got);
-        const int f = f0 + j / 4 * 16 + j % 2 * 8 + (lane >> 3) * 2, c = col + j / 2 % 2 * 8 + (lane & 3) * 2 + odd;
-        if (f < a.features && c < t.n)
-            *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + (size_t)(t.row0 + c) * a.features + f) = pair;
+    for (int g = 0; g < 2; ++g) {
+        uint32_t pair[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {   // features 8 m to 8 m + 7, 2 h + p = m
+            const __nv_bfloat162 b = __floats2bfloat162_rn(sum[8 * (m / 2) + 4 * g + 2 * (m % 2)], sum[8 * (m / 2) + 4 * g + 2 * (m % 2) + 1]);
+            pair[m] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};"
+                     ::"r"(smem_addr(buffer + place(8 * g + lane % 8, lane / 8))), "r"(pair[0]), "r"(pair[1]), "r"(pair[2]), "r"(pair[3])
+                     : "memory");
+    }
+    __syncwarp();
+    const int f = f0 + lane % 4 * 8;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int column = half * 8 + lane / 4;
+        if (f < a.features && col + column < t.n)
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + (size_t)(t.row0 + col + column) * a.features + f) =
+                *reinterpret_cast<const uint4 *>(buffer + place(column, lane % 4));
     }
 }
 
@@ -840,7 +856,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
     Ring sums(C::kSums), fours(kScaleSlots);
     constexpr int kStep = 16 * C::kSides, kChunks = (kCols + kStep - 1) / kStep;
     const float *scales = reinterpret_cast<const float *>(beside);
-    char *const buffer = beside + (warp - kFirstReader) * kStoreBytes;
+    char *const buffer = beside + C::kScaleBytes + (warp - kFirstReader) * C::kStore;
     const bool ok = each_tile(a, c, [&](const Tile &t) {
         const int f = t.a0 + (int)rank * kRows + q * 32 + lane;
         if constexpr (C::kE4m3) {
@@ -896,7 +912,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
 #pragma unroll
             for (int i = 0; i < kChunks; ++i) {
                 const int col = i * kStep + side * 16;
-                if (col < t.n) store_fragments(a, t, t.a0 + (int)rank * kRows + q * 32, col, sum[i]);
+                if (col < t.n) store_fragments(a, t, t.a0 + (int)rank * kRows + q * 32, col, sum[i], buffer);
             }
         } else {
             const bool some = t.blocks > 0;
