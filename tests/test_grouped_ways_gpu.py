@@ -142,6 +142,47 @@ def test_weights_shared(moe, name, dtype):
         close(again[e], want + s, size + s.abs(), rows + 1, half)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+def test_shared_weights_follow_the_prefix(moe, dtype):
+    """One capture of a shared gradient serves rows for one expert, for all, for none, and a prefix with a bad end."""
+    _, prefix, x, g = weights_operands("uneven experts")
+    E, M, status = prefix.numel() - 1, x.shape[0], moe.new_status()
+    out = torch.empty(E, g.shape[1], x.shape[1], dtype=dtype, device=DEV)
+    call = lambda: moe.moe_grouped_linear_grad_w(g, x, prefix, out=out, accumulate=False, status=status)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    half = 2.0 ** -24 if dtype == torch.float32 else 2.0 ** -8
+    for p in ([0, M, M, M, M], [0, 1, 2, 3, 4], [M] * 5, [0, 63, 128, 2000, M], [0, 5, 5, 5, M]):
+        prefix.copy_(torch.tensor(p, dtype=torch.int32))
+        out.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        for e in range(E):
+            xe, ge = x[p[e]: p[e + 1]].double(), g[p[e]: p[e + 1]].double()
+            close(out[e], ge.T @ xe, ge.abs().T @ xe.abs(), max(1, p[e + 1] - p[e]), half)
+    moe.check_status(status)
+    prefix[-1] = M + 1
+    graph.replay()
+    assert int(status.item()) == moe.MOE_ERR_BAD_PREFIX
+
+
+def test_shared_weights_at_once(moe):
+    calls = []
+    for name in WEIGHTS:
+        _, prefix, x, g = weights_operands(name)
+        calls.append(lambda x=x, g=g, prefix=prefix, **kw: moe.moe_grouped_linear_grad_w(g, x, prefix, **kw))
+    want = [c() for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [c(stream=s) for c, s in zip(calls, streams)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_e4m3_scales_far_apart(moe):
     """Blocks whose scales differ by 2^40, and scales at no 16-byte boundary."""
     gen = torch.Generator(DEV).manual_seed(9)
