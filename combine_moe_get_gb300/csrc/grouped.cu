@@ -145,6 +145,12 @@ __device__ __forceinline__ void arrive_expect_at(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, uint64_t ns) {
     return mbar_wait_bounded(bar, parity, ns);
 }
+__device__ __forceinline__ bool arrived(uint64_t *bar, uint32_t parity) {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(yes) : "r"(smem_addr(bar)), "r"(parity) : "memory");
+    return yes != 0;
+}
 // By a whole warp, which goes on or gives up as one. What is waited for has often happened: the rest stays out of the
 // way of the code around (E4M3's readers were 4% slower with it in each place).
 __device__ __noinline__ bool warp_wait_longer(uint64_t *bar, uint32_t parity, uint64_t ns) {
@@ -582,14 +588,11 @@ __device__ bool load_scales(const Args &a, Control &c, float *scales, uint32_t r
 // loads from shared memory were 60% of the time.
 __device__ __forceinline__ void tmem_load_fragments(uint32_t addr, float (&v)[16]) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t r[8];
+    for (int h = 0; h < 2; ++h)
         asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "=f"(v[8 * h]), "=f"(v[8 * h + 1]), "=f"(v[8 * h + 2]), "=f"(v[8 * h + 3]), "=f"(v[8 * h + 4]),
+                       "=f"(v[8 * h + 5]), "=f"(v[8 * h + 6]), "=f"(v[8 * h + 7])
                      : "r"(addr + ((uint32_t)(16 * h) << 16)));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[8 * h + i] = __uint_as_float(r[i]);
-    }
 }
 // Two columns to an instruction: a multiplication and an addition for each pair of sums, as fast as two of each but half
 // the instructions, which are what the readers run out of.
@@ -605,9 +608,9 @@ __device__ __forceinline__ void scaled_add(float (&sum)[16], const float (&v)[16
             : "f"(v[2 * j]), "f"(v[2 * j + 1]), "f"(c.x), "f"(c.y), "f"(features[j / 4 * 2 + j % 2]));
     }
 }
-// One block's sums, kN times 16 columns kStep apart.
-template <int kN, int kStep>
-__device__ __forceinline__ void add_block(float (*sum)[16], uint32_t from, const float *sx, const float (&features)[4]) {
+// One block's sums, kN times 16 columns kStep apart; `read` comes when the last have been read, before they are added.
+template <int kN, int kStep, class Read>
+__device__ __forceinline__ void add_block(float (*sum)[16], uint32_t from, const float *sx, const float (&features)[4], Read read) {
 #pragma unroll
     for (int i = 0; i < kN; ++i) {
         float v[16];
@@ -615,8 +618,10 @@ __device__ __forceinline__ void add_block(float (*sum)[16], uint32_t from, const
         const float2 columns[2] = {*reinterpret_cast<const float2 *>(sx + i * kStep),
                                    *reinterpret_cast<const float2 *>(sx + i * kStep + 8)};
         tmem_load_wait(v);
+        if (i == kN - 1) read();
         scaled_add(sum[i], v, columns, features);
     }
+    if (kN == 0) read();
 }
 
 // 32 features of 16 columns leave through shared memory, transposed on the way in, so that a lane writes eight features of a
@@ -855,6 +860,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
     const int tid = threadIdx.x - kFirstReader * 32;
     const uint32_t lanes = tmem + ((uint32_t)(q * 32) << 16);
     Ring sums(C::kSums), fours(kScaleSlots);
+    bool ready = false;   // E4M3: the next block's sums are there
     constexpr int kStep = 16 * C::kSides, kChunks = (kCols + kStep - 1) / kStep;
     const float *scales = reinterpret_cast<const float *>(beside);
     char *const buffer = beside + C::kScaleBytes + (warp - kFirstReader) * C::kStore;
@@ -875,13 +881,16 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
                         float features[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) features[j] = sx[kCols + q * 32 + j * 8 + lane / 4];
-                        if (!warp_wait(&c.sums_full[sums.slot], sums.round, a.limits.wait_ns)) return false;
+                        if (!ready && !warp_wait(&c.sums_full[sums.slot], sums.round, a.limits.wait_ns)) return false;
                         tc_fence_after();
-                        add_block<kN, kStep>(sum, lanes + sums.slot * kCols + side * 16, sx + side * 16 + (lane & 3) * 2, features);
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) arrive_at(empty + sums.slot * 8);
-                        sums.next();
+                        // the block's place is given back and the next one looked for while the last sums are added: 4% and 2%
+                        add_block<kN, kStep>(sum, lanes + sums.slot * kCols + side * 16, sx + side * 16 + (lane & 3) * 2, features, [&] {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) arrive_at(empty + sums.slot * 8);
+                            sums.next();
+                            ready = __all_sync(0xffffffffu, arrived(&c.sums_full[sums.slot], sums.round));
+                        });
                     }
                     if (lane == 0) mbar_arrive(&c.scales_empty[fours.slot]);   // behind the last block's __syncwarp
                 }
