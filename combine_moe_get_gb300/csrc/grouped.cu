@@ -25,7 +25,7 @@
 // multiplied by the product of their two scales and added: two operations for each of
 // D's elements and block, 128 x n of them while the pair's products take 2 n cycles.
 // That is all that the ordinary cores have to give, so these readers bound E4M3 where
-// rows are many: 1.8 PFLOP/s (the rate without them 3.2, without their
+// rows are many: 1.8 to 1.9 PFLOP/s (the rate without them 3.2, without their
 // arithmetic 2.7), and what helped was fewer instructions and waits around it.
 #include <algorithm>
 #include <atomic>
