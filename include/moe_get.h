@@ -761,7 +761,7 @@ MOE_API int moe_grouped_linear_grad_x(const void *grad, int num_rows, int out_fe
  *
  *   grad_w[e] = sum over r in [expert_prefix[e], expert_prefix[e+1]) of grad[r] x[r]^T
  *
- * summed in fp32 in an order fixed by the number of rows. An expert without rows gets zeros.
+ * summed in fp32 in an order fixed by the sizes and the rows. An expert without rows gets zeros.
  *
  *   grad [M, N], x [M, K] bf16.
  *   grad_type   MOE_GRAD_F32 or MOE_GRAD_BF16: the type of grad_w [E, N, K].
