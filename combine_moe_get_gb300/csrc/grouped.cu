@@ -274,7 +274,7 @@ __device__ __forceinline__ int columns_of(const Tile &t) {
     return kOp == kGradW ? (t.n + kCtas * 64 - 1) / (kCtas * 64) * (kCtas * 64) : round16(t.n);
 }
 
-// Rows of expert e, whatever the prefix holds: inside [0, M], in order.
+// Rows of expert e, whatever the prefix holds: inside [0, M], none where it descends.
 struct Range {
     int lo, hi;
     bool bad;
@@ -341,10 +341,28 @@ __device__ bool find_tiles(const Args &a, Control &c) {
         const int F = a.feature_tiles, kb0 = blockIdx.x / kCtas % a.split * a.per_split;
         const int blocks = min(a.per_split, a.blocks - kb0);
         int64_t before = 0;
+        int end = 0;         // of the rows of the experts before these 32
+        bool bad = false;    // a fault of the prefix so far
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             Range r{};
             if (e0 + lane < a.E) r = rows_of(a, e0 + lane);
             if (r.bad && blockIdx.x == 0) report(a.status, MOE_ERR_BAD_PREFIX);
+            bad = __any_sync(0xffffffffu, r.bad) || bad;
+            if (bad) {   // rows before the end of earlier experts' are theirs: no row has two writers, and none has more
+                         // tiles than most_row_tiles (clusters that share tiles take one each)
+                int most = r.lo < r.hi ? r.hi : 0;   // end of this expert's rows and those before it
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, most, o);
+                    if (lane >= o) most = max(most, y);
+                }
+                const int earlier = __shfl_up_sync(0xffffffffu, most, 1);
+                r.lo = max(r.lo, lane > 0 ? max(end, earlier) : end);
+                r.hi = max(r.hi, r.lo);
+                end = max(end, __shfl_sync(0xffffffffu, most, 31));
+            } else if (const uint32_t some = __ballot_sync(0xffffffffu, r.lo < r.hi)) {
+                end = __shfl_sync(0xffffffffu, r.hi, 31 - __clz(some));
+            }
             const int rows = r.hi - r.lo, R = (rows + kCols - 1) / kCols;
             const int per = R > 1 ? round16((int)quotient(rows + R - 1, R)) : rows;   // row tiles of equal size
             const int64_t mine = (int64_t)R * F;

@@ -726,8 +726,8 @@ MOE_API int moe_adapter_linear(const void *x, int num_tokens, int in_features, c
  * no expert, those of a receive buffer behind the last one among them, are not
  * written, whatever they hold; an expert without rows is not read. Sums are fp32.
  * A prefix outside [0, num_rows] or one that descends raises MOE_ERR_BAD_PREFIX; each
- * expert's rows are cut to those inside, and a row that several experts then claim
- * gets one's product.
+ * expert's rows are then cut to those inside, from the end of the earlier experts' rows
+ * on (none where the prefix descends), and the others are not written.
  *
  *   x              [M, K] bf16, or E4M3 codes (uint8, MOE_WEIGHTS_E4M3) with
  *   x_scales       [M, K/128] fp32, as MOE_DISPATCH_QUANTIZE_FP8 and moe_swiglu make them.
@@ -761,7 +761,8 @@ MOE_API int moe_grouped_linear_grad_x(const void *grad, int num_rows, int out_fe
  *
  *   grad_w[e] = sum over r in [expert_prefix[e], expert_prefix[e+1]) of grad[r] x[r]^T
  *
- * summed in fp32 in an order fixed by the sizes and the rows. An expert without rows gets zeros.
+ * summed in fp32 in an order fixed by the sizes and the rows. An expert without rows gets zeros. With
+ * a prefix that raises MOE_ERR_BAD_PREFIX an expert's sum goes over all its rows inside, others' too.
  *
  *   grad [M, N], x [M, K] bf16.
  *   grad_type   MOE_GRAD_F32 or MOE_GRAD_BF16: the type of grad_w [E, N, K].
