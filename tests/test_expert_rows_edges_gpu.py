@@ -1,4 +1,5 @@
-"""The operators around a dispatch's rows in calls at the edge of what is allowed, or past it: prefixes that descend."""
+"""The operators around a dispatch's rows in calls at the edge of what is allowed, or past it: prefixes that
+descend, and outputs as torch allocates them."""
 from __future__ import annotations
 
 import pytest
@@ -82,3 +83,82 @@ def test_rows_of_a_descending_prefix(moe, name):
         close(gw[e], ge.T @ xe, ge.abs().T @ xe.abs(), max(1, r.stop - r.start), 2.0 ** -24)
     for t in (out, gx) + ((out8,) if x8 is not None else ()):
         assert (t[free.to(DEV)] == 7).all()
+
+
+# ------------------------------------------------------------------ what allocates an output
+
+@pytest.fixture
+def deterministic():
+    torch.use_deterministic_algorithms(True)
+    yield
+    torch.use_deterministic_algorithms(False)
+
+
+def some_rows(gen, M, K, N):
+    """Rows of which the first and last belong to no expert."""
+    prefix = torch.tensor([2, 5, M - 3], dtype=torch.int32, device=DEV)
+    return normal(gen, M, K), normal(gen, 2, N, K), prefix
+
+
+def test_outputs_are_filled_as_torch_fills_them(moe, deterministic):
+    """With deterministic algorithms torch.empty holds NaN: rows that a call does not write show it."""
+    gen = torch.Generator(DEV).manual_seed(22)
+    x, w, prefix = some_rows(gen, 40, 64, 72)
+    free = [0, 1, 37, 38, 39]
+    for dirty in (normal(gen, 40, 72), normal(gen, 40, 64)):   # memory that the allocator gives out again
+        del dirty
+    out = moe.moe_grouped_linear(x, w, prefix)
+    gx = moe.moe_grouped_linear_grad_x(out.nan_to_num(), w, prefix)
+    h, _ = moe.moe_swiglu(x, num_rows=torch.tensor([37], dtype=torch.int32, device=DEV))
+    assert out[free].isnan().all() and out[2:37].isfinite().all()
+    assert gx[free].isnan().all() and gx[2:37].isfinite().all()
+    assert h[37:].isnan().all() and h[:37].isfinite().all()
+    torch.utils.deterministic.fill_uninitialized_memory = False
+    try:
+        assert torch.equal(moe.moe_grouped_linear(x, w, prefix)[2:37], out[2:37])
+    finally:
+        torch.utils.deterministic.fill_uninitialized_memory = True
+
+
+def test_dispatch_modes_see_outputs(moe):
+    from torch.utils._python_dispatch import TorchDispatchMode
+
+    class Seen(TorchDispatchMode):
+        def __init__(self):
+            super().__init__()
+            self.made = []
+
+        def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+            if "empty" in str(func):
+                self.made.append(tuple(args[0]))
+            return func(*args, **(kwargs or {}))
+
+    gen = torch.Generator(DEV).manual_seed(23)
+    x, w, prefix = some_rows(gen, 40, 64, 72)
+    status, logits = moe.new_status(), torch.randn(3, 8, device=DEV, generator=gen)
+    with Seen() as seen:
+        moe.moe_grouped_linear(x, w, prefix, status=status)
+        moe.moe_swiglu(x, status=status)
+        moe.moe_add_rms_norm(x, normal(gen, 64), residual=x, status=status)
+        moe.moe_topk_gate(logits, 2, status=status)
+    assert [s for s in seen.made if s != (64,)] == [(40, 72), (40, 32), (40, 64), (40, 64), (3, 2), (3, 2)]
+
+
+def test_outputs_in_inference_mode(moe):
+    gen = torch.Generator(DEV).manual_seed(24)
+    x, w, prefix = some_rows(gen, 40, 64, 72)
+    with torch.inference_mode():
+        assert moe.moe_grouped_linear(x, w, prefix).is_inference()
+    assert not moe.moe_grouped_linear(x, w, prefix).is_inference()
+
+
+def test_outputs_on_the_given_stream_with_deterministic_algorithms(moe, deterministic):
+    gen = torch.Generator(DEV).manual_seed(25)
+    x, w, prefix = some_rows(gen, 40, 64, 72)
+    want = moe.moe_grouped_linear(x, w, prefix)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):   # the fill goes before the call on the call's stream
+        got = moe.moe_grouped_linear(x, w, prefix, stream=side)
+        side.synchronize()
+        assert torch.equal(got[2:37], want[2:37]) and got[:2].isnan().all()
