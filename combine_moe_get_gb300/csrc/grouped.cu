@@ -1290,6 +1290,9 @@ int launch_grouped_grad_w(const GroupedGradWLaunch &L) {
     a.features = L.out_features, a.depth = L.in_features;
     a.accumulate = L.accumulate;
     a.limits = wait_limits();
+    // One wait may cover all of a tile's reduction (its sums, its last block, the tile after next): 2^22 rows of one expert
+    // take 16 ms, so that 2^30 took four times the limit of 1 s. A limit more for every 2^22 rows.
+    a.limits.wait_ns *= 1 + (uint64_t)(L.num_rows >> 22);
     a.trace = trace_args();
     return L.out_type == MOE_GRAD_F32 ? launch_weights<float>(a, s) : launch_weights<__nv_bfloat16>(a, s);
 }

@@ -1,5 +1,5 @@
 """The operators around a dispatch's rows in calls at the edge of what is allowed, or past it: prefixes that
-descend, and outputs as torch allocates them."""
+descend, outputs as torch allocates them, and sums over so many rows that one wait for them outlasts a short limit."""
 from __future__ import annotations
 
 import pytest
@@ -162,3 +162,25 @@ def test_outputs_on_the_given_stream_with_deterministic_algorithms(moe, determin
         got = moe.moe_grouped_linear(x, w, prefix, stream=side)
         side.synchronize()
         assert torch.equal(got[2:37], want[2:37]) and got[:2].isnan().all()
+
+
+# ------------------------------------------------------------------ long reductions
+
+@pytest.mark.parametrize("dtype", [torch.float32, BF])
+@pytest.mark.parametrize("rows", [2 ** 25, 2 ** 25 - 4])
+def test_a_long_sum_of_one_expert_is_waited_for(moe, dtype, rows):
+    """2^25 rows of one expert among many take some 130 ms; a limit of 40 ms holds for each 2^22 of them. Rows of ones: sums
+    up to 2^24 are whole numbers of 24 bits, beyond that they grow by 16 and at last by 16 or 12, all of them multiples of 4
+    where fp32 holds multiples of 2."""
+    M = 2 ** 25
+    x, g = (torch.ones(M, 8, dtype=BF, device=DEV) for _ in range(2))
+    prefix = torch.zeros(161, dtype=torch.int32, device=DEV)
+    prefix[40:] = rows
+    status = moe.new_status()
+    with moe.test_wait_limits(40_000_000):
+        got = moe.moe_grouped_linear_grad_w(g, x, prefix, dtype=dtype, status=status)
+        torch.cuda.synchronize()
+    moe.check_status(status)
+    want = torch.zeros(160, 8, 8, device=DEV)
+    want[39] = rows
+    assert torch.equal(got, want.to(dtype))
