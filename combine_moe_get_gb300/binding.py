@@ -246,8 +246,9 @@ def status_string(code: int) -> str:
 @contextlib.contextmanager
 def test_wait_limits(wait_timeout_ns: int, withheld_cta: int = -1):
     """For tests: within the context, kernels of moe_experts, moe_layer,
-    moe_adapter_linear and the grouped products give up a wait after ``wait_timeout_ns``, and their CTA
-    ``withheld_cta`` does not announce its first results to the others."""
+    moe_adapter_linear, the grouped products and moe_add_rms_norm_backward give
+    up a wait after ``wait_timeout_ns``, and their CTA ``withheld_cta`` does not
+    announce its first results to the others."""
     _check(LIB.moe_test_wait_limits(wait_timeout_ns, withheld_cta), "moe_test_wait_limits")
     try:
         yield

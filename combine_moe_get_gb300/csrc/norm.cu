@@ -27,7 +27,7 @@ struct NormArgs {
     float *scales;
     float *parts, *grad_weight;          // backward: [parts][H] sums of a CTA's rows each
     int32_t *status;
-    uint64_t wait_ns;
+    WaitLimits limits;
     int stages;
     int T, H, num_parts;
     int row_warps;                       // warps of a row
@@ -137,9 +137,13 @@ __global__ __launch_bounds__(512, kVec == 4 ? 2 : 3) void norm_kernel(const __gr
     }
 }
 
-// Barrier `id` for `threads` of the CTA.
-__device__ __forceinline__ void barrier(int id, int threads) {
-    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+// Barrier `id` for `threads` of the CTA; whether all of them say `yes`.
+__device__ __forceinline__ bool barrier_all(int id, int threads, bool yes) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.cta.red.and.pred p, %1, %2, p;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(all) : "r"(id), "r"(threads), "r"((uint32_t)yes) : "memory");
+    return all != 0;
 }
 
 // Two vectors a thread and 28 warps, in groups where rows are short: fewer shuffles a row than with one vector, and two
@@ -194,12 +198,12 @@ __global__ __launch_bounds__(backward_warps(kVec) * 32) void norm_backward_kerne
     int64_t row = (int64_t)blockIdx.x * groups + group;
     const uint64_t policy = policy_evict_first();
     if (tid == 0)
-        for (int i = 0; i < a.stages; ++i) ring.fetch(a, row + i * step, i, policy);
+        for (int i = (int)blockIdx.x == a.limits.withheld_cta; i < a.stages; ++i) ring.fetch(a, row + i * step, i, policy);
     int slot = 0, turn = 0;
     uint32_t round = 0;
     bool ok = true;
     for (; row < a.T; row += step, turn ^= 1) {
-        ok = mbar_wait_bounded(ring.full + slot, round, a.wait_ns) && ok;
+        ok = mbar_wait_bounded(ring.full + slot, round, a.limits.wait_ns);
         uint4 now[kVec][3];
         float sum[2] = {};   // of h^2 and of d h
 #pragma unroll
@@ -226,7 +230,7 @@ __global__ __launch_bounds__(backward_warps(kVec) * 32) void norm_backward_kerne
             for (int o = 16; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
         if (a.row_warps > 1) {   // the two halves of `space` in turn, so that one barrier a row is enough
             if (lane == 0) space[turn][0][warp] = sum[0], space[turn][1][warp] = sum[1];
-            barrier(1 + group, threads);
+            ok = barrier_all(1 + group, threads, ok);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 sum[i] = lane < a.row_warps ? space[turn][i][first + lane] : 0.0f;
@@ -234,8 +238,9 @@ __global__ __launch_bounds__(backward_warps(kVec) * 32) void norm_backward_kerne
                 for (int o = 16; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
             }
         } else {
-            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok);
         }
+        if (!ok) break;   // the group as one
         if (tid == 0) ring.fetch(a, row + a.stages * step, slot, policy);   // every thread has read the stage
         if (++slot == a.stages) slot = 0, round ^= 1;
         const float r = rsqrtf(sum[0] / a.H + a.eps), m = r * r * (sum[1] / a.H);   // m h = n mean(d n)
@@ -256,7 +261,13 @@ __global__ __launch_bounds__(backward_warps(kVec) * 32) void norm_backward_kerne
             *reinterpret_cast<uint4 *>(a.out + (size_t)row * a.H + col) = narrow(add);
         }
     }
-    if (!ok && lane == 0) report(a.status, MOE_ERR_TIMEOUT);
+    if (!ok && tid == 0) {
+        report(a.status, MOE_ERR_TIMEOUT);
+        for (int i = 0; i < a.stages && row + i * step < a.T; ++i) {   // rows on their way all the same
+            mbar_wait_bounded(ring.full + slot, round, a.limits.wait_ns);
+            if (++slot == a.stages) slot = 0, round ^= 1;
+        }
+    }
     __syncthreads();   // no copy is under way: every stage that was fetched has been waited for
     float *sums = reinterpret_cast<float *>(rings);   // [groups][H]: half of the smallest ring
 #pragma unroll
@@ -378,7 +389,7 @@ int launch_norm_backward(const NormLaunch &L) {
     a.parts = static_cast<float *>(L.workspace), a.grad_weight = L.grad_weight;
     a.T = L.num_tokens, a.H = L.hidden;
     a.status = L.status;
-    a.wait_ns = wait_limits().wait_ns;
+    a.limits = wait_limits();
     a.trace = trace_args();
     cudaError_t e;
     e = a.H <= 14336 ? launch_backward<2>(a, s) : launch_backward<4>(a, s);

@@ -862,8 +862,8 @@ MOE_API int moe_add_rms_norm_backward(const void *h, const void *weight, int wei
                                       void *stream);
 
 /*
- * Failure injection for tests of moe_experts, moe_layer, moe_adapter_linear and the grouped products:
- * the process's later calls bound each wait inside their kernels by
+ * Failure injection for tests of moe_experts, moe_layer, moe_adapter_linear, the grouped products and
+ * moe_add_rms_norm_backward: the process's later calls bound each wait inside their kernels by
  * `wait_timeout_ns` of the GPU's global timer (<= 0: the default, 1 s; as much again
  * for every 2^22 rows of a weights' gradient, whose sums are waited for), and their
  * CTA `withheld_cta` keeps the first results that others wait for to itself, so

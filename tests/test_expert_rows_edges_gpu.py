@@ -1,6 +1,9 @@
 """The operators around a dispatch's rows in calls at the edge of what is allowed, or past it: prefixes that
-descend, outputs as torch allocates them, and sums over so many rows that one wait for them outlasts a short limit."""
+descend, outputs as torch allocates them, sums over so many rows that one wait for them outlasts a short limit, and waits
+that run out in the norm's gradient."""
 from __future__ import annotations
+
+import time
 
 import pytest
 import torch
@@ -184,3 +187,29 @@ def test_a_long_sum_of_one_expert_is_waited_for(moe, dtype, rows):
     want = torch.zeros(160, 8, 8, device=DEV)
     want[39] = rows
     assert torch.equal(got, want.to(dtype))
+
+
+# ------------------------------------------------------------------ waits that run out
+
+# one group of warps to a CTA and several, one warp to a row, rows for one stage and for many rounds of the ring
+@pytest.mark.parametrize("T,H", [(1, 64), (5, 16384), (1300, 16384), (1000, 14336), (3000, 7168), (9000, 1000), (40000, 256)])
+@pytest.mark.parametrize("cta", [0, 3])
+def test_the_norms_gradient_gives_up(moe, T, H, cta):
+    """A CTA that does not fetch its first rows reports the timeout and ends, with none of its other rows on their way."""
+    gen = torch.Generator(DEV).manual_seed(26)
+    x, w, g, gr = normal(gen, T, H), normal(gen, H), normal(gen, T, H), normal(gen, T, H)
+    status = moe.new_status()
+    want = moe.moe_add_rms_norm_backward(x, w, g, grad_residual=gr, status=status)
+    moe.check_status(status)
+    torch.cuda.synchronize()
+    with moe.test_wait_limits(20_000_000, cta):
+        start = time.monotonic()
+        moe.moe_add_rms_norm_backward(x, w, g, grad_residual=gr, status=status)
+        torch.cuda.synchronize()
+        took = time.monotonic() - start
+    assert int(status.item()) == (moe.MOE_ERR_TIMEOUT if T > cta else moe.MOE_OK)
+    assert took < 0.5   # a wait and one more for the rows on their way, of 20 ms each
+    status.zero_()
+    got = moe.moe_add_rms_norm_backward(x, w, g, grad_residual=gr, status=status)
+    moe.check_status(status)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
