@@ -544,6 +544,8 @@ MOE_API int moe_combine_fp8_ex(const void *partial_codes, const float *partial_s
 
 MOE_API int moe_test_wait_limits(int64_t wait_timeout_ns, int withheld_cta) {
     if (withheld_cta < -1) return MOE_ERR_INVALID_ARG;
+    // copies under way when a wait has run out are waited for as long again: long enough for any to land
+    if (wait_timeout_ns > 0 && wait_timeout_ns < 1000000) return MOE_ERR_INVALID_ARG;
     moe::g_wait_ns.store(wait_timeout_ns, std::memory_order_relaxed);
     moe::g_withheld_cta.store(withheld_cta, std::memory_order_relaxed);
     return MOE_OK;

@@ -870,6 +870,7 @@ MOE_API int moe_add_rms_norm_backward(const void *h, const void *weight, int wei
  * that those waits run out, the kernel ends and MOE_ERR_TIMEOUT is reported
  * (-1: none, the only value for production use). The rows of an adapter
  * projection that are not sorted by adapter wait for no other CTA's results.
+ * A limit below 1 ms is refused: copies under way would outlast it.
  */
 MOE_API int moe_test_wait_limits(int64_t wait_timeout_ns, int withheld_cta);
 
