@@ -76,6 +76,7 @@ struct Args {
     bool read_once;          // hardly any expert has rows for two tiles: its weights pass once
     bool accumulate;
     WaitLimits limits;
+    uint64_t tile_wait_ns;   // limit of waits that may cover all of a tile's reduction
     TraceArgs trace;
 };
 
@@ -305,7 +306,7 @@ __device__ bool find_tiles(const Args &a, Control &c) {
     bool ok = true;
     auto hand = [&](const Tile &t) {   // by lane 0
         if (lane == 0) {
-            ok = wait(&c.tile_empty[ring.slot], ring.round ^ 1, a.limits.wait_ns);
+            ok = wait(&c.tile_empty[ring.slot], ring.round ^ 1, a.tile_wait_ns);
             if (ok) {
                 c.tiles[ring.slot] = t;
                 mbar_arrive(&c.tile_full[ring.slot]);
@@ -402,7 +403,7 @@ template <class F>
 __device__ bool each_tile(const Args &a, Control &c, F f) {
     TileRing ring;
     for (;; ring.next()) {
-        if (!warp_wait(&c.tile_full[ring.slot], ring.round, a.limits.wait_ns)) return false;
+        if (!warp_wait(&c.tile_full[ring.slot], ring.round, a.tile_wait_ns)) return false;
         const Tile t = c.tiles[ring.slot];
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(&c.tile_empty[ring.slot]);
@@ -531,7 +532,7 @@ __device__ bool mask_blocks(const Args &a, Control &c, char *ring) {
         if (t.blocks == 0) return true;
         for (int kb = 0; kb < t.blocks - 1; ++kb) r.next();
         if (t.last % 16 != 0) {
-            if (!warp_wait(&c.masked_full[r.slot], seen >> r.slot & 1, a.limits.wait_ns)) return false;
+            if (!warp_wait(&c.masked_full[r.slot], seen >> r.slot & 1, a.tile_wait_ns)) return false;
             seen ^= 1u << r.slot;
             char *at = ring + (size_t)r.slot * (kTileA + C::kTileB);
             const int chunks = 2 + columns_of<kGradW, kCtas>(t) / kCtas / 64;
@@ -948,7 +949,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
             if constexpr (kOp == kGradW && sizeof(Out) == 2)
                 if (some && a.accumulate && a.split == 1)
                     load_rows(a, t, t.a0 + (int)rank * kRows + q * 32, side * 64, before);
-            if (some && !warp_wait(&c.sums_full[sums.slot], sums.round, a.limits.wait_ns)) return false;
+            if (some && !warp_wait(&c.sums_full[sums.slot], sums.round, a.tile_wait_ns)) return false;
             tc_fence_after();
             if (a.split > 1) {
                 shared = true;
@@ -1248,6 +1249,7 @@ int launch_grouped_linear(const GroupedLaunch &L) {
     a.E = L.num_experts, a.M = L.num_rows;
     a.features = L.out_features, a.depth = L.in_features;
     a.limits = wait_limits();
+    a.tile_wait_ns = a.limits.wait_ns;
     a.trace = trace_args();
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
     return e4m3 ? launch_best<kForwardE4m3, 160>(a, s) : launch_best<kForward, 256>(a, s);
@@ -1264,6 +1266,7 @@ int launch_grouped_grad_x(const GroupedLaunch &L) {
     a.E = L.num_experts, a.M = L.num_rows;
     a.features = L.in_features, a.depth = L.out_features;
     a.limits = wait_limits();
+    a.tile_wait_ns = a.limits.wait_ns;
     a.trace = trace_args();
     return launch_best<kGradX, 256>(a, static_cast<cudaStream_t>(L.stream));
 }
@@ -1290,9 +1293,8 @@ int launch_grouped_grad_w(const GroupedGradWLaunch &L) {
     a.features = L.out_features, a.depth = L.in_features;
     a.accumulate = L.accumulate;
     a.limits = wait_limits();
-    // One wait may cover all of a tile's reduction (its sums, its last block, the tile after next): 2^22 rows of one expert
-    // take 16 ms, so that 2^30 took four times the limit of 1 s. A limit more for every 2^22 rows.
-    a.limits.wait_ns *= 1 + (uint64_t)(L.num_rows >> 22);
+    // 2^22 rows of one expert take 16 ms, so that 2^30 took four times the limit of 1 s: a limit more for every 2^22 rows
+    a.tile_wait_ns = a.limits.wait_ns * (1 + (uint64_t)(L.num_rows >> 22));
     a.trace = trace_args();
     return L.out_type == MOE_GRAD_F32 ? launch_weights<float>(a, s) : launch_weights<__nv_bfloat16>(a, s);
 }

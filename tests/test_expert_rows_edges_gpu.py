@@ -213,3 +213,24 @@ def test_the_norms_gradient_gives_up(moe, T, H, cta):
     got = moe.moe_add_rms_norm_backward(x, w, g, grad_residual=gr, status=status)
     moe.check_status(status)
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_a_withheld_cta_of_a_long_sum_ends_soon(moe):
+    """Of the waits of a CTA that gives up, only those for a whole tile have the longer limit of many rows, 100 ms here; the
+    six or seven for its copies under way have 20."""
+    M = 2 ** 24
+    x, g = (torch.ones(M, 256, dtype=BF, device=DEV) for _ in range(2))
+    prefix = torch.full((161,), M, dtype=torch.int32, device=DEV)
+    prefix[0] = 0
+    status = moe.new_status()
+    out = torch.empty(160, 256, 256, device=DEV)
+    moe.moe_grouped_linear_grad_w(g, x, prefix, out=out, status=status)
+    moe.check_status(status)
+    torch.cuda.synchronize()
+    with moe.test_wait_limits(20_000_000, 1):
+        start = time.monotonic()
+        moe.moe_grouped_linear_grad_w(g, x, prefix, out=out, status=status)
+        torch.cuda.synchronize()
+        took = time.monotonic() - start
+    assert int(status.item()) == moe.MOE_ERR_TIMEOUT
+    assert took < 0.45, took
