@@ -80,6 +80,12 @@ struct Args {
     TraceArgs trace;
 };
 
+// CTAs (pairs) that share a tile's reduction at most, and each one's part of a shared tile's n columns.
+constexpr int most_split(int ctas) { return ctas == 2 ? 4 : 8; }
+__host__ __device__ constexpr int shared_width(int n, int split) { return ((n + split - 1) / split + 7) & ~7; }
+// Bytes of a CTA's sums of n columns with the others' of its own.
+constexpr int shared_bytes(int n, int split) { return (n + (split - 1) * shared_width(n, split)) * kRows * 4; }
+
 // kCols: the most columns of a tile. kCtas: CTAs of a cluster that work on one tile of kCtas * 128 features,
 // each with its part of the columns' operand.
 template <Op kOp, int kCtas, int kCols>
@@ -99,6 +105,9 @@ struct Config {
     static constexpr int kBlock = kE4m3 ? 128 : kDepth;
     static constexpr size_t smem() { return 1024 + (size_t)kStages * (kTileA + kTileB) + kBeside; }
     static_assert(kStages >= 3 && kSums >= 2);
+    // a shared tile's sums take the ring's place, and for 256 columns and four pairs that of what stands beside it too
+    static constexpr int kShared = kStages * (kTileA + kTileB) + kBeside;
+    static_assert(shared_bytes(kCols, 2) <= kShared && shared_bytes(kCols, 4) <= kShared && shared_bytes(kCols, most_split(kCtas)) <= kShared);
     // who takes a tile from the scan: loads, products (one CTA of a pair), warp 3 (if it has work), readers
     static constexpr bool kHelper = kOp == kGradW || kE4m3;
 };
@@ -771,8 +780,9 @@ __device__ __forceinline__ void store_weights(const Args &a, const Tile &t, int 
 }
 
 // A tile whose reduction a cluster shares: each of its CTAs (of a pair's two, each for its own features) adds up the
-// sums of as many columns. Every CTA lays its sums out in its ring, which no copy or product uses any more once every
-// CTA's roles have ended, and bulk copies take each column's to the CTA that adds them, in the order of the reduction.
+// sums of as many columns. Every CTA lays its sums out in its ring and in the space beside it (scales, or readers'
+// buffers, idle like the ring: a cluster that shares has one tile), which no copy or product uses any more once every CTA's
+// roles have ended, and bulk copies take each column's to the CTA that adds them, in the order of the reduction.
 // (Sums stored into the other CTAs' memory four bytes a lane took some 10 us longer for 256 x 256.) `put` hands this
 // thread's sums to f(column, feature, value); take(first column, columns, sum) stores this CTA's, where sum(i, f) is
 // what the i-th of them has for features f and f + 1. All warps of all CTAs of the cluster come here, or through
@@ -780,7 +790,7 @@ __device__ __forceinline__ void store_weights(const Args &a, const Tile &t, int 
 template <int kCtas, class Put, class Take>
 __device__ bool share_tile(const Args &a, Control &c, const Tile &t, char *ring, int tid, Put put, Take take) {
     const int split = a.split, side = blockIdx.x % kCtas, part = blockIdx.x / kCtas % split;
-    const int width = ((t.n + split - 1) / split + 7) & ~7, mine = max(min(width, t.n - part * width), 0);
+    const int width = shared_width(t.n, split), mine = max(min(width, t.n - part * width), 0);
     float *sums = reinterpret_cast<float *>(ring), *others = sums + t.n * kRows;   // [column][feature]; the others' of mine
     cluster_sync();
     put([&](int col, int feature, float v) { sums[col * kRows + feature] = v; });
@@ -1179,7 +1189,7 @@ Way way_for(const Args &a, int block_cells, int pair_cols) {
         const int64_t tiles = (int64_t)groups * per * ceil_div(a.features, (int)features);
         const int64_t most = most_row_tiles(a.M, a.E, cols) * ceil_div(a.features, (int)features);
         const double block = std::max(2.0 * n, (128 * 128 + (pair ? n / 2 : n) * 128) / (pair ? 64.0 : 70.0));
-        for (int split = 1; split <= (pair ? 4 : 8); split *= 2) {
+        for (int split = 1; split <= most_split(pair ? 2 : 1); split *= 2) {
             const int step = block_cells == 128 ? 4 : 1, of = ceil_div(a.blocks, split * step) * step;
             const int size = split * (pair ? 2 : 1);
             // the grid has a cluster for every tile there may be; four fifths of the SMs take clusters of eight at once
@@ -1204,7 +1214,7 @@ Way way_for_weights(const Args &a) {
         const int edge = pair ? 256 : 128;
         const int64_t tiles = (int64_t)a.E * ceil_div(a.features, edge) * ceil_div(a.depth, edge);
         const double block = pair ? 512 : 468;
-        for (int split = 1; split <= (pair ? 4 : 8); split *= 2) {
+        for (int split = 1; split <= most_split(pair ? 2 : 1); split *= 2) {
             const int size = split * (pair ? 2 : 1), of = ceil_div(blocks, split);
             if (split > 1 && (tiles * size > (size == 8 ? sms * 4 / 5 : sms) || (split - 1) * of >= blocks)) break;
             const int64_t at_once = sms / size;
