@@ -146,6 +146,11 @@ __device__ __forceinline__ bool barrier_all(int id, int threads, bool yes) {
     return all != 0;
 }
 
+// What is waited for is mostly there: the rest stays out of line (3000 x 14336 took 66.4 us with it in place, not 65.2).
+static __device__ __noinline__ bool wait_longer(uint64_t *bar, uint32_t parity, uint64_t ns) {
+    return mbar_wait_bounded(bar, parity, ns);
+}
+
 // Two vectors a thread and 28 warps, in groups where rows are short: fewer shuffles a row than with one vector, and two
 // rows at once where 28 warps in step would all wait for each row's sums. Rows beyond 14336 take four and 16 warps.
 __host__ __device__ constexpr int backward_warps(int vec) { return vec == 2 ? 28 : 16; }
@@ -203,7 +208,7 @@ __global__ __launch_bounds__(backward_warps(kVec) * 32) void norm_backward_kerne
     uint32_t round = 0;
     bool ok = true;
     for (; row < a.T; row += step, turn ^= 1) {
-        ok = mbar_wait_bounded(ring.full + slot, round, a.limits.wait_ns);
+        ok = mbar_try_wait(ring.full + slot, round) || wait_longer(ring.full + slot, round, a.limits.wait_ns);
         uint4 now[kVec][3];
         float sum[2] = {};   // of h^2 and of d h
 #pragma unroll
