@@ -76,7 +76,6 @@ struct Args {
     bool read_once;          // hardly any expert has rows for two tiles: its weights pass once
     bool accumulate;
     WaitLimits limits;
-    uint64_t tile_wait_ns;   // limit of waits that may cover all of a tile's reduction
     TraceArgs trace;
 };
 
@@ -298,6 +297,25 @@ __device__ __forceinline__ Range rows_of(const Args &a, int e) {
     return r;
 }
 
+// Rows of 32 experts of a wrong prefix, a lane each, without those before the end of earlier experts' rows, so that no row
+// has two writers, and there are no more tiles than most_row_tiles (clusters that share tiles take one each). Returns {lo, hi,
+// the end of all so far}; `end` is what it was before these 32, kNoEnd behind a prefix without a fault, where the first one's
+// start tells if any had rows (`some`).
+constexpr int kNoEnd = -1;
+static __device__ __noinline__ int3 behind_earlier(int lo, int hi, int end, bool some) {
+    const int lane = threadIdx.x & 31, first = __shfl_sync(0xffffffffu, lo, 0);
+    if (end == kNoEnd) end = some ? first : 0;
+    int most = lo < hi ? hi : 0;   // end of this expert's rows and those before it
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, most, o);
+        if (lane >= o) most = max(most, y);
+    }
+    const int earlier = __shfl_up_sync(0xffffffffu, most, 1);
+    lo = max(lo, lane > 0 ? max(end, earlier) : end);
+    return make_int3(lo, max(hi, lo), max(end, __shfl_sync(0xffffffffu, most, 31)));
+}
+
 struct TileRing {
     int slot = 0;
     uint32_t round = 0;
@@ -315,7 +333,7 @@ __device__ bool find_tiles(const Args &a, Control &c) {
     bool ok = true;
     auto hand = [&](const Tile &t) {   // by lane 0
         if (lane == 0) {
-            ok = wait(&c.tile_empty[ring.slot], ring.round ^ 1, a.tile_wait_ns);
+            ok = wait(&c.tile_empty[ring.slot], ring.round ^ 1, a.limits.wait_ns);
             if (ok) {
                 c.tiles[ring.slot] = t;
                 mbar_arrive(&c.tile_full[ring.slot]);
@@ -351,38 +369,30 @@ __device__ bool find_tiles(const Args &a, Control &c) {
         const int F = a.feature_tiles, kb0 = blockIdx.x / kCtas % a.split * a.per_split;
         const int blocks = min(a.per_split, a.blocks - kb0);
         int64_t before = 0;
-        int end = 0;         // of the rows of the experts before these 32
-        bool bad = false;    // a fault of the prefix so far
+        bool wrong = false;      // a fault in this lane's part of the prefix so far
+        int end = kNoEnd;        // once there is one: of the rows of the experts before these 32
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             Range r{};
             if (e0 + lane < a.E) r = rows_of(a, e0 + lane);
             if (r.bad && blockIdx.x == 0) report(a.status, MOE_ERR_BAD_PREFIX);
-            bad = __any_sync(0xffffffffu, r.bad) || bad;
-            if (bad) {   // rows before the end of earlier experts' are theirs: no row has two writers, and none has more
-                         // tiles than most_row_tiles (clusters that share tiles take one each)
-                int most = r.lo < r.hi ? r.hi : 0;   // end of this expert's rows and those before it
+            wrong = wrong || r.bad;
+            int rows, R, per;
+            int64_t mine, upto, all;
+            for (bool flag = wrong;; flag = false) {
+                rows = r.hi - r.lo, R = (rows + kCols - 1) / kCols;
+                per = R > 1 ? round16((int)quotient(rows + R - 1, R)) : rows;   // row tiles of equal size
+                mine = (int64_t)R * F + ((int64_t)flag << 56);   // faults go with the sum: a vote of their own takes 50 ns more
+                upto = mine;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, most, o);
-                    if (lane >= o) most = max(most, y);
+                    const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+                    if (lane >= o) upto += y;
                 }
-                const int earlier = __shfl_up_sync(0xffffffffu, most, 1);
-                r.lo = max(r.lo, lane > 0 ? max(end, earlier) : end);
-                r.hi = max(r.hi, r.lo);
-                end = max(end, __shfl_sync(0xffffffffu, most, 31));
-            } else if (const uint32_t some = __ballot_sync(0xffffffffu, r.lo < r.hi)) {
-                end = __shfl_sync(0xffffffffu, r.hi, 31 - __clz(some));
+                all = __shfl_sync(0xffffffffu, upto, 31);
+                if (all >> 56 == 0) break;
+                const int3 cut = behind_earlier(r.lo, r.hi, end, before > 0);
+                r.lo = cut.x, r.hi = cut.y, end = cut.z;
             }
-            const int rows = r.hi - r.lo, R = (rows + kCols - 1) / kCols;
-            const int per = R > 1 ? round16((int)quotient(rows + R - 1, R)) : rows;   // row tiles of equal size
-            const int64_t mine = (int64_t)R * F;
-            int64_t upto = mine;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += y;
-            }
-            const int64_t all = __shfl_sync(0xffffffffu, upto, 31);
             while (t < before + all) {
                 const int l = __ffs(__ballot_sync(0xffffffffu, before + upto > t)) - 1;
                 const int64_t i = t - before - __shfl_sync(0xffffffffu, upto - mine, l);
@@ -412,7 +422,7 @@ template <class F>
 __device__ bool each_tile(const Args &a, Control &c, F f) {
     TileRing ring;
     for (;; ring.next()) {
-        if (!warp_wait(&c.tile_full[ring.slot], ring.round, a.tile_wait_ns)) return false;
+        if (!warp_wait(&c.tile_full[ring.slot], ring.round, a.limits.wait_ns)) return false;
         const Tile t = c.tiles[ring.slot];
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(&c.tile_empty[ring.slot]);
@@ -479,9 +489,10 @@ __device__ bool load(const Args &a, Control &c, uint32_t ring_base, uint32_t ran
         }
         return true;
     });
-    // the last fills have been used, so none is in flight
+    // the last fills have been used, so none is in flight; where one is not, no product takes the others either, and each has
+    // had a limit's time to land
     for (int fill = max(issued - C::kStages, 0); fill < issued; ++fill)
-        warp_wait(&c.empty[fill % C::kStages], (fill / C::kStages) & 1, a.limits.wait_ns);
+        if (!warp_wait(&c.empty[fill % C::kStages], (fill / C::kStages) & 1, a.limits.wait_ns)) break;
     return ok;
 }
 
@@ -541,7 +552,7 @@ __device__ bool mask_blocks(const Args &a, Control &c, char *ring) {
         if (t.blocks == 0) return true;
         for (int kb = 0; kb < t.blocks - 1; ++kb) r.next();
         if (t.last % 16 != 0) {
-            if (!warp_wait(&c.masked_full[r.slot], seen >> r.slot & 1, a.tile_wait_ns)) return false;
+            if (!warp_wait(&c.masked_full[r.slot], seen >> r.slot & 1, a.limits.wait_ns)) return false;
             seen ^= 1u << r.slot;
             char *at = ring + (size_t)r.slot * (kTileA + C::kTileB);
             const int chunks = 2 + columns_of<kGradW, kCtas>(t) / kCtas / 64;
@@ -959,7 +970,7 @@ __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, u
             if constexpr (kOp == kGradW && sizeof(Out) == 2)
                 if (some && a.accumulate && a.split == 1)
                     load_rows(a, t, t.a0 + (int)rank * kRows + q * 32, side * 64, before);
-            if (some && !warp_wait(&c.sums_full[sums.slot], sums.round, a.tile_wait_ns)) return false;
+            if (some && !warp_wait(&c.sums_full[sums.slot], sums.round, a.limits.wait_ns)) return false;
             tc_fence_after();
             if (a.split > 1) {
                 shared = true;
@@ -1259,7 +1270,6 @@ int launch_grouped_linear(const GroupedLaunch &L) {
     a.E = L.num_experts, a.M = L.num_rows;
     a.features = L.out_features, a.depth = L.in_features;
     a.limits = wait_limits();
-    a.tile_wait_ns = a.limits.wait_ns;
     a.trace = trace_args();
     const cudaStream_t s = static_cast<cudaStream_t>(L.stream);
     return e4m3 ? launch_best<kForwardE4m3, 160>(a, s) : launch_best<kForward, 256>(a, s);
@@ -1276,7 +1286,6 @@ int launch_grouped_grad_x(const GroupedLaunch &L) {
     a.E = L.num_experts, a.M = L.num_rows;
     a.features = L.in_features, a.depth = L.out_features;
     a.limits = wait_limits();
-    a.tile_wait_ns = a.limits.wait_ns;
     a.trace = trace_args();
     return launch_best<kGradX, 256>(a, static_cast<cudaStream_t>(L.stream));
 }
@@ -1303,8 +1312,9 @@ int launch_grouped_grad_w(const GroupedGradWLaunch &L) {
     a.features = L.out_features, a.depth = L.in_features;
     a.accumulate = L.accumulate;
     a.limits = wait_limits();
-    // 2^22 rows of one expert take 16 ms, so that 2^30 took four times the limit of 1 s: a limit more for every 2^22 rows
-    a.tile_wait_ns = a.limits.wait_ns * (1 + (uint64_t)(L.num_rows >> 22));
+    // One wait may cover all of a tile's reduction (its sums, its last block, the tile after next): 2^22 rows of one expert
+    // take 16 ms, so that 2^30 took four times the limit of 1 s. A limit more for every 2^22 rows.
+    a.limits.wait_ns *= 1 + (uint64_t)(L.num_rows >> 22);
     a.trace = trace_args();
     return L.out_type == MOE_GRAD_F32 ? launch_weights<float>(a, s) : launch_weights<__nv_bfloat16>(a, s);
 }
