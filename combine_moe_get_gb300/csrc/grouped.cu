@@ -9,7 +9,7 @@
 // expert with 140 rows costs 144 and not 256; features fill its fixed 128 rows,
 // or 256 of a pair of CTAs that work as one (each holds half of both operands, which
 // halves what a block takes from L2: 128 x 128 tiles of single CTAs ran at 1.13
-// PFLOP/s where pairs' 256 x 256 run at 1.5 to 1.67, 16384 rows, 32 experts, 7168 x 4096;
+// PFLOP/s where pairs' 256 x 256 run at 1.6 to 1.7, 16384 rows, 32 experts, 7168 x 4096;
 // one expert 1.8, where a dense library product has 1.9). One persistent CTA per SM;
 // each finds its tiles by a scan over the experts' numbers of rows, which stay on
 // the device. Few rows to an expert are bound by reading the weights: 128 a piece 6.5
@@ -25,8 +25,13 @@
 // multiplied by the product of their two scales and added: two operations for each of
 // D's elements and block, 128 x n of them while the pair's products take 2 n cycles.
 // That is all that the ordinary cores have to give, so these readers bound E4M3 where
-// rows are many: 1.8 to 1.9 PFLOP/s (the rate without them 3.2, without their
+// rows are many: 1.77 to 1.86 PFLOP/s (the rate without them 3.2, without their
 // arithmetic 2.7), and what helped was fewer instructions and waits around it.
+//
+// The tensor core's sums are fp32, but of each 16 products what lies below 2^-25 of
+// the sum's leading bit is cut off, as in a library's bf16 products: off by 5e-7 of
+// their norm over 512 rows, 2e-5 over 16384 (8e-5 where all have one sign), where one
+// CTA has them all. fp32 sums of dW show it; bf16's rounding covers it to some 2^17 rows.
 #include <algorithm>
 #include <atomic>
 #include <cstdint>
@@ -892,7 +897,8 @@ __device__ void store_shared_weights(const Args &a, const Tile &t, int readers, 
     }
 }
 
-// Warps 4 to 11: a quarter of tensor memory's lanes each, every other 16 columns.
+// The warps from the fourth on, eight or (E4M3) twelve: a quarter of tensor memory's lanes each, every second or third 16
+// columns (weights' gradients: 128 bytes of the result).
 template <Op kOp, int kCtas, int kCols, typename Out>
 __device__ bool read_sums(const Args &a, Control &c, char *ring, char *beside, uint32_t tmem, uint32_t rank, bool &shared) {
     using C = Config<kOp, kCtas, kCols>;

@@ -372,7 +372,10 @@ int launch_norm(const NormLaunch &L) {
     cudaError_t e;
     // Fewer warps with more of a row each, where that keeps enough of them at work. us (7 of them the launch's), at most 8
     // warps / 16: 4096 channels, 16384 rows to E4M3 85 / 95, to bf16 85 / 91, 128 rows 9.4 / 9.4; 7168 channels to E4M3 alone
-    // 134 / 143, 4096 rows 42 / 44; but with bf16 rows 4096 rows 50 / 48, 128 rows 11.4 / 9.4.
+    // 134 / 143, 4096 rows 42 / 44; but with bf16 rows 4096 rows 50 / 48, 128 rows 11.4 / 9.4. In a graph, without the 7:
+    // 16384 rows to E4M3 alone 5120 channels 92 / 99, 6144 109 / 112, 8192 143 / 150, to bf16 99 / 98, 119 / 118, 157 / 156, to
+    // both 113 / 114, 134 / 134, 177 / 177; 4096 rows to both 32.4 / 32.1, 37.9 / 37.1, 48.7 / 48.2; 128 rows to E4M3 alone
+    // the other way, 4.3 to 4.7 / 3.4 to 3.9.
     switch (vectors(a.H, a.H <= 4096 || (a.H <= 8192 && !a.out) ? 8 : 16)) {
         case 1: e = launch_forward<1>(a, s); break;
         case 2: e = launch_forward<2>(a, s); break;

@@ -49,7 +49,7 @@ __device__ __forceinline__ float quantise(const float (&x)[8], uint2 &codes) {
     const float q0 = amax * k;
     float scale = fmaf(fmaf(-q0, 448.0f, amax), k, q0);
     uint32_t q[4];
-    if (amax > 5.7e-28f && amax < 3.0e38f) {   // 448 * 2^-100
+    if (amax > 5.7e-28f && amax < 3.0e38f) {   // far inside what has a normal scale and reciprocal
         float r;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(scale));
 #pragma unroll

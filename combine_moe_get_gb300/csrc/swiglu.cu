@@ -58,7 +58,8 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
     asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(a.v) : "l"(b.v), "l"(c.v));
     return a;
 }
-// exp and the reciprocal are the fast ones, off by some 2^-21 of the sigmoid: an eighth of an E4M3 or bf16 rounding's 2^-9 at most
+// exp and the reciprocal are the fast ones, the exponent rounded before: off by 2^-22 + |z| 2^-23 of the sigmoid (2^-16 at most,
+// where bf16's rounding has 2^-9) down to z = -87.3; below, where the reciprocal is no normal number, the sigmoid is 0
 __device__ __forceinline__ Two sigmoid(Two z) {
     float a, b;
     (z * Two(-1.4426950408889634f)).parts(a, b);   // log2(e)
